@@ -20,6 +20,7 @@ OK, ERR_INVALID, ERR_ALIGNMENT, ERR_UNSUPPORTED, ERR_CUDA, ERR_TIMEOUT, ERR_NO_D
 K_MAJOR, MN_MAJOR = 0, 1
 F32, F16, BF16 = 0, 1, 2
 IN_F16, IN_BF16, IN_TF32, IN_E4M3, IN_E5M2, IN_E3M2, IN_E2M3, IN_E2M1, IN_NVF4 = 0, 1, 2, 3, 4, 5, 6, 7, 8
+W4_INT4, W4_MXF4, W4_NVF4 = 0, 1, 2
 
 _i64, _i32, _u32, _u64, _vp = ctypes.c_int64, ctypes.c_int, ctypes.c_uint32, ctypes.c_uint64, ctypes.c_void_p
 
@@ -33,6 +34,14 @@ class GemmArgs(ctypes.Structure):
                 ("D", _vp), ("d_type", _i32), ("ldd", _i64), ("acc_type", _i32),
                 ("cta_group", _i32), ("raster_group", _i32), ("sf_staging", _i32), ("split_k", _i32),
                 ("epilogue", _i32)]
+
+
+class GemvW4Args(ctypes.Structure):
+    """Mirror of ``tcg_gemv_w4_args``."""
+    _fields_ = [("format", _i32), ("in_type", _i32), ("R", _i64), ("N", _i64), ("K", _i64), ("G", _i32),
+                ("group", _i32), ("A", _vp), ("lda", _i64), ("offsets", _vp), ("B", _vp), ("ldb", _i64),
+                ("stride_b", _i64), ("scale", _vp), ("ld_scale", _i64), ("stride_scale", _i64), ("zero", _vp),
+                ("alpha", _vp), ("D", _vp), ("d_type", _i32), ("ldd", _i64)]
 
 
 class ProbeOperand(ctypes.Structure):
@@ -60,6 +69,15 @@ _SIGS = {
     "tcg_prepare_scales_ab": ([_i32, _vp, _i64, _vp, _vp, _i64, _i32, _vp, _i64, _vp], _i32),
     "tcg_gemm": ([ctypes.POINTER(GemmArgs), _vp], _i32),
     "tcg_gemm_chain": ([_i32, _i64, _i64, _i64, _i64, _vp, _i64, _vp, _i64, _vp, _i64, _vp, _i32, _i64, _vp], _i32),
+    "tcg_moe_sort": ([_i64, _i32, _i32, _vp, _vp, _vp, _vp, _vp], _i32),
+    "tcg_moe_dispatch": ([_i32, _i64, _i32, _i64, _vp, _i64, _vp, _vp, _i64, _vp], _i32),
+    "tcg_moe_combine": ([_i32, _i64, _i32, _i64, _vp, _i64, _vp, _vp, _vp, _i64, _vp], _i32),
+    "tcg_moe_combine_grad": ([_i32, _i64, _i32, _i64, _vp, _i64, _vp, _i64, _vp, _vp, _vp, _i64, _vp, _vp], _i32),
+    "tcg_gemm_grouped": ([_i32, _i64, _i64, _i64, _i32, _vp, _i64, _vp, _vp, _i32, _i64, _i64, _vp, _i32, _i64,
+                          _vp], _i32),
+    "tcg_gemm_grouped_wgrad": ([_i32, _i64, _i64, _i64, _i32, _vp, _i64, _vp, _i64, _vp, _vp, _i32, _i64, _i64,
+                                _vp], _i32),
+    "tcg_gemv_w4": ([ctypes.POINTER(GemvW4Args), _vp], _i32),
     "tcg_mxf8_scale_image_bytes": ([_i64, _i64, _i32], _i64),
     "tcg_mxf8_tile_n": ([_i64, _i64, _i64, _i32, _i32], _i32),
     "tcg_tile_n": ([_i32, _i64, _i64, _i64, _i32, _i32], _i32),
@@ -227,6 +245,52 @@ def gemm(M, N, K, in_type, A, a_major, lda, B, b_major, ldb, D, d_type, ldd, acc
                  sf_staging, split_k, epilogue)
     rc = _lib.tcg_gemm(ctypes.byref(a), _stream(stream))
     return _ok(rc, "gemm") if check else rc
+
+
+def moe_sort(T, topk, E, expert, offsets, position, source, stream=None):
+    """Order of the T x topk choices by expert (``tcg_moe_sort``)."""
+    return _ok(_lib.tcg_moe_sort(T, topk, E, _ptr(expert), _ptr(offsets), _ptr(position), _ptr(source),
+                                 _stream(stream)), "moe_sort")
+
+
+def moe_dispatch(dtype, T, topk, H, X, ldx, position, Xs, ldxs, stream=None):
+    """Token rows to their sorted positions (``tcg_moe_dispatch``)."""
+    return _ok(_lib.tcg_moe_dispatch(dtype, T, topk, H, _ptr(X), ldx, _ptr(position), _ptr(Xs), ldxs,
+                                     _stream(stream)), "moe_dispatch")
+
+
+def moe_combine(dtype, T, topk, H, Ys, ldys, position, weight, Y, ldy, stream=None):
+    """Weighted sum of each token's sorted rows (``tcg_moe_combine``); weight None: the gradient of moe_dispatch."""
+    return _ok(_lib.tcg_moe_combine(dtype, T, topk, H, _ptr(Ys), ldys, _ptr(position), _ptr(weight), _ptr(Y), ldy,
+                                    _stream(stream)), "moe_combine")
+
+
+def moe_combine_grad(dtype, T, topk, H, dY, lddy, Ys, ldys, position, weight, dYs, lddys, dweight, stream=None):
+    """Gradient of moe_combine (``tcg_moe_combine_grad``); Ys and dweight both given or both None."""
+    return _ok(_lib.tcg_moe_combine_grad(dtype, T, topk, H, _ptr(dY), lddy, _ptr(Ys), ldys, _ptr(position),
+                                         _ptr(weight), _ptr(dYs), lddys, _ptr(dweight), _stream(stream)),
+               "moe_combine_grad")
+
+
+def gemm_grouped(in_type, R, N, K, G, A, lda, offsets, B, b_major, ldb, stride_b, D, d_type, ldd, stream=None):
+    """Sorted rows times their group's matrix (``tcg_gemm_grouped``)."""
+    return _ok(_lib.tcg_gemm_grouped(in_type, R, N, K, G, _ptr(A), lda, _ptr(offsets), _ptr(B), b_major, ldb,
+                                     stride_b, _ptr(D), d_type, ldd, _stream(stream)), "gemm_grouped")
+
+
+def gemm_grouped_wgrad(in_type, R, N, K, G, DY, lddy, A, lda, offsets, DW, dw_type, lddw, stride_dw, stream=None):
+    """Gradient of gemm_grouped's matrices (``tcg_gemm_grouped_wgrad``)."""
+    return _ok(_lib.tcg_gemm_grouped_wgrad(in_type, R, N, K, G, _ptr(DY), lddy, _ptr(A), lda, _ptr(offsets), _ptr(DW),
+                                           dw_type, lddw, stride_dw, _stream(stream)), "gemm_grouped_wgrad")
+
+
+def gemv_w4(fmt, in_type, R, N, K, A, lda, B, scale, D, d_type, ldd, group=0, zero=None, groups=1, offsets=None,
+            alpha=None, ldb=0, stride_b=0, ld_scale=0, stride_scale=0, stream=None, check=True):
+    """Few rows against 4-bit matrices (``tcg_gemv_w4``); returns the status (raises if ``check``)."""
+    a = GemvW4Args(fmt, in_type, R, N, K, groups, group, _ptr(A), lda, _ptr(offsets), _ptr(B), ldb, stride_b,
+                   _ptr(scale), ld_scale, stride_scale, _ptr(zero), _ptr(alpha), _ptr(D), d_type, ldd)
+    rc = _lib.tcg_gemv_w4(ctypes.byref(a), _stream(stream))
+    return _ok(rc, "gemv_w4") if check else rc
 
 
 def mxf8_scale_image_bytes(rows, K, tile_rows) -> int:

@@ -75,4 +75,15 @@ void set_launch_count(int n);
 namespace tcg {
 // Sets the text tcg_last_error_string() returns on this thread.
 void set_error_message(const char* msg);
+
+// Runs an entry point's body; no C++ exception (host memory running out in a
+// container) leaves the C ABI.
+template <class F>
+int guarded(F&& body) noexcept {
+  try {
+    return body();
+  } catch (...) {
+    return TCG_ERR_CUDA;
+  }
+}
 }  // namespace tcg

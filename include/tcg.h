@@ -31,7 +31,8 @@
  * use library-owned device workspaces per (device, stream), allocated on
  * first use and grown when needed (growing frees the old one, which waits for
  * the device); nothing else allocates device memory.  Calls on different
- * streams use different workspaces and may run concurrently.  A call may be
+ * streams use different workspaces and may run concurrently.  tcg_moe_sort
+ * uses the block-scale workspace of its stream in the same way.  A call may be
  * captured into a CUDA graph once an earlier call on the same stream has
  * allocated a workspace at least as large (a workspace that would have to
  * grow during capture fails the call with TCG_ERR_CUDA); the graph reuses
@@ -278,6 +279,110 @@ int tcg_gemm_chain(tcg_input in_type, int64_t M, int64_t N1, int64_t N2, int64_t
                    const void* A, int64_t lda, const void* B1, int64_t ldb1,
                    const void* B2, int64_t ldb2, void* E, tcg_dtype e_type, int64_t lde,
                    void* stream);
+
+/* ---------------------------------------------------------------------------
+ * Mixture-of-experts operators: the order of the tokens' choices, rows to the
+ * experts and back, and products over the sorted rows (dense 16-bit matrices,
+ * or 4-bit ones for a few rows).  All pointers are device memory.
+ *
+ * T tokens choose topk of E experts each; choice j of token t is entry
+ * i = t * topk + j.  Entries sorted by expert, and by i within an expert, are
+ * the sorted rows p = 0 .. T * topk - 1; expert e owns rows [offsets[e],
+ * offsets[e+1]).  An entry whose expert lies outside [0, E) (a masked token,
+ * an expert held elsewhere) is dropped: it sorts after the last expert and its
+ * position is stored inverted, -1 - p.
+ * ------------------------------------------------------------------------- */
+
+/* offsets [E+1], position [T][topk] (p, or -1 - p for a dropped entry) and
+ * source [T * topk] (the entry i at sorted row p) from expert [T][topk].
+ * 1 <= E <= 1024, 1 <= topk, T * topk < 2^30 (TCG_ERR_UNSUPPORTED beyond).
+ * T == 0: only offsets is written.  The result is the same on every call
+ * (no atomics decide an order).  Uses the stream's library workspace for
+ * more than 16384 entries. */
+int tcg_moe_sort(int64_t T, int topk, int E, const int32_t* expert, int32_t* offsets, int32_t* position,
+                 int32_t* source, void* stream);
+
+/* Xs[p][0..H) = X[t][0..H) for every kept entry, 0 for a dropped one; type is
+ * the element type of both.  Leading dimensions in elements (0 = H); no
+ * alignment beyond the element's (16-byte aligned bases and rows move as
+ * 16-byte words).  Its gradient is tcg_moe_combine with weight = NULL. */
+int tcg_moe_dispatch(tcg_dtype type, int64_t T, int topk, int64_t H, const void* X, int64_t ldx,
+                     const int32_t* position, void* Xs, int64_t ldxs, void* stream);
+
+/* Y[t][h] = sum over kept j of weight[t][j] * Ys[position[t][j]][h], summed in
+ * fp32 in the order of j and rounded once; weight fp32 [T][topk], or NULL for
+ * ones.  Rows of dropped entries are not read; a token without kept entries
+ * gets zeros.  1 <= topk <= 64. */
+int tcg_moe_combine(tcg_dtype type, int64_t T, int topk, int64_t H, const void* Ys, int64_t ldys,
+                    const int32_t* position, const float* weight, void* Y, int64_t ldy, void* stream);
+
+/* The gradient of tcg_moe_combine: dYs[position[t][j]][h] = weight[t][j] *
+ * dY[t][h] (0 in the rows of dropped entries) and dweight[t][j] = sum_h
+ * dY[t][h] * Ys[position[t][j]][h] (0 for dropped entries), fp32.  Ys and
+ * dweight are both given or both NULL (no weight gradient); dYs must not
+ * overlap Ys. */
+int tcg_moe_combine_grad(tcg_dtype type, int64_t T, int topk, int64_t H, const void* dY, int64_t lddy,
+                         const void* Ys, int64_t ldys, const int32_t* position, const float* weight, void* dYs,
+                         int64_t lddys, float* dweight, void* stream);
+
+/* Product of sorted rows with their group's matrix:
+ *     D[r, n] = sum_k A[r, k] * B[g][k, n]     for r in [offsets[g], offsets[g+1])
+ * A [R][K] and B are f16 or bf16 (in_type), D is d_type; fp32 accumulation,
+ * one rounding.  b_major TCG_K_MAJOR: B[g] is N x K, element (k, n) at
+ * B[g*stride_b + n*ldb + k]; TCG_MN_MAJOR: K x N, at B[g*stride_b + k*ldb + n]
+ * (with the forward matrices in place, the gradient of the rows).  Rows before
+ * offsets[0] and from offsets[G] on belong to no group: their D is zero.
+ * offsets [G+1] is read on the device, 1 <= G <= 1024 and R < 2^30 (no entry
+ * is read or written out of range for any offsets: each is clamped to [the
+ * previous one, R]).  A, B bases, lda, ldb and stride_b follow the 16-byte
+ * rules of the dense GEMMs; D is element aligned.  Leading dimensions of 0
+ * mean packed, stride_b of 0 N * ldb (K * ldb).  K == 0: D = 0. */
+int tcg_gemm_grouped(tcg_input in_type, int64_t R, int64_t N, int64_t K, int G, const void* A, int64_t lda,
+                     const int32_t* offsets, const void* B, tcg_major b_major, int64_t ldb, int64_t stride_b,
+                     void* D, tcg_dtype d_type, int64_t ldd, void* stream);
+
+/* The gradient of the matrices of tcg_gemm_grouped (K-major B):
+ *     DW[g][n, k] = sum over r in [offsets[g], offsets[g+1]) of DY[r, n] * A[r, k]
+ * DY [R][N], A [R][K] f16 or bf16; DW element (g, n, k) at DW[g*stride_dw +
+ * n*lddw + k] of dw_type, zero for a group without rows.  Alignment of DY and
+ * A as above. */
+int tcg_gemm_grouped_wgrad(tcg_input in_type, int64_t R, int64_t N, int64_t K, int G, const void* DY, int64_t lddy,
+                           const void* A, int64_t lda, const int32_t* offsets, void* DW, tcg_dtype dw_type,
+                           int64_t lddw, int64_t stride_dw, void* stream);
+
+/* 4-bit weight formats of tcg_gemv_w4.  MXFP4 and NVFP4 hold codes and scales
+ * exactly as tcg_gemm_mxf4_blockscaled / tcg_gemm_nvf4_blockscaled take them
+ * as B, so that one copy of the weights serves both. */
+typedef enum {
+  TCG_W4_INT4 = 0,  /* unsigned codes 0..15; value (code - zero) * scale */
+  TCG_W4_MXF4 = 1,  /* E2M1, e8m0 scale per 32 */
+  TCG_W4_NVF4 = 2   /* E2M1, unsigned E4M3 scale per 16 */
+} tcg_w4;
+
+/* Few rows against 4-bit matrices, activations kept in 16 bits:
+ *     D[r, n] = alpha[g] * sum_k A[r, k] * w[g][n, k]
+ *     w[g][n, k] = value(code[g][n, k]) * scale[g][n, k / group]
+ * for the rows [offsets[g], offsets[g+1]) of group g (offsets NULL: G = 1 and
+ * all R rows); rows of no group give zero.  Codes are packed two per byte,
+ * low nibble first, rows of K codes. */
+typedef struct {
+  tcg_w4 format;
+  tcg_input in_type;        /* A: TCG_IN_F16 or TCG_IN_BF16 */
+  int64_t R, N, K;          /* K a multiple of 32 and of group */
+  int G;                    /* groups, 1 .. 1024 */
+  int group;                /* K per scale: INT4 32, 64 or 128; 0 or 32 MXF4; 0 or 16 NVF4 */
+  const void* A; int64_t lda;              /* [R][K], 16-byte aligned base and rows */
+  const int32_t* offsets;                  /* device [G+1], or NULL with G == 1 */
+  const uint8_t* B; int64_t ldb;           /* ldb in codes (0 = K), a multiple of 32; base 16-byte aligned */
+  int64_t stride_b;                        /* codes between groups (0 = N * ldb), a multiple of 32 */
+  const void* scale;                       /* [G][N][K / group]: INT4 in in_type's type, else bytes */
+  int64_t ld_scale, stride_scale;          /* elements between rows / groups (0 = packed) */
+  const uint8_t* zero;                     /* INT4: [G][N][K / group] laid out as scale, or NULL: 8 */
+  const float* alpha;                      /* [G], or NULL: 1 */
+  void* D; tcg_dtype d_type; int64_t ldd;  /* [R][N], element aligned */
+} tcg_gemv_w4_args;
+
+int tcg_gemv_w4(const tcg_gemv_w4_args* args, void* stream);
 
 /* ---------------------------------------------------------------------------
  * Block-scale layout (the scale-factor rearrangement step).

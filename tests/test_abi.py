@@ -173,3 +173,126 @@ def test_fails_loudly_without_a_device(tcg):
     assert _call(tcg, "bf16") == tcg.ERR_NO_DEVICE
     with pytest.raises(tcg.TcgError):
         tcg.gemm_bf16(256, 256, 64, 0x10000, 0, 0, 0x20000, 0, 0, 0x30000, 2, 0, 0, stream=0)
+
+
+def test_moe_validation_before_any_device_work(tcg):
+    def sort(T=4, topk=2, E=8, ex=0x10000, off=0x20000, pos=0x30000, src=0x40000):
+        return tcg.raw_call("tcg_moe_sort", T, topk, E, ex, off, pos, src, None)
+    assert sort(T=-1) == tcg.ERR_INVALID
+    assert sort(topk=0) == tcg.ERR_INVALID
+    assert sort(E=0) == tcg.ERR_INVALID
+    assert sort(E=1025) == tcg.ERR_UNSUPPORTED
+    assert sort(T=1 << 28, topk=8) == tcg.ERR_UNSUPPORTED
+    assert sort(T=(1 << 62), topk=8) == tcg.ERR_UNSUPPORTED
+    for p in ("ex", "off", "pos", "src"):
+        assert sort(**{p: None}) == tcg.ERR_INVALID
+        assert sort(**{p: 0x10002}) == tcg.ERR_ALIGNMENT
+    assert sort(T=0, off=None) == tcg.ERR_INVALID
+
+    def disp(t=2, T=4, topk=2, H=64, X=0x10000, ldx=0, pos=0x20000, Xs=0x30000, ldxs=0):
+        return tcg.raw_call("tcg_moe_dispatch", t, T, topk, H, X, ldx, pos, Xs, ldxs, None)
+    assert disp(t=3) == tcg.ERR_INVALID
+    assert disp(H=-1) == tcg.ERR_INVALID
+    assert disp(topk=65) == tcg.ERR_UNSUPPORTED
+    assert disp(ldx=63) == tcg.ERR_INVALID
+    assert disp(ldxs=63) == tcg.ERR_INVALID
+    assert disp(X=None) == tcg.ERR_INVALID
+    assert disp(X=0x10001) == tcg.ERR_ALIGNMENT
+    assert disp(t=0, Xs=0x30002) == tcg.ERR_ALIGNMENT
+    assert disp(pos=0x20002) == tcg.ERR_ALIGNMENT
+    assert disp(T=0, X=None, Xs=None, pos=None) == tcg.OK
+    assert disp(H=0, X=None, Xs=None, pos=None) == tcg.OK
+
+    def comb(t=2, T=4, topk=2, H=64, Ys=0x10000, ldys=0, pos=0x20000, w=0x30000, Y=0x40000, ldy=0):
+        return tcg.raw_call("tcg_moe_combine", t, T, topk, H, Ys, ldys, pos, w, Y, ldy, None)
+    assert comb(Ys=None) == tcg.ERR_INVALID
+    assert comb(ldy=8) == tcg.ERR_INVALID
+    assert comb(w=0x30002) == tcg.ERR_ALIGNMENT
+    assert comb(T=0, Ys=None, Y=None, pos=None, w=None) == tcg.OK
+
+    def grad(t=2, T=4, topk=2, H=64, dY=0x10000, Ys=0x20000, pos=0x30000, w=0x40000, dYs=0x50000, dw=0x60000):
+        return tcg.raw_call("tcg_moe_combine_grad", t, T, topk, H, dY, 0, Ys, 0, pos, w, dYs, 0, dw, None)
+    assert grad(Ys=None) == tcg.ERR_INVALID                  # Ys and dweight go together
+    assert grad(dw=None) == tcg.ERR_INVALID
+    assert grad(dYs=None) == tcg.ERR_INVALID
+    assert grad(dw=0x60002) == tcg.ERR_ALIGNMENT
+    assert grad(T=0, dY=None, Ys=None, dYs=None, dw=None) == tcg.OK
+
+
+def test_grouped_validation_before_any_device_work(tcg):
+    def call(t=1, R=64, N=64, K=64, G=4, A=0x10000, lda=0, off=0x20000, B=0x30000, major=0, ldb=0, sb=0, D=0x40000,
+             dt=2, ldd=0):
+        return tcg.raw_call("tcg_gemm_grouped", t, R, N, K, G, A, lda, off, B, major, ldb, sb, D, dt, ldd, None)
+    assert call(t=2) == tcg.ERR_INVALID                       # 16-bit operands only
+    assert call(R=-1) == tcg.ERR_INVALID
+    assert call(G=0) == tcg.ERR_INVALID
+    assert call(G=1025) == tcg.ERR_UNSUPPORTED
+    assert call(R=1 << 30) == tcg.ERR_UNSUPPORTED
+    assert call(major=2) == tcg.ERR_INVALID
+    assert call(dt=3) == tcg.ERR_INVALID
+    for p in ("A", "off", "B", "D"):
+        assert call(**{p: None}) == tcg.ERR_INVALID
+    assert call(lda=56) == tcg.ERR_INVALID
+    assert call(ldb=56) == tcg.ERR_INVALID
+    assert call(ldd=56) == tcg.ERR_INVALID
+    assert call(sb=-8) == tcg.ERR_INVALID
+    assert call(K=60) == tcg.ERR_ALIGNMENT                    # packed rows of 120 bytes
+    assert call(N=60, major=1) == tcg.ERR_ALIGNMENT
+    assert call(sb=64 * 64 + 4) == tcg.ERR_ALIGNMENT
+    assert call(A=0x10008) == tcg.ERR_ALIGNMENT
+    assert call(off=0x20002) == tcg.ERR_ALIGNMENT
+    assert call(D=0x40001) == tcg.ERR_ALIGNMENT
+    assert call(R=0, A=None, off=None, B=None, D=None) == tcg.OK
+    assert call(N=0, A=None, off=None, B=None, D=None) == tcg.OK
+
+    def wgrad(t=1, R=64, N=64, K=64, G=4, DY=0x10000, lddy=0, A=0x20000, lda=0, off=0x30000, DW=0x40000, dt=0,
+              lddw=0, sw=0):
+        return tcg.raw_call("tcg_gemm_grouped_wgrad", t, R, N, K, G, DY, lddy, A, lda, off, DW, dt, lddw, sw, None)
+    assert wgrad(t=3) == tcg.ERR_INVALID
+    assert wgrad(K=-1) == tcg.ERR_INVALID
+    for p in ("DY", "A", "off", "DW"):
+        assert wgrad(**{p: None}) == tcg.ERR_INVALID
+    assert wgrad(lddw=32) == tcg.ERR_INVALID
+    assert wgrad(sw=-1) == tcg.ERR_INVALID
+    assert wgrad(DW=0x40002) == tcg.ERR_ALIGNMENT
+    assert wgrad(N=60) == tcg.ERR_ALIGNMENT
+    assert wgrad(lda=68) == tcg.ERR_ALIGNMENT
+    assert wgrad(N=0, DY=None, A=None, off=None, DW=None) == tcg.OK
+
+
+def test_gemv_w4_validation_before_any_device_work(tcg):
+    def call(fmt=0, t=1, R=2, N=64, K=256, A=0x10000, lda=0, B=0x20000, scale=0x30000, D=0x40000, dt=2, ldd=0,
+             group=64, **kw):
+        return tcg.gemv_w4(fmt, t, R, N, K, A, lda, B, scale, D, dt, ldd, group=group, check=False, stream=0, **kw)
+    assert tcg.raw_call("tcg_gemv_w4", None, None) == tcg.ERR_INVALID
+    assert call(fmt=3) == tcg.ERR_INVALID
+    assert call(t=2) == tcg.ERR_INVALID
+    assert call(dt=4) == tcg.ERR_INVALID
+    assert call(R=-1) == tcg.ERR_INVALID
+    assert call(groups=0) == tcg.ERR_INVALID
+    assert call(groups=2) == tcg.ERR_INVALID                  # groups need offsets
+    assert call(groups=1025, offsets=0x50000) == tcg.ERR_UNSUPPORTED
+    assert call(group=0) == tcg.ERR_INVALID
+    assert call(group=16) == tcg.ERR_UNSUPPORTED
+    assert call(fmt=1, group=64) == tcg.ERR_INVALID           # MXFP4: 32
+    assert call(fmt=2, group=32) == tcg.ERR_INVALID           # NVFP4: 16
+    assert call(fmt=1, group=0, zero=0x60000) == tcg.ERR_INVALID
+    assert call(K=80, group=32) == tcg.ERR_ALIGNMENT
+    assert call(K=96, group=64) == tcg.ERR_ALIGNMENT          # half a group
+    for p in ("A", "B", "scale", "D"):
+        assert call(**{p: None}) == tcg.ERR_INVALID
+    assert call(lda=248) == tcg.ERR_INVALID
+    assert call(ldb=224) == tcg.ERR_INVALID
+    assert call(ld_scale=3) == tcg.ERR_INVALID
+    assert call(ldd=63) == tcg.ERR_INVALID
+    assert call(stride_b=-32) == tcg.ERR_INVALID
+    assert call(lda=260) == tcg.ERR_ALIGNMENT
+    assert call(ldb=272) == tcg.ERR_ALIGNMENT
+    assert call(stride_b=16) == tcg.ERR_ALIGNMENT
+    assert call(A=0x10008) == tcg.ERR_ALIGNMENT
+    assert call(B=0x20008) == tcg.ERR_ALIGNMENT
+    assert call(scale=0x30001) == tcg.ERR_ALIGNMENT
+    assert call(alpha=0x50002) == tcg.ERR_ALIGNMENT
+    assert call(D=0x40001) == tcg.ERR_ALIGNMENT
+    assert call(R=0, A=None, B=None, scale=None, D=None) == tcg.OK
+    assert call(N=0, A=None, B=None, scale=None, D=None) == tcg.OK

@@ -1,0 +1,238 @@
+"""Products of sorted rows with their group's matrix and the matrices' gradient
+against float64, at sizes that cut tiles, with empty groups and loose rows.
+
+Tolerance: products of 16-bit values are exact in fp32, and a sum of K of them
+makes at most K roundings of 2^-23 relative to the sum of magnitudes (the
+tensor core may truncate), so |error| <= K 2^-23 sum |a b| before the rounding
+to the stored type."""
+import numpy as np
+import pytest
+import torch
+
+from moe_cases import DTYPE, IN_TYPE, TORCH, close, group_offsets, rows, to_host
+
+pytestmark = pytest.mark.gpu
+
+
+@pytest.fixture(scope="module")
+def tcg():
+    assert torch.cuda.is_available(), "GPU tests need a GPU"
+    from blackwell_tensor_core_swizzled_gb300 import build
+    build.build()
+    import blackwell_tensor_core_swizzled_gb300 as m
+    return m
+
+
+def _ok(tcg):
+    rc = tcg.check()
+    assert rc == 0, tcg.last_error_string()
+
+
+def pad_to(n, extra=0):
+    """Padding that makes a row of n elements a multiple of 8, plus `extra` octets."""
+    return -n % 8 + 8 * extra
+
+
+CASES = [
+    # sizes of the groups, loose rows before and after, N, K, B rows padded by
+    ([1], 0, 0, 8, 8, 0),
+    ([5], 0, 0, 1, 1, 0),
+    ([0, 3, 0, 0, 130, 1, 0], 0, 0, 264, 72, 1),
+    ([128, 128, 256], 0, 0, 256, 128, 0),
+    ([17, 33, 64, 65, 127, 129], 0, 5, 200, 136, 0),
+    ([700, 0, 300], 3, 4, 130, 520, 1),
+    ([0, 0, 0], 0, 9, 72, 64, 0),
+    ([257, 255, 513], 0, 0, 513, 1000, 0),
+    ([3] * 40, 1, 1, 384, 192, 0),
+    ([1, 2, 4, 8, 16, 31, 32, 48], 0, 0, 1030, 2056, 0),
+    ([2100], 0, 0, 300, 64, 0),
+]
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f16"])
+@pytest.mark.parametrize("major", ["k", "mn"])
+@pytest.mark.parametrize("sizes,before,after,N,K,extra", CASES)
+def test_grouped(tcg, dtype, major, sizes, before, after, N, K, extra):
+    G, R = len(sizes), sum(sizes) + before + after
+    off = group_offsets(sizes, before)
+    A, a = rows((R, K), dtype, 1, pad_to(K, 1))
+    shape = (G, N, K) if major == "k" else (G, K, N)
+    B, b = rows(shape, dtype, 2, pad_to(shape[2], extra))
+    if major == "mn":
+        b = b.transpose(0, 2, 1)
+    for out in (dtype, "f32") if sizes != [2100] else ("bf16",):
+        D = torch.full((R, N + 3), 7.0, dtype=TORCH[out], device="cuda")
+        tcg.gemm_grouped(IN_TYPE[dtype], R, N, K, G, A, A.shape[1], torch.from_numpy(off).cuda(), B,
+                         tcg.K_MAJOR if major == "k" else tcg.MN_MAJOR, B.shape[2], 0, D, DTYPE[out], N + 3)
+        _ok(tcg)
+        ref, S = np.zeros((R, N)), np.zeros((R, N))
+        for g in range(G):
+            sl = slice(off[g], off[g + 1])
+            ref[sl], S[sl] = a[sl] @ b[g].T, np.abs(a[sl]) @ np.abs(b[g].T)
+        close(to_host(D)[:, :N], ref, S, K * 2.0 ** -23, out, (major, out))
+        assert bool((D[:, N:] == 7.0).all()), "wrote past the row"
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f16"])
+@pytest.mark.parametrize("sizes,before,after,N,K,extra", CASES)
+def test_wgrad(tcg, dtype, sizes, before, after, N, K, extra):
+    G, R = len(sizes), sum(sizes) + before + after
+    off = group_offsets(sizes, before)
+    DY, dy = rows((R, N), dtype, 3, pad_to(N, extra))
+    A, a = rows((R, K), dtype, 4, pad_to(K, 1))
+    for out in (dtype, "f32"):
+        DW = torch.full((G, N, K + 5), 7.0, dtype=TORCH[out], device="cuda")
+        tcg.gemm_grouped_wgrad(IN_TYPE[dtype], R, N, K, G, DY, DY.shape[1], A, A.shape[1],
+                               torch.from_numpy(off).cuda(), DW, DTYPE[out], K + 5, 0)
+        _ok(tcg)
+        ref, S = np.zeros((G, N, K)), np.zeros((G, N, K))
+        for g in range(G):
+            sl = slice(off[g], off[g + 1])
+            ref[g], S[g] = dy[sl].T @ a[sl], np.abs(dy[sl]).T @ np.abs(a[sl])
+        close(to_host(DW)[:, :, :K], ref, S, max(sizes) * 2.0 ** -23, out, out)
+        assert bool((DW[:, :, K:] == 7.0).all())
+
+
+def test_gradients_against_differences(tcg):
+    """Small integers: every sum is exact, so the gradients equal differences
+    of L = <DY, grouped(A, B)> exactly (it is bilinear)."""
+    sizes, N, K = [3, 0, 20, 6], 40, 24
+    G, R = len(sizes), sum(sizes)
+    off = torch.from_numpy(group_offsets(sizes)).cuda()
+    rng = np.random.default_rng(9)
+
+    def ints(*s):
+        return torch.from_numpy(rng.integers(-3, 4, size=s)).to(torch.bfloat16).cuda()
+    A, B, DY = ints(R, K), ints(G, N, K), ints(R, N)
+
+    def loss(a, b):
+        D = torch.empty(R, N, device="cuda")
+        tcg.gemm_grouped(tcg.IN_BF16, R, N, K, G, a, K, off, b, tcg.K_MAJOR, K, 0, D, tcg.F32, N)
+        return float((D * DY.float()).double().sum())
+    DA = torch.empty(R, K, device="cuda")
+    tcg.gemm_grouped(tcg.IN_BF16, R, K, N, G, DY, N, off, B, tcg.MN_MAJOR, K, N * K, DA, tcg.F32, K)
+    DW = torch.empty(G, N, K, device="cuda")
+    tcg.gemm_grouped_wgrad(tcg.IN_BF16, R, N, K, G, DY, N, A, K, off, DW, tcg.F32, K, N * K)
+    base = loss(A, B)
+    for i in range(R):
+        a2 = A.clone()
+        a2[i, (7 * i) % K] += 1
+        assert loss(a2, B) - base == float(DA[i, (7 * i) % K])
+    for g in range(G):
+        for n in (0, 17, N - 1):
+            b2 = B.clone()
+            b2[g, n, (n + g) % K] += 1
+            assert loss(A, b2) - base == float(DW[g, n, (n + g) % K])
+
+
+@pytest.mark.parametrize("bad", [float("nan"), float("inf")])
+def test_other_groups_values_stay_out(tcg, bad):
+    """NaN and infinities in one group's rows or matrix reach no other group,
+    nor do they come back through loose rows."""
+    sizes, N, K = [5, 9, 70, 3], 136, 72
+    G, R = len(sizes), sum(sizes) + 4
+    off = group_offsets(sizes, 2)
+    t_off = torch.from_numpy(off).cuda()
+    A, _ = rows((R, K), "bf16", 1)
+    B, _ = rows((G, N, K), "bf16", 2)
+    DY, _ = rows((R, N), "bf16", 3)
+    outs = []
+    for poison in (False, True):
+        if poison:
+            A[off[1]:off[2]] = bad
+            A[:2], A[-2:], DY[:2], DY[-2:] = bad, bad, bad, bad
+            B[2] = bad
+            DY[off[1]:off[2]] = bad
+        D = torch.empty(R, N, device="cuda")
+        tcg.gemm_grouped(tcg.IN_BF16, R, N, K, G, A, K, t_off, B, tcg.K_MAJOR, K, 0, D, tcg.F32, N)
+        DW = torch.empty(G, N, K, device="cuda")
+        tcg.gemm_grouped_wgrad(tcg.IN_BF16, R, N, K, G, DY, N, A, K, t_off, DW, tcg.F32, K, 0)
+        _ok(tcg)
+        outs.append((D, DW))
+    (d0, w0), (d1, w1) = outs
+    for g in (0, 3):
+        assert torch.equal(d0[off[g]:off[g + 1]], d1[off[g]:off[g + 1]])
+    for g in (0, 2, 3):
+        assert torch.equal(w0[g], w1[g])
+    assert not bool(d1[off[1]:off[2]].isfinite().any()) and not bool(w1[1].isfinite().any())
+    assert bool((d1[:2] == 0).all()) and bool((d1[-2:] == 0).all())
+
+
+def test_wild_offsets_stay_in_range(tcg):
+    """Offsets that decrease, are negative or pass R are clamped to [previous, R]."""
+    R, N, K = 40, 16, 16
+    A, a = rows((R, K), "bf16", 1)
+    B, b = rows((4, N, K), "bf16", 2)
+    off = torch.tensor([-5, 10, 4, 1000000, 7], dtype=torch.int32, device="cuda")   # 0, 10, 10, 40, 40
+    D = torch.empty(R, N, device="cuda")
+    tcg.gemm_grouped(tcg.IN_BF16, R, N, K, 4, A, K, off, B, tcg.K_MAJOR, K, 0, D, tcg.F32, N)
+    DW = torch.empty(4, N, K, device="cuda")
+    tcg.gemm_grouped_wgrad(tcg.IN_BF16, R, N, K, 4, A, K, A, K, off, DW, tcg.F32, K, 0)
+    _ok(tcg)
+    ref = np.concatenate([a[:10] @ b[0].T, a[10:] @ b[2].T])
+    S = np.concatenate([np.abs(a[:10]) @ np.abs(b[0].T), np.abs(a[10:]) @ np.abs(b[2].T)])
+    close(to_host(D), ref, S, K * 2.0 ** -23, "f32")
+    wref = np.stack([a[:10].T @ a[:10], np.zeros((N, K)), a[10:].T @ a[10:], np.zeros((N, K))])
+    wS = np.stack([np.abs(a[:10]).T @ np.abs(a[:10]), np.zeros((N, K)), np.abs(a[10:]).T @ np.abs(a[10:]),
+                   np.zeros((N, K))])
+    close(to_host(DW), wref, wS, R * 2.0 ** -23, "f32")
+
+
+def test_empty_contractions(tcg):
+    off = torch.tensor([0, 3, 5], dtype=torch.int32, device="cuda")
+    D = torch.full((5, 24), 7.0, device="cuda")
+    tcg.gemm_grouped(tcg.IN_BF16, 5, 24, 0, 2, None, 0, off, None, tcg.K_MAJOR, 0, 0, D, tcg.F32, 24)
+    DW = torch.full((2, 24, 8), 7.0, device="cuda")
+    zero = torch.zeros(3, dtype=torch.int32, device="cuda")
+    tcg.gemm_grouped_wgrad(tcg.IN_BF16, 0, 24, 8, 2, None, 0, None, 0, zero, DW, tcg.F32, 8, 0)
+    _ok(tcg)
+    assert bool((D == 0).all()) and bool((DW == 0).all())
+
+
+def test_separate_matrices_and_many_groups(tcg):
+    """A stride between the groups' matrices beyond N * ldb, and 1000 groups."""
+    rng = np.random.default_rng(4)
+    sizes = rng.integers(0, 4, size=1000)
+    G, R, N, K = 1000, int(sizes.sum()), 24, 40
+    off = group_offsets(sizes)
+    A, a = rows((R, K), "f16", 1)
+    Bfull, b = rows((G, N + 2, K), "f16", 2)
+    D = torch.empty(R, N, device="cuda", dtype=torch.float16)
+    tcg.gemm_grouped(tcg.IN_F16, R, N, K, G, A, K, torch.from_numpy(off).cuda(), Bfull, tcg.K_MAJOR, K,
+                     (N + 2) * K, D, tcg.F16, N)
+    DWfull = torch.full((G, N + 2, K), 7.0, device="cuda")
+    tcg.gemm_grouped_wgrad(tcg.IN_F16, R, K, K, G, A, K, A, K, torch.from_numpy(off).cuda(),
+                           torch.empty(G, K, K, device="cuda"), tcg.F32, K, 0)
+    DY, dy = rows((R, N), "f16", 5)
+    tcg.gemm_grouped_wgrad(tcg.IN_F16, R, N, K, G, DY, N, A, K, torch.from_numpy(off).cuda(), DWfull, tcg.F32, K,
+                           (N + 2) * K)
+    _ok(tcg)
+    group = np.repeat(np.arange(G), sizes)
+    ref = np.einsum("rk,rnk->rn", a, b[group][:, :N])
+    S = np.einsum("rk,rnk->rn", np.abs(a), np.abs(b[group][:, :N]))
+    close(to_host(D), ref, S, K * 2.0 ** -23, "f16")
+    wref, wS = np.zeros((G, N, K)), np.zeros((G, N, K))
+    np.add.at(wref, group, dy[:, :, None] * a[:, None])
+    np.add.at(wS, group, np.abs(dy[:, :, None] * a[:, None]))
+    close(to_host(DWfull)[:, :N], wref, wS, 4 * 2.0 ** -23, "f32")
+    assert bool((DWfull[:, N:] == 7.0).all())
+
+
+def test_rerun_is_identical_and_other_streams(tcg):
+    sizes = [100, 0, 345, 60]
+    R, N, K = sum(sizes), 520, 384
+    off = torch.from_numpy(group_offsets(sizes)).cuda()
+    A, _ = rows((R, K), "bf16", 1)
+    B, _ = rows((4, N, K), "bf16", 2)
+    DY, _ = rows((R, N), "bf16", 3)
+    torch.cuda.synchronize()
+    outs = []
+    for st in (torch.cuda.Stream(), torch.cuda.Stream(), torch.cuda.current_stream()):
+        D = torch.empty(R, N, device="cuda", dtype=torch.bfloat16)
+        DW = torch.empty(4, N, K, device="cuda")
+        tcg.gemm_grouped(tcg.IN_BF16, R, N, K, 4, A, K, off, B, tcg.K_MAJOR, K, 0, D, tcg.BF16, N, stream=st)
+        tcg.gemm_grouped_wgrad(tcg.IN_BF16, R, N, K, 4, DY, N, A, K, off, DW, tcg.F32, K, 0, stream=st)
+        outs.append((D, DW))
+    torch.cuda.synchronize()
+    for D, DW in outs[1:]:
+        assert torch.equal(D, outs[0][0]) and torch.equal(DW, outs[0][1])
