@@ -860,6 +860,35 @@ unsigned long long* device_error_word(int dev) {
   return st ? st->err : nullptr;
 }
 
+int device_sms(int dev) { return device_state(dev)->sms; }
+
+int max_resident_clusters(int dev, const KernelInfo& ki, int* out) {
+  return max_clusters_for(device_state(dev), ki, out);
+}
+
+int stream_workspace(int dev, cudaStream_t s, size_t bytes, void** out) { return workspace(dev, s, bytes, out); }
+
+int make_operand_map(CUtensorMap* map, const void* base, bool bf16, uint64_t inner, uint64_t mid, uint64_t outer,
+                     uint64_t stride_mid, uint64_t stride_outer, uint32_t box_mid) {
+  if (encode_ready() != TCG_OK) {
+    t_last_error = "cuTensorMapEncodeTiled entry point unavailable";
+    return TCG_ERR_CUDA;
+  }
+  const cuuint64_t dims[3] = {inner, mid, outer};
+  const cuuint64_t strides[2] = {2 * stride_mid, 2 * stride_outer};
+  const cuuint32_t box[3] = {64, box_mid, 1};
+  const cuuint32_t estr[3] = {1, 1, 1};
+  const CUresult r = g_encode(map, bf16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16,
+                              outer ? 3 : 2, const_cast<void*>(base), dims, strides, box, estr,
+                              CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+                              CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+  if (r != CUDA_SUCCESS) {
+    t_last_error = "cuTensorMapEncodeTiled (grouped operand) failed (" + std::to_string(static_cast<int>(r)) + ")";
+    return TCG_ERR_CUDA;
+  }
+  return TCG_OK;
+}
+
 uint64_t wait_timeout_ns() {
   load_timeout_env();
   return g_timeout_ns.load();

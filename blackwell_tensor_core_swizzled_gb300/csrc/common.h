@@ -1,6 +1,7 @@
 // Internal host-side interface shared by the library's translation units.
 #pragma once
 
+#include <cuda.h>
 #include <cuda_runtime.h>
 
 #include <cstdint>
@@ -68,6 +69,17 @@ int record_cuda(cudaError_t e);              // stores the message, returns TCG_
 int current_device_checked(int* dev);        // TCG_OK if the current device is usable sm_103
 unsigned long long* device_error_word(int dev);
 uint64_t wait_timeout_ns();
+// SMs of a device current_device_checked accepted.
+int device_sms(int dev);
+// Clusters of the variant that fit on the device at once (its shared-memory
+// attribute is set on the first call).
+int max_resident_clusters(int dev, const KernelInfo& ki, int* out);
+// The stream's library workspace, at least `bytes` (grown when smaller).
+int stream_workspace(int dev, cudaStream_t s, size_t bytes, void** out);
+// 128-byte swizzled tiled map of 16-bit elements over [outer][mid][inner] with
+// strides in elements, boxes of 64 x box_mid (x 1); outer 0: a 2-D map.
+int make_operand_map(CUtensorMap* map, const void* base, bool bf16, uint64_t inner, uint64_t mid, uint64_t outer,
+                     uint64_t stride_mid, uint64_t stride_outer, uint32_t box_mid);
 void set_launch_count(int n);
 
 }  // namespace tcg

@@ -1,12 +1,47 @@
 // Products of sorted rows with their group's matrix, and the gradient of the
-// matrices.  Entry points and kernels; the contract is in include/tcg.h.
+// matrices, on the tensor cores.  Entry points, host plan and kernel; the
+// contract is in include/tcg.h.
+//
+// One kernel serves all three products.  It computes C[m, c] = sum_k P[m, k]
+// Q[c, k] in tiles of 128 * CG rows m by up to BN columns c and stores it
+// transposed, element (m, c) at out[c * ldd + m]:
+//
+//             P (MMA rows)              Q (MMA columns)      contraction
+//   forward   B[g], rows n, K-major     the group's rows r   K
+//   input     B[g], rows n, MN-major    the group's rows r   K
+//   weight    A, columns k, MN-major    DY, columns n        the group's rows
+//
+// The ragged extent of a product, the group's rows, is thus on the MMA's N
+// side, which any multiple of 16 (32 for a CTA pair) up to 256 may have: a
+// tile with few rows costs few columns, nothing is padded in memory, and no
+// tile store needs clipping at a group's end, because a warp stores one
+// output row segment (32 lanes, consecutive m) at a time.  A group's rows are
+// split evenly into as few tiles of at most BN as they need.
+//
+// In the weight product the contraction is ragged: the last 64-row block of a
+// group also loads rows of the next group.  The MMAs of 16 rows beyond the
+// end are not issued, and the rows of the last partial 16 are overwritten with
+// zeros in shared memory (both operands: the neighbour's rows may hold
+// infinities) before the MMA reads them.
+//
+// The structure is the dense kernel's: a persistent CTA (or pair) per SM, a
+// TMA producer warp, an MMA warp, two accumulators in TMEM, epilogue warps.
+// The tile list depends on offsets, which only the device knows, so each CTA
+// reads them once and keeps the running tile count per group in shared memory;
+// a unit index is turned into (group, tile) by a binary search.
+#include <cuda.h>
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 #include <cuda_runtime.h>
 
+#include <algorithm>
 #include <cstdint>
+#include <cstring>
 
 #include "common.h"
+#include "desc.cuh"
+#include "gemm_kernel.cuh"
+#include "ptx.cuh"
 
 namespace tcg {
 
@@ -14,121 +49,475 @@ namespace {
 
 constexpr int MAX_GROUPS = 1024;
 constexpr int64_t MAX_EXTENT = int64_t{1} << 30;
+constexpr int EPI_WARPS = 8;
+constexpr int GROUPED_THREADS = 32 * (4 + EPI_WARPS);
+constexpr int BAND = 8;  // column tiles of a group that sweep its row tiles together
 
-struct GroupedArgs {
-  const void *A, *B;
+struct GroupedParams {
+  CUtensorMap tmap_p;    // [G or 1][rows][64-element boxes]
+  CUtensorMap tmap_q;    // Q in boxes of a full tile's rows (MN-major: 64)
+  CUtensorMap tmap_q16;  // K-major Q in boxes of 16 rows, for partial tiles
   const int32_t* offsets;
+  int G, R;
+  int weight;    // the contraction runs over the group's rows
+  int p_mn;      // P is MN-major
+  int M;         // extent of m
+  int C;         // weight: extent of c
+  int K;         // forward, input: contraction length
+  int m_tiles;
+  uint64_t p_hi, q_hi;
+  uint32_t p_kstep, q_kstep;  // 16-byte units per 16 of the contraction
+  uint32_t idesc;             // without N
   void* D;
-  int64_t R, N, K, lda, ldb, stride_b, ldd, stride_d;
-  int G;
-  int bf16, mn, d_type;
+  int64_t ldd, stride_d;
+  int d_type;
+  unsigned long long* err;
+  uint64_t timeout_ns;
 };
 
-__device__ __forceinline__ float load16(const void* p, int64_t i, int bf16) {
-  return bf16 ? __bfloat162float(static_cast<const __nv_bfloat16*>(p)[i])
-              : __half2float(static_cast<const __half*>(p)[i]);
+template <int CG, int BN, int STAGES>
+struct GroupedCfg {
+  static constexpr int P_BYTES = 128 * 128;
+  static constexpr int Q_ROWS = BN / CG;
+  static constexpr int Q_BYTES = Q_ROWS * 128;
+  static constexpr int STAGE_BYTES = P_BYTES + Q_BYTES;
+  static constexpr int BAR_OFF = STAGES * STAGE_BYTES;
+  // full[S], empty[S], rag[S], peer[S], acc_full[2], acc_empty[2], drain
+  static constexpr int NUM_BARS = 4 * STAGES + 5;
+  static constexpr int SEG_OFF = BAR_OFF + NUM_BARS * 8 + 8;  // then tmem slot + abort flag before it
+  static constexpr int SMEM_BYTES = 1024 + SEG_OFF + 2 * (MAX_GROUPS + 1) * 4;
+  static_assert(Q_BYTES % 1024 == 0, "swizzle period");
+  static_assert(SMEM_BYTES <= 232448, "dynamic shared memory");
+  static_assert(2 * BN <= 512, "two accumulators");
+};
+
+// One unit: a tile of one group.
+struct GTile {
+  int g;
+  int lo;     // first row of the group
+  int m0;     // first m of the tile (of the pair's tile)
+  int c0;     // first column within the group (weight: within C)
+  int ncols;  // columns of the tile that exist
+  int mma_n;  // columns the MMA computes
+  int nkb;    // 64-deep blocks of the contraction (0: the tile is zero)
+  int last;   // depth of the last block
+};
+
+// A group's columns n: tiles of `per` columns each, the last one shorter.
+template <int CG, int BN>
+__device__ __forceinline__ void split_columns(int n, int& tiles, int& per) {
+  const int t = (n + BN - 1) / BN;
+  per = t ? ((n + t - 1) / t + 16 * CG - 1) / (16 * CG) * (16 * CG) : 16 * CG;
+  tiles = (n + per - 1) / per;
 }
 
-__device__ __forceinline__ void store_out(void* p, int64_t i, int type, float v) {
-  if (type == TCG_F32)
-    static_cast<float*>(p)[i] = v;
-  else if (type == TCG_F16)
-    static_cast<__half*>(p)[i] = __float2half_rn(v);
-  else
-    static_cast<__nv_bfloat16*>(p)[i] = __float2bfloat16_rn(v);
-}
-
-// offsets[g] as the kernels use it: never below the previous one, never past R
-__device__ __forceinline__ int64_t clamp_offset(int64_t o, int64_t lo, int64_t R) {
-  return o < lo ? lo : o > R ? R : o;
-}
-
-// 64 x 64 tiles of C = P^T Q over a contracted range, 256 threads, 4 x 4 each.
-// Forward: one block per (row tile, column tile), each row of the tile with
-// its own group, the tile walked group by group.
-__global__ void __launch_bounds__(256) grouped_kernel(const GroupedArgs a) {
-  __shared__ float sa[16][65], sb[16][65];
-  __shared__ int64_t bounds[2];
-  const int tx = threadIdx.x & 15, ty = threadIdx.x >> 4;
-  const int64_t r0 = static_cast<int64_t>(blockIdx.y) * 64, n0 = static_cast<int64_t>(blockIdx.x) * 64;
-  float out[4][4] = {};
-  int64_t prev = 0;
-  for (int g = 0; g < a.G; ++g) {
-    if (threadIdx.x == 0) {
-      bounds[0] = clamp_offset(a.offsets[g], prev, a.R);
-      bounds[1] = clamp_offset(a.offsets[g + 1], bounds[0], a.R);
+// seg[0..G]: clamped offsets; pre[0..G]: units of the groups before (forward).
+template <int CG, int BN>
+__device__ __forceinline__ GTile decode_unit(const GroupedParams& p, const int* seg, const int* pre, int u) {
+  GTile t;
+  int v, tiles, per, n;
+  if (p.weight) {
+    split_columns<CG, BN>(p.C, tiles, per);
+    const int per_group = tiles * p.m_tiles;
+    t.g = u / per_group;
+    v = u - t.g * per_group;
+    n = p.C;
+  } else {
+    int a = 0, b = p.G;  // pre[a] <= u < pre[b]
+    while (b - a > 1) {
+      const int mid = (a + b) >> 1;
+      if (pre[mid] <= u)
+        a = mid;
+      else
+        b = mid;
     }
-    __syncthreads();
-    const int64_t lo = bounds[0], hi = bounds[1];
-    prev = lo;
-    __syncthreads();
-    if (hi <= r0 || lo >= r0 + 64 || lo == hi) continue;
-    float acc[4][4] = {};
-    for (int64_t k0 = 0; k0 < a.K; k0 += 16) {
-      for (int i = threadIdx.x; i < 1024; i += 256) {
-        const int kk = i & 15, m = i >> 4;
-        sa[kk][m] = r0 + m < a.R && k0 + kk < a.K ? load16(a.A, (r0 + m) * a.lda + k0 + kk, a.bf16) : 0.0f;
-        const int64_t n = n0 + m, k = k0 + kk;
-        sb[kk][m] = n < a.N && k < a.K ? load16(a.B, g * a.stride_b + (a.mn ? k * a.ldb + n : n * a.ldb + k), a.bf16) : 0.0f;
-      }
-      __syncthreads();
-      for (int kk = 0; kk < 16; ++kk)
-        for (int i = 0; i < 4; ++i)
-          for (int j = 0; j < 4; ++j) acc[i][j] += sa[kk][ty + 16 * i] * sb[kk][tx + 16 * j];
-      __syncthreads();
-    }
-    for (int i = 0; i < 4; ++i) {
-      const int64_t r = r0 + ty + 16 * i;
-      if (r >= lo && r < hi)
-        for (int j = 0; j < 4; ++j) out[i][j] = acc[i][j];
+    t.g = a;
+    v = u - pre[a];
+    n = seg[a + 1] - seg[a];
+    split_columns<CG, BN>(n, tiles, per);
+  }
+  t.lo = seg[t.g];
+  const int depth = p.weight ? seg[t.g + 1] - t.lo : p.K;
+  const int band = v / (BAND * p.m_tiles);
+  const int first = band * BAND;
+  const int width = min(tiles - first, BAND);
+  v -= first * p.m_tiles;
+  t.m0 = (v / width) * (128 * CG);
+  t.c0 = (first + v % width) * per;
+  t.ncols = min(per, n - t.c0);
+  t.mma_n = (t.ncols + 16 * CG - 1) / (16 * CG) * (16 * CG);
+  t.nkb = (depth + 63) >> 6;
+  t.last = depth - 64 * (t.nkb - 1);
+  return t;
+}
+
+// Store 32 accumulator columns of one warp: lane = m, register i = column i.
+__device__ __forceinline__ void store_columns(const GroupedParams& p, int64_t base, int ncols, bool m_ok,
+                                              const uint32_t (&r)[32]) {
+  if (p.d_type == OUT_F32) {
+    uint32_t* dst = static_cast<uint32_t*>(p.D) + base;
+#pragma unroll
+    for (int i = 0; i < 32; ++i)
+      if (i < ncols && m_ok) dst[i * p.ldd] = r[i];
+  } else {
+    uint16_t* dst = static_cast<uint16_t*>(p.D) + base;
+    const bool bf = p.d_type == OUT_BF16;
+#pragma unroll
+    for (int i = 0; i < 32; i += 2) {
+      const uint32_t h = bf ? pack_bf16(r[i], r[i + 1]) : pack_f16(r[i], r[i + 1]);
+      if (i < ncols && m_ok) dst[i * p.ldd] = static_cast<uint16_t>(h);
+      if (i + 1 < ncols && m_ok) dst[(i + 1) * p.ldd] = static_cast<uint16_t>(h >> 16);
     }
   }
-  for (int i = 0; i < 4; ++i)
-    for (int j = 0; j < 4; ++j) {
-      const int64_t r = r0 + ty + 16 * i, n = n0 + tx + 16 * j;
-      if (r < a.R && n < a.N) store_out(a.D, r * a.ldd + n, a.d_type, out[i][j]);
-    }
 }
 
-// Matrix gradient: one block per (k tile, n tile, group); A = DY, B = A.
-__global__ void __launch_bounds__(256) grouped_wgrad_kernel(const GroupedArgs a) {
-  __shared__ float sa[16][65], sb[16][65];
-  __shared__ int64_t bounds[2];
-  const int tx = threadIdx.x & 15, ty = threadIdx.x >> 4;
-  const int64_t k0 = static_cast<int64_t>(blockIdx.x) * 64, n0 = static_cast<int64_t>(blockIdx.y) * 64;
-  const int g = blockIdx.z;
-  if (threadIdx.x == 0) {
-    int64_t lo = 0, hi = 0;
-    for (int i = 0; i <= g + 1; ++i) {
-      lo = hi;
-      hi = clamp_offset(a.offsets[i], hi, a.R);
-    }
-    bounds[0] = lo;
-    bounds[1] = hi;
+template <int CG, int BN, int STAGES>
+__global__ void __launch_bounds__(GROUPED_THREADS, 1) grouped_kernel(const __grid_constant__ GroupedParams p) {
+  using C = GroupedCfg<CG, BN, STAGES>;
+  extern __shared__ uint8_t smem_raw[];
+  const uint32_t raw = smem_u32(smem_raw);
+  const uint32_t sbase = (raw + 1023u) & ~1023u;
+  uint8_t* gbase = smem_raw + (sbase - raw);
+  const uint32_t bar0 = sbase + C::BAR_OFF;
+  auto full_bar = [&](uint32_t s) { return bar0 + 8u * s; };
+  auto empty_bar = [&](uint32_t s) { return bar0 + 8u * (STAGES + s); };
+  auto rag_bar = [&](uint32_t s) { return bar0 + 8u * (2 * STAGES + s); };
+  auto peer_bar = [&](uint32_t s) { return bar0 + 8u * (3 * STAGES + s); };
+  auto accf_bar = [&](uint32_t b) { return bar0 + 8u * (4 * STAGES + b); };
+  auto acce_bar = [&](uint32_t b) { return bar0 + 8u * (4 * STAGES + 2 + b); };
+  const uint32_t drain_bar = bar0 + 8u * (4 * STAGES + 4);
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(gbase + C::BAR_OFF + 8 * C::NUM_BARS);
+  volatile uint32_t* abort_flag = tmem_slot + 1;
+  int* seg = reinterpret_cast<int*>(gbase + C::SEG_OFF);
+  int* pre = seg + p.G + 1;
+
+  const int warp = threadIdx.x >> 5;
+  const int lane = threadIdx.x & 31;
+  const uint32_t rank = (CG == 2) ? cluster_ctarank() : 0u;
+  const int cluster_id = blockIdx.x / CG;
+  const int num_clusters = gridDim.x / CG;
+  const WaitCtx wctx{p.timeout_ns, p.err, abort_flag};
+
+  // the maps exist unless the contraction is empty
+  if (warp == 0 && lane == 0 && (p.weight ? p.R : p.K) > 0) {
+    prefetch_tmap(&p.tmap_p);
+    prefetch_tmap(&p.tmap_q);
+    if (!p.weight) prefetch_tmap(&p.tmap_q16);
   }
+  if (threadIdx.x == 96) {
+    for (uint32_t s = 0; s < STAGES; ++s) {
+      mbar_init(full_bar(s), 1);
+      mbar_init(empty_bar(s), 1);
+      mbar_init(rag_bar(s), 1);
+      mbar_init(peer_bar(s), 1);
+    }
+    for (uint32_t b = 0; b < 2; ++b) {
+      mbar_init(accf_bar(b), 1);
+      mbar_init(acce_bar(b), EPI_WARPS * CG);
+    }
+    mbar_init(drain_bar, 1);
+    *abort_flag = 0u;
+    fence_mbarrier_init();
+  }
+  // a programmatic dependent of the previous kernel: no global access before
+  griddep_wait();
+  if (warp == 2) {
+    tmem_alloc<CG>(smem_u32(tmem_slot), 512);
+    tmem_relinquish<CG>();
+  }
+  // offsets, each clamped to [the previous one, R], and the units before each group
+  for (int g = threadIdx.x; g <= p.G; g += GROUPED_THREADS) seg[g] = p.offsets[g];
   __syncthreads();
-  const int64_t lo = bounds[0], hi = bounds[1];
-  float acc[4][4] = {};
-  for (int64_t r0 = lo; r0 < hi; r0 += 16) {
-    for (int i = threadIdx.x; i < 1024; i += 256) {
-      const int m = i & 63, rr = i >> 6;
-      sa[rr][m] = r0 + rr < hi && n0 + m < a.N ? load16(a.A, (r0 + rr) * a.lda + n0 + m, a.bf16) : 0.0f;
-      sb[rr][m] = r0 + rr < hi && k0 + m < a.K ? load16(a.B, (r0 + rr) * a.ldb + k0 + m, a.bf16) : 0.0f;
+  if (warp == 3) {
+    int run_max = 0, run_units = 0;
+    for (int g0 = 0; g0 <= p.G; g0 += 32) {
+      const int g = g0 + lane;
+      int v = g <= p.G ? min(max(seg[g], 0), p.R) : 0;
+#pragma unroll
+      for (int d = 1; d < 32; d <<= 1) {
+        const int o = __shfl_up_sync(0xffffffffu, v, d);
+        if (lane >= d) v = max(v, o);
+      }
+      v = max(v, run_max);
+      int before = __shfl_up_sync(0xffffffffu, v, 1);
+      if (lane == 0) before = run_max;
+      // units of group g - 1
+      int tiles = 0, per, units = 0;
+      if (g >= 1 && g <= p.G && !p.weight) {
+        split_columns<CG, BN>(v - before, tiles, per);
+        units = tiles * p.m_tiles;
+      }
+#pragma unroll
+      for (int d = 1; d < 32; d <<= 1) {
+        const int o = __shfl_up_sync(0xffffffffu, units, d);
+        if (lane >= d) units += o;
+      }
+      units += run_units;
+      if (g <= p.G) {
+        seg[g] = v;
+        pre[g] = units;
+      }
+      run_max = __shfl_sync(0xffffffffu, v, 31);
+      run_units = __shfl_sync(0xffffffffu, units, 31);
     }
-    __syncthreads();
-    for (int rr = 0; rr < 16; ++rr)
-      for (int i = 0; i < 4; ++i)
-        for (int j = 0; j < 4; ++j) acc[i][j] += sa[rr][ty + 16 * i] * sb[rr][tx + 16 * j];
-    __syncthreads();
   }
-  for (int i = 0; i < 4; ++i)
-    for (int j = 0; j < 4; ++j) {
-      const int64_t n = n0 + ty + 16 * i, k = k0 + tx + 16 * j;
-      if (n < a.N && k < a.K) store_out(a.D, g * a.stride_d + n * a.ldd + k, a.d_type, acc[i][j]);
+  tc_fence_before();
+  __syncthreads();
+  if constexpr (CG == 2) cluster_sync();
+  tc_fence_after();
+  const uint32_t tmem_base = *tmem_slot;
+  griddep_launch_dependents();
+  int total_units;
+  if (p.weight) {
+    int tiles, per;
+    split_columns<CG, BN>(p.C, tiles, per);
+    total_units = p.G * tiles * p.m_tiles;
+  } else {
+    total_units = p.K > 0 ? pre[p.G] : 0;
+  }
+
+  if (warp == 0) {
+    // ------------------------------------------------------------ producer
+    uint32_t it = 0, s = 0, ph = 0;
+    bool ok = true;
+    for (int u = cluster_id; u < total_units && ok; u += num_clusters) {
+      const GTile t = decode_unit<CG, BN>(p, seg, pre, u);
+      const int half = t.mma_n / CG;
+      const int m0 = t.m0 + static_cast<int>(rank) * 128;
+      const int c0 = t.c0 + static_cast<int>(rank) * half;
+      const int q_chunks = (half + 63) >> 6;
+      for (int kb = 0; kb < t.nkb; ++kb) {
+        if (!wait_uniform(empty_bar(s), ph ^ 1u, wctx, SITE_PROD_EMPTY)) {
+          ok = false;
+          break;
+        }
+        if (elect_one()) {
+          const uint32_t sp = sbase + s * C::STAGE_BYTES;
+          const uint32_t sq = sp + C::P_BYTES;
+          const uint32_t tx = C::P_BYTES + static_cast<uint32_t>(p.weight ? q_chunks * 8192 : half * 128);
+          const int k0 = 64 * kb;
+          if (p.weight) {
+            const int r0 = t.lo + k0;
+            if (kb == t.nkb - 1 && (t.last & 15)) {
+              // the warp that zeroes the rows past the group's end waits for
+              // this CTA's bytes alone; full[s] just marks the stage
+              if (rank == 0) mbar_arrive(full_bar(s));
+              mbar_arrive_expect_tx(rag_bar(s), tx);
+              for (int i = 0; i < 2; ++i) tma_load3<1>(sp + 8192 * i, &p.tmap_p, m0 + 64 * i, r0, 0, rag_bar(s));
+              for (int i = 0; i < q_chunks; ++i) tma_load_2d(sq + 8192 * i, &p.tmap_q, c0 + 64 * i, r0, rag_bar(s));
+            } else {
+              const uint32_t fb = (CG == 2) ? mapa_shared(full_bar(s), 0) : full_bar(s);
+              if (rank == 0) mbar_arrive_expect_tx(full_bar(s), tx * CG);
+              for (int i = 0; i < 2; ++i) tma_load3<CG>(sp + 8192 * i, &p.tmap_p, m0 + 64 * i, r0, 0, fb);
+              for (int i = 0; i < q_chunks; ++i) tma_load<CG>(sq + 8192 * i, &p.tmap_q, c0 + 64 * i, r0, fb);
+            }
+          } else {
+            const uint32_t fb = (CG == 2) ? mapa_shared(full_bar(s), 0) : full_bar(s);
+            if (rank == 0) mbar_arrive_expect_tx(full_bar(s), tx * CG);
+            if (p.p_mn) {
+              for (int i = 0; i < 2; ++i) tma_load3<CG>(sp + 8192 * i, &p.tmap_p, m0 + 64 * i, k0, t.g, fb);
+            } else {
+              tma_load3<CG>(sp, &p.tmap_p, k0, m0, t.g, fb);
+            }
+            if (half == C::Q_ROWS) {
+              tma_load<CG>(sq, &p.tmap_q, k0, t.lo + c0, fb);
+            } else {
+              for (int i = 0; i < half; i += 16) tma_load<CG>(sq + 128 * i, &p.tmap_q16, k0, t.lo + c0 + i, fb);
+            }
+          }
+        }
+        __syncwarp();
+        ++it;
+        if (++s == STAGES) {
+          s = 0;
+          ph ^= 1u;
+        }
+      }
     }
+    if (!ok && elect_one()) {
+      // let the copies in flight land before the CTA can exit: full[s] counts
+      // the leader's and (for a pair) the peer's; ragged stages are waited
+      // for by time, as the peer's are
+      const uint32_t n_out = it < static_cast<uint32_t>(STAGES) ? it : static_cast<uint32_t>(STAGES);
+      if ((CG == 1 || rank == 0) && !p.weight) {
+        for (uint32_t j = it - n_out; j < it; ++j) {
+          const uint64_t t0 = globaltimer();
+          while (!mbar_try_wait(full_bar(j % STAGES), (j / STAGES) & 1u) && globaltimer() - t0 < 20000000ull) {
+          }
+        }
+      } else {
+        const uint64_t t0 = globaltimer();
+        while (globaltimer() - t0 < 2000000ull) {
+        }
+      }
+    }
+    __syncwarp();
+  } else if (warp == 1) {
+    // --------------------------------- MMA issuer (leader), row zeroing (both)
+    const uint64_t p_desc0 = sdesc(sbase, p.p_hi);
+    const uint64_t q_desc0 = sdesc(sbase + C::P_BYTES, p.q_hi);
+    uint32_t s = 0, ph = 0, tcount = 0, rag_ph = 0;  // rag_ph: one parity bit per stage
+    bool ok = true;
+    for (int u = cluster_id; u < total_units && ok; u += num_clusters) {
+      const GTile t = decode_unit<CG, BN>(p, seg, pre, u);
+      if (t.nkb == 0) continue;
+      const bool issue = CG == 1 || rank == 0;
+      const uint32_t b = tcount & 1u;
+      if (issue) {
+        if (!wait_uniform(acce_bar(b), ((tcount >> 1) & 1u) ^ 1u, wctx, SITE_MMA_ACC_EMPTY)) {
+          ok = false;
+          break;
+        }
+        tc_fence_after();
+      }
+      ++tcount;
+      const uint32_t idesc = p.idesc | (static_cast<uint32_t>(t.mma_n >> 3) << 17);
+      const uint32_t d_tmem = tmem_base + b * BN;
+      for (int kb = 0; kb < t.nkb; ++kb) {
+        const bool last = kb == t.nkb - 1;
+        const bool ragged = p.weight && last && (t.last & 15);
+        if (issue && !wait_uniform(full_bar(s), ph, wctx, SITE_MMA_FULL)) {
+          ok = false;
+          break;
+        }
+        if (ragged) {
+          const uint32_t par = (rag_ph >> s) & 1u;
+          rag_ph ^= 1u << s;
+          if (!warp_wait(rag_bar(s), par, wctx, SITE_MMA_FULL)) {
+            ok = false;
+            break;
+          }
+          // rows [last, next multiple of 16) of the two P chunks and the Q
+          // chunks; a row's 128 bytes are the same under the swizzle
+          const uint32_t sp = sbase + s * C::STAGE_BYTES;
+          const int rows = 16 - (t.last & 15);
+          const int chunks = 2 + ((t.mma_n / CG + 63) >> 6);
+          for (int i = lane; i < chunks * rows * 8; i += 32) {
+            const int ch = i / (rows * 8), rr = i - ch * rows * 8;
+            const uint32_t at = (ch < 2 ? sp + 8192u * ch : sp + C::P_BYTES + 8192u * (ch - 2)) + 128u * (t.last + (rr >> 3)) +
+                                16u * (rr & 7);
+            st_shared_v4(at, 0u, 0u, 0u, 0u);
+          }
+          fence_proxy_async_shared();
+          __syncwarp();
+          if constexpr (CG == 2) {
+            if (rank != 0) {
+              if (lane == 0) mbar_arrive_cluster(mapa_shared(peer_bar(s), 0));
+            } else if (!warp_wait(peer_bar(s), par, wctx, SITE_MMA_FULL) || !mbar_try_wait_cluster(peer_bar(s), par)) {
+              ok = false;
+              break;
+            }
+          }
+        }
+        if (issue) {
+          tc_fence_after();
+          if (elect_one()) {
+            const uint64_t st = (s * static_cast<uint32_t>(C::STAGE_BYTES)) >> 4;
+            const int steps = last ? (t.last + 15) >> 4 : 4;
+#pragma unroll
+            for (int j = 0; j < 4; ++j)
+              if (j < steps)
+                mma_f16<CG>(d_tmem, p_desc0 + st + j * p.p_kstep, q_desc0 + st + j * p.q_kstep, idesc,
+                            (kb | j) ? 1u : 0u);
+            tc_commit<CG>(empty_bar(s));
+          }
+          __syncwarp();
+        }
+        if (++s == STAGES) {
+          s = 0;
+          ph ^= 1u;
+        }
+      }
+      if (!ok) break;
+      if (issue && elect_one()) tc_commit<CG>(accf_bar(b));
+      __syncwarp();
+    }
+    if (!ok && (CG == 1 || rank == 0) && elect_one()) {
+      tc_commit<CG>(drain_bar);
+      const uint64_t t0 = globaltimer();
+      while (!mbar_try_wait(drain_bar, 0) && globaltimer() - t0 < 20000000ull) {
+      }
+    }
+    __syncwarp();
+  } else if (warp >= 4) {
+    // ------------------------------------------------------------ epilogue
+    const int q = warp & 3;            // TMEM lane quadrant
+    const int part = (warp - 4) >> 2;  // 32-column chunks part, part + 2, ...
+    uint32_t tcount = 0;
+    for (int u = cluster_id; u < total_units; u += num_clusters) {
+      const GTile t = decode_unit<CG, BN>(p, seg, pre, u);
+      const int m = t.m0 + static_cast<int>(rank) * 128 + 32 * q + lane;
+      const bool m_ok = m < p.M;
+      const int64_t base = (p.weight ? t.g * p.stride_d + t.c0 * p.ldd : (t.lo + t.c0) * p.ldd) + m;
+      if (t.nkb == 0) {
+        const uint32_t zero[32] = {};
+        for (int c = 32 * part; c < t.ncols; c += 64) store_columns(p, base + c * p.ldd, t.ncols - c, m_ok, zero);
+        continue;
+      }
+      const uint32_t b = tcount & 1u;
+      if (!warp_wait(accf_bar(b), (tcount >> 1) & 1u, wctx, SITE_EPI_ACC_FULL)) break;
+      ++tcount;
+      tc_fence_after();
+      const uint32_t tb = tmem_base + (static_cast<uint32_t>(32 * q) << 16) + b * BN;
+#pragma unroll 1
+      for (int c = 32 * part; c < t.ncols; c += 64) {
+        uint32_t r[32];
+        tmem_ld_32x32b_x32(tb + c, r);
+        tc_wait_ld();
+        store_columns(p, base + c * p.ldd, t.ncols - c, m_ok, r);
+      }
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) {
+        if constexpr (CG == 2)
+          mbar_arrive_cluster(mapa_shared(acce_bar(b), 0));
+        else
+          mbar_arrive(acce_bar(b));
+      }
+    }
+    if (!p.weight) {
+      // rows of no group (and all rows when K is 0): zero
+      const int t = threadIdx.x - 128;
+      const int first = seg[0], end = p.K > 0 ? seg[p.G] : first;
+      for (int r = blockIdx.x; r < p.R; r += gridDim.x) {
+        if (r >= first && r < end) {
+          r += (end - 1 - r) / gridDim.x * gridDim.x;  // the last row below `end` this block meets
+          continue;
+        }
+        for (int m = t; m < p.M; m += 32 * EPI_WARPS) {
+          const int64_t i = r * p.ldd + m;
+          if (p.d_type == OUT_F32)
+            static_cast<float*>(p.D)[i] = 0.0f;
+          else
+            static_cast<uint16_t*>(p.D)[i] = 0;
+        }
+      }
+    }
+  }
+
+  // ------------------------------------------------------------ teardown
+  tc_fence_before();
+  cta_barrier_unaligned();
+  __syncwarp();
+  if constexpr (CG == 2) cluster_sync();
+  tc_fence_after();
+  if (warp == 2) tmem_dealloc<CG>(tmem_base, 512);
 }
 
 // ---------------------------------------------------------------------- host
+
+struct Variant {
+  KernelInfo ki;
+  int bn;
+};
+
+template <int CG, int BN, int STAGES>
+Variant variant() {
+  using C = GroupedCfg<CG, BN, STAGES>;
+  return {KernelInfo{reinterpret_cast<const void*>(&grouped_kernel<CG, BN, STAGES>), C::SMEM_BYTES, CG, BN, KIND_F16,
+                     GROUPED_THREADS},
+          BN};
+}
 
 int check_problem(tcg_input in_type, int64_t R, int64_t N, int64_t K, int G, tcg_dtype d_type) {
   if (in_type != TCG_IN_F16 && in_type != TCG_IN_BF16) return TCG_ERR_INVALID;
@@ -155,6 +544,36 @@ int check_offsets(const int32_t* p) {
   return reinterpret_cast<uintptr_t>(p) % 4 ? TCG_ERR_ALIGNMENT : TCG_OK;
 }
 
+int64_t ceil_div(int64_t a, int64_t b) { return (a + b - 1) / b; }
+
+// Launches the variant on all SMs (or on fewer, never more than `units`
+// clusters), as a programmatic dependent of the stream's previous kernel.
+int launch_grouped(const Variant& v, GroupedParams& p, int dev, int64_t units, cudaStream_t s) {
+  int clusters = 0;
+  if (int rc = max_resident_clusters(dev, v.ki, &clusters)) return rc;
+  const int cg = v.ki.cta_group;
+  p.err = device_error_word(dev);
+  p.timeout_ns = wait_timeout_ns();
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(static_cast<unsigned>(cg * std::max<int64_t>(1, std::min<int64_t>(units, clusters))), 1, 1);
+  cfg.blockDim = dim3(GROUPED_THREADS, 1, 1);
+  cfg.dynamicSmemBytes = v.ki.smem_bytes;
+  cfg.stream = s;
+  cudaLaunchAttribute attr[2];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  attr[1].id = cudaLaunchAttributeClusterDimension;
+  attr[1].val.clusterDim.x = cg;
+  attr[1].val.clusterDim.y = 1;
+  attr[1].val.clusterDim.z = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = cg > 1 ? 2 : 1;
+  void* args[] = {&p};
+  if (int rc = record_cuda(cudaLaunchKernelExC(&cfg, v.ki.func, args))) return rc;
+  set_launch_count(1);
+  return TCG_OK;
+}
+
 int run_grouped(tcg_input in_type, int64_t R, int64_t N, int64_t K, int G, const void* A, int64_t lda,
                 const int32_t* offsets, const void* B, tcg_major b_major, int64_t ldb, int64_t stride_b, void* D,
                 tcg_dtype d_type, int64_t ldd, cudaStream_t s) {
@@ -164,22 +583,48 @@ int run_grouped(tcg_input in_type, int64_t R, int64_t N, int64_t K, int G, const
   if (R == 0 || N == 0) return TCG_OK;
   if (int rc = check_output(D, N, &ldd, d_type)) return rc;
   if (int rc = check_offsets(offsets)) return rc;
+  const bool mn = b_major == TCG_MN_MAJOR;
   if (K > 0) {
-    const int64_t inner = b_major == TCG_K_MAJOR ? K : N, outer = b_major == TCG_K_MAJOR ? N : K;
     if (int rc = check_operand16(A, K, &lda)) return rc;
-    if (int rc = check_operand16(B, inner, &ldb)) return rc;
-    if (stride_b == 0) stride_b = outer * ldb;
+    if (int rc = check_operand16(B, mn ? N : K, &ldb)) return rc;
+    if (stride_b == 0) stride_b = (mn ? K : N) * ldb;
     if (stride_b < 0) return TCG_ERR_INVALID;
     if (stride_b % 8) return TCG_ERR_ALIGNMENT;
   }
   int dev;
   if (int rc = current_device_checked(&dev)) return rc;
-  GroupedArgs a{A, B, offsets, D, R, N, K, lda, ldb, stride_b, ldd, 0, G, in_type == TCG_IN_BF16,
-                b_major == TCG_MN_MAJOR, d_type};
-  grouped_kernel<<<dim3(static_cast<unsigned>((N + 63) / 64), static_cast<unsigned>((R + 63) / 64)), 256, 0, s>>>(a);
-  if (int rc = record_cuda(cudaGetLastError())) return rc;
-  set_launch_count(1);
-  return TCG_OK;
+  const bool bf16 = in_type == TCG_IN_BF16;
+  const bool wide = R > 64 * static_cast<int64_t>(G);
+  const Variant v = wide ? variant<2, 256, 6>() : variant<1, 64, 8>();
+  const int cg = v.ki.cta_group;
+  GroupedParams p;
+  std::memset(&p, 0, sizeof p);
+  if (K > 0) {
+    if (int rc = mn ? make_operand_map(&p.tmap_p, B, bf16, N, K, G, ldb, stride_b, 64)
+                    : make_operand_map(&p.tmap_p, B, bf16, K, N, G, ldb, stride_b, 128))
+      return rc;
+    if (int rc = make_operand_map(&p.tmap_q, A, bf16, K, R, 0, lda, 0, static_cast<uint32_t>(v.bn / cg))) return rc;
+    if (int rc = make_operand_map(&p.tmap_q16, A, bf16, K, R, 0, lda, 0, 16)) return rc;
+  }
+  p.offsets = offsets;
+  p.G = G;
+  p.R = static_cast<int>(R);
+  p.p_mn = mn;
+  p.M = static_cast<int>(N);
+  p.K = static_cast<int>(K);
+  p.m_tiles = static_cast<int>(ceil_div(N, 128 * cg));
+  p.p_hi = mn ? sdesc_hi(8192, 1024, SW_128B) : sdesc_hi(16, 1024, SW_128B);
+  p.p_kstep = mn ? 2048 / 16 : 32 / 16;
+  p.q_hi = sdesc_hi(16, 1024, SW_128B);
+  p.q_kstep = 32 / 16;
+  p.idesc = idesc_f16(bf16, true, mn, false, 128 * cg, 0);
+  p.D = D;
+  p.ldd = ldd;
+  p.d_type = d_type;
+  // an upper bound of the units: a full tile per BN rows and one more per group
+  const int64_t units = (R / v.bn + std::min<int64_t>(G, R)) * 2 * p.m_tiles;
+  if (units > INT32_MAX / 2) return TCG_ERR_UNSUPPORTED;
+  return launch_grouped(v, p, dev, units, s);
 }
 
 int run_wgrad(tcg_input in_type, int64_t R, int64_t N, int64_t K, int G, const void* DY, int64_t lddy, const void* A,
@@ -198,12 +643,33 @@ int run_wgrad(tcg_input in_type, int64_t R, int64_t N, int64_t K, int G, const v
   }
   int dev;
   if (int rc = current_device_checked(&dev)) return rc;
-  GroupedArgs a{DY, A, offsets, DW, R, N, K, lddy, lda, 0, lddw, stride_dw, G, in_type == TCG_IN_BF16, 0, dw_type};
-  grouped_wgrad_kernel<<<dim3(static_cast<unsigned>((K + 63) / 64), static_cast<unsigned>((N + 63) / 64),
-                              static_cast<unsigned>(G)), 256, 0, s>>>(a);
-  if (int rc = record_cuda(cudaGetLastError())) return rc;
-  set_launch_count(1);
-  return TCG_OK;
+  const bool bf16 = in_type == TCG_IN_BF16;
+  const Variant v = variant<2, 256, 6>();
+  const int cg = v.ki.cta_group;
+  GroupedParams p;
+  std::memset(&p, 0, sizeof p);
+  if (R > 0) {
+    if (int rc = make_operand_map(&p.tmap_p, A, bf16, K, R, 1, lda, R * lda, 64)) return rc;
+    if (int rc = make_operand_map(&p.tmap_q, DY, bf16, N, R, 0, lddy, 0, 64)) return rc;
+  }
+  p.offsets = offsets;
+  p.G = G;
+  p.R = static_cast<int>(R);
+  p.weight = 1;
+  p.p_mn = 1;
+  p.M = static_cast<int>(K);
+  p.C = static_cast<int>(N);
+  p.m_tiles = static_cast<int>(ceil_div(K, 128 * cg));
+  p.p_hi = p.q_hi = sdesc_hi(8192, 1024, SW_128B);
+  p.p_kstep = p.q_kstep = 2048 / 16;
+  p.idesc = idesc_f16(bf16, true, true, true, 128 * cg, 0);
+  p.D = DW;
+  p.ldd = lddw;
+  p.stride_d = stride_dw;
+  p.d_type = dw_type;
+  const int64_t units = static_cast<int64_t>(G) * 2 * ceil_div(N, v.bn) * p.m_tiles;
+  if (units > INT32_MAX / 2) return TCG_ERR_UNSUPPORTED;
+  return launch_grouped(v, p, dev, units, s);
 }
 
 }  // namespace
