@@ -375,9 +375,11 @@ typedef struct {
   const int32_t* offsets;                  /* device [G+1], or NULL with G == 1 */
   const uint8_t* B; int64_t ldb;           /* ldb in codes (0 = K), a multiple of 32; base 16-byte aligned */
   int64_t stride_b;                        /* codes between groups (0 = N * ldb), a multiple of 32 */
-  const void* scale;                       /* [G][N][K / group]: INT4 in in_type's type, else bytes */
+  const void* scale;                       /* [G][N][K / group]: INT4 in in_type's type, else bytes;
+                                              4-byte aligned base */
   int64_t ld_scale, stride_scale;          /* elements between rows / groups (0 = packed) */
-  const uint8_t* zero;                     /* INT4: [G][N][K / group] laid out as scale, or NULL: 8 */
+  const uint8_t* zero;                     /* INT4: [G][N][K / group] laid out as scale, 4-byte
+                                              aligned base, or NULL: 8 */
   const float* alpha;                      /* [G], or NULL: 1 */
   void* D; tcg_dtype d_type; int64_t ldd;  /* [R][N], element aligned */
 } tcg_gemv_w4_args;
