@@ -80,6 +80,14 @@ int stream_workspace(int dev, cudaStream_t s, size_t bytes, void** out);
 // strides in elements, boxes of 64 x box_mid (x 1); outer 0: a 2-D map.
 int make_operand_map(CUtensorMap* map, const void* base, bool bf16, uint64_t inner, uint64_t mid, uint64_t outer,
                      uint64_t stride_mid, uint64_t stride_outer, uint32_t box_mid);
+// The same over bytes, strides in bytes, boxes of box_inner (32, 64 or 128,
+// the swizzle's span) x box_mid x 1.
+int make_byte_map(CUtensorMap* map, const void* base, uint64_t inner, uint64_t mid, uint64_t outer,
+                  uint64_t stride_mid, uint64_t stride_outer, uint32_t box_inner, uint32_t box_mid);
+// Bytes of [outer][mid][slabs * inner] seen as [outer][slabs][mid][inner], boxes
+// of inner x box_mid x box_slabs x 1.
+int make_slab_map(CUtensorMap* map, const void* base, uint64_t inner, uint64_t mid, uint64_t slabs, uint64_t outer,
+                  uint64_t stride_mid, uint64_t stride_outer, uint32_t box_mid, uint32_t box_slabs);
 void set_launch_count(int n);
 
 }  // namespace tcg

@@ -5,24 +5,36 @@
 // Codes are decoded to f16 in registers (every E2M1 value, and code - zero of
 // INT4, is exact there) and multiplied by mma m16n8k16 with fp32
 // accumulation: 16 matrix rows by 8 activation rows, so that up to 8 rows cost
-// the decoding once.  (A 64 x 64-bit product on tcgen05 would take the decoded
-// codes through shared or tensor memory first; the register path has no such
-// stop, and at 8 rows the mma rate is a third of what HBM can feed.)  A
-// group's sum is multiplied by its scale in fp32: the scale meets sums, not
-// weights, which keeps every product exact.
+// the decoding once.  (A tcgen05 product would take the decoded codes through
+// shared or tensor memory first; the register path has no such stop, and at 8
+// rows the mma rate is a third of what HBM can feed.)  Scales keep every
+// product exact: NVFP4's unsigned E4M3 scale times an E2M1 value has 6
+// significant bits between 2^-10 and 2688, an f16 value, so it is multiplied
+// into the decoded codes and the whole contraction is one chain of mma; e8m0
+// and 16-bit scales do not fit f16 that way and multiply the group's fp32 sum.
 //
-// A warp owns a slab of 256 of K for KSL slabs and walks down the matrix in
-// tiles of 16 rows; its activations stay in registers for all of them.  A
-// team of warps covers K (across a cluster of CTAs when the slabs are more
-// than a CTA's warps), adds its warps' sums in a fixed order through shared
-// memory, and takes an equal share of the tiles.  Tiles arrive by cp.async
-// into a ring private to the warp: no barrier stands between load and use.
+// Decoding, not HBM, is the first bound: integer and conversion instructions
+// issue at half rate, so the 16 decoding warps do little else, and what feeds
+// and empties them has warps of its own:
+//   warps 0..15   a slab of 256 of K each, whose activations stay in
+//                 registers, walking down the matrix in tiles of 16 rows;
+//   warp 16       brings a tile into a ring of stages: codes, scales and zero
+//                 points by a TMA copy each, for all slabs at once (a copy
+//                 takes its issuing thread 150 cycles, one for every warp or
+//                 row would take longer than the decoding);
+//   warps 17..19  add the warps' parts of a tile in a fixed order and store it
+//                 while the next tiles are decoded.
+// A team of warps covers K (the 16, or fewer when K is short: then a CTA has
+// several teams) and takes an equal share of the matrix rows; a K of more
+// slabs than warps is taken in passes over a chunk of tiles, whose sums wait
+// in shared memory.  What lies beyond K or N is zero, so the inner loop has no
+// bounds.
 //
 // bf16 activations are brought into f16's range by a power of two per row and
-// slab (the largest finite value to [2^14, 2^15)), undone on each group's fp32
-// sum before its scale (the other order could overflow on the way): exact for values down to 2^-29 of the slab's largest; smaller ones
-// round at 2^-39 of it, below the fp32 sums' own rounding of that largest
-// value's product.
+// slab (the largest finite value to [2^14, 2^15)), undone on fp32 sums (before
+// a scale that could overflow with it): exact for values down to 2^-29 of the
+// slab's largest; smaller ones round at 2^-39 of it, below the fp32 sums' own
+// rounding of that largest value's product.
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 #include <cuda_runtime.h>
@@ -33,6 +45,7 @@
 #include <mutex>
 
 #include "common.h"
+#include "gemm_kernel.cuh"
 #include "ptx.cuh"
 
 namespace tcg {
@@ -42,80 +55,119 @@ namespace {
 constexpr int MAX_GROUPS = 1024;
 constexpr int64_t MAX_EXTENT = int64_t{1} << 30;
 
-constexpr int WARPS = 16;
-constexpr int THREADS = 32 * WARPS;
-constexpr int SLAB = 256;          // K per warp and tile: 128 bytes of codes
-constexpr int TILE_N = 16;         // matrix rows per tile
-constexpr int STAGES = 4;          // ring stages per warp
-constexpr int CODE_BYTES = TILE_N * SLAB / 2;
-constexpr int SCALE_PITCH = 20;    // bytes: up to 16 of scales, from a 4-byte boundary
-constexpr int ZERO_PITCH = 12;     // up to 8 of zero points
-constexpr int STAGE_BYTES = CODE_BYTES + TILE_N * (SCALE_PITCH + ZERO_PITCH);
-constexpr int PART_PITCH = 20;     // floats between activation rows of a partial tile
-constexpr int ROUND = 16;          // units a cluster sums before its CTAs meet
+constexpr int WARPS = 16;          // decoding warps
+constexpr int ADD_WARPS = 3;       // one for each buffer of parts
+constexpr int THREADS = 32 * (WARPS + 1 + ADD_WARPS);
+constexpr int SLAB = 256;          // K per warp: 128 bytes of codes
+constexpr int TILE_N = 16;         // matrix rows per tile: one mma's
+// bytes of a matrix row's scales, zero points in a stage when they are copied
+// word by word: up to 16, 8 a warp, and 4 a team for rows that start off a
+// 4-byte boundary; rows on different banks
+constexpr int SCALE_PITCH = 336, ZERO_PITCH = 208;
+// a swizzled box of rows of `span` bytes: where byte x of row r lies
+__device__ __forceinline__ uint32_t box_at(uint32_t r, uint32_t x, uint32_t span) {
+  const uint32_t swizzle = span == 128 ? r & 7u : span == 64 ? (r >> 1) & 3u : (r >> 2) & 1u;
+  return r * span + (x ^ (swizzle << 4));
+}
+
+// What a kernel is compiled for: a format, and for INT4 its group.
+enum Kind4 : int { K_INT4_32 = 0, K_INT4_64 = 1, K_INT4_128 = 2, K_MXF4 = 3, K_NVF4 = 4, KINDS4 = 5 };
+constexpr bool is_int4(int k) { return k <= K_INT4_128; }
+constexpr int group_of_kind(int k) { return k == K_NVF4 ? 16 : k == K_MXF4 ? 32 : 32 << k; }
+constexpr int scale_bytes(int k) { return SLAB / group_of_kind(k) * (is_int4(k) ? 2 : 1); }  // of a row's slab
+constexpr int GRAIN = 2;           // matrix rows: the unit in which teams share them
 
 struct GemvParams {
+  // codes as bytes in 128-byte swizzled boxes of 16 rows: whole slabs
+  // [G][K / 256][N][128], a team's slabs in one box (K a multiple of 256), or
+  // rows [G][N][K / 2], one slab a box
+  CUtensorMap tmap_b;
+  int whole;
+  // scales, zero points as bytes [G][N][bytes of a row] in swizzled boxes of 16
+  // rows, where their rows are 16-byte aligned (`bulk`)
+  CUtensorMap tmap_s, tmap_z;
+  int box_s, box_z;  // bytes of a box's rows: 32, 64 or 128
   int R, N, K, G;
-  int group_shift;   // log2 of K per scale
   const uint8_t* A;  // 16-bit elements
   int64_t lda;
+  int a_row_lines, a_lines;  // 128-byte lines of a row, of all rows
   const int32_t* offsets;
-  const uint8_t* B;
-  int64_t ldb, stride_b;  // bytes
   const uint8_t* scale;
-  int64_t ld_scale, stride_scale, scale_bytes;  // bytes; size of the array
+  int64_t ld_scale, stride_scale;  // bytes
+  int scale_row;                   // scales of a row
   const uint8_t* zero;
-  int64_t ld_zero, stride_zero, zero_bytes;
-  int scale_words, zero_words;  // 4-byte words that hold a row's slab of scales, zero points
+  int64_t ld_zero, stride_zero;
+  int bulk;
   const float* alpha;
   void* D;
   int d_type;
   int64_t ldd;
-  int tiles;        // 16-row tiles of a matrix
+  int grains;       // GRAIN-row units of a matrix
   int slabs;        // ceil(K / 256)
   int team_warps;   // warps of a team in one CTA
   int teams;        // teams in a CTA
+  unsigned long long* err;
+  uint64_t timeout_ns;
 };
 
-template <int NT>
-struct GemvSmem {
-  static constexpr int RING = WARPS * STAGES * STAGE_BYTES;
-  static constexpr int PART = 2 * WARPS * 8 * NT * PART_PITCH * 4;  // two tiles of every warp
-  static constexpr int SUM = ROUND * 8 * NT * 16 * 4;               // a cluster CTA's sums of a round
-  static constexpr int SEG = 2 * (MAX_GROUPS + 1) * 4;
-  static constexpr int BYTES = RING + PART + SUM + SEG;
+// TOK activation rows per block: 4, 8 or 16.  They are the columns of one mma
+// (16: of two); 4 rows take its even columns, which are half of a lane's
+// accumulators, so that scaling costs half.
+template <int TOK>
+struct Shape {
+  static constexpr int NT = TOK == 16 ? 2 : 1;        // mma column blocks
+  static constexpr int STEP = TOK == 4 ? 2 : 1;       // accumulator columns between rows
+  static constexpr int OUT = TOK * TILE_N;            // sums of a tile
+  static constexpr int CAP = (TOK == 16 ? 4096 : TOK == 8 ? 2048 : 1024) / OUT;  // tiles of a chunk that is passed over more than once
+  static constexpr int STAGES = TOK == 16 ? 3 : 4;    // ring stages
+  // buffers of parts: tile i of a chunk uses number i % PARTS, which adding
+  // warp i % PARTS empties, so that in every pass the same warp has the tile
+  static constexpr int PARTS = ADD_WARPS;
+  static constexpr int PART_PITCH = TOK == 4 ? 24 : 20;  // floats between a part's activation rows
+  static constexpr int TILE_PART = TOK * PART_PITCH;  // floats of a warp's part
+  // a stage: codes [warp][16 rows][128 bytes]; scales, then zero points [16 rows][pitch]
+  static constexpr int CODE_BYTES = WARPS * TILE_N * SLAB / 2;
+  static constexpr int SCALES = STAGES * CODE_BYTES;
+  // (boxes: up to 16 x 16 bytes a warp, teams on 1 KiB boundaries)
+  static constexpr int ZERO_OFF = 6 * 1024;
+  static constexpr int SCALE_STAGE = 10 * 1024;
+  static_assert(TILE_N * SCALE_PITCH <= ZERO_OFF && TILE_N * ZERO_PITCH <= SCALE_STAGE - ZERO_OFF, "");
+  static constexpr int PART = SCALES + STAGES * SCALE_STAGE;
+  // an activation row on its way to each warp's registers
+  static constexpr int ACT = PART + PARTS * WARPS * TILE_PART * 4;
+  static constexpr int ACT_BYTES = TOK == 4 ? SLAB * 2 : 0;
+  static constexpr int SUM = ACT + WARPS * ACT_BYTES;
+  // per team: full[STAGES], empty[STAGES], part_full[PARTS], part_free[PARTS]
+  static constexpr int BARS = SUM + CAP * OUT * 4;
+  static constexpr int TEAM_BARS = 2 * STAGES + 2 * PARTS;
+  static constexpr int SEG = BARS + WARPS * TEAM_BARS * 8 + 8;
+  static constexpr int BYTES = 1024 + SEG + 2 * (MAX_GROUPS + 1) * 4;
   static_assert(BYTES <= 232448, "dynamic shared memory");
 };
 
-__device__ __forceinline__ void cp_async16(uint32_t dst, const void* src, uint32_t bytes) {
-  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(bytes) : "memory");
-}
 __device__ __forceinline__ void cp_async4(uint32_t dst, const void* src, uint32_t bytes) {
   asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"(dst), "l"(src), "r"(bytes) : "memory");
 }
-__device__ __forceinline__ uint32_t lds32(uint32_t a) {
-  uint32_t v;
-  asm volatile("ld.shared.u32 %0, [%1];" : "=r"(v) : "r"(a));
-  return v;
-}
-__device__ __forceinline__ uint32_t lds16(uint32_t a) {
-  uint16_t v;
-  asm volatile("ld.shared.u16 %0, [%1];" : "=h"(v) : "r"(a));
-  return v;
-}
-__device__ __forceinline__ uint32_t lds8(uint32_t a) {
-  uint32_t v;
-  asm volatile("ld.shared.u8 %0, [%1];" : "=r"(v) : "r"(a));
-  return v;
+// Loads by shared-memory address that the compiler may move between waits.
+template <class T>
+__device__ __forceinline__ T lds(const uint8_t* base, uint32_t off) {
+  return *reinterpret_cast<const T*>(base + off);
 }
 
+// d += a b (16 x 16 by 16 x 8, f16 in, fp32 out); mma16816_zero: d = a b
 __device__ __forceinline__ void mma16816(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3,
                                          uint32_t b0, uint32_t b1) {
-  asm volatile(
-      "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, "
+  asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, "
       "{%0, %1, %2, %3};"
       : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
       : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+__device__ __forceinline__ void mma16816_zero(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3,
+                                              uint32_t b0, uint32_t b1) {
+  asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, "
+      "{%10, %10, %10, %10};"
+      : "=f"(d[0]), "=f"(d[1]), "=f"(d[2]), "=f"(d[3])
+      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1), "f"(0.0f));
 }
 
 // the eight E2M1 codes of a word as four f16 pairs, in order
@@ -126,15 +178,14 @@ __device__ __forceinline__ void e2m1_word(uint32_t w, uint32_t (&h)[4]) {
       : "=r"(h[0]), "=r"(h[1]), "=r"(h[2]), "=r"(h[3])
       : "r"(w));
 }
-__device__ __forceinline__ void e2m1_half(uint32_t w, uint32_t (&h)[2]) {
-  asm("{\n\t.reg .b8 a, b, c, d;\n\tmov.b32 {a, b, c, d}, %2;\n\t"
-      "cvt.rn.f16x2.e2m1x2 %0, a;\n\tcvt.rn.f16x2.e2m1x2 %1, b;\n\t}"
-      : "=r"(h[0]), "=r"(h[1])
-      : "r"(w));
-}
 __device__ __forceinline__ uint32_t hsub2(uint32_t a, uint32_t b) {
   uint32_t r;
   asm("sub.rn.f16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+  return r;
+}
+__device__ __forceinline__ uint32_t hmul2(uint32_t a, uint32_t b) {
+  uint32_t r;
+  asm("mul.rn.f16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
   return r;
 }
 __device__ __forceinline__ uint32_t hfma2(uint32_t a, uint32_t b, uint32_t c) {
@@ -147,11 +198,10 @@ __device__ __forceinline__ uint32_t hfma2(uint32_t a, uint32_t b, uint32_t c) {
 // (0,4) (1,5) (2,6) (3,7).  A code in the low bits of a half under the
 // exponent of 1024 is 1024 + code; four bits higher it is 1024 + 16 code,
 // which fma brings back: (1024 + 16 code) / 16 - (64 + zero), exact.  z1024
-// holds 1024 + zero twice.
-__device__ __forceinline__ void int4_word(uint32_t w, uint32_t z1024, uint32_t (&h)[4]) {
-  constexpr uint32_t K1024 = 0x64006400u, SIXTEENTH = 0x2C002C00u, K960 = 0x63806380u;
+// holds 1024 + zero twice, nz -(64 + zero).
+__device__ __forceinline__ void int4_word(uint32_t w, uint32_t z1024, uint32_t nz, uint32_t (&h)[4]) {
+  constexpr uint32_t K1024 = 0x64006400u, SIXTEENTH = 0x2C002C00u;
   const uint32_t w8 = w >> 8;
-  const uint32_t nz = hsub2(K960, z1024);  // -(64 + zero)
   h[0] = hsub2((w & 0x000F000Fu) | K1024, z1024);
   h[1] = hfma2((w & 0x00F000F0u) | K1024, SIXTEENTH, nz);
   h[2] = hsub2((w8 & 0x000F000Fu) | K1024, z1024);
@@ -159,20 +209,6 @@ __device__ __forceinline__ void int4_word(uint32_t w, uint32_t z1024, uint32_t (
 }
 
 __device__ __forceinline__ float half_bits(uint32_t h) { return __half2float(__ushort_as_half(static_cast<uint16_t>(h))); }
-
-// Barrier of a team's warps in a CTA (two warps or more: at most 8 teams)
-__device__ __forceinline__ void team_sync(int team, int warps) {
-  if (warps == 1)
-    __syncwarp();
-  else
-    asm volatile("barrier.sync %0, %1;" ::"r"(team + 1), "r"(32 * warps) : "memory");
-}
-
-__device__ __forceinline__ float ld_cluster_f32(uint32_t addr) {
-  float v;
-  asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(v) : "r"(addr));
-  return v;
-}
 
 __device__ __forceinline__ void store_d(const GemvParams& p, int64_t i, float v) {
   if (p.d_type == TCG_F32)
@@ -183,15 +219,17 @@ __device__ __forceinline__ void store_d(const GemvParams& p, int64_t i, float v)
     static_cast<__nv_bfloat16*>(p.D)[i] = __float2bfloat16_rn(v);
 }
 
-// A row block: up to 8 * NT rows of one group.
+// A row block: up to TOK rows of one group.
 struct RowBlock {
   int g, row0, rows;
 };
 
-template <int NT>
-__device__ __forceinline__ RowBlock row_block(const GemvParams& p, const int* seg, const int* pre, int rb) {
-  constexpr int ROWS = 8 * NT;
-  if (!p.offsets) return {0, rb * ROWS, min(ROWS, p.R - rb * ROWS)};
+// `span`: the rows of a single block (first, last + 1), when there is but one
+template <int TOK>
+__device__ __noinline__ RowBlock row_block(const GemvParams& p, const int* seg, const int* pre, bool single, int2 span,
+                                           int rb) {
+  if (single) return {0, span.x, span.y - span.x};
+  if (!p.offsets) return {0, rb * TOK, min(TOK, p.R - rb * TOK)};
   int a = 0, b = p.G;  // pre[a] <= rb < pre[b]
   while (b - a > 1) {
     const int mid = (a + b) >> 1;
@@ -200,225 +238,412 @@ __device__ __forceinline__ RowBlock row_block(const GemvParams& p, const int* se
     else
       b = mid;
   }
-  const int row0 = seg[a] + (rb - pre[a]) * ROWS;
-  return {a, row0, min(ROWS, seg[a + 1] - row0)};
+  const int row0 = seg[a] + (rb - pre[a]) * TOK;
+  return {a, row0, min(TOK, seg[a + 1] - row0)};
 }
 
 // The activations of a row block for one slab as B fragments.  Lane (g, c) =
-// (lane / 4, lane % 4) holds row 8 nt + g; `frag[ch][nt]` covers 32 of K in
-// the order in which the codes' words decode.  Returns (bf16) the factors that
-// undo the scaling for the accumulator's columns 2c and 2c + 1.
-template <int FMT, bool BF16, int NT>
+// (lane / 4, lane % 4) holds column 8 nt + g (TOK = 4: row g / 2, even g
+// alone count); `frag[ch][nt]` covers 32 of K in the order in which the codes
+// decode.  With up to 4 rows a row is read 8 elements a lane, brought into
+// f16's range and passed through the warp's scratch, where element order is
+// fragment order: converting them as fragments would repeat the work of the
+// columns that do not count.
+// undo (bf16): the factors that take the scaling back, for the accumulator's
+// columns 2c and 2c + 1 (TOK = 4: row c).
+template <int KIND, bool BF16, int TOK, int NT = Shape<TOK>::NT>
 __device__ __forceinline__ void load_fragments(const GemvParams& p, const RowBlock& rb, int slab, int lane,
-                                               uint32_t (&frag)[8][NT][4], float (&undo)[NT][2]) {
+                                               uint8_t* scratch, uint32_t (&frag)[8][NT][4], float (&undo)[NT][2]) {
   const int g = lane >> 2, c = lane & 3;
+  if (TOK > 4) {
+    // many rows: each lane reads its own fragments, a quad shares a row
 #pragma unroll
-  for (int nt = 0; nt < NT; ++nt) {
-    const int r = 8 * nt + g;
-    const uint8_t* row = p.A + 2 * (static_cast<int64_t>(rb.row0 + r) * p.lda + slab * SLAB);
-    uint32_t v[8][4];
+    for (int nt = 0; nt < NT; ++nt) {
+      const int r = 8 * nt + g;
+      const uint8_t* row = p.A + 2 * ((rb.row0 + r) * p.lda + slab * SLAB + 8 * c);
 #pragma unroll
-    for (int ch = 0; ch < 8; ++ch) {
-      const bool in = r < rb.rows && slab * SLAB + 32 * ch < p.K;
-      if (FMT == TCG_W4_NVF4) {  // 4 of each group of 16
-        uint2 x = make_uint2(0u, 0u), y = x;
-        if (in) {
-          x = *reinterpret_cast<const uint2*>(row + 64 * ch + 8 * c);
-          y = *reinterpret_cast<const uint2*>(row + 64 * ch + 32 + 8 * c);
-        }
-        v[ch][0] = x.x;
-        v[ch][1] = x.y;
-        v[ch][2] = y.x;
-        v[ch][3] = y.y;
-      } else {  // 8 consecutive
-        uint4 x = make_uint4(0u, 0u, 0u, 0u);
-        if (in) x = *reinterpret_cast<const uint4*>(row + 64 * ch + 16 * c);
-        v[ch][0] = x.x;
-        v[ch][1] = x.y;
-        v[ch][2] = x.z;
-        v[ch][3] = x.w;
+      for (int ch = 0; ch < 8; ++ch) {
+        uint4 v = make_uint4(0u, 0u, 0u, 0u);
+        if (r < rb.rows && slab * SLAB + 32 * ch < p.K) v = *reinterpret_cast<const uint4*>(row + 64 * ch);
+        uint32_t(&f)[4] = frag[ch][nt];
+        f[0] = v.x;
+        f[1] = v.y;
+        f[2] = v.z;
+        f[3] = v.w;
       }
     }
-    if (BF16) {
-      // the largest magnitude of the row's slab; max drops NaN, and infinities
-      // are looked past when there are any
-      uint32_t m2 = 0;
 #pragma unroll
-      for (int ch = 0; ch < 8; ++ch)
+    for (int nt = 0; nt < NT; ++nt) {
+      undo[nt][0] = undo[nt][1] = 1.0f;
+      if (BF16) {
+        uint32_t m2 = 0;
 #pragma unroll
-        for (int i = 0; i < 4; ++i)
-          asm("max.bf16x2 %0, %0, %1;" : "+r"(m2) : "r"(v[ch][i] & 0x7FFF7FFFu));
-      uint32_t m = max(m2 & 0xFFFFu, m2 >> 16);
-      if (m >= 0x7F80u) {
-        m = 0;
+        for (int ch = 0; ch < 8; ++ch)
+#pragma unroll
+          for (int i = 0; i < 4; ++i) asm("max.bf16x2 %0, %0, %1;" : "+r"(m2) : "r"(frag[ch][nt][i] & 0x7FFF7FFFu));
+        uint32_t m = max(m2 & 0xFFFFu, m2 >> 16);
+        if (m >= 0x7F80u) {  // past infinities
+          m = 0;
+#pragma unroll
+          for (int ch = 0; ch < 8; ++ch)
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+              const uint32_t lo = frag[ch][nt][i] & 0x7FFFu, hi = (frag[ch][nt][i] >> 16) & 0x7FFFu;
+              if (lo < 0x7F80u) m = max(m, lo);
+              if (hi < 0x7F80u) m = max(m, hi);
+            }
+        }
+        m = max(m, __shfl_xor_sync(0xffffffffu, m, 1));
+        m = max(m, __shfl_xor_sync(0xffffffffu, m, 2));
+        const int e = min(141 - static_cast<int>(m >> 7), 126);  // 2^e brings the largest to [2^14, 2^15)
+        const float up = __uint_as_float(static_cast<uint32_t>(e + 127) << 23);
+        const float down = __uint_as_float(static_cast<uint32_t>(127 - e) << 23);
 #pragma unroll
         for (int ch = 0; ch < 8; ++ch)
 #pragma unroll
           for (int i = 0; i < 4; ++i) {
-            const uint32_t lo = v[ch][i] & 0x7FFFu, hi = (v[ch][i] >> 16) & 0x7FFFu;
-            if (lo < 0x7F80u) m = max(m, lo);
-            if (hi < 0x7F80u) m = max(m, hi);
+            const uint32_t v = frag[ch][nt][i];
+            const __half2 h = __floats2half2_rn(__uint_as_float(v << 16) * up, __uint_as_float(v & 0xFFFF0000u) * up);
+            frag[ch][nt][i] = *reinterpret_cast<const uint32_t*>(&h);
           }
+        // the factors of rows 2c and 2c + 1, held by the lanes of those rows
+        undo[nt][0] = __shfl_sync(0xffffffffu, down, 8 * c);
+        undo[nt][1] = __shfl_sync(0xffffffffu, down, 8 * c + 4);
       }
-      m = max(m, __shfl_xor_sync(0xffffffffu, m, 1));
-      m = max(m, __shfl_xor_sync(0xffffffffu, m, 2));
-      const int e = 141 - static_cast<int>(m >> 7);  // 2^e brings the largest to [2^14, 2^15)
-      const int s = min(e, 126);
-      const float up = __uint_as_float(static_cast<uint32_t>(s + 127) << 23);
-      const float down = __uint_as_float(static_cast<uint32_t>(127 - s) << 23);
+      if (is_int4(KIND)) {  // pairs (0,4) (1,5) (2,6) (3,7)
 #pragma unroll
-      for (int ch = 0; ch < 8; ++ch)
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          const __half2 h = __floats2half2_rn(__uint_as_float(v[ch][i] << 16) * up,
-                                              __uint_as_float(v[ch][i] & 0xFFFF0000u) * up);
-          v[ch][i] = *reinterpret_cast<const uint32_t*>(&h);
+        for (int ch = 0; ch < 8; ++ch) {
+          uint32_t(&f)[4] = frag[ch][nt];
+          const uint32_t v0 = f[0], v1 = f[1], v2 = f[2], v3 = f[3];
+          f[0] = __byte_perm(v0, v2, 0x5410);
+          f[1] = __byte_perm(v0, v2, 0x7632);
+          f[2] = __byte_perm(v1, v3, 0x5410);
+          f[3] = __byte_perm(v1, v3, 0x7632);
         }
-      // the factors of rows 2c and 2c + 1, held by the lanes of those rows
-      undo[nt][0] = __shfl_sync(0xffffffffu, down, 8 * c);
-      undo[nt][1] = __shfl_sync(0xffffffffu, down, 8 * c + 4);
-    }
-#pragma unroll
-    for (int ch = 0; ch < 8; ++ch) {
-      if (FMT == TCG_W4_INT4) {  // pairs (0,4) (1,5) (2,6) (3,7)
-        frag[ch][nt][0] = __byte_perm(v[ch][0], v[ch][2], 0x5410);
-        frag[ch][nt][1] = __byte_perm(v[ch][0], v[ch][2], 0x7632);
-        frag[ch][nt][2] = __byte_perm(v[ch][1], v[ch][3], 0x5410);
-        frag[ch][nt][3] = __byte_perm(v[ch][1], v[ch][3], 0x7632);
-      } else {
-#pragma unroll
-        for (int i = 0; i < 4; ++i) frag[ch][nt][i] = v[ch][i];
       }
+    }
+    return;
+  }
+#pragma unroll
+  for (int ch = 0; ch < 8; ++ch)
+#pragma unroll
+    for (int i = 0; i < 4; ++i) frag[ch][0][i] = 0u;
+  const uint8_t* src = p.A + 2 * (rb.row0 * p.lda + slab * SLAB + 8 * lane);
+  const bool in = slab * SLAB + 8 * lane < p.K;
+  float down = 1.0f;  // row c's factor
+  uint4 x = make_uint4(0u, 0u, 0u, 0u);
+  if (in && rb.rows > 0) x = *reinterpret_cast<const uint4*>(src);
+#pragma unroll 1
+  for (int r = 0; r < rb.rows; ++r) {
+    uint32_t v[4] = {x.x, x.y, x.z, x.w};
+    src += 2 * p.lda;
+    if (in && r + 1 < rb.rows) x = *reinterpret_cast<const uint4*>(src);
+    if (BF16) {
+      // the largest magnitude of the row's slab; max drops NaN, and
+      // infinities are looked past when there are any
+      uint32_t m2 = 0;
+#pragma unroll
+      for (int i = 0; i < 4; ++i) asm("max.bf16x2 %0, %0, %1;" : "+r"(m2) : "r"(v[i] & 0x7FFF7FFFu));
+      uint32_t m = max(m2 & 0xFFFFu, m2 >> 16);
+      if (m >= 0x7F80u) {
+        m = 0;
+#pragma unroll 1
+        for (int i = 0; i < 8; ++i) {
+          const uint32_t h = ((i & 4) ? ((i & 2) ? v[3] : v[2]) : ((i & 2) ? v[1] : v[0])) >> (16 * (i & 1)) & 0x7FFFu;
+          if (h < 0x7F80u) m = max(m, h);
+        }
+      }
+      m = __reduce_max_sync(0xffffffffu, m);
+      const int e = min(141 - static_cast<int>(m >> 7), 126);  // 2^e brings the largest to [2^14, 2^15)
+      const float up = __uint_as_float(static_cast<uint32_t>(e + 127) << 23);
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const __half2 h = __floats2half2_rn(__uint_as_float(v[i] << 16) * up, __uint_as_float(v[i] & 0xFFFF0000u) * up);
+        v[i] = *reinterpret_cast<const uint32_t*>(&h);
+      }
+      if (c == r) down = __uint_as_float(static_cast<uint32_t>(127 - e) << 23);
+    }
+    uint4 y = make_uint4(v[0], v[1], v[2], v[3]);
+    if (is_int4(KIND))  // pairs (0,4) (1,5) (2,6) (3,7)
+      y = make_uint4(__byte_perm(v[0], v[2], 0x5410), __byte_perm(v[0], v[2], 0x7632),
+                     __byte_perm(v[1], v[3], 0x5410), __byte_perm(v[1], v[3], 0x7632));
+    *reinterpret_cast<uint4*>(scratch + 16 * lane) = y;
+    __syncwarp();
+    if (g == 2 * r) {  // the row of this even column: 8 consecutive elements of each 32
+#pragma unroll
+      for (int ch = 0; ch < 8; ++ch) {
+        const uint4 a = lds<uint4>(scratch, 64 * ch + 16 * c);
+        uint32_t(&f)[4] = frag[ch][0];
+        f[0] = a.x;
+        f[1] = a.y;
+        f[2] = a.z;
+        f[3] = a.w;
+      }
+    }
+    __syncwarp();
+  }
+  undo[0][0] = undo[0][1] = down;
+  __syncwarp();
+}
+
+// A row's scales of a slab as words, from a byte offset that may be off a
+// 4-byte boundary (then `shift` bits into its word).
+template <int W>
+__device__ __forceinline__ void scale_words(const uint8_t* at, bool aligned, uint32_t (&w)[W]) {
+  if (aligned) {
+    if constexpr (W == 4) {
+      const uint4 v = lds<uint4>(at, 0);
+      w[0] = v.x;
+      w[1] = v.y;
+      w[2] = v.z;
+      w[3] = v.w;
+    } else if constexpr (W == 2) {
+      const uint2 v = lds<uint2>(at, 0);
+      w[0] = v.x;
+      w[1] = v.y;
+    } else {
+      w[0] = lds<uint32_t>(at, 0);
+    }
+  } else {
+    const uint32_t off = static_cast<uint32_t>(reinterpret_cast<uintptr_t>(at)) & 3u;
+    const uint8_t* base = at - off;
+    uint32_t lo = lds<uint32_t>(base, 0);
+#pragma unroll
+    for (int i = 0; i < W; ++i) {
+      const uint32_t hi = lds<uint32_t>(base, 4 * i + 4);
+      w[i] = __funnelshift_r(lo, hi, 8 * off);
+      lo = hi;
     }
   }
 }
 
-// One tile's slab: acc[nt] += (codes . activations) * scales; `stage` is its
-// ring stage, ms / mz the byte offsets of rows g and g + 8's scales and zero
-// points from their 4-byte boundary.
-template <int FMT, bool BF16, int NT>
-__device__ __forceinline__ void tile_slab(const GemvParams& p, uint32_t stage, int lane, int chunks, uint32_t ms0,
-                                          uint32_t ms1, uint32_t mz0, uint32_t mz1, const uint32_t (&frag)[8][NT][4],
-                                          const float (&undo)[NT][2], float (&acc)[NT][4]) {
-  auto add = [&](int nt, const float (&part)[4], float f0, float f1) {
-#pragma unroll
-    for (int i = 0; i < 4; ++i) acc[nt][i] += (BF16 ? part[i] * undo[nt][i & 1] : part[i]) * (i < 2 ? f0 : f1);
-  };
+// 16 rows of a tile and a slab: acc[nt] = (codes . activations) * scales.
+// `codes` is the first of the rows' 128-byte lines; s0, s1 (z0, z1) the slab's
+// scales (zero points) of rows g and g + 8.
+template <int KIND, bool BF16, int TOK, int NT = Shape<TOK>::NT>
+__device__ __forceinline__ void rows16(const uint8_t* codes, const uint8_t* s0, const uint8_t* s1, const uint8_t* z0,
+                                       const uint8_t* z1, bool aligned, int lane, const uint32_t (&frag)[8][NT][4],
+                                       const float (&undo)[NT][2], float (&acc)[NT][4]) {
+  constexpr int STEP = Shape<TOK>::STEP;
+  constexpr int W = scale_bytes(KIND) / 4;
   const uint32_t g = lane >> 2, c = lane & 3;
-  const uint32_t code0 = stage + 128u * g, code1 = code0 + 1024u;
-  const uint32_t sc0 = stage + CODE_BYTES + SCALE_PITCH * g + ms0, sc1 = stage + CODE_BYTES + SCALE_PITCH * (g + 8) + ms1;
-  uint32_t b0[4], b1[4];  // scale bytes of rows g and g + 8
-  if (FMT != TCG_W4_INT4) {
-    constexpr int W = FMT == TCG_W4_MXF4 ? 2 : 4;
-    const uint32_t a0 = sc0 - ms0, a1 = sc1 - ms1;
-    uint32_t lo0 = lds32(a0), lo1 = lds32(a1);
+  // row g's chunk ch (32 of K, 16 bytes) lies at chunk ch ^ (g & 7)
+  const uint32_t code = 144u * g + 4u * c;
+  uint32_t w0[W], w1[W];
+  scale_words<W>(s0, aligned, w0);
+  scale_words<W>(s1, aligned, w1);
+  if constexpr (KIND == K_NVF4) {
+    // unsigned E4M3: a byte with the top bit set is NaN (0xFF)
+    if ((w0[0] | w0[1] | w0[2] | w0[3] | w1[0] | w1[1] | w1[2] | w1[3]) & 0x80808080u) {
 #pragma unroll
-    for (int i = 0; i < W; ++i) {
-      const uint32_t hi0 = lds32(a0 + 4 * i + 4), hi1 = lds32(a1 + 4 * i + 4);
-      b0[i] = __funnelshift_r(lo0, hi0, 8 * ms0);
-      b1[i] = __funnelshift_r(lo1, hi1, 8 * ms1);
-      lo0 = hi0;
-      lo1 = hi1;
+      for (int i = 0; i < W; ++i) {
+        const uint32_t t0 = w0[i] & 0x80808080u, t1 = w1[i] & 0x80808080u;
+        w0[i] |= t0 - (t0 >> 7);
+        w1[i] |= t1 - (t1 >> 7);
+      }
     }
-    if (FMT == TCG_W4_NVF4) {
-      // unsigned E4M3: a byte with the top bit set is NaN (0xFF)
+    // scales go into the codes: two chains over the slab (one mma waits for
+    // the last of its chain).  The lanes with c < 2 hold the codes of the
+    // chunk's first group.
+    const uint32_t pick = c < 2 ? 0x1010u : 0x3232u;
+    float sum[2][NT][4];
+#pragma unroll
+    for (int ch = 0; ch < 8; ++ch) {
+      const uint32_t at = code ^ (16u * ch);
+      uint32_t h0[4], h1[4], f0, f1;
+      e2m1_word(lds<uint32_t>(codes, at), h0);
+      e2m1_word(lds<uint32_t>(codes, at + 1024), h1);
+      if (ch & 1) {
+        asm("{\n\t.reg .b16 a, b;\n\tmov.b32 {a, b}, %1;\n\tcvt.rn.f16x2.e4m3x2 %0, b;\n\t}" : "=r"(f0) : "r"(w0[ch / 2]));
+        asm("{\n\t.reg .b16 a, b;\n\tmov.b32 {a, b}, %1;\n\tcvt.rn.f16x2.e4m3x2 %0, b;\n\t}" : "=r"(f1) : "r"(w1[ch / 2]));
+      } else {
+        asm("{\n\t.reg .b16 a, b;\n\tmov.b32 {a, b}, %1;\n\tcvt.rn.f16x2.e4m3x2 %0, a;\n\t}" : "=r"(f0) : "r"(w0[ch / 2]));
+        asm("{\n\t.reg .b16 a, b;\n\tmov.b32 {a, b}, %1;\n\tcvt.rn.f16x2.e4m3x2 %0, a;\n\t}" : "=r"(f1) : "r"(w1[ch / 2]));
+      }
+      f0 = __byte_perm(f0, 0, pick);
+      f1 = __byte_perm(f1, 0, pick);
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
-        const uint32_t t0 = b0[i] & 0x80808080u, t1 = b1[i] & 0x80808080u;
-        b0[i] |= t0 - (t0 >> 7);
-        b1[i] |= t1 - (t1 >> 7);
-      }
-    }
-  }
-#pragma unroll
-  for (int ch = 0; ch < 8; ++ch) {
-    if (ch >= chunks) break;
-    const uint32_t at = ((ch ^ g) & 7u) * 16u;
-    if (FMT == TCG_W4_NVF4) {
-      // scales 2 ch and 2 ch + 1 of both rows
-      uint32_t s0, s1;
-      const uint32_t w0 = b0[ch / 2] >> (16 * (ch & 1)), w1 = b1[ch / 2] >> (16 * (ch & 1));
-      asm("{\n\t.reg .b16 lo, hi;\n\tmov.b32 {lo, hi}, %1;\n\tcvt.rn.f16x2.e4m3x2 %0, lo;\n\t}" : "=r"(s0) : "r"(w0));
-      asm("{\n\t.reg .b16 lo, hi;\n\tmov.b32 {lo, hi}, %1;\n\tcvt.rn.f16x2.e4m3x2 %0, lo;\n\t}" : "=r"(s1) : "r"(w1));
-#pragma unroll
-      for (int q = 0; q < 2; ++q) {
-        uint32_t h0[2], h1[2];
-        e2m1_half(lds16(code0 + at + 8 * q + 2 * c), h0);
-        e2m1_half(lds16(code1 + at + 8 * q + 2 * c), h1);
-        const float f0 = half_bits(q ? s0 >> 16 : s0), f1 = half_bits(q ? s1 >> 16 : s1);
-#pragma unroll
-        for (int nt = 0; nt < NT; ++nt) {
-          float part[4] = {};
-          mma16816(part, h0[0], h1[0], h0[1], h1[1], frag[ch][nt][2 * q], frag[ch][nt][2 * q + 1]);
-          add(nt, part, f0, f1);
-        }
-      }
-    } else {
-      uint32_t h0[4], h1[4];
-      float f0, f1;
-      const uint32_t w0 = lds32(code0 + at + 4 * c), w1 = lds32(code1 + at + 4 * c);
-      if (FMT == TCG_W4_MXF4) {
-        e2m1_word(w0, h0);
-        e2m1_word(w1, h1);
-        // both rows' e8m0 bytes to bf16 pairs, exact (0 is 2^-127, 255 NaN)
-        const uint32_t pair = __byte_perm(b0[ch / 4], b1[ch / 4], (ch & 3) | ((4 + (ch & 3)) << 4));
-        uint32_t s;
-        asm("{\n\t.reg .b16 lo, hi;\n\tmov.b32 {lo, hi}, %1;\n\tcvt.rn.bf16x2.ue8m0x2 %0, lo;\n\t}" : "=r"(s) : "r"(pair));
-        f0 = __uint_as_float(s << 16);
-        f1 = __uint_as_float(s & 0xFFFF0000u);
-      } else {
-        const uint32_t gi = static_cast<uint32_t>(32 * ch) >> p.group_shift;
-        const uint32_t s0 = lds16(sc0 + 2 * gi), s1 = lds16(sc1 + 2 * gi);
-        f0 = BF16 ? __uint_as_float(s0 << 16) : half_bits(s0);
-        f1 = BF16 ? __uint_as_float(s1 << 16) : half_bits(s1);
-        uint32_t z0 = 8, z1 = 8;
-        if (p.zero) {
-          const uint32_t zb = stage + CODE_BYTES + TILE_N * SCALE_PITCH + gi;
-          z0 = lds8(zb + ZERO_PITCH * g + mz0);
-          z1 = lds8(zb + ZERO_PITCH * (g + 8) + mz1);
-        }
-        int4_word(w0, 0x64006400u + z0 * 0x10001u, h0);
-        int4_word(w1, 0x64006400u + z1 * 0x10001u, h1);
+        h0[i] = hmul2(h0[i], f0);
+        h1[i] = hmul2(h1[i], f1);
       }
 #pragma unroll
       for (int nt = 0; nt < NT; ++nt) {
-        float part[4] = {};
-        mma16816(part, h0[0], h1[0], h0[1], h1[1], frag[ch][nt][0], frag[ch][nt][1]);
-        mma16816(part, h0[2], h1[2], h0[3], h1[3], frag[ch][nt][2], frag[ch][nt][3]);
-        add(nt, part, f0, f1);
+        if (ch == 0) {
+          mma16816_zero(sum[0][nt], h0[0], h1[0], h0[1], h1[1], frag[ch][nt][0], frag[ch][nt][1]);
+          mma16816_zero(sum[1][nt], h0[2], h1[2], h0[3], h1[3], frag[ch][nt][2], frag[ch][nt][3]);
+        } else {
+          mma16816(sum[0][nt], h0[0], h1[0], h0[1], h1[1], frag[ch][nt][0], frag[ch][nt][1]);
+          mma16816(sum[1][nt], h0[2], h1[2], h0[3], h1[3], frag[ch][nt][2], frag[ch][nt][3]);
+        }
+      }
+    }
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+      for (int i = 0; i < 4; i += STEP) {
+        const float v = sum[0][nt][i] + sum[1][nt][i];
+        acc[nt][i] = BF16 ? v * undo[nt][i & 1] : v;
+      }
+  } else {
+    constexpr int PER = group_of_kind(KIND) / 32;  // chunks per scale
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+      for (int i = 0; i < 4; ++i) acc[nt][i] = 0.0f;
+    uint32_t y0 = 0x64086408u, y1 = y0, n0 = 0xD480D480u, n1 = n0;  // 1024 + zero, -(64 + zero), zero 8
+    float part[2][NT][4];
+#pragma unroll
+    for (int ch = 0; ch < 8; ++ch) {
+      const uint32_t at = code ^ (16u * ch);
+      constexpr uint32_t K960 = 0x63806380u;
+      const int gi = ch / PER;
+      uint32_t h0[4], h1[4];
+      const uint32_t c0 = lds<uint32_t>(codes, at), c1 = lds<uint32_t>(codes, at + 1024);
+      if constexpr (KIND == K_MXF4) {
+        e2m1_word(c0, h0);
+        e2m1_word(c1, h1);
+      } else {
+        if (ch % PER == 0 && z0) {
+          y0 = 0x64006400u + lds<uint8_t>(z0, gi) * 0x10001u;
+          y1 = 0x64006400u + lds<uint8_t>(z1, gi) * 0x10001u;
+          n0 = hsub2(K960, y0);
+          n1 = hsub2(K960, y1);
+        }
+        int4_word(c0, y0, n0, h0);
+        int4_word(c1, y1, n1, h1);
+      }
+#pragma unroll
+      for (int nt = 0; nt < NT; ++nt) {
+        if (ch % PER == 0) {
+          mma16816_zero(part[0][nt], h0[0], h1[0], h0[1], h1[1], frag[ch][nt][0], frag[ch][nt][1]);
+          mma16816_zero(part[1][nt], h0[2], h1[2], h0[3], h1[3], frag[ch][nt][2], frag[ch][nt][3]);
+        } else {
+          mma16816(part[0][nt], h0[0], h1[0], h0[1], h1[1], frag[ch][nt][0], frag[ch][nt][1]);
+          mma16816(part[1][nt], h0[2], h1[2], h0[3], h1[3], frag[ch][nt][2], frag[ch][nt][3]);
+        }
+      }
+      if (ch % PER == PER - 1) {
+        float f0, f1;
+        if constexpr (KIND == K_MXF4) {
+          // both rows' e8m0 bytes to bf16 pairs, exact (0 is 2^-127, 255 NaN)
+          const uint32_t pair = __byte_perm(w0[gi / 4], w1[gi / 4], (gi & 3) | ((4 + (gi & 3)) << 4));
+          uint32_t f;
+          asm("{\n\t.reg .b16 a, b;\n\tmov.b32 {a, b}, %1;\n\tcvt.rn.bf16x2.ue8m0x2 %0, a;\n\t}" : "=r"(f) : "r"(pair));
+          f0 = __uint_as_float(f << 16);
+          f1 = __uint_as_float(f & 0xFFFF0000u);
+        } else if (BF16) {
+          f0 = __uint_as_float((gi & 1) ? w0[gi / 2] & 0xFFFF0000u : w0[gi / 2] << 16);
+          f1 = __uint_as_float((gi & 1) ? w1[gi / 2] & 0xFFFF0000u : w1[gi / 2] << 16);
+        } else {
+          f0 = half_bits((gi & 1) ? w0[gi / 2] >> 16 : w0[gi / 2]);
+          f1 = half_bits((gi & 1) ? w1[gi / 2] >> 16 : w1[gi / 2]);
+        }
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+          for (int i = 0; i < 4; i += STEP) {
+            const float v = part[0][nt][i] + part[1][nt][i];
+            acc[nt][i] += (BF16 ? v * undo[nt][i & 1] : v) * (i < 2 ? f0 : f1);
+          }
       }
     }
   }
 }
 
-template <int FMT, bool BF16, int NT, int KSL>
+// A team's tiles in order: chunks of tiles, for each its passes over K, for
+// each the tiles.  Without a second pass all tiles are one chunk.
+template <int CAP>
+struct Cursor {
+  int chunk, pos, end;   // grains, counted over the row blocks
+  int i, pass;           // tile within the chunk, pass
+  int block, n0, rows;   // the tile: row block, first matrix row, rows (0: no more)
+
+  __device__ __forceinline__ void locate(const GemvParams& p) {
+    if (pos >= end) {
+      rows = 0;
+      return;
+    }
+    block = pos / p.grains;
+    n0 = (pos - block * p.grains) * GRAIN;
+    rows = min(min(TILE_N, (end - pos) * GRAIN), p.N - n0);
+  }
+  __device__ __forceinline__ void next(const GemvParams& p, int passes) {
+    pos += (rows + GRAIN - 1) / GRAIN;
+    n0 += rows;
+    ++i;
+    if (passes > 1 && (pos >= end || i == CAP)) {
+      i = 0;
+      if (++pass < passes) {
+        pos = chunk;
+      } else {
+        pass = 0;
+        chunk = pos;
+      }
+      locate(p);
+    } else if (n0 < p.N && pos < end) {  // further down the same matrix
+      rows = min(min(TILE_N, (end - pos) * GRAIN), p.N - n0);
+    } else {
+      locate(p);
+    }
+  }
+};
+
+template <int KIND, bool BF16, int TOK>
 __global__ void __launch_bounds__(THREADS, 1) gemv_kernel(const __grid_constant__ GemvParams p) {
-  using S = GemvSmem<NT>;
-  extern __shared__ __align__(16) uint8_t smem[];
-  float* part = reinterpret_cast<float*>(smem + S::RING);
-  float* sums = reinterpret_cast<float*>(smem + S::RING + S::PART);
-  int* seg = reinterpret_cast<int*>(smem + S::RING + S::PART + S::SUM);
+  using S = Shape<TOK>;
+  constexpr int NT = S::NT, STAGES = S::STAGES, PARTS = S::PARTS;
+  extern __shared__ uint8_t smem_raw[];
+  const uint32_t raw = smem_u32(smem_raw);
+  uint8_t* smem = smem_raw + (((raw + 1023u) & ~1023u) - raw);
+  const uint32_t base = smem_u32(smem);
+  uint32_t* abort_word = reinterpret_cast<uint32_t*>(smem + S::SEG - 8);
+  int* seg = reinterpret_cast<int*>(smem + S::SEG);
   int* pre = seg + p.G + 1;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int g = lane >> 2, c = lane & 3;
-  uint32_t cluster_size;
-  asm("mov.u32 %0, %%cluster_nctarank;" : "=r"(cluster_size));
-  const int rank = static_cast<int>(cluster_ctarank());
-  const int team = warp / p.team_warps, wk = warp - team * p.team_warps;
-  const bool idle = team >= p.teams;  // warps left over when teams do not fill the CTA
-  const int num_teams = static_cast<int>(gridDim.x / cluster_size) * p.teams;
-  // neighbouring teams sit in different CTAs, so that few tiles spread over all
-  // (a cluster has one team; its CTAs' spare warps follow it to the cluster's barriers)
-  const int team_id = (cluster_size > 1 ? 0 : team) * static_cast<int>(gridDim.x / cluster_size) +
-                      static_cast<int>(blockIdx.x / cluster_size);
+  const WaitCtx wctx{p.timeout_ns, p.err, abort_word};
+  auto bars = [&](int team) { return base + S::BARS + 8u * S::TEAM_BARS * team; };  // full[], then
+  constexpr uint32_t EMPTY = 8 * STAGES, PFULL = 16 * STAGES, PFREE = PFULL + 8 * PARTS;
 
+  if (threadIdx.x < p.teams) {
+    const uint32_t b = bars(threadIdx.x);
+    for (int i = 0; i < STAGES; ++i) {
+      mbar_init(b + 8 * i, p.bulk ? 1 : 33);  // the copies' bytes, and every feeding lane's own copies
+      mbar_init(b + EMPTY + 8 * i, p.team_warps);
+    }
+    for (int i = 0; i < PARTS; ++i) {
+      mbar_init(b + PFULL + 8 * i, p.team_warps);
+      mbar_init(b + PFREE + 8 * i, 1);
+    }
+    if (threadIdx.x == 0) {
+      *abort_word = 0u;
+      prefetch_tmap(&p.tmap_b);
+    }
+    fence_mbarrier_init();
+  }
   griddep_wait();
   griddep_launch_dependents();
-  int blocks;
-  if (p.offsets) {
-    constexpr int ROWS = 8 * NT;
+  // one group of few rows: its block is there whatever the offsets say, and
+  // the codes need not wait for them
+  const bool single = p.offsets && p.G == 1 && p.R <= TOK;
+  int2 span = make_int2(0, 0);
+  if (single) {
+    span.x = min(max(p.offsets[0], 0), p.R);
+    span.y = min(max(p.offsets[1], span.x), p.R);
+  }
+  // the activations will be asked for late and by every CTA
+  for (int64_t i = static_cast<int64_t>(blockIdx.x) * THREADS + threadIdx.x; i < p.a_lines;
+       i += static_cast<int64_t>(gridDim.x) * THREADS) {
+    const int64_t row = i / p.a_row_lines;
+    asm volatile("prefetch.global.L2 [%0];" ::"l"(p.A + 2 * row * p.lda + 128 * (i - row * p.a_row_lines)));
+  }
+  if (p.offsets && !single)
     for (int i = threadIdx.x; i <= p.G; i += THREADS) seg[i] = p.offsets[i];
-    __syncthreads();
+  __syncthreads();
+  int blocks;
+  if (single) {
+    blocks = 1;
+  } else if (p.offsets) {
     if (warp == 0) {  // clamp to [previous, R]; row blocks before each group
       int run_max = 0, run_blocks = 0;
       for (int i0 = 0; i0 <= p.G; i0 += 32) {
@@ -432,7 +657,7 @@ __global__ void __launch_bounds__(THREADS, 1) gemv_kernel(const __grid_constant_
         v = max(v, run_max);
         int before = __shfl_up_sync(0xffffffffu, v, 1);
         if (lane == 0) before = run_max;
-        int n = i >= 1 && i <= p.G ? (v - before + ROWS - 1) / ROWS : 0;
+        int n = i >= 1 && i <= p.G ? (v - before + TOK - 1) / TOK : 0;
 #pragma unroll
         for (int d = 1; d < 32; d <<= 1) {
           const int o = __shfl_up_sync(0xffffffffu, n, d);
@@ -449,240 +674,314 @@ __global__ void __launch_bounds__(THREADS, 1) gemv_kernel(const __grid_constant_
     }
     __syncthreads();
     blocks = pre[p.G];
-    // rows of no group give zero
-    const int first = seg[0], end = seg[p.G];
-    for (int r = blockIdx.x; r < p.R; r += gridDim.x) {
-      if (r >= first && r < end) continue;
-      for (int n = threadIdx.x; n < p.N; n += THREADS) store_d(p, r * p.ldd + n, 0.0f);
-    }
   } else {
-    blocks = (p.R + 8 * NT - 1) / (8 * NT);
+    blocks = (p.R + TOK - 1) / TOK;
   }
 
-  const int64_t units = static_cast<int64_t>(blocks) * p.tiles;
-  const bool no_team = idle && cluster_size == 1;
-  const int64_t u0 = no_team ? 0 : units * team_id / num_teams;
-  const int64_t u1 = no_team ? 0 : units * (team_id + 1) / num_teams;
-  // this warp's slabs: slab0 + sl * slab_step, each pass
-  const int slab_step = p.team_warps * static_cast<int>(cluster_size);
-  const int slab0 = rank * p.team_warps + wk;
-  const int passes = (p.slabs + slab_step * KSL - 1) / (slab_step * KSL);
-  const uint32_t ring = smem_u32(smem) + warp * STAGES * STAGE_BYTES;
-
-  // ---- ring: steps (unit, pass, slab) in order; the load cursor runs ahead
-  int64_t lu = idle ? u1 : u0;
-  int ltile = 0, lpass = 0, lsl = 0, lrb = -1, lgroup = 0;
-  if (u0 < u1) {
-    lrb = static_cast<int>(u0 / p.tiles);
-    ltile = static_cast<int>(u0 - static_cast<int64_t>(lrb) * p.tiles);
-    lgroup = row_block<NT>(p, seg, pre, lrb).g;
-  }
-  uint32_t lstage = 0;
-  auto issue = [&] {
-    if (lu < u1) {
-      const int slab = slab0 + (lpass * KSL + lsl) * slab_step;
-      if (slab < p.slabs) {
-        const uint32_t st = ring + lstage * STAGE_BYTES;
-        const int n0 = ltile * TILE_N;
-        const uint8_t* base = p.B + lgroup * p.stride_b + slab * (SLAB / 2);
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          const int row = (lane >> 3) + 4 * i, ch = lane & 7;
-          const bool in = n0 + row < p.N && slab * SLAB + 32 * ch < p.K;
-          cp_async16(st + 128 * row + ((ch ^ row) & 7) * 16, in ? base + (n0 + row) * p.ldb + 16 * ch : p.B, in ? 16 : 0);
-        }
-        auto words = [&](uint32_t dst, int pitch, int count, const uint8_t* array, int64_t at, int64_t ld, int64_t size) {
-          for (int i = lane; i < TILE_N * count; i += 32) {
-            const int row = i / count, w = i - row * count;
-            const int64_t off = ((at + (n0 + row) * ld) & ~int64_t{3}) + 4 * w;
-            const bool in = n0 + row < p.N && off < size;
-            cp_async4(dst + row * pitch + 4 * w, in ? array + off : array,
-                      in ? static_cast<uint32_t>(min(int64_t{4}, size - off)) : 0u);
-          }
-        };
-        const int64_t per = FMT == TCG_W4_INT4 ? 2 : 1;
-        const int64_t s_at = lgroup * p.stride_scale + per * ((slab * SLAB) >> p.group_shift);
-        words(st + CODE_BYTES, SCALE_PITCH, p.scale_words, p.scale, s_at, p.ld_scale, p.scale_bytes);
-        if (FMT == TCG_W4_INT4 && p.zero)
-          words(st + CODE_BYTES + TILE_N * SCALE_PITCH, ZERO_PITCH, p.zero_words, p.zero,
-                lgroup * p.stride_zero + ((slab * SLAB) >> p.group_shift), p.ld_zero, p.zero_bytes);
-      }
-      if (++lsl == KSL) {
-        lsl = 0;
-        if (++lpass == passes) {
-          lpass = 0;
-          ++lu;
-          if (++ltile == p.tiles) {
-            ltile = 0;
-            ++lrb;
-            if (lu < u1) lgroup = row_block<NT>(p, seg, pre, lrb).g;
-          }
-        }
-      }
-      if (++lstage == STAGES) lstage = 0;
-    }
-    asm volatile("cp.async.commit_group;" ::: "memory");
+  // a team's share of the grains; the slab of its warp k in pass i is k + i * team_warps
+  const int total = blocks * p.grains, num_teams = static_cast<int>(gridDim.x) * p.teams;
+  const int share = total / num_teams, more = total - share * num_teams;
+  const int passes = (p.slabs + p.team_warps - 1) / p.team_warps;
+  using Cur = Cursor<S::CAP>;
+  auto start = [&](int team) {
+    // neighbouring teams sit in different CTAs, so that few rows spread over all
+    const int id = team * static_cast<int>(gridDim.x) + static_cast<int>(blockIdx.x);
+    Cur cu;
+    cu.chunk = cu.pos = id * share + min(id, more);
+    cu.end = cu.pos + share + (id < more ? 1 : 0);
+    cu.i = cu.pass = cu.block = cu.n0 = 0;
+    cu.locate(p);
+    return cu;
   };
-#pragma unroll 1
-  for (int i = 0; i < STAGES - 1; ++i) issue();
+  bool ok = true;
 
-  uint32_t frag[KSL][8][NT][4];
-  float undo[KSL][NT][2];
-  RowBlock rb{0, 0, 0};
-  int have = -1;  // row block whose fragments are loaded
-  uint32_t stage = 0;
-  int buf = 0;
-  int crb = lrb, ctile = 0;
-  if (u0 < u1) {
-    crb = static_cast<int>(u0 / p.tiles);
-    ctile = static_cast<int>(u0 - static_cast<int64_t>(crb) * p.tiles);
-  }
-  // one round, or for a cluster (whose CTAs share one unit range) rounds of ROUND units
-  for (int64_t r0 = u0, r1; r0 < u1; r0 = r1) {
-    r1 = cluster_size > 1 ? min(u1, r0 + ROUND) : u1;
-    for (int64_t u = idle ? r1 : r0; u < r1; ++u) {
-      float acc[NT][4] = {};
-      for (int pass = 0; pass < passes; ++pass) {
-        if (have != crb || passes > 1) {
-          rb = row_block<NT>(p, seg, pre, crb);
-          have = crb;
-#pragma unroll
-          for (int sl = 0; sl < KSL; ++sl)
-            load_fragments<FMT, BF16, NT>(p, rb, slab0 + (pass * KSL + sl) * slab_step, lane, frag[sl], undo[sl]);
-        }
-#pragma unroll
-        for (int sl = 0; sl < KSL; ++sl) {
-          issue();
-          asm volatile("cp.async.wait_group %0;" ::"n"(STAGES - 1) : "memory");
-          __syncwarp();
-          const int slab = slab0 + (pass * KSL + sl) * slab_step;
-          if (slab < p.slabs) {
-            const int n0 = ctile * TILE_N;
-            const uint32_t per = FMT == TCG_W4_INT4 ? 2u : 1u;
-            const uint32_t gi = static_cast<uint32_t>(slab * SLAB) >> p.group_shift;
-            const uint32_t s_at = static_cast<uint32_t>(rb.g * p.stride_scale) + per * gi;
-            const uint32_t z_at = static_cast<uint32_t>(rb.g * p.stride_zero) + gi;
-            const uint32_t lds = static_cast<uint32_t>(p.ld_scale), ldz = static_cast<uint32_t>(p.ld_zero);
-            const uint32_t ra = static_cast<uint32_t>(n0 + g), rc = ra + 8;
-            const int chunks = min(8, (p.K - slab * SLAB) >> 5);
-            const uint32_t st = ring + stage * STAGE_BYTES;
-            tile_slab<FMT, BF16, NT>(p, st, lane, chunks, (s_at + ra * lds) & 3u, (s_at + rc * lds) & 3u,
-                                     (z_at + ra * ldz) & 3u, (z_at + rc * ldz) & 3u, frag[sl], undo[sl], acc);
+  constexpr int SB = scale_bytes(KIND), ZB = SLAB / group_of_kind(KIND);  // a row's scales, zero points of a slab
+  constexpr int ES = is_int4(KIND) ? 2 : 1;
+  // where a team's scales, zero points start after those of the team before:
+  // whole boxes of 16 rows, or so far along each row
+  const int team_sb = p.bulk ? TILE_N * ((p.team_warps * SB + p.box_s - 1) / p.box_s * p.box_s) : p.team_warps * SB + 4;
+  const int team_zb = p.bulk ? TILE_N * p.box_z : (p.team_warps * ZB + 3) / 4 * 4 + 4;
+
+  if (warp == WARPS) {
+    // -------------------------------------------------------------- feeding
+    // Lane t < teams follows team t; the teams' tiles in turn.
+    Cur mine = start(lane);
+    if (lane >= p.teams) mine.rows = 0;
+    int group = 0, block = -1;
+    uint32_t stage = 0, ph = 1;
+    while (ok && __any_sync(0xffffffffu, mine.rows > 0)) {
+      if (mine.rows && mine.block != block) {
+        block = mine.block;
+        group = p.G == 1 ? 0 : row_block<TOK>(p, seg, pre, false, span, block).g;
+      }
+#pragma unroll 1
+      for (int t = 0; t < p.teams; ++t) {
+        const int rows = __shfl_sync(0xffffffffu, mine.rows, t);
+        if (!rows) continue;
+        const int n0 = __shfl_sync(0xffffffffu, mine.n0, t), gr = __shfl_sync(0xffffffffu, group, t);
+        const int first = __shfl_sync(0xffffffffu, mine.pass, t) * p.team_warps;  // slab
+        const int slabs = min(p.team_warps, p.slabs - first);
+        const uint32_t bar = bars(t) + 8 * stage;
+        ok = wait_uniform(bar + EMPTY, ph, wctx, SITE_PROD_EMPTY);  // the stage's last readers
+        if (!ok) break;
+        const uint32_t box = TILE_N * SLAB / 2;
+        const uint32_t codes = base + stage * S::CODE_BYTES + t * p.team_warps * box;
+        const uint32_t sdst = base + S::SCALES + stage * S::SCALE_STAGE + t * team_sb;
+        const uint32_t zdst = base + S::SCALES + stage * S::SCALE_STAGE + S::ZERO_OFF + t * team_zb;
+        const bool zeros = is_int4(KIND) && p.zero;
+        if (elect_one()) {
+          uint32_t bytes = p.team_warps * box;
+          if (p.bulk) bytes += TILE_N * (team_sb / TILE_N + (zeros ? team_zb / TILE_N : 0));
+          mbar_arrive_expect_tx(bar, bytes);
+          if (p.whole) tma_load_4d(codes, &p.tmap_b, 0, n0, first, gr, bar);
+          if (p.bulk) {
+            for (int x = 0; x < team_sb / TILE_N; x += p.box_s)
+              tma_load3<1>(sdst + TILE_N * x, &p.tmap_s, first * SB + x, n0, gr, bar);
+            if (zeros) tma_load3<1>(zdst, &p.tmap_z, first * ZB, n0, gr, bar);
           }
-          __syncwarp();  // the stage is refilled by the next issue
-          if (++stage == STAGES) stage = 0;
+        }
+        __syncwarp();
+        if (!p.whole && lane < p.team_warps)  // a slab a lane, zeros beyond K
+          tma_load3<1>(codes + lane * box, &p.tmap_b, (first + lane) * (SLAB / 2), n0, gr, bar);
+        if (!p.bulk) {
+          const uint8_t* src = p.scale + gr * p.stride_scale + n0 * p.ld_scale + first * SB;
+          const uint8_t* zsrc = p.zero + gr * p.stride_zero + n0 * p.ld_zero + first * ZB;
+          // 4-byte words from the boundary below each row's start; what lies
+          // past the row's end is zero.  One row at a time, a word a lane.
+          auto words = [&](uint32_t dst, uint32_t pitch, const uint8_t* at, int64_t ld, int want, int left) {
+#pragma unroll 1
+            for (int r = 0; r < rows; ++r, at += ld, dst += pitch) {
+              const int mis = static_cast<int>(reinterpret_cast<uintptr_t>(at)) & 3;
+#pragma unroll 1
+              for (int i = 4 * lane; i < want + mis; i += 128)
+                cp_async4(dst + i, i < left + mis ? at - mis + i : p.scale, max(0, min(4, left + mis - i)));
+            }
+          };
+          words(sdst, SCALE_PITCH, src, p.ld_scale, p.team_warps * SB, p.scale_row * ES - first * SB);
+          if (zeros) words(zdst, ZERO_PITCH, zsrc, p.ld_zero, p.team_warps * ZB, p.scale_row - first * ZB);
+          asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(bar) : "memory");
         }
       }
-      // the team's sum, activation row major with 16 matrix rows each
-      float* mine = part + ((buf * WARPS + warp) * 8 * NT) * PART_PITCH;
+      if (mine.rows) mine.next(p, passes);
+      if (++stage == STAGES) {
+        stage = 0;
+        ph ^= 1u;
+      }
+    }
+    asm volatile("cp.async.wait_all;" ::: "memory");
+    if (!ok && lane == 0) {
+      // let the copies in flight land before the CTA can exit
+      const uint64_t t0 = globaltimer();
+      while (globaltimer() - t0 < 2000000ull) {
+      }
+    }
+  } else if (warp < WARPS) {
+    // ------------------------------------------------------------- decoding
+    const int team = warp / p.team_warps, wk = warp - team * p.team_warps;
+    const int g = lane >> 2, c = lane & 3;
+    Cur cu = start(team);
+    if (team >= p.teams) cu.rows = 0;  // warps left over when teams do not fill the CTA
+    uint32_t frag[8][NT][4];
+    float undo[NT][2];
+    int have_block = -1, have_pass = -1, group = 0;  // whose fragments are loaded
+    uint32_t stage = 0, ph = 0, buf = 0, buf_ph = ~0u;  // buf_ph: a parity bit per buffer
+    const uint32_t bar = bars(team);
+    const uint8_t* codes0 = smem + warp * (TILE_N * SLAB / 2);
+    const uint8_t* scales0 = smem + S::SCALES + team * team_sb;
+    const uint8_t* zeros0 = smem + S::SCALES + S::ZERO_OFF + team * team_zb;
+    int to_s1 = 8 * SCALE_PITCH, to_z1 = 8 * ZERO_PITCH;  // from row g to row g + 8
+    if (p.bulk) {
+      // 128 bytes of a row to a box; a box's rows 8 apart are swizzled alike
+      const uint32_t x = wk * SB;
+      scales0 += (x >> 7) * (TILE_N * 128) + box_at(g, x & 127u, p.box_s);
+      zeros0 += box_at(g, wk * ZB, p.box_z);
+      to_s1 = 8 * p.box_s;
+      to_z1 = 8 * p.box_z;
+    } else {
+      scales0 += g * SCALE_PITCH + wk * SB;
+      zeros0 += g * ZERO_PITCH + wk * ZB;
+    }
+    float* part0 = reinterpret_cast<float*>(smem + S::PART) + warp * S::TILE_PART +
+                   (TOK == 4 ? c : 2 * c) * S::PART_PITCH + g;
+    while (cu.rows) {
+      if (have_block != cu.block || have_pass != cu.pass) {
+        const RowBlock rb = row_block<TOK>(p, seg, pre, single, span, cu.block);
+        group = rb.g;
+        have_block = cu.block;
+        have_pass = cu.pass;
+        load_fragments<KIND, BF16, TOK>(p, rb, wk + cu.pass * p.team_warps, lane, smem + S::ACT + warp * S::ACT_BYTES,
+                                       frag, undo);
+      }
+      ok = wait_uniform(bar + 8 * stage, ph, wctx, SITE_MMA_FULL) &&
+           wait_uniform(bar + PFREE + 8 * buf, (buf_ph >> buf) & 1u, wctx, SITE_MMA_ACC_EMPTY);
+      if (!ok) break;
+      float acc[NT][4] = {};
+      const int slab = wk + cu.pass * p.team_warps;
+      if (slab < p.slabs) {
+        const uint8_t *s0 = scales0 + stage * S::SCALE_STAGE, *s1 = s0 + to_s1;
+        const uint8_t *z0 = nullptr, *z1 = nullptr;
+        if (is_int4(KIND) && p.zero) {
+          z0 = zeros0 + stage * S::SCALE_STAGE;
+          z1 = z0 + to_z1;
+        }
+        if (!p.bulk) {
+          // each row starts as far past a 4-byte boundary as it does in memory
+          const uint32_t first = static_cast<uint32_t>(cu.pass * p.team_warps);
+          const uint32_t ld_s = static_cast<uint32_t>(p.ld_scale), ra = static_cast<uint32_t>(cu.n0 + g);
+          const uint32_t at = static_cast<uint32_t>(group) * static_cast<uint32_t>(p.stride_scale) + first * SB + ra * ld_s;
+          s0 += at & 3u;
+          s1 += (at + 8u * ld_s) & 3u;
+          if (is_int4(KIND) && p.zero) {
+            const uint32_t ld_z = static_cast<uint32_t>(p.ld_zero);
+            const uint32_t zat = static_cast<uint32_t>(group) * static_cast<uint32_t>(p.stride_zero) + first * ZB + ra * ld_z;
+            z0 += zat & 3u;
+            z1 += (zat + 8u * ld_z) & 3u;
+          }
+        }
+        rows16<KIND, BF16, TOK>(codes0 + stage * S::CODE_BYTES, s0, s1, z0, z1, p.bulk, lane, frag, undo, acc);
+      }
+      float* mine = part0 + buf * (WARPS * S::TILE_PART);
 #pragma unroll
       for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-        for (int i = 0; i < 4; ++i) mine[(8 * nt + 2 * c + (i & 1)) * PART_PITCH + g + 8 * (i >> 1)] = acc[nt][i];
-      team_sync(team, p.team_warps);
-      const float* base = part + ((buf * WARPS + team * p.team_warps) * 8 * NT) * PART_PITCH;
-      for (int j = wk * 32 + lane; j < 128 * NT; j += 32 * p.team_warps) {
-        const int row = j >> 4, n = j & 15;
-        float s = 0.0f;
-        for (int w = 0; w < p.team_warps; ++w) s += base[(w * 8 * NT + row) * PART_PITCH + n];
-        if (cluster_size > 1) {
-          sums[(u - r0) * 128 * NT + j] = s;
-        } else if (row < rb.rows && ctile * TILE_N + n < p.N) {
-          store_d(p, (rb.row0 + row) * p.ldd + ctile * TILE_N + n, p.alpha ? s * p.alpha[rb.g] : s);
-        }
+        for (int i = 0; i < 4; i += S::STEP) mine[(8 * nt + (i & 1)) * S::PART_PITCH + 8 * (i >> 1)] = acc[nt][i];
+      __syncwarp();
+      if (lane == 0) {
+        mbar_arrive(bar + EMPTY + 8 * stage);
+        mbar_arrive(bar + PFULL + 8 * buf);
       }
-      buf ^= 1;
-      if (++ctile == p.tiles) {
-        ctile = 0;
-        ++crb;
+      if (++stage == STAGES) {
+        stage = 0;
+        ph ^= 1u;
       }
+      buf_ph ^= 1u << buf;
+      cu.next(p, passes);
+      if (++buf == PARTS || cu.i == 0) buf = 0;
     }
-    if (cluster_size > 1) {
-      cluster_sync();
-      // the round's outputs, spread over the cluster's threads
-      const int count = static_cast<int>(r1 - r0) * 128 * NT;
-      for (int j = rank * THREADS + threadIdx.x; j < count; j += cluster_size * THREADS) {
-        const int64_t u = r0 + j / (128 * NT);
-        const int row = (j >> 4) % (8 * NT), n = j & 15;
-        const int b = static_cast<int>(u / p.tiles), tile = static_cast<int>(u - static_cast<int64_t>(b) * p.tiles);
-        const RowBlock o = row_block<NT>(p, seg, pre, b);
-        if (row < o.rows && tile * TILE_N + n < p.N) {
-          float s = 0.0f;
-          for (uint32_t k = 0; k < cluster_size; ++k) s += ld_cluster_f32(mapa_shared(smem_u32(sums + j), k));
-          store_d(p, (o.row0 + row) * p.ldd + tile * TILE_N + n, p.alpha ? s * p.alpha[o.g] : s);
+  } else {
+    // --------------------------------------------------------------- adding
+    const int buf = warp - (WARPS + 1);
+    const float* parts0 = reinterpret_cast<const float*>(smem + S::PART);
+    float* sums = reinterpret_cast<float*>(smem + S::SUM);
+    uint32_t ph = 0;  // a parity bit per team
+    // lane t < teams follows team t
+    Cur mine = start(lane);
+    if (lane >= p.teams) mine.rows = 0;
+    RowBlock o{0, 0, 0};
+    int block = -1;
+    float alpha = 1.0f;
+    while (ok && __any_sync(0xffffffffu, mine.rows > 0)) {
+#pragma unroll 1
+      for (int t = 0; t < p.teams; ++t) {
+        const int rows = __shfl_sync(0xffffffffu, mine.rows, t), idx = __shfl_sync(0xffffffffu, mine.i, t);
+        if (!rows || idx % PARTS != buf) continue;
+        const int n0 = __shfl_sync(0xffffffffu, mine.n0, t), pass = __shfl_sync(0xffffffffu, mine.pass, t);
+        const int blk = __shfl_sync(0xffffffffu, mine.block, t);
+        if (blk != block) {
+          block = blk;
+          o = row_block<TOK>(p, seg, pre, single, span, block);
+          if (p.alpha) alpha = p.alpha[o.g];
         }
+        ok = wait_uniform(bars(t) + PFULL + 8 * buf, (ph >> t) & 1u, wctx, SITE_EPI_ACC_FULL);
+        if (!ok) break;
+        ph ^= 1u << t;
+        const float* parts = parts0 + (buf * WARPS + t * p.team_warps) * S::TILE_PART;
+#pragma unroll
+        for (int j0 = 0; j0 < S::OUT; j0 += 128) {
+          const int row = j0 / TILE_N + (lane >> 2), n = 4 * (lane & 3);
+          const float4* at = reinterpret_cast<const float4*>(parts + (row < TOK ? row : 0) * S::PART_PITCH + n);
+          float4 s = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+#pragma unroll 8
+          for (int w = 0; w < p.team_warps; ++w) {
+            const float4 v = at[w * (S::TILE_PART / 4)];
+            s.x += v.x;
+            s.y += v.y;
+            s.z += v.z;
+            s.w += v.w;
+          }
+          if (row < TOK && passes > 1) {
+            float4* keep = reinterpret_cast<float4*>(sums + idx * S::OUT + j0 + 4 * lane);
+            if (pass > 0) {
+              const float4 v = *keep;
+              s.x += v.x;
+              s.y += v.y;
+              s.z += v.z;
+              s.w += v.w;
+            }
+            *keep = s;
+          }
+          if (pass == passes - 1 && row < o.rows) {
+            const int64_t d = (o.row0 + row) * p.ldd + n0 + n;
+            const float v[4] = {s.x, s.y, s.z, s.w};
+#pragma unroll
+            for (int k = 0; k < 4; ++k)
+              if (n + k < rows) store_d(p, d + k, v[k] * alpha);
+          }
+        }
+        __syncwarp();
+        if (lane == 0) mbar_arrive(bars(t) + PFREE + 8 * buf);
       }
-      cluster_sync();  // peers have read this CTA's sums
+      if (mine.rows) mine.next(p, passes);
+    }
+    if (p.offsets) {  // rows of no group give zero
+      const int first = single ? span.x : seg[0], end = single ? span.y : seg[p.G];
+#pragma unroll 1
+      for (int r = blockIdx.x; r < p.R; r += gridDim.x) {
+        if (r >= first && r < end) continue;
+#pragma unroll 1
+        for (int n = threadIdx.x - 32 * (WARPS + 1); n < p.N; n += 32 * ADD_WARPS) store_d(p, r * p.ldd + n, 0.0f);
+      }
     }
   }
-  asm volatile("cp.async.wait_all;" ::: "memory");
 }
 
 // ---------------------------------------------------------------------- host
 
 using Kernel = void (*)(GemvParams);
 
-// Index of a variant: format, bf16, (NT, KSL) = (1, 1), (1, 2), (2, 1).
-constexpr int SHAPES = 3, VARIANTS = 3 * 2 * SHAPES;
-constexpr int shape_index(int nt, int ksl) { return nt == 2 ? 2 : ksl - 1; }
+// Index of a variant: Kind4, bf16, TOK (4, 8, 16).
+constexpr int SHAPES = 3, VARIANTS = KINDS4 * 2 * SHAPES;
+constexpr int shape_index(int tok) { return tok == 16 ? 2 : tok == 8 ? 1 : 0; }
 
-template <int FMT, bool BF16>
+template <int KIND>
 void fill(Kernel* k) {
-  k[0] = gemv_kernel<FMT, BF16, 1, 1>;
-  k[1] = gemv_kernel<FMT, BF16, 1, 2>;
-  k[2] = gemv_kernel<FMT, BF16, 2, 1>;
+  k[0] = gemv_kernel<KIND, false, 4>;
+  k[1] = gemv_kernel<KIND, false, 8>;
+  k[2] = gemv_kernel<KIND, false, 16>;
+  k[3] = gemv_kernel<KIND, true, 4>;
+  k[4] = gemv_kernel<KIND, true, 8>;
+  k[5] = gemv_kernel<KIND, true, 16>;
 }
 
 struct Variants {
   Kernel k[VARIANTS];
   Variants() {
-    fill<TCG_W4_INT4, false>(k);
-    fill<TCG_W4_INT4, true>(k + SHAPES);
-    fill<TCG_W4_MXF4, false>(k + 2 * SHAPES);
-    fill<TCG_W4_MXF4, true>(k + 3 * SHAPES);
-    fill<TCG_W4_NVF4, false>(k + 4 * SHAPES);
-    fill<TCG_W4_NVF4, true>(k + 5 * SHAPES);
+    fill<K_INT4_32>(k);
+    fill<K_INT4_64>(k + 2 * SHAPES);
+    fill<K_INT4_128>(k + 4 * SHAPES);
+    fill<K_MXF4>(k + 6 * SHAPES);
+    fill<K_NVF4>(k + 8 * SHAPES);
   }
 };
 const Variants g_variants;
+constexpr int SHAPE_SMEM[SHAPES] = {Shape<4>::BYTES, Shape<8>::BYTES, Shape<16>::BYTES};
 
-int smem_bytes(int nt) { return nt == 2 ? GemvSmem<2>::BYTES : GemvSmem<1>::BYTES; }
-
-// Per device, on the first call: the variants' shared-memory attribute and the
-// clusters of 1, 2 and 4 CTAs that are resident at once.
+// Per device, on the first call: the variants' shared-memory attribute.
 constexpr int MAX_DEVICES = 64;
 struct DeviceInfo {
   std::once_flag once;
   cudaError_t err = cudaSuccess;
-  int clusters[3] = {0, 0, 0};
 };
 DeviceInfo g_info[MAX_DEVICES];
 
-const DeviceInfo& device_info(int dev) {
+cudaError_t device_setup(int dev) {
   DeviceInfo& d = g_info[dev];
   std::call_once(d.once, [&] {
     for (int i = 0; i < VARIANTS && d.err == cudaSuccess; ++i)
       d.err = cudaFuncSetAttribute(reinterpret_cast<const void*>(g_variants.k[i]),
-                                   cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                   smem_bytes(i % SHAPES == shape_index(2, 1) ? 2 : 1));
-    d.clusters[0] = device_sms(dev);
-    for (int i = 1; i < 3 && d.err == cudaSuccess; ++i) {
-      cudaLaunchConfig_t cfg = {};
-      cfg.gridDim = dim3(static_cast<unsigned>(d.clusters[0] >> i << i), 1, 1);
-      cfg.blockDim = dim3(THREADS, 1, 1);
-      cfg.dynamicSmemBytes = smem_bytes(2);
-      cudaLaunchAttribute attr;
-      attr.id = cudaLaunchAttributeClusterDimension;
-      attr.val.clusterDim.x = 1u << i;
-      attr.val.clusterDim.y = 1;
-      attr.val.clusterDim.z = 1;
-      cfg.attrs = &attr;
-      cfg.numAttrs = 1;
-      d.err = cudaOccupancyMaxActiveClusters(&d.clusters[i],
-                                             reinterpret_cast<const void*>(g_variants.k[shape_index(2, 1)]), &cfg);
-    }
+                                   cudaFuncAttributeMaxDynamicSharedMemorySize, SHAPE_SMEM[i % SHAPES]);
   });
-  return d;
+  return d.err;
 }
 
 int run_gemv(const tcg_gemv_w4_args* args, cudaStream_t s) {
@@ -739,81 +1038,76 @@ int run_gemv(const tcg_gemv_w4_args* args, cudaStream_t s) {
   p.N = static_cast<int>(a.N);
   p.K = static_cast<int>(a.K);
   p.G = a.G;
-  p.group_shift = a.group == 16 ? 4 : a.group == 32 ? 5 : a.group == 64 ? 6 : 7;
   p.A = static_cast<const uint8_t*>(a.A);
   p.lda = a.lda;
   p.offsets = a.offsets;
-  p.B = a.B;
-  p.ldb = a.ldb / 2;
-  p.stride_b = a.stride_b / 2;
-  const int64_t scales = (a.G - 1) * a.stride_scale + (a.N - 1) * a.ld_scale + blocks_k;
   p.scale = static_cast<const uint8_t*>(a.scale);
   p.ld_scale = a.ld_scale * es;
   p.stride_scale = a.stride_scale * es;
-  p.scale_bytes = scales * es;
+  p.scale_row = static_cast<int>(blocks_k);
   p.zero = a.zero;
   p.ld_zero = a.ld_scale;
   p.stride_zero = a.stride_scale;
-  p.zero_bytes = scales;
-  // words that hold a row's slab: one more where rows start off a 4-byte boundary
-  const int seg_s = SLAB / a.group * es, seg_z = SLAB / a.group;
-  p.scale_words = seg_s / 4 + (p.ld_scale % 4 || p.stride_scale % 4 ? 1 : 0);
-  p.zero_words = (seg_z + 3) / 4 + (p.ld_zero % 4 || p.stride_zero % 4 ? 1 : 0);
+  // (then K is a multiple of 256, and of so much that a team's share of a row
+  // is one of 16 bytes)
+  const int64_t s_low = blocks_k * es | p.ld_scale | (a.G > 1 ? p.stride_scale : 0) |
+                        static_cast<int64_t>(reinterpret_cast<uintptr_t>(a.scale));
+  const int64_t z_low = blocks_k | p.ld_zero | (a.G > 1 ? p.stride_zero : 0) |
+                        static_cast<int64_t>(reinterpret_cast<uintptr_t>(a.zero));
+  p.bulk = s_low % 16 == 0 && (!a.zero || z_low % 16 == 0);
+  const int64_t lines = (a.K * 2 + 127) / 128;
+  p.a_row_lines = static_cast<int>(lines);
+  p.a_lines = a.R * lines <= 16384 ? static_cast<int>(a.R * lines) : 0;  // 2 MiB at most
   p.alpha = a.alpha;
   p.D = a.D;
   p.d_type = a.d_type;
   p.ldd = a.ldd;
-  p.tiles = static_cast<int>((a.N + TILE_N - 1) / TILE_N);
+  p.grains = static_cast<int>((a.N + GRAIN - 1) / GRAIN);
+  p.err = device_error_word(dev);
+  p.timeout_ns = wait_timeout_ns();
   p.slabs = static_cast<int>((a.K + SLAB - 1) / SLAB);
 
-  // rows per block: 16 when groups are expected to have more than 8 rows
+  // rows per block: as many as the groups are expected to have
   const int64_t active = std::min<int64_t>(a.G, a.R);
-  const int nt = a.R > 8 * active ? 2 : 1;
-  const int64_t units = std::max<int64_t>(active, (a.R + 8 * nt - 1) / (8 * nt)) * p.tiles;
-  if (units > INT32_MAX) return TCG_ERR_UNSUPPORTED;
-  // The team: KSL slabs a warp, over a cluster of `cl` CTAs.  The busiest
-  // team's tiles times the slabs each of its warps takes is the time; of equal
-  // ones the first below (fewer CTAs, then more slabs a warp) is taken.
-  const DeviceInfo& info = device_info(dev);
-  if (info.err != cudaSuccess) return record_cuda(info.err);
-  int best_ksl = 1, best_cl = 1;
-  int64_t best = INT64_MAX;
-  for (int i = 0, cl = 1; i < 3; ++i, cl *= 2) {
-    if (info.clusters[i] < 1) continue;
-    for (int ksl = nt == 1 ? 2 : 1; ksl >= 1; --ksl) {
-      const int want = (p.slabs + cl * ksl - 1) / (cl * ksl);
-      if (cl > 1 && want <= WARPS / 2) continue;  // half a CTA would idle
-      const int team_warps = std::min(WARPS, want);
-      const int teams = cl > 1 ? 1 : WARPS / team_warps;
-      const int64_t n = static_cast<int64_t>(info.clusters[i]) * teams;
-      const int64_t passes = (p.slabs + cl * ksl * team_warps - 1) / (cl * ksl * team_warps);
-      const int64_t time = (units + n - 1) / n * passes * ksl * (passes > 1 ? 2 : 1);
-      if (time < best) {
-        best = time;
-        best_ksl = ksl;
-        best_cl = cl;
-      }
-    }
+  const int tok = a.R > 8 * active ? 16 : a.R > 4 * active ? 8 : 4;
+  // (a block for every `tok` rows and one more per group there can be at most)
+  if ((a.R / tok + active) * p.grains > INT32_MAX) return TCG_ERR_UNSUPPORTED;
+  if (int rc = record_cuda(device_setup(dev))) return rc;
+  p.team_warps = std::min(WARPS, p.slabs);
+  p.teams = WARPS / p.team_warps;
+  p.whole = a.K % SLAB == 0;
+  const auto box = [](int bytes) { return bytes <= 32 ? 32 : bytes <= 64 ? 64 : 128; };
+  p.box_s = box(p.team_warps * (SLAB / a.group) * es);
+  p.box_z = box(p.team_warps * (SLAB / a.group));
+  if (p.bulk) {
+    if (int rc = make_byte_map(&p.tmap_s, a.scale, blocks_k * es, a.N, a.G, p.ld_scale, p.stride_scale, p.box_s, TILE_N))
+      return rc;
+    if (a.zero)
+      if (int rc = make_byte_map(&p.tmap_z, a.zero, blocks_k, a.N, a.G, p.ld_zero, p.stride_zero, p.box_z, TILE_N))
+        return rc;
   }
-  p.team_warps = std::min(WARPS, (p.slabs + best_cl * best_ksl - 1) / (best_cl * best_ksl));
-  p.teams = best_cl > 1 ? 1 : WARPS / p.team_warps;
-  const bool bf16 = a.in_type == TCG_IN_BF16;
-  const Kernel k = g_variants.k[(a.format * 2 + (bf16 ? 1 : 0)) * SHAPES + shape_index(nt, best_ksl)];
+  if (p.whole) {
+    if (int rc = make_slab_map(&p.tmap_b, a.B, SLAB / 2, a.N, a.K / SLAB, a.G, a.ldb / 2, a.stride_b / 2, TILE_N, p.team_warps))
+      return rc;
+  } else {
+    if (int rc = make_byte_map(&p.tmap_b, a.B, a.K / 2, a.N, a.G, a.ldb / 2, a.stride_b / 2, SLAB / 2, TILE_N)) return rc;
+  }
+  const int kind = a.format == TCG_W4_MXF4   ? K_MXF4
+                   : a.format == TCG_W4_NVF4 ? K_NVF4
+                   : a.group == 32           ? K_INT4_32
+                   : a.group == 64           ? K_INT4_64
+                                             : K_INT4_128;
+  const Kernel k = g_variants.k[(kind * 2 + (a.in_type == TCG_IN_BF16 ? 1 : 0)) * SHAPES + shape_index(tok)];
   cudaLaunchConfig_t cfg = {};
-  const int64_t ctas = std::min<int64_t>(info.clusters[best_cl / 2], units);
-  cfg.gridDim = dim3(static_cast<unsigned>(ctas * best_cl), 1, 1);
+  cfg.gridDim = dim3(static_cast<unsigned>(std::min<int64_t>(device_sms(dev), (a.R / tok + active) * p.grains)), 1, 1);
   cfg.blockDim = dim3(THREADS, 1, 1);
-  cfg.dynamicSmemBytes = smem_bytes(nt);
+  cfg.dynamicSmemBytes = SHAPE_SMEM[shape_index(tok)];
   cfg.stream = s;
-  cudaLaunchAttribute attr[2];
-  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  attr[0].val.programmaticStreamSerializationAllowed = 1;
-  attr[1].id = cudaLaunchAttributeClusterDimension;
-  attr[1].val.clusterDim.x = best_cl;
-  attr[1].val.clusterDim.y = 1;
-  attr[1].val.clusterDim.z = 1;
-  cfg.attrs = attr;
-  cfg.numAttrs = best_cl > 1 ? 2 : 1;
+  cudaLaunchAttribute attr;
+  attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr.val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = &attr;
+  cfg.numAttrs = 1;
   void* params[] = {&p};
   if (int rc = record_cuda(cudaLaunchKernelExC(&cfg, reinterpret_cast<const void*>(k), params))) return rc;
   set_launch_count(1);

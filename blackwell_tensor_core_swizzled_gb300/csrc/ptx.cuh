@@ -172,6 +172,15 @@ __device__ __forceinline__ void tma_load3(uint32_t dst, const void* map, int32_t
         : "memory");
 }
 
+__device__ __forceinline__ void tma_load_4d(uint32_t dst, const void* map, int32_t x, int32_t y, int32_t z, int32_t w,
+                                            uint32_t bar) {
+  asm volatile(
+      "cp.async.bulk.tensor.4d.shared::cluster.global.mbarrier::complete_tx::bytes"
+      " [%0], [%1, {%2, %3, %4, %5}], [%6];" ::"r"(dst),
+      "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(y), "r"(z), "r"(w), "r"(bar)
+      : "memory");
+}
+
 // Tile load global -> shared of every CTA in `mask` (cluster ranks): the
 // tile lands at the same CTA-relative address `dst` in each, and each
 // destination's mbarrier at offset `bar` receives its bytes.
