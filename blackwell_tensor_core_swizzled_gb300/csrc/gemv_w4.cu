@@ -22,8 +22,9 @@
 //                 points by a TMA copy each, for all slabs at once (a copy
 //                 takes its issuing thread 150 cycles, one for every warp or
 //                 row would take longer than the decoding);
-//   warps 17..19  add the warps' parts of a tile in a fixed order and store it
-//                 while the next tiles are decoded.
+//   the others    (three; with 16 activation rows, whose fragments want the
+//                 registers, one) add the warps' parts of a tile in a fixed
+//                 order and store it while the next tiles are decoded.
 // A team of warps covers K (the 16, or fewer when K is short: then a CTA has
 // several teams) and takes an equal share of the matrix rows; a K of more
 // slabs than warps is taken in passes over a chunk of tiles, whose sums wait
@@ -56,8 +57,6 @@ constexpr int MAX_GROUPS = 1024;
 constexpr int64_t MAX_EXTENT = int64_t{1} << 30;
 
 constexpr int WARPS = 16;          // decoding warps
-constexpr int ADD_WARPS = 3;       // one for each buffer of parts
-constexpr int THREADS = 32 * (WARPS + 1 + ADD_WARPS);
 constexpr int SLAB = 256;          // K per warp: 128 bytes of codes
 constexpr int TILE_N = 16;         // matrix rows per tile: one mma's
 // bytes of a matrix row's scales, zero points in a stage when they are copied
@@ -120,9 +119,11 @@ struct Shape {
   static constexpr int OUT = TOK * TILE_N;            // sums of a tile
   static constexpr int CAP = (TOK == 16 ? 4096 : TOK == 8 ? 2048 : 1024) / OUT;  // tiles of a chunk that is passed over more than once
   static constexpr int STAGES = TOK == 16 ? 3 : 4;    // ring stages
-  // buffers of parts: tile i of a chunk uses number i % PARTS, which adding
-  // warp i % PARTS empties, so that in every pass the same warp has the tile
-  static constexpr int PARTS = ADD_WARPS;
+  // buffers of parts: tile i of a chunk uses number i % PARTS, which one
+  // adding warp empties, so that in every pass the same warp has the tile
+  static constexpr int PARTS = TOK == 16 ? 2 : 3;
+  static constexpr int ADD_WARPS = TOK == 16 ? 1 : 3;
+  static constexpr int THREADS = 32 * (WARPS + 1 + ADD_WARPS);
   static constexpr int PART_PITCH = TOK == 4 ? 24 : 20;  // floats between a part's activation rows
   static constexpr int TILE_PART = TOK * PART_PITCH;  // floats of a warp's part
   // a stage: codes [warp][16 rows][128 bytes]; scales, then zero points [16 rows][pitch]
@@ -590,9 +591,9 @@ struct Cursor {
 };
 
 template <int KIND, bool BF16, int TOK>
-__global__ void __launch_bounds__(THREADS, 1) gemv_kernel(const __grid_constant__ GemvParams p) {
+__global__ void __launch_bounds__(Shape<TOK>::THREADS, 1) gemv_kernel(const __grid_constant__ GemvParams p) {
   using S = Shape<TOK>;
-  constexpr int NT = S::NT, STAGES = S::STAGES, PARTS = S::PARTS;
+  constexpr int NT = S::NT, STAGES = S::STAGES, PARTS = S::PARTS, THREADS = S::THREADS, ADD_WARPS = S::ADD_WARPS;
   extern __shared__ uint8_t smem_raw[];
   const uint32_t raw = smem_u32(smem_raw);
   uint8_t* smem = smem_raw + (((raw + 1023u) & ~1023u) - raw);
@@ -812,8 +813,7 @@ __global__ void __launch_bounds__(THREADS, 1) gemv_kernel(const __grid_constant_
         load_fragments<KIND, BF16, TOK>(p, rb, wk + cu.pass * p.team_warps, lane, smem + S::ACT + warp * S::ACT_BYTES,
                                        frag, undo);
       }
-      ok = wait_uniform(bar + 8 * stage, ph, wctx, SITE_MMA_FULL) &&
-           wait_uniform(bar + PFREE + 8 * buf, (buf_ph >> buf) & 1u, wctx, SITE_MMA_ACC_EMPTY);
+      ok = wait_uniform(bar + 8 * stage, ph, wctx, SITE_MMA_FULL);
       if (!ok) break;
       float acc[NT][4] = {};
       const int slab = wk + cu.pass * p.team_warps;
@@ -840,16 +840,17 @@ __global__ void __launch_bounds__(THREADS, 1) gemv_kernel(const __grid_constant_
         }
         rows16<KIND, BF16, TOK>(codes0 + stage * S::CODE_BYTES, s0, s1, z0, z1, p.bulk, lane, frag, undo, acc);
       }
+      __syncwarp();
+      if (lane == 0) mbar_arrive(bar + EMPTY + 8 * stage);
+      ok = wait_uniform(bar + PFREE + 8 * buf, (buf_ph >> buf) & 1u, wctx, SITE_MMA_ACC_EMPTY);
+      if (!ok) break;
       float* mine = part0 + buf * (WARPS * S::TILE_PART);
 #pragma unroll
       for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
         for (int i = 0; i < 4; i += S::STEP) mine[(8 * nt + (i & 1)) * S::PART_PITCH + 8 * (i >> 1)] = acc[nt][i];
       __syncwarp();
-      if (lane == 0) {
-        mbar_arrive(bar + EMPTY + 8 * stage);
-        mbar_arrive(bar + PFULL + 8 * buf);
-      }
+      if (lane == 0) mbar_arrive(bar + PFULL + 8 * buf);
       if (++stage == STAGES) {
         stage = 0;
         ph ^= 1u;
@@ -860,10 +861,10 @@ __global__ void __launch_bounds__(THREADS, 1) gemv_kernel(const __grid_constant_
     }
   } else {
     // --------------------------------------------------------------- adding
-    const int buf = warp - (WARPS + 1);
+    const int me = warp - (WARPS + 1);
     const float* parts0 = reinterpret_cast<const float*>(smem + S::PART);
     float* sums = reinterpret_cast<float*>(smem + S::SUM);
-    uint32_t ph = 0;  // a parity bit per team
+    uint32_t ph[PARTS / ADD_WARPS] = {};  // for each of its buffers a parity bit per team
     // lane t < teams follows team t
     Cur mine = start(lane);
     if (lane >= p.teams) mine.rows = 0;
@@ -874,7 +875,8 @@ __global__ void __launch_bounds__(THREADS, 1) gemv_kernel(const __grid_constant_
 #pragma unroll 1
       for (int t = 0; t < p.teams; ++t) {
         const int rows = __shfl_sync(0xffffffffu, mine.rows, t), idx = __shfl_sync(0xffffffffu, mine.i, t);
-        if (!rows || idx % PARTS != buf) continue;
+        const int buf = idx % PARTS;
+        if (!rows || buf % ADD_WARPS != me) continue;
         const int n0 = __shfl_sync(0xffffffffu, mine.n0, t), pass = __shfl_sync(0xffffffffu, mine.pass, t);
         const int blk = __shfl_sync(0xffffffffu, mine.block, t);
         if (blk != block) {
@@ -882,9 +884,10 @@ __global__ void __launch_bounds__(THREADS, 1) gemv_kernel(const __grid_constant_
           o = row_block<TOK>(p, seg, pre, single, span, block);
           if (p.alpha) alpha = p.alpha[o.g];
         }
-        ok = wait_uniform(bars(t) + PFULL + 8 * buf, (ph >> t) & 1u, wctx, SITE_EPI_ACC_FULL);
+        uint32_t& parity = ph[PARTS == ADD_WARPS || buf == 0 ? 0 : PARTS / ADD_WARPS - 1];
+        ok = wait_uniform(bars(t) + PFULL + 8 * buf, (parity >> t) & 1u, wctx, SITE_EPI_ACC_FULL);
         if (!ok) break;
-        ph ^= 1u << t;
+        parity ^= 1u << t;
         const float* parts = parts0 + (buf * WARPS + t * p.team_warps) * S::TILE_PART;
 #pragma unroll
         for (int j0 = 0; j0 < S::OUT; j0 += 128) {
@@ -965,6 +968,7 @@ struct Variants {
 };
 const Variants g_variants;
 constexpr int SHAPE_SMEM[SHAPES] = {Shape<4>::BYTES, Shape<8>::BYTES, Shape<16>::BYTES};
+constexpr int SHAPE_THREADS[SHAPES] = {Shape<4>::THREADS, Shape<8>::THREADS, Shape<16>::THREADS};
 
 // Per device, on the first call: the variants' shared-memory attribute.
 constexpr int MAX_DEVICES = 64;
@@ -1100,7 +1104,7 @@ int run_gemv(const tcg_gemv_w4_args* args, cudaStream_t s) {
   const Kernel k = g_variants.k[(kind * 2 + (a.in_type == TCG_IN_BF16 ? 1 : 0)) * SHAPES + shape_index(tok)];
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(static_cast<unsigned>(std::min<int64_t>(device_sms(dev), (a.R / tok + active) * p.grains)), 1, 1);
-  cfg.blockDim = dim3(THREADS, 1, 1);
+  cfg.blockDim = dim3(SHAPE_THREADS[shape_index(tok)], 1, 1);
   cfg.dynamicSmemBytes = SHAPE_SMEM[shape_index(tok)];
   cfg.stream = s;
   cudaLaunchAttribute attr;
