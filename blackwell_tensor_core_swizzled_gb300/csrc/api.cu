@@ -866,8 +866,6 @@ int max_resident_clusters(int dev, const KernelInfo& ki, int* out) {
   return max_clusters_for(device_state(dev), ki, out);
 }
 
-int stream_workspace(int dev, cudaStream_t s, size_t bytes, void** out) { return workspace(dev, s, bytes, out); }
-
 namespace {
 
 // Swizzled tiled map (span: 128, 64 or 32 bytes), encoded on every call

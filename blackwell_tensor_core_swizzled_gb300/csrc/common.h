@@ -74,8 +74,6 @@ int device_sms(int dev);
 // Clusters of the variant that fit on the device at once (its shared-memory
 // attribute is set on the first call).
 int max_resident_clusters(int dev, const KernelInfo& ki, int* out);
-// The stream's library workspace, at least `bytes` (grown when smaller).
-int stream_workspace(int dev, cudaStream_t s, size_t bytes, void** out);
 // 128-byte swizzled tiled map of 16-bit elements over [outer][mid][inner] with
 // strides in elements, boxes of 64 x box_mid (x 1); outer 0: a 2-D map.
 int make_operand_map(CUtensorMap* map, const void* base, bool bf16, uint64_t inner, uint64_t mid, uint64_t outer,

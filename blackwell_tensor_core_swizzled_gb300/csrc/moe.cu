@@ -5,9 +5,13 @@
 #include <cuda_fp16.h>
 #include <cuda_runtime.h>
 
+#include <algorithm>
 #include <cstdint>
+#include <mutex>
+#include <type_traits>
 
 #include "common.h"
+#include "ptx.cuh"
 
 namespace tcg {
 
@@ -30,30 +34,74 @@ __device__ __forceinline__ __nv_bfloat16 from_f32<__nv_bfloat16>(float v) { retu
 // ---------------------------------------------------------------------- sort
 //
 // A stable counting sort: rank of entry i in bucket e (its expert, or E when
-// dropped) = entries of smaller buckets + entries of e before i.  Every warp
-// owns a contiguous range of entries; counts[w][e] is first the number of
-// entries of e in warp w's range, then (exclusive sums over warps and
-// buckets) the rank of the warp's next entry of e.  Within 32 entries the
-// lanes of one bucket find each other with match_any and take consecutive
-// ranks in lane order, so the order never depends on timing.
+// dropped) = entries of smaller buckets + entries of e before i.  A cluster of
+// SORT_CTAS CTAs sorts (one CTA up to SORT_ONE entries, where the cluster's
+// barriers would cost more than they save); every warp owns a contiguous range
+// of entries.  counts[w][e] is first the number of entries of e in warp w's
+// range; exclusive sums over the warps of a CTA, the CTAs of the cluster (read
+// from their shared memory) and the buckets turn it into the rank of the
+// warp's next entry of e.  Within 32 entries the lanes of one bucket find each
+// other with match_any and take consecutive ranks in lane order, so the order
+// never depends on timing.
 constexpr int SORT_WARPS = 32;
+constexpr int SORT_CTAS = 8;
+constexpr int SORT_ONE = 2048;
 
 __device__ __forceinline__ int bucket_of(int expert, int E) {
   return static_cast<unsigned>(expert) < static_cast<unsigned>(E) ? expert : E;
 }
 
+__device__ __forceinline__ int ld_cluster_s32(uint32_t addr) {
+  int v;
+  asm volatile("ld.shared::cluster.s32 %0, [%1];" : "=r"(v) : "r"(addr));
+  return v;
+}
+
+// Exclusive sum of one value a thread over the CTA's 32 warps; total to all.
+__device__ __forceinline__ int block_scan(int v, int* warp_sum, int* total) {
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  int incl = v;
+#pragma unroll
+  for (int d = 1; d < 32; d <<= 1) {
+    const int o = __shfl_up_sync(0xffffffffu, incl, d);
+    if (lane >= d) incl += o;
+  }
+  if (lane == 31) warp_sum[warp] = incl;
+  __syncthreads();
+  if (warp == 0) {
+    int w = warp_sum[lane];
+#pragma unroll
+    for (int d = 1; d < 32; d <<= 1) {
+      const int o = __shfl_up_sync(0xffffffffu, w, d);
+      if (lane >= d) w += o;
+    }
+    warp_sum[lane] = w;
+  }
+  __syncthreads();
+  *total = warp_sum[31];
+  return incl - v + (warp ? warp_sum[warp - 1] : 0);
+}
+
+template <int CTAS>
 __global__ void __launch_bounds__(32 * SORT_WARPS) sort_kernel(int n, int E, const int32_t* __restrict__ expert,
                                                                int32_t* __restrict__ offsets,
                                                                int32_t* __restrict__ position,
                                                                int32_t* __restrict__ source) {
-  extern __shared__ int counts[];  // [SORT_WARPS][E + 1]
+  extern __shared__ int counts[];  // [SORT_WARPS][E + 1], then this CTA's counts [E + 1]
   __shared__ int warp_sum[32];
   const int NB = E + 1;
+  int* cta_counts = counts + SORT_WARPS * NB;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int rank = CTAS > 1 ? static_cast<int>(cluster_ctarank()) : 0;
   for (int i = threadIdx.x; i < SORT_WARPS * NB; i += blockDim.x) counts[i] = 0;
   __syncthreads();
-  const int per = ((n + SORT_WARPS - 1) / SORT_WARPS + 31) / 32 * 32;  // entries per warp, whole rounds
-  const int lo = min(n, warp * per), hi = min(n, lo + per);
+  griddep_wait();
+  griddep_launch_dependents();
+  const int parts = CTAS * SORT_WARPS;
+  const int per = ((n + parts - 1) / parts + 31) / 32 * 32;  // entries per warp, whole rounds
+  const int64_t from = static_cast<int64_t>(rank * SORT_WARPS + warp) * per;
+  const int lo = static_cast<int>(min(static_cast<int64_t>(n), from));
+  const int hi = static_cast<int>(min(static_cast<int64_t>(n), from + per));
   int* mine = counts + warp * NB;
   for (int i0 = lo; i0 < hi; i0 += 32) {
     const int i = i0 + lane;
@@ -63,48 +111,49 @@ __global__ void __launch_bounds__(32 * SORT_WARPS) sort_kernel(int n, int E, con
     __syncwarp();
   }
   __syncthreads();
-  // exclusive sums over the warps for each bucket, then over the buckets: the
-  // thread of bucket b (NB <= 1025: the thread of bucket 0 also takes 1024)
-  int total = 0;
-  const int b = threadIdx.x;
-  if (b < NB) {
+  // over the warps, for each bucket (a thread each; NB <= 1025: two for the first)
+  for (int b = threadIdx.x; b < NB; b += 32 * SORT_WARPS) {
+    int total = 0;
+#pragma unroll 8
     for (int w = 0; w < SORT_WARPS; ++w) {
       const int c = counts[w * NB + b];
       counts[w * NB + b] = total;
       total += c;
     }
+    cta_counts[b] = total;
   }
-  int incl = total;
-  for (int d = 1; d < 32; d <<= 1) {
-    const int v = __shfl_up_sync(0xffffffffu, incl, d);
-    if (lane >= d) incl += v;
-  }
-  if (lane == 31) warp_sum[warp] = incl;
-  __syncthreads();
-  if (warp == 0) {
-    int s = warp_sum[lane];
-    for (int d = 1; d < 32; d <<= 1) {
-      const int v = __shfl_up_sync(0xffffffffu, s, d);
-      if (lane >= d) s += v;
+  if constexpr (CTAS > 1)
+    cluster_sync();
+  else
+    __syncthreads();
+  // over the cluster's CTAs and the buckets; bucket 1024 follows the others
+  int carry = 0;
+  for (int b0 = 0; b0 < NB; b0 += 32 * SORT_WARPS) {
+    const int b = b0 + static_cast<int>(threadIdx.x);
+    int total = 0, before = 0;
+    if (b < NB) {
+      if constexpr (CTAS > 1) {
+        const uint32_t at = smem_u32(cta_counts + b);
+#pragma unroll
+        for (int r = 0; r < CTAS; ++r) {
+          const int c = ld_cluster_s32(mapa_shared(at, r));
+          if (r < rank) before += c;
+          total += c;
+        }
+      } else {
+        total = cta_counts[b];
+      }
     }
-    warp_sum[lane] = s;
-  }
-  __syncthreads();
-  const int start = incl - total + (warp ? warp_sum[warp - 1] : 0);
-  if (b < NB) {
-    offsets[b] = start;  // offsets[E] = start of the dropped bucket
-    for (int w = 0; w < SORT_WARPS; ++w) counts[w * NB + b] += start;
-  }
-  if (NB > 1024 && b == 0) {  // bucket 1024: the dropped entries of E = 1024
-    int t = warp_sum[31];
-    offsets[1024] = t;
-    for (int w = 0; w < SORT_WARPS; ++w) {
-      const int c = counts[w * NB + 1024];
-      counts[w * NB + 1024] = t;
-      t += c;
+    int sum;
+    const int start = carry + block_scan(total, warp_sum, &sum);
+    carry += sum;
+    if (b < NB) {
+      if (rank == 0) offsets[b] = start;  // offsets[E]: the start of the dropped entries
+#pragma unroll 8
+      for (int w = 0; w < SORT_WARPS; ++w) counts[w * NB + b] += start + before;
     }
+    __syncthreads();
   }
-  __syncthreads();
   for (int i0 = lo; i0 < hi; i0 += 32) {
     const int i = i0 + lane;
     const int e = i < hi ? bucket_of(expert[i], E) : -1;
@@ -118,61 +167,189 @@ __global__ void __launch_bounds__(32 * SORT_WARPS) sort_kernel(int n, int E, con
     if (e >= 0 && lane == __ffs(same) - 1) mine[e] += __popc(same);
     __syncwarp();
   }
+  if constexpr (CTAS > 1) cluster_sync();  // peers have read this CTA's counts
 }
 
 // ------------------------------------------------------- dispatch and combine
+//
+// All three walk the tokens, so that a token's own row moves once and its
+// topk sorted rows once each; what bounds them is those bytes.  A thread takes
+// PACK elements of a row at a time (16 bytes where bases and rows allow, else
+// one element) and has the loads of up to 8 rows in flight.
 
-template <class T>
-__global__ void dispatch_kernel(int topk, int64_t H, const T* __restrict__ X, int64_t ldx,
-                                const int32_t* __restrict__ position, T* __restrict__ Xs, int64_t ldxs) {
-  const int64_t i = blockIdx.x;
-  const int p = position[i];
-  const T* src = X + (i / topk) * ldx;
-  T* dst = Xs + static_cast<int64_t>(p < 0 ? -1 - p : p) * ldxs;
-  for (int64_t h = threadIdx.x; h < H; h += blockDim.x) dst[h] = p < 0 ? from_f32<T>(0.0f) : src[h];
+template <class T, bool WIDE>
+struct Pack {
+  static constexpr int N = WIDE ? 16 / sizeof(T) : 1;
+  T v[N];
+  __device__ __forceinline__ static Pack load(const T* p) {
+    Pack r;
+    if constexpr (WIDE)
+      *reinterpret_cast<uint4*>(r.v) = __ldcs(reinterpret_cast<const uint4*>(p));
+    else
+      r.v[0] = *p;
+    return r;
+  }
+  __device__ __forceinline__ void store(T* p) const {
+    if constexpr (WIDE)
+      __stcs(reinterpret_cast<uint4*>(p), *reinterpret_cast<const uint4*>(v));
+    else
+      *p = v[0];
+  }
+};
+
+constexpr int MOVE_THREADS = 256;
+constexpr int AHEAD = 8;  // rows of a token in flight
+
+// Sorted row of a position, and whether the entry is kept; positions outside
+// the sorted rows (not a result of the sort) are left alone.
+struct Place {
+  int64_t row;
+  bool kept, valid;
+};
+__device__ __forceinline__ Place place(int p, int64_t rows) {
+  Place r;
+  r.kept = p >= 0;
+  r.row = r.kept ? p : -1 - static_cast<int64_t>(p);
+  r.valid = r.row < rows;
+  return r;
 }
 
-template <class T>
-__global__ void combine_kernel(int topk, int64_t H, const T* __restrict__ Ys, int64_t ldys,
-                               const int32_t* __restrict__ position, const float* __restrict__ weight,
-                               T* __restrict__ Y, int64_t ldy) {
+// Grid: (tokens, parts of a row).
+template <class T, bool WIDE>
+__global__ void __launch_bounds__(MOVE_THREADS) dispatch_kernel(int topk, int64_t rows, int64_t H,
+                                                                const T* __restrict__ X, int64_t ldx,
+                                                                const int32_t* __restrict__ position,
+                                                                T* __restrict__ Xs, int64_t ldxs) {
+  using P = Pack<T, WIDE>;
+  griddep_wait();
+  griddep_launch_dependents();
   const int64_t t = blockIdx.x;
-  for (int64_t h = threadIdx.x; h < H; h += blockDim.x) {
-    float acc = 0.0f;
+  const int32_t* pos = position + t * topk;
+  const T* src = X + t * ldx;
+  const int64_t step = static_cast<int64_t>(gridDim.y) * MOVE_THREADS * P::N;
+  for (int64_t h = (static_cast<int64_t>(blockIdx.y) * MOVE_THREADS + threadIdx.x) * P::N; h < H; h += step) {
+    const P x = P::load(src + h);
     for (int j = 0; j < topk; ++j) {
-      const int p = position[t * topk + j];
-      if (p >= 0) acc += (weight ? weight[t * topk + j] : 1.0f) * to_f32(Ys[static_cast<int64_t>(p) * ldys + h]);
+      const Place d = place(pos[j], rows);
+      if (!d.valid) continue;
+      P y = x;
+      if (!d.kept)
+#pragma unroll
+        for (int i = 0; i < P::N; ++i) y.v[i] = from_f32<T>(0.0f);
+      y.store(Xs + d.row * ldxs + h);
     }
-    Y[t * ldy + h] = from_f32<T>(acc);
   }
 }
 
-template <class T>
-__global__ void __launch_bounds__(256) combine_grad_kernel(int topk, int64_t H, const T* __restrict__ dY, int64_t lddy,
-                                                           const T* __restrict__ Ys, int64_t ldys,
-                                                           const int32_t* __restrict__ position,
-                                                           const float* __restrict__ weight, T* __restrict__ dYs,
-                                                           int64_t lddys, float* __restrict__ dweight) {
-  const int64_t i = blockIdx.x;
-  const int p = position[i];
-  const int64_t row = p < 0 ? -1 - p : p;
-  const T* g = dY + (i / topk) * lddy;
-  const float w = weight ? weight[i] : 1.0f;
-  float dot = 0.0f;
-  for (int64_t h = threadIdx.x; h < H; h += blockDim.x) {
-    const float d = p < 0 ? 0.0f : to_f32(g[h]);
-    dYs[row * lddys + h] = from_f32<T>(p < 0 ? 0.0f : w * d);
-    if (Ys && p >= 0) dot += d * to_f32(Ys[row * ldys + h]);
+template <class T, bool WIDE>
+__global__ void __launch_bounds__(MOVE_THREADS) combine_kernel(int topk, int64_t rows, int64_t H,
+                                                               const T* __restrict__ Ys, int64_t ldys,
+                                                               const int32_t* __restrict__ position,
+                                                               const float* __restrict__ weight, T* __restrict__ Y,
+                                                               int64_t ldy) {
+  using P = Pack<T, WIDE>;
+  griddep_wait();
+  griddep_launch_dependents();
+  const int64_t t = blockIdx.x;
+  const int32_t* pos = position + t * topk;
+  const float* wt = weight ? weight + t * topk : nullptr;
+  const int64_t step = static_cast<int64_t>(gridDim.y) * MOVE_THREADS * P::N;
+  for (int64_t h = (static_cast<int64_t>(blockIdx.y) * MOVE_THREADS + threadIdx.x) * P::N; h < H; h += step) {
+    float acc[P::N] = {};
+    for (int j0 = 0; j0 < topk; j0 += AHEAD) {
+      P y[AHEAD];
+      float w[AHEAD];
+      bool use[AHEAD];
+#pragma unroll
+      for (int j = 0; j < AHEAD; ++j) {
+        use[j] = false;
+        if (j0 + j < topk) {
+          const Place s = place(pos[j0 + j], rows);
+          use[j] = s.kept && s.valid;
+          if (use[j]) {
+            y[j] = P::load(Ys + s.row * ldys + h);
+            w[j] = wt ? wt[j0 + j] : 1.0f;
+          }
+        }
+      }
+#pragma unroll
+      for (int j = 0; j < AHEAD; ++j)
+        if (use[j])
+#pragma unroll
+          for (int i = 0; i < P::N; ++i) acc[i] = fmaf(w[j], to_f32(y[j].v[i]), acc[i]);
+    }
+    P out;
+#pragma unroll
+    for (int i = 0; i < P::N; ++i) out.v[i] = from_f32<T>(acc[i]);
+    out.store(Y + t * ldy + h);
   }
-  if (!dweight) return;
-  __shared__ float part[8];
-  for (int d = 16; d > 0; d >>= 1) dot += __shfl_xor_sync(0xffffffffu, dot, d);
-  if ((threadIdx.x & 31) == 0) part[threadIdx.x >> 5] = dot;
-  __syncthreads();
-  if (threadIdx.x == 0) {
-    float s = 0.0f;
-    for (int k = 0; k < 8; ++k) s += part[k];
-    dweight[i] = s;
+}
+
+// One block a token: dYs rows and (dweight) the dots, up to AHEAD choices at a
+// time.  A thread's terms are added in the order of h, then the warp's lanes
+// and the block's warps in a fixed order.
+template <class T, bool WIDE>
+__global__ void __launch_bounds__(MOVE_THREADS) combine_grad_kernel(int topk, int64_t rows, int64_t H,
+                                                                    const T* __restrict__ dY, int64_t lddy,
+                                                                    const T* __restrict__ Ys, int64_t ldys,
+                                                                    const int32_t* __restrict__ position,
+                                                                    const float* __restrict__ weight,
+                                                                    T* __restrict__ dYs, int64_t lddys,
+                                                                    float* __restrict__ dweight) {
+  using P = Pack<T, WIDE>;
+  constexpr int MINE = AHEAD / 2;  // choices at a time: a row to read and one to write each
+  __shared__ float part[MOVE_THREADS / 32][MINE];
+  griddep_wait();
+  griddep_launch_dependents();
+  const int64_t t = blockIdx.x;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const T* g = dY + t * lddy;
+  for (int j0 = 0; j0 < topk; j0 += MINE) {
+    Place s[MINE];
+    float w[MINE], dot[MINE] = {};
+#pragma unroll
+    for (int j = 0; j < MINE; ++j) {
+      s[j] = Place{0, false, false};
+      w[j] = 0.0f;
+      if (j0 + j < topk) {
+        s[j] = place(position[t * topk + j0 + j], rows);
+        if (s[j].kept) w[j] = weight ? weight[t * topk + j0 + j] : 1.0f;
+      }
+    }
+    for (int64_t h = static_cast<int64_t>(threadIdx.x) * P::N; h < H; h += MOVE_THREADS * P::N) {
+      P y[MINE];
+#pragma unroll
+      for (int j = 0; j < MINE; ++j)
+        if (dweight && s[j].kept && s[j].valid) y[j] = P::load(Ys + s[j].row * ldys + h);
+      const P d = P::load(g + h);
+#pragma unroll
+      for (int j = 0; j < MINE; ++j) {
+        if (!s[j].valid) continue;
+        P o;
+#pragma unroll
+        for (int i = 0; i < P::N; ++i) {
+          const float v = to_f32(d.v[i]);
+          o.v[i] = from_f32<T>(s[j].kept ? w[j] * v : 0.0f);
+          if (dweight && s[j].kept) dot[j] = fmaf(v, to_f32(y[j].v[i]), dot[j]);
+        }
+        o.store(dYs + s[j].row * lddys + h);
+      }
+    }
+    if (!dweight) continue;
+#pragma unroll
+    for (int j = 0; j < MINE; ++j) {
+#pragma unroll
+      for (int k = 16; k > 0; k >>= 1) dot[j] += __shfl_xor_sync(0xffffffffu, dot[j], k);
+      if (lane == 0) part[warp][j] = dot[j];
+    }
+    __syncthreads();
+    if (threadIdx.x < MINE && j0 + static_cast<int>(threadIdx.x) < topk) {
+      float sum = 0.0f;
+#pragma unroll
+      for (int k = 0; k < MOVE_THREADS / 32; ++k) sum += part[k][threadIdx.x];
+      dweight[t * topk + j0 + threadIdx.x] = sum;
+    }
+    __syncthreads();
   }
 }
 
@@ -199,11 +376,47 @@ int check_words(const void* p) {
   return reinterpret_cast<uintptr_t>(p) % 4 ? TCG_ERR_ALIGNMENT : TCG_OK;
 }
 
-int launched(int launches) {
-  const cudaError_t e = cudaGetLastError();
-  if (e != cudaSuccess) return record_cuda(e);
-  set_launch_count(launches);
+// Launch as a programmatic dependent of the stream's previous kernel (every
+// kernel here waits with griddepcontrol.wait before it touches memory).
+template <class... Params, class... Args>
+int launch(void (*kernel)(Params...), dim3 grid, int threads, int smem, int cluster, cudaStream_t s, Args... args) {
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = grid;
+  cfg.blockDim = dim3(static_cast<unsigned>(threads), 1, 1);
+  cfg.dynamicSmemBytes = static_cast<size_t>(smem);
+  cfg.stream = s;
+  cudaLaunchAttribute attr[2];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  attr[1].id = cudaLaunchAttributeClusterDimension;
+  attr[1].val.clusterDim.x = static_cast<unsigned>(cluster);
+  attr[1].val.clusterDim.y = 1;
+  attr[1].val.clusterDim.z = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = cluster > 1 ? 2 : 1;
+  if (int rc = record_cuda(cudaLaunchKernelEx(&cfg, kernel, static_cast<Params>(args)...))) return rc;
+  set_launch_count(1);
   return TCG_OK;
+}
+
+// Both sort kernels' shared-memory attribute, once a device.
+constexpr int MAX_DEVICES = 64;
+constexpr int sort_smem(int E) { return (SORT_WARPS + 1) * (E + 1) * 4; }
+struct SortSetup {
+  std::once_flag once;
+  cudaError_t err = cudaSuccess;
+};
+SortSetup g_sort[MAX_DEVICES];
+
+cudaError_t sort_setup(int dev) {
+  SortSetup& d = g_sort[dev];
+  std::call_once(d.once, [&] {
+    d.err = cudaFuncSetAttribute(sort_kernel<1>, cudaFuncAttributeMaxDynamicSharedMemorySize, sort_smem(MAX_EXPERTS));
+    if (d.err == cudaSuccess)
+      d.err = cudaFuncSetAttribute(sort_kernel<SORT_CTAS>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                   sort_smem(MAX_EXPERTS));
+  });
+  return d.err;
 }
 
 int run_sort(int64_t T, int topk, int E, const int32_t* expert, int32_t* offsets, int32_t* position, int32_t* source,
@@ -220,21 +433,35 @@ int run_sort(int64_t T, int topk, int E, const int32_t* expert, int32_t* offsets
   }
   int dev;
   if (int rc = current_device_checked(&dev)) return rc;
-  const int smem = SORT_WARPS * (E + 1) * 4;
-  if (int rc = record_cuda(cudaFuncSetAttribute(sort_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem)))
-    return rc;
-  sort_kernel<<<1, 32 * SORT_WARPS, smem, s>>>(static_cast<int>(T * topk), E, expert, offsets, position, source);
-  return launched(1);
+  if (int rc = record_cuda(sort_setup(dev))) return rc;
+  const int n = static_cast<int>(T * topk);
+  if (n <= SORT_ONE)
+    return launch(sort_kernel<1>, dim3(1), 32 * SORT_WARPS, sort_smem(E), 1, s, n, E, expert, offsets, position, source);
+  return launch(sort_kernel<SORT_CTAS>, dim3(SORT_CTAS), 32 * SORT_WARPS, sort_smem(E), SORT_CTAS, s, n, E, expert,
+                offsets, position, source);
 }
 
+// f(element type's value, whether rows move as 16-byte words)
 template <class F>
-void for_type(tcg_dtype type, F&& f) {
-  if (type == TCG_F32)
-    f(float{});
-  else if (type == TCG_F16)
-    f(__half{});
-  else
-    f(__nv_bfloat16{});
+int for_type(tcg_dtype type, bool wide, F&& f) {
+  if (type == TCG_F32) return wide ? f(float{}, std::true_type{}) : f(float{}, std::false_type{});
+  if (type == TCG_F16) return wide ? f(__half{}, std::true_type{}) : f(__half{}, std::false_type{});
+  return wide ? f(__nv_bfloat16{}, std::true_type{}) : f(__nv_bfloat16{}, std::false_type{});
+}
+
+// Rows of H elements whose starts are all 16-byte aligned.
+bool wide_rows(tcg_dtype type, int64_t H, const void* a, int64_t lda, const void* b, int64_t ldb) {
+  const int per = type == TCG_F32 ? 4 : 8;
+  return H % per == 0 && lda % per == 0 && ldb % per == 0 &&
+         (reinterpret_cast<uintptr_t>(a) | reinterpret_cast<uintptr_t>(b)) % 16 == 0;
+}
+
+// Blocks a token's row is split into: one, unless there are so few tokens that
+// SMs would idle.
+unsigned row_parts(int64_t T, int64_t H, tcg_dtype type, bool wide, int dev) {
+  const int64_t packs = wide ? H / (type == TCG_F32 ? 4 : 8) : H;
+  const int64_t most = std::max<int64_t>(1, (packs + MOVE_THREADS - 1) / MOVE_THREADS);
+  return static_cast<unsigned>(std::min<int64_t>(most, std::max<int64_t>(1, 4 * device_sms(dev) / T)));
 }
 
 int run_dispatch(tcg_dtype type, int64_t T, int topk, int64_t H, const void* X, int64_t ldx, const int32_t* position,
@@ -247,12 +474,13 @@ int run_dispatch(tcg_dtype type, int64_t T, int topk, int64_t H, const void* X, 
   if (int rc = check_words(position)) return rc;
   int dev;
   if (int rc = current_device_checked(&dev)) return rc;
-  for_type(type, [&](auto z) {
+  const bool wide = wide_rows(type, H, X, ldx, Xs, ldxs);
+  const unsigned parts = row_parts(T, H, type, wide, dev);
+  return for_type(type, wide, [&](auto z, auto w) {
     using E = decltype(z);
-    dispatch_kernel<E><<<static_cast<unsigned>(T * topk), 256, 0, s>>>(topk, H, static_cast<const E*>(X), ldx, position,
-                                                                       static_cast<E*>(Xs), ldxs);
+    return launch(dispatch_kernel<E, decltype(w)::value>, dim3(static_cast<unsigned>(T), parts), MOVE_THREADS, 0, 1, s,
+                  topk, T * topk, H, static_cast<const E*>(X), ldx, position, static_cast<E*>(Xs), ldxs);
   });
-  return launched(1);
 }
 
 int run_combine(tcg_dtype type, int64_t T, int topk, int64_t H, const void* Ys, int64_t ldys, const int32_t* position,
@@ -266,12 +494,13 @@ int run_combine(tcg_dtype type, int64_t T, int topk, int64_t H, const void* Ys, 
   if (reinterpret_cast<uintptr_t>(weight) % 4) return TCG_ERR_ALIGNMENT;
   int dev;
   if (int rc = current_device_checked(&dev)) return rc;
-  for_type(type, [&](auto z) {
+  const bool wide = wide_rows(type, H, Ys, ldys, Y, ldy);
+  const unsigned parts = row_parts(T, H, type, wide, dev);
+  return for_type(type, wide, [&](auto z, auto w) {
     using E = decltype(z);
-    combine_kernel<E><<<static_cast<unsigned>(T), 256, 0, s>>>(topk, H, static_cast<const E*>(Ys), ldys, position,
-                                                               weight, static_cast<E*>(Y), ldy);
+    return launch(combine_kernel<E, decltype(w)::value>, dim3(static_cast<unsigned>(T), parts), MOVE_THREADS, 0, 1, s,
+                  topk, T * topk, H, static_cast<const E*>(Ys), ldys, position, weight, static_cast<E*>(Y), ldy);
   });
-  return launched(1);
 }
 
 int run_combine_grad(tcg_dtype type, int64_t T, int topk, int64_t H, const void* dY, int64_t lddy, const void* Ys,
@@ -291,13 +520,13 @@ int run_combine_grad(tcg_dtype type, int64_t T, int topk, int64_t H, const void*
   if (reinterpret_cast<uintptr_t>(weight) % 4) return TCG_ERR_ALIGNMENT;
   int dev;
   if (int rc = current_device_checked(&dev)) return rc;
-  for_type(type, [&](auto z) {
+  const bool wide = wide_rows(type, H, dY, lddy, dYs, lddys) && (!Ys || wide_rows(type, H, Ys, ldys, Ys, ldys));
+  return for_type(type, wide, [&](auto z, auto w) {
     using E = decltype(z);
-    combine_grad_kernel<E><<<static_cast<unsigned>(T * topk), 256, 0, s>>>(
-        topk, H, static_cast<const E*>(dY), lddy, static_cast<const E*>(Ys), ldys, position, weight,
-        static_cast<E*>(dYs), lddys, dweight);
+    return launch(combine_grad_kernel<E, decltype(w)::value>, dim3(static_cast<unsigned>(T)), MOVE_THREADS, 0, 1, s, topk,
+                  T * topk, H, static_cast<const E*>(dY), lddy, static_cast<const E*>(Ys), ldys, position, weight,
+                  static_cast<E*>(dYs), lddys, dweight);
   });
-  return launched(1);
 }
 
 }  // namespace

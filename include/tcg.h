@@ -31,8 +31,7 @@
  * use library-owned device workspaces per (device, stream), allocated on
  * first use and grown when needed (growing frees the old one, which waits for
  * the device); nothing else allocates device memory.  Calls on different
- * streams use different workspaces and may run concurrently.  tcg_moe_sort
- * uses the block-scale workspace of its stream in the same way.  A call may be
+ * streams use different workspaces and may run concurrently.  A call may be
  * captured into a CUDA graph once an earlier call on the same stream has
  * allocated a workspace at least as large (a workspace that would have to
  * grow during capture fails the call with TCG_ERR_CUDA); the graph reuses
@@ -297,15 +296,15 @@ int tcg_gemm_chain(tcg_input in_type, int64_t M, int64_t N1, int64_t N2, int64_t
  * source [T * topk] (the entry i at sorted row p) from expert [T][topk].
  * 1 <= E <= 1024, 1 <= topk, T * topk < 2^30 (TCG_ERR_UNSUPPORTED beyond).
  * T == 0: only offsets is written.  The result is the same on every call
- * (no atomics decide an order).  Uses the stream's library workspace for
- * more than 16384 entries. */
+ * (no atomics decide an order). */
 int tcg_moe_sort(int64_t T, int topk, int E, const int32_t* expert, int32_t* offsets, int32_t* position,
                  int32_t* source, void* stream);
 
 /* Xs[p][0..H) = X[t][0..H) for every kept entry, 0 for a dropped one; type is
  * the element type of both.  Leading dimensions in elements (0 = H); no
  * alignment beyond the element's (16-byte aligned bases and rows move as
- * 16-byte words).  Its gradient is tcg_moe_combine with weight = NULL. */
+ * 16-byte words).  Its gradient is tcg_moe_combine with weight = NULL.
+ * Positions that name no sorted row are passed over, here and below. */
 int tcg_moe_dispatch(tcg_dtype type, int64_t T, int topk, int64_t H, const void* X, int64_t ldx,
                      const int32_t* position, void* Xs, int64_t ldxs, void* stream);
 
