@@ -125,8 +125,10 @@ def _load():
 
 
 class _Lazy:
-    def __getattr__(self, name):
-        return getattr(_load(), name)
+    def __getattr__(self, name):  # a name's first use; kept as an attribute
+        f = getattr(_load(), name)
+        setattr(self, name, f)
+        return f
 
 
 _lib = _Lazy()

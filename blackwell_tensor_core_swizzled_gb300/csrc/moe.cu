@@ -41,11 +41,17 @@ __device__ __forceinline__ __nv_bfloat16 from_f32<__nv_bfloat16>(float v) { retu
 // range; exclusive sums over the warps of a CTA, the CTAs of the cluster (read
 // from their shared memory) and the buckets turn it into the rank of the
 // warp's next entry of e.  Within 32 entries the lanes of one bucket find each
-// other with match_any and take consecutive ranks in lane order, so the order
-// never depends on timing.
+// other with a vote for every bit of the bucket's number (match_any walks the
+// distinct values one by one) and take consecutive ranks in lane order, so the
+// order never depends on timing.
+//
+// It is bound by the latency of its rounds, so the entries are spread: 65536
+// of 64 experts take 8.9 us on 16 CTAs, 12.6 on 8 (1 M entries 78 and 150);
+// below SORT_ONE one CTA is quicker (144 entries 3.1 us; 2048 5.6 on 16).
 constexpr int SORT_WARPS = 32;
-constexpr int SORT_CTAS = 8;
+constexpr int SORT_CTAS = 16;  // above 8: opted in to
 constexpr int SORT_ONE = 2048;
+constexpr int SORT_ROUNDS = 8;
 
 __device__ __forceinline__ int bucket_of(int expert, int E) {
   return static_cast<unsigned>(expert) < static_cast<unsigned>(E) ? expert : E;
@@ -55,6 +61,17 @@ __device__ __forceinline__ int ld_cluster_s32(uint32_t addr) {
   int v;
   asm volatile("ld.shared::cluster.s32 %0, [%1];" : "=r"(v) : "r"(addr));
   return v;
+}
+
+// Lanes whose bucket is this lane's; buckets below 2^bits, -1 matches -1.
+__device__ __forceinline__ unsigned same_bucket(int b, int bits) {
+  unsigned same = __ballot_sync(0xffffffffu, b < 0);
+  if (b >= 0) same = ~same;
+  for (int i = 0; i < bits; ++i) {
+    const unsigned ones = __ballot_sync(0xffffffffu, (b >> i) & 1);
+    same &= (b >> i) & 1 ? ones : ~ones;
+  }
+  return same;
 }
 
 // Exclusive sum of one value a thread over the CTA's 32 warps; total to all.
@@ -103,12 +120,25 @@ __global__ void __launch_bounds__(32 * SORT_WARPS) sort_kernel(int n, int E, con
   const int lo = static_cast<int>(min(static_cast<int64_t>(n), from));
   const int hi = static_cast<int>(min(static_cast<int64_t>(n), from + per));
   int* mine = counts + warp * NB;
-  for (int i0 = lo; i0 < hi; i0 += 32) {
-    const int i = i0 + lane;
-    const int b = i < hi ? bucket_of(expert[i], E) : -1;
-    const unsigned same = __match_any_sync(0xffffffffu, b);
-    if (b >= 0 && lane == __ffs(same) - 1) mine[b] += __popc(same);
-    __syncwarp();
+  const int bits = 32 - __clz(E);  // of the largest bucket, E
+  // SORT_ROUNDS rounds of 32 entries are read at once
+  int buckets[SORT_ROUNDS];
+  auto read = [&](int i0) {
+#pragma unroll
+    for (int r = 0; r < SORT_ROUNDS; ++r) {
+      const int i = i0 + 32 * r + lane;
+      buckets[r] = i < hi ? bucket_of(expert[i], E) : -1;
+    }
+  };
+  for (int i0 = lo; i0 < hi; i0 += 32 * SORT_ROUNDS) {
+    read(i0);
+#pragma unroll
+    for (int r = 0; r < SORT_ROUNDS; ++r) {
+      if (i0 + 32 * r >= hi) break;
+      const unsigned same = same_bucket(buckets[r], bits);
+      if (buckets[r] >= 0 && lane == __ffs(same) - 1) mine[buckets[r]] += __popc(same);
+      __syncwarp();
+    }
   }
   __syncthreads();
   // over the warps, for each bucket (a thread each; NB <= 1025: two for the first)
@@ -154,18 +184,22 @@ __global__ void __launch_bounds__(32 * SORT_WARPS) sort_kernel(int n, int E, con
     }
     __syncthreads();
   }
-  for (int i0 = lo; i0 < hi; i0 += 32) {
-    const int i = i0 + lane;
-    const int e = i < hi ? bucket_of(expert[i], E) : -1;
-    const unsigned same = __match_any_sync(0xffffffffu, e);
-    if (e >= 0) {
-      const int p = mine[e] + __popc(same & ((1u << lane) - 1u));
-      position[i] = e < E ? p : -1 - p;
-      source[p] = i;
+  for (int i0 = lo; i0 < hi; i0 += 32 * SORT_ROUNDS) {
+    if (hi - lo > 32 * SORT_ROUNDS) read(i0);
+#pragma unroll
+    for (int r = 0; r < SORT_ROUNDS; ++r) {
+      if (i0 + 32 * r >= hi) break;
+      const int i = i0 + 32 * r + lane, e = buckets[r];
+      const unsigned same = same_bucket(e, bits);
+      if (e >= 0) {
+        const int p = mine[e] + __popc(same & ((1u << lane) - 1u));
+        position[i] = e < E ? p : -1 - p;
+        source[p] = i;
+      }
+      __syncwarp();
+      if (e >= 0 && lane == __ffs(same) - 1) mine[e] += __popc(same);
+      __syncwarp();
     }
-    __syncwarp();
-    if (e >= 0 && lane == __ffs(same) - 1) mine[e] += __popc(same);
-    __syncwarp();
   }
   if constexpr (CTAS > 1) cluster_sync();  // peers have read this CTA's counts
 }
@@ -174,8 +208,10 @@ __global__ void __launch_bounds__(32 * SORT_WARPS) sort_kernel(int n, int E, con
 //
 // All three walk the tokens, so that a token's own row moves once and its
 // topk sorted rows once each; what bounds them is those bytes.  A thread takes
-// PACK elements of a row at a time (16 bytes where bases and rows allow, else
-// one element) and has the loads of up to 8 rows in flight.
+// a pack of a row at a time (16 bytes where bases and rows allow, else one
+// element) and has 8 loads in flight.  16384 tokens of 4096 bf16 and 4 choices:
+// dispatch 100 us (6.7 TB/s, the rate of a plain copy), combine 136 us (4.9
+// TB/s; 8 choices 5.8 TB/s; a row's loads one after the other gave 2.2).
 
 template <class T, bool WIDE>
 struct Pack {
@@ -198,7 +234,10 @@ struct Pack {
 };
 
 constexpr int MOVE_THREADS = 256;
-constexpr int AHEAD = 8;  // rows of a token in flight
+constexpr int COMBINE_THREADS = 128;
+constexpr int GRAD_THREADS = 128;
+constexpr int AHEAD = 8;      // combine: rows of a token in flight
+constexpr int GRAD_ROWS = 2;  // its gradient: choices at a time
 
 // Sorted row of a position, and whether the entry is kept; positions outside
 // the sorted rows (not a result of the sort) are left alone.
@@ -241,8 +280,9 @@ __global__ void __launch_bounds__(MOVE_THREADS) dispatch_kernel(int topk, int64_
   }
 }
 
-template <class T, bool WIDE>
-__global__ void __launch_bounds__(MOVE_THREADS) combine_kernel(int topk, int64_t rows, int64_t H,
+// ROWS choices at a time of PACKS packs: 8 loads in flight a thread.
+template <class T, bool WIDE, int ROWS>
+__global__ void __launch_bounds__(COMBINE_THREADS) combine_kernel(int topk, int64_t rows, int64_t H,
                                                                const T* __restrict__ Ys, int64_t ldys,
                                                                const int32_t* __restrict__ position,
                                                                const float* __restrict__ weight, T* __restrict__ Y,
@@ -253,43 +293,55 @@ __global__ void __launch_bounds__(MOVE_THREADS) combine_kernel(int topk, int64_t
   const int64_t t = blockIdx.x;
   const int32_t* pos = position + t * topk;
   const float* wt = weight ? weight + t * topk : nullptr;
-  const int64_t step = static_cast<int64_t>(gridDim.y) * MOVE_THREADS * P::N;
-  for (int64_t h = (static_cast<int64_t>(blockIdx.y) * MOVE_THREADS + threadIdx.x) * P::N; h < H; h += step) {
-    float acc[P::N] = {};
-    for (int j0 = 0; j0 < topk; j0 += AHEAD) {
-      P y[AHEAD];
-      float w[AHEAD];
-      bool use[AHEAD];
+  constexpr int PACKS = AHEAD / ROWS;
+  constexpr int64_t STRIDE = static_cast<int64_t>(COMBINE_THREADS) * P::N;  // between a thread's packs
+  const int64_t step = static_cast<int64_t>(gridDim.y) * STRIDE * PACKS;
+  for (int64_t h = blockIdx.y * STRIDE * PACKS + static_cast<int64_t>(threadIdx.x) * P::N; h < H; h += step) {
+    float acc[PACKS][P::N] = {};
+    for (int j0 = 0; j0 < topk; j0 += ROWS) {
+      // positions and weights first, so that the rows' loads follow each other
+      int64_t row[ROWS];  // -1: none
+      float w[ROWS];
 #pragma unroll
-      for (int j = 0; j < AHEAD; ++j) {
-        use[j] = false;
-        if (j0 + j < topk) {
-          const Place s = place(pos[j0 + j], rows);
-          use[j] = s.kept && s.valid;
-          if (use[j]) {
-            y[j] = P::load(Ys + s.row * ldys + h);
-            w[j] = wt ? wt[j0 + j] : 1.0f;
-          }
-        }
+      for (int j = 0; j < ROWS; ++j) {
+        row[j] = j0 + j < topk ? pos[j0 + j] : -1;
+        w[j] = j0 + j < topk && wt ? wt[j0 + j] : 1.0f;
+      }
+      P y[ROWS][PACKS];
+#pragma unroll
+      for (int j = 0; j < ROWS; ++j) {
+        if (row[j] >= rows) row[j] = -1;
+#pragma unroll
+        for (int k = 0; k < PACKS; ++k)
+          if (row[j] >= 0 && h + k * STRIDE < H) y[j][k] = P::load(Ys + row[j] * ldys + h + k * STRIDE);
       }
 #pragma unroll
-      for (int j = 0; j < AHEAD; ++j)
-        if (use[j])
+      for (int j = 0; j < ROWS; ++j)
 #pragma unroll
-          for (int i = 0; i < P::N; ++i) acc[i] = fmaf(w[j], to_f32(y[j].v[i]), acc[i]);
+        for (int k = 0; k < PACKS; ++k)
+          if (row[j] >= 0)
+#pragma unroll
+            for (int i = 0; i < P::N; ++i) acc[k][i] = fmaf(w[j], to_f32(y[j][k].v[i]), acc[k][i]);
     }
-    P out;
 #pragma unroll
-    for (int i = 0; i < P::N; ++i) out.v[i] = from_f32<T>(acc[i]);
-    out.store(Y + t * ldy + h);
+    for (int k = 0; k < PACKS; ++k) {
+      if (h + k * STRIDE >= H) break;
+      P out;
+#pragma unroll
+      for (int i = 0; i < P::N; ++i) out.v[i] = from_f32<T>(acc[k][i]);
+      out.store(Y + t * ldy + h + k * STRIDE);
+    }
   }
 }
 
-// One block a token: dYs rows and (dweight) the dots, up to AHEAD choices at a
-// time.  A thread's terms are added in the order of h, then the warp's lanes
+// One block a token: dYs rows and (dweight) the dots, GRAD_ROWS choices at a
+// time, the token's own row coming from the caches again after the first ones.
+// Few choices and small blocks are what keeps the streams of reads and writes
+// of an SM apart: at 8191 x 8 x 4096 bf16 2 choices and 128 threads take 185
+// us, 4 and 256 221, 8 and 256 336, 1 and 128 232.  A thread's terms are added in the order of h, then the warp's lanes
 // and the block's warps in a fixed order.
 template <class T, bool WIDE>
-__global__ void __launch_bounds__(MOVE_THREADS) combine_grad_kernel(int topk, int64_t rows, int64_t H,
+__global__ void __launch_bounds__(GRAD_THREADS) combine_grad_kernel(int topk, int64_t rows, int64_t H,
                                                                     const T* __restrict__ dY, int64_t lddy,
                                                                     const T* __restrict__ Ys, int64_t ldys,
                                                                     const int32_t* __restrict__ position,
@@ -297,18 +349,17 @@ __global__ void __launch_bounds__(MOVE_THREADS) combine_grad_kernel(int topk, in
                                                                     T* __restrict__ dYs, int64_t lddys,
                                                                     float* __restrict__ dweight) {
   using P = Pack<T, WIDE>;
-  constexpr int MINE = AHEAD / 2;  // choices at a time: a row to read and one to write each
-  __shared__ float part[MOVE_THREADS / 32][MINE];
+  __shared__ float part[GRAD_THREADS / 32][GRAD_ROWS];
   griddep_wait();
   griddep_launch_dependents();
   const int64_t t = blockIdx.x;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const T* g = dY + t * lddy;
-  for (int j0 = 0; j0 < topk; j0 += MINE) {
-    Place s[MINE];
-    float w[MINE], dot[MINE] = {};
+  for (int j0 = 0; j0 < topk; j0 += GRAD_ROWS) {
+    Place s[GRAD_ROWS];
+    float w[GRAD_ROWS], dot[GRAD_ROWS] = {};
 #pragma unroll
-    for (int j = 0; j < MINE; ++j) {
+    for (int j = 0; j < GRAD_ROWS; ++j) {
       s[j] = Place{0, false, false};
       w[j] = 0.0f;
       if (j0 + j < topk) {
@@ -316,14 +367,14 @@ __global__ void __launch_bounds__(MOVE_THREADS) combine_grad_kernel(int topk, in
         if (s[j].kept) w[j] = weight ? weight[t * topk + j0 + j] : 1.0f;
       }
     }
-    for (int64_t h = static_cast<int64_t>(threadIdx.x) * P::N; h < H; h += MOVE_THREADS * P::N) {
-      P y[MINE];
+    for (int64_t h = static_cast<int64_t>(threadIdx.x) * P::N; h < H; h += GRAD_THREADS * P::N) {
+      P y[GRAD_ROWS];
 #pragma unroll
-      for (int j = 0; j < MINE; ++j)
+      for (int j = 0; j < GRAD_ROWS; ++j)
         if (dweight && s[j].kept && s[j].valid) y[j] = P::load(Ys + s[j].row * ldys + h);
       const P d = P::load(g + h);
 #pragma unroll
-      for (int j = 0; j < MINE; ++j) {
+      for (int j = 0; j < GRAD_ROWS; ++j) {
         if (!s[j].valid) continue;
         P o;
 #pragma unroll
@@ -337,16 +388,16 @@ __global__ void __launch_bounds__(MOVE_THREADS) combine_grad_kernel(int topk, in
     }
     if (!dweight) continue;
 #pragma unroll
-    for (int j = 0; j < MINE; ++j) {
+    for (int j = 0; j < GRAD_ROWS; ++j) {
 #pragma unroll
       for (int k = 16; k > 0; k >>= 1) dot[j] += __shfl_xor_sync(0xffffffffu, dot[j], k);
       if (lane == 0) part[warp][j] = dot[j];
     }
     __syncthreads();
-    if (threadIdx.x < MINE && j0 + static_cast<int>(threadIdx.x) < topk) {
+    if (threadIdx.x < GRAD_ROWS && j0 + static_cast<int>(threadIdx.x) < topk) {
       float sum = 0.0f;
 #pragma unroll
-      for (int k = 0; k < MOVE_THREADS / 32; ++k) sum += part[k][threadIdx.x];
+      for (int k = 0; k < GRAD_THREADS / 32; ++k) sum += part[k][threadIdx.x];
       dweight[t * topk + j0 + threadIdx.x] = sum;
     }
     __syncthreads();
@@ -415,6 +466,8 @@ cudaError_t sort_setup(int dev) {
     if (d.err == cudaSuccess)
       d.err = cudaFuncSetAttribute(sort_kernel<SORT_CTAS>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                    sort_smem(MAX_EXPERTS));
+    if (d.err == cudaSuccess)
+      d.err = cudaFuncSetAttribute(sort_kernel<SORT_CTAS>, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
   });
   return d.err;
 }
@@ -458,9 +511,9 @@ bool wide_rows(tcg_dtype type, int64_t H, const void* a, int64_t lda, const void
 
 // Blocks a token's row is split into: one, unless there are so few tokens that
 // SMs would idle.
-unsigned row_parts(int64_t T, int64_t H, tcg_dtype type, bool wide, int dev) {
+unsigned row_parts(int64_t T, int64_t H, tcg_dtype type, bool wide, int threads, int dev) {
   const int64_t packs = wide ? H / (type == TCG_F32 ? 4 : 8) : H;
-  const int64_t most = std::max<int64_t>(1, (packs + MOVE_THREADS - 1) / MOVE_THREADS);
+  const int64_t most = std::max<int64_t>(1, (packs + threads - 1) / threads);
   return static_cast<unsigned>(std::min<int64_t>(most, std::max<int64_t>(1, 4 * device_sms(dev) / T)));
 }
 
@@ -475,7 +528,7 @@ int run_dispatch(tcg_dtype type, int64_t T, int topk, int64_t H, const void* X, 
   int dev;
   if (int rc = current_device_checked(&dev)) return rc;
   const bool wide = wide_rows(type, H, X, ldx, Xs, ldxs);
-  const unsigned parts = row_parts(T, H, type, wide, dev);
+  const unsigned parts = row_parts(T, H, type, wide, MOVE_THREADS, dev);
   return for_type(type, wide, [&](auto z, auto w) {
     using E = decltype(z);
     return launch(dispatch_kernel<E, decltype(w)::value>, dim3(static_cast<unsigned>(T), parts), MOVE_THREADS, 0, 1, s,
@@ -495,11 +548,17 @@ int run_combine(tcg_dtype type, int64_t T, int topk, int64_t H, const void* Ys, 
   int dev;
   if (int rc = current_device_checked(&dev)) return rc;
   const bool wide = wide_rows(type, H, Ys, ldys, Y, ldy);
-  const unsigned parts = row_parts(T, H, type, wide, dev);
+  const unsigned parts = row_parts(T, H, type, wide, COMBINE_THREADS, dev);
   return for_type(type, wide, [&](auto z, auto w) {
     using E = decltype(z);
-    return launch(combine_kernel<E, decltype(w)::value>, dim3(static_cast<unsigned>(T), parts), MOVE_THREADS, 0, 1, s,
-                  topk, T * topk, H, static_cast<const E*>(Ys), ldys, position, weight, static_cast<E*>(Y), ldy);
+    constexpr bool W = decltype(w)::value;
+    // choices at a time: as many as there are, up to 8; one pack each where
+    // the row is split over blocks already
+    const auto kernel = topk > 4 || parts > 1 ? combine_kernel<E, W, 8>
+                        : topk > 2            ? combine_kernel<E, W, 4>
+                                              : combine_kernel<E, W, 2>;
+    return launch(kernel, dim3(static_cast<unsigned>(T), parts), COMBINE_THREADS, 0, 1, s, topk, T * topk, H,
+                  static_cast<const E*>(Ys), ldys, position, weight, static_cast<E*>(Y), ldy);
   });
 }
 
@@ -523,7 +582,7 @@ int run_combine_grad(tcg_dtype type, int64_t T, int topk, int64_t H, const void*
   const bool wide = wide_rows(type, H, dY, lddy, dYs, lddys) && (!Ys || wide_rows(type, H, Ys, ldys, Ys, ldys));
   return for_type(type, wide, [&](auto z, auto w) {
     using E = decltype(z);
-    return launch(combine_grad_kernel<E, decltype(w)::value>, dim3(static_cast<unsigned>(T)), MOVE_THREADS, 0, 1, s, topk,
+    return launch(combine_grad_kernel<E, decltype(w)::value>, dim3(static_cast<unsigned>(T)), GRAD_THREADS, 0, 1, s, topk,
                   T * topk, H, static_cast<const E*>(dY), lddy, static_cast<const E*>(Ys), ldys, position, weight,
                   static_cast<E*>(dYs), lddys, dweight);
   });
