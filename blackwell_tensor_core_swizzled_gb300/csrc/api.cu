@@ -868,7 +868,7 @@ int max_resident_clusters(int dev, const KernelInfo& ki, int* out) {
 
 namespace {
 
-// Swizzled tiled map (span: 128, 64 or 32 bytes), encoded on every call
+// Tiled map swizzled over `span` bytes (128, 64 or 32), encoded on every call
 int encode_tiled(CUtensorMap* map, CUtensorMapDataType dt, int rank, const void* base, const cuuint64_t* dims,
                  const cuuint64_t* strides, const cuuint32_t* box, uint32_t span = 128) {
   if (encode_ready() != TCG_OK) {
@@ -905,6 +905,14 @@ int make_byte_map(CUtensorMap* map, const void* base, uint64_t inner, uint64_t m
   const cuuint64_t dims[3] = {inner, mid, outer}, strides[2] = {stride_mid, stride_outer};
   const cuuint32_t box[3] = {box_inner, box_mid, 1};
   return encode_tiled(map, CU_TENSOR_MAP_DATA_TYPE_UINT8, 3, base, dims, strides, box, box_inner);
+}
+
+int make_store_map(CUtensorMap* map, const void* base, bool bf16, uint64_t inner, uint64_t mid, uint64_t outer,
+                   uint64_t stride_mid, uint64_t stride_outer) {
+  const cuuint64_t dims[3] = {inner, mid, outer}, strides[2] = {2 * stride_mid, 2 * stride_outer};
+  const cuuint32_t box[3] = {32, 32, 1};
+  return encode_tiled(map, bf16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16, 3, base, dims,
+                      strides, box, 64);
 }
 
 int make_slab_map(CUtensorMap* map, const void* base, uint64_t inner, uint64_t mid, uint64_t slabs, uint64_t outer,

@@ -13,10 +13,15 @@
 //
 // The ragged extent of a product, the group's rows, is thus on the MMA's N
 // side, which any multiple of 16 (32 for a CTA pair) up to 256 may have: a
-// tile with few rows costs few columns, nothing is padded in memory, and no
-// tile store needs clipping at a group's end, because a warp stores one
-// output row segment (32 lanes, consecutive m) at a time.  A group's rows are
-// split evenly into as few tiles of at most BN as they need.
+// tile with few rows costs few columns and nothing is padded in memory.  A
+// group's rows are split evenly into as few tiles of at most BN as they need.
+//
+// 16-bit outputs leave in blocks of 32 m by 32 columns through a shared
+// staging tile and a TMA store, rows of the tile being output rows; a block
+// that a group's end cuts, outputs that are not 16-byte aligned, and fp32 ones
+// are stored by the lanes, an output row an instruction.  Matrices' gradient,
+// 16384 rows, 32 groups of 2048 x 4096: bf16 256 us by the lanes (64 bytes an
+// instruction), 220 by TMA; fp32 278 and 295.
 //
 // In the weight product the contraction is ragged: the last 64-row block of a
 // group also loads rows of the next group.  The MMAs of 16 rows beyond the
@@ -50,6 +55,7 @@ namespace {
 constexpr int MAX_GROUPS = 1024;
 constexpr int64_t MAX_EXTENT = int64_t{1} << 30;
 constexpr int EPI_WARPS = 8;
+constexpr int STAGING_BYTES = 2048;
 constexpr int GROUPED_THREADS = 32 * (4 + EPI_WARPS);
 constexpr int BAND = 8;  // column tiles of a group that sweep its row tiles together
 
@@ -57,6 +63,8 @@ struct GroupedParams {
   CUtensorMap tmap_p;    // [G or 1][rows][64-element boxes]
   CUtensorMap tmap_q;    // Q in boxes of a full tile's rows (MN-major: 64)
   CUtensorMap tmap_q16;  // K-major Q in boxes of 16 rows, for partial tiles
+  CUtensorMap tmap_d;    // 16-bit output [G or 1][c][m] in boxes of 32 m and 32 rows
+  int d_tma;
   const int32_t* offsets;
   int G, R;
   int weight;    // the contraction runs over the group's rows
@@ -70,22 +78,25 @@ struct GroupedParams {
   uint32_t idesc;             // without N
   void* D;
   int64_t ldd, stride_d;
-  int d_type;
+  int d_type, d_size;
+  int pairs;  // 16-bit outputs: two m at a time are 4-byte aligned, and M is even
   unsigned long long* err;
   uint64_t timeout_ns;
 };
 
-template <int CG, int BN, int STAGES>
+template <int CG, int BN, int STAGES, int GROUPS>
 struct GroupedCfg {
   static constexpr int P_BYTES = 128 * 128;
   static constexpr int Q_ROWS = BN / CG;
   static constexpr int Q_BYTES = Q_ROWS * 128;
   static constexpr int STAGE_BYTES = P_BYTES + Q_BYTES;
-  static constexpr int BAR_OFF = STAGES * STAGE_BYTES;
+  // two staging tiles for each epilogue warp
+  static constexpr int EPI_OFF = STAGES * STAGE_BYTES;
+  static constexpr int BAR_OFF = EPI_OFF + EPI_WARPS * 2 * STAGING_BYTES;
   // full[S], empty[S], rag[S], peer[S], acc_full[2], acc_empty[2], drain
   static constexpr int NUM_BARS = 4 * STAGES + 5;
   static constexpr int SEG_OFF = BAR_OFF + NUM_BARS * 8 + 8;  // then tmem slot + abort flag before it
-  static constexpr int SMEM_BYTES = 1024 + SEG_OFF + 2 * (MAX_GROUPS + 1) * 4;
+  static constexpr int SMEM_BYTES = 1024 + SEG_OFF + 2 * (GROUPS + 1) * 4;
   static_assert(Q_BYTES % 1024 == 0, "swizzle period");
   static_assert(SMEM_BYTES <= 232448, "dynamic shared memory");
   static_assert(2 * BN <= 512, "two accumulators");
@@ -151,29 +162,55 @@ __device__ __forceinline__ GTile decode_unit(const GroupedParams& p, const int* 
   return t;
 }
 
-// Store 32 accumulator columns of one warp: lane = m, register i = column i.
-__device__ __forceinline__ void store_columns(const GroupedParams& p, int64_t base, int ncols, bool m_ok,
-                                              const uint32_t (&r)[32]) {
-  if (p.d_type == OUT_F32) {
-    uint32_t* dst = static_cast<uint32_t*>(p.D) + base;
+// Store up to 32 accumulator columns of one warp: lane = m, register i =
+// column i, whose row of the output starts i * pitch bytes after `dst` (this
+// lane's element of the first).  Addresses advance by additions alone: as a
+// multiplication for each column they took more of the epilogue than the
+// stores.  16-bit outputs in pairs: neighbouring lanes exchange halves, so that
+// an even lane stores two m of column i and an odd one two m of column i + 1.
+__device__ __forceinline__ void store_columns(uint8_t* dst, int64_t pitch, int ncols, bool m_ok, int type, bool pairs,
+                                              int lane, const uint32_t (&r)[32]) {
+  if (type == OUT_F32) {
+    if (ncols >= 32) {
+      if (m_ok) {
 #pragma unroll
-    for (int i = 0; i < 32; ++i)
-      if (i < ncols && m_ok) dst[i * p.ldd] = r[i];
-  } else {
-    uint16_t* dst = static_cast<uint16_t*>(p.D) + base;
-    const bool bf = p.d_type == OUT_BF16;
+        for (int i = 0; i < 32; ++i, dst += pitch) __stcs(reinterpret_cast<uint32_t*>(dst), r[i]);
+      }
+    } else {
 #pragma unroll
-    for (int i = 0; i < 32; i += 2) {
+      for (int i = 0; i < 32; ++i, dst += pitch) {
+        if (i >= ncols) break;
+        if (m_ok) __stcs(reinterpret_cast<uint32_t*>(dst), r[i]);
+      }
+    }
+    return;
+  }
+  const bool bf = type == OUT_BF16;
+  if (pairs) {
+    const uint32_t pick = (lane & 1) ? 0x3276u : 0x5410u;
+    dst += (lane & 1) ? pitch - 2 : 0;
+    pitch *= 2;
+#pragma unroll
+    for (int i = 0; i < 32; i += 2, dst += pitch) {
+      if (i >= ncols) break;
       const uint32_t h = bf ? pack_bf16(r[i], r[i + 1]) : pack_f16(r[i], r[i + 1]);
-      if (i < ncols && m_ok) dst[i * p.ldd] = static_cast<uint16_t>(h);
-      if (i + 1 < ncols && m_ok) dst[(i + 1) * p.ldd] = static_cast<uint16_t>(h >> 16);
+      const uint32_t o = __shfl_xor_sync(0xffffffffu, h, 1);
+      if (m_ok && ((lane & 1) == 0 || i + 1 < ncols)) *reinterpret_cast<uint32_t*>(dst) = __byte_perm(h, o, pick);
+    }
+  } else {
+#pragma unroll
+    for (int i = 0; i < 32; i += 2, dst += 2 * pitch) {
+      if (i >= ncols) break;
+      const uint32_t h = bf ? pack_bf16(r[i], r[i + 1]) : pack_f16(r[i], r[i + 1]);
+      if (m_ok) *reinterpret_cast<uint16_t*>(dst) = static_cast<uint16_t>(h);
+      if (m_ok && i + 1 < ncols) *reinterpret_cast<uint16_t*>(dst + pitch) = static_cast<uint16_t>(h >> 16);
     }
   }
 }
 
-template <int CG, int BN, int STAGES>
+template <int CG, int BN, int STAGES, int GROUPS>
 __global__ void __launch_bounds__(GROUPED_THREADS, 1) grouped_kernel(const __grid_constant__ GroupedParams p) {
-  using C = GroupedCfg<CG, BN, STAGES>;
+  using C = GroupedCfg<CG, BN, STAGES, GROUPS>;
   extern __shared__ uint8_t smem_raw[];
   const uint32_t raw = smem_u32(smem_raw);
   const uint32_t sbase = (raw + 1023u) & ~1023u;
@@ -444,14 +481,40 @@ __global__ void __launch_bounds__(GROUPED_THREADS, 1) grouped_kernel(const __gri
     const int q = warp & 3;            // TMEM lane quadrant
     const int part = (warp - 4) >> 2;  // 32-column chunks part, part + 2, ...
     uint32_t tcount = 0;
+    const uint32_t buf0 = sbase + C::EPI_OFF + static_cast<uint32_t>((warp - 4) * 2 * STAGING_BYTES);
+    uint32_t stores = 0;
+    // the staging tile to fill next: its store before the last has read it
+    auto staging = [&] {
+      if (stores >= 2) {
+        if (lane == 0) bulk_wait_group_read<1>();
+        __syncwarp();
+      }
+      return buf0 + (stores & 1u) * STAGING_BYTES;
+    };
+    auto send = [&](uint32_t buf, int m0, int c, int g) {
+      fence_proxy_async_shared();
+      __syncwarp();
+      if (lane == 0) {
+        tma_store_3d(&p.tmap_d, buf, m0, c, g);
+        bulk_commit_group();
+      }
+      ++stores;
+    };
     for (int u = cluster_id; u < total_units; u += num_clusters) {
       const GTile t = decode_unit<CG, BN>(p, seg, pre, u);
+      const int m_warp = t.m0 + static_cast<int>(rank) * 128 + 32 * q;
+      // output rows of the map: all c of a matrix clip at its end, rows of a
+      // group do not
+      const int row0 = p.weight ? t.c0 : t.lo + t.c0, outer = p.weight ? t.g : 0;
       const int m = t.m0 + static_cast<int>(rank) * 128 + 32 * q + lane;
       const bool m_ok = m < p.M;
-      const int64_t base = (p.weight ? t.g * p.stride_d + t.c0 * p.ldd : (t.lo + t.c0) * p.ldd) + m;
+      const int64_t pitch = p.ldd * p.d_size;
+      uint8_t* dst = static_cast<uint8_t*>(p.D) + (p.weight ? t.g * p.stride_d * p.d_size + t.c0 * pitch : (t.lo + t.c0) * pitch) +
+                     static_cast<int64_t>(m) * p.d_size;
       if (t.nkb == 0) {
         const uint32_t zero[32] = {};
-        for (int c = 32 * part; c < t.ncols; c += 64) store_columns(p, base + c * p.ldd, t.ncols - c, m_ok, zero);
+        for (int c = 32 * part; c < t.ncols; c += 64)
+          store_columns(dst + c * pitch, pitch, t.ncols - c, m_ok, p.d_type, p.pairs, lane, zero);
         continue;
       }
       const uint32_t b = tcount & 1u;
@@ -461,10 +524,32 @@ __global__ void __launch_bounds__(GROUPED_THREADS, 1) grouped_kernel(const __gri
       const uint32_t tb = tmem_base + (static_cast<uint32_t>(32 * q) << 16) + b * BN;
 #pragma unroll 1
       for (int c = 32 * part; c < t.ncols; c += 64) {
+        if (p.d_tma && (p.weight || c + 32 <= t.ncols)) {
+          if (m_warp >= p.M) break;
+          // fragments of 16 m each; stmatrix turns 8 m of 8 columns into 8
+          // rows of 16 bytes: lane 8k + i addresses row 8j + i, m 8k..8k+7
+          uint32_t lo[16], hi[16];
+          tmem_ld_16x256b_x4(tb + c, lo);
+          tmem_ld_16x256b_x4(tb + c + (16u << 16), hi);
+          tc_wait_ld();
+          const uint32_t buf = staging();
+          const bool bf = p.d_type == OUT_BF16;
+          const uint32_t k = static_cast<uint32_t>(lane) >> 3, i = static_cast<uint32_t>(lane) & 7u;
+#pragma unroll
+          for (uint32_t j = 0; j < 4; ++j) {
+            const uint32_t row = 8u * j + i;
+            auto pk = [&](uint32_t a, uint32_t b) { return bf ? pack_bf16(a, b) : pack_f16(a, b); };
+            stmatrix_x4_trans(buf + 64u * row + 16u * (k ^ ((row >> 1) & 3u)), pk(lo[4 * j], lo[4 * j + 1]),
+                              pk(lo[4 * j + 2], lo[4 * j + 3]), pk(hi[4 * j], hi[4 * j + 1]),
+                              pk(hi[4 * j + 2], hi[4 * j + 3]));
+          }
+          send(buf, m_warp, row0 + c, outer);
+          continue;
+        }
         uint32_t r[32];
         tmem_ld_32x32b_x32(tb + c, r);
         tc_wait_ld();
-        store_columns(p, base + c * p.ldd, t.ncols - c, m_ok, r);
+        store_columns(dst + c * pitch, pitch, t.ncols - c, m_ok, p.d_type, p.pairs, lane, r);
       }
       tc_fence_before();
       __syncwarp();
@@ -475,6 +560,8 @@ __global__ void __launch_bounds__(GROUPED_THREADS, 1) grouped_kernel(const __gri
           mbar_arrive(acce_bar(b));
       }
     }
+    if (lane == 0) bulk_wait_group_all();
+    __syncwarp();
     if (!p.weight) {
       // rows of no group (and all rows when K is 0): zero
       const int t = threadIdx.x - 128;
@@ -511,13 +598,16 @@ struct Variant {
   int bn;
 };
 
-template <int CG, int BN, int STAGES>
+template <int CG, int BN, int STAGES, int GROUPS>
 Variant variant() {
-  using C = GroupedCfg<CG, BN, STAGES>;
-  return {KernelInfo{reinterpret_cast<const void*>(&grouped_kernel<CG, BN, STAGES>), C::SMEM_BYTES, CG, BN, KIND_F16,
-                     GROUPED_THREADS},
+  using C = GroupedCfg<CG, BN, STAGES, GROUPS>;
+  return {KernelInfo{reinterpret_cast<const void*>(&grouped_kernel<CG, BN, STAGES, GROUPS>), C::SMEM_BYTES, CG, BN,
+                     KIND_F16, GROUPED_THREADS},
           BN};
 }
+
+// CTA pairs; more than 224 groups' tile counts take a ring stage's memory.
+Variant pair_variant(int G) { return G <= 224 ? variant<2, 256, 6, 224>() : variant<2, 256, 5, MAX_GROUPS>(); }
 
 int check_problem(tcg_input in_type, int64_t R, int64_t N, int64_t K, int G, tcg_dtype d_type) {
   if (in_type != TCG_IN_F16 && in_type != TCG_IN_BF16) return TCG_ERR_INVALID;
@@ -552,6 +642,19 @@ int launch_grouped(const Variant& v, GroupedParams& p, int dev, int64_t units, c
   int clusters = 0;
   if (int rc = max_resident_clusters(dev, v.ki, &clusters)) return rc;
   const int cg = v.ki.cta_group;
+  p.d_size = p.d_type == TCG_F32 ? 4 : 2;
+  p.pairs = reinterpret_cast<uintptr_t>(p.D) % 4 == 0 && p.ldd % 2 == 0 && p.stride_d % 2 == 0 && p.M % 2 == 0;
+  // TMA stores where the output's rows and matrices are 16-byte aligned and
+  // end on such a boundary (a store is cut at 16-byte steps: rows of 513 bf16
+  // were written up to their 516th element)
+  const int64_t low = reinterpret_cast<int64_t>(p.D) | p.ldd * p.d_size | p.stride_d * p.d_size |
+                      static_cast<int64_t>(p.M) * p.d_size;
+  p.d_tma = p.d_type != TCG_F32 && low % 16 == 0;
+  if (p.d_tma) {
+    const uint64_t rows = static_cast<uint64_t>(p.weight ? p.C : p.R), outer = p.weight ? p.G : 1;
+    if (int rc = make_store_map(&p.tmap_d, p.D, p.d_type == TCG_BF16, p.M, rows, outer, p.ldd, p.weight ? p.stride_d : p.R * p.ldd))
+      return rc;
+  }
   p.err = device_error_word(dev);
   p.timeout_ns = wait_timeout_ns();
   cudaLaunchConfig_t cfg = {};
@@ -595,7 +698,7 @@ int run_grouped(tcg_input in_type, int64_t R, int64_t N, int64_t K, int G, const
   if (int rc = current_device_checked(&dev)) return rc;
   const bool bf16 = in_type == TCG_IN_BF16;
   const bool wide = R > 64 * static_cast<int64_t>(G);
-  const Variant v = wide ? variant<2, 256, 6>() : variant<1, 64, 8>();
+  const Variant v = wide ? pair_variant(G) : variant<1, 64, 7, MAX_GROUPS>();
   const int cg = v.ki.cta_group;
   GroupedParams p;
   std::memset(&p, 0, sizeof p);
@@ -644,7 +747,7 @@ int run_wgrad(tcg_input in_type, int64_t R, int64_t N, int64_t K, int G, const v
   int dev;
   if (int rc = current_device_checked(&dev)) return rc;
   const bool bf16 = in_type == TCG_IN_BF16;
-  const Variant v = variant<2, 256, 6>();
+  const Variant v = pair_variant(G);
   const int cg = v.ki.cta_group;
   GroupedParams p;
   std::memset(&p, 0, sizeof p);

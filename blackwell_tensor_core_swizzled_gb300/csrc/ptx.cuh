@@ -463,6 +463,14 @@ __device__ __forceinline__ void stmatrix_x4(uint32_t addr, uint32_t a, uint32_t 
                : "memory");
 }
 
+// The same with .trans: register m of lane 4i+w holds row i, columns 2w and
+// 2w+1 of matrix m, and row j of the stored matrix is its column j.
+__device__ __forceinline__ void stmatrix_x4_trans(uint32_t addr, uint32_t a, uint32_t b, uint32_t c, uint32_t d) {
+  asm volatile("stmatrix.sync.aligned.m8n8.x4.trans.shared.b16 [%0], {%1, %2, %3, %4};" ::"r"(addr), "r"(a), "r"(b),
+               "r"(c), "r"(d)
+               : "memory");
+}
+
 // tcgen05.ld .32x32b.x16.pack::16b: 16 registers covering 32 columns; each
 // register holds the low 16 bits of columns 2c and 2c+1 ("tcgen05.ld /
 // tcgen05.st" page, "Pack/unpack is a different TMEM image").
