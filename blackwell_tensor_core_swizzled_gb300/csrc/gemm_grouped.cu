@@ -29,6 +29,13 @@
 // zeros in shared memory (both operands: the neighbour's rows may hold
 // infinities) before the MMA reads them.
 //
+// fp32 outputs keep the accuracy of fp32 sums: the tensor core cuts a running
+// sum's last bits at every step, which over a contraction of 4096 grew to 14
+// times the error of rounded fp32 sums.  So every CHAIN blocks the MMAs change
+// to the other accumulator, and the epilogue adds the finished one to sums in
+// its registers (rounded), while the next is computed.  16-bit outputs round
+// far more than that and take the whole contraction in one accumulator.
+//
 // The structure is the dense kernel's: a persistent CTA (or pair) per SM, a
 // TMA producer warp, an MMA warp, two accumulators in TMEM, epilogue warps.
 // The tile list depends on offsets, which only the device knows, so each CTA
@@ -47,6 +54,7 @@
 #include "desc.cuh"
 #include "gemm_kernel.cuh"
 #include "ptx.cuh"
+#include "tmem_ldst.cuh"
 
 namespace tcg {
 
@@ -57,6 +65,7 @@ constexpr int64_t MAX_EXTENT = int64_t{1} << 30;
 constexpr int EPI_WARPS = 8;
 constexpr int STAGING_BYTES = 2048;
 constexpr int GROUPED_THREADS = 32 * (4 + EPI_WARPS);
+constexpr int CHAIN = 8;  // fp32 outputs: blocks of the contraction summed by the tensor core
 constexpr int BAND = 8;  // column tiles of a group that sweep its row tiles together
 
 struct GroupedParams {
@@ -112,6 +121,7 @@ struct GTile {
   int mma_n;  // columns the MMA computes
   int nkb;    // 64-deep blocks of the contraction (0: the tile is zero)
   int last;   // depth of the last block
+  int chain;  // blocks one accumulator takes
 };
 
 // A group's columns n: tiles of `per` columns each, the last one shorter.
@@ -159,6 +169,7 @@ __device__ __forceinline__ GTile decode_unit(const GroupedParams& p, const int* 
   t.mma_n = (t.ncols + 16 * CG - 1) / (16 * CG) * (16 * CG);
   t.nkb = (depth + 63) >> 6;
   t.last = depth - 64 * (t.nkb - 1);
+  t.chain = p.d_type == OUT_F32 ? CHAIN : max(1, t.nkb);
   return t;
 }
 
@@ -399,20 +410,22 @@ __global__ void __launch_bounds__(GROUPED_THREADS, 1) grouped_kernel(const __gri
       const GTile t = decode_unit<CG, BN>(p, seg, pre, u);
       if (t.nkb == 0) continue;
       const bool issue = CG == 1 || rank == 0;
-      const uint32_t b = tcount & 1u;
-      if (issue) {
-        if (!wait_uniform(acce_bar(b), ((tcount >> 1) & 1u) ^ 1u, wctx, SITE_MMA_ACC_EMPTY)) {
-          ok = false;
-          break;
-        }
-        tc_fence_after();
-      }
-      ++tcount;
       const uint32_t idesc = p.idesc | (static_cast<uint32_t>(t.mma_n >> 3) << 17);
-      const uint32_t d_tmem = tmem_base + b * BN;
+      uint32_t b = 0, d_tmem = 0;
+      int link = 0;  // blocks in the accumulator
       for (int kb = 0; kb < t.nkb; ++kb) {
         const bool last = kb == t.nkb - 1;
         const bool ragged = p.weight && last && (t.last & 15);
+        if (issue && link == 0) {
+          b = tcount & 1u;
+          if (!wait_uniform(acce_bar(b), ((tcount >> 1) & 1u) ^ 1u, wctx, SITE_MMA_ACC_EMPTY)) {
+            ok = false;
+            break;
+          }
+          tc_fence_after();
+          ++tcount;
+          d_tmem = tmem_base + b * BN;
+        }
         if (issue && !wait_uniform(full_bar(s), ph, wctx, SITE_MMA_FULL)) {
           ok = false;
           break;
@@ -455,19 +468,18 @@ __global__ void __launch_bounds__(GROUPED_THREADS, 1) grouped_kernel(const __gri
             for (int j = 0; j < 4; ++j)
               if (j < steps)
                 mma_f16<CG>(d_tmem, p_desc0 + st + j * p.p_kstep, q_desc0 + st + j * p.q_kstep, idesc,
-                            (kb | j) ? 1u : 0u);
+                            (link | j) ? 1u : 0u);
             tc_commit<CG>(empty_bar(s));
+            if (last || link == t.chain - 1) tc_commit<CG>(accf_bar(b));
           }
           __syncwarp();
         }
+        if (++link == t.chain) link = 0;
         if (++s == STAGES) {
           s = 0;
           ph ^= 1u;
         }
       }
-      if (!ok) break;
-      if (issue && elect_one()) tc_commit<CG>(accf_bar(b));
-      __syncwarp();
     }
     if (!ok && (CG == 1 || rank == 0) && elect_one()) {
       tc_commit<CG>(drain_bar);
@@ -517,11 +529,61 @@ __global__ void __launch_bounds__(GROUPED_THREADS, 1) grouped_kernel(const __gri
           store_columns(dst + c * pitch, pitch, t.ncols - c, m_ok, p.d_type, p.pairs, lane, zero);
         continue;
       }
+      const uint32_t lanes = tmem_base + (static_cast<uint32_t>(32 * q) << 16);
+      auto release = [&](uint32_t b) {
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) {
+          if constexpr (CG == 2)
+            mbar_arrive_cluster(mapa_shared(acce_bar(b), 0));
+          else
+            mbar_arrive(acce_bar(b));
+        }
+      };
+      if (p.d_type == OUT_F32) {
+        constexpr int MINE = (BN + 63) / 64;  // blocks of 32 columns of this warp
+        uint32_t sum[MINE][32];
+        bool done = true;
+        for (int kb = 0; kb < t.nkb; kb += t.chain, ++tcount) {
+          const uint32_t b = tcount & 1u;
+          done = warp_wait(accf_bar(b), (tcount >> 1) & 1u, wctx, SITE_EPI_ACC_FULL);
+          if (!done) break;
+          tc_fence_after();
+#pragma unroll
+          for (int i = 0; i < MINE; ++i) {
+            const int c = 32 * part + 64 * i;
+            if (c >= t.ncols) break;
+            if (kb == 0) {
+              tmem_ld_32x32b_x32(lanes + b * BN + c, sum[i]);
+              tc_wait_ld();
+            } else {
+#pragma unroll
+              for (int h = 0; h < 32; h += 16) {  // 16 at a time: registers
+                uint32_t r[16];
+                ldx_32x32b_x16(lanes + b * BN + c + h, r);
+                tc_wait_ld();
+#pragma unroll
+                for (int k = 0; k < 16; ++k)
+                  sum[i][h + k] = __float_as_uint(__uint_as_float(sum[i][h + k]) + __uint_as_float(r[k]));
+              }
+            }
+          }
+          release(b);
+        }
+        if (!done) break;
+#pragma unroll
+        for (int i = 0; i < MINE; ++i) {
+          const int c = 32 * part + 64 * i;
+          if (c >= t.ncols) break;
+          store_columns(dst + c * pitch, pitch, t.ncols - c, m_ok, p.d_type, false, lane, sum[i]);
+        }
+        continue;
+      }
       const uint32_t b = tcount & 1u;
       if (!warp_wait(accf_bar(b), (tcount >> 1) & 1u, wctx, SITE_EPI_ACC_FULL)) break;
       ++tcount;
       tc_fence_after();
-      const uint32_t tb = tmem_base + (static_cast<uint32_t>(32 * q) << 16) + b * BN;
+      const uint32_t tb = lanes + b * BN;
 #pragma unroll 1
       for (int c = 32 * part; c < t.ncols; c += 64) {
         if (p.d_tma && (p.weight || c + 32 <= t.ncols)) {
@@ -551,14 +613,7 @@ __global__ void __launch_bounds__(GROUPED_THREADS, 1) grouped_kernel(const __gri
         tc_wait_ld();
         store_columns(dst + c * pitch, pitch, t.ncols - c, m_ok, p.d_type, p.pairs, lane, r);
       }
-      tc_fence_before();
-      __syncwarp();
-      if (lane == 0) {
-        if constexpr (CG == 2)
-          mbar_arrive_cluster(mapa_shared(acce_bar(b), 0));
-        else
-          mbar_arrive(acce_bar(b));
-      }
+      release(b);
     }
     if (lane == 0) bulk_wait_group_all();
     __syncwarp();
