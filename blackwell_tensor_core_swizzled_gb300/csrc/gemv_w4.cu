@@ -17,12 +17,13 @@
 // issue at half rate, so the 16 decoding warps do little else, and what feeds
 // and empties them has warps of its own:
 //   warps 0..15   a slab of 256 of K each, whose activations stay in
-//                 registers, walking down the matrix in tiles of 16 rows;
-//   warp 16       brings a tile into a ring of stages: codes, scales and zero
+//                 registers, walking down the matrix in tiles of 32 rows (16
+//                 with 16 activation rows);
+//   warp 16       brings 16 rows to a stage of a ring: codes, scales and zero
 //                 points by a TMA copy each, for all slabs at once (a copy
 //                 takes its issuing thread 150 cycles, one for every warp or
 //                 row would take longer than the decoding);
-//   the others    (three; with 16 activation rows, whose fragments want the
+//   the others    (two; with 16 activation rows, whose fragments want the
 //                 registers, one) add the warps' parts of a tile in a fixed
 //                 order and store it while the next tiles are decoded.
 // A team of warps covers K (the 16, or fewer when K is short: then a CTA has
@@ -56,9 +57,8 @@ namespace {
 constexpr int MAX_GROUPS = 1024;
 constexpr int64_t MAX_EXTENT = int64_t{1} << 30;
 
-constexpr int WARPS = 16;          // decoding warps
 constexpr int SLAB = 256;          // K per warp: 128 bytes of codes
-constexpr int TILE_N = 16;         // matrix rows per tile: one mma's
+constexpr int STAGE_N = 16;        // matrix rows per stage: one mma's
 // bytes of a matrix row's scales, zero points in a stage when they are copied
 // word by word: up to 16, 8 a warp, and 4 a team for rows that start off a
 // 4-byte boundary; rows on different banks
@@ -116,23 +116,25 @@ template <int TOK>
 struct Shape {
   static constexpr int NT = TOK == 16 ? 2 : 1;        // mma column blocks
   static constexpr int STEP = TOK == 4 ? 2 : 1;       // accumulator columns between rows
+  static constexpr int WARPS = TOK == 16 ? 8 : 16;    // decoding warps
+  static constexpr int TILE_N = 32;                   // matrix rows per tile
   static constexpr int OUT = TOK * TILE_N;            // sums of a tile
-  static constexpr int CAP = (TOK == 16 ? 4096 : TOK == 8 ? 2048 : 1024) / OUT;  // tiles of a chunk that is passed over more than once
-  static constexpr int STAGES = TOK == 16 ? 3 : 4;    // ring stages
+  static constexpr int CAP = (TOK == 16 ? 4096 : 1024) / OUT;  // tiles of a chunk that is passed over more than once
+  static constexpr int STAGES = TOK == 16 ? 6 : 4;    // ring stages
   // buffers of parts: tile i of a chunk uses number i % PARTS, which one
   // adding warp empties, so that in every pass the same warp has the tile
-  static constexpr int PARTS = TOK == 16 ? 2 : 3;
-  static constexpr int ADD_WARPS = TOK == 16 ? 1 : 3;
+  static constexpr int PARTS = 2;
+  static constexpr int ADD_WARPS = 2;
   static constexpr int THREADS = 32 * (WARPS + 1 + ADD_WARPS);
-  static constexpr int PART_PITCH = TOK == 4 ? 24 : 20;  // floats between a part's activation rows
+  static constexpr int PART_PITCH = TILE_N + (TOK == 4 ? 8 : 4);  // floats between a part's activation rows
   static constexpr int TILE_PART = TOK * PART_PITCH;  // floats of a warp's part
   // a stage: codes [warp][16 rows][128 bytes]; scales, then zero points [16 rows][pitch]
-  static constexpr int CODE_BYTES = WARPS * TILE_N * SLAB / 2;
+  static constexpr int CODE_BYTES = WARPS * STAGE_N * SLAB / 2;
   static constexpr int SCALES = STAGES * CODE_BYTES;
   // (boxes: up to 16 x 16 bytes a warp, teams on 1 KiB boundaries)
   static constexpr int ZERO_OFF = 6 * 1024;
   static constexpr int SCALE_STAGE = 10 * 1024;
-  static_assert(TILE_N * SCALE_PITCH <= ZERO_OFF && TILE_N * ZERO_PITCH <= SCALE_STAGE - ZERO_OFF, "");
+  static_assert(STAGE_N * SCALE_PITCH <= ZERO_OFF && STAGE_N * ZERO_PITCH <= SCALE_STAGE - ZERO_OFF, "");
   static constexpr int PART = SCALES + STAGES * SCALE_STAGE;
   // an activation row on its way to each warp's registers
   static constexpr int ACT = PART + PARTS * WARPS * TILE_PART * 4;
@@ -554,7 +556,7 @@ __device__ __forceinline__ void rows16(const uint8_t* codes, const uint8_t* s0, 
 
 // A team's tiles in order: chunks of tiles, for each its passes over K, for
 // each the tiles.  Without a second pass all tiles are one chunk.
-template <int CAP>
+template <int CAP, int TILE_N>
 struct Cursor {
   int chunk, pos, end;   // grains, counted over the row blocks
   int i, pass;           // tile within the chunk, pass
@@ -593,7 +595,7 @@ struct Cursor {
 template <int KIND, bool BF16, int TOK>
 __global__ void __launch_bounds__(Shape<TOK>::THREADS, 1) gemv_kernel(const __grid_constant__ GemvParams p) {
   using S = Shape<TOK>;
-  constexpr int NT = S::NT, STAGES = S::STAGES, PARTS = S::PARTS, THREADS = S::THREADS, ADD_WARPS = S::ADD_WARPS;
+  constexpr int WARPS = S::WARPS, NT = S::NT, STAGES = S::STAGES, PARTS = S::PARTS, THREADS = S::THREADS, TILE_N = S::TILE_N, ADD_WARPS = S::ADD_WARPS;
   extern __shared__ uint8_t smem_raw[];
   const uint32_t raw = smem_u32(smem_raw);
   uint8_t* smem = smem_raw + (((raw + 1023u) & ~1023u) - raw);
@@ -683,7 +685,7 @@ __global__ void __launch_bounds__(Shape<TOK>::THREADS, 1) gemv_kernel(const __gr
   const int total = blocks * p.grains, num_teams = static_cast<int>(gridDim.x) * p.teams;
   const int share = total / num_teams, more = total - share * num_teams;
   const int passes = (p.slabs + p.team_warps - 1) / p.team_warps;
-  using Cur = Cursor<S::CAP>;
+  using Cur = Cursor<S::CAP, S::TILE_N>;
   auto start = [&](int team) {
     // neighbouring teams sit in different CTAs, so that few rows spread over all
     const int id = team * static_cast<int>(gridDim.x) + static_cast<int>(blockIdx.x);
@@ -700,8 +702,8 @@ __global__ void __launch_bounds__(Shape<TOK>::THREADS, 1) gemv_kernel(const __gr
   constexpr int ES = is_int4(KIND) ? 2 : 1;
   // where a team's scales, zero points start after those of the team before:
   // whole boxes of 16 rows, or so far along each row
-  const int team_sb = p.bulk ? TILE_N * ((p.team_warps * SB + p.box_s - 1) / p.box_s * p.box_s) : p.team_warps * SB + 4;
-  const int team_zb = p.bulk ? TILE_N * p.box_z : (p.team_warps * ZB + 3) / 4 * 4 + 4;
+  const int team_sb = p.bulk ? STAGE_N * ((p.team_warps * SB + p.box_s - 1) / p.box_s * p.box_s) : p.team_warps * SB + 4;
+  const int team_zb = p.bulk ? STAGE_N * p.box_z : (p.team_warps * ZB + 3) / 4 * 4 + 4;
 
   if (warp == WARPS) {
     // -------------------------------------------------------------- feeding
@@ -709,7 +711,8 @@ __global__ void __launch_bounds__(Shape<TOK>::THREADS, 1) gemv_kernel(const __gr
     Cur mine = start(lane);
     if (lane >= p.teams) mine.rows = 0;
     int group = 0, block = -1;
-    uint32_t stage = 0, ph = 1;
+    // stage and parity of each team
+    uint32_t stage_of = 0, ph_of = 1;
     while (ok && __any_sync(0xffffffffu, mine.rows > 0)) {
       if (mine.rows && mine.block != block) {
         block = mine.block;
@@ -717,57 +720,67 @@ __global__ void __launch_bounds__(Shape<TOK>::THREADS, 1) gemv_kernel(const __gr
       }
 #pragma unroll 1
       for (int t = 0; t < p.teams; ++t) {
-        const int rows = __shfl_sync(0xffffffffu, mine.rows, t);
-        if (!rows) continue;
-        const int n0 = __shfl_sync(0xffffffffu, mine.n0, t), gr = __shfl_sync(0xffffffffu, group, t);
+        const int tile_rows = __shfl_sync(0xffffffffu, mine.rows, t);
+        if (!tile_rows) continue;
+        const int tile_n0 = __shfl_sync(0xffffffffu, mine.n0, t), gr = __shfl_sync(0xffffffffu, group, t);
         const int first = __shfl_sync(0xffffffffu, mine.pass, t) * p.team_warps;  // slab
         const int slabs = min(p.team_warps, p.slabs - first);
-        const uint32_t bar = bars(t) + 8 * stage;
-        ok = wait_uniform(bar + EMPTY, ph, wctx, SITE_PROD_EMPTY);  // the stage's last readers
-        if (!ok) break;
-        const uint32_t box = TILE_N * SLAB / 2;
-        const uint32_t codes = base + stage * S::CODE_BYTES + t * p.team_warps * box;
-        const uint32_t sdst = base + S::SCALES + stage * S::SCALE_STAGE + t * team_sb;
-        const uint32_t zdst = base + S::SCALES + stage * S::SCALE_STAGE + S::ZERO_OFF + t * team_zb;
-        const bool zeros = is_int4(KIND) && p.zero;
-        if (elect_one()) {
-          uint32_t bytes = p.team_warps * box;
-          if (p.bulk) bytes += TILE_N * (team_sb / TILE_N + (zeros ? team_zb / TILE_N : 0));
-          mbar_arrive_expect_tx(bar, bytes);
-          if (p.whole) tma_load_4d(codes, &p.tmap_b, 0, n0, first, gr, bar);
-          if (p.bulk) {
-            for (int x = 0; x < team_sb / TILE_N; x += p.box_s)
-              tma_load3<1>(sdst + TILE_N * x, &p.tmap_s, first * SB + x, n0, gr, bar);
-            if (zeros) tma_load3<1>(zdst, &p.tmap_z, first * ZB, n0, gr, bar);
+        uint32_t stage = __shfl_sync(0xffffffffu, stage_of, t), ph = __shfl_sync(0xffffffffu, ph_of, t);
+#pragma unroll 1
+        for (int h = 0; h < tile_rows && ok; h += STAGE_N) {
+          const int n0 = tile_n0 + h, rows = min(STAGE_N, tile_rows - h);
+          const uint32_t bar = bars(t) + 8 * stage;
+          ok = wait_uniform(bar + EMPTY, ph, wctx, SITE_PROD_EMPTY);  // the stage's last readers
+          if (!ok) break;
+          const uint32_t box = STAGE_N * SLAB / 2;
+          const uint32_t codes = base + stage * S::CODE_BYTES + t * p.team_warps * box;
+          const uint32_t sdst = base + S::SCALES + stage * S::SCALE_STAGE + t * team_sb;
+          const uint32_t zdst = base + S::SCALES + stage * S::SCALE_STAGE + S::ZERO_OFF + t * team_zb;
+          const bool zeros = is_int4(KIND) && p.zero;
+          if (elect_one()) {
+            uint32_t bytes = p.team_warps * box;
+            if (p.bulk) bytes += team_sb + (zeros ? team_zb : 0);
+            mbar_arrive_expect_tx(bar, bytes);
+            if (p.whole) tma_load_4d(codes, &p.tmap_b, 0, n0, first, gr, bar);
+            if (p.bulk) {
+              for (int x = 0; x < team_sb / STAGE_N; x += p.box_s)
+                tma_load3<1>(sdst + STAGE_N * x, &p.tmap_s, first * SB + x, n0, gr, bar);
+              if (zeros) tma_load3<1>(zdst, &p.tmap_z, first * ZB, n0, gr, bar);
+            }
+          }
+          __syncwarp();
+          if (!p.whole && lane < p.team_warps)  // a slab a lane, zeros beyond K
+            tma_load3<1>(codes + lane * box, &p.tmap_b, (first + lane) * (SLAB / 2), n0, gr, bar);
+          if (!p.bulk) {
+            const uint8_t* src = p.scale + gr * p.stride_scale + n0 * p.ld_scale + first * SB;
+            const uint8_t* zsrc = p.zero + gr * p.stride_zero + n0 * p.ld_zero + first * ZB;
+            // 4-byte words from the boundary below each row's start; what lies
+            // past the row's end is zero.  One row at a time, a word a lane.
+            auto words = [&](uint32_t dst, uint32_t pitch, const uint8_t* at, int64_t ld, int want, int left) {
+#pragma unroll 1
+              for (int r = 0; r < rows; ++r, at += ld, dst += pitch) {
+                const int mis = static_cast<int>(reinterpret_cast<uintptr_t>(at)) & 3;
+#pragma unroll 1
+                for (int i = 4 * lane; i < want + mis; i += 128)
+                  cp_async4(dst + i, i < left + mis ? at - mis + i : p.scale, max(0, min(4, left + mis - i)));
+              }
+            };
+            words(sdst, SCALE_PITCH, src, p.ld_scale, p.team_warps * SB, p.scale_row * ES - first * SB);
+            if (zeros) words(zdst, ZERO_PITCH, zsrc, p.ld_zero, p.team_warps * ZB, p.scale_row - first * ZB);
+            asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(bar) : "memory");
+          }
+          if (++stage == STAGES) {
+            stage = 0;
+            ph ^= 1u;
           }
         }
-        __syncwarp();
-        if (!p.whole && lane < p.team_warps)  // a slab a lane, zeros beyond K
-          tma_load3<1>(codes + lane * box, &p.tmap_b, (first + lane) * (SLAB / 2), n0, gr, bar);
-        if (!p.bulk) {
-          const uint8_t* src = p.scale + gr * p.stride_scale + n0 * p.ld_scale + first * SB;
-          const uint8_t* zsrc = p.zero + gr * p.stride_zero + n0 * p.ld_zero + first * ZB;
-          // 4-byte words from the boundary below each row's start; what lies
-          // past the row's end is zero.  One row at a time, a word a lane.
-          auto words = [&](uint32_t dst, uint32_t pitch, const uint8_t* at, int64_t ld, int want, int left) {
-#pragma unroll 1
-            for (int r = 0; r < rows; ++r, at += ld, dst += pitch) {
-              const int mis = static_cast<int>(reinterpret_cast<uintptr_t>(at)) & 3;
-#pragma unroll 1
-              for (int i = 4 * lane; i < want + mis; i += 128)
-                cp_async4(dst + i, i < left + mis ? at - mis + i : p.scale, max(0, min(4, left + mis - i)));
-            }
-          };
-          words(sdst, SCALE_PITCH, src, p.ld_scale, p.team_warps * SB, p.scale_row * ES - first * SB);
-          if (zeros) words(zdst, ZERO_PITCH, zsrc, p.ld_zero, p.team_warps * ZB, p.scale_row - first * ZB);
-          asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(bar) : "memory");
+        if (!ok) break;
+        if (lane == t) {
+          stage_of = stage;
+          ph_of = ph;
         }
       }
       if (mine.rows) mine.next(p, passes);
-      if (++stage == STAGES) {
-        stage = 0;
-        ph ^= 1u;
-      }
     }
     asm volatile("cp.async.wait_all;" ::: "memory");
     if (!ok && lane == 0) {
@@ -787,14 +800,14 @@ __global__ void __launch_bounds__(Shape<TOK>::THREADS, 1) gemv_kernel(const __gr
     int have_block = -1, have_pass = -1, group = 0;  // whose fragments are loaded
     uint32_t stage = 0, ph = 0, buf = 0, buf_ph = ~0u;  // buf_ph: a parity bit per buffer
     const uint32_t bar = bars(team);
-    const uint8_t* codes0 = smem + warp * (TILE_N * SLAB / 2);
+    const uint8_t* codes0 = smem + warp * (STAGE_N * SLAB / 2);
     const uint8_t* scales0 = smem + S::SCALES + team * team_sb;
     const uint8_t* zeros0 = smem + S::SCALES + S::ZERO_OFF + team * team_zb;
     int to_s1 = 8 * SCALE_PITCH, to_z1 = 8 * ZERO_PITCH;  // from row g to row g + 8
     if (p.bulk) {
       // 128 bytes of a row to a box; a box's rows 8 apart are swizzled alike
       const uint32_t x = wk * SB;
-      scales0 += (x >> 7) * (TILE_N * 128) + box_at(g, x & 127u, p.box_s);
+      scales0 += (x >> 7) * (STAGE_N * 128) + box_at(g, x & 127u, p.box_s);
       zeros0 += box_at(g, wk * ZB, p.box_z);
       to_s1 = 8 * p.box_s;
       to_z1 = 8 * p.box_z;
@@ -813,48 +826,54 @@ __global__ void __launch_bounds__(Shape<TOK>::THREADS, 1) gemv_kernel(const __gr
         load_fragments<KIND, BF16, TOK>(p, rb, wk + cu.pass * p.team_warps, lane, smem + S::ACT + warp * S::ACT_BYTES,
                                        frag, undo);
       }
-      ok = wait_uniform(bar + 8 * stage, ph, wctx, SITE_MMA_FULL);
-      if (!ok) break;
-      float acc[NT][4] = {};
       const int slab = wk + cu.pass * p.team_warps;
-      if (slab < p.slabs) {
-        const uint8_t *s0 = scales0 + stage * S::SCALE_STAGE, *s1 = s0 + to_s1;
-        const uint8_t *z0 = nullptr, *z1 = nullptr;
-        if (is_int4(KIND) && p.zero) {
-          z0 = zeros0 + stage * S::SCALE_STAGE;
-          z1 = z0 + to_z1;
-        }
-        if (!p.bulk) {
-          // each row starts as far past a 4-byte boundary as it does in memory
-          const uint32_t first = static_cast<uint32_t>(cu.pass * p.team_warps);
-          const uint32_t ld_s = static_cast<uint32_t>(p.ld_scale), ra = static_cast<uint32_t>(cu.n0 + g);
-          const uint32_t at = static_cast<uint32_t>(group) * static_cast<uint32_t>(p.stride_scale) + first * SB + ra * ld_s;
-          s0 += at & 3u;
-          s1 += (at + 8u * ld_s) & 3u;
+#pragma unroll 1
+      for (int h = 0; h < cu.rows; h += STAGE_N) {
+        ok = wait_uniform(bar + 8 * stage, ph, wctx, SITE_MMA_FULL);
+        if (!ok) break;
+        float acc[NT][4] = {};
+        if (slab < p.slabs) {
+          const uint8_t *s0 = scales0 + stage * S::SCALE_STAGE, *s1 = s0 + to_s1;
+          const uint8_t *z0 = nullptr, *z1 = nullptr;
           if (is_int4(KIND) && p.zero) {
-            const uint32_t ld_z = static_cast<uint32_t>(p.ld_zero);
-            const uint32_t zat = static_cast<uint32_t>(group) * static_cast<uint32_t>(p.stride_zero) + first * ZB + ra * ld_z;
-            z0 += zat & 3u;
-            z1 += (zat + 8u * ld_z) & 3u;
+            z0 = zeros0 + stage * S::SCALE_STAGE;
+            z1 = z0 + to_z1;
           }
+          if (!p.bulk) {
+            // each row starts as far past a 4-byte boundary as it does in memory
+            const uint32_t first = static_cast<uint32_t>(cu.pass * p.team_warps);
+            const uint32_t ld_s = static_cast<uint32_t>(p.ld_scale), ra = static_cast<uint32_t>(cu.n0 + h + g);
+            const uint32_t at = static_cast<uint32_t>(group) * static_cast<uint32_t>(p.stride_scale) + first * SB + ra * ld_s;
+            s0 += at & 3u;
+            s1 += (at + 8u * ld_s) & 3u;
+            if (is_int4(KIND) && p.zero) {
+              const uint32_t ld_z = static_cast<uint32_t>(p.ld_zero);
+              const uint32_t zat = static_cast<uint32_t>(group) * static_cast<uint32_t>(p.stride_zero) + first * ZB + ra * ld_z;
+              z0 += zat & 3u;
+              z1 += (zat + 8u * ld_z) & 3u;
+            }
+          }
+          rows16<KIND, BF16, TOK>(codes0 + stage * S::CODE_BYTES, s0, s1, z0, z1, p.bulk, lane, frag, undo, acc);
         }
-        rows16<KIND, BF16, TOK>(codes0 + stage * S::CODE_BYTES, s0, s1, z0, z1, p.bulk, lane, frag, undo, acc);
+        __syncwarp();
+        if (lane == 0) mbar_arrive(bar + EMPTY + 8 * stage);
+        if (++stage == STAGES) {
+          stage = 0;
+          ph ^= 1u;
+        }
+        if (h == 0) {  // the buffer its parts go to
+          ok = wait_uniform(bar + PFREE + 8 * buf, (buf_ph >> buf) & 1u, wctx, SITE_MMA_ACC_EMPTY);
+          if (!ok) break;
+        }
+        float* mine = part0 + buf * (WARPS * S::TILE_PART) + h;
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+          for (int i = 0; i < 4; i += S::STEP) mine[(8 * nt + (i & 1)) * S::PART_PITCH + 8 * (i >> 1)] = acc[nt][i];
       }
-      __syncwarp();
-      if (lane == 0) mbar_arrive(bar + EMPTY + 8 * stage);
-      ok = wait_uniform(bar + PFREE + 8 * buf, (buf_ph >> buf) & 1u, wctx, SITE_MMA_ACC_EMPTY);
       if (!ok) break;
-      float* mine = part0 + buf * (WARPS * S::TILE_PART);
-#pragma unroll
-      for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-        for (int i = 0; i < 4; i += S::STEP) mine[(8 * nt + (i & 1)) * S::PART_PITCH + 8 * (i >> 1)] = acc[nt][i];
       __syncwarp();
       if (lane == 0) mbar_arrive(bar + PFULL + 8 * buf);
-      if (++stage == STAGES) {
-        stage = 0;
-        ph ^= 1u;
-      }
       buf_ph ^= 1u << buf;
       cu.next(p, passes);
       if (++buf == PARTS || cu.i == 0) buf = 0;
@@ -891,7 +910,8 @@ __global__ void __launch_bounds__(Shape<TOK>::THREADS, 1) gemv_kernel(const __gr
         const float* parts = parts0 + (buf * WARPS + t * p.team_warps) * S::TILE_PART;
 #pragma unroll
         for (int j0 = 0; j0 < S::OUT; j0 += 128) {
-          const int row = j0 / TILE_N + (lane >> 2), n = 4 * (lane & 3);
+          constexpr int LANES = TILE_N / 4;  // lanes an activation row takes
+          const int row = j0 / TILE_N + lane / LANES, n = 4 * (lane % LANES);
           const float4* at = reinterpret_cast<const float4*>(parts + (row < TOK ? row : 0) * S::PART_PITCH + n);
           float4 s = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
 #pragma unroll 8
@@ -968,6 +988,7 @@ struct Variants {
 };
 const Variants g_variants;
 constexpr int SHAPE_SMEM[SHAPES] = {Shape<4>::BYTES, Shape<8>::BYTES, Shape<16>::BYTES};
+constexpr int SHAPE_WARPS[SHAPES] = {Shape<4>::WARPS, Shape<8>::WARPS, Shape<16>::WARPS};
 constexpr int SHAPE_THREADS[SHAPES] = {Shape<4>::THREADS, Shape<8>::THREADS, Shape<16>::THREADS};
 
 // Per device, on the first call: the variants' shared-memory attribute.
@@ -1077,24 +1098,25 @@ int run_gemv(const tcg_gemv_w4_args* args, cudaStream_t s) {
   // (a block for every `tok` rows and one more per group there can be at most)
   if ((a.R / tok + active) * p.grains > INT32_MAX) return TCG_ERR_UNSUPPORTED;
   if (int rc = record_cuda(device_setup(dev))) return rc;
-  p.team_warps = std::min(WARPS, p.slabs);
-  p.teams = WARPS / p.team_warps;
+  const int warps = SHAPE_WARPS[shape_index(tok)];
+  p.team_warps = std::min(warps, p.slabs);
+  p.teams = warps / p.team_warps;
   p.whole = a.K % SLAB == 0;
   const auto box = [](int bytes) { return bytes <= 32 ? 32 : bytes <= 64 ? 64 : 128; };
   p.box_s = box(p.team_warps * (SLAB / a.group) * es);
   p.box_z = box(p.team_warps * (SLAB / a.group));
   if (p.bulk) {
-    if (int rc = make_byte_map(&p.tmap_s, a.scale, blocks_k * es, a.N, a.G, p.ld_scale, p.stride_scale, p.box_s, TILE_N))
+    if (int rc = make_byte_map(&p.tmap_s, a.scale, blocks_k * es, a.N, a.G, p.ld_scale, p.stride_scale, p.box_s, STAGE_N))
       return rc;
     if (a.zero)
-      if (int rc = make_byte_map(&p.tmap_z, a.zero, blocks_k, a.N, a.G, p.ld_zero, p.stride_zero, p.box_z, TILE_N))
+      if (int rc = make_byte_map(&p.tmap_z, a.zero, blocks_k, a.N, a.G, p.ld_zero, p.stride_zero, p.box_z, STAGE_N))
         return rc;
   }
   if (p.whole) {
-    if (int rc = make_slab_map(&p.tmap_b, a.B, SLAB / 2, a.N, a.K / SLAB, a.G, a.ldb / 2, a.stride_b / 2, TILE_N, p.team_warps))
+    if (int rc = make_slab_map(&p.tmap_b, a.B, SLAB / 2, a.N, a.K / SLAB, a.G, a.ldb / 2, a.stride_b / 2, STAGE_N, p.team_warps))
       return rc;
   } else {
-    if (int rc = make_byte_map(&p.tmap_b, a.B, a.K / 2, a.N, a.G, a.ldb / 2, a.stride_b / 2, SLAB / 2, TILE_N)) return rc;
+    if (int rc = make_byte_map(&p.tmap_b, a.B, a.K / 2, a.N, a.G, a.ldb / 2, a.stride_b / 2, SLAB / 2, STAGE_N)) return rc;
   }
   const int kind = a.format == TCG_W4_MXF4   ? K_MXF4
                    : a.format == TCG_W4_NVF4 ? K_NVF4
