@@ -17,20 +17,21 @@
 // issue at half rate, so the 16 decoding warps do little else, and what feeds
 // and empties them has warps of its own:
 //   warps 0..15   a slab of 256 of K each, whose activations stay in
-//                 registers, walking down the matrix in tiles of 32 rows (16
-//                 with 16 activation rows);
-//   warp 16       brings 16 rows to a stage of a ring: codes, scales and zero
-//                 points by a TMA copy each, for all slabs at once (a copy
-//                 takes its issuing thread 150 cycles, one for every warp or
-//                 row would take longer than the decoding);
-//   the others    (two; with 16 activation rows, whose fragments want the
-//                 registers, one) add the warps' parts of a tile in a fixed
-//                 order and store it while the next tiles are decoded.
-// A team of warps covers K (the 16, or fewer when K is short: then a CTA has
-// several teams) and takes an equal share of the matrix rows; a K of more
-// slabs than warps is taken in passes over a chunk of tiles, whose sums wait
-// in shared memory.  What lies beyond K or N is zero, so the inner loop has no
-// bounds.
+//                 registers, walking down the matrix 16 rows at a time (eight
+//                 warps when there are 16 activation rows: their fragments
+//                 take 64 registers, and what spills goes past an L1 that
+//                 shared memory leaves almost nothing of)
+//   the next      brings the rows of a stage to a ring: codes, scales and
+//                 zero points by a TMA copy each, for all slabs at once (a
+//                 copy takes its issuing thread 150 cycles; one for every
+//                 warp or row would take longer than the decoding)
+//   two more      add the warps' parts of a tile of two stages in a fixed
+//                 order and store it while the next tile is decoded.
+// The warps cover K side by side; when K is short, the others stand below
+// them and a stage has so many more rows.  Each CTA takes an equal share of
+// the matrix rows.  A K of more slabs than warps is taken in passes over a
+// chunk of tiles, whose sums wait in shared memory.  What lies beyond K or N
+// is zero, so the inner loop has no bounds.
 //
 // bf16 activations are brought into f16's range by a power of two per row and
 // slab (the largest finite value to [2^14, 2^15)), undone on fp32 sums (before
@@ -59,10 +60,6 @@ constexpr int64_t MAX_EXTENT = int64_t{1} << 30;
 
 constexpr int SLAB = 256;          // K per warp: 128 bytes of codes
 constexpr int STAGE_N = 16;        // matrix rows per stage: one mma's
-// bytes of a matrix row's scales, zero points in a stage when they are copied
-// word by word: up to 16, 8 a warp, and 4 a team for rows that start off a
-// 4-byte boundary; rows on different banks
-constexpr int SCALE_PITCH = 336, ZERO_PITCH = 208;
 // a swizzled box of rows of `span` bytes: where byte x of row r lies
 __device__ __forceinline__ uint32_t box_at(uint32_t r, uint32_t x, uint32_t span) {
   const uint32_t swizzle = span == 128 ? r & 7u : span == 64 ? (r >> 1) & 3u : (r >> 2) & 1u;
@@ -74,22 +71,22 @@ enum Kind4 : int { K_INT4_32 = 0, K_INT4_64 = 1, K_INT4_128 = 2, K_MXF4 = 3, K_N
 constexpr bool is_int4(int k) { return k <= K_INT4_128; }
 constexpr int group_of_kind(int k) { return k == K_NVF4 ? 16 : k == K_MXF4 ? 32 : 32 << k; }
 constexpr int scale_bytes(int k) { return SLAB / group_of_kind(k) * (is_int4(k) ? 2 : 1); }  // of a row's slab
-constexpr int GRAIN = 2;           // matrix rows: the unit in which teams share them
+constexpr int SCALE_BYTES = 6 * 1024, ZERO_BYTES = 4 * 1024;  // room for them in a stage
+constexpr int GRAIN = 2;           // matrix rows: the unit in which the CTAs share them
 
 struct GemvParams {
-  // codes as bytes in 128-byte swizzled boxes of 16 rows: whole slabs
-  // [G][K / 256][N][128], a team's slabs in one box (K a multiple of 256), or
+  // codes as bytes in 128-byte swizzled boxes of a stage's rows: whole slabs
+  // [G][K / 256][N][128], all of a stage in one box (K a multiple of 256), or
   // rows [G][N][K / 2], one slab a box
   CUtensorMap tmap_b;
   int whole;
-  // scales, zero points as bytes [G][N][bytes of a row] in swizzled boxes of 16
-  // rows, where their rows are 16-byte aligned (`bulk`)
+  // scales, zero points as bytes [G][N][bytes of a row] in swizzled boxes of a
+  // stage's rows, where their rows are 16-byte aligned (`bulk`)
   CUtensorMap tmap_s, tmap_z;
   int box_s, box_z;  // bytes of a box's rows: 32, 64 or 128
   int R, N, K, G;
   const uint8_t* A;  // 16-bit elements
   int64_t lda;
-  int a_row_lines, a_lines;  // 128-byte lines of a row, of all rows
   const int32_t* offsets;
   const uint8_t* scale;
   int64_t ld_scale, stride_scale;  // bytes
@@ -103,8 +100,9 @@ struct GemvParams {
   int64_t ldd;
   int grains;       // GRAIN-row units of a matrix
   int slabs;        // ceil(K / 256)
-  int team_warps;   // warps of a team in one CTA
-  int teams;        // teams in a CTA
+  int across;       // warps side by side along K
+  int tile_rows;    // 32 down
+  int down;         // warps below each other: 16 rows of a stage each
   unsigned long long* err;
   uint64_t timeout_ns;
 };
@@ -117,33 +115,28 @@ struct Shape {
   static constexpr int NT = TOK == 16 ? 2 : 1;        // mma column blocks
   static constexpr int STEP = TOK == 4 ? 2 : 1;       // accumulator columns between rows
   static constexpr int WARPS = TOK == 16 ? 8 : 16;    // decoding warps
-  static constexpr int TILE_N = 32;                   // matrix rows per tile
-  static constexpr int OUT = TOK * TILE_N;            // sums of a tile
+  static constexpr int TILE_N = 32;                   // matrix rows a warp has of a tile: two stages
+  static constexpr int OUT = TOK * TILE_N;            // sums of them
   static constexpr int CAP = (TOK == 16 ? 4096 : 1024) / OUT;  // tiles of a chunk that is passed over more than once
   static constexpr int STAGES = TOK == 16 ? 6 : 4;    // ring stages
-  // buffers of parts: tile i of a chunk uses number i % PARTS, which one
-  // adding warp empties, so that in every pass the same warp has the tile
+  // buffers of parts: tile i of a chunk uses number i % PARTS, and each adding
+  // warp empties one: in every pass the same warp has the tile's sums
   static constexpr int PARTS = 2;
-  static constexpr int ADD_WARPS = 2;
+  static constexpr int ADD_WARPS = PARTS;
   static constexpr int THREADS = 32 * (WARPS + 1 + ADD_WARPS);
   static constexpr int PART_PITCH = TILE_N + (TOK == 4 ? 8 : 4);  // floats between a part's activation rows
   static constexpr int TILE_PART = TOK * PART_PITCH;  // floats of a warp's part
-  // a stage: codes [warp][16 rows][128 bytes]; scales, then zero points [16 rows][pitch]
+  // a stage: codes [slab][row][128 bytes]; scales, then zero points [row][pitch]
+  // or as boxes
   static constexpr int CODE_BYTES = WARPS * STAGE_N * SLAB / 2;
   static constexpr int SCALES = STAGES * CODE_BYTES;
-  // (boxes: up to 16 x 16 bytes a warp, teams on 1 KiB boundaries)
-  static constexpr int ZERO_OFF = 6 * 1024;
-  static constexpr int SCALE_STAGE = 10 * 1024;
-  static_assert(STAGE_N * SCALE_PITCH <= ZERO_OFF && STAGE_N * ZERO_PITCH <= SCALE_STAGE - ZERO_OFF, "");
-  static constexpr int PART = SCALES + STAGES * SCALE_STAGE;
+  static constexpr int PART = SCALES + STAGES * (SCALE_BYTES + ZERO_BYTES);
   // an activation row on its way to each warp's registers
   static constexpr int ACT = PART + PARTS * WARPS * TILE_PART * 4;
   static constexpr int ACT_BYTES = TOK == 4 ? SLAB * 2 : 0;
   static constexpr int SUM = ACT + WARPS * ACT_BYTES;
-  // per team: full[STAGES], empty[STAGES], part_full[PARTS], part_free[PARTS]
-  static constexpr int BARS = SUM + CAP * OUT * 4;
-  static constexpr int TEAM_BARS = 2 * STAGES + 2 * PARTS;
-  static constexpr int SEG = BARS + WARPS * TEAM_BARS * 8 + 8;
+  static constexpr int BARS = SUM + CAP * OUT * 4;  // full[STAGES], empty[STAGES], part_full[PARTS], part_free[PARTS]
+  static constexpr int SEG = BARS + (2 * STAGES + 2 * PARTS) * 8 + 8;
   static constexpr int BYTES = 1024 + SEG + 2 * (MAX_GROUPS + 1) * 4;
   static_assert(BYTES <= 232448, "dynamic shared memory");
 };
@@ -258,7 +251,7 @@ template <int KIND, bool BF16, int TOK, int NT = Shape<TOK>::NT>
 __device__ __forceinline__ void load_fragments(const GemvParams& p, const RowBlock& rb, int slab, int lane,
                                                uint8_t* scratch, uint32_t (&frag)[8][NT][4], float (&undo)[NT][2]) {
   const int g = lane >> 2, c = lane & 3;
-  if (TOK > 4) {
+  if constexpr (TOK > 4) {
     // many rows: each lane reads its own fragments, a quad shares a row
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt) {
@@ -325,68 +318,73 @@ __device__ __forceinline__ void load_fragments(const GemvParams& p, const RowBlo
         }
       }
     }
-    return;
-  }
+  } else {
 #pragma unroll
-  for (int ch = 0; ch < 8; ++ch)
+    for (int ch = 0; ch < 8; ++ch)
 #pragma unroll
-    for (int i = 0; i < 4; ++i) frag[ch][0][i] = 0u;
-  const uint8_t* src = p.A + 2 * (rb.row0 * p.lda + slab * SLAB + 8 * lane);
-  const bool in = slab * SLAB + 8 * lane < p.K;
-  float down = 1.0f;  // row c's factor
-  uint4 x = make_uint4(0u, 0u, 0u, 0u);
-  if (in && rb.rows > 0) x = *reinterpret_cast<const uint4*>(src);
+      for (int i = 0; i < 4; ++i) frag[ch][0][i] = 0u;
+    const uint8_t* src = p.A + 2 * (rb.row0 * p.lda + slab * SLAB + 8 * lane);
+    const bool in = slab * SLAB + 8 * lane < p.K;
+    float down = 1.0f;  // row c's factor
+    uint4 next[4];  // all rows in flight at once
+#pragma unroll
+    for (int r = 0; r < 4; ++r) {
+      next[r] = make_uint4(0u, 0u, 0u, 0u);
+      if (in && r < rb.rows) next[r] = *reinterpret_cast<const uint4*>(src + 2 * r * p.lda);
+    }
 #pragma unroll 1
-  for (int r = 0; r < rb.rows; ++r) {
-    uint32_t v[4] = {x.x, x.y, x.z, x.w};
-    src += 2 * p.lda;
-    if (in && r + 1 < rb.rows) x = *reinterpret_cast<const uint4*>(src);
-    if (BF16) {
-      // the largest magnitude of the row's slab; max drops NaN, and
-      // infinities are looked past when there are any
-      uint32_t m2 = 0;
+    for (int r = 0; r < rb.rows; ++r) {
+      uint32_t v[4] = {next[0].x, next[0].y, next[0].z, next[0].w};
+      next[0] = next[1];
+      next[1] = next[2];
+      next[2] = next[3];
+      if (BF16) {
+        // the largest magnitude of the row's slab; max drops NaN, and
+        // infinities are looked past when there are any
+        uint32_t m2 = 0;
 #pragma unroll
-      for (int i = 0; i < 4; ++i) asm("max.bf16x2 %0, %0, %1;" : "+r"(m2) : "r"(v[i] & 0x7FFF7FFFu));
-      uint32_t m = max(m2 & 0xFFFFu, m2 >> 16);
-      if (m >= 0x7F80u) {
-        m = 0;
+        for (int i = 0; i < 4; ++i) asm("max.bf16x2 %0, %0, %1;" : "+r"(m2) : "r"(v[i] & 0x7FFF7FFFu));
+        uint32_t m = max(m2 & 0xFFFFu, m2 >> 16);
+        if (m >= 0x7F80u) {
+          m = 0;
 #pragma unroll 1
-        for (int i = 0; i < 8; ++i) {
-          const uint32_t h = ((i & 4) ? ((i & 2) ? v[3] : v[2]) : ((i & 2) ? v[1] : v[0])) >> (16 * (i & 1)) & 0x7FFFu;
-          if (h < 0x7F80u) m = max(m, h);
+          for (int i = 0; i < 8; ++i) {
+            const uint32_t h = ((i & 4) ? ((i & 2) ? v[3] : v[2]) : ((i & 2) ? v[1] : v[0])) >> (16 * (i & 1)) & 0x7FFFu;
+            if (h < 0x7F80u) m = max(m, h);
+          }
+        }
+        m = __reduce_max_sync(0xffffffffu, m);
+        const int e = min(141 - static_cast<int>(m >> 7), 126);  // 2^e brings the largest to [2^14, 2^15)
+        const float up = __uint_as_float(static_cast<uint32_t>(e + 127) << 23);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const __half2 h = __floats2half2_rn(__uint_as_float(v[i] << 16) * up, __uint_as_float(v[i] & 0xFFFF0000u) * up);
+          v[i] = *reinterpret_cast<const uint32_t*>(&h);
+        }
+        if (c == r) down = __uint_as_float(static_cast<uint32_t>(127 - e) << 23);
+      }
+      uint4 y = make_uint4(v[0], v[1], v[2], v[3]);
+      if (is_int4(KIND))  // pairs (0,4) (1,5) (2,6) (3,7)
+        y = make_uint4(__byte_perm(v[0], v[2], 0x5410), __byte_perm(v[0], v[2], 0x7632),
+                       __byte_perm(v[1], v[3], 0x5410), __byte_perm(v[1], v[3], 0x7632));
+      *reinterpret_cast<uint4*>(scratch + 16 * lane) = y;
+      __syncwarp();
+      if (g == 2 * r) {  // the row of this even column: 8 consecutive elements of each 32
+#pragma unroll
+        for (int ch = 0; ch < 8; ++ch) {
+          const uint4 a = lds<uint4>(scratch, 64 * ch + 16 * c);
+          uint32_t(&f)[4] = frag[ch][0];
+          f[0] = a.x;
+          f[1] = a.y;
+          f[2] = a.z;
+          f[3] = a.w;
         }
       }
-      m = __reduce_max_sync(0xffffffffu, m);
-      const int e = min(141 - static_cast<int>(m >> 7), 126);  // 2^e brings the largest to [2^14, 2^15)
-      const float up = __uint_as_float(static_cast<uint32_t>(e + 127) << 23);
-#pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        const __half2 h = __floats2half2_rn(__uint_as_float(v[i] << 16) * up, __uint_as_float(v[i] & 0xFFFF0000u) * up);
-        v[i] = *reinterpret_cast<const uint32_t*>(&h);
-      }
-      if (c == r) down = __uint_as_float(static_cast<uint32_t>(127 - e) << 23);
+      __syncwarp();
     }
-    uint4 y = make_uint4(v[0], v[1], v[2], v[3]);
-    if (is_int4(KIND))  // pairs (0,4) (1,5) (2,6) (3,7)
-      y = make_uint4(__byte_perm(v[0], v[2], 0x5410), __byte_perm(v[0], v[2], 0x7632),
-                     __byte_perm(v[1], v[3], 0x5410), __byte_perm(v[1], v[3], 0x7632));
-    *reinterpret_cast<uint4*>(scratch + 16 * lane) = y;
-    __syncwarp();
-    if (g == 2 * r) {  // the row of this even column: 8 consecutive elements of each 32
-#pragma unroll
-      for (int ch = 0; ch < 8; ++ch) {
-        const uint4 a = lds<uint4>(scratch, 64 * ch + 16 * c);
-        uint32_t(&f)[4] = frag[ch][0];
-        f[0] = a.x;
-        f[1] = a.y;
-        f[2] = a.z;
-        f[3] = a.w;
-      }
-    }
+    undo[0][0] = undo[0][1] = down;
     __syncwarp();
   }
-  undo[0][0] = undo[0][1] = down;
-  __syncwarp();
 }
 
 // A row's scales of a slab as words, from a byte offset that may be off a
@@ -554,9 +552,9 @@ __device__ __forceinline__ void rows16(const uint8_t* codes, const uint8_t* s0, 
   }
 }
 
-// A team's tiles in order: chunks of tiles, for each its passes over K, for
+// A CTA's tiles in order: chunks of tiles, for each its passes over K, for
 // each the tiles.  Without a second pass all tiles are one chunk.
-template <int CAP, int TILE_N>
+template <int CAP>
 struct Cursor {
   int chunk, pos, end;   // grains, counted over the row blocks
   int i, pass;           // tile within the chunk, pass
@@ -569,7 +567,7 @@ struct Cursor {
     }
     block = pos / p.grains;
     n0 = (pos - block * p.grains) * GRAIN;
-    rows = min(min(TILE_N, (end - pos) * GRAIN), p.N - n0);
+    rows = min(min(p.tile_rows, (end - pos) * GRAIN), p.N - n0);
   }
   __device__ __forceinline__ void next(const GemvParams& p, int passes) {
     pos += (rows + GRAIN - 1) / GRAIN;
@@ -585,7 +583,7 @@ struct Cursor {
       }
       locate(p);
     } else if (n0 < p.N && pos < end) {  // further down the same matrix
-      rows = min(min(TILE_N, (end - pos) * GRAIN), p.N - n0);
+      rows = min(min(p.tile_rows, (end - pos) * GRAIN), p.N - n0);
     } else {
       locate(p);
     }
@@ -595,7 +593,7 @@ struct Cursor {
 template <int KIND, bool BF16, int TOK>
 __global__ void __launch_bounds__(Shape<TOK>::THREADS, 1) gemv_kernel(const __grid_constant__ GemvParams p) {
   using S = Shape<TOK>;
-  constexpr int WARPS = S::WARPS, NT = S::NT, STAGES = S::STAGES, PARTS = S::PARTS, THREADS = S::THREADS, TILE_N = S::TILE_N, ADD_WARPS = S::ADD_WARPS;
+  constexpr int WARPS = S::WARPS, NT = S::NT, STAGES = S::STAGES, PARTS = S::PARTS, ADD_WARPS = S::ADD_WARPS;
   extern __shared__ uint8_t smem_raw[];
   const uint32_t raw = smem_u32(smem_raw);
   uint8_t* smem = smem_raw + (((raw + 1023u) & ~1023u) - raw);
@@ -605,25 +603,24 @@ __global__ void __launch_bounds__(Shape<TOK>::THREADS, 1) gemv_kernel(const __gr
   int* pre = seg + p.G + 1;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const WaitCtx wctx{p.timeout_ns, p.err, abort_word};
-  auto bars = [&](int team) { return base + S::BARS + 8u * S::TEAM_BARS * team; };  // full[], then
-  constexpr uint32_t EMPTY = 8 * STAGES, PFULL = 16 * STAGES, PFREE = PFULL + 8 * PARTS;
+  const uint32_t full = base + S::BARS, empty = full + 8 * STAGES, part_full = empty + 8 * STAGES,
+                 part_free = part_full + 8 * PARTS;
 
-  if (threadIdx.x < p.teams) {
-    const uint32_t b = bars(threadIdx.x);
+  const int active = p.across * p.down;  // decoding warps at work
+  if (threadIdx.x == 0) {
     for (int i = 0; i < STAGES; ++i) {
-      mbar_init(b + 8 * i, p.bulk ? 1 : 33);  // the copies' bytes, and every feeding lane's own copies
-      mbar_init(b + EMPTY + 8 * i, p.team_warps);
+      mbar_init(full + 8 * i, p.bulk ? 1 : 33);  // the copies' bytes, and each lane's that copies words
+      mbar_init(empty + 8 * i, active);
     }
     for (int i = 0; i < PARTS; ++i) {
-      mbar_init(b + PFULL + 8 * i, p.team_warps);
-      mbar_init(b + PFREE + 8 * i, 1);
+      mbar_init(part_full + 8 * i, active);
+      mbar_init(part_free + 8 * i, 1);
     }
-    if (threadIdx.x == 0) {
-      *abort_word = 0u;
-      prefetch_tmap(&p.tmap_b);
-    }
+    *abort_word = 0u;
+    prefetch_tmap(&p.tmap_b);
     fence_mbarrier_init();
   }
+  __syncthreads();
   griddep_wait();
   griddep_launch_dependents();
   // one group of few rows: its block is there whatever the offsets say, and
@@ -634,45 +631,59 @@ __global__ void __launch_bounds__(Shape<TOK>::THREADS, 1) gemv_kernel(const __gr
     span.x = min(max(p.offsets[0], 0), p.R);
     span.y = min(max(p.offsets[1], span.x), p.R);
   }
-  // the activations will be asked for late and by every CTA
-  for (int64_t i = static_cast<int64_t>(blockIdx.x) * THREADS + threadIdx.x; i < p.a_lines;
-       i += static_cast<int64_t>(gridDim.x) * THREADS) {
-    const int64_t row = i / p.a_row_lines;
-    asm volatile("prefetch.global.L2 [%0];" ::"l"(p.A + 2 * row * p.lda + 128 * (i - row * p.a_row_lines)));
-  }
-  if (p.offsets && !single)
-    for (int i = threadIdx.x; i <= p.G; i += THREADS) seg[i] = p.offsets[i];
-  __syncthreads();
   int blocks;
   if (single) {
     blocks = 1;
   } else if (p.offsets) {
-    if (warp == 0) {  // clamp to [previous, R]; row blocks before each group
+    if (warp == WARPS) {  // clamp to [previous, R]; row blocks before each group; four groups a lane
       int run_max = 0, run_blocks = 0;
-      for (int i0 = 0; i0 <= p.G; i0 += 32) {
-        const int i = i0 + lane;
-        int v = i <= p.G ? min(max(seg[i], 0), p.R) : 0;
+#pragma unroll 1
+      for (int i0 = 0; i0 <= p.G; i0 += 128) {
+        int v[4], n[4];
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+          const int i = i0 + 4 * lane + k;
+          v[k] = i <= p.G ? p.offsets[i] : 0;
+        }
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+          v[k] = min(max(v[k], 0), p.R);
+          if (k) v[k] = max(v[k], v[k - 1]);
+        }
+        int top = v[3];
 #pragma unroll
         for (int d = 1; d < 32; d <<= 1) {
-          const int o = __shfl_up_sync(0xffffffffu, v, d);
-          if (lane >= d) v = max(v, o);
+          const int o = __shfl_up_sync(0xffffffffu, top, d);
+          if (lane >= d) top = max(top, o);
         }
-        v = max(v, run_max);
-        int before = __shfl_up_sync(0xffffffffu, v, 1);
-        if (lane == 0) before = run_max;
-        int n = i >= 1 && i <= p.G ? (v - before + TOK - 1) / TOK : 0;
+        int before = __shfl_up_sync(0xffffffffu, top, 1);
+        before = lane == 0 ? run_max : max(before, run_max);
+        int sum = 0, last = before;
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+          const int i = i0 + 4 * lane + k;
+          v[k] = max(v[k], before);
+          sum += i >= 1 && i <= p.G ? (v[k] - last + TOK - 1) / TOK : 0;
+          last = v[k];
+          n[k] = sum;
+        }
+        int all = sum;
 #pragma unroll
         for (int d = 1; d < 32; d <<= 1) {
-          const int o = __shfl_up_sync(0xffffffffu, n, d);
-          if (lane >= d) n += o;
+          const int o = __shfl_up_sync(0xffffffffu, all, d);
+          if (lane >= d) all += o;
         }
-        n += run_blocks;
-        if (i <= p.G) {
-          seg[i] = v;
-          pre[i] = n;
+        const int mine = run_blocks + all - sum;
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+          const int i = i0 + 4 * lane + k;
+          if (i <= p.G) {
+            seg[i] = v[k];
+            pre[i] = mine + n[k];
+          }
         }
-        run_max = __shfl_sync(0xffffffffu, v, 31);
-        run_blocks = __shfl_sync(0xffffffffu, n, 31);
+        run_max = max(run_max, __shfl_sync(0xffffffffu, top, 31));
+        run_blocks += __shfl_sync(0xffffffffu, all, 31);
       }
     }
     __syncthreads();
@@ -681,106 +692,85 @@ __global__ void __launch_bounds__(Shape<TOK>::THREADS, 1) gemv_kernel(const __gr
     blocks = (p.R + TOK - 1) / TOK;
   }
 
-  // a team's share of the grains; the slab of its warp k in pass i is k + i * team_warps
-  const int total = blocks * p.grains, num_teams = static_cast<int>(gridDim.x) * p.teams;
-  const int share = total / num_teams, more = total - share * num_teams;
-  const int passes = (p.slabs + p.team_warps - 1) / p.team_warps;
-  using Cur = Cursor<S::CAP, S::TILE_N>;
-  auto start = [&](int team) {
-    // neighbouring teams sit in different CTAs, so that few rows spread over all
-    const int id = team * static_cast<int>(gridDim.x) + static_cast<int>(blockIdx.x);
-    Cur cu;
-    cu.chunk = cu.pos = id * share + min(id, more);
-    cu.end = cu.pos + share + (id < more ? 1 : 0);
-    cu.i = cu.pass = cu.block = cu.n0 = 0;
-    cu.locate(p);
-    return cu;
-  };
+  // a CTA's share of the grains; the slab of a warp in pass i is its column + i * across
+  const int total = blocks * p.grains, ctas = static_cast<int>(gridDim.x), cta = static_cast<int>(blockIdx.x);
+  const int share = total / ctas, more = total - share * ctas;
+  const int passes = (p.slabs + p.across - 1) / p.across;
+  Cursor<S::CAP> cu;
+  cu.chunk = cu.pos = cta * share + min(cta, more);
+  cu.end = cu.pos + share + (cta < more ? 1 : 0);
+  cu.i = cu.pass = cu.block = cu.n0 = 0;
+  cu.locate(p);
   bool ok = true;
 
   constexpr int SB = scale_bytes(KIND), ZB = SLAB / group_of_kind(KIND);  // a row's scales, zero points of a slab
   constexpr int ES = is_int4(KIND) ? 2 : 1;
-  // where a team's scales, zero points start after those of the team before:
-  // whole boxes of 16 rows, or so far along each row
-  const int team_sb = p.bulk ? STAGE_N * ((p.team_warps * SB + p.box_s - 1) / p.box_s * p.box_s) : p.team_warps * SB + 4;
-  const int team_zb = p.bulk ? STAGE_N * p.box_z : (p.team_warps * ZB + 3) / 4 * 4 + 4;
-
+  const int stage_rows = STAGE_N * p.down;
+  // bytes of a stage's scales, zero points: whole boxes, or rows with a word to spare
+  const int want_s = p.across * SB, want_z = p.across * ZB;
+  const int pitch_s = want_s + 4, pitch_z = (want_z + 3) / 4 * 4 + 4;
+  const uint32_t scales = S::SCALES, zeros = S::SCALES + STAGES * SCALE_BYTES;
+  const bool has_zero = is_int4(KIND) && p.zero;
   if (warp == WARPS) {
     // -------------------------------------------------------------- feeding
-    // Lane t < teams follows team t; the teams' tiles in turn.
-    Cur mine = start(lane);
-    if (lane >= p.teams) mine.rows = 0;
     int group = 0, block = -1;
-    // stage and parity of each team
-    uint32_t stage_of = 0, ph_of = 1;
-    while (ok && __any_sync(0xffffffffu, mine.rows > 0)) {
-      if (mine.rows && mine.block != block) {
-        block = mine.block;
+    uint32_t stage = 0, ph = 1;
+    const uint32_t box = stage_rows * (SLAB / 2);  // a slab's codes
+    const uint32_t bytes =
+        p.across * box + (p.bulk ? stage_rows * ((want_s + p.box_s - 1) / p.box_s * p.box_s + (has_zero ? p.box_z : 0)) : 0);
+    for (; cu.rows; cu.next(p, passes)) {
+      if (cu.block != block) {
+        block = cu.block;
         group = p.G == 1 ? 0 : row_block<TOK>(p, seg, pre, false, span, block).g;
       }
+      const int first = cu.pass * p.across;  // slab
 #pragma unroll 1
-      for (int t = 0; t < p.teams; ++t) {
-        const int tile_rows = __shfl_sync(0xffffffffu, mine.rows, t);
-        if (!tile_rows) continue;
-        const int tile_n0 = __shfl_sync(0xffffffffu, mine.n0, t), gr = __shfl_sync(0xffffffffu, group, t);
-        const int first = __shfl_sync(0xffffffffu, mine.pass, t) * p.team_warps;  // slab
-        const int slabs = min(p.team_warps, p.slabs - first);
-        uint32_t stage = __shfl_sync(0xffffffffu, stage_of, t), ph = __shfl_sync(0xffffffffu, ph_of, t);
-#pragma unroll 1
-        for (int h = 0; h < tile_rows && ok; h += STAGE_N) {
-          const int n0 = tile_n0 + h, rows = min(STAGE_N, tile_rows - h);
-          const uint32_t bar = bars(t) + 8 * stage;
-          ok = wait_uniform(bar + EMPTY, ph, wctx, SITE_PROD_EMPTY);  // the stage's last readers
-          if (!ok) break;
-          const uint32_t box = STAGE_N * SLAB / 2;
-          const uint32_t codes = base + stage * S::CODE_BYTES + t * p.team_warps * box;
-          const uint32_t sdst = base + S::SCALES + stage * S::SCALE_STAGE + t * team_sb;
-          const uint32_t zdst = base + S::SCALES + stage * S::SCALE_STAGE + S::ZERO_OFF + t * team_zb;
-          const bool zeros = is_int4(KIND) && p.zero;
-          if (elect_one()) {
-            uint32_t bytes = p.team_warps * box;
-            if (p.bulk) bytes += team_sb + (zeros ? team_zb : 0);
-            mbar_arrive_expect_tx(bar, bytes);
-            if (p.whole) tma_load_4d(codes, &p.tmap_b, 0, n0, first, gr, bar);
-            if (p.bulk) {
-              for (int x = 0; x < team_sb / STAGE_N; x += p.box_s)
-                tma_load3<1>(sdst + STAGE_N * x, &p.tmap_s, first * SB + x, n0, gr, bar);
-              if (zeros) tma_load3<1>(zdst, &p.tmap_z, first * ZB, n0, gr, bar);
-            }
-          }
-          __syncwarp();
-          if (!p.whole && lane < p.team_warps)  // a slab a lane, zeros beyond K
-            tma_load3<1>(codes + lane * box, &p.tmap_b, (first + lane) * (SLAB / 2), n0, gr, bar);
-          if (!p.bulk) {
-            const uint8_t* src = p.scale + gr * p.stride_scale + n0 * p.ld_scale + first * SB;
-            const uint8_t* zsrc = p.zero + gr * p.stride_zero + n0 * p.ld_zero + first * ZB;
-            // 4-byte words from the boundary below each row's start; what lies
-            // past the row's end is zero.  One row at a time, a word a lane.
-            auto words = [&](uint32_t dst, uint32_t pitch, const uint8_t* at, int64_t ld, int want, int left) {
-#pragma unroll 1
-              for (int r = 0; r < rows; ++r, at += ld, dst += pitch) {
-                const int mis = static_cast<int>(reinterpret_cast<uintptr_t>(at)) & 3;
-#pragma unroll 1
-                for (int i = 4 * lane; i < want + mis; i += 128)
-                  cp_async4(dst + i, i < left + mis ? at - mis + i : p.scale, max(0, min(4, left + mis - i)));
-              }
-            };
-            words(sdst, SCALE_PITCH, src, p.ld_scale, p.team_warps * SB, p.scale_row * ES - first * SB);
-            if (zeros) words(zdst, ZERO_PITCH, zsrc, p.ld_zero, p.team_warps * ZB, p.scale_row - first * ZB);
-            asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(bar) : "memory");
-          }
-          if (++stage == STAGES) {
-            stage = 0;
-            ph ^= 1u;
+      for (int h = 0; h < cu.rows; h += stage_rows) {
+        const int n0 = cu.n0 + h;
+        const uint32_t bar = full + 8 * stage, codes = base + stage * S::CODE_BYTES;
+        const uint32_t sdst = base + scales + stage * SCALE_BYTES, zdst = base + zeros + stage * ZERO_BYTES;
+        ok = wait_uniform(empty + 8 * stage, ph, wctx, SITE_PROD_EMPTY);  // the stage's last readers
+        if (!ok) break;
+        if (elect_one()) {
+          mbar_arrive_expect_tx(bar, bytes);
+          if (p.whole) tma_load_4d(codes, &p.tmap_b, 0, n0, first, group, bar);
+          if (p.bulk) {
+            for (int x = 0; x < want_s; x += p.box_s)
+              tma_load3<1>(sdst + stage_rows * x, &p.tmap_s, first * SB + x, n0, group, bar);
+            if (has_zero) tma_load3<1>(zdst, &p.tmap_z, first * ZB, n0, group, bar);
           }
         }
-        if (!ok) break;
-        if (lane == t) {
-          stage_of = stage;
-          ph_of = ph;
+        __syncwarp();
+        if (!p.whole && lane < p.across)  // a slab a lane, zeros beyond K
+          tma_load3<1>(codes + lane * box, &p.tmap_b, (first + lane) * (SLAB / 2), n0, group, bar);
+        if (!p.bulk) {
+          const int rows = min(stage_rows, cu.rows - h);
+          // 4-byte words from the boundary below each row's start; what lies
+          // past the row's end is zero.  Neighbouring lanes take a row's words.
+          auto words = [&](uint32_t dst, int pitch, const uint8_t* at, int64_t ld, int want, int left) {
+            const int n = (want + 6) / 4;  // words of a row that starts 3 bytes past a boundary
+#pragma unroll 1
+            for (int i = lane; i < rows * n; i += 32) {
+              const int r = i / n, x = 4 * (i - r * n);
+              const uint8_t* row = at + r * ld;
+              const int mis = static_cast<int>(reinterpret_cast<uintptr_t>(row)) & 3;
+              if (x < want + mis)
+                cp_async4(dst + r * pitch + x, x < left + mis ? row - mis + x : p.scale, max(0, min(4, left + mis - x)));
+            }
+          };
+          words(sdst, pitch_s, p.scale + group * p.stride_scale + n0 * p.ld_scale + first * SB, p.ld_scale, want_s,
+                p.scale_row * ES - first * SB);
+          if (has_zero)
+            words(zdst, pitch_z, p.zero + group * p.stride_zero + n0 * p.ld_zero + first * ZB, p.ld_zero, want_z,
+                  p.scale_row - first * ZB);
+          asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(bar) : "memory");
+        }
+        if (++stage == STAGES) {
+          stage = 0;
+          ph ^= 1u;
         }
       }
-      if (mine.rows) mine.next(p, passes);
+      if (!ok) break;
     }
     asm volatile("cp.async.wait_all;" ::: "memory");
     if (!ok && lane == 0) {
@@ -791,29 +781,26 @@ __global__ void __launch_bounds__(Shape<TOK>::THREADS, 1) gemv_kernel(const __gr
     }
   } else if (warp < WARPS) {
     // ------------------------------------------------------------- decoding
-    const int team = warp / p.team_warps, wk = warp - team * p.team_warps;
-    const int g = lane >> 2, c = lane & 3;
-    Cur cu = start(team);
-    if (team >= p.teams) cu.rows = 0;  // warps left over when teams do not fill the CTA
+    const int below = warp / p.across, wk = warp - below * p.across;
+    const int g = lane >> 2, c = lane & 3, row = STAGE_N * below + g;
+    if (warp >= active) cu.rows = 0;
     uint32_t frag[8][NT][4];
     float undo[NT][2];
     int have_block = -1, have_pass = -1, group = 0;  // whose fragments are loaded
     uint32_t stage = 0, ph = 0, buf = 0, buf_ph = ~0u;  // buf_ph: a parity bit per buffer
-    const uint32_t bar = bars(team);
-    const uint8_t* codes0 = smem + warp * (STAGE_N * SLAB / 2);
-    const uint8_t* scales0 = smem + S::SCALES + team * team_sb;
-    const uint8_t* zeros0 = smem + S::SCALES + S::ZERO_OFF + team * team_zb;
-    int to_s1 = 8 * SCALE_PITCH, to_z1 = 8 * ZERO_PITCH;  // from row g to row g + 8
+    const uint8_t* codes0 = smem + (wk * stage_rows + STAGE_N * below) * (SLAB / 2);
+    const uint8_t *scales0 = smem + scales, *zeros0 = smem + zeros;
+    int to_s1 = 8 * pitch_s, to_z1 = 8 * pitch_z;  // from row g to row g + 8
     if (p.bulk) {
       // 128 bytes of a row to a box; a box's rows 8 apart are swizzled alike
       const uint32_t x = wk * SB;
-      scales0 += (x >> 7) * (STAGE_N * 128) + box_at(g, x & 127u, p.box_s);
-      zeros0 += box_at(g, wk * ZB, p.box_z);
+      scales0 += (x >> 7) * (stage_rows * 128) + box_at(row, x & 127u, p.box_s);
+      zeros0 += box_at(row, wk * ZB, p.box_z);
       to_s1 = 8 * p.box_s;
       to_z1 = 8 * p.box_z;
     } else {
-      scales0 += g * SCALE_PITCH + wk * SB;
-      zeros0 += g * ZERO_PITCH + wk * ZB;
+      scales0 += row * pitch_s + wk * SB;
+      zeros0 += row * pitch_z + wk * ZB;
     }
     float* part0 = reinterpret_cast<float*>(smem + S::PART) + warp * S::TILE_PART +
                    (TOK == 4 ? c : 2 * c) * S::PART_PITCH + g;
@@ -823,30 +810,30 @@ __global__ void __launch_bounds__(Shape<TOK>::THREADS, 1) gemv_kernel(const __gr
         group = rb.g;
         have_block = cu.block;
         have_pass = cu.pass;
-        load_fragments<KIND, BF16, TOK>(p, rb, wk + cu.pass * p.team_warps, lane, smem + S::ACT + warp * S::ACT_BYTES,
+        load_fragments<KIND, BF16, TOK>(p, rb, wk + cu.pass * p.across, lane, smem + S::ACT + warp * S::ACT_BYTES,
                                        frag, undo);
       }
-      const int slab = wk + cu.pass * p.team_warps;
+      const int slab = wk + cu.pass * p.across;
 #pragma unroll 1
-      for (int h = 0; h < cu.rows; h += STAGE_N) {
-        ok = wait_uniform(bar + 8 * stage, ph, wctx, SITE_MMA_FULL);
+      for (int h = 0; h < cu.rows; h += stage_rows) {
+        ok = wait_uniform(full + 8 * stage, ph, wctx, SITE_MMA_FULL);
         if (!ok) break;
         float acc[NT][4] = {};
-        if (slab < p.slabs) {
-          const uint8_t *s0 = scales0 + stage * S::SCALE_STAGE, *s1 = s0 + to_s1;
+        if (slab < p.slabs && h + STAGE_N * below < cu.rows) {
+          const uint8_t *s0 = scales0 + stage * SCALE_BYTES, *s1 = s0 + to_s1;
           const uint8_t *z0 = nullptr, *z1 = nullptr;
-          if (is_int4(KIND) && p.zero) {
-            z0 = zeros0 + stage * S::SCALE_STAGE;
+          if (has_zero) {
+            z0 = zeros0 + stage * ZERO_BYTES;
             z1 = z0 + to_z1;
           }
           if (!p.bulk) {
             // each row starts as far past a 4-byte boundary as it does in memory
-            const uint32_t first = static_cast<uint32_t>(cu.pass * p.team_warps);
-            const uint32_t ld_s = static_cast<uint32_t>(p.ld_scale), ra = static_cast<uint32_t>(cu.n0 + h + g);
+            const uint32_t first = static_cast<uint32_t>(cu.pass * p.across);
+            const uint32_t ld_s = static_cast<uint32_t>(p.ld_scale), ra = static_cast<uint32_t>(cu.n0 + h + row);
             const uint32_t at = static_cast<uint32_t>(group) * static_cast<uint32_t>(p.stride_scale) + first * SB + ra * ld_s;
             s0 += at & 3u;
             s1 += (at + 8u * ld_s) & 3u;
-            if (is_int4(KIND) && p.zero) {
+            if (has_zero) {
               const uint32_t ld_z = static_cast<uint32_t>(p.ld_zero);
               const uint32_t zat = static_cast<uint32_t>(group) * static_cast<uint32_t>(p.stride_zero) + first * ZB + ra * ld_z;
               z0 += zat & 3u;
@@ -856,16 +843,16 @@ __global__ void __launch_bounds__(Shape<TOK>::THREADS, 1) gemv_kernel(const __gr
           rows16<KIND, BF16, TOK>(codes0 + stage * S::CODE_BYTES, s0, s1, z0, z1, p.bulk, lane, frag, undo, acc);
         }
         __syncwarp();
-        if (lane == 0) mbar_arrive(bar + EMPTY + 8 * stage);
+        if (lane == 0) mbar_arrive(empty + 8 * stage);
         if (++stage == STAGES) {
           stage = 0;
           ph ^= 1u;
         }
         if (h == 0) {  // the buffer its parts go to
-          ok = wait_uniform(bar + PFREE + 8 * buf, (buf_ph >> buf) & 1u, wctx, SITE_MMA_ACC_EMPTY);
+          ok = wait_uniform(part_free + 8 * buf, (buf_ph >> buf) & 1u, wctx, SITE_MMA_ACC_EMPTY);
           if (!ok) break;
         }
-        float* mine = part0 + buf * (WARPS * S::TILE_PART) + h;
+        float* mine = part0 + buf * (WARPS * S::TILE_PART) + (h ? STAGE_N : 0);
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
@@ -873,7 +860,7 @@ __global__ void __launch_bounds__(Shape<TOK>::THREADS, 1) gemv_kernel(const __gr
       }
       if (!ok) break;
       __syncwarp();
-      if (lane == 0) mbar_arrive(bar + PFULL + 8 * buf);
+      if (lane == 0) mbar_arrive(part_full + 8 * buf);
       buf_ph ^= 1u << buf;
       cu.next(p, passes);
       if (++buf == PARTS || cu.i == 0) buf = 0;
@@ -883,39 +870,33 @@ __global__ void __launch_bounds__(Shape<TOK>::THREADS, 1) gemv_kernel(const __gr
     const int me = warp - (WARPS + 1);
     const float* parts0 = reinterpret_cast<const float*>(smem + S::PART);
     float* sums = reinterpret_cast<float*>(smem + S::SUM);
-    uint32_t ph[PARTS / ADD_WARPS] = {};  // for each of its buffers a parity bit per team
-    // lane t < teams follows team t
-    Cur mine = start(lane);
-    if (lane >= p.teams) mine.rows = 0;
+    uint32_t parity = 0;
     RowBlock o{0, 0, 0};
     int block = -1;
     float alpha = 1.0f;
-    while (ok && __any_sync(0xffffffffu, mine.rows > 0)) {
+    for (; ok && cu.rows; cu.next(p, passes)) {
+      const int buf = cu.i % PARTS;
+      if (buf != me) continue;
+      if (cu.block != block) {
+        block = cu.block;
+        o = row_block<TOK>(p, seg, pre, single, span, block);
+        if (p.alpha) alpha = p.alpha[o.g];
+      }
+      ok = wait_uniform(part_full + 8 * buf, parity, wctx, SITE_EPI_ACC_FULL);
+      if (!ok) break;
+      parity ^= 1u;
 #pragma unroll 1
-      for (int t = 0; t < p.teams; ++t) {
-        const int rows = __shfl_sync(0xffffffffu, mine.rows, t), idx = __shfl_sync(0xffffffffu, mine.i, t);
-        const int buf = idx % PARTS;
-        if (!rows || buf % ADD_WARPS != me) continue;
-        const int n0 = __shfl_sync(0xffffffffu, mine.n0, t), pass = __shfl_sync(0xffffffffu, mine.pass, t);
-        const int blk = __shfl_sync(0xffffffffu, mine.block, t);
-        if (blk != block) {
-          block = blk;
-          o = row_block<TOK>(p, seg, pre, single, span, block);
-          if (p.alpha) alpha = p.alpha[o.g];
-        }
-        uint32_t& parity = ph[PARTS == ADD_WARPS || buf == 0 ? 0 : PARTS / ADD_WARPS - 1];
-        ok = wait_uniform(bars(t) + PFULL + 8 * buf, (parity >> t) & 1u, wctx, SITE_EPI_ACC_FULL);
-        if (!ok) break;
-        parity ^= 1u << t;
-        const float* parts = parts0 + (buf * WARPS + t * p.team_warps) * S::TILE_PART;
+      for (int below = 0; below < p.down; ++below) {
+        // 32 rows of the tile: 16 of each stage
+        const float* parts = parts0 + (buf * WARPS + below * p.across) * S::TILE_PART;
 #pragma unroll
         for (int j0 = 0; j0 < S::OUT; j0 += 128) {
-          constexpr int LANES = TILE_N / 4;  // lanes an activation row takes
-          const int row = j0 / TILE_N + lane / LANES, n = 4 * (lane % LANES);
+          constexpr int LANES = S::TILE_N / 4;  // lanes an activation row takes
+          const int row = j0 / S::TILE_N + lane / LANES, n = 4 * (lane % LANES);
           const float4* at = reinterpret_cast<const float4*>(parts + (row < TOK ? row : 0) * S::PART_PITCH + n);
           float4 s = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
 #pragma unroll 8
-          for (int w = 0; w < p.team_warps; ++w) {
+          for (int w = 0; w < p.across; ++w) {
             const float4 v = at[w * (S::TILE_PART / 4)];
             s.x += v.x;
             s.y += v.y;
@@ -923,8 +904,8 @@ __global__ void __launch_bounds__(Shape<TOK>::THREADS, 1) gemv_kernel(const __gr
             s.w += v.w;
           }
           if (row < TOK && passes > 1) {
-            float4* keep = reinterpret_cast<float4*>(sums + idx * S::OUT + j0 + 4 * lane);
-            if (pass > 0) {
+            float4* keep = reinterpret_cast<float4*>(sums + cu.i * S::OUT + j0 + 4 * lane);
+            if (cu.pass > 0) {
               const float4 v = *keep;
               s.x += v.x;
               s.y += v.y;
@@ -933,18 +914,18 @@ __global__ void __launch_bounds__(Shape<TOK>::THREADS, 1) gemv_kernel(const __gr
             }
             *keep = s;
           }
-          if (pass == passes - 1 && row < o.rows) {
-            const int64_t d = (o.row0 + row) * p.ldd + n0 + n;
+          if (cu.pass == passes - 1 && row < o.rows) {
+            const int first = (n < STAGE_N ? n : n + stage_rows - STAGE_N) + STAGE_N * below;  // row of the tile
+            const int64_t d = (o.row0 + row) * p.ldd + cu.n0 + first;
             const float v[4] = {s.x, s.y, s.z, s.w};
 #pragma unroll
             for (int k = 0; k < 4; ++k)
-              if (n + k < rows) store_d(p, d + k, v[k] * alpha);
+              if (first + k < cu.rows) store_d(p, d + k, v[k] * alpha);
           }
         }
-        __syncwarp();
-        if (lane == 0) mbar_arrive(bars(t) + PFREE + 8 * buf);
       }
-      if (mine.rows) mine.next(p, passes);
+      __syncwarp();
+      if (lane == 0) mbar_arrive(part_free + 8 * buf);
     }
     if (p.offsets) {  // rows of no group give zero
       const int first = single ? span.x : seg[0], end = single ? span.y : seg[p.G];
@@ -1073,16 +1054,13 @@ int run_gemv(const tcg_gemv_w4_args* args, cudaStream_t s) {
   p.zero = a.zero;
   p.ld_zero = a.ld_scale;
   p.stride_zero = a.stride_scale;
-  // (then K is a multiple of 256, and of so much that a team's share of a row
+  // (then K is a multiple of 256, and of so much that a pass's share of a row
   // is one of 16 bytes)
   const int64_t s_low = blocks_k * es | p.ld_scale | (a.G > 1 ? p.stride_scale : 0) |
                         static_cast<int64_t>(reinterpret_cast<uintptr_t>(a.scale));
   const int64_t z_low = blocks_k | p.ld_zero | (a.G > 1 ? p.stride_zero : 0) |
                         static_cast<int64_t>(reinterpret_cast<uintptr_t>(a.zero));
   p.bulk = s_low % 16 == 0 && (!a.zero || z_low % 16 == 0);
-  const int64_t lines = (a.K * 2 + 127) / 128;
-  p.a_row_lines = static_cast<int>(lines);
-  p.a_lines = a.R * lines <= 16384 ? static_cast<int>(a.R * lines) : 0;  // 2 MiB at most
   p.alpha = a.alpha;
   p.D = a.D;
   p.d_type = a.d_type;
@@ -1099,24 +1077,31 @@ int run_gemv(const tcg_gemv_w4_args* args, cudaStream_t s) {
   if ((a.R / tok + active) * p.grains > INT32_MAX) return TCG_ERR_UNSUPPORTED;
   if (int rc = record_cuda(device_setup(dev))) return rc;
   const int warps = SHAPE_WARPS[shape_index(tok)];
-  p.team_warps = std::min(warps, p.slabs);
-  p.teams = warps / p.team_warps;
+  p.across = std::min(warps, p.slabs);
+  // when K is short, the other warps go below: as far as every CTA still gets
+  // that many rows, and their scales fit
+  const int64_t blocks = std::max(active, (a.R + tok - 1) / tok);
+  const int64_t wanted = (blocks * a.N / device_sms(dev) + STAGE_N - 1) / STAGE_N;
+  p.down = static_cast<int>(std::max<int64_t>(1, std::min<int64_t>(warps / p.across, wanted)));
   p.whole = a.K % SLAB == 0;
   const auto box = [](int bytes) { return bytes <= 32 ? 32 : bytes <= 64 ? 64 : 128; };
-  p.box_s = box(p.team_warps * (SLAB / a.group) * es);
-  p.box_z = box(p.team_warps * (SLAB / a.group));
+  p.box_s = box(p.across * (SLAB / a.group) * es);
+  p.box_z = box(p.across * (SLAB / a.group));
+  if (p.bulk) p.down = std::min(p.down, std::min(SCALE_BYTES / (STAGE_N * p.box_s), ZERO_BYTES / (STAGE_N * p.box_z)));
+  p.tile_rows = 2 * STAGE_N * p.down;
+  const int stage_rows = STAGE_N * p.down;
   if (p.bulk) {
-    if (int rc = make_byte_map(&p.tmap_s, a.scale, blocks_k * es, a.N, a.G, p.ld_scale, p.stride_scale, p.box_s, STAGE_N))
+    if (int rc = make_byte_map(&p.tmap_s, a.scale, blocks_k * es, a.N, a.G, p.ld_scale, p.stride_scale, p.box_s, stage_rows))
       return rc;
     if (a.zero)
-      if (int rc = make_byte_map(&p.tmap_z, a.zero, blocks_k, a.N, a.G, p.ld_zero, p.stride_zero, p.box_z, STAGE_N))
+      if (int rc = make_byte_map(&p.tmap_z, a.zero, blocks_k, a.N, a.G, p.ld_zero, p.stride_zero, p.box_z, stage_rows))
         return rc;
   }
   if (p.whole) {
-    if (int rc = make_slab_map(&p.tmap_b, a.B, SLAB / 2, a.N, a.K / SLAB, a.G, a.ldb / 2, a.stride_b / 2, STAGE_N, p.team_warps))
+    if (int rc = make_slab_map(&p.tmap_b, a.B, SLAB / 2, a.N, a.K / SLAB, a.G, a.ldb / 2, a.stride_b / 2, stage_rows, p.across))
       return rc;
   } else {
-    if (int rc = make_byte_map(&p.tmap_b, a.B, a.K / 2, a.N, a.G, a.ldb / 2, a.stride_b / 2, SLAB / 2, STAGE_N)) return rc;
+    if (int rc = make_byte_map(&p.tmap_b, a.B, a.K / 2, a.N, a.G, a.ldb / 2, a.stride_b / 2, SLAB / 2, stage_rows)) return rc;
   }
   const int kind = a.format == TCG_W4_MXF4   ? K_MXF4
                    : a.format == TCG_W4_NVF4 ? K_NVF4
