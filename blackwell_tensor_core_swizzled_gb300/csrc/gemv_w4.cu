@@ -26,7 +26,9 @@
 //                 copy takes its issuing thread 150 cycles; one for every
 //                 warp or row would take longer than the decoding)
 //   two more      add the warps' parts of a tile of two stages in a fixed
-//                 order and store it while the next tile is decoded.
+//                 order and store it while the next tile is decoded;
+//   the last      brings scales and zero points whose rows TMA cannot, since
+//                 they do not start on 16-byte boundaries.
 // The warps cover K side by side; when K is short, the others stand below
 // them and a stage has so many more rows.  Each CTA takes an equal share of
 // the matrix rows.  A K of more slabs than warps is taken in passes over a
@@ -71,19 +73,21 @@ enum Kind4 : int { K_INT4_32 = 0, K_INT4_64 = 1, K_INT4_128 = 2, K_MXF4 = 3, K_N
 constexpr bool is_int4(int k) { return k <= K_INT4_128; }
 constexpr int group_of_kind(int k) { return k == K_NVF4 ? 16 : k == K_MXF4 ? 32 : 32 << k; }
 constexpr int scale_bytes(int k) { return SLAB / group_of_kind(k) * (is_int4(k) ? 2 : 1); }  // of a row's slab
-constexpr int SCALE_BYTES = 6 * 1024, ZERO_BYTES = 4 * 1024;  // room for them in a stage
+// room in a stage for scales, and zero points behind the first 8 KiB: 16 rows
+// for a K of 8000
+constexpr int SCALE_STAGE = 12 * 1024, ZERO_OFF = 8 * 1024;
 constexpr int GRAIN = 2;           // matrix rows: the unit in which the CTAs share them
 
 struct GemvParams {
   // codes as bytes in 128-byte swizzled boxes of a stage's rows: whole slabs
-  // [G][K / 256][N][128], all of a stage in one box (K a multiple of 256), or
-  // rows [G][N][K / 2], one slab a box
-  CUtensorMap tmap_b;
-  int whole;
+  // [G][K / 256][N][128], all that a stage has of them in one box; when K has
+  // a part of a slab more, also rows [G][N][K / 2], one slab a box
+  CUtensorMap tmap_b, tmap_part;
   // scales, zero points as bytes [G][N][bytes of a row] in swizzled boxes of a
   // stage's rows, where their rows are 16-byte aligned (`bulk`)
   CUtensorMap tmap_s, tmap_z;
-  int box_s, box_z;  // bytes of a box's rows: 32, 64 or 128
+  int box_s, box_z;  // bytes of a box's rows: 32, 64 or 128 (not `bulk`: from row to row)
+  int one_run;       // not `bulk`: a stage's rows are copied with what lies between them, not one by one
   int R, N, K, G;
   const uint8_t* A;  // 16-bit elements
   int64_t lda;
@@ -118,19 +122,19 @@ struct Shape {
   static constexpr int TILE_N = 32;                   // matrix rows a warp has of a tile: two stages
   static constexpr int OUT = TOK * TILE_N;            // sums of them
   static constexpr int CAP = (TOK == 16 ? 4096 : 1024) / OUT;  // tiles of a chunk that is passed over more than once
-  static constexpr int STAGES = TOK == 16 ? 6 : 4;    // ring stages
+  static constexpr int STAGES = TOK == 16 ? 5 : 4;    // ring stages
   // buffers of parts: tile i of a chunk uses number i % PARTS, and each adding
   // warp empties one: in every pass the same warp has the tile's sums
   static constexpr int PARTS = 2;
   static constexpr int ADD_WARPS = PARTS;
-  static constexpr int THREADS = 32 * (WARPS + 1 + ADD_WARPS);
+  static constexpr int THREADS = 32 * (WARPS + 1 + ADD_WARPS + 1);
   static constexpr int PART_PITCH = TILE_N + (TOK == 4 ? 8 : 4);  // floats between a part's activation rows
   static constexpr int TILE_PART = TOK * PART_PITCH;  // floats of a warp's part
   // a stage: codes [slab][row][128 bytes]; scales, then zero points [row][pitch]
   // or as boxes
   static constexpr int CODE_BYTES = WARPS * STAGE_N * SLAB / 2;
   static constexpr int SCALES = STAGES * CODE_BYTES;
-  static constexpr int PART = SCALES + STAGES * (SCALE_BYTES + ZERO_BYTES);
+  static constexpr int PART = SCALES + STAGES * SCALE_STAGE;
   // an activation row on its way to each warp's registers
   static constexpr int ACT = PART + PARTS * WARPS * TILE_PART * 4;
   static constexpr int ACT_BYTES = TOK == 4 ? SLAB * 2 : 0;
@@ -143,6 +147,21 @@ struct Shape {
 
 __device__ __forceinline__ void cp_async4(uint32_t dst, const void* src, uint32_t bytes) {
   asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"(dst), "l"(src), "r"(bytes) : "memory");
+}
+// Bytes [src, src + len) of a tensor that starts on a 4-byte boundary to shared
+// memory, as far past the 16-byte boundary dst as src is past one: a bulk copy,
+// and words before and after it.  Returns the bulk copy's bytes.
+__device__ __forceinline__ uint32_t copy_run(uint32_t dst, const uint8_t* src, int len, uint32_t bar) {
+  const int mis = static_cast<int>(reinterpret_cast<uintptr_t>(src)) & 15;
+  src -= mis;
+  len += mis;
+  const int head = mis ? 16 : 0, tail = max(len & ~15, head);
+#pragma unroll 1
+  for (int x = mis & ~3; x < min(head, len); x += 4) cp_async4(dst + x, src + x, min(4, len - x));
+#pragma unroll 1
+  for (int x = tail; x < len; x += 4) cp_async4(dst + x, src + x, min(4, len - x));
+  if (tail > head) bulk_copy(dst + head, src + head, tail - head, bar);
+  return tail - head;
 }
 // Loads by shared-memory address that the compiler may move between waits.
 template <class T>
@@ -388,9 +407,9 @@ __device__ __forceinline__ void load_fragments(const GemvParams& p, const RowBlo
 }
 
 // A row's scales of a slab as words, from a byte offset that may be off a
-// 4-byte boundary (then `shift` bits into its word).
+// 4-byte boundary, and followed by another row's after `left` bytes.
 template <int W>
-__device__ __forceinline__ void scale_words(const uint8_t* at, bool aligned, uint32_t (&w)[W]) {
+__device__ __forceinline__ void scale_words(const uint8_t* at, bool aligned, int left, uint32_t (&w)[W]) {
   if (aligned) {
     if constexpr (W == 4) {
       const uint4 v = lds<uint4>(at, 0);
@@ -415,15 +434,20 @@ __device__ __forceinline__ void scale_words(const uint8_t* at, bool aligned, uin
       w[i] = __funnelshift_r(lo, hi, 8 * off);
       lo = hi;
     }
+    if (left < 4 * W) {
+#pragma unroll
+      for (int i = 0; i < W; ++i)
+        w[i] &= left >= 4 * i + 4 ? ~0u : left > 4 * i ? (1u << (8 * (left - 4 * i))) - 1u : 0u;
+    }
   }
 }
 
 // 16 rows of a tile and a slab: acc[nt] = (codes . activations) * scales.
 // `codes` is the first of the rows' 128-byte lines; s0, s1 (z0, z1) the slab's
-// scales (zero points) of rows g and g + 8.
+// scales (zero points) of rows g and g + 8, of which `left` bytes are K's.
 template <int KIND, bool BF16, int TOK, int NT = Shape<TOK>::NT>
 __device__ __forceinline__ void rows16(const uint8_t* codes, const uint8_t* s0, const uint8_t* s1, const uint8_t* z0,
-                                       const uint8_t* z1, bool aligned, int lane, const uint32_t (&frag)[8][NT][4],
+                                       const uint8_t* z1, bool aligned, int left, int lane, const uint32_t (&frag)[8][NT][4],
                                        const float (&undo)[NT][2], float (&acc)[NT][4]) {
   constexpr int STEP = Shape<TOK>::STEP;
   constexpr int W = scale_bytes(KIND) / 4;
@@ -431,8 +455,8 @@ __device__ __forceinline__ void rows16(const uint8_t* codes, const uint8_t* s0, 
   // row g's chunk ch (32 of K, 16 bytes) lies at chunk ch ^ (g & 7)
   const uint32_t code = 144u * g + 4u * c;
   uint32_t w0[W], w1[W];
-  scale_words<W>(s0, aligned, w0);
-  scale_words<W>(s1, aligned, w1);
+  scale_words<W>(s0, aligned, left, w0);
+  scale_words<W>(s1, aligned, left, w1);
   if constexpr (KIND == K_NVF4) {
     // unsigned E4M3: a byte with the top bit set is NaN (0xFF)
     if ((w0[0] | w0[1] | w0[2] | w0[3] | w1[0] | w1[1] | w1[2] | w1[3]) & 0x80808080u) {
@@ -609,7 +633,7 @@ __global__ void __launch_bounds__(Shape<TOK>::THREADS, 1) gemv_kernel(const __gr
   const int active = p.across * p.down;  // decoding warps at work
   if (threadIdx.x == 0) {
     for (int i = 0; i < STAGES; ++i) {
-      mbar_init(full + 8 * i, p.bulk ? 1 : 33);  // the copies' bytes, and each lane's that copies words
+      mbar_init(full + 8 * i, p.bulk ? 1 : 34);  // the copies' bytes, twice; each lane's that copies words
       mbar_init(empty + 8 * i, active);
     }
     for (int i = 0; i < PARTS; ++i) {
@@ -617,7 +641,6 @@ __global__ void __launch_bounds__(Shape<TOK>::THREADS, 1) gemv_kernel(const __gr
       mbar_init(part_free + 8 * i, 1);
     }
     *abort_word = 0u;
-    prefetch_tmap(&p.tmap_b);
     fence_mbarrier_init();
   }
   __syncthreads();
@@ -706,13 +729,13 @@ __global__ void __launch_bounds__(Shape<TOK>::THREADS, 1) gemv_kernel(const __gr
   constexpr int SB = scale_bytes(KIND), ZB = SLAB / group_of_kind(KIND);  // a row's scales, zero points of a slab
   constexpr int ES = is_int4(KIND) ? 2 : 1;
   const int stage_rows = STAGE_N * p.down;
-  // bytes of a stage's scales, zero points: whole boxes, or rows with a word to spare
+  // bytes of a stage's rows of scales, zero points
   const int want_s = p.across * SB, want_z = p.across * ZB;
-  const int pitch_s = want_s + 4, pitch_z = (want_z + 3) / 4 * 4 + 4;
-  const uint32_t scales = S::SCALES, zeros = S::SCALES + STAGES * SCALE_BYTES;
   const bool has_zero = is_int4(KIND) && p.zero;
-  if (warp == WARPS) {
+  if (warp == WARPS || warp == WARPS + 1 + ADD_WARPS) {
     // -------------------------------------------------------------- feeding
+    const bool copies = warp != WARPS;  // scales and zero points that TMA cannot bring
+    if (copies && p.bulk) return;
     int group = 0, block = -1;
     uint32_t stage = 0, ph = 1;
     const uint32_t box = stage_rows * (SLAB / 2);  // a slab's codes
@@ -724,45 +747,46 @@ __global__ void __launch_bounds__(Shape<TOK>::THREADS, 1) gemv_kernel(const __gr
         group = p.G == 1 ? 0 : row_block<TOK>(p, seg, pre, false, span, block).g;
       }
       const int first = cu.pass * p.across;  // slab
+      const bool part = p.K % SLAB && cu.pass == passes - 1;
 #pragma unroll 1
       for (int h = 0; h < cu.rows; h += stage_rows) {
         const int n0 = cu.n0 + h;
         const uint32_t bar = full + 8 * stage, codes = base + stage * S::CODE_BYTES;
-        const uint32_t sdst = base + scales + stage * SCALE_BYTES, zdst = base + zeros + stage * ZERO_BYTES;
+        const uint32_t sdst = base + S::SCALES + stage * SCALE_STAGE, zdst = sdst + ZERO_OFF;
         ok = wait_uniform(empty + 8 * stage, ph, wctx, SITE_PROD_EMPTY);  // the stage's last readers
         if (!ok) break;
-        if (elect_one()) {
-          mbar_arrive_expect_tx(bar, bytes);
-          if (p.whole) tma_load_4d(codes, &p.tmap_b, 0, n0, first, group, bar);
-          if (p.bulk) {
-            for (int x = 0; x < want_s; x += p.box_s)
-              tma_load3<1>(sdst + stage_rows * x, &p.tmap_s, first * SB + x, n0, group, bar);
-            if (has_zero) tma_load3<1>(zdst, &p.tmap_z, first * ZB, n0, group, bar);
-          }
-        }
-        __syncwarp();
-        if (!p.whole && lane < p.across)  // a slab a lane, zeros beyond K
-          tma_load3<1>(codes + lane * box, &p.tmap_b, (first + lane) * (SLAB / 2), n0, group, bar);
-        if (!p.bulk) {
-          const int rows = min(stage_rows, cu.rows - h);
-          // 4-byte words from the boundary below each row's start; what lies
-          // past the row's end is zero.  Neighbouring lanes take a row's words.
-          auto words = [&](uint32_t dst, int pitch, const uint8_t* at, int64_t ld, int want, int left) {
-            const int n = (want + 6) / 4;  // words of a row that starts 3 bytes past a boundary
-#pragma unroll 1
-            for (int i = lane; i < rows * n; i += 32) {
-              const int r = i / n, x = 4 * (i - r * n);
-              const uint8_t* row = at + r * ld;
-              const int mis = static_cast<int>(reinterpret_cast<uintptr_t>(row)) & 3;
-              if (x < want + mis)
-                cp_async4(dst + r * pitch + x, x < left + mis ? row - mis + x : p.scale, max(0, min(4, left + mis - x)));
+        if (!copies) {
+          if (elect_one()) {
+            mbar_arrive_expect_tx(bar, bytes);
+            // (a part of a slab goes with the whole ones before it when K is one
+            // pass; the last of several passes takes slab by slab, below)
+            if (!part || (passes == 1 && p.slabs > 1)) tma_load_4d(codes, &p.tmap_b, 0, n0, first, group, bar);
+            if (part && passes == 1)
+              tma_load3<1>(codes + (p.slabs - 1) * box, &p.tmap_part, (p.slabs - 1) * (SLAB / 2), n0, group, bar);
+            if (p.bulk) {
+              for (int x = 0; x < want_s; x += p.box_s)
+                tma_load3<1>(sdst + stage_rows * x, &p.tmap_s, first * SB + x, n0, group, bar);
+              if (has_zero) tma_load3<1>(zdst, &p.tmap_z, first * ZB, n0, group, bar);
             }
+          }
+          __syncwarp();
+          if (part && passes > 1 && lane < p.across)  // zeros beyond K
+            tma_load3<1>(codes + lane * box, &p.tmap_part, (first + lane) * (SLAB / 2), n0, group, bar);
+        } else {
+          const int rows = min(stage_rows, cu.rows - h), runs = p.one_run ? 1 : rows;
+          auto copy = [&](uint32_t dst, int pitch, const uint8_t* at, int64_t ld, int len) {
+            if (p.one_run) len += (rows - 1) * pitch;
+            uint32_t bulk_bytes = 0;
+            for (int i = lane; i < runs; i += 32) bulk_bytes += copy_run(dst + i * pitch, at + i * ld, len, bar);
+            return bulk_bytes;
           };
-          words(sdst, pitch_s, p.scale + group * p.stride_scale + n0 * p.ld_scale + first * SB, p.ld_scale, want_s,
-                p.scale_row * ES - first * SB);
+          uint32_t sent = copy(sdst, p.box_s, p.scale + group * p.stride_scale + n0 * p.ld_scale + first * SB, p.ld_scale,
+                               min(want_s, p.scale_row * ES - first * SB));
           if (has_zero)
-            words(zdst, pitch_z, p.zero + group * p.stride_zero + n0 * p.ld_zero + first * ZB, p.ld_zero, want_z,
-                  p.scale_row - first * ZB);
+            sent += copy(zdst, p.box_z, p.zero + group * p.stride_zero + n0 * p.ld_zero + first * ZB, p.ld_zero,
+                         min(want_z, p.scale_row - first * ZB));
+          sent = __reduce_add_sync(0xffffffffu, sent);
+          if (lane == 0) mbar_arrive_expect_tx(bar, sent);
           asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(bar) : "memory");
         }
         if (++stage == STAGES) {
@@ -789,18 +813,16 @@ __global__ void __launch_bounds__(Shape<TOK>::THREADS, 1) gemv_kernel(const __gr
     int have_block = -1, have_pass = -1, group = 0;  // whose fragments are loaded
     uint32_t stage = 0, ph = 0, buf = 0, buf_ph = ~0u;  // buf_ph: a parity bit per buffer
     const uint8_t* codes0 = smem + (wk * stage_rows + STAGE_N * below) * (SLAB / 2);
-    const uint8_t *scales0 = smem + scales, *zeros0 = smem + zeros;
-    int to_s1 = 8 * pitch_s, to_z1 = 8 * pitch_z;  // from row g to row g + 8
+    const uint8_t *scales0 = smem + S::SCALES, *zeros0 = scales0 + ZERO_OFF;
+    const int to_s1 = 8 * p.box_s, to_z1 = 8 * p.box_z;  // from row g to row g + 8
     if (p.bulk) {
       // 128 bytes of a row to a box; a box's rows 8 apart are swizzled alike
       const uint32_t x = wk * SB;
       scales0 += (x >> 7) * (stage_rows * 128) + box_at(row, x & 127u, p.box_s);
       zeros0 += box_at(row, wk * ZB, p.box_z);
-      to_s1 = 8 * p.box_s;
-      to_z1 = 8 * p.box_z;
     } else {
-      scales0 += row * pitch_s + wk * SB;
-      zeros0 += row * pitch_z + wk * ZB;
+      scales0 += row * p.box_s + wk * SB;
+      zeros0 += row * p.box_z + wk * ZB;
     }
     float* part0 = reinterpret_cast<float*>(smem + S::PART) + warp * S::TILE_PART +
                    (TOK == 4 ? c : 2 * c) * S::PART_PITCH + g;
@@ -820,27 +842,31 @@ __global__ void __launch_bounds__(Shape<TOK>::THREADS, 1) gemv_kernel(const __gr
         if (!ok) break;
         float acc[NT][4] = {};
         if (slab < p.slabs && h + STAGE_N * below < cu.rows) {
-          const uint8_t *s0 = scales0 + stage * SCALE_BYTES, *s1 = s0 + to_s1;
+          const uint8_t *s0 = scales0 + stage * SCALE_STAGE, *s1 = s0 + to_s1;
           const uint8_t *z0 = nullptr, *z1 = nullptr;
           if (has_zero) {
-            z0 = zeros0 + stage * ZERO_BYTES;
+            z0 = zeros0 + stage * SCALE_STAGE;
             z1 = z0 + to_z1;
           }
           if (!p.bulk) {
-            // each row starts as far past a 4-byte boundary as it does in memory
-            const uint32_t first = static_cast<uint32_t>(cu.pass * p.across);
-            const uint32_t ld_s = static_cast<uint32_t>(p.ld_scale), ra = static_cast<uint32_t>(cu.n0 + h + row);
-            const uint32_t at = static_cast<uint32_t>(group) * static_cast<uint32_t>(p.stride_scale) + first * SB + ra * ld_s;
-            s0 += at & 3u;
-            s1 += (at + 8u * ld_s) & 3u;
+            // each row, or the stage, starts as far past a 16-byte boundary as in memory
+            const uint32_t first = static_cast<uint32_t>(cu.pass * p.across), n0 = static_cast<uint32_t>(cu.n0 + h);
+            const uint32_t below_s = p.one_run ? 0 : static_cast<uint32_t>(p.ld_scale);
+            const uint32_t at = static_cast<uint32_t>(reinterpret_cast<uintptr_t>(p.scale)) + first * SB +
+                                n0 * static_cast<uint32_t>(p.ld_scale) + row * below_s +
+                                static_cast<uint32_t>(group) * static_cast<uint32_t>(p.stride_scale);
+            s0 += at & 15u;
+            s1 += (at + 8u * below_s) & 15u;
             if (has_zero) {
-              const uint32_t ld_z = static_cast<uint32_t>(p.ld_zero);
-              const uint32_t zat = static_cast<uint32_t>(group) * static_cast<uint32_t>(p.stride_zero) + first * ZB + ra * ld_z;
-              z0 += zat & 3u;
-              z1 += (zat + 8u * ld_z) & 3u;
+              const uint32_t below_z = p.one_run ? 0 : static_cast<uint32_t>(p.ld_zero);
+              const uint32_t zat = static_cast<uint32_t>(reinterpret_cast<uintptr_t>(p.zero)) + first * ZB +
+                                   n0 * static_cast<uint32_t>(p.ld_zero) + row * below_z +
+                                   static_cast<uint32_t>(group) * static_cast<uint32_t>(p.stride_zero);
+              z0 += zat & 15u;
+              z1 += (zat + 8u * below_z) & 15u;
             }
           }
-          rows16<KIND, BF16, TOK>(codes0 + stage * S::CODE_BYTES, s0, s1, z0, z1, p.bulk, lane, frag, undo, acc);
+          rows16<KIND, BF16, TOK>(codes0 + stage * S::CODE_BYTES, s0, s1, z0, z1, p.bulk, p.scale_row * ES - slab * SB, lane, frag, undo, acc);
         }
         __syncwarp();
         if (lane == 0) mbar_arrive(empty + 8 * stage);
@@ -1083,11 +1109,26 @@ int run_gemv(const tcg_gemv_w4_args* args, cudaStream_t s) {
   const int64_t blocks = std::max(active, (a.R + tok - 1) / tok);
   const int64_t wanted = (blocks * a.N / device_sms(dev) + STAGE_N - 1) / STAGE_N;
   p.down = static_cast<int>(std::max<int64_t>(1, std::min<int64_t>(warps / p.across, wanted)));
-  p.whole = a.K % SLAB == 0;
   const auto box = [](int bytes) { return bytes <= 32 ? 32 : bytes <= 64 ? 64 : 128; };
-  p.box_s = box(p.across * (SLAB / a.group) * es);
-  p.box_z = box(p.across * (SLAB / a.group));
-  if (p.bulk) p.down = std::min(p.down, std::min(SCALE_BYTES / (STAGE_N * p.box_s), ZERO_BYTES / (STAGE_N * p.box_z)));
+  const auto pitch = [](int bytes) { return 16 * ((bytes + 30) / 16 | 1); };  // 16 bytes to spare; rows on different banks
+  const int want_z = p.across * (SLAB / a.group), want_s = want_z * es;
+  const int64_t room_s = a.zero ? ZERO_OFF : SCALE_STAGE, room_z = a.zero ? SCALE_STAGE - ZERO_OFF : INT64_MAX;
+  // (up to 15 bytes before a run, and a word read past it)
+  const auto fits = [&](int64_t row_s, int64_t row_z) {
+    return STAGE_N * p.down * row_s + 19 <= room_s && STAGE_N * p.down * row_z + 19 <= room_z;
+  };
+  const int down = p.down;
+  p.one_run = 0;
+  if (!p.bulk) {
+    while (p.down > 1 && !fits(p.ld_scale, p.ld_zero)) --p.down;
+    p.one_run = fits(p.ld_scale, p.ld_zero);
+  }
+  p.box_s = p.bulk ? box(want_s) : p.one_run ? static_cast<int>(p.ld_scale) : pitch(want_s);
+  p.box_z = p.bulk ? box(want_z) : p.one_run ? static_cast<int>(p.ld_zero) : pitch(want_z);
+  if (!p.one_run) {
+    p.down = down;
+    while (p.down > 1 && !fits(p.box_s, p.box_z)) --p.down;
+  }
   p.tile_rows = 2 * STAGE_N * p.down;
   const int stage_rows = STAGE_N * p.down;
   if (p.bulk) {
@@ -1097,12 +1138,15 @@ int run_gemv(const tcg_gemv_w4_args* args, cudaStream_t s) {
       if (int rc = make_byte_map(&p.tmap_z, a.zero, blocks_k, a.N, a.G, p.ld_zero, p.stride_zero, p.box_z, stage_rows))
         return rc;
   }
-  if (p.whole) {
-    if (int rc = make_slab_map(&p.tmap_b, a.B, SLAB / 2, a.N, a.K / SLAB, a.G, a.ldb / 2, a.stride_b / 2, stage_rows, p.across))
+  const bool part = a.K % SLAB != 0;
+  if (a.K >= SLAB) {
+    const int slabs = part && p.slabs == p.across ? p.across - 1 : p.across;
+    if (int rc = make_slab_map(&p.tmap_b, a.B, SLAB / 2, a.N, a.K / SLAB, a.G, a.ldb / 2, a.stride_b / 2, stage_rows, slabs))
       return rc;
-  } else {
-    if (int rc = make_byte_map(&p.tmap_b, a.B, a.K / 2, a.N, a.G, a.ldb / 2, a.stride_b / 2, SLAB / 2, stage_rows)) return rc;
   }
+  if (part)
+    if (int rc = make_byte_map(&p.tmap_part, a.B, a.K / 2, a.N, a.G, a.ldb / 2, a.stride_b / 2, SLAB / 2, stage_rows))
+      return rc;
   const int kind = a.format == TCG_W4_MXF4   ? K_MXF4
                    : a.format == TCG_W4_NVF4 ? K_NVF4
                    : a.group == 32           ? K_INT4_32

@@ -181,6 +181,13 @@ __device__ __forceinline__ void tma_load_4d(uint32_t dst, const void* map, int32
       : "memory");
 }
 
+// Untiled: `bytes` (a multiple of 16) between 16-byte boundaries.
+__device__ __forceinline__ void bulk_copy(uint32_t dst, const void* src, uint32_t bytes, uint32_t bar) {
+  asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(dst),
+               "l"(src), "r"(bytes), "r"(bar)
+               : "memory");
+}
+
 // Tile load global -> shared of every CTA in `mask` (cluster ranks): the
 // tile lands at the same CTA-relative address `dst` in each, and each
 // destination's mbarrier at offset `bar` receives its bytes.

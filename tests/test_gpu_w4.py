@@ -233,3 +233,27 @@ def test_no_contraction_and_graph(tcg):
     graph.replay()
     torch.cuda.synchronize()
     assert torch.equal(D, want)
+
+
+@pytest.mark.parametrize("fmt,group,zeros", FORMATS)
+@pytest.mark.parametrize("K", [384, 2048, 4224])
+def test_scales_off_a_boundary(tcg, fmt, group, zeros, K):
+    """Scales and zero points may start on any 4-byte boundary; the answers are
+    those of the same bytes elsewhere, to the bit."""
+    G, N, R = 2, 70, 5
+    A, _ = rows((R, K), "bf16", 3, 8)
+    off = torch.from_numpy(group_offsets([2, 3])).cuda()
+    B, scale, zero, _ = matrices(fmt, G, N, K, group, zeros, "bf16", K)
+    want = run(tcg, fmt, "bf16", "f32", A, K, N, off, group, B, scale, zero, G)
+
+    def moved(t, by):
+        if t is None:
+            return None
+        flat = t.contiguous().view(torch.uint8).flatten()
+        room = torch.full((flat.numel() + 64,), 0xFF, dtype=torch.uint8, device="cuda")
+        room[by:by + flat.numel()] = flat
+        return room[by:by + flat.numel()].view(t.dtype)
+
+    for by in (4, 8, 12, 16):
+        got = run(tcg, fmt, "bf16", "f32", A, K, N, off, group, B, moved(scale, by), moved(zero, by), G)
+        assert np.array_equal(got, want), by
