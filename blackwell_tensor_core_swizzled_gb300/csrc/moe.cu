@@ -209,9 +209,8 @@ __global__ void __launch_bounds__(32 * SORT_WARPS) sort_kernel(int n, int E, con
 // All three walk the tokens, so that a token's own row moves once and its
 // topk sorted rows once each; what bounds them is those bytes.  A thread takes
 // a pack of a row at a time (16 bytes where bases and rows allow, else one
-// element) and has 8 loads in flight.  16384 tokens of 4096 bf16 and 4 choices:
-// dispatch 100 us (6.7 TB/s, the rate of a plain copy), combine 136 us (4.9
-// TB/s; 8 choices 5.8 TB/s; a row's loads one after the other gave 2.2).
+// element).  16384 tokens of 4096 bf16 and 4 choices: dispatch 100 us, combine
+// 101 us (6.7 TB/s both, the rate of a plain copy).
 
 template <class T, bool WIDE>
 struct Pack {
@@ -236,7 +235,6 @@ struct Pack {
 constexpr int MOVE_THREADS = 256;
 constexpr int COMBINE_THREADS = 128;
 constexpr int GRAD_THREADS = 128;
-constexpr int AHEAD = 8;      // combine: rows of a token in flight
 constexpr int GRAD_ROWS = 2;  // its gradient: choices at a time
 
 // Sorted row of a position, and whether the entry is kept; positions outside
@@ -280,8 +278,8 @@ __global__ void __launch_bounds__(MOVE_THREADS) dispatch_kernel(int topk, int64_
   }
 }
 
-// ROWS choices at a time of PACKS packs: 8 loads in flight a thread.
-template <class T, bool WIDE, int ROWS>
+// ROWS choices at a time of PACKS packs.
+template <class T, bool WIDE, int ROWS, int PACKS>
 __global__ void __launch_bounds__(COMBINE_THREADS) combine_kernel(int topk, int64_t rows, int64_t H,
                                                                const T* __restrict__ Ys, int64_t ldys,
                                                                const int32_t* __restrict__ position,
@@ -293,7 +291,6 @@ __global__ void __launch_bounds__(COMBINE_THREADS) combine_kernel(int topk, int6
   const int64_t t = blockIdx.x;
   const int32_t* pos = position + t * topk;
   const float* wt = weight ? weight + t * topk : nullptr;
-  constexpr int PACKS = AHEAD / ROWS;
   constexpr int64_t STRIDE = static_cast<int64_t>(COMBINE_THREADS) * P::N;  // between a thread's packs
   const int64_t step = static_cast<int64_t>(gridDim.y) * STRIDE * PACKS;
   for (int64_t h = blockIdx.y * STRIDE * PACKS + static_cast<int64_t>(threadIdx.x) * P::N; h < H; h += step) {
@@ -552,11 +549,11 @@ int run_combine(tcg_dtype type, int64_t T, int topk, int64_t H, const void* Ys, 
   return for_type(type, wide, [&](auto z, auto w) {
     using E = decltype(z);
     constexpr bool W = decltype(w)::value;
-    // choices at a time: as many as there are, up to 8; one pack each where
-    // the row is split over blocks already
-    const auto kernel = topk > 4 || parts > 1 ? combine_kernel<E, W, 8>
-                        : topk > 2            ? combine_kernel<E, W, 4>
-                                              : combine_kernel<E, W, 2>;
+    // Few tokens want their rows' latencies side by side (64 tokens x 8 x 4096
+    // bf16 2.2 us, 3.1 two by two).  With more, two choices keep the rows that
+    // are read together few: 16384 x 4 101 us, 139 four by four, 169 eight;
+    // 2432 x 8 32 us, 35 eight; 1216 x 8 19 either way.
+    const auto kernel = topk > 4 && parts > 1 ? combine_kernel<E, W, 8, 1> : combine_kernel<E, W, 2, 2>;
     return launch(kernel, dim3(static_cast<unsigned>(T), parts), COMBINE_THREADS, 0, 1, s, topk, T * topk, H,
                   static_cast<const E*>(Ys), ldys, position, weight, static_cast<E*>(Y), ldy);
   });
