@@ -36,6 +36,13 @@
 // its registers (rounded), while the next is computed.  16-bit outputs round
 // far more than that and take the whole contraction in one accumulator.
 //
+// What bounds it: many rows a group, the tensor cores (65536 rows x 2048 x
+// 4096 in 32 groups: 625 to 670 us with the clock, 1.64 to 1.76 PFLOP/s); few,
+// the matrices' bytes from HBM (96 us for 537 MB: 5.6 TB/s); the matrices'
+// gradient in fp32, the way between L2 and the SMs, which the operands' tiles
+// and the output share (295 to 350 us; 175 without the stores, 169 for the
+// stores alone).
+//
 // The structure is the dense kernel's: a persistent CTA (or pair) per SM, a
 // TMA producer warp, an MMA warp, two accumulators in TMEM, epilogue warps.
 // The tile list depends on offsets, which only the device knows, so each CTA
@@ -65,8 +72,12 @@ constexpr int64_t MAX_EXTENT = int64_t{1} << 30;
 constexpr int EPI_WARPS = 8;
 constexpr int STAGING_BYTES = 2048;
 constexpr int GROUPED_THREADS = 32 * (4 + EPI_WARPS);
-constexpr int CHAIN = 8;  // fp32 outputs: blocks of the contraction summed by the tensor core
-constexpr int BAND = 8;  // column tiles of a group that sweep its row tiles together
+// fp32 outputs: blocks of the contraction summed by the tensor core (16384 x
+// 2048 x 4096 in 32 groups: 8 blocks 233 us, 4 299, 16 229, all 226)
+constexpr int CHAIN = 8;
+// column tiles of a group that sweep its row tiles together (1, 4, 8 and 16
+// are within 4 % of each other at 32 groups of 2048 x 4096)
+constexpr int BAND = 8;
 
 struct GroupedParams {
   CUtensorMap tmap_p;    // [G or 1][rows][64-element boxes]
@@ -661,7 +672,9 @@ Variant variant() {
           BN};
 }
 
-// CTA pairs; more than 224 groups' tile counts take a ring stage's memory.
+// CTA pairs; more than 224 groups' tile counts take a ring stage's memory (32
+// groups of 2048 x 4096, 16384 rows: fp32 matrices' gradient 351 us with six
+// stages, 357 with five; rows' gradient 238 and 245).
 Variant pair_variant(int G) { return G <= 224 ? variant<2, 256, 6, 224>() : variant<2, 256, 5, MAX_GROUPS>(); }
 
 int check_problem(tcg_input in_type, int64_t R, int64_t N, int64_t K, int G, tcg_dtype d_type) {
@@ -752,6 +765,10 @@ int run_grouped(tcg_input in_type, int64_t R, int64_t N, int64_t K, int G, const
   int dev;
   if (int rc = current_device_checked(&dev)) return rc;
   const bool bf16 = in_type == TCG_IN_BF16;
+  // Few rows a group stream the matrices: CTAs of 128 x 64 are then quicker
+  // than pairs of 256 x 256, which win once a group takes two narrow tiles (32
+  // groups of 2048 x 4096: 16 rows a group 96 us and 104, 64 103 and 106, 80
+  // 133 and 108, 128 168 and 112).
   const bool wide = R > 64 * static_cast<int64_t>(G);
   const Variant v = wide ? pair_variant(G) : variant<1, 64, 7, MAX_GROUPS>();
   const int cg = v.ki.cta_group;
