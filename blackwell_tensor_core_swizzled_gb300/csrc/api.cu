@@ -860,68 +860,6 @@ unsigned long long* device_error_word(int dev) {
   return st ? st->err : nullptr;
 }
 
-int device_sms(int dev) { return device_state(dev)->sms; }
-
-int max_resident_clusters(int dev, const KernelInfo& ki, int* out) {
-  return max_clusters_for(device_state(dev), ki, out);
-}
-
-namespace {
-
-// Tiled map swizzled over `span` bytes (128, 64 or 32), encoded on every call
-int encode_tiled(CUtensorMap* map, CUtensorMapDataType dt, int rank, const void* base, const cuuint64_t* dims,
-                 const cuuint64_t* strides, const cuuint32_t* box, uint32_t span = 128) {
-  if (encode_ready() != TCG_OK) {
-    t_last_error = "cuTensorMapEncodeTiled entry point unavailable";
-    return TCG_ERR_CUDA;
-  }
-  const cuuint32_t estr[4] = {1, 1, 1, 1};
-  const CUresult r = g_encode(map, dt, static_cast<cuuint32_t>(rank), const_cast<void*>(base), dims, strides, box, estr,
-                              CU_TENSOR_MAP_INTERLEAVE_NONE,
-                              span == 128  ? CU_TENSOR_MAP_SWIZZLE_128B
-                              : span == 64 ? CU_TENSOR_MAP_SWIZZLE_64B
-                                           : CU_TENSOR_MAP_SWIZZLE_32B,
-                              CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
-  if (r != CUDA_SUCCESS) {
-    t_last_error = "cuTensorMapEncodeTiled (rank " + std::to_string(rank) + ") failed (" +
-                   std::to_string(static_cast<int>(r)) + ")";
-    return TCG_ERR_CUDA;
-  }
-  return TCG_OK;
-}
-
-}  // namespace
-
-int make_operand_map(CUtensorMap* map, const void* base, bool bf16, uint64_t inner, uint64_t mid, uint64_t outer,
-                     uint64_t stride_mid, uint64_t stride_outer, uint32_t box_mid) {
-  const cuuint64_t dims[3] = {inner, mid, outer}, strides[2] = {2 * stride_mid, 2 * stride_outer};
-  const cuuint32_t box[3] = {64, box_mid, 1};
-  return encode_tiled(map, bf16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16, outer ? 3 : 2,
-                      base, dims, strides, box);
-}
-
-int make_byte_map(CUtensorMap* map, const void* base, uint64_t inner, uint64_t mid, uint64_t outer,
-                  uint64_t stride_mid, uint64_t stride_outer, uint32_t box_inner, uint32_t box_mid) {
-  const cuuint64_t dims[3] = {inner, mid, outer}, strides[2] = {stride_mid, stride_outer};
-  const cuuint32_t box[3] = {box_inner, box_mid, 1};
-  return encode_tiled(map, CU_TENSOR_MAP_DATA_TYPE_UINT8, 3, base, dims, strides, box, box_inner);
-}
-
-int make_store_map(CUtensorMap* map, const void* base, bool bf16, uint64_t inner, uint64_t mid, uint64_t outer,
-                   uint64_t stride_mid, uint64_t stride_outer) {
-  const cuuint64_t dims[3] = {inner, mid, outer}, strides[2] = {2 * stride_mid, 2 * stride_outer};
-  const cuuint32_t box[3] = {32, 32, 1};
-  return encode_tiled(map, bf16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16, 3, base, dims,
-                      strides, box, 64);
-}
-
-int make_slab_map(CUtensorMap* map, const void* base, uint64_t inner, uint64_t mid, uint64_t slabs, uint64_t outer,
-                  uint64_t stride_mid, uint64_t stride_outer, uint32_t box_mid, uint32_t box_slabs) {
-  const cuuint64_t dims[4] = {inner, mid, slabs, outer}, strides[3] = {stride_mid, inner, stride_outer};
-  const cuuint32_t box[4] = {static_cast<cuuint32_t>(inner), box_mid, box_slabs, 1};
-  return encode_tiled(map, CU_TENSOR_MAP_DATA_TYPE_UINT8, 4, base, dims, strides, box);
-}
-
 uint64_t wait_timeout_ns() {
   load_timeout_env();
   return g_timeout_ns.load();

@@ -61,6 +61,7 @@
 #include "desc.cuh"
 #include "gemm_kernel.cuh"
 #include "ptx.cuh"
+#include "ptx_moe.cuh"
 #include "tmem_ldst.cuh"
 
 namespace tcg {

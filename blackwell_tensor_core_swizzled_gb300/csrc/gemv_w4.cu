@@ -60,6 +60,7 @@
 #include "common.h"
 #include "gemm_kernel.cuh"
 #include "ptx.cuh"
+#include "ptx_moe.cuh"
 
 namespace tcg {
 

@@ -140,7 +140,7 @@ class MoeDecoder:
         return route.combine(self.product(route, torch.nn.functional.silu(h), self.w2), weight)
 
 
-def microseconds(f, n: int = 20) -> float:
+def microseconds(f, n: int) -> float:
     for _ in range(3):
         f()
     start, end = torch.cuda.Event(enable_timing=True), torch.cuda.Event(enable_timing=True)
@@ -155,7 +155,8 @@ def microseconds(f, n: int = 20) -> float:
 
 def main() -> None:
     ap = argparse.ArgumentParser(description=__doc__, formatter_class=argparse.RawDescriptionHelpFormatter)
-    for name, value in (("tokens", 4096), ("hidden", 2048), ("inner", 1024), ("experts", 32), ("topk", 4), ("batch", 8)):
+    for name, value in (("tokens", 4096), ("hidden", 2048), ("inner", 1024), ("experts", 32), ("topk", 4), ("batch", 8),
+                        ("repeat", 20)):
         ap.add_argument("--" + name, type=int, default=value)
     o = ap.parse_args()
     torch.manual_seed(0)
@@ -165,14 +166,14 @@ def main() -> None:
     x, dy = draw(o.tokens, o.hidden) * o.hidden ** 0.5, draw(o.tokens, o.hidden)
     expert, weight = layer.choose(x)
     kept = layer.forward(x, expert, weight)[1]
-    print(f"forward  {o.tokens} tokens: {microseconds(lambda: layer.forward(x, expert, weight)):.0f} us")
-    print(f"backward {o.tokens} tokens: {microseconds(lambda: layer.backward(dy, kept)):.0f} us")
+    print(f"forward  {o.tokens} tokens: {microseconds(lambda: layer.forward(x, expert, weight), o.repeat):.0f} us")
+    print(f"backward {o.tokens} tokens: {microseconds(lambda: layer.backward(dy, kept), o.repeat):.0f} us")
     decoder, few = MoeDecoder(layer), slice(0, o.batch)
     y16, _ = layer.forward(x[few], expert[few], weight[few])
     y4 = decoder.forward(x[few], expert[few], weight[few])
     off = ((y4 - y16).float().norm() / y16.float().norm()).item()
     print(f"decoding {o.batch} tokens with 4-bit experts: "
-          f"{microseconds(lambda: decoder.forward(x[few], expert[few], weight[few])):.0f} us, "
+          f"{microseconds(lambda: decoder.forward(x[few], expert[few], weight[few]), o.repeat):.0f} us, "
           f"{100 * off:.1f} % from the 16-bit layer")
     rc = tcg.check()
     if rc:
