@@ -145,19 +145,26 @@ class TcgError(RuntimeError):
 
 
 def _ptr(x) -> int | None:
-    if x is None:
-        return None
-    if isinstance(x, int):
-        return x
-    return x.data_ptr()
+    try:
+        return x.data_ptr()
+    except AttributeError:
+        if x is None or isinstance(x, int):
+            return x
+        raise
+
+
+_current = None  # torch's raw handle of a device's current stream, and its current device
 
 
 def _stream(s) -> int | None:
     if s is None:
         # the raw handle: torch.cuda.current_stream() builds a Stream object,
         # 3 us of a small call on the Grace host against 0.2 us
-        import torch
-        return torch._C._cuda_getCurrentRawStream(torch._C._cuda_getDevice())
+        global _current
+        if _current is None:
+            import torch
+            _current = torch._C._cuda_getCurrentRawStream, torch._C._cuda_getDevice
+        return _current[0](_current[1]())
     if isinstance(s, int):
         return s
     return s.cuda_stream
