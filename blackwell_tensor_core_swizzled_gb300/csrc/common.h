@@ -82,9 +82,9 @@ int make_operand_map(CUtensorMap* map, const void* base, bool bf16, uint64_t inn
 // the swizzle's span) x box_mid x 1.
 int make_byte_map(CUtensorMap* map, const void* base, uint64_t inner, uint64_t mid, uint64_t outer,
                   uint64_t stride_mid, uint64_t stride_outer, uint32_t box_inner, uint32_t box_mid);
-// A 16-bit output [outer][mid][inner] (strides in elements) in store boxes of
-// 32 elements by 32 rows, 64-byte swizzled.
-int make_store_map(CUtensorMap* map, const void* base, bool bf16, uint64_t inner, uint64_t mid, uint64_t outer,
+// An output [outer][mid][inner] (strides in elements) in store boxes of 32
+// elements by 32 rows, 64-byte swizzled, or, fp32, by 16 rows, as they are.
+int make_store_map(CUtensorMap* map, const void* base, tcg_dtype type, uint64_t inner, uint64_t mid, uint64_t outer,
                    uint64_t stride_mid, uint64_t stride_outer);
 // Bytes of [outer][mid][slabs * inner] seen as [outer][slabs][mid][inner], boxes
 // of inner x box_mid x box_slabs x 1.

@@ -72,6 +72,7 @@ constexpr int MAX_GROUPS = 1024;
 constexpr int64_t MAX_EXTENT = int64_t{1} << 30;
 constexpr int EPI_WARPS = 8;
 constexpr int STAGING_BYTES = 2048;
+constexpr int TILES = 4;  // decoded tiles ahead of the warps that work on them
 constexpr int GROUPED_THREADS = 32 * (4 + EPI_WARPS);
 // fp32 outputs: blocks of the contraction summed by the tensor core (16384 x
 // 2048 x 4096 in 32 groups: 8 blocks 233 us, 4 299, 16 229, all 226)
@@ -114,9 +115,10 @@ struct GroupedCfg {
   // two staging tiles for each epilogue warp
   static constexpr int EPI_OFF = STAGES * STAGE_BYTES;
   static constexpr int BAR_OFF = EPI_OFF + EPI_WARPS * 2 * STAGING_BYTES;
-  // full[S], empty[S], rag[S], peer[S], acc_full[2], acc_empty[2], drain
-  static constexpr int NUM_BARS = 4 * STAGES + 5;
-  static constexpr int SEG_OFF = BAR_OFF + NUM_BARS * 8 + 8;  // then tmem slot + abort flag before it
+  // full[S], empty[S], rag[S], peer[S], acc_full[2], acc_empty[2], drain, tile_full[T], tile_empty[T]
+  static constexpr int NUM_BARS = 4 * STAGES + 5 + 2 * TILES;
+  static constexpr int TILE_OFF = (BAR_OFF + NUM_BARS * 8 + 8 + 15) / 16 * 16;  // tmem slot + abort flag before it
+  static constexpr int SEG_OFF = TILE_OFF + TILES * 48;
   static constexpr int SMEM_BYTES = 1024 + SEG_OFF + 2 * (GROUPS + 1) * 4;
   static_assert(Q_BYTES % 1024 == 0, "swizzle period");
   static_assert(SMEM_BYTES <= 232448, "dynamic shared memory");
@@ -124,7 +126,7 @@ struct GroupedCfg {
 };
 
 // One unit: a tile of one group.
-struct GTile {
+struct alignas(16) GTile {
   int g;
   int lo;     // first row of the group
   int m0;     // first m of the tile (of the pair's tile)
@@ -181,7 +183,13 @@ __device__ __forceinline__ GTile decode_unit(const GroupedParams& p, const int* 
   t.mma_n = (t.ncols + 16 * CG - 1) / (16 * CG) * (16 * CG);
   t.nkb = (depth + 63) >> 6;
   t.last = depth - 64 * (t.nkb - 1);
-  t.chain = p.d_type == OUT_F32 ? CHAIN : max(1, t.nkb);
+  // fp32 outputs: equal chains of at most CHAIN blocks (with 8 and then 1, nine
+  // blocks left the short chain's epilogue uncovered: 17 % of the product's time)
+  t.chain = max(1, t.nkb);
+  if (p.d_type == OUT_F32 && t.nkb > CHAIN) {
+    const int chains = (t.nkb + CHAIN - 1) / CHAIN;
+    t.chain = (t.nkb + chains - 1) / chains;
+  }
   return t;
 }
 
@@ -194,17 +202,10 @@ __device__ __forceinline__ GTile decode_unit(const GroupedParams& p, const int* 
 __device__ __forceinline__ void store_columns(uint8_t* dst, int64_t pitch, int ncols, bool m_ok, int type, bool pairs,
                                               int lane, const uint32_t (&r)[32]) {
   if (type == OUT_F32) {
-    if (ncols >= 32) {
-      if (m_ok) {
 #pragma unroll
-        for (int i = 0; i < 32; ++i, dst += pitch) __stcs(reinterpret_cast<uint32_t*>(dst), r[i]);
-      }
-    } else {
-#pragma unroll
-      for (int i = 0; i < 32; ++i, dst += pitch) {
-        if (i >= ncols) break;
-        if (m_ok) __stcs(reinterpret_cast<uint32_t*>(dst), r[i]);
-      }
+    for (int i = 0; i < 32; ++i, dst += pitch) {
+      if (i >= ncols) break;
+      if (m_ok) __stcs(reinterpret_cast<uint32_t*>(dst), r[i]);
     }
     return;
   }
@@ -246,6 +247,8 @@ __global__ void __launch_bounds__(GROUPED_THREADS, 1) grouped_kernel(const __gri
   auto accf_bar = [&](uint32_t b) { return bar0 + 8u * (4 * STAGES + b); };
   auto acce_bar = [&](uint32_t b) { return bar0 + 8u * (4 * STAGES + 2 + b); };
   const uint32_t drain_bar = bar0 + 8u * (4 * STAGES + 4);
+  auto tile_full = [&](uint32_t i) { return bar0 + 8u * (4 * STAGES + 5 + i); };
+  auto tile_empty = [&](uint32_t i) { return bar0 + 8u * (4 * STAGES + 5 + TILES + i); };
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(gbase + C::BAR_OFF + 8 * C::NUM_BARS);
   volatile uint32_t* abort_flag = tmem_slot + 1;
   int* seg = reinterpret_cast<int*>(gbase + C::SEG_OFF);
@@ -276,6 +279,10 @@ __global__ void __launch_bounds__(GROUPED_THREADS, 1) grouped_kernel(const __gri
       mbar_init(acce_bar(b), EPI_WARPS * CG);
     }
     mbar_init(drain_bar, 1);
+    for (uint32_t i = 0; i < TILES; ++i) {
+      mbar_init(tile_full(i), 1);
+      mbar_init(tile_empty(i), 2 + EPI_WARPS);
+    }
     *abort_flag = 0u;
     fence_mbarrier_init();
   }
@@ -336,12 +343,39 @@ __global__ void __launch_bounds__(GROUPED_THREADS, 1) grouped_kernel(const __gri
     total_units = p.K > 0 ? pre[p.G] : 0;
   }
 
-  if (warp == 0) {
+  // The n-th tile of this CTA, decoded by warp 3: half a dozen divisions, 1150
+  // cycles of each tile of a small contraction when every warp did its own.
+  GTile* tiles = reinterpret_cast<GTile*>(gbase + C::TILE_OFF);
+  auto fetch = [&](uint32_t n, GTile& t) {
+    const uint32_t i = n % TILES;
+    if (!wait_uniform(tile_full(i), (n / TILES) & 1u, wctx, SITE_PROD_EMPTY)) return false;
+    t = tiles[i];
+    __syncwarp();
+    if (lane == 0) mbar_arrive(tile_empty(i));
+    return true;
+  };
+
+  if (warp == 3) {
+    // ------------------------------------------------------------ tile list
+    uint32_t n = 0;
+    for (int u = cluster_id; u < total_units; u += num_clusters, ++n) {
+      const GTile t = decode_unit<CG, BN>(p, seg, pre, u);
+      const uint32_t i = n % TILES;
+      if (!wait_uniform(tile_empty(i), ((n / TILES) & 1u) ^ 1u, wctx, SITE_PROD_EMPTY)) break;
+      if (lane == 0) {
+        tiles[i] = t;
+        mbar_arrive(tile_full(i));
+      }
+      __syncwarp();
+    }
+  } else if (warp == 0) {
     // ------------------------------------------------------------ producer
-    uint32_t it = 0, s = 0, ph = 0;
+    uint32_t it = 0, s = 0, ph = 0, n = 0;
     bool ok = true;
     for (int u = cluster_id; u < total_units && ok; u += num_clusters) {
-      const GTile t = decode_unit<CG, BN>(p, seg, pre, u);
+      GTile t;
+      ok = fetch(n++, t);
+      if (!ok) break;
       const int half = t.mma_n / CG;
       const int m0 = t.m0 + static_cast<int>(rank) * 128;
       const int c0 = t.c0 + static_cast<int>(rank) * half;
@@ -416,10 +450,12 @@ __global__ void __launch_bounds__(GROUPED_THREADS, 1) grouped_kernel(const __gri
     // --------------------------------- MMA issuer (leader), row zeroing (both)
     const uint64_t p_desc0 = sdesc(sbase, p.p_hi);
     const uint64_t q_desc0 = sdesc(sbase + C::P_BYTES, p.q_hi);
-    uint32_t s = 0, ph = 0, tcount = 0, rag_ph = 0;  // rag_ph: one parity bit per stage
+    uint32_t s = 0, ph = 0, n = 0, tcount = 0, rag_ph = 0;  // rag_ph: one parity bit per stage
     bool ok = true;
     for (int u = cluster_id; u < total_units && ok; u += num_clusters) {
-      const GTile t = decode_unit<CG, BN>(p, seg, pre, u);
+      GTile t;
+      ok = fetch(n++, t);
+      if (!ok) break;
       if (t.nkb == 0) continue;
       const bool issue = CG == 1 || rank == 0;
       const uint32_t idesc = p.idesc | (static_cast<uint32_t>(t.mma_n >> 3) << 17);
@@ -524,8 +560,10 @@ __global__ void __launch_bounds__(GROUPED_THREADS, 1) grouped_kernel(const __gri
       }
       ++stores;
     };
+    uint32_t n = 0;
     for (int u = cluster_id; u < total_units; u += num_clusters) {
-      const GTile t = decode_unit<CG, BN>(p, seg, pre, u);
+      GTile t;
+      if (!fetch(n++, t)) break;
       const int m_warp = t.m0 + static_cast<int>(rank) * 128 + 32 * q;
       // output rows of the map: all c of a matrix clip at its end, rows of a
       // group do not
@@ -554,7 +592,7 @@ __global__ void __launch_bounds__(GROUPED_THREADS, 1) grouped_kernel(const __gri
       };
       if (p.d_type == OUT_F32) {
         constexpr int MINE = (BN + 63) / 64;  // blocks of 32 columns of this warp
-        uint32_t sum[MINE][32];
+        float sum[MINE][32] = {};
         bool done = true;
         for (int kb = 0; kb < t.nkb; kb += t.chain, ++tcount) {
           const uint32_t b = tcount & 1u;
@@ -565,19 +603,13 @@ __global__ void __launch_bounds__(GROUPED_THREADS, 1) grouped_kernel(const __gri
           for (int i = 0; i < MINE; ++i) {
             const int c = 32 * part + 64 * i;
             if (c >= t.ncols) break;
-            if (kb == 0) {
-              tmem_ld_32x32b_x32(lanes + b * BN + c, sum[i]);
+#pragma unroll
+            for (int h = 0; h < 32; h += 16) {  // 16 at a time: registers
+              uint32_t r[16];
+              ldx_32x32b_x16(lanes + b * BN + c + h, r);
               tc_wait_ld();
-            } else {
 #pragma unroll
-              for (int h = 0; h < 32; h += 16) {  // 16 at a time: registers
-                uint32_t r[16];
-                ldx_32x32b_x16(lanes + b * BN + c + h, r);
-                tc_wait_ld();
-#pragma unroll
-                for (int k = 0; k < 16; ++k)
-                  sum[i][h + k] = __float_as_uint(__uint_as_float(sum[i][h + k]) + __uint_as_float(r[k]));
-              }
+              for (int k = 0; k < 16; ++k) sum[i][h + k] += __uint_as_float(r[k]);
             }
           }
           release(b);
@@ -587,7 +619,20 @@ __global__ void __launch_bounds__(GROUPED_THREADS, 1) grouped_kernel(const __gri
         for (int i = 0; i < MINE; ++i) {
           const int c = 32 * part + 64 * i;
           if (c >= t.ncols) break;
-          store_columns(dst + c * pitch, pitch, t.ncols - c, m_ok, p.d_type, false, lane, sum[i]);
+          if (!p.d_tma || !(p.weight || c + 32 <= t.ncols)) {
+#pragma unroll
+            for (int k = 0; k < 32; ++k)
+              if (m_ok && c + k < t.ncols) __stcs(reinterpret_cast<float*>(dst + (c + k) * pitch), sum[i][k]);
+            continue;
+          }
+          if (m_warp >= p.M) break;
+#pragma unroll
+          for (int h = 0; h < 32; h += 16) {  // a staging tile holds 16 rows of 32 m
+            const uint32_t buf = staging();
+#pragma unroll
+            for (int k = 0; k < 16; ++k) st_shared_u32(buf + 128u * k + 4u * lane, __float_as_uint(sum[i][h + k]));
+            send(buf, m_warp, row0 + c + h, outer);
+          }
         }
         continue;
       }
@@ -673,10 +718,10 @@ Variant variant() {
           BN};
 }
 
-// CTA pairs; more than 224 groups' tile counts take a ring stage's memory (32
+// CTA pairs; more than 184 groups' tile counts take a ring stage's memory (32
 // groups of 2048 x 4096, 16384 rows: fp32 matrices' gradient 351 us with six
 // stages, 357 with five; rows' gradient 238 and 245).
-Variant pair_variant(int G) { return G <= 224 ? variant<2, 256, 6, 224>() : variant<2, 256, 5, MAX_GROUPS>(); }
+Variant pair_variant(int G) { return G <= 184 ? variant<2, 256, 6, 184>() : variant<2, 256, 5, MAX_GROUPS>(); }
 
 int check_problem(tcg_input in_type, int64_t R, int64_t N, int64_t K, int G, tcg_dtype d_type) {
   if (in_type != TCG_IN_F16 && in_type != TCG_IN_BF16) return TCG_ERR_INVALID;
@@ -718,10 +763,10 @@ int launch_grouped(const Variant& v, GroupedParams& p, int dev, int64_t units, c
   // were written up to their 516th element)
   const int64_t low = reinterpret_cast<int64_t>(p.D) | p.ldd * p.d_size | p.stride_d * p.d_size |
                       static_cast<int64_t>(p.M) * p.d_size;
-  p.d_tma = p.d_type != TCG_F32 && low % 16 == 0;
+  p.d_tma = low % 16 == 0;
   if (p.d_tma) {
     const uint64_t rows = static_cast<uint64_t>(p.weight ? p.C : p.R), outer = p.weight ? p.G : 1;
-    if (int rc = make_store_map(&p.tmap_d, p.D, p.d_type == TCG_BF16, p.M, rows, outer, p.ldd, p.weight ? p.stride_d : p.R * p.ldd))
+    if (int rc = make_store_map(&p.tmap_d, p.D, static_cast<tcg_dtype>(p.d_type), p.M, rows, outer, p.ldd, p.weight ? p.stride_d : p.R * p.ldd))
       return rc;
   }
   p.err = device_error_word(dev);

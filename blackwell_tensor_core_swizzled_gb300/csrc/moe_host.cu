@@ -39,7 +39,8 @@ bool encode_ready() {
   return g_encode != nullptr;
 }
 
-// Tiled map swizzled over `span` bytes (128, 64 or 32), encoded on every call
+// Tiled map swizzled over `span` bytes (128, 64, 32 or, not at all, 0), encoded
+// on every call
 int encode_tiled(CUtensorMap* map, CUtensorMapDataType dt, int rank, const void* base, const cuuint64_t* dims,
                  const cuuint64_t* strides, const cuuint32_t* box, uint32_t span = 128) {
   if (!encode_ready()) {
@@ -51,7 +52,8 @@ int encode_tiled(CUtensorMap* map, CUtensorMapDataType dt, int rank, const void*
                               CU_TENSOR_MAP_INTERLEAVE_NONE,
                               span == 128  ? CU_TENSOR_MAP_SWIZZLE_128B
                               : span == 64 ? CU_TENSOR_MAP_SWIZZLE_64B
-                                           : CU_TENSOR_MAP_SWIZZLE_32B,
+                              : span == 32 ? CU_TENSOR_MAP_SWIZZLE_32B
+                                           : CU_TENSOR_MAP_SWIZZLE_NONE,
                               CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
   if (r != CUDA_SUCCESS) {
     set_error_message(("cuTensorMapEncodeTiled (rank " + std::to_string(rank) + ") failed (" +
@@ -79,12 +81,17 @@ int make_byte_map(CUtensorMap* map, const void* base, uint64_t inner, uint64_t m
   return encode_tiled(map, CU_TENSOR_MAP_DATA_TYPE_UINT8, 3, base, dims, strides, box, box_inner);
 }
 
-int make_store_map(CUtensorMap* map, const void* base, bool bf16, uint64_t inner, uint64_t mid, uint64_t outer,
+int make_store_map(CUtensorMap* map, const void* base, tcg_dtype type, uint64_t inner, uint64_t mid, uint64_t outer,
                    uint64_t stride_mid, uint64_t stride_outer) {
-  const cuuint64_t dims[3] = {inner, mid, outer}, strides[2] = {2 * stride_mid, 2 * stride_outer};
-  const cuuint32_t box[3] = {32, 32, 1};
-  return encode_tiled(map, bf16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16, 3, base, dims,
-                      strides, box, 64);
+  const bool f32 = type == TCG_F32;
+  const uint64_t size = f32 ? 4 : 2;
+  const cuuint64_t dims[3] = {inner, mid, outer}, strides[2] = {size * stride_mid, size * stride_outer};
+  const cuuint32_t box[3] = {32, f32 ? 16u : 32u, 1};
+  return encode_tiled(map,
+                      f32                ? CU_TENSOR_MAP_DATA_TYPE_FLOAT32
+                      : type == TCG_BF16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16
+                                         : CU_TENSOR_MAP_DATA_TYPE_FLOAT16,
+                      3, base, dims, strides, box, f32 ? 0 : 64);
 }
 
 int make_slab_map(CUtensorMap* map, const void* base, uint64_t inner, uint64_t mid, uint64_t slabs, uint64_t outer,
