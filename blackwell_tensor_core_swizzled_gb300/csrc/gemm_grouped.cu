@@ -585,7 +585,7 @@ __global__ void __launch_bounds__(GROUPED_THREADS, 1) grouped_kernel(const __gri
         __syncwarp();
         if (lane == 0) {
           if constexpr (CG == 2)
-            mbar_arrive_cluster(mapa_shared(acce_bar(b), 0));
+            mbar_arrive_relaxed(mapa_shared(acce_bar(b), 0));  // no memory to order, only TMEM reads
           else
             mbar_arrive(acce_bar(b));
         }

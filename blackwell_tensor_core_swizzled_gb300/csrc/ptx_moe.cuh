@@ -19,6 +19,12 @@ __device__ __forceinline__ bool mbar_try_wait_cluster(uint32_t bar, uint32_t par
   return ok != 0;
 }
 
+// Arrive on a barrier of the cluster without ordering memory: a release at
+// cluster scope waits for the thread's stores, 1500 cycles behind an epilogue's.
+__device__ __forceinline__ void mbar_arrive_relaxed(uint32_t bar_cluster) {
+  asm volatile("mbarrier.arrive.relaxed.cluster.shared::cluster.b64 _, [%0];" ::"r"(bar_cluster) : "memory");
+}
+
 // 3-D tiled loads (x, y within a matrix, z = matrix).
 template <int CG>
 __device__ __forceinline__ void tma_load3(uint32_t dst, const void* map, int32_t x, int32_t y, int32_t z,
