@@ -281,7 +281,7 @@ __global__ void __launch_bounds__(GROUPED_THREADS, 1) grouped_kernel(const __gri
     mbar_init(drain_bar, 1);
     for (uint32_t i = 0; i < TILES; ++i) {
       mbar_init(tile_full(i), 1);
-      mbar_init(tile_empty(i), 2 + EPI_WARPS);
+      mbar_init(tile_empty(i), 3 + EPI_WARPS);
     }
     *abort_flag = 0u;
     fence_mbarrier_init();
@@ -368,8 +368,11 @@ __global__ void __launch_bounds__(GROUPED_THREADS, 1) grouped_kernel(const __gri
       }
       __syncwarp();
     }
-  } else if (warp == 0) {
-    // ------------------------------------------------------------ producer
+  } else if (warp == 0 || warp == 2) {
+    // ---------------------------------------------- producers, of P and of Q:
+    // one thread takes 150 cycles a copy, and the matrices' gradient has four
+    // to a block whose MMAs take 512
+    const bool brings_p = warp == 0;
     uint32_t it = 0, s = 0, ph = 0, n = 0;
     bool ok = true;
     for (int u = cluster_id; u < total_units && ok; u += num_clusters) {
@@ -380,6 +383,7 @@ __global__ void __launch_bounds__(GROUPED_THREADS, 1) grouped_kernel(const __gri
       const int m0 = t.m0 + static_cast<int>(rank) * 128;
       const int c0 = t.c0 + static_cast<int>(rank) * half;
       const int q_chunks = (half + 63) >> 6;
+      const uint32_t tx = C::P_BYTES + static_cast<uint32_t>(p.weight ? q_chunks * 8192 : half * 128);
       for (int kb = 0; kb < t.nkb; ++kb) {
         if (!wait_uniform(empty_bar(s), ph ^ 1u, wctx, SITE_PROD_EMPTY)) {
           ok = false;
@@ -388,36 +392,33 @@ __global__ void __launch_bounds__(GROUPED_THREADS, 1) grouped_kernel(const __gri
         if (elect_one()) {
           const uint32_t sp = sbase + s * C::STAGE_BYTES;
           const uint32_t sq = sp + C::P_BYTES;
-          const uint32_t tx = C::P_BYTES + static_cast<uint32_t>(p.weight ? q_chunks * 8192 : half * 128);
           const int k0 = 64 * kb;
-          if (p.weight) {
+          const uint32_t fb = (CG == 2) ? mapa_shared(full_bar(s), 0) : full_bar(s);
+          if (p.weight && kb == t.nkb - 1 && (t.last & 15)) {
+            // the warp that zeroes the rows past the group's end waits for
+            // this CTA's bytes alone; full[s] just marks the stage
             const int r0 = t.lo + k0;
-            if (kb == t.nkb - 1 && (t.last & 15)) {
-              // the warp that zeroes the rows past the group's end waits for
-              // this CTA's bytes alone; full[s] just marks the stage
+            if (brings_p) {
               if (rank == 0) mbar_arrive(full_bar(s));
               mbar_arrive_expect_tx(rag_bar(s), tx);
               for (int i = 0; i < 2; ++i) tma_load3<1>(sp + 8192 * i, &p.tmap_p, m0 + 64 * i, r0, 0, rag_bar(s));
+            } else {
               for (int i = 0; i < q_chunks; ++i) tma_load_2d(sq + 8192 * i, &p.tmap_q, c0 + 64 * i, r0, rag_bar(s));
-            } else {
-              const uint32_t fb = (CG == 2) ? mapa_shared(full_bar(s), 0) : full_bar(s);
-              if (rank == 0) mbar_arrive_expect_tx(full_bar(s), tx * CG);
-              for (int i = 0; i < 2; ++i) tma_load3<CG>(sp + 8192 * i, &p.tmap_p, m0 + 64 * i, r0, 0, fb);
-              for (int i = 0; i < q_chunks; ++i) tma_load<CG>(sq + 8192 * i, &p.tmap_q, c0 + 64 * i, r0, fb);
             }
-          } else {
-            const uint32_t fb = (CG == 2) ? mapa_shared(full_bar(s), 0) : full_bar(s);
+          } else if (brings_p) {
             if (rank == 0) mbar_arrive_expect_tx(full_bar(s), tx * CG);
-            if (p.p_mn) {
-              for (int i = 0; i < 2; ++i) tma_load3<CG>(sp + 8192 * i, &p.tmap_p, m0 + 64 * i, k0, t.g, fb);
-            } else {
+            if (!p.p_mn) {
               tma_load3<CG>(sp, &p.tmap_p, k0, m0, t.g, fb);
-            }
-            if (half == C::Q_ROWS) {
-              tma_load<CG>(sq, &p.tmap_q, k0, t.lo + c0, fb);
             } else {
-              for (int i = 0; i < half; i += 16) tma_load<CG>(sq + 128 * i, &p.tmap_q16, k0, t.lo + c0 + i, fb);
+              for (int i = 0; i < 2; ++i)
+                tma_load3<CG>(sp + 8192 * i, &p.tmap_p, m0 + 64 * i, p.weight ? t.lo + k0 : k0, p.weight ? 0 : t.g, fb);
             }
+          } else if (p.weight) {
+            for (int i = 0; i < q_chunks; ++i) tma_load<CG>(sq + 8192 * i, &p.tmap_q, c0 + 64 * i, t.lo + k0, fb);
+          } else if (half == C::Q_ROWS) {
+            tma_load<CG>(sq, &p.tmap_q, k0, t.lo + c0, fb);
+          } else {
+            for (int i = 0; i < half; i += 16) tma_load<CG>(sq + 128 * i, &p.tmap_q16, k0, t.lo + c0 + i, fb);
           }
         }
         __syncwarp();
@@ -433,7 +434,7 @@ __global__ void __launch_bounds__(GROUPED_THREADS, 1) grouped_kernel(const __gri
       // the leader's and (for a pair) the peer's; ragged stages are waited
       // for by time, as the peer's are
       const uint32_t n_out = it < static_cast<uint32_t>(STAGES) ? it : static_cast<uint32_t>(STAGES);
-      if ((CG == 1 || rank == 0) && !p.weight) {
+      if ((CG == 1 || rank == 0) && !p.weight && brings_p) {
         for (uint32_t j = it - n_out; j < it; ++j) {
           const uint64_t t0 = globaltimer();
           while (!mbar_try_wait(full_bar(j % STAGES), (j / STAGES) & 1u) && globaltimer() - t0 < 20000000ull) {
