@@ -16,12 +16,11 @@
 // tile with few rows costs few columns and nothing is padded in memory.  A
 // group's rows are split evenly into as few tiles of at most BN as they need.
 //
-// 16-bit outputs leave in blocks of 32 m by 32 columns through a shared
+// Outputs leave in blocks of 32 m by 32 columns (fp32: 16) through a shared
 // staging tile and a TMA store, rows of the tile being output rows; a block
-// that a group's end cuts, outputs that are not 16-byte aligned, and fp32 ones
-// are stored by the lanes, an output row an instruction.  Matrices' gradient,
-// 16384 rows, 32 groups of 2048 x 4096: bf16 256 us by the lanes (64 bytes an
-// instruction), 220 by TMA; fp32 278 and 295.
+// that a group's end cuts and outputs that are not 16-byte aligned are stored
+// by the lanes, an output row an instruction.  (Blocks of 64 m by pairs of
+// warps, and fp32 ones of 32 columns, were 1 and 15 % slower.)
 //
 // In the weight product the contraction is ragged: the last 64-row block of a
 // group also loads rows of the next group.  The MMAs of 16 rows beyond the
@@ -31,20 +30,21 @@
 //
 // fp32 outputs keep the accuracy of fp32 sums: the tensor core cuts a running
 // sum's last bits at every step, which over a contraction of 4096 grew to 14
-// times the error of rounded fp32 sums.  So every CHAIN blocks the MMAs change
-// to the other accumulator, and the epilogue adds the finished one to sums in
-// its registers (rounded), while the next is computed.  16-bit outputs round
-// far more than that and take the whole contraction in one accumulator.
+// times the error of rounded fp32 sums.  So every few blocks (at most CHAIN)
+// the MMAs change to the other accumulator, and the epilogue adds the finished
+// one to sums in its registers (rounded), while the next is computed.  16-bit
+// outputs round far more than that and take the whole contraction in one
+// accumulator.
 //
-// What bounds it: many rows a group, the tensor cores (65536 rows x 2048 x
-// 4096 in 32 groups: 625 to 670 us with the clock, 1.64 to 1.76 PFLOP/s); few,
-// the matrices' bytes from HBM (96 us for 537 MB: 5.6 TB/s); the matrices'
-// gradient in fp32, the way between L2 and the SMs, which the operands' tiles
-// and the output share (295 to 350 us; 175 without the stores, 169 for the
-// stores alone).
+// What bounds it: many rows a group, the tensor cores (32768 rows x 4096 x 4096
+// of one group 558 us, where the dense kernel takes 537; 65536 x 2048 x 4096 in
+// 32 groups 1.64 to 1.76 PFLOP/s with the clock); few, the matrices' bytes from
+// HBM (96 us for 537 MB: 5.6 TB/s); the matrices' gradient, the epilogue: 8
+// blocks a warp and tile of some 700 cycles each in fp32 (32 groups of 2048 x
+// 4096: 64 rows 172 us fp32, 6.2 TB/s, and 102 bf16; 512 rows 231 and 180).
 //
-// The structure is the dense kernel's: a persistent CTA (or pair) per SM, a
-// TMA producer warp, an MMA warp, two accumulators in TMEM, epilogue warps.
+// The structure is the dense kernel's: a persistent CTA (or pair) per SM, TMA
+// producer warps, an MMA warp, two accumulators in TMEM, epilogue warps.
 // The tile list depends on offsets, which only the device knows, so each CTA
 // reads them once and keeps the running tile count per group in shared memory;
 // a unit index is turned into (group, tile) by a binary search.
@@ -74,8 +74,8 @@ constexpr int EPI_WARPS = 8;
 constexpr int STAGING_BYTES = 2048;
 constexpr int TILES = 4;  // decoded tiles ahead of the warps that work on them
 constexpr int GROUPED_THREADS = 32 * (4 + EPI_WARPS);
-// fp32 outputs: blocks of the contraction summed by the tensor core (16384 x
-// 2048 x 4096 in 32 groups: 8 blocks 233 us, 4 299, 16 229, all 226)
+// fp32 outputs: blocks of the contraction summed by the tensor core at most
+// (16384 x 2048 x 4096 in 32 groups: 8 blocks 233 us, 4 299, 16 229, all 226)
 constexpr int CHAIN = 8;
 // column tiles of a group that sweep its row tiles together (1, 4, 8 and 16
 // are within 4 % of each other at 32 groups of 2048 x 4096)
@@ -720,8 +720,8 @@ Variant variant() {
 }
 
 // CTA pairs; more than 184 groups' tile counts take a ring stage's memory (32
-// groups of 2048 x 4096, 16384 rows: fp32 matrices' gradient 351 us with six
-// stages, 357 with five; rows' gradient 238 and 245).
+// groups of 2048 x 4096, 16384 rows: fp32 matrices' gradient 2 % slower with
+// five stages than with six, rows' gradient 3 %).
 Variant pair_variant(int G) { return G <= 184 ? variant<2, 256, 6, 184>() : variant<2, 256, 5, MAX_GROUPS>(); }
 
 int check_problem(tcg_input in_type, int64_t R, int64_t N, int64_t K, int G, tcg_dtype d_type) {
