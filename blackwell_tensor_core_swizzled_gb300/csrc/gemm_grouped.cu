@@ -47,7 +47,7 @@
 // producer warps, an MMA warp, two accumulators in TMEM, epilogue warps.
 // The tile list depends on offsets, which only the device knows, so each CTA
 // reads them once and keeps the running tile count per group in shared memory;
-// a unit index is turned into (group, tile) by a binary search.
+// a warp turns unit indexes into tiles by a binary search, ahead of the others.
 #include <cuda.h>
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
