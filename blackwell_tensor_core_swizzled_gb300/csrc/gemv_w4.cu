@@ -176,7 +176,11 @@ int run_gemv(const tcg_gemv_w4_args* args, cudaStream_t s) {
                                              : K_INT4_128;
   const void* k = variant((kind * 2 + (a.in_type == TCG_IN_BF16 ? 1 : 0)) * SHAPES + shape_index(tok), p.bulk);
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(static_cast<unsigned>(std::min<int64_t>(device_sms(dev), (a.R / tok + active) * p.grains)), 1, 1);
+  const int64_t ctas = std::min<int64_t>(device_sms(dev), (a.R / tok + active) * p.grains);
+  p.passes = (p.slabs + p.across - 1) / p.across;
+  p.blocks = static_cast<int>(blocks);
+  p.share = static_cast<int>(blocks * p.grains / ctas);
+  cfg.gridDim = dim3(static_cast<unsigned>(ctas), 1, 1);
   cfg.blockDim = dim3(static_cast<unsigned>(SHAPE_THREADS[shape_index(tok)] + (p.bulk ? 0 : 32)), 1, 1);
   cfg.dynamicSmemBytes = SHAPE_SMEM[shape_index(tok)];
   cfg.stream = s;

@@ -116,6 +116,8 @@ struct GemvParams {
   int64_t ldd;
   int grains;       // GRAIN-row units of a matrix
   int slabs;        // ceil(K / 256)
+  int passes;       // of `across` slabs
+  int blocks, share;  // row blocks there probably are, and then a CTA's grains
   int across;       // warps side by side along K
   int tile_rows;    // 32 down
   int down;         // warps below each other: 16 rows of a stage each
@@ -601,7 +603,7 @@ struct Cursor {
       rows = 0;
       return;
     }
-    block = pos / p.grains;
+    block = pos < p.grains ? 0 : pos / p.grains;
     n0 = (pos - block * p.grains) * GRAIN;
     rows = min(min(p.tile_rows, (end - pos) * GRAIN), p.N - n0);
   }
@@ -730,9 +732,8 @@ __global__ void __launch_bounds__(Shape<TOK>::threads(BULK), 1) gemv_kernel(cons
   }
 
   // a CTA's share of the grains; the slab of a warp in pass i is its column + i * across
-  const int total = blocks * p.grains, ctas = static_cast<int>(gridDim.x), cta = static_cast<int>(blockIdx.x);
-  const int share = total / ctas, more = total - share * ctas;
-  const int passes = (p.slabs + p.across - 1) / p.across;
+  const int ctas = static_cast<int>(gridDim.x), cta = static_cast<int>(blockIdx.x), passes = p.passes;
+  const int total = blocks * p.grains, share = blocks == p.blocks ? p.share : total / ctas, more = total - share * ctas;
   Cursor<S::CAP> cu;
   cu.chunk = cu.pos = cta * share + min(cta, more);
   cu.end = cu.pos + share + (cta < more ? 1 : 0);
