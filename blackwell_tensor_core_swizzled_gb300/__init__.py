@@ -11,6 +11,7 @@ from __future__ import annotations
 
 import ctypes
 import os
+import struct
 
 _HERE = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(_HERE, "libtcg.so")
@@ -42,6 +43,12 @@ class GemvW4Args(ctypes.Structure):
                 ("group", _i32), ("A", _vp), ("lda", _i64), ("offsets", _vp), ("B", _vp), ("ldb", _i64),
                 ("stride_b", _i64), ("scale", _vp), ("ld_scale", _i64), ("stride_scale", _i64), ("zero", _vp),
                 ("alpha", _vp), ("D", _vp), ("d_type", _i32), ("ldd", _i64)]
+
+
+#: GemvW4Args in its native layout (building the structure and passing it by
+#: reference took 0.9 us more of a small call)
+_W4_ARGS = struct.Struct("@2i3q2iPqPP2qP2q3Piq")
+assert _W4_ARGS.size == ctypes.sizeof(GemvW4Args)
 
 
 class ProbeOperand(ctypes.Structure):
@@ -77,7 +84,7 @@ _SIGS = {
                           _vp], _i32),
     "tcg_gemm_grouped_wgrad": ([_i32, _i64, _i64, _i64, _i32, _vp, _i64, _vp, _i64, _vp, _vp, _i32, _i64, _i64,
                                 _vp], _i32),
-    "tcg_gemv_w4": ([ctypes.POINTER(GemvW4Args), _vp], _i32),
+    "tcg_gemv_w4": ([_vp, _vp], _i32),
     "tcg_mxf8_scale_image_bytes": ([_i64, _i64, _i32], _i64),
     "tcg_mxf8_tile_n": ([_i64, _i64, _i64, _i32, _i32], _i32),
     "tcg_tile_n": ([_i32, _i64, _i64, _i64, _i32, _i32], _i32),
@@ -298,9 +305,10 @@ def gemm_grouped_wgrad(in_type, R, N, K, G, DY, lddy, A, lda, offsets, DW, dw_ty
 def gemv_w4(fmt, in_type, R, N, K, A, lda, B, scale, D, d_type, ldd, group=0, zero=None, groups=1, offsets=None,
             alpha=None, ldb=0, stride_b=0, ld_scale=0, stride_scale=0, stream=None, check=True):
     """Few rows against 4-bit matrices (``tcg_gemv_w4``); returns the status (raises if ``check``)."""
-    a = GemvW4Args(fmt, in_type, R, N, K, groups, group, _ptr(A), lda, _ptr(offsets), _ptr(B), ldb, stride_b,
-                   _ptr(scale), ld_scale, stride_scale, _ptr(zero), _ptr(alpha), _ptr(D), d_type, ldd)
-    rc = _lib.tcg_gemv_w4(ctypes.byref(a), _stream(stream))
+    a = _W4_ARGS.pack(fmt, in_type, R, N, K, groups, group, _ptr(A) or 0, lda, _ptr(offsets) or 0, _ptr(B) or 0, ldb,
+                      stride_b, _ptr(scale) or 0, ld_scale, stride_scale, _ptr(zero) or 0, _ptr(alpha) or 0,
+                      _ptr(D) or 0, d_type, ldd)
+    rc = _lib.tcg_gemv_w4(a, _stream(stream))
     return _ok(rc, "gemv_w4") if check else rc
 
 
