@@ -45,10 +45,15 @@
 // TB/s); 16 rows on int4 16384 x 8192: 34 us.
 //
 // bf16 activations are brought into f16's range by a power of two per row and
-// slab (the largest finite value to [2^14, 2^15)), undone on fp32 sums (before
-// a scale that could overflow with it): exact for values down to 2^-29 of the
-// slab's largest; smaller ones round at 2^-39 of it, below the fp32 sums' own
-// rounding of that largest value's product.
+// slab (the largest finite value to [2^14, 2^15)), undone on fp32 sums, before a
+// scale that could overflow with it.  f16 then holds every value down to 2^-31
+// of the slab's largest with all its bits.  Smaller ones may be all that counts
+// (where the larger ones meet zero codes, or their groups a small scale), so a
+// CTA that meets one, or a slab near either end of bf16's range, does its share
+// once more with such slabs in bands of 32 binades each: mxf4 8192 x 8192, 1 row,
+// 13 us without and 58 to 63 with them, nvf4 16384 x 8192, 8 rows, 26 and 87
+// (six such values) to 115 (in all slabs).  (What looks for them costs usual
+// calls 1 to 7 %, 8 rows of nvf4 11.)
 #pragma once
 
 #include <cuda_bf16.h>
@@ -153,8 +158,10 @@ struct Shape {
   static constexpr int ACT = PART + PARTS * WARPS * TILE_PART * 4;
   static constexpr int ACT_BYTES = TOK == 4 ? SLAB * 2 : 0;
   static constexpr int SUM = ACT + WARPS * ACT_BYTES;
-  static constexpr int BARS = SUM + CAP * OUT * 4;  // full[STAGES], empty[STAGES], part_full[PARTS], part_free[PARTS]
-  static constexpr int SEG = BARS + (2 * STAGES + 2 * PARTS) * 8 + 8;
+  // full[STAGES], empty[STAGES], part_full[PARTS], part_free[PARTS]; and others
+  // for doing the share again
+  static constexpr int BARS = SUM + CAP * OUT * 4, BAR_BYTES = (2 * STAGES + 2 * PARTS) * 8;
+  static constexpr int SEG = BARS + 2 * BAR_BYTES + 8;  // abort and unusual flags before it
   static constexpr int BYTES = 1024 + SEG + 2 * (MAX_GROUPS + 1) * 4;
   static_assert(BYTES <= 232448, "dynamic shared memory");
 };
@@ -271,6 +278,74 @@ __device__ __noinline__ RowBlock row_block(const GemvParams& p, const int* seg, 
   return {a, row0, min(TOK, seg[a + 1] - row0)};
 }
 
+// How a row's slab of bf16 activations is brought into f16: 2^e brings the
+// largest finite one to [2^14, 2^15), and undo = 2^-e takes it back.  f16 holds
+// all bits of a bf16 value from 2^-17 on.  Where smaller ones are among them,
+// the slab is taken in bands, band b with those that 2^(e + 32 b) brings to
+// [2^-17, 2^15) (up to 2^126, where every bf16 value is in range).
+//
+// 2^-e comes before the scale, which could overflow with it.  A group's sum is 0
+// or in [2^-25, 2^30), so that this stays a normal number for e in [-96, 96];
+// for others `after` behind the scale makes up the rest.  A slab of one band and
+// such an e is a usual one.
+constexpr int EXACT_BINADES = 31;  // below the largest value's, that f16 holds
+constexpr int BAND_STEP = 32, MAX_UNDO = 96;
+__device__ __forceinline__ float power_of_2(int e) { return __uint_as_float(static_cast<uint32_t>(127 + e) << 23); }
+// Magnitude bits of two values: the running maximum, NaN dropped, and the
+// minimum of each less 1 (0xFFFF: a zero)
+__device__ __forceinline__ void extremes(uint32_t v, uint32_t& largest, uint32_t& smallest) {
+  const uint32_t mag = v & 0x7FFF7FFFu;
+  asm("max.bf16x2 %0, %0, %1;" : "+r"(largest) : "r"(mag));
+  asm("{\n\t.reg .b32 t;\n\tadd.u16x2 t, %1, %2;\n\tmin.u16x2 %0, %0, t;\n\t}"
+      : "+r"(smallest)
+      : "r"(mag), "r"(0xFFFFFFFFu));
+}
+// The scaling of a row by the magnitude bits of its largest value.
+struct Scaling {
+  int e;
+  float after;
+  uint32_t low, high;  // magnitude bits of a band
+};
+__device__ __forceinline__ int first_exponent(uint32_t largest) { return min(141 - static_cast<int>(largest >> 7), 126); }
+// Whether it wants bands or `after` (`smallest`: a lane's, as above).
+__device__ __forceinline__ bool is_unusual(uint32_t largest, uint32_t smallest) {
+  const int s = static_cast<int>(min(smallest & 0xFFFFu, smallest >> 16));
+  return s < static_cast<int>(largest & 0x7F80u) - (EXACT_BINADES << 7) || largest >= (141 + MAX_UNDO + 1) << 7 ||
+         largest - 1 < ((141 - MAX_UNDO) << 7) - 1;
+}
+__device__ __forceinline__ Scaling scaling_of_band(uint32_t largest, int band) {
+  Scaling r;
+  // magnitude bits of 2^x, 0 below bf16's subnormals, inf above its range
+  const auto bits = [](int x) {
+    return x > 127 ? 0x7F80u : x >= -126 ? static_cast<uint32_t>(x + 127) << 7 : x >= -133 ? 1u << (x + 133) : 0u;
+  };
+  const int e0 = largest ? first_exponent(largest) : 0;
+  r.e = min(e0 + BAND_STEP * band, 126);
+  r.after = power_of_2(min(max(r.e, -MAX_UNDO), MAX_UNDO) - r.e);
+  r.low = bits(-17 - r.e);
+  r.high = band ? bits(-17 - min(e0 + BAND_STEP * (band - 1), 126)) : 0x8000u;
+  return r;
+}
+// v without the values of other bands
+__device__ __forceinline__ uint32_t of_band(uint32_t v, const Scaling& r) {
+  const uint32_t x = v & 0x7FFFu, y = (v >> 16) & 0x7FFFu;
+  return (x >= r.low && x < r.high ? v & 0xFFFFu : 0u) | (y >= r.low && y < r.high ? v & 0xFFFF0000u : 0u);
+}
+
+// Two bf16 values times `up` as f16
+__device__ __forceinline__ uint32_t to_f16(uint32_t v, float up) {
+  const __half2 h = __floats2half2_rn(__uint_as_float(v << 16) * up, __uint_as_float(v & 0xFFFF0000u) * up);
+  return *reinterpret_cast<const uint32_t*>(&h);
+}
+// Eight elements in the order in which int4_word decodes: (0,4) (1,5) (2,6) (3,7)
+__device__ __forceinline__ void order_int4(uint32_t (&f)[4]) {
+  const uint32_t v0 = f[0], v1 = f[1], v2 = f[2], v3 = f[3];
+  f[0] = __byte_perm(v0, v2, 0x5410);
+  f[1] = __byte_perm(v0, v2, 0x7632);
+  f[2] = __byte_perm(v1, v3, 0x5410);
+  f[3] = __byte_perm(v1, v3, 0x7632);
+}
+
 // The activations of a row block for one slab as B fragments.  Lane (g, c) =
 // (lane / 4, lane % 4) holds column 8 nt + g (TOK = 4: row g / 2, even g
 // alone count); `frag[ch][nt]` covers 32 of K in the order in which the codes
@@ -279,10 +354,12 @@ __device__ __noinline__ RowBlock row_block(const GemvParams& p, const int* seg, 
 // fragment order: converting them as fragments would repeat the work of the
 // columns that do not count.
 // undo (bf16): the factors that take the scaling back, for the accumulator's
-// columns 2c and 2c + 1 (TOK = 4: row c).
+// columns 2c and 2c + 1 (TOK = 4: row c).  Sets *unusual if the slab is not a
+// usual one; the fragments are of no use then.
 template <int KIND, bool BF16, int TOK, int NT = Shape<TOK>::NT>
 __device__ __forceinline__ void load_fragments(const GemvParams& p, const RowBlock& rb, int slab, int lane,
-                                               uint8_t* scratch, uint32_t (&frag)[8][NT][4], float (&undo)[NT][2]) {
+                                               uint8_t* scratch, volatile uint32_t* unusual,
+                                               uint32_t (&frag)[8][NT][4], float (&undo)[NT][2]) {
   const int g = lane >> 2, c = lane & 3;
   if constexpr (TOK > 4) {
     // many rows: each lane reads its own fragments, a quad shares a row
@@ -305,50 +382,28 @@ __device__ __forceinline__ void load_fragments(const GemvParams& p, const RowBlo
     for (int nt = 0; nt < NT; ++nt) {
       undo[nt][0] = undo[nt][1] = 1.0f;
       if (BF16) {
-        uint32_t m2 = 0;
+        uint32_t m2 = 0, least = 0xFFFFFFFFu;
 #pragma unroll
         for (int ch = 0; ch < 8; ++ch)
 #pragma unroll
-          for (int i = 0; i < 4; ++i) asm("max.bf16x2 %0, %0, %1;" : "+r"(m2) : "r"(frag[ch][nt][i] & 0x7FFF7FFFu));
+          for (int i = 0; i < 4; ++i) extremes(frag[ch][nt][i], m2, least);
         uint32_t m = max(m2 & 0xFFFFu, m2 >> 16);
-        if (m >= 0x7F80u) {  // past infinities
-          m = 0;
-#pragma unroll
-          for (int ch = 0; ch < 8; ++ch)
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
-              const uint32_t lo = frag[ch][nt][i] & 0x7FFFu, hi = (frag[ch][nt][i] >> 16) & 0x7FFFu;
-              if (lo < 0x7F80u) m = max(m, lo);
-              if (hi < 0x7F80u) m = max(m, hi);
-            }
-        }
         m = max(m, __shfl_xor_sync(0xffffffffu, m, 1));
         m = max(m, __shfl_xor_sync(0xffffffffu, m, 2));
-        const int e = min(141 - static_cast<int>(m >> 7), 126);  // 2^e brings the largest to [2^14, 2^15)
-        const float up = __uint_as_float(static_cast<uint32_t>(e + 127) << 23);
-        const float down = __uint_as_float(static_cast<uint32_t>(127 - e) << 23);
+        if (is_unusual(m, least)) *unusual = 1u;
+        const int e = first_exponent(m);
+        const float up = power_of_2(e), down = power_of_2(-e);
 #pragma unroll
         for (int ch = 0; ch < 8; ++ch)
 #pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            const uint32_t v = frag[ch][nt][i];
-            const __half2 h = __floats2half2_rn(__uint_as_float(v << 16) * up, __uint_as_float(v & 0xFFFF0000u) * up);
-            frag[ch][nt][i] = *reinterpret_cast<const uint32_t*>(&h);
-          }
+          for (int i = 0; i < 4; ++i) frag[ch][nt][i] = to_f16(frag[ch][nt][i], up);
         // the factors of rows 2c and 2c + 1, held by the lanes of those rows
         undo[nt][0] = __shfl_sync(0xffffffffu, down, 8 * c);
         undo[nt][1] = __shfl_sync(0xffffffffu, down, 8 * c + 4);
       }
-      if (is_int4(KIND)) {  // pairs (0,4) (1,5) (2,6) (3,7)
+      if (is_int4(KIND)) {
 #pragma unroll
-        for (int ch = 0; ch < 8; ++ch) {
-          uint32_t(&f)[4] = frag[ch][nt];
-          const uint32_t v0 = f[0], v1 = f[1], v2 = f[2], v3 = f[3];
-          f[0] = __byte_perm(v0, v2, 0x5410);
-          f[1] = __byte_perm(v0, v2, 0x7632);
-          f[2] = __byte_perm(v1, v3, 0x5410);
-          f[3] = __byte_perm(v1, v3, 0x7632);
-        }
+        for (int ch = 0; ch < 8; ++ch) order_int4(frag[ch][nt]);
       }
     }
   } else {
@@ -372,35 +427,19 @@ __device__ __forceinline__ void load_fragments(const GemvParams& p, const RowBlo
       next[1] = next[2];
       next[2] = next[3];
       if (BF16) {
-        // the largest magnitude of the row's slab; max drops NaN, and
-        // infinities are looked past when there are any
-        uint32_t m2 = 0;
+        uint32_t m2 = 0, least = 0xFFFFFFFFu;
 #pragma unroll
-        for (int i = 0; i < 4; ++i) asm("max.bf16x2 %0, %0, %1;" : "+r"(m2) : "r"(v[i] & 0x7FFF7FFFu));
-        uint32_t m = max(m2 & 0xFFFFu, m2 >> 16);
-        if (m >= 0x7F80u) {
-          m = 0;
-#pragma unroll 1
-          for (int i = 0; i < 8; ++i) {
-            const uint32_t h = ((i & 4) ? ((i & 2) ? v[3] : v[2]) : ((i & 2) ? v[1] : v[0])) >> (16 * (i & 1)) & 0x7FFFu;
-            if (h < 0x7F80u) m = max(m, h);
-          }
-        }
-        m = __reduce_max_sync(0xffffffffu, m);
-        const int e = min(141 - static_cast<int>(m >> 7), 126);  // 2^e brings the largest to [2^14, 2^15)
-        const float up = __uint_as_float(static_cast<uint32_t>(e + 127) << 23);
+        for (int i = 0; i < 4; ++i) extremes(v[i], m2, least);
+        const uint32_t m = __reduce_max_sync(0xffffffffu, max(m2 & 0xFFFFu, m2 >> 16));
+        if (is_unusual(m, least)) *unusual = 1u;
+        const int e = first_exponent(m);
+        const float up = power_of_2(e);
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          const __half2 h = __floats2half2_rn(__uint_as_float(v[i] << 16) * up, __uint_as_float(v[i] & 0xFFFF0000u) * up);
-          v[i] = *reinterpret_cast<const uint32_t*>(&h);
-        }
-        if (c == r) down = __uint_as_float(static_cast<uint32_t>(127 - e) << 23);
+        for (int i = 0; i < 4; ++i) v[i] = to_f16(v[i], up);
+        if (c == r) down = power_of_2(-e);
       }
-      uint4 y = make_uint4(v[0], v[1], v[2], v[3]);
-      if (is_int4(KIND))  // pairs (0,4) (1,5) (2,6) (3,7)
-        y = make_uint4(__byte_perm(v[0], v[2], 0x5410), __byte_perm(v[0], v[2], 0x7632),
-                       __byte_perm(v[1], v[3], 0x5410), __byte_perm(v[1], v[3], 0x7632));
-      *reinterpret_cast<uint4*>(scratch + 16 * lane) = y;
+      if (is_int4(KIND)) order_int4(v);
+      *reinterpret_cast<uint4*>(scratch + 16 * lane) = make_uint4(v[0], v[1], v[2], v[3]);
       __syncwarp();
       if (g == 2 * r) {  // the row of this even column: 8 consecutive elements of each 32
 #pragma unroll
@@ -418,6 +457,65 @@ __device__ __forceinline__ void load_fragments(const GemvParams& p, const RowBlo
     undo[0][0] = undo[0][1] = down;
     __syncwarp();
   }
+}
+
+// The same of one band of any slab: undo before the scale and `after` behind it.
+// Returns whether a row has values of a later band.
+template <int KIND, int TOK, int NT = Shape<TOK>::NT>
+__device__ __forceinline__ bool load_band(const GemvParams& p, const RowBlock& rb, int slab, int band, int lane,
+                                          uint32_t (&frag)[8][NT][4], float (&undo)[NT][2], float (&after)[NT][2]) {
+  const int g = lane >> 2, c = lane & 3;
+  bool later = false;
+#pragma unroll
+  for (int nt = 0; nt < NT; ++nt) {
+    const int r = TOK > 4 ? 8 * nt + g : g & 1 ? TOK : g / 2;  // the column's row; TOK: none
+    const uint8_t* row = p.A + 2 * ((rb.row0 + r) * p.lda + slab * SLAB + 8 * c);
+    uint32_t m2 = 0, least = 0xFFFFFFFFu;
+#pragma unroll
+    for (int ch = 0; ch < 8; ++ch) {
+      uint4 v = make_uint4(0u, 0u, 0u, 0u);
+      if (r < rb.rows && slab * SLAB + 32 * ch < p.K) v = *reinterpret_cast<const uint4*>(row + 64 * ch);
+      uint32_t(&f)[4] = frag[ch][nt];
+      f[0] = v.x;
+      f[1] = v.y;
+      f[2] = v.z;
+      f[3] = v.w;
+#pragma unroll
+      for (int i = 0; i < 4; ++i) extremes(f[i], m2, least);
+    }
+    uint32_t m = max(m2 & 0xFFFFu, m2 >> 16);
+    if (m >= 0x7F80u) {  // past infinities
+      m = 0;
+#pragma unroll
+      for (int ch = 0; ch < 8; ++ch)
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const uint32_t lo = frag[ch][nt][i] & 0x7FFFu, hi = (frag[ch][nt][i] >> 16) & 0x7FFFu;
+          if (lo < 0x7F80u) m = max(m, lo);
+          if (hi < 0x7F80u) m = max(m, hi);
+        }
+    }
+    m = max(m, __shfl_xor_sync(0xffffffffu, m, 1));
+    m = max(m, __shfl_xor_sync(0xffffffffu, m, 2));
+    const Scaling s = scaling_of_band(m, band);
+    const float up = power_of_2(s.e), down = power_of_2(-min(max(s.e, -MAX_UNDO), MAX_UNDO));
+    least = min(least & 0xFFFFu, least >> 16);
+    later |= least != 0xFFFFu && least + 1 < s.low;
+#pragma unroll
+    for (int ch = 0; ch < 8; ++ch) {
+      uint32_t(&f)[4] = frag[ch][nt];
+#pragma unroll
+      for (int i = 0; i < 4; ++i) f[i] = to_f16(of_band(f[i], s), up);
+      if (is_int4(KIND)) order_int4(f);
+    }
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      const int from = 8 * c + (TOK > 4 ? 4 * i : 0);
+      undo[nt][i] = __shfl_sync(0xffffffffu, down, from);
+      after[nt][i] = __shfl_sync(0xffffffffu, s.after, from);
+    }
+  }
+  return __any_sync(0xffffffffu, later);
 }
 
 // A row's scales of a slab as words, from a byte offset that may be off a
@@ -628,109 +726,34 @@ struct Cursor {
   }
 };
 
-// BULK: scales and zero points come by TMA (a runtime choice took 5 to 8 % of
-// the kernel's time).
-template <int KIND, bool BF16, int TOK, bool BULK>
-__global__ void __launch_bounds__(Shape<TOK>::threads(BULK), 1) gemv_kernel(const __grid_constant__ GemvParams p) {
+template <int TOK, bool BULK>
+__device__ __forceinline__ void init_barriers(uint32_t bars, const GemvParams& p) {
+  using S = Shape<TOK>;
+  const int active = p.across * p.down;
+  for (int i = 0; i < S::STAGES; ++i) {
+    mbar_init(bars + 8 * i, BULK ? 1 : 34);  // the copies' bytes, twice; each lane's that copies words
+    mbar_init(bars + 8 * (S::STAGES + i), active);
+  }
+  for (int i = 0; i < S::PARTS; ++i) {
+    mbar_init(bars + 8 * (2 * S::STAGES + i), active);
+    mbar_init(bars + 8 * (2 * S::STAGES + S::PARTS + i), 1);
+  }
+  fence_mbarrier_init();
+}
+
+// A CTA's share of the matrix rows, by all its warps.  `blocks` row blocks.
+template <int KIND, bool BF16, int TOK, bool BULK, bool BANDS>
+__device__ __forceinline__ void do_share(const GemvParams& p, uint8_t* smem, const int* seg, const int* pre, bool single,
+                                         int2 span, int blocks) {
   using S = Shape<TOK>;
   constexpr int WARPS = S::WARPS, NT = S::NT, STAGES = S::STAGES, PARTS = S::PARTS, ADD_WARPS = S::ADD_WARPS;
-  extern __shared__ uint8_t smem_raw[];
-  const uint32_t raw = smem_u32(smem_raw);
-  uint8_t* smem = smem_raw + (((raw + 1023u) & ~1023u) - raw);
   const uint32_t base = smem_u32(smem);
-  uint32_t* abort_word = reinterpret_cast<uint32_t*>(smem + S::SEG - 8);
-  int* seg = reinterpret_cast<int*>(smem + S::SEG);
-  int* pre = seg + p.G + 1;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const WaitCtx wctx{p.timeout_ns, p.err, abort_word};
-  const uint32_t full = base + S::BARS, empty = full + 8 * STAGES, part_full = empty + 8 * STAGES,
-                 part_free = part_full + 8 * PARTS;
-
+  uint32_t* flags = reinterpret_cast<uint32_t*>(smem + S::SEG - 8);  // abort, unusual
+  const WaitCtx wctx{p.timeout_ns, p.err, flags};
+  const uint32_t full = base + S::BARS + (BANDS ? S::BAR_BYTES : 0), empty = full + 8 * STAGES,
+                 part_full = empty + 8 * STAGES, part_free = part_full + 8 * PARTS;
   const int active = p.across * p.down;  // decoding warps at work
-  if (threadIdx.x == 0) {
-    for (int i = 0; i < STAGES; ++i) {
-      mbar_init(full + 8 * i, BULK ? 1 : 34);  // the copies' bytes, twice; each lane's that copies words
-      mbar_init(empty + 8 * i, active);
-    }
-    for (int i = 0; i < PARTS; ++i) {
-      mbar_init(part_full + 8 * i, active);
-      mbar_init(part_free + 8 * i, 1);
-    }
-    *abort_word = 0u;
-    fence_mbarrier_init();
-  }
-  __syncthreads();
-  griddep_wait();
-  griddep_launch_dependents();
-  // one group of few rows: its block is there whatever the offsets say, and
-  // the codes need not wait for them
-  const bool single = p.offsets && p.G == 1 && p.R <= TOK;
-  int2 span = make_int2(0, 0);
-  if (single) {
-    span.x = min(max(p.offsets[0], 0), p.R);
-    span.y = min(max(p.offsets[1], span.x), p.R);
-  }
-  int blocks;
-  if (single) {
-    blocks = 1;
-  } else if (p.offsets) {
-    if (warp == WARPS) {  // clamp to [previous, R]; row blocks before each group; four groups a lane
-      int run_max = 0, run_blocks = 0;
-#pragma unroll 1
-      for (int i0 = 0; i0 <= p.G; i0 += 128) {
-        int v[4], n[4];
-#pragma unroll
-        for (int k = 0; k < 4; ++k) {
-          const int i = i0 + 4 * lane + k;
-          v[k] = i <= p.G ? p.offsets[i] : 0;
-        }
-#pragma unroll
-        for (int k = 0; k < 4; ++k) {
-          v[k] = min(max(v[k], 0), p.R);
-          if (k) v[k] = max(v[k], v[k - 1]);
-        }
-        int top = v[3];
-#pragma unroll
-        for (int d = 1; d < 32; d <<= 1) {
-          const int o = __shfl_up_sync(0xffffffffu, top, d);
-          if (lane >= d) top = max(top, o);
-        }
-        int before = __shfl_up_sync(0xffffffffu, top, 1);
-        before = lane == 0 ? run_max : max(before, run_max);
-        int sum = 0, last = before;
-#pragma unroll
-        for (int k = 0; k < 4; ++k) {
-          const int i = i0 + 4 * lane + k;
-          v[k] = max(v[k], before);
-          sum += i >= 1 && i <= p.G ? (v[k] - last + TOK - 1) / TOK : 0;
-          last = v[k];
-          n[k] = sum;
-        }
-        int all = sum;
-#pragma unroll
-        for (int d = 1; d < 32; d <<= 1) {
-          const int o = __shfl_up_sync(0xffffffffu, all, d);
-          if (lane >= d) all += o;
-        }
-        const int mine = run_blocks + all - sum;
-#pragma unroll
-        for (int k = 0; k < 4; ++k) {
-          const int i = i0 + 4 * lane + k;
-          if (i <= p.G) {
-            seg[i] = v[k];
-            pre[i] = mine + n[k];
-          }
-        }
-        run_max = max(run_max, __shfl_sync(0xffffffffu, top, 31));
-        run_blocks += __shfl_sync(0xffffffffu, all, 31);
-      }
-    }
-    __syncthreads();
-    blocks = pre[p.G];
-  } else {
-    blocks = (p.R + TOK - 1) / TOK;
-  }
-
   // a CTA's share of the grains; the slab of a warp in pass i is its column + i * across
   const int ctas = static_cast<int>(gridDim.x), cta = static_cast<int>(blockIdx.x), passes = p.passes;
   const int total = blocks * p.grains, share = blocks == p.blocks ? p.share : total / ctas, more = total - share * ctas;
@@ -823,7 +846,10 @@ __global__ void __launch_bounds__(Shape<TOK>::threads(BULK), 1) gemv_kernel(cons
     const int g = lane >> 2, c = lane & 3, row = STAGE_N * below + g;
     if (warp >= active) cu.rows = 0;
     uint32_t frag[8][NT][4];
-    float undo[NT][2];
+    float undo[NT][2], after[NT][2];
+    // BANDS: a tile is gone through for each band, upwards, the next one down
+    int band = 0, have_band = 0;
+    bool rising = true, later = false, first = true, more = false;
     int have_block = -1, have_pass = -1, group = 0;  // whose fragments are loaded
     uint32_t stage = 0, ph = 0, buf = 0, buf_ph = ~0u;  // buf_ph: a parity bit per buffer
     const uint8_t* codes0 = smem + (wk * stage_rows + STAGE_N * below) * (SLAB / 2);
@@ -841,14 +867,24 @@ __global__ void __launch_bounds__(Shape<TOK>::threads(BULK), 1) gemv_kernel(cons
     float* part0 = reinterpret_cast<float*>(smem + S::PART) + warp * S::TILE_PART +
                    (TOK == 4 ? c : 2 * c) * S::PART_PITCH + g;
     while (cu.rows) {
-      if (have_block != cu.block || have_pass != cu.pass) {
+      if (have_block != cu.block || have_pass != cu.pass || (BANDS && have_band != band)) {
         const RowBlock rb = row_block<TOK>(p, seg, pre, single, span, cu.block);
         group = rb.g;
         have_block = cu.block;
         have_pass = cu.pass;
-        load_fragments<KIND, BF16, TOK>(p, rb, wk + cu.pass * p.across, lane, smem + S::ACT + warp * S::ACT_BYTES,
-                                       frag, undo);
+        if constexpr (BANDS) {
+          if (have_band == band) {  // other activations
+            band = 0;
+            rising = true;
+          }
+          have_band = band;
+          later = load_band<KIND, TOK>(p, rb, wk + cu.pass * p.across, band, lane, frag, undo, after);
+        } else {
+          load_fragments<KIND, BF16, TOK>(p, rb, wk + cu.pass * p.across, lane, smem + S::ACT + warp * S::ACT_BYTES,
+                                         flags + 1, frag, undo);
+        }
       }
+      if (BANDS) more = rising ? later : band > 0;
       const int slab = wk + cu.pass * p.across;
 #pragma unroll 1
       for (int h = 0; h < cu.rows; h += stage_rows) {
@@ -883,7 +919,7 @@ __global__ void __launch_bounds__(Shape<TOK>::threads(BULK), 1) gemv_kernel(cons
           rows16<KIND, BF16, TOK, BULK>(codes0 + stage * S::CODE_BYTES, s0, s1, z0, z1, p.scale_row * ES - slab * SB, lane, frag, undo, acc);
         }
         __syncwarp();
-        if (lane == 0) mbar_arrive(empty + 8 * stage);
+        if (lane == 0 && !more) mbar_arrive(empty + 8 * stage);
         if (++stage == STAGES) {
           stage = 0;
           ph ^= 1u;
@@ -896,9 +932,23 @@ __global__ void __launch_bounds__(Shape<TOK>::threads(BULK), 1) gemv_kernel(cons
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-          for (int i = 0; i < 4; i += S::STEP) mine[(8 * nt + (i & 1)) * S::PART_PITCH + 8 * (i >> 1)] = acc[nt][i];
+          for (int i = 0; i < 4; i += S::STEP) {
+            float& part = mine[(8 * nt + (i & 1)) * S::PART_PITCH + 8 * (i >> 1)];
+            part = BANDS ? fmaf(acc[nt][i], after[nt][i & 1], first ? 0.0f : part) : acc[nt][i];
+          }
       }
       if (!ok) break;
+      if (BANDS && more) {  // the tile's stages again
+        for (int h = 0; h < cu.rows; h += stage_rows) {
+          ph ^= stage == 0 ? 1u : 0u;
+          stage = stage == 0 ? STAGES - 1 : stage - 1;
+        }
+        band += rising ? 1 : -1;
+        first = false;
+        continue;
+      }
+      rising = !rising;
+      first = true;
       __syncwarp();
       if (lane == 0) mbar_arrive(part_full + 8 * buf);
       buf_ph ^= 1u << buf;
@@ -967,7 +1017,7 @@ __global__ void __launch_bounds__(Shape<TOK>::threads(BULK), 1) gemv_kernel(cons
       __syncwarp();
       if (lane == 0) mbar_arrive(part_free + 8 * buf);
     }
-    if (p.offsets) {  // rows of no group give zero
+    if (!BANDS && p.offsets) {  // rows of no group give zero
       const int first = single ? span.x : seg[0], end = single ? span.y : seg[p.G];
 #pragma unroll 1
       for (int r = blockIdx.x; r < p.R; r += gridDim.x) {
@@ -976,6 +1026,131 @@ __global__ void __launch_bounds__(Shape<TOK>::threads(BULK), 1) gemv_kernel(cons
         for (int n = threadIdx.x - 32 * (WARPS + 1); n < p.N; n += 32 * ADD_WARPS) store_d(p, r * p.ldd + n, 0.0f);
       }
     }
+  }
+}
+
+__device__ __forceinline__ uint8_t* aligned_smem() {
+  extern __shared__ uint8_t smem_raw[];
+  const uint32_t raw = smem_u32(smem_raw);
+  return smem_raw + (((raw + 1023u) & ~1023u) - raw);
+}
+
+// One group of few rows: its block is there whatever the offsets say, and the
+// codes need not wait for them.
+template <int TOK>
+__device__ __forceinline__ bool single_block(const GemvParams& p, int2* span) {
+  const bool single = p.offsets && p.G == 1 && p.R <= TOK;
+  *span = make_int2(0, 0);
+  if (single) {
+    span->x = min(max(p.offsets[0], 0), p.R);
+    span->y = min(max(p.offsets[1], span->x), p.R);
+  }
+  return single;
+}
+
+// The share once more, since a warp has met a slab that is not usual.  (Apart,
+// and with nothing kept for it: with what bands need in one loop with the
+// others, that took 4 to 10 % more.)
+template <int KIND, int TOK, bool BULK>
+__device__ __noinline__ void do_share_in_bands(const GemvParams& p) {
+  using S = Shape<TOK>;
+  uint8_t* smem = aligned_smem();
+  if (threadIdx.x == 0) init_barriers<TOK, BULK>(smem_u32(smem) + S::BARS + S::BAR_BYTES, p);
+  __syncthreads();
+  const int* seg = reinterpret_cast<const int*>(smem + S::SEG);
+  const int* pre = seg + p.G + 1;
+  int2 span;
+  const bool single = single_block<TOK>(p, &span);
+  do_share<KIND, true, TOK, BULK, true>(p, smem, seg, pre, single, span,
+                                        single ? 1 : p.offsets ? pre[p.G] : (p.R + TOK - 1) / TOK);
+}
+
+// BULK: scales and zero points come by TMA (a runtime choice took 5 to 8 % of
+// the kernel's time).
+template <int KIND, bool BF16, int TOK, bool BULK>
+__global__ void __launch_bounds__(Shape<TOK>::threads(BULK), 1) gemv_kernel(const __grid_constant__ GemvParams p) {
+  using S = Shape<TOK>;
+  uint8_t* smem = aligned_smem();
+  volatile uint32_t* flags = reinterpret_cast<uint32_t*>(smem + S::SEG - 8);  // abort, unusual
+  int* seg = reinterpret_cast<int*>(smem + S::SEG);
+  int* pre = seg + p.G + 1;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+
+  if (threadIdx.x == 0) {
+    init_barriers<TOK, BULK>(smem_u32(smem) + S::BARS, p);
+    flags[0] = flags[1] = 0u;
+  }
+  __syncthreads();
+  griddep_wait();
+  griddep_launch_dependents();
+  int2 span;
+  const bool single = single_block<TOK>(p, &span);
+  int blocks;
+  if (single) {
+    blocks = 1;
+  } else if (p.offsets) {
+    if (warp == S::WARPS) {  // clamp to [previous, R]; row blocks before each group; four groups a lane
+      int run_max = 0, run_blocks = 0;
+#pragma unroll 1
+      for (int i0 = 0; i0 <= p.G; i0 += 128) {
+        int v[4], n[4];
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+          const int i = i0 + 4 * lane + k;
+          v[k] = i <= p.G ? p.offsets[i] : 0;
+        }
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+          v[k] = min(max(v[k], 0), p.R);
+          if (k) v[k] = max(v[k], v[k - 1]);
+        }
+        int top = v[3];
+#pragma unroll
+        for (int d = 1; d < 32; d <<= 1) {
+          const int o = __shfl_up_sync(0xffffffffu, top, d);
+          if (lane >= d) top = max(top, o);
+        }
+        int before = __shfl_up_sync(0xffffffffu, top, 1);
+        before = lane == 0 ? run_max : max(before, run_max);
+        int sum = 0, last = before;
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+          const int i = i0 + 4 * lane + k;
+          v[k] = max(v[k], before);
+          sum += i >= 1 && i <= p.G ? (v[k] - last + TOK - 1) / TOK : 0;
+          last = v[k];
+          n[k] = sum;
+        }
+        int all = sum;
+#pragma unroll
+        for (int d = 1; d < 32; d <<= 1) {
+          const int o = __shfl_up_sync(0xffffffffu, all, d);
+          if (lane >= d) all += o;
+        }
+        const int mine = run_blocks + all - sum;
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+          const int i = i0 + 4 * lane + k;
+          if (i <= p.G) {
+            seg[i] = v[k];
+            pre[i] = mine + n[k];
+          }
+        }
+        run_max = max(run_max, __shfl_sync(0xffffffffu, top, 31));
+        run_blocks += __shfl_sync(0xffffffffu, all, 31);
+      }
+    }
+    __syncthreads();
+    blocks = pre[p.G];
+  } else {
+    blocks = (p.R + TOK - 1) / TOK;
+  }
+
+  do_share<KIND, BF16, TOK, BULK, false>(p, smem, seg, pre, single, span, blocks);
+  if constexpr (BF16) {
+    __syncthreads();
+    volatile uint32_t* f = reinterpret_cast<uint32_t*>(aligned_smem() + S::SEG - 8);
+    if (f[1] && !f[0]) do_share_in_bands<KIND, TOK, BULK>(p);
   }
 }
 

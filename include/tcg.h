@@ -358,7 +358,9 @@ typedef enum {
   TCG_W4_NVF4 = 2   /* E2M1, unsigned E4M3 scale per 16 */
 } tcg_w4;
 
-/* Few rows against 4-bit matrices, activations kept in 16 bits:
+/* Few rows against 4-bit matrices.  Activations keep all their bits, whatever
+ * their range (bf16 ones that a step of 256 of K spreads over more than 2^31
+ * take several times as long); products are summed in fp32:
  *     D[r, n] = alpha[g] * sum_k A[r, k] * w[g][n, k]
  *     w[g][n, k] = value(code[g][n, k]) * scale[g][n, k / group]
  * for the rows [offsets[g], offsets[g+1]) of group g (offsets NULL: G = 1 and

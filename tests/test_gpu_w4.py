@@ -257,3 +257,158 @@ def test_scales_off_a_boundary(tcg, fmt, group, zeros, K):
     for by in (4, 8, 12, 16):
         got = run(tcg, fmt, "bf16", "f32", A, K, N, off, group, B, moved(scale, by), moved(zero, by), G)
         assert np.array_equal(got, want), by
+
+
+def zero_weights(fmt, shape, zero):
+    """Codes whose weight is 0: E2M1 0 or -0, INT4 the zero point (None: 8)."""
+    if fmt != "int4":
+        return np.random.default_rng(0).choice([0, 8], size=shape)
+    return np.full(shape, 8) if zero is None else zero
+
+
+@pytest.mark.parametrize("fmt,group,zeros", FORMATS)
+@pytest.mark.parametrize("R", [1, 4, 7, 13])
+def test_small_activations_beside_large_ones(tcg, fmt, group, zeros, R):
+    """Column k's activations are of the size 2^(40 (k % 6) - 100), and matrix
+    row n has weights in the columns of one such size alone: whatever else the
+    row of activations holds is multiplied by zero and must not count."""
+    K, N = 640, 36
+    rng = np.random.default_rng(R)
+    x = rng.standard_normal((R, K)) * 2.0 ** (40.0 * (np.arange(K) % 6) - 100)
+    A = torch.from_numpy(x).float().bfloat16()
+    a = A.double().numpy()
+    nb = K // group
+    codes = rng.integers(0, 16, size=(N, K))
+    zero, zv = None, None
+    if zeros:
+        zero = rng.integers(0, 16, size=(1, N, nb)).astype(np.uint8)
+        zv = np.repeat(zero[0].astype(int), group, axis=1)
+    mine = np.arange(K)[None] % 6 == np.arange(N)[:, None] % 6
+    codes = np.where(mine, codes, zero_weights(fmt, (N, K), zv))
+    if fmt == "int4":
+        st = torch.from_numpy(rng.uniform(0.01, 0.1, size=(1, N, nb))).float().bfloat16()
+        s, val = st.double().numpy()[0], codes - (8 if zv is None else zv)
+    else:
+        sb = rng.integers(*((120, 130) if fmt == "mxf4" else (0x10, 0x60)), size=(1, N, nb)).astype(np.uint8)
+        st, val = torch.from_numpy(sb), E2M1[codes]
+        s = 2.0 ** (sb[0].astype(float) - 127) if fmt == "mxf4" else ue4m3(sb[0])
+    w = val * np.repeat(s, group, axis=1)
+    packed = torch.from_numpy((codes[:, 0::2] | (codes[:, 1::2] << 4)).astype(np.uint8)).cuda()
+    got = run(tcg, fmt, "bf16", "f32", A.cuda(), K, N, None, group, packed, st.cuda(),
+              None if zero is None else torch.from_numpy(zero).cuda(), 1)
+    close(got, a @ w.T, np.abs(a) @ np.abs(w.T), (K + 8) * 2.0 ** -23, "f32")
+
+
+@pytest.mark.parametrize("R", [1, 4, 7, 13])
+def test_scales_against_activations(tcg, R):
+    """Groups of one slab whose scales undo their activations' sizes, over the
+    whole range of both: every group counts alike."""
+    K, N, group = 512, 24, 32
+    rng = np.random.default_rng(R + 20)
+    size = rng.integers(-100, 120, size=K // group)
+    x = rng.standard_normal((R, K)) * 2.0 ** np.repeat(size, group)
+    A = torch.from_numpy(x).float().bfloat16()
+    a = A.double().numpy()
+    codes = rng.integers(0, 16, size=(N, K))
+    B = torch.from_numpy((codes[:, 0::2] | (codes[:, 1::2] << 4)).astype(np.uint8)).cuda()
+    for fmt in ("mxf4", "int4"):
+        if fmt == "mxf4":
+            st = torch.from_numpy(np.broadcast_to(127 - size, (N, K // group)).astype(np.uint8).copy())
+        else:
+            st = torch.from_numpy(np.broadcast_to(2.0 ** -size, (N, K // group)).copy()).float().bfloat16()
+        val = E2M1[codes] if fmt == "mxf4" else codes - 8
+        w = val * np.repeat(2.0 ** -size.astype(float), group)
+        got = run(tcg, fmt, "bf16", "f32", A.cuda(), K, N, None, group, B, st.cuda(), None, 1)
+        close(got, a @ w.T, np.abs(a) @ np.abs(w.T), (K + 8) * 2.0 ** -23, "f32", fmt)
+
+
+def test_smallest_activations(tcg):
+    """bf16's subnormal activations under a scale that brings them back, beside
+    ones of ordinary size that meet zero weights."""
+    K, N, R = 256, 16, 3
+    rng = np.random.default_rng(31)
+    A = torch.from_numpy(rng.integers(-127, 128, size=(R, K)) * 2.0 ** -133).float().bfloat16()
+    A[1:, ::7] = 1.0
+    a = A.double().numpy()
+    codes = rng.integers(0, 16, size=(N, K))
+    codes[:, ::7] = 0
+    B = torch.from_numpy((codes[:, 0::2] | (codes[:, 1::2] << 4)).astype(np.uint8)).cuda()
+    sb = np.full((N, K // 32), 127 + 100, np.uint8)
+    got = run(tcg, "mxf4", "bf16", "f32", A.cuda(), K, N, None, 32, B, torch.from_numpy(sb).cuda(), None, 1)
+    w = E2M1[codes] * 2.0 ** 100
+    close(got, a @ w.T, np.abs(a) @ np.abs(w.T), (K + 8) * 2.0 ** -23, "f32")
+
+
+@pytest.mark.parametrize("R", [1, 7, 13])
+def test_finite_results_of_the_largest_activations(tcg, R):
+    """Activations near the end of bf16's range whose scales keep the result
+    far from fp32's."""
+    K, N, group = 256, 16, 32
+    A = torch.full((R, K), 2.0 ** 126, dtype=torch.bfloat16)
+    a = A.double().numpy()
+    B = torch.full((N, K // 2), 0x77, dtype=torch.uint8, device="cuda")  # 6, INT4 7 - 8
+    for fmt, st, w in (("mxf4", torch.full((N, K // group), 127 - 20, dtype=torch.uint8), 6 * 2.0 ** -20),
+                       ("int4", torch.full((N, K // group), 2.0 ** -20, dtype=torch.bfloat16), -2.0 ** -20)):
+        got = run(tcg, fmt, "bf16", "f32", A.cuda(), K, N, None, group, B, st.cuda(), None, 1)
+        ref = a @ np.full((K, N), w)
+        close(got, ref, np.abs(ref), (K + 8) * 2.0 ** -23, "f32", fmt)
+
+
+def device_matrices(fmt, G, N, K, group, zeros, dtype, seed, pad_s):
+    """As matrices(), made on the GPU: device codes, scales, zero points, and
+    weights(g) -> float64 matrix g."""
+    gen = torch.Generator(device="cuda").manual_seed(seed)
+    nb = K // group
+    B = torch.randint(0, 256, (G, N, K // 2), dtype=torch.uint8, device="cuda", generator=gen)
+    zero = None
+    if fmt == "int4":
+        scale = (0.01 + 0.09 * torch.rand((G, N, nb + pad_s), device="cuda", generator=gen)).to(TORCH[dtype])
+        if zeros:
+            zero = torch.randint(0, 16, (G, N, nb + pad_s), dtype=torch.uint8, device="cuda", generator=gen)
+    else:
+        lo, hi = (120, 130) if fmt == "mxf4" else (0x01, 0x60)
+        scale = torch.randint(lo, hi, (G, N, nb + pad_s), dtype=torch.uint8, device="cuda", generator=gen)
+    table = torch.from_numpy(E2M1).cuda()
+
+    def weights(g):
+        code = torch.stack([B[g] & 15, B[g] >> 4], -1).view(N, nb, group)
+        sc = scale[g, :, :nb]
+        if fmt == "int4":
+            val = code.double() - (8 if zero is None else zero[g, :, :nb, None].double())
+            s = sc.double()
+        else:
+            val = table[code.int()]
+            s = torch.exp2(sc.double() - 127) if fmt == "mxf4" else sc.view(torch.float8_e4m3fn).double()
+        return (val * s[..., None]).view(N, K)
+    return B, scale, zero, weights
+
+
+@pytest.mark.parametrize("fmt,group,zeros", FORMATS)
+@pytest.mark.parametrize("sizes,N,K", [([3], 20001, 1024), ([8], 12000, 4608), ([16], 9001, 2560),
+                                       ([3, 0, 9, 2], 4001, 4608)])
+def test_many_tiles_of_a_wide_range(tcg, fmt, group, zeros, sizes, N, K):
+    """Activations of the sizes 2^90, 1 and 2^-90 column by column, in every
+    other 256 of K; a matrix row has weights under all of them, under the two
+    smaller or under the smallest alone.  Every output is compared."""
+    G, R = len(sizes), sum(sizes)
+    off = group_offsets(sizes)
+    rng = np.random.default_rng(K)
+    column = np.arange(K) % 3 * (np.arange(K) // 256 % 2) + np.arange(K) // 256 % 2 - 1  # -1: usual, 0..3
+    x = rng.standard_normal((R, K)) * np.choose(column + 1, [1.0, 2.0 ** 90, 1.0, 2.0 ** -90, 1.0])
+    A = torch.from_numpy(x).float().bfloat16().cuda()
+    x = A.double()
+    none = torch.from_numpy(np.where(column[None] < 0, np.arange(3)[:, None] > 0,
+                                     column[None] < np.arange(3)[:, None])).cuda()[torch.arange(N).cuda() % 3]
+    for pad_s in (0, 1):
+        B, scale, zero, weights = device_matrices(fmt, G, N, K, group, zeros, "bf16", N + K, pad_s)
+        for g in range(G):
+            null = torch.zeros((), dtype=torch.uint8, device="cuda")
+            if fmt == "int4":
+                null = null + 8 if zero is None else zero[g, :, :K // group].repeat_interleave(group, 1)
+            code = torch.where(none, null, torch.stack([B[g] & 15, B[g] >> 4], -1).view(N, K))
+            B[g] = code[:, 0::2] | code[:, 1::2] << 4
+        got = run(tcg, fmt, "bf16", "f32", A, K, N, torch.from_numpy(off).cuda(), group, B, scale, zero, G, None, 0,
+                  pad_s)
+        for g in range(G):
+            sl, w = slice(off[g], off[g + 1]), weights(g)
+            close(got[sl], to_host(x[sl] @ w.T), to_host(x[sl].abs() @ w.abs().T), (K + 8) * 2.0 ** -23, "f32", (g, pad_s))
