@@ -68,6 +68,8 @@ int run_gemv(const tcg_gemv_w4_args* args, cudaStream_t s) {
         a.stride_b % 32)
       return TCG_ERR_ALIGNMENT;
     if ((reinterpret_cast<uintptr_t>(a.scale) | reinterpret_cast<uintptr_t>(a.zero)) % 4) return TCG_ERR_ALIGNMENT;
+    // with one group no stride is ever taken, but a tensor map wants an aligned one
+    if (a.G == 1) a.stride_scale = a.N * a.ld_scale;
   }
   int dev;
   if (int rc = current_device_checked(&dev)) return rc;
@@ -100,9 +102,9 @@ int run_gemv(const tcg_gemv_w4_args* args, cudaStream_t s) {
   // by one; 64 experts 46 and 180; a run of rows is nearly as quick as a box)
   // (then K is a multiple of 256, and of so much that a pass's share of a row
   // is one of 16 bytes)
-  const int64_t s_low = blocks_k * es | p.ld_scale | (a.G > 1 ? p.stride_scale : 0) |
+  const int64_t s_low = blocks_k * es | p.ld_scale | p.stride_scale |
                         static_cast<int64_t>(reinterpret_cast<uintptr_t>(a.scale));
-  const int64_t z_low = blocks_k | p.ld_zero | (a.G > 1 ? p.stride_zero : 0) |
+  const int64_t z_low = blocks_k | p.ld_zero | p.stride_zero |
                         static_cast<int64_t>(reinterpret_cast<uintptr_t>(a.zero));
   p.bulk = s_low % 16 == 0 && (!a.zero || z_low % 16 == 0);
   p.alpha = a.alpha;

@@ -412,3 +412,17 @@ def test_many_tiles_of_a_wide_range(tcg, fmt, group, zeros, sizes, N, K):
         for g in range(G):
             sl, w = slice(off[g], off[g + 1]), weights(g)
             close(got[sl], to_host(x[sl] @ w.T), to_host(x[sl].abs() @ w.abs().T), (K + 8) * 2.0 ** -23, "f32", (g, pad_s))
+
+
+@pytest.mark.parametrize("fmt,group,zeros", FORMATS)
+@pytest.mark.parametrize("stride", [1, 8, 3000001])
+def test_one_group_takes_any_scale_stride(tcg, fmt, group, zeros, stride):
+    """With one group nothing lies a stride further on."""
+    R, N, K = 2, 40, 4096
+    A, a = rows((R, K), "bf16", 1)
+    B, scale, zero, w = matrices(fmt, 1, N, K, group, zeros, "bf16", 2)
+    D = torch.empty(R, N, device="cuda")
+    tcg.gemv_w4({"int4": 0, "mxf4": 1, "nvf4": 2}[fmt], tcg.IN_BF16, R, N, K, A, K, B, scale, D, tcg.F32, N,
+                group=group, zero=zero, stride_scale=stride)
+    _ok(tcg)
+    close(to_host(D), a @ w[0].T, np.abs(a) @ np.abs(w[0].T), (K + 8) * 2.0 ** -23, "f32")
