@@ -236,3 +236,129 @@ def test_rerun_is_identical_and_other_streams(tcg):
     torch.cuda.synchronize()
     for D, DW in outs[1:]:
         assert torch.equal(D, outs[0][0]) and torch.equal(DW, outs[0][1])
+
+
+#: both kernel forms (up to 64 rows a group on average, and more), groups that
+#: end inside a block of 32 columns, a last tile that is not full
+ALIGNED = [
+    ([40, 64, 33, 0, 100, 5], 0, 0, 264, 72),
+    ([32, 48, 64, 1], 3, 2, 128, 200),
+    ([257, 255, 513], 0, 0, 520, 200),
+    ([700, 0, 300], 1, 6, 1032, 136),
+    ([96, 160, 290], 0, 0, 264, 1032),
+    ([1100], 0, 0, 40, 64),
+]
+
+
+def guarded_output(shape, ld, gap, dtype, guard=64):
+    """A tensor of `shape` with rows of `ld` elements and `gap` elements between
+    matrices, inside a buffer of sevens (16-byte aligned), and that buffer."""
+    n = 1
+    for d in shape[:-2]:
+        n *= d
+    stride = shape[-2] * ld + gap
+    buf = torch.full((2 * guard + n * stride,), 7.0, dtype=TORCH[dtype], device="cuda")
+    strides = (stride, ld, 1)[3 - len(shape):]
+    return buf.as_strided(shape, strides, guard), buf
+
+
+def untouched(view, buf):
+    """Whether all of the buffer but the view still holds sevens."""
+    view.fill_(7.0)
+    return bool((buf == 7.0).all())
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f16"])
+@pytest.mark.parametrize("major", ["k", "mn"])
+@pytest.mark.parametrize("sizes,before,after,N,K", ALIGNED)
+def test_grouped_aligned_outputs(tcg, dtype, major, sizes, before, after, N, K):
+    """Output rows on 16-byte boundaries (packed and padded) and off them."""
+    G, R = len(sizes), sum(sizes) + before + after
+    off = group_offsets(sizes, before)
+    A, a = rows((R, K), dtype, 1)
+    B, b = rows((G, N, K) if major == "k" else (G, K, N), dtype, 2)
+    if major == "mn":
+        b = b.transpose(0, 2, 1)
+    ref, S = np.zeros((R, N)), np.zeros((R, N))
+    for g in range(G):
+        sl = slice(off[g], off[g + 1])
+        ref[sl], S[sl] = a[sl] @ b[g].T, np.abs(a[sl]) @ np.abs(b[g].T)
+    for out in (dtype, "f32"):
+        for pad in (0, 8, 3):
+            D, buf = guarded_output((R, N), N + pad, 0, out)
+            tcg.gemm_grouped(IN_TYPE[dtype], R, N, K, G, A, K, torch.from_numpy(off).cuda(), B,
+                             tcg.K_MAJOR if major == "k" else tcg.MN_MAJOR, 0, 0, D, DTYPE[out], N + pad)
+            _ok(tcg)
+            close(to_host(D), ref, S, K * 2.0 ** -23, out, (out, pad))
+            assert untouched(D, buf), (out, pad)
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f16"])
+@pytest.mark.parametrize("sizes,before,after,N,K", ALIGNED)
+def test_wgrad_aligned_outputs(tcg, dtype, sizes, before, after, N, K):
+    G, R = len(sizes), sum(sizes) + before + after
+    off = group_offsets(sizes, before)
+    DY, dy = rows((R, N), dtype, 3)
+    A, a = rows((R, K), dtype, 4)
+    ref, S = np.zeros((G, N, K)), np.zeros((G, N, K))
+    for g in range(G):
+        sl = slice(off[g], off[g + 1])
+        ref[g], S[g] = dy[sl].T @ a[sl], np.abs(dy[sl]).T @ np.abs(a[sl])
+    for out in (dtype, "f32"):
+        for pad, gap in ((0, 0), (8, 16), (0, 40), (3, 5)):
+            DW, buf = guarded_output((G, N, K), K + pad, gap, out)
+            tcg.gemm_grouped_wgrad(IN_TYPE[dtype], R, N, K, G, DY, N, A, K, torch.from_numpy(off).cuda(), DW,
+                                   DTYPE[out], K + pad, DW.stride(0))
+            _ok(tcg)
+            close(to_host(DW), ref, S, max(sizes) * 2.0 ** -23, out, (out, pad, gap))
+            assert untouched(DW, buf), (out, pad, gap)
+
+
+def test_long_fp32_sums(tcg):
+    """fp32 outputs of contractions of 4096 are closer than one running sum of
+    the tensor core gets.  It drops what lies below its last bit at each step of
+    16 terms, half a bit of 2^-23 on average and always towards zero; a sum that
+    grows as a walk does loses 2/3 n 2^-24 of itself over n steps.  One sum of
+    4096 (n = 256) may lose 1.0e-5; sums of at most 512 (n = 32), added in
+    rounded fp32, 1.3e-6."""
+    bound = 2 / 3 * 32 * 2.0 ** -24
+    K, N, R = 4096, 256, 512
+    A, a = rows((R, K), "bf16", 1)
+    B, b = rows((2, N, K), "bf16", 2)
+    off = torch.tensor([0, 200, 512], dtype=torch.int32, device="cuda")
+    D = torch.empty(R, N, device="cuda")
+    tcg.gemm_grouped(tcg.IN_BF16, R, N, K, 2, A, K, off, B, tcg.K_MAJOR, K, 0, D, tcg.F32, N)
+    ref = np.concatenate([a[:200] @ b[0].T, a[200:] @ b[1].T])
+    assert np.linalg.norm(to_host(D) - ref) <= bound * np.linalg.norm(ref)
+    R = 4096 + 64
+    DY, dy = rows((R, N), "bf16", 3)
+    A, a = rows((R, N), "bf16", 4)
+    off = torch.tensor([0, 64, R], dtype=torch.int32, device="cuda")
+    DW = torch.empty(2, N, N, device="cuda")
+    tcg.gemm_grouped_wgrad(tcg.IN_BF16, R, N, N, 2, DY, N, A, N, off, DW, tcg.F32, N, 0)
+    _ok(tcg)
+    ref = dy[64:].T @ a[64:]
+    assert np.linalg.norm(to_host(DW[1]) - ref) <= bound * np.linalg.norm(ref)
+
+
+def test_large_16_bit_outputs_repeat(tcg):
+    """Long contractions of unequal groups, many tiles a CTA: the same inputs
+    give the same bits each time, and every value is within its bound."""
+    gen = torch.Generator(device="cuda").manual_seed(5)
+    sizes = [1, 2500, 700, 0, 1311, 4096, 513, 2047]
+    G, R, N, K = len(sizes), sum(sizes), 2048, 4096
+    off = torch.from_numpy(group_offsets(sizes)).cuda()
+    A = torch.randn(R, K, generator=gen, device="cuda").bfloat16()
+    B = (torch.randn(G, N, K, generator=gen, device="cuda") * K ** -0.5).bfloat16()
+    outs = []
+    for _ in range(6):
+        D = torch.full((R, N), 7.0, device="cuda", dtype=torch.bfloat16)
+        tcg.gemm_grouped(tcg.IN_BF16, R, N, K, G, A, K, off, B, tcg.K_MAJOR, K, 0, D, tcg.BF16, N)
+        outs.append(D)
+    _ok(tcg)
+    assert all(torch.equal(D, outs[0]) for D in outs[1:])
+    lo = 0
+    for g, n in enumerate(sizes):
+        x, w = A[lo:lo + n].double(), B[g].double()
+        close(to_host(outs[0][lo:lo + n]), to_host(x @ w.T), to_host(x.abs() @ w.abs().T), K * 2.0 ** -23, "bf16", g)
+        lo += n

@@ -426,3 +426,47 @@ def test_one_group_takes_any_scale_stride(tcg, fmt, group, zeros, stride):
                 group=group, zero=zero, stride_scale=stride)
     _ok(tcg)
     close(to_host(D), a @ w[0].T, np.abs(a) @ np.abs(w[0].T), (K + 8) * 2.0 ** -23, "f32")
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f16"])
+@pytest.mark.parametrize("fmt,group,zeros", FORMATS)
+@pytest.mark.parametrize("R,N,K", [(1, 45001, 256), (8, 30001, 512), (16, 20003, 512), (3, 45001, 4608),
+                                   (7, 40003, 4352), (13, 45000, 2304), (2, 20000, 1152)])
+def test_many_tiles(tcg, dtype, fmt, group, zeros, R, N, K):
+    """Many tiles a CTA, one below the other: short contractions, whose tiles
+    hold up to 512 rows, and ones of several passes over more tiles than their
+    sums have room for.  Every output is compared, scales on 16-byte
+    boundaries and off them."""
+    A, a = rows((R, K), dtype, 1, 8)
+    for pad_s in (0, 1):
+        B, scale, zero, weights = device_matrices(fmt, 1, N, K, group, zeros, dtype, N + K, pad_s)
+        got = run(tcg, fmt, dtype, "f32", A, K, N, None, group, B, scale, zero, 1, None, 0, pad_s, N + 3)
+        w, x = weights(0), torch.from_numpy(a).cuda()
+        close(got, to_host(x @ w.T), to_host(x.abs() @ w.abs().T), (K + 8) * 2.0 ** -23, "f32", pad_s)
+
+
+@pytest.mark.parametrize("fmt,group,zeros", FORMATS)
+@pytest.mark.parametrize("sizes,N,K", [([3, 0, 1, 5, 2, 4], 9001, 512), ([9, 0, 20, 1], 7000, 2304)])
+def test_many_tiles_of_groups(tcg, fmt, group, zeros, sizes, N, K):
+    G, R = len(sizes), sum(sizes)
+    off = group_offsets(sizes)
+    A, a = rows((R, K), "bf16", 1, 8)
+    x = torch.from_numpy(a).cuda()
+    for pad_s in (0, 1):
+        B, scale, zero, weights = device_matrices(fmt, G, N, K, group, zeros, "bf16", N + K, pad_s)
+        got = run(tcg, fmt, "bf16", "f32", A, K, N, torch.from_numpy(off).cuda(), group, B, scale, zero, G, None, 0,
+                  pad_s)
+        for g in range(G):
+            sl, w = slice(off[g], off[g + 1]), weights(g)
+            close(got[sl], to_host(x[sl] @ w.T), to_host(x[sl].abs() @ w.abs().T), (K + 8) * 2.0 ** -23, "f32", (g, pad_s))
+
+
+def test_long_matrix_every_output(tcg):
+    """All outputs of a matrix of 65536 rows of 8192, the second of two groups."""
+    N, K, G = 65536, 8192, 2
+    A, a = rows((2, K), "bf16", 1)
+    B, scale, _, weights = device_matrices("mxf4", G, N, K, 32, False, "bf16", 3, 0)
+    off = torch.tensor([0, 0, 2], dtype=torch.int32, device="cuda")
+    got = run(tcg, "mxf4", "bf16", "f32", A, K, N, off, 32, B, scale, None, G)
+    w, x = weights(1), torch.from_numpy(a).cuda()
+    close(got, to_host(x @ w.T), to_host(x.abs() @ w.abs().T), (K + 8) * 2.0 ** -23, "f32")
