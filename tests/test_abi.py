@@ -4,6 +4,7 @@ before touching the device.  Nothing here launches a kernel."""
 import ctypes
 import os
 import re
+import sys
 
 import pytest
 
@@ -296,3 +297,28 @@ def test_gemv_w4_validation_before_any_device_work(tcg):
     assert call(D=0x40001) == tcg.ERR_ALIGNMENT
     assert call(R=0, A=None, B=None, scale=None, D=None) == tcg.OK
     assert call(N=0, A=None, B=None, scale=None, D=None) == tcg.OK
+
+
+def test_none_and_addresses_are_not_asked_for_data_ptr(tcg):
+    """A call passes up to four None scales and any pointer as an address: none
+    of them goes through a raised AttributeError."""
+    events = []
+
+    def trace(frame, event, arg):
+        events.append(event)
+        return trace
+
+    class Tensor:
+        def data_ptr(self):
+            return 0x30000
+
+    before = sys.gettrace()
+    sys.settrace(trace)
+    try:
+        got = [tcg._ptr(None), tcg._ptr(0), tcg._ptr(0x20000), tcg._ptr(Tensor())]
+    finally:
+        sys.settrace(before)
+    assert got == [None, 0, 0x20000, 0x30000]
+    assert "exception" not in events
+    with pytest.raises(AttributeError):
+        tcg._ptr(object())
