@@ -33,6 +33,9 @@ thread_local int t_last_launches = 0;
 // (formatting on every call measured a quarter of a microsecond).
 struct PlanRecord {
   bool valid = false;
+  bool grouped = false;
+  int w4_rows = 0, w4_across = 0, w4_down = 0, w4_ctas = 0;  // 4-bit products; w4_rows 0: another
+  bool w4_boxes = false;
   bool k_zero = false;
   int cg = 0, bn = 0, clusters = 0, split = 0;
   int mc = 1;  // CTAs per cluster sharing B tiles by multicast
@@ -867,6 +870,29 @@ uint64_t wait_timeout_ns() {
 
 void set_launch_count(int n) { t_last_launches = n; }
 
+void begin_product() {
+  t_last_launches = 0;
+  t_plan = PlanRecord();
+}
+
+void record_zero_plan() { t_plan.valid = t_plan.k_zero = true; }
+
+void record_grouped_plan(int cta_group, int tile_n, int clusters) {
+  t_plan.valid = t_plan.grouped = true;
+  t_plan.cg = cta_group;
+  t_plan.bn = tile_n;
+  t_plan.clusters = clusters;
+}
+
+void record_w4_plan(int rows, int across, int down, int ctas, bool boxes) {
+  t_plan.valid = true;
+  t_plan.w4_rows = rows;
+  t_plan.w4_across = across;
+  t_plan.w4_down = down;
+  t_plan.w4_ctas = ctas;
+  t_plan.w4_boxes = boxes;
+}
+
 void set_error_message(const char* msg) { t_last_error = msg ? msg : ""; }
 
 }  // namespace tcg
@@ -1186,6 +1212,15 @@ const char* tcg_last_plan_string(void) {
     t_last_plan.clear();
   } else if (p.k_zero) {
     t_last_plan = "K = 0: D zeroed";
+  } else if (p.w4_rows) {
+    char buf[200];
+    std::snprintf(buf, sizeof buf, "4-bit, blocks of %d rows, warps %d across K and %d down, scales in %s, %d CTAs",
+                  p.w4_rows, p.w4_across, p.w4_down, p.w4_boxes ? "boxes" : "runs", p.w4_ctas);
+    t_last_plan = buf;
+  } else if (p.grouped) {
+    char buf[200];
+    std::snprintf(buf, sizeof buf, "grouped, cta_group %d, tile %dx%d, %d clusters", p.cg, 128 * p.cg, p.bn, p.clusters);
+    t_last_plan = buf;
   } else {
     char buf[200];
     std::snprintf(buf, sizeof buf, "cta_group %d, tile %dx%d%s, %d clusters%s, %s%s%s", p.cg, 128 * p.cg, p.bn,

@@ -91,6 +91,12 @@ int make_store_map(CUtensorMap* map, const void* base, tcg_dtype type, uint64_t 
 int make_slab_map(CUtensorMap* map, const void* base, uint64_t inner, uint64_t mid, uint64_t slabs, uint64_t outer,
                   uint64_t stride_mid, uint64_t stride_outer, uint32_t box_mid, uint32_t box_slabs);
 void set_launch_count(int n);
+// A product's call: no launches and no plan yet; then the plan of one that
+// queued work, for tcg_last_plan_string.
+void begin_product();
+void record_zero_plan();
+void record_grouped_plan(int cta_group, int tile_n, int clusters);
+void record_w4_plan(int rows, int across, int down, int ctas, bool boxes);
 
 }  // namespace tcg
 

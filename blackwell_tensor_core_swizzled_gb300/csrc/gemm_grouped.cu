@@ -789,13 +789,14 @@ int launch_grouped(const Variant& v, GroupedParams& p, int dev, int64_t units, c
   void* args[] = {&p};
   if (int rc = record_cuda(cudaLaunchKernelExC(&cfg, v.ki.func, args))) return rc;
   set_launch_count(1);
+  record_grouped_plan(cg, v.bn, static_cast<int>(cfg.gridDim.x) / cg);
   return TCG_OK;
 }
 
 int run_grouped(tcg_input in_type, int64_t R, int64_t N, int64_t K, int G, const void* A, int64_t lda,
                 const int32_t* offsets, const void* B, tcg_major b_major, int64_t ldb, int64_t stride_b, void* D,
                 tcg_dtype d_type, int64_t ldd, cudaStream_t s) {
-  set_launch_count(0);
+  begin_product();
   if (int rc = check_problem(in_type, R, N, K, G, d_type)) return rc;
   if (b_major != TCG_K_MAJOR && b_major != TCG_MN_MAJOR) return TCG_ERR_INVALID;
   if (R == 0 || N == 0) return TCG_OK;
@@ -852,7 +853,7 @@ int run_grouped(tcg_input in_type, int64_t R, int64_t N, int64_t K, int G, const
 int run_wgrad(tcg_input in_type, int64_t R, int64_t N, int64_t K, int G, const void* DY, int64_t lddy, const void* A,
               int64_t lda, const int32_t* offsets, void* DW, tcg_dtype dw_type, int64_t lddw, int64_t stride_dw,
               cudaStream_t s) {
-  set_launch_count(0);
+  begin_product();
   if (int rc = check_problem(in_type, R, N, K, G, dw_type)) return rc;
   if (N == 0 || K == 0) return TCG_OK;
   if (int rc = check_output(DW, K, &lddw, dw_type)) return rc;

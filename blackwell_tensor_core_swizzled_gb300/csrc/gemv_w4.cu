@@ -33,7 +33,7 @@ cudaError_t device_setup(int dev) {
 }
 
 int run_gemv(const tcg_gemv_w4_args* args, cudaStream_t s) {
-  set_launch_count(0);
+  begin_product();
   if (!args) return TCG_ERR_INVALID;
   tcg_gemv_w4_args a = *args;
   if (a.format < TCG_W4_INT4 || a.format > TCG_W4_NVF4) return TCG_ERR_INVALID;
@@ -79,6 +79,7 @@ int run_gemv(const tcg_gemv_w4_args* args, cudaStream_t s) {
                                                static_cast<size_t>(a.R), s)))
       return rc;
     set_launch_count(1);
+    record_zero_plan();
     return TCG_OK;
   }
   GemvParams p;
@@ -194,6 +195,7 @@ int run_gemv(const tcg_gemv_w4_args* args, cudaStream_t s) {
   void* params[] = {&p};
   if (int rc = record_cuda(cudaLaunchKernelExC(&cfg, k, params))) return rc;
   set_launch_count(1);
+  record_w4_plan(tok, p.across, p.down, static_cast<int>(ctas), p.bulk);
   return TCG_OK;
 }
 

@@ -467,9 +467,10 @@ const char* tcg_last_error_string(void);
 /* Number of kernels the most recent successful call on this thread queued. */
 int tcg_last_launch_count(void);
 
-/* How the most recent successful GEMM call on this thread was run (kernel
- * tile, CTA group, clusters, one pass / split-K / stream-K, operand swap), as
- * text for logs and tests; empty if the call queued nothing.  The string is
+/* How the most recent product on this thread was run (kernel tile, CTA group,
+ * clusters, one pass / split-K / stream-K, operand swap; for the grouped and
+ * 4-bit products their own), as text for logs and tests; empty if the call
+ * queued nothing or failed.  The string is
  * formatted by this call, owned by the library and valid until this thread's
  * next tcg_last_plan_string call. */
 const char* tcg_last_plan_string(void);

@@ -362,3 +362,38 @@ def test_large_16_bit_outputs_repeat(tcg):
         x, w = A[lo:lo + n].double(), B[g].double()
         close(to_host(outs[0][lo:lo + n]), to_host(x @ w.T), to_host(x.abs() @ w.abs().T), K * 2.0 ** -23, "bf16", g)
         lo += n
+
+
+def test_plan_is_the_last_products(tcg):
+    """The plan string describes the product that was called last, dense,
+    grouped or 4-bit, and is empty after one that queued nothing or failed."""
+    N = K = 64
+    A, B = torch.zeros(4, K, device="cuda").bfloat16(), torch.zeros(2, N, K, device="cuda").bfloat16()
+    D, DW = torch.empty(4, N, device="cuda"), torch.empty(2, N, K, device="cuda")
+    off = torch.tensor([0, 1, 4], dtype=torch.int32, device="cuda")
+    codes, scale = torch.zeros(N, K // 2, dtype=torch.uint8, device="cuda"), torch.zeros(
+        N, K // 32, dtype=torch.uint8, device="cuda")
+
+    def dense():
+        tcg.gemm_bf16(4, N, K, A, tcg.K_MAJOR, K, B, tcg.K_MAJOR, K, D, tcg.F32, N, tcg.F32)
+        assert "pass" in tcg.last_plan_string()
+
+    def grouped(rows=4, major=tcg.K_MAJOR):
+        tcg.gemm_grouped(tcg.IN_BF16, rows, N, K, 2, A, K, off, B, major, K, 0, D, tcg.F32, N)
+
+    def wgrad():
+        tcg.gemm_grouped_wgrad(tcg.IN_BF16, 4, K, K, 2, A, K, A, K, off, DW, tcg.F32, K, 0)
+
+    def w4(k=K):
+        tcg.gemv_w4(tcg.W4_MXF4, tcg.IN_BF16, 4, N, k, A, K, codes, scale, D, tcg.F32, N)
+    for call, text in ((grouped, "grouped, cta_group 1"), (wgrad, "grouped, cta_group 2"), (w4, "4-bit, blocks of 4"),
+                       (lambda: grouped(0), ""), (lambda: w4(0), "K = 0")):
+        dense()
+        call()
+        plan = tcg.last_plan_string()
+        assert plan.startswith(text) and bool(plan) == bool(text), plan
+    dense()
+    with pytest.raises(tcg.TcgError):
+        grouped(major=7)
+    assert tcg.last_plan_string() == ""
+    _ok(tcg)
