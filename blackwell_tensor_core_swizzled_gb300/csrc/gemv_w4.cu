@@ -1,6 +1,7 @@
 // Few rows of 16-bit activations against 4-bit matrices with group scales:
 // entry point and host plan.  The contract is in include/tcg.h.
 #include "gemv_w4.cuh"
+#include "once.h"
 
 namespace tcg {
 
@@ -14,22 +15,19 @@ constexpr int SHAPE_WARPS[SHAPES] = {Shape<4>::WARPS, Shape<8>::WARPS, Shape<16>
 constexpr int SHAPE_THREADS[SHAPES] = {Shape<4>::threads(true), Shape<8>::threads(true), Shape<16>::threads(true)};
 const void* variant(int i, bool bulk) { return bulk ? g_variants.k[i] : w4_runs_kernel(i); }
 
-// Per device, on the first call: the variants' shared-memory attribute.
-constexpr int MAX_DEVICES = 64;
-struct DeviceInfo {
-  std::once_flag once;
-  cudaError_t err = cudaSuccess;
-};
-DeviceInfo g_info[MAX_DEVICES];
+// Per device, on the first call: the variants' shared-memory attribute (all of
+// them, 3 ms, so that no later call, one under capture say, loads a kernel).
+OncePerDevice<cudaError_t> g_setup;
 
 cudaError_t device_setup(int dev) {
-  DeviceInfo& d = g_info[dev];
-  std::call_once(d.once, [&] {
-    for (int i = 0; i < 2 * VARIANTS && d.err == cudaSuccess; ++i)
-      d.err = cudaFuncSetAttribute(variant(i / 2, i % 2 != 0), cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                   SHAPE_SMEM[i / 2 % SHAPES]);
+  return g_setup(dev, [] {
+    for (int i = 0; i < 2 * VARIANTS; ++i)
+      if (const cudaError_t e =
+              cudaFuncSetAttribute(variant(i / 2, i % 2 != 0), cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                   SHAPE_SMEM[i / 2 % SHAPES]))
+        return e;
+    return cudaSuccess;
   });
-  return d.err;
 }
 
 int run_gemv(const tcg_gemv_w4_args* args, cudaStream_t s) {

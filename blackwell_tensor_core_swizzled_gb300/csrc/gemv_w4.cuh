@@ -63,7 +63,6 @@
 #include <algorithm>
 #include <cstdint>
 #include <cstring>
-#include <mutex>
 
 #include "common.h"
 #include "gemm_kernel.cuh"

@@ -7,10 +7,10 @@
 
 #include <algorithm>
 #include <cstdint>
-#include <mutex>
 #include <type_traits>
 
 #include "common.h"
+#include "once.h"
 #include "ptx.cuh"
 
 namespace tcg {
@@ -448,25 +448,20 @@ int launch(void (*kernel)(Params...), dim3 grid, int threads, int smem, int clus
 }
 
 // Both sort kernels' shared-memory attribute, once a device.
-constexpr int MAX_DEVICES = 64;
 constexpr int sort_smem(int E) { return (SORT_WARPS + 1) * (E + 1) * 4; }
-struct SortSetup {
-  std::once_flag once;
-  cudaError_t err = cudaSuccess;
-};
-SortSetup g_sort[MAX_DEVICES];
+OncePerDevice<cudaError_t> g_sort;
 
 cudaError_t sort_setup(int dev) {
-  SortSetup& d = g_sort[dev];
-  std::call_once(d.once, [&] {
-    d.err = cudaFuncSetAttribute(sort_kernel<1>, cudaFuncAttributeMaxDynamicSharedMemorySize, sort_smem(MAX_EXPERTS));
-    if (d.err == cudaSuccess)
-      d.err = cudaFuncSetAttribute(sort_kernel<SORT_CTAS>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                   sort_smem(MAX_EXPERTS));
-    if (d.err == cudaSuccess)
-      d.err = cudaFuncSetAttribute(sort_kernel<SORT_CTAS>, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
+  return g_sort(dev, [] {
+    cudaError_t e =
+        cudaFuncSetAttribute(sort_kernel<1>, cudaFuncAttributeMaxDynamicSharedMemorySize, sort_smem(MAX_EXPERTS));
+    if (e == cudaSuccess)
+      e = cudaFuncSetAttribute(sort_kernel<SORT_CTAS>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                               sort_smem(MAX_EXPERTS));
+    if (e == cudaSuccess)
+      e = cudaFuncSetAttribute(sort_kernel<SORT_CTAS>, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
+    return e;
   });
-  return d.err;
 }
 
 int run_sort(int64_t T, int topk, int E, const int32_t* expert, int32_t* offsets, int32_t* position, int32_t* source,

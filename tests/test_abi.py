@@ -4,6 +4,7 @@ before touching the device.  Nothing here launches a kernel."""
 import ctypes
 import os
 import re
+import subprocess
 import sys
 
 import pytest
@@ -322,3 +323,33 @@ def test_none_and_addresses_are_not_asked_for_data_ptr(tcg):
     assert "exception" not in events
     with pytest.raises(AttributeError):
         tcg._ptr(object())
+
+
+def test_a_failed_setup_is_tried_again(tmp_path):
+    """What the library does once for each device is done again after an error,
+    once after success, and apart for each device and thread."""
+    csrc = os.path.join(ROOT, "blackwell_tensor_core_swizzled_gb300", "csrc")
+    src = tmp_path / "once.cpp"
+    src.write_text(r"""
+#include <thread>
+#include <vector>
+#include "once.h"
+enum Err { Ok = 0, NoMemory = 2 };
+int main() {
+  tcg::OncePerDevice<Err> once;
+  int calls = 0;
+  Err result = NoMemory;
+  auto setup = [&] { ++calls; return result; };
+  if (once(1, setup) != NoMemory || once(1, setup) != NoMemory || calls != 2) return 1;
+  result = Ok;
+  if (once(1, setup) != Ok || once(1, setup) != Ok || calls != 3) return 2;
+  if (once(2, setup) != Ok || calls != 4) return 3;
+  std::vector<std::thread> all;
+  for (int i = 0; i < 8; ++i) all.emplace_back([&] { once(3, setup); });
+  for (auto& t : all) t.join();
+  return calls == 5 ? 0 : 4;
+}
+""")
+    exe = tmp_path / "once"
+    subprocess.run(["g++", "-std=c++17", "-pthread", "-I", csrc, str(src), "-o", str(exe)], check=True)
+    assert subprocess.run([str(exe)]).returncode == 0
