@@ -407,7 +407,7 @@ constexpr int64_t MAX_ENTRIES = int64_t{1} << 30;
 
 int check_route(tcg_dtype type, int64_t T, int topk, int64_t H) {
   if (type < TCG_F32 || type > TCG_BF16 || T < 0 || topk < 1 || H < 0) return TCG_ERR_INVALID;
-  if (topk > 64 || T * topk >= MAX_ENTRIES || T >= MAX_ENTRIES || H >= MAX_ENTRIES) return TCG_ERR_UNSUPPORTED;
+  if (topk > 64 || T >= MAX_ENTRIES || T * topk >= MAX_ENTRIES || H >= MAX_ENTRIES) return TCG_ERR_UNSUPPORTED;
   return TCG_OK;
 }
 

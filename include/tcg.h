@@ -301,7 +301,8 @@ int tcg_moe_sort(int64_t T, int topk, int E, const int32_t* expert, int32_t* off
                  int32_t* source, void* stream);
 
 /* Xs[p][0..H) = X[t][0..H) for every kept entry, 0 for a dropped one; type is
- * the element type of both.  Leading dimensions in elements (0 = H); no
+ * the element type of both.  1 <= topk <= 64 (TCG_ERR_UNSUPPORTED beyond), here
+ * and in the two functions below.  Leading dimensions in elements (0 = H); no
  * alignment beyond the element's (16-byte aligned bases and rows move as
  * 16-byte words).  Its gradient is tcg_moe_combine with weight = NULL.
  * Positions that name no sorted row are passed over, here and below. */
@@ -311,7 +312,7 @@ int tcg_moe_dispatch(tcg_dtype type, int64_t T, int topk, int64_t H, const void*
 /* Y[t][h] = sum over kept j of weight[t][j] * Ys[position[t][j]][h], summed in
  * fp32 in the order of j and rounded once; weight fp32 [T][topk], or NULL for
  * ones.  Rows of dropped entries are not read; a token without kept entries
- * gets zeros.  1 <= topk <= 64. */
+ * gets zeros. */
 int tcg_moe_combine(tcg_dtype type, int64_t T, int topk, int64_t H, const void* Ys, int64_t ldys,
                     const int32_t* position, const float* weight, void* Y, int64_t ldy, void* stream);
 

@@ -353,3 +353,13 @@ int main() {
     exe = tmp_path / "once"
     subprocess.run(["g++", "-std=c++17", "-pthread", "-I", csrc, str(src), "-o", str(exe)], check=True)
     assert subprocess.run([str(exe)]).returncode == 0
+
+
+def test_moe_refuses_sizes_whose_product_overflows(tcg):
+    for T, topk in ((1 << 62, 8), (1 << 61, 64), ((1 << 63) - 1, 64), (1 << 30, 1), (1 << 29, 2)):
+        big = (T, topk, 64)
+        assert tcg.raw_call("tcg_moe_dispatch", 2, *big, 0x10000, 0, 0x20000, 0x30000, 0, None) == tcg.ERR_UNSUPPORTED
+        assert tcg.raw_call("tcg_moe_combine", 2, *big, 0x10000, 0, 0x20000, None, 0x40000, 0,
+                            None) == tcg.ERR_UNSUPPORTED
+        assert tcg.raw_call("tcg_moe_combine_grad", 2, *big, 0x10000, 0, None, 0, 0x20000, None, 0x50000, 0, None,
+                            None) == tcg.ERR_UNSUPPORTED
