@@ -28,20 +28,25 @@
 // zeros in shared memory (both operands: the neighbour's rows may hold
 // infinities) before the MMA reads them.
 //
-// fp32 outputs keep the accuracy of fp32 sums: the tensor core cuts a running
-// sum's last bits at every step, which over a contraction of 4096 grew to 14
-// times the error of rounded fp32 sums.  So every few blocks (at most CHAIN)
-// the MMAs change to the other accumulator, and the epilogue adds the finished
-// one to sums in its registers (rounded), while the next is computed.  16-bit
-// outputs round far more than that and take the whole contraction in one
-// accumulator.
+// fp32 outputs: the tensor core cuts a running sum's last bits at every step, an
+// error that grows with the contraction (2.6e-6 of the result at 4096).  So
+// every few blocks (at most CHAIN) the MMAs change to the other accumulator, and
+// the epilogue adds the finished one to sums in its registers (rounded), while
+// the next is computed.  The error stays that of one chain, 4.7e-7 at 512 and at
+// 16384; plain fp32 products are at 1.6e-7 to 6.1e-7.  16-bit outputs round far
+// more than that and take the whole contraction in one accumulator: at 4096,
+// 0.2 % of bf16 values round to the other neighbour than a plain fp32 sum's do,
+// and both are as far from the exact result (1.66e-3).
 //
 // What bounds it: many rows a group, the tensor cores (32768 rows x 4096 x 4096
 // of one group 558 us, where the dense kernel takes 537; 65536 x 2048 x 4096 in
 // 32 groups 1.64 to 1.76 PFLOP/s with the clock); few, the matrices' bytes from
-// HBM (96 us for 537 MB: 5.6 TB/s); the matrices' gradient, the epilogue: 8
-// blocks a warp and tile of some 700 cycles each in fp32 (32 groups of 2048 x
-// 4096: 64 rows 172 us fp32, 6.2 TB/s, and 102 bf16; 512 rows 231 and 180).
+// HBM (96 us for 537 MB: 5.6 TB/s); the matrices' gradient in fp32, the stores:
+// a warp's block of 2 KB leaves in some 700 cycles, which for all SMs is HBM's
+// rate, but nothing leaves while the same warps add a chain, and every 512 rows
+// begin one more (32 groups of 2048 x 4096: 64 rows 172 us fp32, 6.2 TB/s, and
+// 102 bf16; 512 rows each 236 and 190; the same rows unevenly, spread 0.5, 291
+// to 328 and 241).  (The pair kernels spill 24 bytes.)
 //
 // The structure is the dense kernel's: a persistent CTA (or pair) per SM, TMA
 // producer warps, an MMA warp, two accumulators in TMEM, epilogue warps.
@@ -816,7 +821,9 @@ int run_grouped(tcg_input in_type, int64_t R, int64_t N, int64_t K, int G, const
   // Few rows a group stream the matrices: CTAs of 128 x 64 are then quicker
   // than pairs of 256 x 256, which win once a group takes two narrow tiles (32
   // groups of 2048 x 4096: 16 rows a group 96 us and 104, 64 103 and 106, 80
-  // 133 and 108, 128 168 and 112).
+  // 133 and 108, 128 168 and 112).  Only the average is known here: 512 rows all
+  // in one of the 32 groups 24 us and 27, 128 in each of four 25 and 27, but 2048
+  // all in one 77 and 29.
   const bool wide = R > 64 * static_cast<int64_t>(G);
   const Variant v = wide ? pair_variant(G) : variant<1, 64, 7, MAX_GROUPS>();
   const int cg = v.ki.cta_group;

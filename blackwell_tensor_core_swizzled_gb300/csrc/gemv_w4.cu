@@ -97,8 +97,11 @@ int run_gemv(const tcg_gemv_w4_args* args, cudaStream_t s) {
   p.zero = a.zero;
   p.ld_zero = a.ld_scale;
   p.stride_zero = a.stride_scale;
-  // boxes when rows are aligned (one token 12.9 us, 25 when rows are copied one
-  // by one; 64 experts 46 and 180; a run of rows is nearly as quick as a box)
+  // boxes when rows are aligned, else runs of rows where they fit a stage (mxf4,
+  // 1 row: 14000 x 4096 10.8 us in boxes, 14000 x 4000 11.8 in runs; nvf4, 32
+  // experts: 4096 x 4096 67, 4000 x 4064 78; int4 with zero points, 16 rows:
+  // 16384 x 8192 41, 16384 x 7968 54), else row by row (one token on 8192 x 8192
+  // 25 us where boxes take 13, 64 experts 180 and 46)
   // (then K is a multiple of 256, and of so much that a pass's share of a row
   // is one of 16 bytes)
   const int64_t s_low = blocks_k * es | p.ld_scale | p.stride_scale |
@@ -118,7 +121,10 @@ int run_gemv(const tcg_gemv_w4_args* args, cudaStream_t s) {
   // rows per block: as many as the groups are expected to have (int4 16384 x
   // 8192: 4 rows 24 us in blocks of 4 or 8, 34 of 16; 5 rows 42, 25, 34; 8 rows
   // 44, 24, 35; 9 rows 63, 45, 35; 32 rows 150, 82, 66; nvf4 8192 x 4096: 8
-  // rows 14.3, 10.8, 13.5; 16 rows 21.6, 15.0, 14.3)
+  // rows 14.3, 10.8, 13.5; 16 rows 21.6, 15.0, 14.3).  Only the average is known
+  // here: 32 rows on 64 nvf4 experts of 4096 x 4096 take 23 us in blocks of 4
+  // when one expert has them all (16: 21), 24 on four (16: 26), 67 on 32 (16:
+  // 112).
   const int64_t active = std::min<int64_t>(a.G, a.R);
   const int tok = a.R > 8 * active ? 16 : a.R > 4 * active ? 8 : 4;
   // (a block for every `tok` rows and one more per group there can be at most)

@@ -7,8 +7,10 @@
 // INT4, is exact there) and multiplied by mma m16n8k16 with fp32
 // accumulation: 16 matrix rows by 8 activation rows, so that up to 8 rows cost
 // the decoding once.  (A tcgen05 product would take the decoded codes through
-// shared or tensor memory first; the register path has no such stop, and 8
-// rows' mma take a third of the time that HBM takes to bring the codes.)  Scales keep every
+// shared or tensor memory first, four times the codes' bytes: 7 us each way for
+// 16384 x 8192 at 128 bytes a cycle and SM.  For up to 8 rows, 24 us, that is
+// too much; for 17 and more, which decode the matrix again for every 16 (int4
+// 16384 x 8192: 16 rows 34 us, 32 rows 62), it would pay.)  Scales keep every
 // product exact: NVFP4's unsigned E4M3 scale times an E2M1 value has 6
 // significant bits between 2^-10 and 2688, an f16 value, so it is multiplied
 // into the decoded codes and the whole contraction is one chain of mma; e8m0
@@ -21,7 +23,10 @@
 //                 registers, walking down the matrix 16 rows at a time (eight
 //                 warps when there are 16 activation rows: their fragments
 //                 take 64 registers, and what spills goes past an L1 that
-//                 shared memory leaves almost nothing of)
+//                 shared memory leaves almost nothing of; at the 96 registers
+//                 that 19 warps leave, most variants of 4 and 8 rows spill a
+//                 few, int4 in groups of 32 with 4 rows and nvf4 bf16 with 8
+//                 up to 116 bytes)
 //   the next      brings the rows of a stage to a ring: codes, scales and
 //                 zero points by a TMA copy each, for all slabs at once (a
 //                 copy takes its issuing thread 150 cycles; one for every
@@ -38,11 +43,14 @@
 //
 // Decoding 16 rows of 256 takes a scheduler 253 cycles in mxf4, 310 in nvf4,
 // 400 in int4 (16 activation rows 520), where HBM feeds them in 370; a tile's
-// hand-overs add about 100.  One token on mxf4 8192 x 8192 takes 12.9 us, of
+// hand-overs add about 100.  One token on mxf4 8192 x 8192 takes 13.0 us, of
 // which 5 are the codes' bytes at HBM's rate and 5 the start: the offsets, the
 // activations, the first bytes and the code itself are all fetched cold, one
-// after the other.  32 rows on 64 nvf4 experts of 4096 x 4096: 46 us (5.1
-// TB/s); 16 rows on int4 16384 x 8192: 34 us.
+// after the other.  32 rows on 64 nvf4 experts of 4096 x 4096: 45 us (5.3
+// TB/s).  16 rows on int4 16384 x 8192: 33.5 us, of which the four passes are 3
+// (as 65536 x 2048, one pass, 30.6): two decoding warps a scheduler, of which
+// 0.7 can issue on average, leave half of its cycles empty.  With 8 rows, 24.6
+// us, 1.5 of four warps can, and 63 % of the cycles issue.
 //
 // bf16 activations are brought into f16's range by a power of two per row and
 // slab (the largest finite value to [2^14, 2^15)), undone on fp32 sums, before a
