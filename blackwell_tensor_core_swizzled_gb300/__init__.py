@@ -22,6 +22,7 @@ K_MAJOR, MN_MAJOR = 0, 1
 F32, F16, BF16 = 0, 1, 2
 IN_F16, IN_BF16, IN_TF32, IN_E4M3, IN_E5M2, IN_E3M2, IN_E2M3, IN_E2M1, IN_NVF4 = 0, 1, 2, 3, 4, 5, 6, 7, 8
 W4_INT4, W4_MXF4, W4_NVF4 = 0, 1, 2
+F8_ROW, F8_COLUMN, F8_SQUARE = 0, 1, 2
 
 _i64, _i32, _u32, _u64, _vp = ctypes.c_int64, ctypes.c_int, ctypes.c_uint32, ctypes.c_uint64, ctypes.c_void_p
 
@@ -85,6 +86,13 @@ _SIGS = {
     "tcg_gemm_grouped_wgrad": ([_i32, _i64, _i64, _i64, _i32, _vp, _i64, _vp, _i64, _vp, _vp, _i32, _i64, _i64,
                                 _vp], _i32),
     "tcg_gemv_w4": ([_vp, _vp], _i32),
+    "tcg_f8_quantize": ([_i32, _i32, _i32, _i64, _i64, _i32, _vp, _i64, _i32, _vp, _vp, _i64, _vp, _i64, _vp], _i32),
+    "tcg_gemm_f8": ([_i32, _i64, _i64, _i64, _vp, _i32, _i64, _vp, _i64, _vp, _i32, _i64, _vp, _i64, _i32, _vp, _i32,
+                     _i64, _vp], _i32),
+    "tcg_gemm_f8_grouped": ([_i32, _i64, _i64, _i64, _i32, _vp, _i64, _vp, _i64, _vp, _vp, _i32, _i64, _i64, _vp, _i64,
+                             _i64, _vp, _i32, _i64, _vp], _i32),
+    "tcg_gemm_f8_grouped_wgrad": ([_i32, _i64, _i64, _i64, _i32, _vp, _i64, _vp, _i64, _vp, _i64, _vp, _i64, _vp, _vp,
+                                   _i32, _i64, _i64, _vp], _i32),
     "tcg_mxf8_scale_image_bytes": ([_i64, _i64, _i32], _i64),
     "tcg_mxf8_tile_n": ([_i64, _i64, _i64, _i32, _i32], _i32),
     "tcg_tile_n": ([_i32, _i64, _i64, _i64, _i32, _i32], _i32),
@@ -308,6 +316,36 @@ def gemv_w4(fmt, in_type, R, N, K, A, lda, B, scale, D, d_type, ldd, group=0, ze
                       _ptr(D) or 0, d_type, ldd)
     rc = _lib.tcg_gemv_w4(a, _stream(stream))
     return _ok(rc, "gemv_w4") if check else rc
+
+
+def f8_quantize(q_type, blocks, R, C, x_type, X, ldx, Q, ldq, scale, ld_scale, pow2=False, groups=1, offsets=None,
+                stream=None):
+    """8-bit codes of X and an fp32 scale for each block of 128 (``tcg_f8_quantize``)."""
+    return _ok(_lib.tcg_f8_quantize(q_type, blocks, int(pow2), R, C, x_type, _ptr(X), ldx, groups, _ptr(offsets),
+                                    _ptr(Q), ldq, _ptr(scale), ld_scale, _stream(stream)), "f8_quantize")
+
+
+def gemm_f8(in_type, M, N, K, A, a_major, lda, SA, ld_sa, B, b_major, ldb, SB, ld_sb, sb_square, D, d_type, ldd,
+            stream=None):
+    """Product of 8-bit codes with scales for each block of 128 (``tcg_gemm_f8``)."""
+    return _ok(_lib.tcg_gemm_f8(in_type, M, N, K, _ptr(A), a_major, lda, _ptr(SA), ld_sa, _ptr(B), b_major, ldb,
+                                _ptr(SB), ld_sb, int(sb_square), _ptr(D), d_type, ldd, _stream(stream)), "gemm_f8")
+
+
+def gemm_f8_grouped(in_type, R, N, K, G, A, lda, SA, ld_sa, offsets, B, b_major, ldb, stride_b, SB, ld_sb, stride_sb,
+                    D, d_type, ldd, stream=None):
+    """Sorted rows of 8-bit codes times their group's matrix (``tcg_gemm_f8_grouped``)."""
+    return _ok(_lib.tcg_gemm_f8_grouped(in_type, R, N, K, G, _ptr(A), lda, _ptr(SA), ld_sa, _ptr(offsets), _ptr(B),
+                                        b_major, ldb, stride_b, _ptr(SB), ld_sb, stride_sb, _ptr(D), d_type, ldd,
+                                        _stream(stream)), "gemm_f8_grouped")
+
+
+def gemm_f8_grouped_wgrad(in_type, R, N, K, G, DY, lddy, SDY, ld_sdy, A, lda, SA, ld_sa, offsets, DW, dw_type, lddw,
+                          stride_dw, stream=None):
+    """Gradient of gemm_f8_grouped's matrices from column blocks (``tcg_gemm_f8_grouped_wgrad``)."""
+    return _ok(_lib.tcg_gemm_f8_grouped_wgrad(in_type, R, N, K, G, _ptr(DY), lddy, _ptr(SDY), ld_sdy, _ptr(A), lda,
+                                              _ptr(SA), ld_sa, _ptr(offsets), _ptr(DW), dw_type, lddw, stride_dw,
+                                              _stream(stream)), "gemm_f8_grouped_wgrad")
 
 
 def mxf8_scale_image_bytes(rows, K, tile_rows) -> int:

@@ -1,0 +1,1017 @@
+// Products of 8-bit floating point with an fp32 scale for each block of 128, on
+// the tensor cores: dense, by group, and the matrices' gradient by group.  Entry
+// points, host plan and kernel; the contract is in include/tcg.h.
+//
+// One kernel serves them all.  It computes C[m, c] = sum_b SP[b, m] SQ[b, c]
+// sum_{k in b} P[m, k] Q[c, k] over blocks b of 128 k, in tiles of 128 * CG rows
+// m by up to BN columns c, and stores it transposed, element (m, c) at
+// out[c * ldd + m]:
+//
+//             P (MMA rows)              Q (MMA columns)       contraction
+//   dense     B, rows n                 A, rows m             K
+//   grouped   B[g], rows n              the group's rows r    K
+//   weight    A, columns k, MN-major    DY, columns n         the group's rows
+//
+// No MMA kind takes fp32 scales.  So a block's sum is one accumulator (four
+// MMAs of 32 k), and the epilogue warps add it, scaled, to sums in their
+// registers, while the MMAs fill the other accumulator: 128 x 256 sums of a CTA
+// are 128 registers of 256 threads.  Each block costs the tensor pipe 512 cycles
+// (256 x 256 x 128 of a pair), the epilogue 256 cycles of tensor-memory reads
+// beside 256 of fp32 multiply-adds (512 where P's scales differ from row to row
+// as well: the factor is then formed for each element).
+//
+// A warp loads the blocks' scales ahead into a shared ring, multiplied where P
+// has one scale for 128 rows: the epilogue then reads one factor a column, four
+// at a time, all lanes the same.
+//
+// The ragged extent of a product, the group's rows, is on the MMA's N side, any
+// multiple of 16 (32 for a pair) up to BN, so few rows cost few columns.  MN-major
+// Q (the gradients) takes whole boxes of 128 columns.  In the weight product the
+// contraction is ragged: rows of the next group within the last block are
+// overwritten with zeros in shared memory up to the next multiple of 32, and the
+// MMAs beyond are not issued.
+#include <cuda.h>
+#include <cuda_bf16.h>
+#include <cuda_fp16.h>
+#include <cuda_runtime.h>
+
+#include <algorithm>
+#include <cstdint>
+#include <cstring>
+
+#include "common.h"
+#include "desc.cuh"
+#include "gemm_kernel.cuh"
+#include "ptx.cuh"
+#include "ptx_moe.cuh"
+#include "tmem_ldst.cuh"
+
+namespace tcg {
+
+namespace {
+
+constexpr int MAX_GROUPS = 1024;
+constexpr int64_t MAX_EXTENT = int64_t{1} << 30;
+constexpr int BLOCK = 128;  // k of a scale, and of a ring stage
+constexpr int EPI_WARPS = 8;
+constexpr int STAGING_BYTES = 2048;
+constexpr int TILES = 4;   // decoded tiles ahead of the warps that work on them
+constexpr int SLOTS = 8;   // blocks whose scales are in shared memory
+constexpr int BATCH = 4;   // blocks whose scales are loaded together
+constexpr int F8_THREADS = 32 * (4 + EPI_WARPS);
+constexpr int BAND = 8;    // column tiles that sweep a group's row tiles together
+
+struct F8Params {
+  CUtensorMap tmap_p;    // [G or 1][rows][128-byte boxes]
+  CUtensorMap tmap_q;    // Q in boxes of a full tile's rows (MN-major: 128 k)
+  CUtensorMap tmap_q16;  // K-major Q in boxes of 16 rows, for partial tiles
+  CUtensorMap tmap_d;    // output [G or 1][c][m] in boxes of 32 m and 32 rows (fp32: 16)
+  int d_tma;
+  const int32_t* offsets;  // or null: one group of all R
+  int G, R;
+  int weight;    // the contraction runs over the group's rows
+  int p_mn, q_mn;
+  int M;         // extent of m
+  int C;         // weight: extent of c
+  int K;         // contraction length unless weight
+  int m_tiles;
+  const float* sp;  // VEC: [block][m]; else one for 128 m: g * sp_group + (m / 128) * sp_m + b * sp_b
+  int64_t sp_group, sp_m, sp_b;
+  const float* sq;  // [block][c]: b * sq_b + c
+  int64_t sq_b;
+  uint64_t p_hi, q_hi;
+  uint32_t p_kstep, q_kstep;  // 16-byte units per 32 of the contraction
+  uint32_t idesc;             // without N
+  void* D;
+  int64_t ldd, stride_d;
+  int d_type, d_size;
+  unsigned long long* err;
+  uint64_t timeout_ns;
+};
+
+// kind::f8f6f4 (E4M3 / E5M2), D fp32 in TMEM, A and B from shared descriptors.
+template <int CG>
+__device__ __forceinline__ void mma_f8(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t accum) {
+  if constexpr (CG == 2)
+    asm volatile(
+        "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
+        "tcgen05.mma.cta_group::2.kind::f8f6f4 [%0], %1, %2, %3, p;\n\t}" ::"r"(d),
+        "l"(a), "l"(b), "r"(idesc), "r"(accum)
+        : "memory");
+  else
+    asm volatile(
+        "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
+        "tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], %1, %2, %3, p;\n\t}" ::"r"(d),
+        "l"(a), "l"(b), "r"(idesc), "r"(accum)
+        : "memory");
+}
+
+// Two fp32 operations in one instruction.
+__device__ __forceinline__ uint64_t pair(uint32_t lo, uint32_t hi) {
+  uint64_t v;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(v) : "r"(lo), "r"(hi));
+  return v;
+}
+__device__ __forceinline__ void unpair(uint64_t v, uint32_t& lo, uint32_t& hi) {
+  asm("mov.b64 {%0, %1}, %2;" : "=r"(lo), "=r"(hi) : "l"(v));
+}
+__device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
+  uint64_t d;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(d) : "l"(a), "l"(b), "l"(c));
+  return d;
+}
+__device__ __forceinline__ uint64_t mul2(uint64_t a, uint64_t b) {
+  uint64_t d;
+  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
+  return d;
+}
+
+__device__ __forceinline__ void ld_shared_2x64(uint32_t addr, uint64_t& a, uint64_t& b) {
+  asm volatile("ld.shared.v2.b64 {%0, %1}, [%2];" : "=l"(a), "=l"(b) : "r"(addr));
+}
+__device__ __forceinline__ float ld_shared_f32(uint32_t addr) {
+  float v;
+  asm volatile("ld.shared.f32 %0, [%1];" : "=f"(v) : "r"(addr));
+  return v;
+}
+__device__ __forceinline__ void st_shared_f32(uint32_t addr, float v) {
+  asm volatile("st.shared.f32 [%0], %1;" ::"r"(addr), "f"(v) : "memory");
+}
+__device__ __forceinline__ void st_shared_u16(uint32_t addr, uint32_t v) {
+  asm volatile("st.shared.b16 [%0], %1;" ::"r"(addr), "h"(static_cast<uint16_t>(v)) : "memory");
+}
+
+template <int CG, int BN, int STAGES, bool VEC>
+struct F8Cfg {
+  static constexpr int P_BYTES = 128 * 128;
+  static constexpr int Q_ROWS = BN / CG;
+  static constexpr int Q_BYTES = Q_ROWS * 128;
+  static constexpr int STAGE_BYTES = P_BYTES + Q_BYTES;
+  // two staging tiles for each epilogue warp
+  static constexpr int EPI_OFF = STAGES * STAGE_BYTES;
+  static constexpr int SC_OFF = EPI_OFF + EPI_WARPS * 2 * STAGING_BYTES;
+  static constexpr int SLOT_BYTES = 4 * (BN + (VEC ? 128 : 0));  // factors of the columns, then P's of the rows
+  static constexpr int BAR_OFF = SC_OFF + SLOTS * SLOT_BYTES;
+  // full[S], empty[S], rag[S], peer[S], acc_full[2], acc_empty[2], drain, tile_full[T], tile_empty[T],
+  // scale_full[L], scale_empty[L]
+  static constexpr int NUM_BARS = 4 * STAGES + 5 + 2 * TILES + 2 * SLOTS;
+  static constexpr int TILE_OFF = (BAR_OFF + NUM_BARS * 8 + 8 + 15) / 16 * 16;  // tmem slot + abort flag before it
+  static constexpr int SEG_OFF = TILE_OFF + TILES * 48;
+  static constexpr int SMEM_BYTES = 1024 + SEG_OFF + 2 * (MAX_GROUPS + 1) * 4;
+  static_assert(Q_BYTES % 1024 == 0, "swizzle period");
+  static_assert(SMEM_BYTES <= 232448, "dynamic shared memory");
+  static_assert(2 * BN <= 512, "two accumulators");
+};
+
+// One unit: a tile of one group.
+struct alignas(16) FTile {
+  int g;
+  int lo;     // first row of the group
+  int m0;     // first m of the tile (of the pair's tile)
+  int c0;     // first column within the group (weight: within C)
+  int ncols;  // columns of the tile that exist
+  int mma_n;  // columns the MMA computes
+  int nkb;    // blocks of the contraction (0: the tile is zero)
+  int last;   // depth of the last block
+};
+static_assert(sizeof(FTile) <= 48, "tile ring");
+
+// A group's columns n: tiles of `per` columns each, the last one shorter.
+template <int CG, int BN>
+__device__ __forceinline__ void split_columns(int n, bool whole, int& tiles, int& per) {
+  const int t = (n + BN - 1) / BN;
+  const int step = whole ? BN : 16 * CG;
+  per = t ? ((n + t - 1) / t + step - 1) / step * step : step;
+  tiles = (n + per - 1) / per;
+}
+
+// seg[0..G]: clamped offsets; pre[0..G]: units of the groups before (unless weight).
+template <int CG, int BN>
+__device__ __forceinline__ FTile decode_unit(const F8Params& p, const int* seg, const int* pre, int u) {
+  FTile t;
+  int v, tiles, per, n;
+  if (p.weight) {
+    split_columns<CG, BN>(p.C, true, tiles, per);
+    const int per_group = tiles * p.m_tiles;
+    t.g = u / per_group;
+    v = u - t.g * per_group;
+    n = p.C;
+  } else {
+    int a = 0, b = p.G;  // pre[a] <= u < pre[b]
+    while (b - a > 1) {
+      const int mid = (a + b) >> 1;
+      if (pre[mid] <= u)
+        a = mid;
+      else
+        b = mid;
+    }
+    t.g = a;
+    v = u - pre[a];
+    n = seg[a + 1] - seg[a];
+    split_columns<CG, BN>(n, p.q_mn, tiles, per);
+  }
+  t.lo = seg[t.g];
+  const int depth = p.weight ? seg[t.g + 1] - t.lo : p.K;
+  const int band = v / (BAND * p.m_tiles);
+  const int first = band * BAND;
+  const int width = min(tiles - first, BAND);
+  v -= first * p.m_tiles;
+  t.m0 = (v / width) * (128 * CG);
+  t.c0 = (first + v % width) * per;
+  t.ncols = min(per, n - t.c0);
+  t.mma_n = p.weight || p.q_mn ? BN : (t.ncols + 16 * CG - 1) / (16 * CG) * (16 * CG);
+  t.nkb = (depth + BLOCK - 1) / BLOCK;
+  t.last = depth - BLOCK * (t.nkb - 1);
+  return t;
+}
+
+template <int CG, int BN, int STAGES, bool VEC>
+__global__ void __launch_bounds__(F8_THREADS, 1) f8_kernel(const __grid_constant__ F8Params p) {
+  using C = F8Cfg<CG, BN, STAGES, VEC>;
+  extern __shared__ uint8_t smem_raw[];
+  const uint32_t raw = smem_u32(smem_raw);
+  const uint32_t sbase = (raw + 1023u) & ~1023u;
+  uint8_t* gbase = smem_raw + (sbase - raw);
+  const uint32_t bar0 = sbase + C::BAR_OFF;
+  auto full_bar = [&](uint32_t s) { return bar0 + 8u * s; };
+  auto empty_bar = [&](uint32_t s) { return bar0 + 8u * (STAGES + s); };
+  auto rag_bar = [&](uint32_t s) { return bar0 + 8u * (2 * STAGES + s); };
+  auto peer_bar = [&](uint32_t s) { return bar0 + 8u * (3 * STAGES + s); };
+  auto accf_bar = [&](uint32_t b) { return bar0 + 8u * (4 * STAGES + b); };
+  auto acce_bar = [&](uint32_t b) { return bar0 + 8u * (4 * STAGES + 2 + b); };
+  const uint32_t drain_bar = bar0 + 8u * (4 * STAGES + 4);
+  auto tile_full = [&](uint32_t i) { return bar0 + 8u * (4 * STAGES + 5 + i); };
+  auto tile_empty = [&](uint32_t i) { return bar0 + 8u * (4 * STAGES + 5 + TILES + i); };
+  auto scf_bar = [&](uint32_t i) { return bar0 + 8u * (4 * STAGES + 5 + 2 * TILES + i); };
+  auto sce_bar = [&](uint32_t i) { return bar0 + 8u * (4 * STAGES + 5 + 2 * TILES + SLOTS + i); };
+  auto slot_at = [&](uint32_t i) { return sbase + C::SC_OFF + i * C::SLOT_BYTES; };
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(gbase + C::BAR_OFF + 8 * C::NUM_BARS);
+  volatile uint32_t* abort_flag = tmem_slot + 1;
+  int* seg = reinterpret_cast<int*>(gbase + C::SEG_OFF);
+  int* pre = seg + p.G + 1;
+
+  const int warp = threadIdx.x >> 5;
+  const int lane = threadIdx.x & 31;
+  const uint32_t rank = (CG == 2) ? cluster_ctarank() : 0u;
+  const int cluster_id = blockIdx.x / CG;
+  const int num_clusters = gridDim.x / CG;
+  const WaitCtx wctx{p.timeout_ns, p.err, abort_flag};
+
+  // the maps exist unless the contraction is empty
+  if (warp == 0 && lane == 0 && (p.weight ? p.R : p.K) > 0) {
+    prefetch_tmap(&p.tmap_p);
+    prefetch_tmap(&p.tmap_q);
+    if (!p.weight && !p.q_mn) prefetch_tmap(&p.tmap_q16);
+  }
+  if (threadIdx.x == 96) {
+    for (uint32_t s = 0; s < STAGES; ++s) {
+      mbar_init(full_bar(s), 1);
+      mbar_init(empty_bar(s), 1);
+      mbar_init(rag_bar(s), 1);
+      mbar_init(peer_bar(s), 1);
+    }
+    for (uint32_t b = 0; b < 2; ++b) {
+      mbar_init(accf_bar(b), 1);
+      mbar_init(acce_bar(b), EPI_WARPS * CG);
+    }
+    mbar_init(drain_bar, 1);
+    for (uint32_t i = 0; i < TILES; ++i) {
+      mbar_init(tile_full(i), 1);
+      mbar_init(tile_empty(i), 3 + EPI_WARPS);
+    }
+    for (uint32_t i = 0; i < SLOTS; ++i) {
+      mbar_init(scf_bar(i), 1);
+      mbar_init(sce_bar(i), EPI_WARPS);
+    }
+    *abort_flag = 0u;
+    fence_mbarrier_init();
+  }
+  // a programmatic dependent of the previous kernel: no global access before
+  griddep_wait();
+  if (warp == 2) {
+    tmem_alloc<CG>(smem_u32(tmem_slot), 512);
+    tmem_relinquish<CG>();
+  }
+  // offsets, each clamped to [the previous one, R], and the units before each group
+  if (p.offsets) {
+    for (int g = threadIdx.x; g <= p.G; g += F8_THREADS) seg[g] = p.offsets[g];
+  } else if (threadIdx.x < 2) {
+    seg[threadIdx.x] = threadIdx.x ? p.R : 0;
+  }
+  __syncthreads();
+  if (warp == 3) {
+    int run_max = 0, run_units = 0;
+    for (int g0 = 0; g0 <= p.G; g0 += 32) {
+      const int g = g0 + lane;
+      int v = g <= p.G ? min(max(seg[g], 0), p.R) : 0;
+#pragma unroll
+      for (int d = 1; d < 32; d <<= 1) {
+        const int o = __shfl_up_sync(0xffffffffu, v, d);
+        if (lane >= d) v = max(v, o);
+      }
+      v = max(v, run_max);
+      int before = __shfl_up_sync(0xffffffffu, v, 1);
+      if (lane == 0) before = run_max;
+      // units of group g - 1
+      int tiles = 0, per, units = 0;
+      if (g >= 1 && g <= p.G && !p.weight) {
+        split_columns<CG, BN>(v - before, p.q_mn, tiles, per);
+        units = tiles * p.m_tiles;
+      }
+#pragma unroll
+      for (int d = 1; d < 32; d <<= 1) {
+        const int o = __shfl_up_sync(0xffffffffu, units, d);
+        if (lane >= d) units += o;
+      }
+      units += run_units;
+      if (g <= p.G) {
+        seg[g] = v;
+        pre[g] = units;
+      }
+      run_max = __shfl_sync(0xffffffffu, v, 31);
+      run_units = __shfl_sync(0xffffffffu, units, 31);
+    }
+  }
+  tc_fence_before();
+  __syncthreads();
+  if constexpr (CG == 2) cluster_sync();
+  tc_fence_after();
+  const uint32_t tmem_base = *tmem_slot;
+  griddep_launch_dependents();
+  int total_units;
+  if (p.weight) {
+    int tiles, per;
+    split_columns<CG, BN>(p.C, true, tiles, per);
+    total_units = p.G * tiles * p.m_tiles;
+  } else {
+    total_units = p.K > 0 ? pre[p.G] : 0;
+  }
+
+  // The n-th tile of this CTA, decoded by warp 3.
+  FTile* tiles = reinterpret_cast<FTile*>(gbase + C::TILE_OFF);
+  auto fetch = [&](uint32_t n, FTile& t) {
+    const uint32_t i = n % TILES;
+    if (!wait_uniform(tile_full(i), (n / TILES) & 1u, wctx, SITE_PROD_EMPTY)) return false;
+    t = tiles[i];
+    __syncwarp();
+    if (lane == 0) mbar_arrive(tile_empty(i));
+    return true;
+  };
+
+  if (warp == 3) {
+    // ------------------------------------------- tile list and blocks' scales
+    uint32_t n = 0, it = 0;
+    auto publish = [&](int u, FTile& t) {
+      t = decode_unit<CG, BN>(p, seg, pre, u);
+      const uint32_t i = n % TILES;
+      if (!wait_uniform(tile_empty(i), ((n / TILES) & 1u) ^ 1u, wctx, SITE_PROD_EMPTY)) return false;
+      if (lane == 0) {
+        tiles[i] = t;
+        mbar_arrive(tile_full(i));
+      }
+      __syncwarp();
+      ++n;
+      return true;
+    };
+    FTile t, next;
+    bool ok = cluster_id >= total_units || publish(cluster_id, next);
+    for (int u = cluster_id; u < total_units && ok; u += num_clusters) {
+      t = next;
+      // the tile after this one, ahead of this one's scales
+      if (u + num_clusters < total_units && !publish(u + num_clusters, next)) break;
+      const int b0 = p.weight ? t.lo / BLOCK + t.g : 0;
+      const float* sq = p.sq + b0 * p.sq_b + (p.weight ? t.c0 : t.lo + t.c0);
+      const int m0 = t.m0 + static_cast<int>(rank) * 128;
+      const float* sp = VEC ? p.sp + b0 * p.sp_b + m0 : p.sp + t.g * p.sp_group + (m0 / BLOCK) * p.sp_m;
+      for (int kb = 0; kb < t.nkb && ok; kb += BATCH) {
+        const int blocks = min(BATCH, t.nkb - kb);
+        float q[BATCH][BN / 32], r[BATCH][VEC ? 4 : 1];
+#pragma unroll
+        for (int j = 0; j < BATCH; ++j) {
+#pragma unroll
+          for (int i = 0; i < BN / 32; ++i)
+            q[j][i] = j < blocks && lane + 32 * i < t.ncols ? __ldg(sq + (kb + j) * p.sq_b + lane + 32 * i) : 0.0f;
+          if constexpr (VEC) {
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+              r[j][i] = j < blocks && m0 + lane + 32 * i < p.M ? __ldg(sp + (kb + j) * p.sp_b + lane + 32 * i) : 0.0f;
+          } else {
+            r[j][0] = j < blocks && m0 < p.M ? __ldg(sp + (kb + j) * p.sp_b) : 0.0f;
+          }
+        }
+#pragma unroll
+        for (int j = 0; j < BATCH; ++j) {
+          if (j >= blocks) break;
+          const uint32_t i = it % SLOTS;
+          if (!wait_uniform(sce_bar(i), ((it / SLOTS) & 1u) ^ 1u, wctx, SITE_PROD_EMPTY)) {
+            ok = false;
+            break;
+          }
+          const uint32_t at = slot_at(i) + 4u * lane;
+#pragma unroll
+          for (int k = 0; k < BN / 32; ++k) st_shared_f32(at + 128u * k, VEC ? q[j][k] : q[j][k] * r[j][0]);
+          if constexpr (VEC) {
+#pragma unroll
+            for (int k = 0; k < 4; ++k) st_shared_f32(at + 4u * BN + 128u * k, r[j][k]);
+          }
+          __syncwarp();
+          if (lane == 0) mbar_arrive(scf_bar(i));
+          ++it;
+        }
+      }
+    }
+  } else if (warp == 0 || warp == 2) {
+    // ---------------------------------------------- producers, of P and of Q
+    const bool brings_p = warp == 0;
+    uint32_t it = 0, s = 0, ph = 0, n = 0;
+    bool ok = true;
+    for (int u = cluster_id; u < total_units && ok; u += num_clusters) {
+      FTile t;
+      ok = fetch(n++, t);
+      if (!ok) break;
+      const int half = t.mma_n / CG;
+      const int m0 = t.m0 + static_cast<int>(rank) * 128;
+      const int c0 = t.c0 + static_cast<int>(rank) * half;
+      const bool q_mn = p.weight || p.q_mn;
+      const uint32_t tx = C::P_BYTES + static_cast<uint32_t>(half * 128);
+      for (int kb = 0; kb < t.nkb; ++kb) {
+        if (!wait_uniform(empty_bar(s), ph ^ 1u, wctx, SITE_PROD_EMPTY)) {
+          ok = false;
+          break;
+        }
+        if (elect_one()) {
+          const uint32_t sp = sbase + s * C::STAGE_BYTES;
+          const uint32_t sq = sp + C::P_BYTES;
+          const int k0 = BLOCK * kb;
+          const uint32_t fb = (CG == 2) ? mapa_shared(full_bar(s), 0) : full_bar(s);
+          if (p.weight && kb == t.nkb - 1 && (t.last & 31)) {
+            // the warp that zeroes the rows past the group's end waits for
+            // this CTA's bytes alone; full[s] just marks the stage
+            const int r0 = t.lo + k0;
+            if (brings_p) {
+              if (rank == 0) mbar_arrive(full_bar(s));
+              mbar_arrive_expect_tx(rag_bar(s), tx);
+              tma_load3<1>(sp, &p.tmap_p, m0, r0, 0, rag_bar(s));
+            } else {
+              tma_load3<1>(sq, &p.tmap_q, c0, r0, 0, rag_bar(s));
+            }
+          } else if (brings_p) {
+            if (rank == 0) mbar_arrive_expect_tx(full_bar(s), tx * CG);
+            if (!p.p_mn)
+              tma_load3<CG>(sp, &p.tmap_p, k0, m0, t.g, fb);
+            else
+              tma_load3<CG>(sp, &p.tmap_p, m0, p.weight ? t.lo + k0 : k0, p.weight ? 0 : t.g, fb);
+          } else if (q_mn) {
+            tma_load3<CG>(sq, &p.tmap_q, c0, p.weight ? t.lo + k0 : k0, 0, fb);
+          } else if (half == C::Q_ROWS) {
+            tma_load3<CG>(sq, &p.tmap_q, k0, t.lo + c0, 0, fb);
+          } else {
+            for (int i = 0; i < half; i += 16) tma_load3<CG>(sq + 128 * i, &p.tmap_q16, k0, t.lo + c0 + i, 0, fb);
+          }
+        }
+        __syncwarp();
+        ++it;
+        if (++s == STAGES) {
+          s = 0;
+          ph ^= 1u;
+        }
+      }
+    }
+    if (!ok && elect_one()) {
+      // let the copies in flight land before the CTA can exit: full[s] counts
+      // the leader's and (for a pair) the peer's; ragged stages are waited
+      // for by time, as the peer's are
+      const uint32_t n_out = it < static_cast<uint32_t>(STAGES) ? it : static_cast<uint32_t>(STAGES);
+      if ((CG == 1 || rank == 0) && !p.weight && brings_p) {
+        for (uint32_t j = it - n_out; j < it; ++j) {
+          const uint64_t t0 = globaltimer();
+          while (!mbar_try_wait(full_bar(j % STAGES), (j / STAGES) & 1u) && globaltimer() - t0 < 20000000ull) {
+          }
+        }
+      } else {
+        const uint64_t t0 = globaltimer();
+        while (globaltimer() - t0 < 2000000ull) {
+        }
+      }
+    }
+    __syncwarp();
+  } else if (warp == 1) {
+    // --------------------------------- MMA issuer (leader), row zeroing (both)
+    const uint64_t p_desc0 = sdesc(sbase, p.p_hi);
+    const uint64_t q_desc0 = sdesc(sbase + C::P_BYTES, p.q_hi);
+    uint32_t s = 0, ph = 0, n = 0, tcount = 0, rag_ph = 0;  // rag_ph: one parity bit per stage
+    bool ok = true;
+    for (int u = cluster_id; u < total_units && ok; u += num_clusters) {
+      FTile t;
+      ok = fetch(n++, t);
+      if (!ok) break;
+      const bool issue = CG == 1 || rank == 0;
+      const uint32_t idesc = p.idesc | (static_cast<uint32_t>(t.mma_n >> 3) << 17);
+      for (int kb = 0; kb < t.nkb; ++kb) {
+        const bool last = kb == t.nkb - 1;
+        const bool ragged = p.weight && last && (t.last & 31);
+        const uint32_t b = tcount & 1u;
+        if (issue && !wait_uniform(acce_bar(b), ((tcount >> 1) & 1u) ^ 1u, wctx, SITE_MMA_ACC_EMPTY)) {
+          ok = false;
+          break;
+        }
+        ++tcount;
+        const uint32_t d_tmem = tmem_base + b * BN;
+        if (issue && !wait_uniform(full_bar(s), ph, wctx, SITE_MMA_FULL)) {
+          ok = false;
+          break;
+        }
+        if (ragged) {
+          const uint32_t par = (rag_ph >> s) & 1u;
+          rag_ph ^= 1u << s;
+          if (!warp_wait(rag_bar(s), par, wctx, SITE_MMA_FULL)) {
+            ok = false;
+            break;
+          }
+          // rows [last, next multiple of 32) of P and Q; a row's 128 bytes are
+          // the same under the swizzle
+          const uint32_t sp = sbase + s * C::STAGE_BYTES;
+          const int rows = 32 - (t.last & 31);
+          for (int i = lane; i < 2 * rows * 8; i += 32) {
+            const int ch = i / (rows * 8), rr = i - ch * rows * 8;
+            st_shared_v4((ch ? sp + C::P_BYTES : sp) + 128u * (t.last + (rr >> 3)) + 16u * (rr & 7), 0u, 0u, 0u, 0u);
+          }
+          fence_proxy_async_shared();
+          __syncwarp();
+          if constexpr (CG == 2) {
+            if (rank != 0) {
+              if (lane == 0) mbar_arrive_cluster(mapa_shared(peer_bar(s), 0));
+            } else if (!warp_wait(peer_bar(s), par, wctx, SITE_MMA_FULL) || !mbar_try_wait_cluster(peer_bar(s), par)) {
+              ok = false;
+              break;
+            }
+          }
+        }
+        if (issue) {
+          tc_fence_after();
+          if (elect_one()) {
+            const uint64_t st = (s * static_cast<uint32_t>(C::STAGE_BYTES)) >> 4;
+            const int steps = p.weight && last ? (t.last + 31) >> 5 : 4;
+#pragma unroll
+            for (int j = 0; j < 4; ++j)
+              if (j < steps)
+                mma_f8<CG>(d_tmem, p_desc0 + st + j * p.p_kstep, q_desc0 + st + j * p.q_kstep, idesc, j ? 1u : 0u);
+            tc_commit<CG>(empty_bar(s));
+            tc_commit<CG>(accf_bar(b));
+          }
+          __syncwarp();
+        }
+        if (++s == STAGES) {
+          s = 0;
+          ph ^= 1u;
+        }
+      }
+    }
+    if (!ok && (CG == 1 || rank == 0) && elect_one()) {
+      tc_commit<CG>(drain_bar);
+      const uint64_t t0 = globaltimer();
+      while (!mbar_try_wait(drain_bar, 0) && globaltimer() - t0 < 20000000ull) {
+      }
+    }
+    __syncwarp();
+  } else if (warp >= 4) {
+    // ------------------------------------------------------------ epilogue
+    const int q = warp & 3;            // TMEM lane quadrant
+    const int part = (warp - 4) >> 2;  // 32-column chunks part, part + 2, ...
+    constexpr int MINE = (BN + 63) / 64;
+    uint32_t tcount = 0, n = 0, stores = 0;
+    const uint32_t buf0 = sbase + C::EPI_OFF + static_cast<uint32_t>((warp - 4) * 2 * STAGING_BYTES);
+    // the staging tile to fill next: its store before the last has read it
+    auto staging = [&] {
+      if (stores >= 2) {
+        if (lane == 0) bulk_wait_group_read<1>();
+        __syncwarp();
+      }
+      return buf0 + (stores & 1u) * STAGING_BYTES;
+    };
+    auto send = [&](uint32_t buf, int m0, int c, int g) {
+      fence_proxy_async_shared();
+      __syncwarp();
+      if (lane == 0) {
+        tma_store_3d(&p.tmap_d, buf, m0, c, g);
+        bulk_commit_group();
+      }
+      ++stores;
+    };
+    const uint32_t lanes = tmem_base + (static_cast<uint32_t>(32 * q) << 16);
+    for (int u = cluster_id; u < total_units; u += num_clusters) {
+      FTile t;
+      if (!fetch(n++, t)) break;
+      uint64_t sum[MINE][16];  // pairs of columns
+#pragma unroll
+      for (int i = 0; i < MINE; ++i)
+#pragma unroll
+        for (int k = 0; k < 16; ++k) sum[i][k] = 0ull;
+      bool done = true;
+      for (int kb = 0; kb < t.nkb; ++kb, ++tcount) {
+        const uint32_t b = tcount & 1u, slot = tcount % SLOTS;
+        done = wait_uniform(scf_bar(slot), (tcount / SLOTS) & 1u, wctx, SITE_EPI_ACC_FULL) &&
+               wait_uniform(accf_bar(b), (tcount >> 1) & 1u, wctx, SITE_EPI_ACC_FULL);
+        if (!done) break;
+        tc_fence_after();
+        const uint32_t at = slot_at(slot);
+        uint64_t row = 0;
+        if constexpr (VEC) {
+          const uint32_t r = __float_as_uint(ld_shared_f32(at + 4u * BN + 4u * (32 * q + lane)));
+          row = pair(r, r);
+        }
+#pragma unroll
+        for (int i = 0; i < MINE; ++i) {
+          const int c = 32 * part + 64 * i;
+          if (c >= t.ncols) break;
+          uint32_t r[32];
+          tmem_ld_32x32b_x32(lanes + b * BN + c, r);
+          tc_wait_ld();
+#pragma unroll
+          for (int k = 0; k < 16; k += 2) {
+            uint64_t f0, f1;
+            ld_shared_2x64(at + 4u * (c + 2 * k), f0, f1);
+            if constexpr (VEC) {
+              sum[i][k] = fma2(mul2(pair(r[2 * k], r[2 * k + 1]), f0), row, sum[i][k]);
+              sum[i][k + 1] = fma2(mul2(pair(r[2 * k + 2], r[2 * k + 3]), f1), row, sum[i][k + 1]);
+            } else {
+              sum[i][k] = fma2(pair(r[2 * k], r[2 * k + 1]), f0, sum[i][k]);
+              sum[i][k + 1] = fma2(pair(r[2 * k + 2], r[2 * k + 3]), f1, sum[i][k + 1]);
+            }
+          }
+        }
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) {
+          mbar_arrive(sce_bar(slot));
+          if constexpr (CG == 2)
+            mbar_arrive_relaxed(mapa_shared(acce_bar(b), 0));  // no memory to order, only TMEM reads
+          else
+            mbar_arrive(acce_bar(b));
+        }
+      }
+      if (!done) break;
+      const int m_warp = t.m0 + static_cast<int>(rank) * 128 + 32 * q;
+      const int m = m_warp + lane;
+      const bool m_ok = m < p.M;
+      const int row0 = p.weight ? t.c0 : t.lo + t.c0, outer = p.weight ? t.g : 0;
+      const int64_t pitch = p.ldd * p.d_size;
+      uint8_t* dst = static_cast<uint8_t*>(p.D) + static_cast<int64_t>(row0) * pitch +
+                     (p.weight ? t.g * p.stride_d * p.d_size : 0) + static_cast<int64_t>(m) * p.d_size;
+#pragma unroll
+      for (int i = 0; i < MINE; ++i) {
+        const int c = 32 * part + 64 * i;
+        if (c >= t.ncols || m_warp >= p.M) break;
+        // rows of a matrix clip at the map's end, rows of a group do not
+        const bool boxed = p.d_tma && (p.weight || c + 32 <= t.ncols);
+        if (p.d_type == OUT_F32) {
+#pragma unroll
+          for (int h = 0; h < 32; h += 16) {  // a staging tile holds 16 rows of 32 m
+            const uint32_t buf = boxed ? staging() : 0u;
+#pragma unroll
+            for (int k = 0; k < 16; k += 2) {
+              uint32_t lo, hi;
+              unpair(sum[i][(h + k) / 2], lo, hi);
+              if (boxed) {
+                st_shared_u32(buf + 128u * k + 4u * lane, lo);
+                st_shared_u32(buf + 128u * (k + 1) + 4u * lane, hi);
+              } else {
+                uint8_t* d = dst + (c + h + k) * pitch;
+                if (m_ok && c + h + k < t.ncols) *reinterpret_cast<uint32_t*>(d) = lo;
+                if (m_ok && c + h + k + 1 < t.ncols) *reinterpret_cast<uint32_t*>(d + pitch) = hi;
+              }
+            }
+            if (boxed) send(buf, m_warp, row0 + c + h, outer);
+          }
+          continue;
+        }
+        const uint32_t buf = boxed ? staging() : 0u;
+#pragma unroll
+        for (int k = 0; k < 32; k += 2) {
+          uint32_t lo, hi;
+          unpair(sum[i][k / 2], lo, hi);
+          const uint32_t h = p.d_type == OUT_BF16 ? pack_bf16(lo, hi) : pack_f16(lo, hi);
+          if (boxed) {
+            // rows of 64 bytes, their four 16-byte words swizzled
+            const uint32_t to = buf + 64u * k + 16u * ((static_cast<uint32_t>(lane) >> 3) ^ ((k >> 1) & 3u)) + 2u * (lane & 7);
+            st_shared_u16(to, h);
+            st_shared_u16(to + 64u, h >> 16);
+          } else {
+            uint8_t* d = dst + (c + k) * pitch;
+            if (m_ok && c + k < t.ncols) *reinterpret_cast<uint16_t*>(d) = static_cast<uint16_t>(h);
+            if (m_ok && c + k + 1 < t.ncols) *reinterpret_cast<uint16_t*>(d + pitch) = static_cast<uint16_t>(h >> 16);
+          }
+        }
+        if (boxed) send(buf, m_warp, row0 + c, outer);
+      }
+    }
+    if (lane == 0) bulk_wait_group_all();
+    __syncwarp();
+    if (!p.weight) {
+      // rows of no group (and all rows when K is 0): zero
+      const int t = threadIdx.x - 128;
+      const int first = seg[0], end = p.K > 0 ? seg[p.G] : first;
+      for (int r = blockIdx.x; r < p.R; r += gridDim.x) {
+        if (r >= first && r < end) {
+          r += (end - 1 - r) / gridDim.x * gridDim.x;  // the last row below `end` this block meets
+          continue;
+        }
+        for (int m = t; m < p.M; m += 32 * EPI_WARPS) {
+          const int64_t i = r * p.ldd + m;
+          if (p.d_type == OUT_F32)
+            static_cast<float*>(p.D)[i] = 0.0f;
+          else
+            static_cast<uint16_t*>(p.D)[i] = 0;
+        }
+      }
+    }
+  }
+
+  // ------------------------------------------------------------ teardown
+  tc_fence_before();
+  cta_barrier_unaligned();
+  __syncwarp();
+  if constexpr (CG == 2) cluster_sync();
+  tc_fence_after();
+  if (warp == 2) tmem_dealloc<CG>(tmem_base, 512);
+}
+
+// ---------------------------------------------------------------------- host
+
+template <int CG, int BN, int STAGES, bool VEC>
+KernelInfo variant() {
+  using C = F8Cfg<CG, BN, STAGES, VEC>;
+  return {reinterpret_cast<const void*>(&f8_kernel<CG, BN, STAGES, VEC>), C::SMEM_BYTES, CG, BN, KIND_F16, F8_THREADS};
+}
+
+int64_t ceil_div(int64_t a, int64_t b) { return (a + b - 1) / b; }
+bool misaligned(const void* p, unsigned n) { return reinterpret_cast<uintptr_t>(p) % n != 0; }
+
+int check_problem(tcg_input in_type, int64_t R, int64_t N, int64_t K, int G, tcg_dtype d_type) {
+  if (in_type != TCG_IN_E4M3 && in_type != TCG_IN_E5M2) return TCG_ERR_INVALID;
+  if (R < 0 || N < 0 || K < 0 || G < 1 || d_type < TCG_F32 || d_type > TCG_BF16) return TCG_ERR_INVALID;
+  if (R >= MAX_EXTENT || N >= MAX_EXTENT || K >= MAX_EXTENT || G > MAX_GROUPS) return TCG_ERR_UNSUPPORTED;
+  return TCG_OK;
+}
+
+// A matrix of codes: rows of `inner`, 16-byte aligned
+int check_codes(const void* p, int64_t inner, int64_t* ld) {
+  if (*ld == 0) *ld = inner;
+  if (!p || *ld < inner || *ld < 1) return TCG_ERR_INVALID;
+  return misaligned(p, 16) || *ld % 16 ? TCG_ERR_ALIGNMENT : TCG_OK;
+}
+
+int check_scales(const float* p, int64_t inner, int64_t* ld) {
+  if (*ld == 0) *ld = inner;
+  if (!p || *ld < inner) return TCG_ERR_INVALID;
+  return misaligned(p, 4) ? TCG_ERR_ALIGNMENT : TCG_OK;
+}
+
+int check_output(const void* p, int64_t inner, int64_t* ld, tcg_dtype type) {
+  if (*ld == 0) *ld = inner;
+  if (!p || *ld < inner) return TCG_ERR_INVALID;
+  return misaligned(p, type == TCG_F32 ? 4 : 2) ? TCG_ERR_ALIGNMENT : TCG_OK;
+}
+
+// Fills what the operands' majors decide: descriptors, steps and maps.  P is
+// [groups][rows m][K] or, MN-major, [groups][K][M]; Q likewise without groups.
+int set_operands(F8Params* p, const KernelInfo& ki, tcg_input type, const void* P, bool p_mn, int64_t ldp,
+                 int64_t stride_p, int64_t groups, int64_t p_depth, const void* Q, bool q_mn, int64_t ldq,
+                 int64_t q_extent, int64_t q_depth) {
+  p->p_mn = p_mn;
+  p->q_mn = q_mn;
+  p->p_hi = p_mn ? sdesc_hi(128 * BLOCK, 1024, SW_128B) : sdesc_hi(16, 1024, SW_128B);
+  p->q_hi = q_mn ? sdesc_hi(128 * BLOCK, 1024, SW_128B) : sdesc_hi(16, 1024, SW_128B);
+  p->p_kstep = p_mn ? 32 * 128 / 16 : 32 / 16;
+  p->q_kstep = q_mn ? 32 * 128 / 16 : 32 / 16;
+  const uint32_t format = type == TCG_IN_E5M2 ? MXF_E5M2 : MXF_E4M3;
+  // kind::f8f6f4's descriptor: D fp32, then formats, majors and sizes as of kind::f16
+  p->idesc = (1u << 4) | (format << 7) | (format << 10) | (static_cast<uint32_t>(p_mn) << 15) |
+             (static_cast<uint32_t>(q_mn) << 16) | (static_cast<uint32_t>(128 * ki.cta_group >> 4) << 24);
+  if (p_depth == 0) return TCG_OK;
+  const uint64_t M = p->M;
+  if (int rc = p_mn ? make_byte_map(&p->tmap_p, P, M, p_depth, groups, ldp, stride_p, 128, BLOCK)
+                    : make_byte_map(&p->tmap_p, P, p_depth, M, groups, ldp, stride_p, 128, 128))
+    return rc;
+  if (q_mn) return make_byte_map(&p->tmap_q, Q, q_extent, q_depth, 1, ldq, q_depth * ldq, 128, BLOCK);
+  if (int rc = make_byte_map(&p->tmap_q, Q, q_depth, q_extent, 1, ldq, q_extent * ldq, 128,
+                             static_cast<uint32_t>(ki.bn / ki.cta_group)))
+    return rc;
+  return make_byte_map(&p->tmap_q16, Q, q_depth, q_extent, 1, ldq, q_extent * ldq, 128, 16);
+}
+
+// Launches the variant on all SMs (or on fewer, never more than `units`
+// clusters), as a programmatic dependent of the stream's previous kernel.
+int launch_f8(const KernelInfo& ki, F8Params& p, int dev, int64_t units, cudaStream_t s) {
+  if (units > INT32_MAX / 2) return TCG_ERR_UNSUPPORTED;
+  int clusters = 0;
+  if (int rc = max_resident_clusters(dev, ki, &clusters)) return rc;
+  const int cg = ki.cta_group;
+  p.d_size = p.d_type == TCG_F32 ? 4 : 2;
+  // TMA stores where the output's rows and matrices are 16-byte aligned and
+  // end on such a boundary
+  const int64_t low = reinterpret_cast<int64_t>(p.D) | p.ldd * p.d_size | p.stride_d * p.d_size |
+                      static_cast<int64_t>(p.M) * p.d_size;
+  p.d_tma = low % 16 == 0;
+  if (p.d_tma) {
+    const uint64_t rows = static_cast<uint64_t>(p.weight ? p.C : p.R), outer = p.weight ? p.G : 1;
+    if (int rc = make_store_map(&p.tmap_d, p.D, static_cast<tcg_dtype>(p.d_type), p.M, rows, outer, p.ldd,
+                                p.weight ? p.stride_d : p.R * p.ldd))
+      return rc;
+  }
+  p.err = device_error_word(dev);
+  p.timeout_ns = wait_timeout_ns();
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(static_cast<unsigned>(cg * std::max<int64_t>(1, std::min<int64_t>(units, clusters))), 1, 1);
+  cfg.blockDim = dim3(F8_THREADS, 1, 1);
+  cfg.dynamicSmemBytes = ki.smem_bytes;
+  cfg.stream = s;
+  cudaLaunchAttribute attr[2];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  attr[1].id = cudaLaunchAttributeClusterDimension;
+  attr[1].val.clusterDim.x = cg;
+  attr[1].val.clusterDim.y = 1;
+  attr[1].val.clusterDim.z = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = cg > 1 ? 2 : 1;
+  void* args[] = {&p};
+  if (int rc = record_cuda(cudaLaunchKernelExC(&cfg, ki.func, args))) return rc;
+  set_launch_count(1);
+  record_grouped_plan(cg, ki.bn, static_cast<int>(cfg.gridDim.x) / cg);
+  return TCG_OK;
+}
+
+KernelInfo rows_variant(int64_t R, int G, bool q_mn, bool vec) {
+  if (vec) return variant<2, 256, 5, true>();
+  if (!q_mn && R <= 64 * static_cast<int64_t>(G)) return variant<1, 64, 7, false>();
+  return variant<2, 256, 5, false>();
+}
+
+int run_dense(tcg_input type, int64_t M, int64_t N, int64_t K, const void* A, tcg_major a_major, int64_t lda,
+              const float* SA, int64_t ld_sa, const void* B, tcg_major b_major, int64_t ldb, const float* SB,
+              int64_t ld_sb, int sb_square, void* D, tcg_dtype d_type, int64_t ldd, cudaStream_t s) {
+  begin_product();
+  if (int rc = check_problem(type, M, N, K, 1, d_type)) return rc;
+  if (a_major != TCG_K_MAJOR && a_major != TCG_MN_MAJOR) return TCG_ERR_INVALID;
+  if (b_major != TCG_K_MAJOR && b_major != TCG_MN_MAJOR) return TCG_ERR_INVALID;
+  if (M == 0 || N == 0) return TCG_OK;
+  if (int rc = check_output(D, N, &ldd, d_type)) return rc;
+  const bool a_mn = a_major == TCG_MN_MAJOR, b_mn = b_major == TCG_MN_MAJOR;
+  const int64_t kb = ceil_div(K, BLOCK), nb = ceil_div(N, BLOCK);
+  if (K > 0) {
+    if (int rc = check_codes(A, a_mn ? M : K, &lda)) return rc;
+    if (int rc = check_codes(B, b_mn ? N : K, &ldb)) return rc;
+    if (int rc = check_scales(SA, M, &ld_sa)) return rc;
+    if (int rc = check_scales(SB, !sb_square ? N : b_mn ? nb : kb, &ld_sb)) return rc;
+  }
+  int dev;
+  if (int rc = current_device_checked(&dev)) return rc;
+  const KernelInfo ki = rows_variant(M, 1, a_mn, !sb_square);
+  F8Params p;
+  std::memset(&p, 0, sizeof p);
+  p.G = 1;
+  p.R = static_cast<int>(M);
+  p.M = static_cast<int>(N);
+  p.K = static_cast<int>(K);
+  p.m_tiles = static_cast<int>(ceil_div(N, 128 * ki.cta_group));
+  if (int rc = set_operands(&p, ki, type, B, b_mn, ldb, (b_mn ? K : N) * ldb, 1, K, A, a_mn, lda, M, K)) return rc;
+  p.sq = SA;
+  p.sq_b = ld_sa;
+  p.sp = SB;
+  p.sp_m = b_mn ? 1 : ld_sb;
+  p.sp_b = !sb_square || b_mn ? ld_sb : 1;
+  p.D = D;
+  p.ldd = ldd;
+  p.d_type = d_type;
+  return launch_f8(ki, p, dev, (M / ki.bn + 1) * 2 * p.m_tiles, s);
+}
+
+int run_grouped(tcg_input type, int64_t R, int64_t N, int64_t K, int G, const void* A, int64_t lda, const float* SA,
+                int64_t ld_sa, const int32_t* offsets, const void* B, tcg_major b_major, int64_t ldb, int64_t stride_b,
+                const float* SB, int64_t ld_sb, int64_t stride_sb, void* D, tcg_dtype d_type, int64_t ldd,
+                cudaStream_t s) {
+  begin_product();
+  if (int rc = check_problem(type, R, N, K, G, d_type)) return rc;
+  if (b_major != TCG_K_MAJOR && b_major != TCG_MN_MAJOR) return TCG_ERR_INVALID;
+  if (R == 0 || N == 0) return TCG_OK;
+  if (int rc = check_output(D, N, &ldd, d_type)) return rc;
+  if (!offsets) return TCG_ERR_INVALID;
+  if (misaligned(offsets, 4)) return TCG_ERR_ALIGNMENT;
+  const bool mn = b_major == TCG_MN_MAJOR;
+  const int64_t kb = ceil_div(K, BLOCK), nb = ceil_div(N, BLOCK);
+  if (K > 0) {
+    if (int rc = check_codes(A, K, &lda)) return rc;
+    if (int rc = check_codes(B, mn ? N : K, &ldb)) return rc;
+    if (stride_b == 0) stride_b = (mn ? K : N) * ldb;
+    if (stride_b < 0) return TCG_ERR_INVALID;
+    if (stride_b % 16) return TCG_ERR_ALIGNMENT;
+    if (int rc = check_scales(SA, R, &ld_sa)) return rc;
+    if (int rc = check_scales(SB, mn ? nb : kb, &ld_sb)) return rc;
+    if (stride_sb == 0) stride_sb = (mn ? kb : nb) * ld_sb;
+    if (stride_sb < 0) return TCG_ERR_INVALID;
+  }
+  int dev;
+  if (int rc = current_device_checked(&dev)) return rc;
+  const KernelInfo ki = rows_variant(R, G, false, false);
+  F8Params p;
+  std::memset(&p, 0, sizeof p);
+  p.offsets = offsets;
+  p.G = G;
+  p.R = static_cast<int>(R);
+  p.M = static_cast<int>(N);
+  p.K = static_cast<int>(K);
+  p.m_tiles = static_cast<int>(ceil_div(N, 128 * ki.cta_group));
+  if (int rc = set_operands(&p, ki, type, B, mn, ldb, stride_b, G, K, A, false, lda, R, K)) return rc;
+  p.sq = SA;
+  p.sq_b = ld_sa;
+  p.sp = SB;
+  p.sp_group = stride_sb;
+  p.sp_m = mn ? 1 : ld_sb;
+  p.sp_b = mn ? ld_sb : 1;
+  p.D = D;
+  p.ldd = ldd;
+  p.d_type = d_type;
+  // an upper bound of the units: a full tile per BN rows and one more per group
+  return launch_f8(ki, p, dev, (R / ki.bn + std::min<int64_t>(G, R)) * 2 * p.m_tiles, s);
+}
+
+int run_wgrad(tcg_input type, int64_t R, int64_t N, int64_t K, int G, const void* DY, int64_t lddy, const float* SDY,
+              int64_t ld_sdy, const void* A, int64_t lda, const float* SA, int64_t ld_sa, const int32_t* offsets,
+              void* DW, tcg_dtype dw_type, int64_t lddw, int64_t stride_dw, cudaStream_t s) {
+  begin_product();
+  if (int rc = check_problem(type, R, N, K, G, dw_type)) return rc;
+  if (N == 0 || K == 0) return TCG_OK;
+  if (int rc = check_output(DW, K, &lddw, dw_type)) return rc;
+  if (stride_dw == 0) stride_dw = N * lddw;
+  if (stride_dw < 0) return TCG_ERR_INVALID;
+  if (!offsets) return TCG_ERR_INVALID;
+  if (misaligned(offsets, 4)) return TCG_ERR_ALIGNMENT;
+  if (R > 0) {
+    if (int rc = check_codes(DY, N, &lddy)) return rc;
+    if (int rc = check_codes(A, K, &lda)) return rc;
+    if (int rc = check_scales(SDY, N, &ld_sdy)) return rc;
+    if (int rc = check_scales(SA, K, &ld_sa)) return rc;
+  }
+  int dev;
+  if (int rc = current_device_checked(&dev)) return rc;
+  const KernelInfo ki = rows_variant(R, G, true, true);
+  F8Params p;
+  std::memset(&p, 0, sizeof p);
+  p.offsets = offsets;
+  p.G = G;
+  p.R = static_cast<int>(R);
+  p.weight = 1;
+  p.M = static_cast<int>(K);
+  p.C = static_cast<int>(N);
+  p.m_tiles = static_cast<int>(ceil_div(K, 128 * ki.cta_group));
+  if (int rc = set_operands(&p, ki, type, A, true, lda, R * lda, 1, R, DY, true, lddy, N, R)) return rc;
+  p.sq = SDY;
+  p.sq_b = ld_sdy;
+  p.sp = SA;
+  p.sp_b = ld_sa;
+  p.D = DW;
+  p.ldd = lddw;
+  p.stride_d = stride_dw;
+  p.d_type = dw_type;
+  return launch_f8(ki, p, dev, static_cast<int64_t>(G) * ceil_div(N, ki.bn) * p.m_tiles, s);
+}
+
+}  // namespace
+
+}  // namespace tcg
+
+using namespace tcg;
+
+extern "C" {
+
+int tcg_gemm_f8(tcg_input in_type, int64_t M, int64_t N, int64_t K, const void* A, tcg_major a_major, int64_t lda,
+                const float* SA, int64_t ld_sa, const void* B, tcg_major b_major, int64_t ldb, const float* SB,
+                int64_t ld_sb, int sb_square, void* D, tcg_dtype d_type, int64_t ldd, void* stream) {
+  return guarded([&] {
+    return run_dense(in_type, M, N, K, A, a_major, lda, SA, ld_sa, B, b_major, ldb, SB, ld_sb, sb_square, D, d_type, ldd,
+                     static_cast<cudaStream_t>(stream));
+  });
+}
+
+int tcg_gemm_f8_grouped(tcg_input in_type, int64_t R, int64_t N, int64_t K, int G, const void* A, int64_t lda,
+                        const float* SA, int64_t ld_sa, const int32_t* offsets, const void* B, tcg_major b_major,
+                        int64_t ldb, int64_t stride_b, const float* SB, int64_t ld_sb, int64_t stride_sb, void* D,
+                        tcg_dtype d_type, int64_t ldd, void* stream) {
+  return guarded([&] {
+    return run_grouped(in_type, R, N, K, G, A, lda, SA, ld_sa, offsets, B, b_major, ldb, stride_b, SB, ld_sb, stride_sb,
+                       D, d_type, ldd, static_cast<cudaStream_t>(stream));
+  });
+}
+
+int tcg_gemm_f8_grouped_wgrad(tcg_input in_type, int64_t R, int64_t N, int64_t K, int G, const void* DY, int64_t lddy,
+                              const float* SDY, int64_t ld_sdy, const void* A, int64_t lda, const float* SA,
+                              int64_t ld_sa, const int32_t* offsets, void* DW, tcg_dtype dw_type, int64_t lddw,
+                              int64_t stride_dw, void* stream) {
+  return guarded([&] {
+    return run_wgrad(in_type, R, N, K, G, DY, lddy, SDY, ld_sdy, A, lda, SA, ld_sa, offsets, DW, dw_type, lddw, stride_dw,
+                     static_cast<cudaStream_t>(stream));
+  });
+}
+
+}  // extern "C"

@@ -389,6 +389,78 @@ typedef struct {
 int tcg_gemv_w4(const tcg_gemv_w4_args* args, void* stream);
 
 /* ---------------------------------------------------------------------------
+ * 8-bit floating point (E4M3 or E5M2) with an fp32 scale for each block of
+ * 128: the quantiser, and the products that add each block's sum, scaled, in
+ * fp32.
+ *
+ * Scales of blocks of 128 along one dimension (a row of 128, or a column) lie
+ * block by block: [block][row or column], the element of row or column i of
+ * block b at scale[b * ld_scale + i].  Scales of square blocks lie as the
+ * blocks do in the stored matrix: [row / 128][column / 128].  The last block of
+ * a dimension may be shorter.
+ * ------------------------------------------------------------------------- */
+typedef enum {
+  TCG_F8_ROW = 0,    /* 1 x 128 */
+  TCG_F8_COLUMN = 1, /* 128 x 1 */
+  TCG_F8_SQUARE = 2  /* 128 x 128 */
+} tcg_f8_blocks;
+
+/* Codes and scales of X [R][C] (x_type).  With a the largest magnitude of a
+ * block (NaN are passed over) and F the largest value of q_type (TCG_IN_E4M3
+ * 448, TCG_IN_E5M2 57344):
+ *     scale = a / F rounded to fp32, but at least 2^-126
+ *     code  = F x / a, rounded once to the nearest (ties to even)
+ * pow2 != 0: scale is the smallest power of two >= a / F and >= 2^-126, code =
+ * x / scale rounded.  (So is it where the bound 2^-126 applies.)  Zeros alone:
+ * scale 1.  An infinity in a block: scale infinite, finite values' codes 0,
+ * infinities' NaN.  NaN have NaN codes.
+ * scale: ROW [ceil(C / 128)][ld_scale >= R], COLUMN [blocks][ld_scale >= C],
+ * SQUARE [ceil(R / 128)][ld_scale >= ceil(C / 128)]; ld 0 = packed.
+ * offsets (device, [G+1], rising, with COLUMN only; else NULL and G = 1): rows
+ * [offsets[g], offsets[g+1]) are group g, whose blocks begin at offsets[g];
+ * its block j is scale row offsets[g] / 128 + g + j, in all R / 128 + G rows
+ * (rounded down).  Codes of rows of no group and scale rows of no block are
+ * left as they are.  X, scale element aligned; rows whose bases and strides are
+ * 16-byte (Q: 4- or 8-byte) multiples move in words.  R, C < 2^30, G <= 1024. */
+int tcg_f8_quantize(tcg_input q_type, tcg_f8_blocks blocks, int pow2, int64_t R, int64_t C, tcg_dtype x_type,
+                    const void* X, int64_t ldx, int G, const int32_t* offsets, void* Q, int64_t ldq, float* scale,
+                    int64_t ld_scale, void* stream);
+
+/* D[m, n] = sum over blocks b of 128 k:
+ *     SA[b, m] * SB[b, n] * sum_{k in b} A[m, k] * B[k, n]
+ * A and B hold codes of in_type (TCG_IN_E4M3 or TCG_IN_E5M2), majors and
+ * leading dimensions as of the dense GEMMs (16-byte aligned bases and rows).
+ * SA: blocks of 128 along k, SA[b * ld_sa + m] (ld 0 = M): TCG_F8_ROW scales of
+ * a K-major A, TCG_F8_COLUMN ones of an MN-major A.  SB: the same with n
+ * (sb_square 0, ld 0 = N), or one for each 128 x 128 of the stored matrix
+ * (sb_square 1): [ceil(N/128)][ceil(K/128)] of a K-major B, [ceil(K/128)]
+ * [ceil(N/128)] of an MN-major one.  A block's sum is the tensor cores'; blocks
+ * are added in fp32, rounded once each; D is rounded once.  Forward
+ * X W^T: both K-major.  Rows' gradient dY W: B = W, MN-major, square scales.
+ * Matrix' gradient dY^T X: both MN-major.  K == 0: D = 0. */
+int tcg_gemm_f8(tcg_input in_type, int64_t M, int64_t N, int64_t K, const void* A, tcg_major a_major, int64_t lda,
+                const float* SA, int64_t ld_sa, const void* B, tcg_major b_major, int64_t ldb, const float* SB,
+                int64_t ld_sb, int sb_square, void* D, tcg_dtype d_type, int64_t ldd, void* stream);
+
+/* tcg_gemm_grouped on codes: D[r, n] of the rows [offsets[g], offsets[g+1]) with
+ * B[g].  A [R][K] with TCG_F8_ROW scales SA [ceil(K/128)][ld_sa >= R]; B[g] with
+ * square scales at SB + g * stride_sb (0 = packed).  Rows of no group give zero;
+ * offsets as of tcg_gemm_grouped. */
+int tcg_gemm_f8_grouped(tcg_input in_type, int64_t R, int64_t N, int64_t K, int G, const void* A, int64_t lda,
+                        const float* SA, int64_t ld_sa, const int32_t* offsets, const void* B, tcg_major b_major,
+                        int64_t ldb, int64_t stride_b, const float* SB, int64_t ld_sb, int64_t stride_sb, void* D,
+                        tcg_dtype d_type, int64_t ldd, void* stream);
+
+/* tcg_gemm_grouped_wgrad on codes: DW[g][n, k] = sum over the group's rows of
+ * DY[r, n] A[r, k], blocks of 128 rows counted from the group's first, with the
+ * scales of tcg_f8_quantize's grouped TCG_F8_COLUMN blocks: SDY [R/128 + G]
+ * [ld_sdy >= N], SA [R/128 + G][ld_sa >= K]. */
+int tcg_gemm_f8_grouped_wgrad(tcg_input in_type, int64_t R, int64_t N, int64_t K, int G, const void* DY, int64_t lddy,
+                              const float* SDY, int64_t ld_sdy, const void* A, int64_t lda, const float* SA,
+                              int64_t ld_sa, const int32_t* offsets, void* DW, tcg_dtype dw_type, int64_t lddw,
+                              int64_t stride_dw, void* stream);
+
+/* ---------------------------------------------------------------------------
  * Block-scale layout (the scale-factor rearrangement step).
  *
  * The "tcgen05.mma" page places the scale of row r at TMEM lane r%32,

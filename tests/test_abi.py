@@ -363,3 +363,92 @@ def test_moe_refuses_sizes_whose_product_overflows(tcg):
                             None) == tcg.ERR_UNSUPPORTED
         assert tcg.raw_call("tcg_moe_combine_grad", 2, *big, 0x10000, 0, None, 0, 0x20000, None, 0x50000, 0, None,
                             None) == tcg.ERR_UNSUPPORTED
+
+
+def test_f8_quantize_validation_before_any_device_work(tcg):
+    def call(q=3, b=0, pow2=0, R=64, C=64, t=2, X=0x10000, ldx=0, G=1, off=None, Q=0x20000, ldq=0, s=0x30000, lds=0):
+        return tcg.raw_call("tcg_f8_quantize", q, b, pow2, R, C, t, X, ldx, G, off, Q, ldq, s, lds, None)
+    assert call(q=2) == tcg.ERR_INVALID
+    assert call(q=5) == tcg.ERR_INVALID
+    assert call(b=3) == tcg.ERR_INVALID
+    assert call(t=3) == tcg.ERR_INVALID
+    assert call(R=-1) == tcg.ERR_INVALID
+    assert call(G=0) == tcg.ERR_INVALID
+    assert call(G=2) == tcg.ERR_INVALID                       # groups need offsets
+    assert call(b=0, G=2, off=0x40000) == tcg.ERR_INVALID     # and columns
+    assert call(b=1, G=1025, off=0x40000) == tcg.ERR_UNSUPPORTED
+    assert call(R=1 << 30) == tcg.ERR_UNSUPPORTED
+    assert call(C=1 << 30) == tcg.ERR_UNSUPPORTED
+    for p in ("X", "Q", "s"):
+        assert call(**{p: None}) == tcg.ERR_INVALID
+    assert call(ldx=63) == tcg.ERR_INVALID
+    assert call(ldq=63) == tcg.ERR_INVALID
+    assert call(R=65, lds=64) == tcg.ERR_INVALID              # rows' scales: [block][row]
+    assert call(b=1, lds=63) == tcg.ERR_INVALID
+    assert call(b=2, C=129, lds=1) == tcg.ERR_INVALID
+    assert call(X=0x10001) == tcg.ERR_ALIGNMENT
+    assert call(t=0, X=0x10002) == tcg.ERR_ALIGNMENT
+    assert call(s=0x30002) == tcg.ERR_ALIGNMENT
+    assert call(b=1, G=2, off=0x40002) == tcg.ERR_ALIGNMENT
+    assert call(R=0, X=None, Q=None, s=None) == tcg.OK
+    assert call(C=0, X=None, Q=None, s=None) == tcg.OK
+
+
+def test_gemm_f8_validation_before_any_device_work(tcg):
+    def call(t=3, M=64, N=64, K=64, A=0x10000, am=0, lda=0, SA=0x20000, ldsa=0, B=0x30000, bm=0, ldb=0, SB=0x40000,
+             ldsb=0, sq=1, D=0x50000, dt=2, ldd=0):
+        return tcg.raw_call("tcg_gemm_f8", t, M, N, K, A, am, lda, SA, ldsa, B, bm, ldb, SB, ldsb, sq, D, dt, ldd, None)
+    assert call(t=1) == tcg.ERR_INVALID
+    assert call(t=5) == tcg.ERR_INVALID
+    assert call(M=-1) == tcg.ERR_INVALID
+    assert call(M=1 << 30) == tcg.ERR_UNSUPPORTED
+    assert call(am=2) == tcg.ERR_INVALID
+    assert call(bm=2) == tcg.ERR_INVALID
+    assert call(dt=3) == tcg.ERR_INVALID
+    for p in ("A", "SA", "B", "SB", "D"):
+        assert call(**{p: None}) == tcg.ERR_INVALID
+    assert call(lda=48) == tcg.ERR_INVALID
+    assert call(ldb=48) == tcg.ERR_INVALID
+    assert call(ldd=63) == tcg.ERR_INVALID
+    assert call(ldsa=63) == tcg.ERR_INVALID
+    assert call(K=256, ldsb=1) == tcg.ERR_INVALID             # [N/128][K/128]
+    assert call(N=256, bm=1, ldsb=1) == tcg.ERR_INVALID       # [K/128][N/128]
+    assert call(sq=0, ldsb=63) == tcg.ERR_INVALID             # [K/128][N]
+    assert call(K=60) == tcg.ERR_ALIGNMENT
+    assert call(M=60, am=1) == tcg.ERR_ALIGNMENT
+    assert call(A=0x10008) == tcg.ERR_ALIGNMENT
+    assert call(B=0x30008) == tcg.ERR_ALIGNMENT
+    assert call(SA=0x20002) == tcg.ERR_ALIGNMENT
+    assert call(D=0x50001) == tcg.ERR_ALIGNMENT
+    assert call(M=0, A=None, SA=None, B=None, SB=None, D=None) == tcg.OK
+
+    def grouped(t=3, R=64, N=64, K=64, G=4, A=0x10000, lda=0, SA=0x20000, ldsa=0, off=0x60000, B=0x30000, bm=0, ldb=0,
+                sb=0, SB=0x40000, ldsb=0, ssb=0, D=0x50000, dt=2, ldd=0):
+        return tcg.raw_call("tcg_gemm_f8_grouped", t, R, N, K, G, A, lda, SA, ldsa, off, B, bm, ldb, sb, SB, ldsb, ssb, D,
+                            dt, ldd, None)
+    assert grouped(t=0) == tcg.ERR_INVALID
+    assert grouped(G=0) == tcg.ERR_INVALID
+    assert grouped(G=1025) == tcg.ERR_UNSUPPORTED
+    for p in ("A", "SA", "off", "B", "SB", "D"):
+        assert grouped(**{p: None}) == tcg.ERR_INVALID
+    assert grouped(sb=-16) == tcg.ERR_INVALID
+    assert grouped(ssb=-1) == tcg.ERR_INVALID
+    assert grouped(sb=64 * 64 + 8) == tcg.ERR_ALIGNMENT
+    assert grouped(off=0x60002) == tcg.ERR_ALIGNMENT
+    assert grouped(K=60) == tcg.ERR_ALIGNMENT
+    assert grouped(R=0, A=None, SA=None, off=None, B=None, SB=None, D=None) == tcg.OK
+
+    def wgrad(t=3, R=64, N=64, K=64, G=4, DY=0x10000, lddy=0, SDY=0x20000, ldsdy=0, A=0x30000, lda=0, SA=0x40000,
+              ldsa=0, off=0x60000, DW=0x50000, dt=0, lddw=0, sw=0):
+        return tcg.raw_call("tcg_gemm_f8_grouped_wgrad", t, R, N, K, G, DY, lddy, SDY, ldsdy, A, lda, SA, ldsa, off, DW,
+                            dt, lddw, sw, None)
+    assert wgrad(t=1) == tcg.ERR_INVALID
+    for p in ("DY", "SDY", "A", "SA", "off", "DW"):
+        assert wgrad(**{p: None}) == tcg.ERR_INVALID
+    assert wgrad(ldsdy=63) == tcg.ERR_INVALID
+    assert wgrad(ldsa=63) == tcg.ERR_INVALID
+    assert wgrad(lddw=63) == tcg.ERR_INVALID
+    assert wgrad(sw=-1) == tcg.ERR_INVALID
+    assert wgrad(N=60) == tcg.ERR_ALIGNMENT
+    assert wgrad(DW=0x50002) == tcg.ERR_ALIGNMENT
+    assert wgrad(N=0, DY=None, SDY=None, A=None, SA=None, off=None, DW=None) == tcg.OK

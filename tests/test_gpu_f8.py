@@ -1,0 +1,167 @@
+"""Products of 8-bit codes with a scale for each block of 128, dense and grouped,
+against float64.
+
+Tolerance, of sum |products|: a product of two codes is exact in fp32 and a
+block's sum makes at most 128 roundings of 2^-23 (the tensor core may
+truncate); forming the factor, scaling and adding the block are four roundings
+of 2^-24, and adding ceil(K/128) blocks at most as many of 2^-24.  Then the
+rounding to the stored type."""
+import numpy as np
+import pytest
+import torch
+
+from f8_cases import BLOCK, IN_TYPE, along, blocks, codes, row_blocks, scales, spread
+from moe_cases import DTYPE, TORCH, close, group_offsets, to_host
+
+pytestmark = pytest.mark.gpu
+
+
+@pytest.fixture(scope="module")
+def tcg():
+    assert torch.cuda.is_available(), "GPU tests need a GPU"
+    from blackwell_tensor_core_swizzled_gb300 import build
+    build.build()
+    import blackwell_tensor_core_swizzled_gb300 as m
+    return m
+
+
+def ok(tcg):
+    rc = tcg.check()
+    assert rc == 0, tcg.last_error_string()
+
+
+def tau(K):
+    return min(K, BLOCK) * 2.0 ** -23 + (4 + blocks(K)) * 2.0 ** -24
+
+
+def dense(tcg, M, N, K, fmt, a_major, b_major, square, out, pad=0):
+    A, a = codes((M, K) if a_major == "k" else (K, M), fmt, 1, pad)
+    B, b = codes((N, K) if b_major == "k" else (K, N), fmt, 2, pad)
+    SA, sa = scales((blocks(K), M), fmt, 3, 1.0, pad)
+    shape = (blocks(K), N) if not square else (blocks(N), blocks(K)) if b_major == "k" else (blocks(K), blocks(N))
+    SB, sb = scales(shape, fmt, 4, K ** -0.5, pad)
+    D = torch.full((M, N + pad), 7.0, dtype=TORCH[out], device="cuda")
+    tcg.gemm_f8(IN_TYPE[fmt], M, N, K, A, tcg.K_MAJOR if a_major == "k" else tcg.MN_MAJOR, A.shape[1], SA,
+                SA.shape[1], B, tcg.K_MAJOR if b_major == "k" else tcg.MN_MAJOR, B.shape[1], SB, SB.shape[1], square, D,
+                DTYPE[out], N + pad)
+    ok(tcg)
+    assert bool((D[:, N:] == 7.0).all()), "wrote past the row"
+    am = (a if a_major == "k" else a.T) * along(sa, K).T
+    if square:
+        bm = b * spread(sb, *b.shape)
+        bm = bm if b_major == "k" else bm.T
+    else:
+        bm = (b if b_major == "k" else b.T) * along(sb, K).T
+    close(to_host(D)[:, :N], am @ bm.T, np.abs(am) @ np.abs(bm).T, tau(K), out, (M, N, K, a_major, b_major, square))
+
+
+SIZES = [(1, 1, 1), (1, 128, 128), (3, 257, 129), (16, 136, 1000), (17, 384, 512), (64, 129, 260), (65, 264, 384),
+         (129, 130, 640), (256, 512, 2048), (300, 1000, 1100), (513, 200, 100)]
+
+
+@pytest.mark.parametrize("fmt", ["e4m3", "e5m2"])
+@pytest.mark.parametrize("M,N,K", SIZES)
+def test_forward(tcg, fmt, M, N, K):
+    for out in ("f32", "bf16", "f16"):
+        dense(tcg, M, N, K, fmt, "k", "k", True, out)
+
+
+@pytest.mark.parametrize("M,N,K", SIZES)
+def test_rows_gradient(tcg, M, N, K):
+    dense(tcg, M, N, K, "e5m2", "k", "mn", True, "f32", 1)
+    dense(tcg, M, N, K, "e4m3", "k", "mn", True, "bf16", 2)
+
+
+@pytest.mark.parametrize("M,N,K", SIZES)
+def test_matrix_gradient(tcg, M, N, K):
+    dense(tcg, M, N, K, "e4m3", "mn", "mn", False, "f32", 1)
+    dense(tcg, M, N, K, "e5m2", "mn", "mn", False, "f16")
+
+
+@pytest.mark.parametrize("M,N,K", [(1, 130, 200), (65, 264, 384), (300, 200, 1000)])
+def test_other_majors(tcg, M, N, K):
+    for a_major in ("k", "mn"):
+        for b_major in ("k", "mn"):
+            for square in (False, True):
+                dense(tcg, M, N, K, "e4m3", a_major, b_major, square, "f32", 1)
+
+
+def test_many_tiles(tcg):
+    dense(tcg, 3000, 2600, 400, "e4m3", "k", "k", True, "bf16")
+    dense(tcg, 40, 20000, 300, "e4m3", "k", "k", True, "f32")
+
+
+def test_empty_contraction_and_empty_outputs(tcg):
+    D = torch.full((5, 40), 7.0, device="cuda")
+    tcg.gemm_f8(tcg.IN_E4M3, 5, 40, 0, None, 0, 0, None, 0, None, 0, 0, None, 0, True, D, tcg.F32, 40)
+    ok(tcg)
+    assert not to_host(D).any()
+    D.fill_(7.0)
+    tcg.gemm_f8(tcg.IN_E4M3, 0, 40, 128, None, 0, 0, None, 0, None, 0, 0, None, 0, True, D, tcg.F32, 40)
+    ok(tcg)
+    assert tcg.last_launch_count() == 0 and bool((D == 7.0).all())
+
+
+CASES = [
+    # sizes of the groups, loose rows before and after, N, K, rows padded by
+    ([1], 0, 0, 16, 16, 0),
+    ([5], 0, 0, 1, 1, 0),
+    ([0, 3, 0, 0, 130, 1, 0], 0, 0, 264, 72, 1),
+    ([128, 128, 256], 0, 0, 256, 128, 0),
+    ([17, 33, 64, 65, 127, 129], 0, 5, 200, 136, 0),
+    ([700, 0, 300], 3, 4, 130, 520, 1),
+    ([0, 0, 0], 0, 9, 72, 64, 0),
+    ([257, 255, 513], 0, 0, 513, 1000, 0),
+    ([3] * 40, 1, 1, 384, 192, 0),
+    ([1, 2, 4, 8, 16, 31, 32, 48], 0, 0, 1030, 2056, 0),
+]
+
+
+@pytest.mark.parametrize("major", ["k", "mn"])
+@pytest.mark.parametrize("sizes,before,after,N,K,pad", CASES)
+def test_grouped(tcg, major, sizes, before, after, N, K, pad):
+    G, R = len(sizes), sum(sizes) + before + after
+    off = group_offsets(sizes, before)
+    fmt = "e4m3" if major == "k" else "e5m2"
+    A, a = codes((R, K), fmt, 1, pad)
+    SA, sa = scales((blocks(K), R), fmt, 2, 1.0, pad)
+    rows, cols = (N, K) if major == "k" else (K, N)
+    B, b = codes((G, rows, cols), fmt, 3, pad)
+    SB, sb = scales((G, blocks(rows), blocks(cols)), fmt, 4, K ** -0.5, pad)
+    a = a * along(sa, K).T
+    b = b * spread(sb, rows, cols)
+    for out in ("f32", "bf16"):
+        D = torch.full((R, N + 3), 7.0, dtype=TORCH[out], device="cuda")
+        tcg.gemm_f8_grouped(IN_TYPE[fmt], R, N, K, G, A, A.shape[1], SA, SA.shape[1], torch.from_numpy(off).cuda(), B,
+                            tcg.K_MAJOR if major == "k" else tcg.MN_MAJOR, B.shape[2], 0, SB, SB.shape[2], 0, D,
+                            DTYPE[out], N + 3)
+        ok(tcg)
+        ref, S = np.zeros((R, N)), np.zeros((R, N))
+        for g in range(G):
+            sl, m = slice(off[g], off[g + 1]), b[g].T if major == "k" else b[g]
+            ref[sl], S[sl] = a[sl] @ m, np.abs(a[sl]) @ np.abs(m)
+        close(to_host(D)[:, :N], ref, S, tau(K), out, (major, out))
+        assert bool((D[:, N:] == 7.0).all()), "wrote past the row"
+
+
+@pytest.mark.parametrize("sizes,before,after,N,K,pad", CASES)
+def test_grouped_wgrad(tcg, sizes, before, after, N, K, pad):
+    G, R = len(sizes), sum(sizes) + before + after
+    off = group_offsets(sizes, before)
+    DY, dy = codes((R, N), "e4m3", 5, pad)
+    A, a = codes((R, K), "e4m3", 6, pad)
+    SDY, sdy = scales((R // BLOCK + G, N), "e4m3", 7, 0.1, pad)
+    SA, sa = scales((R // BLOCK + G, K), "e4m3", 8, 1.0, pad)
+    at = row_blocks(off, R)
+    dy, a = dy * sdy[at], a * sa[at]
+    for out in ("f32", "bf16"):
+        DW = torch.full((G, N, K + 5), 7.0, dtype=TORCH[out], device="cuda")
+        tcg.gemm_f8_grouped_wgrad(tcg.IN_E4M3, R, N, K, G, DY, DY.shape[1], SDY, SDY.shape[1], A, A.shape[1], SA,
+                                  SA.shape[1], torch.from_numpy(off).cuda(), DW, DTYPE[out], K + 5, 0)
+        ok(tcg)
+        ref, S = np.zeros((G, N, K)), np.zeros((G, N, K))
+        for g in range(G):
+            sl = slice(off[g], off[g + 1])
+            ref[g], S[g] = dy[sl].T @ a[sl], np.abs(dy[sl]).T @ np.abs(a[sl])
+        close(to_host(DW)[:, :, :K], ref, S, tau(max(sizes)), out, out)
+        assert bool((DW[:, :, K:] == 7.0).all())
