@@ -106,6 +106,33 @@ __device__ __forceinline__ void mma_f8(uint32_t d, uint64_t a, uint64_t b, uint3
         : "memory");
 }
 
+// wait_uniform without a function call, across which the epilogue's sums would
+// be kept in local memory.
+__device__ __forceinline__ bool wait_inline(uint32_t bar, uint32_t parity, const WaitCtx& w, uint32_t site) {
+  bool ok = mbar_try_wait(bar, parity);
+  if (__all_sync(0xffffffffu, ok)) return true;
+  const uint64_t t0 = globaltimer();
+  while (!ok) {
+#pragma unroll 1
+    for (int i = 0; i < 32 && !ok; ++i) ok = mbar_try_wait(bar, parity);
+    if (ok || *w.abort_flag) break;
+    if (globaltimer() - t0 > w.timeout_ns) {
+      *w.abort_flag = 1u;
+      if (w.err) atomicCAS(w.err, 0ull, make_err(1u, site));
+      break;
+    }
+  }
+  return __all_sync(0xffffffffu, ok);
+}
+
+template <bool MORE, int N>
+__device__ __forceinline__ void set_registers() {
+  if constexpr (MORE)
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(N));
+  else
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(N));
+}
+
 // Two fp32 operations in one instruction.
 __device__ __forceinline__ uint64_t pair(uint32_t lo, uint32_t hi) {
   uint64_t v;
@@ -126,21 +153,33 @@ __device__ __forceinline__ uint64_t mul2(uint64_t a, uint64_t b) {
   return d;
 }
 
-__device__ __forceinline__ void ld_shared_2x64(uint32_t addr, uint64_t& a, uint64_t& b) {
-  asm volatile("ld.shared.v2.b64 {%0, %1}, [%2];" : "=l"(a), "=l"(b) : "r"(addr));
+// Waits for this thread's tensor-memory reads; ties the registers to the wait.
+__device__ __forceinline__ void wait_ld16(uint32_t (&r)[16]) {
+  asm volatile("tcgen05.wait::ld.sync.aligned;"
+               : "+r"(r[0]), "+r"(r[1]), "+r"(r[2]), "+r"(r[3]), "+r"(r[4]), "+r"(r[5]), "+r"(r[6]), "+r"(r[7]), "+r"(r[8]),
+                 "+r"(r[9]), "+r"(r[10]), "+r"(r[11]), "+r"(r[12]), "+r"(r[13]), "+r"(r[14]), "+r"(r[15])
+               :
+               : "memory");
+}
+
+__device__ __forceinline__ uint64_t ld_shared_b64(uint32_t addr) {
+  uint64_t v;
+  asm volatile("ld.shared.b64 %0, [%1];" : "=l"(v) : "r"(addr));
+  return v;
+}
+__device__ __forceinline__ uint16_t ld_shared_u16(uint32_t addr) {
+  uint16_t v;
+  asm volatile("ld.shared.b16 %0, [%1];" : "=h"(v) : "r"(addr) : "memory");
+  return v;
 }
 __device__ __forceinline__ float ld_shared_f32(uint32_t addr) {
   float v;
-  asm volatile("ld.shared.f32 %0, [%1];" : "=f"(v) : "r"(addr));
+  asm volatile("ld.shared.f32 %0, [%1];" : "=f"(v) : "r"(addr) : "memory");
   return v;
 }
 __device__ __forceinline__ void st_shared_f32(uint32_t addr, float v) {
   asm volatile("st.shared.f32 [%0], %1;" ::"r"(addr), "f"(v) : "memory");
 }
-__device__ __forceinline__ void st_shared_u16(uint32_t addr, uint32_t v) {
-  asm volatile("st.shared.b16 [%0], %1;" ::"r"(addr), "h"(static_cast<uint16_t>(v)) : "memory");
-}
-
 template <int CG, int BN, int STAGES, bool VEC>
 struct F8Cfg {
   static constexpr int P_BYTES = 128 * 128;
@@ -351,20 +390,24 @@ __global__ void __launch_bounds__(F8_THREADS, 1) f8_kernel(const __grid_constant
   FTile* tiles = reinterpret_cast<FTile*>(gbase + C::TILE_OFF);
   auto fetch = [&](uint32_t n, FTile& t) {
     const uint32_t i = n % TILES;
-    if (!wait_uniform(tile_full(i), (n / TILES) & 1u, wctx, SITE_PROD_EMPTY)) return false;
+    if (!wait_inline(tile_full(i), (n / TILES) & 1u, wctx, SITE_PROD_EMPTY)) return false;
     t = tiles[i];
     __syncwarp();
     if (lane == 0) mbar_arrive(tile_empty(i));
     return true;
   };
 
+  // 384 threads x 168 registers at launch: 88 for each of the four warps that
+  // feed, 208 for the eight that hold sums
+  if (warp < 4) {
+  set_registers<false, 88>();
   if (warp == 3) {
     // ------------------------------------------- tile list and blocks' scales
     uint32_t n = 0, it = 0;
     auto publish = [&](int u, FTile& t) {
       t = decode_unit<CG, BN>(p, seg, pre, u);
       const uint32_t i = n % TILES;
-      if (!wait_uniform(tile_empty(i), ((n / TILES) & 1u) ^ 1u, wctx, SITE_PROD_EMPTY)) return false;
+      if (!wait_inline(tile_empty(i), ((n / TILES) & 1u) ^ 1u, wctx, SITE_PROD_EMPTY)) return false;
       if (lane == 0) {
         tiles[i] = t;
         mbar_arrive(tile_full(i));
@@ -403,7 +446,7 @@ __global__ void __launch_bounds__(F8_THREADS, 1) f8_kernel(const __grid_constant
         for (int j = 0; j < BATCH; ++j) {
           if (j >= blocks) break;
           const uint32_t i = it % SLOTS;
-          if (!wait_uniform(sce_bar(i), ((it / SLOTS) & 1u) ^ 1u, wctx, SITE_PROD_EMPTY)) {
+          if (!wait_inline(sce_bar(i), ((it / SLOTS) & 1u) ^ 1u, wctx, SITE_PROD_EMPTY)) {
             ok = false;
             break;
           }
@@ -420,7 +463,7 @@ __global__ void __launch_bounds__(F8_THREADS, 1) f8_kernel(const __grid_constant
         }
       }
     }
-  } else if (warp == 0 || warp == 2) {
+  } else if (warp != 1) {
     // ---------------------------------------------- producers, of P and of Q
     const bool brings_p = warp == 0;
     uint32_t it = 0, s = 0, ph = 0, n = 0;
@@ -435,7 +478,7 @@ __global__ void __launch_bounds__(F8_THREADS, 1) f8_kernel(const __grid_constant
       const bool q_mn = p.weight || p.q_mn;
       const uint32_t tx = C::P_BYTES + static_cast<uint32_t>(half * 128);
       for (int kb = 0; kb < t.nkb; ++kb) {
-        if (!wait_uniform(empty_bar(s), ph ^ 1u, wctx, SITE_PROD_EMPTY)) {
+        if (!wait_inline(empty_bar(s), ph ^ 1u, wctx, SITE_PROD_EMPTY)) {
           ok = false;
           break;
         }
@@ -495,7 +538,7 @@ __global__ void __launch_bounds__(F8_THREADS, 1) f8_kernel(const __grid_constant
       }
     }
     __syncwarp();
-  } else if (warp == 1) {
+  } else {
     // --------------------------------- MMA issuer (leader), row zeroing (both)
     const uint64_t p_desc0 = sdesc(sbase, p.p_hi);
     const uint64_t q_desc0 = sdesc(sbase + C::P_BYTES, p.q_hi);
@@ -511,20 +554,20 @@ __global__ void __launch_bounds__(F8_THREADS, 1) f8_kernel(const __grid_constant
         const bool last = kb == t.nkb - 1;
         const bool ragged = p.weight && last && (t.last & 31);
         const uint32_t b = tcount & 1u;
-        if (issue && !wait_uniform(acce_bar(b), ((tcount >> 1) & 1u) ^ 1u, wctx, SITE_MMA_ACC_EMPTY)) {
+        if (issue && !wait_inline(acce_bar(b), ((tcount >> 1) & 1u) ^ 1u, wctx, SITE_MMA_ACC_EMPTY)) {
           ok = false;
           break;
         }
         ++tcount;
         const uint32_t d_tmem = tmem_base + b * BN;
-        if (issue && !wait_uniform(full_bar(s), ph, wctx, SITE_MMA_FULL)) {
+        if (issue && !wait_inline(full_bar(s), ph, wctx, SITE_MMA_FULL)) {
           ok = false;
           break;
         }
         if (ragged) {
           const uint32_t par = (rag_ph >> s) & 1u;
           rag_ph ^= 1u << s;
-          if (!warp_wait(rag_bar(s), par, wctx, SITE_MMA_FULL)) {
+          if (!wait_inline(rag_bar(s), par, wctx, SITE_MMA_FULL)) {
             ok = false;
             break;
           }
@@ -541,7 +584,7 @@ __global__ void __launch_bounds__(F8_THREADS, 1) f8_kernel(const __grid_constant
           if constexpr (CG == 2) {
             if (rank != 0) {
               if (lane == 0) mbar_arrive_cluster(mapa_shared(peer_bar(s), 0));
-            } else if (!warp_wait(peer_bar(s), par, wctx, SITE_MMA_FULL) || !mbar_try_wait_cluster(peer_bar(s), par)) {
+            } else if (!wait_inline(peer_bar(s), par, wctx, SITE_MMA_FULL) || !mbar_try_wait_cluster(peer_bar(s), par)) {
               ok = false;
               break;
             }
@@ -574,8 +617,10 @@ __global__ void __launch_bounds__(F8_THREADS, 1) f8_kernel(const __grid_constant
       }
     }
     __syncwarp();
-  } else if (warp >= 4) {
+  }
+  } else {
     // ------------------------------------------------------------ epilogue
+    set_registers<true, 208>();
     const int q = warp & 3;            // TMEM lane quadrant
     const int part = (warp - 4) >> 2;  // 32-column chunks part, part + 2, ...
     constexpr int MINE = (BN + 63) / 64;
@@ -602,42 +647,48 @@ __global__ void __launch_bounds__(F8_THREADS, 1) f8_kernel(const __grid_constant
     for (int u = cluster_id; u < total_units; u += num_clusters) {
       FTile t;
       if (!fetch(n++, t)) break;
-      uint64_t sum[MINE][16];  // pairs of columns
+      uint64_t sum[MINE][2][8];  // chunk, 16 rows, pairs of columns as in the fragment
 #pragma unroll
       for (int i = 0; i < MINE; ++i)
 #pragma unroll
-        for (int k = 0; k < 16; ++k) sum[i][k] = 0ull;
+        for (int k = 0; k < 16; ++k) sum[i][k >> 3][k & 7] = 0ull;
+      const int mine = (t.ncols - 32 * part + 63) >> 6;  // this warp's chunks of 32 columns that exist
       bool done = true;
       for (int kb = 0; kb < t.nkb; ++kb, ++tcount) {
         const uint32_t b = tcount & 1u, slot = tcount % SLOTS;
-        done = wait_uniform(scf_bar(slot), (tcount / SLOTS) & 1u, wctx, SITE_EPI_ACC_FULL) &&
-               wait_uniform(accf_bar(b), (tcount >> 1) & 1u, wctx, SITE_EPI_ACC_FULL);
+        done = wait_inline(scf_bar(slot), (tcount / SLOTS) & 1u, wctx, SITE_EPI_ACC_FULL) &&
+               wait_inline(accf_bar(b), (tcount >> 1) & 1u, wctx, SITE_EPI_ACC_FULL);
         if (!done) break;
         tc_fence_after();
         const uint32_t at = slot_at(slot);
-        uint64_t row = 0;
+        uint64_t row[4];  // P's factors of this lane's rows lane / 4 + 8 h, twice
         if constexpr (VEC) {
-          const uint32_t r = __float_as_uint(ld_shared_f32(at + 4u * BN + 4u * (32 * q + lane)));
-          row = pair(r, r);
+#pragma unroll
+          for (int h = 0; h < 4; ++h) {
+            const uint32_t r = __float_as_uint(ld_shared_f32(at + 4u * (BN + 32 * q + 8 * h + (lane >> 2))));
+            row[h] = pair(r, r);
+          }
         }
+        // fragments of 16 rows by 32 columns, the next one's read in flight meanwhile
+        const uint32_t from = lanes + b * BN + 32 * part;
+        uint32_t r[2][16];
+        uint64_t f[4];  // factors of this lane's columns 8 j + 2 (lane % 4), + 1
+        if (mine > 0) tmem_ld_16x256b_x4(from, r[0]);
 #pragma unroll
-        for (int i = 0; i < MINE; ++i) {
-          const int c = 32 * part + 64 * i;
-          if (c >= t.ncols) break;
-          uint32_t r[32];
-          tmem_ld_32x32b_x32(lanes + b * BN + c, r);
-          tc_wait_ld();
+        for (int h = 0; h < 2 * MINE; ++h) {
+          if (h / 2 >= mine) break;
+          if ((h & 1) == 0) {
 #pragma unroll
-          for (int k = 0; k < 16; k += 2) {
-            uint64_t f0, f1;
-            ld_shared_2x64(at + 4u * (c + 2 * k), f0, f1);
-            if constexpr (VEC) {
-              sum[i][k] = fma2(mul2(pair(r[2 * k], r[2 * k + 1]), f0), row, sum[i][k]);
-              sum[i][k + 1] = fma2(mul2(pair(r[2 * k + 2], r[2 * k + 3]), f1), row, sum[i][k + 1]);
-            } else {
-              sum[i][k] = fma2(pair(r[2 * k], r[2 * k + 1]), f0, sum[i][k]);
-              sum[i][k + 1] = fma2(pair(r[2 * k + 2], r[2 * k + 3]), f1, sum[i][k + 1]);
-            }
+            for (int j = 0; j < 4; ++j) f[j] = ld_shared_b64(at + 4u * (32 * part + 32 * h + 8 * j + 2 * (lane & 3)));
+          }
+          wait_ld16(r[h & 1]);
+          if (h + 1 < 2 * MINE && (h + 1) / 2 < mine)
+            tmem_ld_16x256b_x4(from + 64 * ((h + 1) / 2) + (static_cast<uint32_t>((h + 1) & 1) << 20), r[(h + 1) & 1]);
+#pragma unroll
+          for (int k = 0; k < 8; ++k) {
+            const uint64_t v = pair(r[h & 1][2 * k], r[h & 1][2 * k + 1]);
+            uint64_t& to = sum[h / 2][h & 1][k];
+            to = VEC ? fma2(mul2(v, f[k / 2]), row[2 * (h & 1) + (k & 1)], to) : fma2(v, f[k / 2], to);
           }
         }
         tc_fence_before();
@@ -652,57 +703,75 @@ __global__ void __launch_bounds__(F8_THREADS, 1) f8_kernel(const __grid_constant
       }
       if (!done) break;
       const int m_warp = t.m0 + static_cast<int>(rank) * 128 + 32 * q;
-      const int m = m_warp + lane;
-      const bool m_ok = m < p.M;
       const int row0 = p.weight ? t.c0 : t.lo + t.c0, outer = p.weight ? t.g : 0;
       const int64_t pitch = p.ldd * p.d_size;
+      const bool m_ok = m_warp + lane < p.M;
       uint8_t* dst = static_cast<uint8_t*>(p.D) + static_cast<int64_t>(row0) * pitch +
-                     (p.weight ? t.g * p.stride_d * p.d_size : 0) + static_cast<int64_t>(m) * p.d_size;
+                     (p.weight ? t.g * p.stride_d * p.d_size : 0) + static_cast<int64_t>(m_warp + lane) * p.d_size;
 #pragma unroll
       for (int i = 0; i < MINE; ++i) {
         const int c = 32 * part + 64 * i;
-        if (c >= t.ncols || m_warp >= p.M) break;
+        if (i >= mine || m_warp >= p.M) break;
         // rows of a matrix clip at the map's end, rows of a group do not
         const bool boxed = p.d_tma && (p.weight || c + 32 <= t.ncols);
         if (p.d_type == OUT_F32) {
 #pragma unroll
-          for (int h = 0; h < 32; h += 16) {  // a staging tile holds 16 rows of 32 m
-            const uint32_t buf = boxed ? staging() : 0u;
+          for (int g = 0; g < 2; ++g) {  // a staging tile holds 16 rows of 32 m
+            const uint32_t buf = staging();
 #pragma unroll
-            for (int k = 0; k < 16; k += 2) {
-              uint32_t lo, hi;
-              unpair(sum[i][(h + k) / 2], lo, hi);
-              if (boxed) {
-                st_shared_u32(buf + 128u * k + 4u * lane, lo);
-                st_shared_u32(buf + 128u * (k + 1) + 4u * lane, hi);
-              } else {
-                uint8_t* d = dst + (c + h + k) * pitch;
-                if (m_ok && c + h + k < t.ncols) *reinterpret_cast<uint32_t*>(d) = lo;
-                if (m_ok && c + h + k + 1 < t.ncols) *reinterpret_cast<uint32_t*>(d + pitch) = hi;
+            for (int h = 0; h < 4; ++h) {
+              const uint32_t m = 8u * h + (static_cast<uint32_t>(lane) >> 2);
+#pragma unroll
+              for (int j = 0; j < 2; ++j) {
+                uint32_t lo, hi;
+                unpair(sum[i][h >> 1][2 * (2 * g + j) + (h & 1)], lo, hi);
+                const uint32_t at = 8u * j + 2u * (lane & 3);
+                st_shared_u32(buf + 128u * at + 16u * ((m >> 2) ^ (at & 7u)) + 4u * (m & 3u), lo);
+                st_shared_u32(buf + 128u * (at + 1) + 16u * ((m >> 2) ^ ((at + 1) & 7u)) + 4u * (m & 3u), hi);
               }
             }
-            if (boxed) send(buf, m_warp, row0 + c + h, outer);
+            if (boxed) {
+              send(buf, m_warp, row0 + c + 16 * g, outer);
+              continue;
+            }
+            __syncwarp();
+            for (int k = 0; k < 16; ++k) {
+              const uint32_t m = static_cast<uint32_t>(lane);
+              if (m_ok && c + 16 * g + k < t.ncols)
+                *reinterpret_cast<float*>(dst + (c + 16 * g + k) * pitch) =
+                    ld_shared_f32(buf + 128u * k + 16u * ((m >> 2) ^ (k & 7u)) + 4u * (m & 3u));
+            }
+            __syncwarp();
           }
           continue;
         }
-        const uint32_t buf = boxed ? staging() : 0u;
+        // stmatrix turns 8 m of 8 columns into 8 rows of 16 bytes: lane 8k + n
+        // addresses row 8j + n, m 8k..8k+7; a row's four 16-byte words are swizzled
+        const uint32_t buf = staging();
+        const bool bf = p.d_type == OUT_BF16;
+        const uint32_t k = static_cast<uint32_t>(lane) >> 3, n8 = static_cast<uint32_t>(lane) & 7u;
 #pragma unroll
-        for (int k = 0; k < 32; k += 2) {
-          uint32_t lo, hi;
-          unpair(sum[i][k / 2], lo, hi);
-          const uint32_t h = p.d_type == OUT_BF16 ? pack_bf16(lo, hi) : pack_f16(lo, hi);
-          if (boxed) {
-            // rows of 64 bytes, their four 16-byte words swizzled
-            const uint32_t to = buf + 64u * k + 16u * ((static_cast<uint32_t>(lane) >> 3) ^ ((k >> 1) & 3u)) + 2u * (lane & 7);
-            st_shared_u16(to, h);
-            st_shared_u16(to + 64u, h >> 16);
-          } else {
-            uint8_t* d = dst + (c + k) * pitch;
-            if (m_ok && c + k < t.ncols) *reinterpret_cast<uint16_t*>(d) = static_cast<uint16_t>(h);
-            if (m_ok && c + k + 1 < t.ncols) *reinterpret_cast<uint16_t*>(d + pitch) = static_cast<uint16_t>(h >> 16);
+        for (uint32_t j = 0; j < 4; ++j) {
+          const uint32_t to = 8u * j + n8;
+          uint32_t w[4];
+#pragma unroll
+          for (int h = 0; h < 4; ++h) {
+            uint32_t lo, hi;
+            unpair(sum[i][h >> 1][2 * j + (h & 1)], lo, hi);
+            w[h] = bf ? pack_bf16(lo, hi) : pack_f16(lo, hi);
           }
+          stmatrix_x4_trans(buf + 64u * to + 16u * (k ^ ((to >> 1) & 3u)), w[0], w[1], w[2], w[3]);
         }
-        if (boxed) send(buf, m_warp, row0 + c, outer);
+        if (boxed) {
+          send(buf, m_warp, row0 + c, outer);
+          continue;
+        }
+        __syncwarp();
+        for (int n = 0; n < 32; ++n)
+          if (m_ok && c + n < t.ncols)
+            *reinterpret_cast<uint16_t*>(dst + (c + n) * pitch) =
+                ld_shared_u16(buf + 64u * n + 16u * (k ^ ((static_cast<uint32_t>(n) >> 1) & 3u)) + 2u * n8);
+        __syncwarp();
       }
     }
     if (lane == 0) bulk_wait_group_all();
@@ -816,7 +885,7 @@ int launch_f8(const KernelInfo& ki, F8Params& p, int dev, int64_t units, cudaStr
   if (p.d_tma) {
     const uint64_t rows = static_cast<uint64_t>(p.weight ? p.C : p.R), outer = p.weight ? p.G : 1;
     if (int rc = make_store_map(&p.tmap_d, p.D, static_cast<tcg_dtype>(p.d_type), p.M, rows, outer, p.ldd,
-                                p.weight ? p.stride_d : p.R * p.ldd))
+                                p.weight ? p.stride_d : p.R * p.ldd, 128))
       return rc;
   }
   p.err = device_error_word(dev);

@@ -82,7 +82,7 @@ int make_byte_map(CUtensorMap* map, const void* base, uint64_t inner, uint64_t m
 }
 
 int make_store_map(CUtensorMap* map, const void* base, tcg_dtype type, uint64_t inner, uint64_t mid, uint64_t outer,
-                   uint64_t stride_mid, uint64_t stride_outer) {
+                   uint64_t stride_mid, uint64_t stride_outer, uint32_t f32_span) {
   const bool f32 = type == TCG_F32;
   const uint64_t size = f32 ? 4 : 2;
   const cuuint64_t dims[3] = {inner, mid, outer}, strides[2] = {size * stride_mid, size * stride_outer};
@@ -91,7 +91,7 @@ int make_store_map(CUtensorMap* map, const void* base, tcg_dtype type, uint64_t 
                       f32                ? CU_TENSOR_MAP_DATA_TYPE_FLOAT32
                       : type == TCG_BF16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16
                                          : CU_TENSOR_MAP_DATA_TYPE_FLOAT16,
-                      3, base, dims, strides, box, f32 ? 0 : 64);
+                      3, base, dims, strides, box, f32 ? f32_span : 64);
 }
 
 int make_slab_map(CUtensorMap* map, const void* base, uint64_t inner, uint64_t mid, uint64_t slabs, uint64_t outer,
