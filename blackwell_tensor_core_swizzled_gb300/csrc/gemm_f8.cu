@@ -20,9 +20,7 @@
 // beside 256 of fp32 multiply-adds (512 where P's scales differ from row to row
 // as well: the factor is then formed for each element).
 //
-// A warp loads the blocks' scales ahead into a shared ring, multiplied where P
-// has one scale for 128 rows: the epilogue then reads one factor a column, four
-// at a time, all lanes the same.
+// A warp copies the blocks' scales ahead into a shared ring.
 //
 // The ragged extent of a product, the group's rows, is on the MMA's N side, any
 // multiple of 16 (32 for a pair) up to BN, so few rows cost few columns.  MN-major
@@ -53,13 +51,14 @@ namespace {
 constexpr int MAX_GROUPS = 1024;
 constexpr int64_t MAX_EXTENT = int64_t{1} << 30;
 constexpr int BLOCK = 128;  // k of a scale, and of a ring stage
-constexpr int EPI_WARPS = 8;
 constexpr int STAGING_BYTES = 2048;
 constexpr int TILES = 4;   // decoded tiles ahead of the warps that work on them
 constexpr int SLOTS = 8;   // blocks whose scales are in shared memory
-constexpr int BATCH = 4;   // blocks whose scales are loaded together
-constexpr int F8_THREADS = 32 * (4 + EPI_WARPS);
 constexpr int BAND = 8;    // column tiles that sweep a group's row tiles together
+
+// What has a scale for each block: the columns (and 128 rows together), rows and
+// columns, or the rows (and 128 columns together).
+enum Scaling : int { COLUMNS = 0, BOTH = 1, ROWS = 2 };
 
 struct F8Params {
   CUtensorMap tmap_p;    // [G or 1][rows][128-byte boxes]
@@ -75,10 +74,12 @@ struct F8Params {
   int C;         // weight: extent of c
   int K;         // contraction length unless weight
   int m_tiles;
-  const float* sp;  // VEC: [block][m]; else one for 128 m: g * sp_group + (m / 128) * sp_m + b * sp_b
-  int64_t sp_group, sp_m, sp_b;
-  const float* sq;  // [block][c]: b * sq_b + c
-  int64_t sq_b;
+  // scales of single rows or columns: [block][row], b * fine_b + row
+  const float* fine;
+  int64_t fine_b;
+  // BOTH: P's, likewise; else one for 128: g * other_group + (row / 128) * other_row + b * other_b
+  const float* other;
+  int64_t other_group, other_row, other_b;
   uint64_t p_hi, q_hi;
   uint32_t p_kstep, q_kstep;  // 16-byte units per 32 of the contraction
   uint32_t idesc;             // without N
@@ -111,6 +112,9 @@ __device__ __forceinline__ void mma_f8(uint32_t d, uint64_t a, uint64_t b, uint3
 __device__ __forceinline__ bool wait_inline(uint32_t bar, uint32_t parity, const WaitCtx& w, uint32_t site) {
   bool ok = mbar_try_wait(bar, parity);
   if (__all_sync(0xffffffffu, ok)) return true;
+#pragma unroll 1
+  for (int i = 0; i < 64 && !ok; ++i) ok = mbar_try_wait(bar, parity);
+  if (__all_sync(0xffffffffu, ok)) return true;
   const uint64_t t0 = globaltimer();
   while (!ok) {
 #pragma unroll 1
@@ -123,6 +127,15 @@ __device__ __forceinline__ bool wait_inline(uint32_t bar, uint32_t parity, const
     }
   }
   return __all_sync(0xffffffffu, ok);
+}
+
+// A 4-byte copy global -> shared in flight (zero if !exists), and this lane's
+// arrival on `bar` (one of 32) once its copies so far have landed.
+__device__ __forceinline__ void copy_f32(uint32_t to, const float* from, bool exists) {
+  asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"(to), "l"(from), "r"(exists ? 4 : 0) : "memory");
+}
+__device__ __forceinline__ void copies_arrive(uint32_t bar) {
+  asm volatile("cp.async.mbarrier.arrive.noinc.shared.b64 [%0];" ::"r"(bar) : "memory");
 }
 
 template <bool MORE, int N>
@@ -142,24 +155,24 @@ __device__ __forceinline__ uint64_t pair(uint32_t lo, uint32_t hi) {
 __device__ __forceinline__ void unpair(uint64_t v, uint32_t& lo, uint32_t& hi) {
   asm("mov.b64 {%0, %1}, %2;" : "=r"(lo), "=r"(hi) : "l"(v));
 }
-__device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
-  uint64_t d;
-  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(d) : "l"(a), "l"(b), "l"(c));
-  return d;
+// sum += {lo, hi} * f (* row), two fp32 operations an instruction.  Volatile, so
+// that none moves before the wait for the tensor-memory read of lo and hi.
+__device__ __forceinline__ void add_scaled(uint64_t& sum, uint32_t lo, uint32_t hi, uint64_t f) {
+  asm volatile("{\n\t.reg .b64 v;\n\tmov.b64 v, {%1, %2};\n\tfma.rn.f32x2 %0, v, %3, %0;\n\t}"
+               : "+l"(sum)
+               : "r"(lo), "r"(hi), "l"(f));
 }
+__device__ __forceinline__ void add_scaled(uint64_t& sum, uint32_t lo, uint32_t hi, uint64_t f, uint64_t row) {
+  asm volatile(
+      "{\n\t.reg .b64 v;\n\tmov.b64 v, {%1, %2};\n\tmul.rn.f32x2 v, v, %3;\n\tfma.rn.f32x2 %0, v, %4, %0;\n\t}"
+      : "+l"(sum)
+      : "r"(lo), "r"(hi), "l"(f), "l"(row));
+}
+
 __device__ __forceinline__ uint64_t mul2(uint64_t a, uint64_t b) {
   uint64_t d;
   asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
   return d;
-}
-
-// Waits for this thread's tensor-memory reads; ties the registers to the wait.
-__device__ __forceinline__ void wait_ld16(uint32_t (&r)[16]) {
-  asm volatile("tcgen05.wait::ld.sync.aligned;"
-               : "+r"(r[0]), "+r"(r[1]), "+r"(r[2]), "+r"(r[3]), "+r"(r[4]), "+r"(r[5]), "+r"(r[6]), "+r"(r[7]), "+r"(r[8]),
-                 "+r"(r[9]), "+r"(r[10]), "+r"(r[11]), "+r"(r[12]), "+r"(r[13]), "+r"(r[14]), "+r"(r[15])
-               :
-               : "memory");
 }
 
 __device__ __forceinline__ uint64_t ld_shared_b64(uint32_t addr) {
@@ -177,19 +190,20 @@ __device__ __forceinline__ float ld_shared_f32(uint32_t addr) {
   asm volatile("ld.shared.f32 %0, [%1];" : "=f"(v) : "r"(addr) : "memory");
   return v;
 }
-__device__ __forceinline__ void st_shared_f32(uint32_t addr, float v) {
-  asm volatile("st.shared.f32 [%0], %1;" ::"r"(addr), "f"(v) : "memory");
-}
-template <int CG, int BN, int STAGES, bool VEC>
+template <int CG, int BN, int STAGES, Scaling MODE>
 struct F8Cfg {
+  static constexpr int PARTS = 2;  // epilogue warps that share a lane quadrant's columns
+  static constexpr int EPI_WARPS = 4 * PARTS;
+  static constexpr int THREADS = 32 * (4 + EPI_WARPS);
   static constexpr int P_BYTES = 128 * 128;
   static constexpr int Q_ROWS = BN / CG;
   static constexpr int Q_BYTES = Q_ROWS * 128;
   static constexpr int STAGE_BYTES = P_BYTES + Q_BYTES;
-  // two staging tiles for each epilogue warp
+  static constexpr int STAGING = PARTS >= 3 ? 1 : 2;  // staging tiles for each epilogue warp
   static constexpr int EPI_OFF = STAGES * STAGE_BYTES;
-  static constexpr int SC_OFF = EPI_OFF + EPI_WARPS * 2 * STAGING_BYTES;
-  static constexpr int SLOT_BYTES = 4 * (BN + (VEC ? 128 : 0));  // factors of the columns, then P's of the rows
+  static constexpr int SC_OFF = EPI_OFF + EPI_WARPS * STAGING * STAGING_BYTES;
+  // a block's scales: Q's of the columns, then P's of the rows or of all; ROWS: P's of the rows, then Q's of 128 columns each
+  static constexpr int SLOT_BYTES = 4 * (MODE == ROWS ? 128 + 4 : BN + (MODE == BOTH ? 128 : 4));
   static constexpr int BAR_OFF = SC_OFF + SLOTS * SLOT_BYTES;
   // full[S], empty[S], rag[S], peer[S], acc_full[2], acc_empty[2], drain, tile_full[T], tile_empty[T],
   // scale_full[L], scale_empty[L]
@@ -212,25 +226,30 @@ struct alignas(16) FTile {
   int mma_n;  // columns the MMA computes
   int nkb;    // blocks of the contraction (0: the tile is zero)
   int last;   // depth of the last block
+  int rows;   // ROWS: rows of the group from m0 on
 };
 static_assert(sizeof(FTile) <= 48, "tile ring");
 
-// A group's columns n: tiles of `per` columns each, the last one shorter.
-template <int CG, int BN>
-__device__ __forceinline__ void split_columns(int n, bool whole, int& tiles, int& per) {
-  const int t = (n + BN - 1) / BN;
-  const int step = whole ? BN : 16 * CG;
-  per = t ? ((n + t - 1) / t + step - 1) / step * step : step;
+// A group's n ragged columns (ROWS: rows): tiles of `per` each, the last shorter.
+template <int CG, int BN, Scaling MODE>
+__device__ __forceinline__ void split_ragged(int n, bool whole, int& tiles, int& per) {
+  if constexpr (MODE == ROWS) {
+    per = 128 * CG;
+  } else {
+    const int t = (n + BN - 1) / BN;
+    const int step = whole ? BN : 16 * CG;
+    per = t ? ((n + t - 1) / t + step - 1) / step * step : step;
+  }
   tiles = (n + per - 1) / per;
 }
 
 // seg[0..G]: clamped offsets; pre[0..G]: units of the groups before (unless weight).
-template <int CG, int BN>
+template <int CG, int BN, Scaling MODE>
 __device__ __forceinline__ FTile decode_unit(const F8Params& p, const int* seg, const int* pre, int u) {
   FTile t;
   int v, tiles, per, n;
   if (p.weight) {
-    split_columns<CG, BN>(p.C, true, tiles, per);
+    split_ragged<CG, BN, MODE>(p.C, true, tiles, per);
     const int per_group = tiles * p.m_tiles;
     t.g = u / per_group;
     v = u - t.g * per_group;
@@ -247,7 +266,7 @@ __device__ __forceinline__ FTile decode_unit(const F8Params& p, const int* seg, 
     t.g = a;
     v = u - pre[a];
     n = seg[a + 1] - seg[a];
-    split_columns<CG, BN>(n, p.q_mn, tiles, per);
+    split_ragged<CG, BN, MODE>(n, p.q_mn, tiles, per);
   }
   t.lo = seg[t.g];
   const int depth = p.weight ? seg[t.g + 1] - t.lo : p.K;
@@ -255,18 +274,27 @@ __device__ __forceinline__ FTile decode_unit(const F8Params& p, const int* seg, 
   const int first = band * BAND;
   const int width = min(tiles - first, BAND);
   v -= first * p.m_tiles;
-  t.m0 = (v / width) * (128 * CG);
-  t.c0 = (first + v % width) * per;
-  t.ncols = min(per, n - t.c0);
+  const int ragged = (first + v % width) * per;
+  if constexpr (MODE == ROWS) {
+    t.m0 = ragged;
+    t.c0 = (v / width) * BN;
+    t.rows = n - ragged;
+    t.ncols = min(BN, p.M - t.c0);
+  } else {
+    t.m0 = (v / width) * (128 * CG);
+    t.c0 = ragged;
+    t.rows = 0;
+    t.ncols = min(per, n - t.c0);
+  }
   t.mma_n = p.weight || p.q_mn ? BN : (t.ncols + 16 * CG - 1) / (16 * CG) * (16 * CG);
   t.nkb = (depth + BLOCK - 1) / BLOCK;
   t.last = depth - BLOCK * (t.nkb - 1);
   return t;
 }
 
-template <int CG, int BN, int STAGES, bool VEC>
-__global__ void __launch_bounds__(F8_THREADS, 1) f8_kernel(const __grid_constant__ F8Params p) {
-  using C = F8Cfg<CG, BN, STAGES, VEC>;
+template <int CG, int BN, int STAGES, Scaling MODE>
+__global__ void __launch_bounds__(F8Cfg<CG, BN, STAGES, MODE>::THREADS, 1) f8_kernel(const __grid_constant__ F8Params p) {
+  using C = F8Cfg<CG, BN, STAGES, MODE>;
   extern __shared__ uint8_t smem_raw[];
   const uint32_t raw = smem_u32(smem_raw);
   const uint32_t sbase = (raw + 1023u) & ~1023u;
@@ -300,7 +328,7 @@ __global__ void __launch_bounds__(F8_THREADS, 1) f8_kernel(const __grid_constant
   if (warp == 0 && lane == 0 && (p.weight ? p.R : p.K) > 0) {
     prefetch_tmap(&p.tmap_p);
     prefetch_tmap(&p.tmap_q);
-    if (!p.weight && !p.q_mn) prefetch_tmap(&p.tmap_q16);
+    if (MODE == COLUMNS) prefetch_tmap(&p.tmap_q16);
   }
   if (threadIdx.x == 96) {
     for (uint32_t s = 0; s < STAGES; ++s) {
@@ -311,16 +339,16 @@ __global__ void __launch_bounds__(F8_THREADS, 1) f8_kernel(const __grid_constant
     }
     for (uint32_t b = 0; b < 2; ++b) {
       mbar_init(accf_bar(b), 1);
-      mbar_init(acce_bar(b), EPI_WARPS * CG);
+      mbar_init(acce_bar(b), C::EPI_WARPS * CG);
     }
     mbar_init(drain_bar, 1);
     for (uint32_t i = 0; i < TILES; ++i) {
       mbar_init(tile_full(i), 1);
-      mbar_init(tile_empty(i), 3 + EPI_WARPS);
+      mbar_init(tile_empty(i), 3 + C::EPI_WARPS);
     }
     for (uint32_t i = 0; i < SLOTS; ++i) {
-      mbar_init(scf_bar(i), 1);
-      mbar_init(sce_bar(i), EPI_WARPS);
+      mbar_init(scf_bar(i), 32);
+      mbar_init(sce_bar(i), C::EPI_WARPS);
     }
     *abort_flag = 0u;
     fence_mbarrier_init();
@@ -333,7 +361,7 @@ __global__ void __launch_bounds__(F8_THREADS, 1) f8_kernel(const __grid_constant
   }
   // offsets, each clamped to [the previous one, R], and the units before each group
   if (p.offsets) {
-    for (int g = threadIdx.x; g <= p.G; g += F8_THREADS) seg[g] = p.offsets[g];
+    for (int g = threadIdx.x; g <= p.G; g += C::THREADS) seg[g] = p.offsets[g];
   } else if (threadIdx.x < 2) {
     seg[threadIdx.x] = threadIdx.x ? p.R : 0;
   }
@@ -354,7 +382,7 @@ __global__ void __launch_bounds__(F8_THREADS, 1) f8_kernel(const __grid_constant
       // units of group g - 1
       int tiles = 0, per, units = 0;
       if (g >= 1 && g <= p.G && !p.weight) {
-        split_columns<CG, BN>(v - before, p.q_mn, tiles, per);
+        split_ragged<CG, BN, MODE>(v - before, p.q_mn, tiles, per);
         units = tiles * p.m_tiles;
       }
 #pragma unroll
@@ -380,7 +408,7 @@ __global__ void __launch_bounds__(F8_THREADS, 1) f8_kernel(const __grid_constant
   int total_units;
   if (p.weight) {
     int tiles, per;
-    split_columns<CG, BN>(p.C, true, tiles, per);
+    split_ragged<CG, BN, MODE>(p.C, true, tiles, per);
     total_units = p.G * tiles * p.m_tiles;
   } else {
     total_units = p.K > 0 ? pre[p.G] : 0;
@@ -397,15 +425,15 @@ __global__ void __launch_bounds__(F8_THREADS, 1) f8_kernel(const __grid_constant
     return true;
   };
 
-  // 384 threads x 168 registers at launch: 88 for each of the four warps that
-  // feed, 208 for the eight that hold sums
+  // registers at launch (384 threads x 168, 512 x 128): few for the four warps
+  // that feed, more for those that hold sums
   if (warp < 4) {
-  set_registers<false, 88>();
+  set_registers<false, C::PARTS == 4 ? 64 : C::PARTS == 3 ? 56 : 88>();
   if (warp == 3) {
     // ------------------------------------------- tile list and blocks' scales
     uint32_t n = 0, it = 0;
     auto publish = [&](int u, FTile& t) {
-      t = decode_unit<CG, BN>(p, seg, pre, u);
+      t = decode_unit<CG, BN, MODE>(p, seg, pre, u);
       const uint32_t i = n % TILES;
       if (!wait_inline(tile_empty(i), ((n / TILES) & 1u) ^ 1u, wctx, SITE_PROD_EMPTY)) return false;
       if (lane == 0) {
@@ -423,46 +451,38 @@ __global__ void __launch_bounds__(F8_THREADS, 1) f8_kernel(const __grid_constant
       // the tile after this one, ahead of this one's scales
       if (u + num_clusters < total_units && !publish(u + num_clusters, next)) break;
       const int b0 = p.weight ? t.lo / BLOCK + t.g : 0;
-      const float* sq = p.sq + b0 * p.sq_b + (p.weight ? t.c0 : t.lo + t.c0);
       const int m0 = t.m0 + static_cast<int>(rank) * 128;
-      const float* sp = VEC ? p.sp + b0 * p.sp_b + m0 : p.sp + t.g * p.sp_group + (m0 / BLOCK) * p.sp_m;
-      for (int kb = 0; kb < t.nkb && ok; kb += BATCH) {
-        const int blocks = min(BATCH, t.nkb - kb);
-        float q[BATCH][BN / 32], r[BATCH][VEC ? 4 : 1];
-#pragma unroll
-        for (int j = 0; j < BATCH; ++j) {
-#pragma unroll
-          for (int i = 0; i < BN / 32; ++i)
-            q[j][i] = j < blocks && lane + 32 * i < t.ncols ? __ldg(sq + (kb + j) * p.sq_b + lane + 32 * i) : 0.0f;
-          if constexpr (VEC) {
-#pragma unroll
-            for (int i = 0; i < 4; ++i)
-              r[j][i] = j < blocks && m0 + lane + 32 * i < p.M ? __ldg(sp + (kb + j) * p.sp_b + lane + 32 * i) : 0.0f;
-          } else {
-            r[j][0] = j < blocks && m0 < p.M ? __ldg(sp + (kb + j) * p.sp_b) : 0.0f;
-          }
+      // single scales of `n` columns or rows, and those of the other operand
+      const int n = MODE == ROWS ? t.rows - static_cast<int>(rank) * 128 : t.ncols;
+      const float* fine = p.fine + b0 * p.fine_b + (p.weight ? t.c0 : MODE == ROWS ? t.lo + m0 : t.lo + t.c0);
+      const float* other = MODE == BOTH   ? p.other + b0 * p.other_b + m0
+                           : MODE == ROWS ? p.other + t.g * p.other_group + (t.c0 / BLOCK + lane) * p.other_row
+                                          : p.other + t.g * p.other_group + (m0 / BLOCK) * p.other_row;
+      constexpr int FINE = MODE == ROWS ? 128 : BN;
+      for (int kb = 0; kb < t.nkb; ++kb, ++it) {
+        const uint32_t i = it % SLOTS;
+        if (!wait_inline(sce_bar(i), ((it / SLOTS) & 1u) ^ 1u, wctx, SITE_PROD_EMPTY)) {
+          ok = false;
+          break;
         }
+        const uint32_t at = slot_at(i) + 4u * lane;
 #pragma unroll
-        for (int j = 0; j < BATCH; ++j) {
-          if (j >= blocks) break;
-          const uint32_t i = it % SLOTS;
-          if (!wait_inline(sce_bar(i), ((it / SLOTS) & 1u) ^ 1u, wctx, SITE_PROD_EMPTY)) {
-            ok = false;
-            break;
-          }
-          const uint32_t at = slot_at(i) + 4u * lane;
+        for (int k = 0; k < FINE / 32; ++k)
+          if (lane + 32 * k < FINE) copy_f32(at + 128u * k, fine + lane + 32 * k, lane + 32 * k < n);
+        if constexpr (MODE == BOTH) {
 #pragma unroll
-          for (int k = 0; k < BN / 32; ++k) st_shared_f32(at + 128u * k, VEC ? q[j][k] : q[j][k] * r[j][0]);
-          if constexpr (VEC) {
-#pragma unroll
-            for (int k = 0; k < 4; ++k) st_shared_f32(at + 4u * BN + 128u * k, r[j][k]);
-          }
-          __syncwarp();
-          if (lane == 0) mbar_arrive(scf_bar(i));
-          ++it;
+          for (int k = 0; k < 4; ++k)
+            copy_f32(at + 4u * FINE + 128u * k, other + lane + 32 * k, m0 + lane + 32 * k < p.M);
+        } else if (lane < (MODE == ROWS ? BN / BLOCK : 1)) {
+          copy_f32(at + 4u * FINE, other, (MODE == ROWS ? t.c0 + BLOCK * lane : m0) < p.M);
         }
+        copies_arrive(scf_bar(i));
+        fine += p.fine_b;
+        other += p.other_b;
       }
     }
+    // none in flight when the CTA ends
+    asm volatile("cp.async.wait_all;" ::: "memory");
   } else if (warp != 1) {
     // ---------------------------------------------- producers, of P and of Q
     const bool brings_p = warp == 0;
@@ -475,8 +495,11 @@ __global__ void __launch_bounds__(F8_THREADS, 1) f8_kernel(const __grid_constant
       const int half = t.mma_n / CG;
       const int m0 = t.m0 + static_cast<int>(rank) * 128;
       const int c0 = t.c0 + static_cast<int>(rank) * half;
-      const bool q_mn = p.weight || p.q_mn;
-      const uint32_t tx = C::P_BYTES + static_cast<uint32_t>(half * 128);
+      // the group is in the rows of the one operand and the matrix of the other
+      const int p_row = MODE == ROWS ? t.lo + m0 : m0, p_mat = MODE == ROWS || p.weight ? 0 : t.g;
+      const int q_row = MODE == ROWS || p.weight ? c0 : t.lo + c0, q_mat = MODE == ROWS ? t.g : 0;
+      const bool boxed = MODE == ROWS || p.weight || p.q_mn || half == C::Q_ROWS;  // Q in one box
+      const uint32_t tx = C::P_BYTES + static_cast<uint32_t>(boxed ? C::Q_BYTES : half * 128);
       for (int kb = 0; kb < t.nkb; ++kb) {
         if (!wait_inline(empty_bar(s), ph ^ 1u, wctx, SITE_PROD_EMPTY)) {
           ok = false;
@@ -501,15 +524,15 @@ __global__ void __launch_bounds__(F8_THREADS, 1) f8_kernel(const __grid_constant
           } else if (brings_p) {
             if (rank == 0) mbar_arrive_expect_tx(full_bar(s), tx * CG);
             if (!p.p_mn)
-              tma_load3<CG>(sp, &p.tmap_p, k0, m0, t.g, fb);
+              tma_load3<CG>(sp, &p.tmap_p, k0, p_row, p_mat, fb);
             else
-              tma_load3<CG>(sp, &p.tmap_p, m0, p.weight ? t.lo + k0 : k0, p.weight ? 0 : t.g, fb);
-          } else if (q_mn) {
-            tma_load3<CG>(sq, &p.tmap_q, c0, p.weight ? t.lo + k0 : k0, 0, fb);
-          } else if (half == C::Q_ROWS) {
-            tma_load3<CG>(sq, &p.tmap_q, k0, t.lo + c0, 0, fb);
+              tma_load3<CG>(sp, &p.tmap_p, p_row, p.weight ? t.lo + k0 : k0, p_mat, fb);
+          } else if (p.q_mn) {
+            tma_load3<CG>(sq, &p.tmap_q, q_row, p.weight ? t.lo + k0 : k0, q_mat, fb);
+          } else if (boxed) {
+            tma_load3<CG>(sq, &p.tmap_q, k0, q_row, q_mat, fb);
           } else {
-            for (int i = 0; i < half; i += 16) tma_load3<CG>(sq + 128 * i, &p.tmap_q16, k0, t.lo + c0 + i, 0, fb);
+            for (int i = 0; i < half; i += 16) tma_load3<CG>(sq + 128 * i, &p.tmap_q16, k0, q_row + i, q_mat, fb);
           }
         }
         __syncwarp();
@@ -620,19 +643,20 @@ __global__ void __launch_bounds__(F8_THREADS, 1) f8_kernel(const __grid_constant
   }
   } else {
     // ------------------------------------------------------------ epilogue
-    set_registers<true, 208>();
+    set_registers<true, C::PARTS == 4 ? 104 : C::PARTS == 3 ? 152 : 208>();
     const int q = warp & 3;            // TMEM lane quadrant
-    const int part = (warp - 4) >> 2;  // 32-column chunks part, part + 2, ...
-    constexpr int MINE = (BN + 63) / 64;
+    const int part = (warp - 4) >> 2;  // 32-column chunks part, part + PARTS, ...
+    constexpr int ACROSS = 32 * C::PARTS;  // a warp's chunks of 32 columns lie so far apart
+    constexpr int MINE = MODE == ROWS ? 1 : (BN + ACROSS - 1) / ACROSS;
     uint32_t tcount = 0, n = 0, stores = 0;
-    const uint32_t buf0 = sbase + C::EPI_OFF + static_cast<uint32_t>((warp - 4) * 2 * STAGING_BYTES);
-    // the staging tile to fill next: its store before the last has read it
+    const uint32_t buf0 = sbase + C::EPI_OFF + static_cast<uint32_t>((warp - 4) * C::STAGING * STAGING_BYTES);
+    // the staging tile to fill next: its last store has read it
     auto staging = [&] {
-      if (stores >= 2) {
-        if (lane == 0) bulk_wait_group_read<1>();
+      if (stores >= C::STAGING) {
+        if (lane == 0) bulk_wait_group_read<C::STAGING - 1>();
         __syncwarp();
       }
-      return buf0 + (stores & 1u) * STAGING_BYTES;
+      return buf0 + stores % C::STAGING * STAGING_BYTES;
     };
     auto send = [&](uint32_t buf, int m0, int c, int g) {
       fence_proxy_async_shared();
@@ -647,12 +671,116 @@ __global__ void __launch_bounds__(F8_THREADS, 1) f8_kernel(const __grid_constant
     for (int u = cluster_id; u < total_units; u += num_clusters) {
       FTile t;
       if (!fetch(n++, t)) break;
+      if constexpr (MODE == ROWS) {
+        constexpr int COLS = BN / C::PARTS, CHUNKS = COLS / 32, STEP = 2;
+        const int c_warp = COLS * part;  // this warp's columns of the tile
+        const int mine = (t.ncols - c_warp + 31) / 32;
+        uint64_t sum[CHUNKS][16];  // pairs of columns
+#pragma unroll
+        for (int i = 0; i < CHUNKS; ++i)
+#pragma unroll
+          for (int k = 0; k < 16; ++k) sum[i][k] = 0ull;
+        bool done = true;
+        for (int kb = 0; kb < t.nkb; ++kb, ++tcount) {
+          const uint32_t b = tcount & 1u, slot = tcount % SLOTS;
+          done = wait_inline(scf_bar(slot), (tcount / SLOTS) & 1u, wctx, SITE_EPI_ACC_FULL);
+          if (!done) break;
+          const uint32_t at = slot_at(slot);
+          const float f = ld_shared_f32(at + 4u * (32 * q + lane)) * ld_shared_f32(at + 4u * (128 + c_warp / BLOCK));
+          const uint64_t ff = pair(__float_as_uint(f), __float_as_uint(f));
+          done = wait_inline(accf_bar(b), (tcount >> 1) & 1u, wctx, SITE_EPI_ACC_FULL);
+          if (!done) break;
+          tc_fence_after();
+#pragma unroll
+          for (int i = 0; i < CHUNKS; i += STEP) {
+            if (i >= mine) break;
+            uint32_t r[STEP][32];
+#pragma unroll
+            for (int j = 0; j < STEP; ++j) tmem_ld_32x32b_x32(lanes + b * BN + c_warp + 32 * (i + j), r[j]);
+            tc_wait_ld();
+#pragma unroll
+            for (int j = 0; j < STEP; ++j)
+#pragma unroll
+              for (int k = 0; k < 16; ++k) add_scaled(sum[i + j][k], r[j][2 * k], r[j][2 * k + 1], ff);
+          }
+          tc_fence_before();
+          __syncwarp();
+          if (lane == 0) {
+            mbar_arrive(sce_bar(slot));
+            if constexpr (CG == 2)
+              mbar_arrive_relaxed(mapa_shared(acce_bar(b), 0));  // no memory to order, only TMEM reads
+            else
+              mbar_arrive(acce_bar(b));
+          }
+        }
+        if (!done) break;
+        const int m_warp = static_cast<int>(rank) * 128 + 32 * q;  // the warp's first row in the tile
+        const int rows = min(32, t.rows - m_warp);
+        const int row0 = t.lo + t.m0 + m_warp;
+#pragma unroll
+        for (int i = 0; i < CHUNKS; ++i) {
+          if (i >= mine || rows <= 0) break;
+          const int n0 = t.c0 + c_warp + 32 * i;
+          const bool boxed = p.d_tma && rows == 32;  // columns clip at the map's end, a group's rows do not
+          uint8_t* dst = static_cast<uint8_t*>(p.D) + (static_cast<int64_t>(row0) * p.ldd + n0 + lane) * p.d_size;
+          if (p.d_type == OUT_F32) {
+            // two staging tiles of 16 rows
+            if (lane == 0) bulk_wait_group_read<0>();
+            __syncwarp();
+            const uint32_t row = static_cast<uint32_t>(lane) & 15u;
+            const uint32_t to = buf0 + STAGING_BYTES * (static_cast<uint32_t>(lane) >> 4) + 128u * row;
+#pragma unroll
+            for (uint32_t j = 0; j < 8; ++j) {
+              uint32_t w[4];
+              unpair(sum[i][2 * j], w[0], w[1]);
+              unpair(sum[i][2 * j + 1], w[2], w[3]);
+              st_shared_v4(to + 16u * (j ^ (row & 7u)), w[0], w[1], w[2], w[3]);
+            }
+            if (boxed) {
+              send(buf0, n0, row0, 0);
+              send(buf0 + STAGING_BYTES, n0, row0 + 16, 0);
+              continue;
+            }
+            __syncwarp();
+            for (int k = 0; k < rows; ++k) {
+              const uint32_t from = buf0 + 128u * k + 16u * ((static_cast<uint32_t>(lane) >> 2) ^ (k & 7u)) + 4u * (lane & 3u);
+              if (n0 + lane < p.M) *reinterpret_cast<float*>(dst + k * p.ldd * 4) = ld_shared_f32(from);
+            }
+            __syncwarp();
+            continue;
+          }
+          const uint32_t buf = staging();
+          const bool bf = p.d_type == OUT_BF16;
+#pragma unroll
+          for (uint32_t j = 0; j < 4; ++j) {
+            uint32_t w[4];
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+              uint32_t lo, hi;
+              unpair(sum[i][4 * j + k], lo, hi);
+              w[k] = bf ? pack_bf16(lo, hi) : pack_f16(lo, hi);
+            }
+            st_shared_v4(buf + 64u * lane + 16u * (j ^ ((static_cast<uint32_t>(lane) >> 1) & 3u)), w[0], w[1], w[2], w[3]);
+          }
+          if (boxed) {
+            send(buf, n0, row0, 0);
+            continue;
+          }
+          __syncwarp();
+          for (int k = 0; k < rows; ++k) {
+            const uint32_t from = buf + 64u * k + 16u * ((static_cast<uint32_t>(lane) >> 3) ^ ((k >> 1) & 3u)) + 2u * (lane & 7u);
+            if (n0 + lane < p.M) *reinterpret_cast<uint16_t*>(dst + k * p.ldd * 2) = ld_shared_u16(from);
+          }
+          __syncwarp();
+        }
+        continue;
+      }
       uint64_t sum[MINE][2][8];  // chunk, 16 rows, pairs of columns as in the fragment
 #pragma unroll
       for (int i = 0; i < MINE; ++i)
 #pragma unroll
         for (int k = 0; k < 16; ++k) sum[i][k >> 3][k & 7] = 0ull;
-      const int mine = (t.ncols - 32 * part + 63) >> 6;  // this warp's chunks of 32 columns that exist
+      const int mine = (t.ncols - 32 * part + ACROSS - 1) / ACROSS;  // this warp's chunks of 32 columns that exist
       bool done = true;
       for (int kb = 0; kb < t.nkb; ++kb, ++tcount) {
         const uint32_t b = tcount & 1u, slot = tcount % SLOTS;
@@ -661,34 +789,49 @@ __global__ void __launch_bounds__(F8_THREADS, 1) f8_kernel(const __grid_constant
         if (!done) break;
         tc_fence_after();
         const uint32_t at = slot_at(slot);
-        uint64_t row[4];  // P's factors of this lane's rows lane / 4 + 8 h, twice
-        if constexpr (VEC) {
+        uint64_t row[MODE == BOTH ? 4 : 1];  // P's factors of this lane's rows lane / 4 + 8 h (or of all), twice
 #pragma unroll
-          for (int h = 0; h < 4; ++h) {
-            const uint32_t r = __float_as_uint(ld_shared_f32(at + 4u * (BN + 32 * q + 8 * h + (lane >> 2))));
-            row[h] = pair(r, r);
-          }
+        for (int h = 0; h < (MODE == BOTH ? 4 : 1); ++h) {
+          const uint32_t r = __float_as_uint(ld_shared_f32(at + 4u * (MODE == BOTH ? BN + 32 * q + 8 * h + (lane >> 2) : BN)));
+          row[h] = pair(r, r);
         }
-        // fragments of 16 rows by 32 columns, the next one's read in flight meanwhile
+        // fragments of 16 rows by 32 columns, the next step's reads in flight meanwhile
         const uint32_t from = lanes + b * BN + 32 * part;
-        uint32_t r[2][16];
+        constexpr int STEP = 2, BUF = 1;  // fragments a step, steps in flight
+        uint32_t r[BUF][STEP][16];
+        auto read = [&](int h0) {
+#pragma unroll
+          for (int h = h0; h < h0 + STEP; ++h)
+            if (h < 2 * MINE && h / 2 < mine)
+              tmem_ld_16x256b_x4(from + ACROSS * (h / 2) + (static_cast<uint32_t>(h & 1) << 20), r[h / STEP % BUF][h % STEP]);
+        };
         uint64_t f[4];  // factors of this lane's columns 8 j + 2 (lane % 4), + 1
-        if (mine > 0) tmem_ld_16x256b_x4(from, r[0]);
+        if (BUF == 2) read(0);
 #pragma unroll
-        for (int h = 0; h < 2 * MINE; ++h) {
-          if (h / 2 >= mine) break;
-          if ((h & 1) == 0) {
+        for (int h0 = 0; h0 < 2 * MINE; h0 += STEP) {
+          if (h0 / 2 >= mine) break;
+          if (BUF == 1) read(h0);
 #pragma unroll
-            for (int j = 0; j < 4; ++j) f[j] = ld_shared_b64(at + 4u * (32 * part + 32 * h + 8 * j + 2 * (lane & 3)));
-          }
-          wait_ld16(r[h & 1]);
-          if (h + 1 < 2 * MINE && (h + 1) / 2 < mine)
-            tmem_ld_16x256b_x4(from + 64 * ((h + 1) / 2) + (static_cast<uint32_t>((h + 1) & 1) << 20), r[(h + 1) & 1]);
+          for (int h = h0; h < h0 + STEP; ++h) {
+            if ((h & 1) == 0) {
 #pragma unroll
-          for (int k = 0; k < 8; ++k) {
-            const uint64_t v = pair(r[h & 1][2 * k], r[h & 1][2 * k + 1]);
-            uint64_t& to = sum[h / 2][h & 1][k];
-            to = VEC ? fma2(mul2(v, f[k / 2]), row[2 * (h & 1) + (k & 1)], to) : fma2(v, f[k / 2], to);
+              for (int j = 0; j < 4; ++j) {
+                f[j] = ld_shared_b64(at + 4u * (32 * part + ACROSS * (h / 2) + 8 * j + 2 * (lane & 3)));
+                if constexpr (MODE != BOTH) f[j] = mul2(f[j], row[0]);
+              }
+            }
+            if (h == h0) {
+              tc_wait_ld();
+              if (BUF == 2) read(h0 + STEP);
+            }
+#pragma unroll
+            for (int k = 0; k < 8; ++k) {
+              uint32_t(&v)[16] = r[h / STEP % BUF][h % STEP];
+              if constexpr (MODE == BOTH)
+                add_scaled(sum[h / 2][h & 1][k], v[2 * k], v[2 * k + 1], f[k / 2], row[2 * (h & 1) + (k & 1)]);
+              else
+                add_scaled(sum[h / 2][h & 1][k], v[2 * k], v[2 * k + 1], f[k / 2]);
+            }
           }
         }
         tc_fence_before();
@@ -710,7 +853,7 @@ __global__ void __launch_bounds__(F8_THREADS, 1) f8_kernel(const __grid_constant
                      (p.weight ? t.g * p.stride_d * p.d_size : 0) + static_cast<int64_t>(m_warp + lane) * p.d_size;
 #pragma unroll
       for (int i = 0; i < MINE; ++i) {
-        const int c = 32 * part + 64 * i;
+        const int c = 32 * part + ACROSS * i;
         if (i >= mine || m_warp >= p.M) break;
         // rows of a matrix clip at the map's end, rows of a group do not
         const bool boxed = p.d_tma && (p.weight || c + 32 <= t.ncols);
@@ -785,7 +928,7 @@ __global__ void __launch_bounds__(F8_THREADS, 1) f8_kernel(const __grid_constant
           r += (end - 1 - r) / gridDim.x * gridDim.x;  // the last row below `end` this block meets
           continue;
         }
-        for (int m = t; m < p.M; m += 32 * EPI_WARPS) {
+        for (int m = t; m < p.M; m += 32 * C::EPI_WARPS) {
           const int64_t i = r * p.ldd + m;
           if (p.d_type == OUT_F32)
             static_cast<float*>(p.D)[i] = 0.0f;
@@ -807,10 +950,10 @@ __global__ void __launch_bounds__(F8_THREADS, 1) f8_kernel(const __grid_constant
 
 // ---------------------------------------------------------------------- host
 
-template <int CG, int BN, int STAGES, bool VEC>
+template <int CG, int BN, int STAGES, Scaling MODE>
 KernelInfo variant() {
-  using C = F8Cfg<CG, BN, STAGES, VEC>;
-  return {reinterpret_cast<const void*>(&f8_kernel<CG, BN, STAGES, VEC>), C::SMEM_BYTES, CG, BN, KIND_F16, F8_THREADS};
+  using C = F8Cfg<CG, BN, STAGES, MODE>;
+  return {reinterpret_cast<const void*>(&f8_kernel<CG, BN, STAGES, MODE>), C::SMEM_BYTES, CG, BN, KIND_F16, C::THREADS};
 }
 
 int64_t ceil_div(int64_t a, int64_t b) { return (a + b - 1) / b; }
@@ -842,31 +985,34 @@ int check_output(const void* p, int64_t inner, int64_t* ld, tcg_dtype type) {
   return misaligned(p, type == TCG_F32 ? 4 : 2) ? TCG_ERR_ALIGNMENT : TCG_OK;
 }
 
-// Fills what the operands' majors decide: descriptors, steps and maps.  P is
-// [groups][rows m][K] or, MN-major, [groups][K][M]; Q likewise without groups.
-int set_operands(F8Params* p, const KernelInfo& ki, tcg_input type, const void* P, bool p_mn, int64_t ldp,
-                 int64_t stride_p, int64_t groups, int64_t p_depth, const void* Q, bool q_mn, int64_t ldq,
-                 int64_t q_extent, int64_t q_depth) {
-  p->p_mn = p_mn;
-  p->q_mn = q_mn;
-  p->p_hi = p_mn ? sdesc_hi(128 * BLOCK, 1024, SW_128B) : sdesc_hi(16, 1024, SW_128B);
-  p->q_hi = q_mn ? sdesc_hi(128 * BLOCK, 1024, SW_128B) : sdesc_hi(16, 1024, SW_128B);
-  p->p_kstep = p_mn ? 32 * 128 / 16 : 32 / 16;
-  p->q_kstep = q_mn ? 32 * 128 / 16 : 32 / 16;
+// An operand: `groups` matrices of `rows` rows along the output, `depth` codes
+// each; MN-major: of `depth` rows.
+struct Operand {
+  const void* codes;
+  bool mn;
+  int64_t ld, stride, groups, rows, depth;
+};
+
+// Fills what the operands' majors decide: descriptors, steps and maps.
+int set_operands(F8Params* p, const KernelInfo& ki, tcg_input type, const Operand& P, const Operand& Q) {
+  p->p_mn = P.mn;
+  p->q_mn = Q.mn;
+  p->p_hi = P.mn ? sdesc_hi(128 * BLOCK, 1024, SW_128B) : sdesc_hi(16, 1024, SW_128B);
+  p->q_hi = Q.mn ? sdesc_hi(128 * BLOCK, 1024, SW_128B) : sdesc_hi(16, 1024, SW_128B);
+  p->p_kstep = P.mn ? 32 * 128 / 16 : 32 / 16;
+  p->q_kstep = Q.mn ? 32 * 128 / 16 : 32 / 16;
   const uint32_t format = type == TCG_IN_E5M2 ? MXF_E5M2 : MXF_E4M3;
   // kind::f8f6f4's descriptor: D fp32, then formats, majors and sizes as of kind::f16
-  p->idesc = (1u << 4) | (format << 7) | (format << 10) | (static_cast<uint32_t>(p_mn) << 15) |
-             (static_cast<uint32_t>(q_mn) << 16) | (static_cast<uint32_t>(128 * ki.cta_group >> 4) << 24);
-  if (p_depth == 0) return TCG_OK;
-  const uint64_t M = p->M;
-  if (int rc = p_mn ? make_byte_map(&p->tmap_p, P, M, p_depth, groups, ldp, stride_p, 128, BLOCK)
-                    : make_byte_map(&p->tmap_p, P, p_depth, M, groups, ldp, stride_p, 128, 128))
-    return rc;
-  if (q_mn) return make_byte_map(&p->tmap_q, Q, q_extent, q_depth, 1, ldq, q_depth * ldq, 128, BLOCK);
-  if (int rc = make_byte_map(&p->tmap_q, Q, q_depth, q_extent, 1, ldq, q_extent * ldq, 128,
-                             static_cast<uint32_t>(ki.bn / ki.cta_group)))
-    return rc;
-  return make_byte_map(&p->tmap_q16, Q, q_depth, q_extent, 1, ldq, q_extent * ldq, 128, 16);
+  p->idesc = (1u << 4) | (format << 7) | (format << 10) | (static_cast<uint32_t>(P.mn) << 15) |
+             (static_cast<uint32_t>(Q.mn) << 16) | (static_cast<uint32_t>(128 * ki.cta_group >> 4) << 24);
+  if (P.depth == 0) return TCG_OK;
+  const auto map = [](CUtensorMap* m, const Operand& o, uint32_t rows) {
+    return o.mn ? make_byte_map(m, o.codes, o.rows, o.depth, o.groups, o.ld, o.stride, 128, BLOCK)
+                : make_byte_map(m, o.codes, o.depth, o.rows, o.groups, o.ld, o.stride, 128, rows);
+  };
+  if (int rc = map(&p->tmap_p, P, 128)) return rc;
+  if (int rc = map(&p->tmap_q, Q, static_cast<uint32_t>(ki.bn / ki.cta_group))) return rc;
+  return Q.mn ? TCG_OK : map(&p->tmap_q16, Q, 16);
 }
 
 // Launches the variant on all SMs (or on fewer, never more than `units`
@@ -892,7 +1038,7 @@ int launch_f8(const KernelInfo& ki, F8Params& p, int dev, int64_t units, cudaStr
   p.timeout_ns = wait_timeout_ns();
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(static_cast<unsigned>(cg * std::max<int64_t>(1, std::min<int64_t>(units, clusters))), 1, 1);
-  cfg.blockDim = dim3(F8_THREADS, 1, 1);
+  cfg.blockDim = dim3(static_cast<unsigned>(ki.threads), 1, 1);
   cfg.dynamicSmemBytes = ki.smem_bytes;
   cfg.stream = s;
   cudaLaunchAttribute attr[2];
@@ -911,10 +1057,34 @@ int launch_f8(const KernelInfo& ki, F8Params& p, int dev, int64_t units, cudaStr
   return TCG_OK;
 }
 
-KernelInfo rows_variant(int64_t R, int G, bool q_mn, bool vec) {
-  if (vec) return variant<2, 256, 5, true>();
-  if (!q_mn && R <= 64 * static_cast<int64_t>(G)) return variant<1, 64, 7, false>();
-  return variant<2, 256, 5, false>();
+// How a product of R rows in G groups is run.
+struct Plan {
+  KernelInfo ki;
+  Scaling mode;
+};
+
+Plan choose(int64_t R, int G, bool a_mn, bool square) {
+  if (!square) return {variant<2, 256, 5, BOTH>(), BOTH};
+  if (!a_mn && R <= 64 * static_cast<int64_t>(G)) return {variant<1, 64, 7, COLUMNS>(), COLUMNS};
+  return {variant<2, 256, 5, ROWS>(), ROWS};
+}
+
+// A's rows and scales against B's, for the dense and the grouped product.
+int run_rows(const Plan& plan, F8Params& p, int dev, tcg_input type, const Operand& A, const float* SA, int64_t ld_sa,
+             const Operand& B, const float* SB, int64_t ld_sb, int64_t stride_sb, int64_t groups, cudaStream_t s) {
+  const bool rows = plan.mode == ROWS;
+  const int cg = plan.ki.cta_group;
+  p.m_tiles = static_cast<int>(ceil_div(p.M, rows ? plan.ki.bn : 128 * cg));
+  if (int rc = rows ? set_operands(&p, plan.ki, type, A, B) : set_operands(&p, plan.ki, type, B, A)) return rc;
+  p.fine = SA;
+  p.fine_b = ld_sa;
+  p.other = SB;
+  p.other_group = stride_sb;
+  p.other_row = B.mn ? 1 : ld_sb;
+  p.other_b = plan.mode == BOTH || B.mn ? ld_sb : 1;
+  // an upper bound of the units: a full tile per so many rows and one more per group
+  const int64_t per = rows ? 128 * cg : plan.ki.bn;
+  return launch_f8(plan.ki, p, dev, (p.R / per + groups) * (rows ? 1 : 2) * p.m_tiles, s);
 }
 
 int run_dense(tcg_input type, int64_t M, int64_t N, int64_t K, const void* A, tcg_major a_major, int64_t lda,
@@ -936,24 +1106,17 @@ int run_dense(tcg_input type, int64_t M, int64_t N, int64_t K, const void* A, tc
   }
   int dev;
   if (int rc = current_device_checked(&dev)) return rc;
-  const KernelInfo ki = rows_variant(M, 1, a_mn, !sb_square);
   F8Params p;
   std::memset(&p, 0, sizeof p);
   p.G = 1;
   p.R = static_cast<int>(M);
   p.M = static_cast<int>(N);
   p.K = static_cast<int>(K);
-  p.m_tiles = static_cast<int>(ceil_div(N, 128 * ki.cta_group));
-  if (int rc = set_operands(&p, ki, type, B, b_mn, ldb, (b_mn ? K : N) * ldb, 1, K, A, a_mn, lda, M, K)) return rc;
-  p.sq = SA;
-  p.sq_b = ld_sa;
-  p.sp = SB;
-  p.sp_m = b_mn ? 1 : ld_sb;
-  p.sp_b = !sb_square || b_mn ? ld_sb : 1;
   p.D = D;
   p.ldd = ldd;
   p.d_type = d_type;
-  return launch_f8(ki, p, dev, (M / ki.bn + 1) * 2 * p.m_tiles, s);
+  return run_rows(choose(M, 1, a_mn, sb_square), p, dev, type, {A, a_mn, lda, (a_mn ? K : M) * lda, 1, M, K}, SA, ld_sa,
+                  {B, b_mn, ldb, (b_mn ? K : N) * ldb, 1, N, K}, SB, ld_sb, 0, 1, s);
 }
 
 int run_grouped(tcg_input type, int64_t R, int64_t N, int64_t K, int G, const void* A, int64_t lda, const float* SA,
@@ -982,7 +1145,6 @@ int run_grouped(tcg_input type, int64_t R, int64_t N, int64_t K, int G, const vo
   }
   int dev;
   if (int rc = current_device_checked(&dev)) return rc;
-  const KernelInfo ki = rows_variant(R, G, false, false);
   F8Params p;
   std::memset(&p, 0, sizeof p);
   p.offsets = offsets;
@@ -990,19 +1152,11 @@ int run_grouped(tcg_input type, int64_t R, int64_t N, int64_t K, int G, const vo
   p.R = static_cast<int>(R);
   p.M = static_cast<int>(N);
   p.K = static_cast<int>(K);
-  p.m_tiles = static_cast<int>(ceil_div(N, 128 * ki.cta_group));
-  if (int rc = set_operands(&p, ki, type, B, mn, ldb, stride_b, G, K, A, false, lda, R, K)) return rc;
-  p.sq = SA;
-  p.sq_b = ld_sa;
-  p.sp = SB;
-  p.sp_group = stride_sb;
-  p.sp_m = mn ? 1 : ld_sb;
-  p.sp_b = mn ? ld_sb : 1;
   p.D = D;
   p.ldd = ldd;
   p.d_type = d_type;
-  // an upper bound of the units: a full tile per BN rows and one more per group
-  return launch_f8(ki, p, dev, (R / ki.bn + std::min<int64_t>(G, R)) * 2 * p.m_tiles, s);
+  return run_rows(choose(R, G, false, true), p, dev, type, {A, false, lda, R * lda, 1, R, K}, SA, ld_sa,
+                  {B, mn, ldb, stride_b, G, N, K}, SB, ld_sb, stride_sb, std::min<int64_t>(G, R), s);
 }
 
 int run_wgrad(tcg_input type, int64_t R, int64_t N, int64_t K, int G, const void* DY, int64_t lddy, const float* SDY,
@@ -1024,7 +1178,7 @@ int run_wgrad(tcg_input type, int64_t R, int64_t N, int64_t K, int G, const void
   }
   int dev;
   if (int rc = current_device_checked(&dev)) return rc;
-  const KernelInfo ki = rows_variant(R, G, true, true);
+  const KernelInfo ki = choose(R, G, true, false).ki;
   F8Params p;
   std::memset(&p, 0, sizeof p);
   p.offsets = offsets;
@@ -1034,11 +1188,11 @@ int run_wgrad(tcg_input type, int64_t R, int64_t N, int64_t K, int G, const void
   p.M = static_cast<int>(K);
   p.C = static_cast<int>(N);
   p.m_tiles = static_cast<int>(ceil_div(K, 128 * ki.cta_group));
-  if (int rc = set_operands(&p, ki, type, A, true, lda, R * lda, 1, R, DY, true, lddy, N, R)) return rc;
-  p.sq = SDY;
-  p.sq_b = ld_sdy;
-  p.sp = SA;
-  p.sp_b = ld_sa;
+  if (int rc = set_operands(&p, ki, type, {A, true, lda, R * lda, 1, K, R}, {DY, true, lddy, R * lddy, 1, N, R})) return rc;
+  p.fine = SDY;
+  p.fine_b = ld_sdy;
+  p.other = SA;
+  p.other_b = ld_sa;
   p.D = DW;
   p.ldd = lddw;
   p.stride_d = stride_dw;
