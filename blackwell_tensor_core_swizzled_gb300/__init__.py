@@ -52,6 +52,20 @@ _W4_ARGS = struct.Struct("@2i3q2iPqPP2qP2q3Piq")
 assert _W4_ARGS.size == ctypes.sizeof(GemvW4Args)
 
 
+class MoeFewArgs(ctypes.Structure):
+    """Mirror of ``tcg_moe_few_args``."""
+    _fields_ = [("x_type", _i32), ("w_type", _i32), ("T", _i64), ("H", _i64), ("I", _i64), ("topk", _i32), ("E", _i32),
+                ("X", _vp), ("ldx", _i64), ("expert", _vp), ("weight", _vp), ("W1", _vp), ("W3", _vp), ("ld1", _i64),
+                ("stride1", _i64), ("W2", _vp), ("ld2", _i64), ("stride2", _i64), ("S1", _vp), ("S3", _vp),
+                ("ld_s1", _i64), ("stride_s1", _i64), ("S2", _vp), ("ld_s2", _i64), ("stride_s2", _i64), ("work", _vp),
+                ("Y", _vp), ("y_type", _i32), ("ldy", _i64)]
+
+
+#: MoeFewArgs in its native layout
+_FEW_ARGS = struct.Struct("@2i3q2iPq4P2qP2q2P2qP2q2Piq")
+assert _FEW_ARGS.size == ctypes.sizeof(MoeFewArgs)
+
+
 class ProbeOperand(ctypes.Structure):
     """Mirror of ``tcg_probe_operand``."""
     _fields_ = [("image", _vp), ("bytes", _i32), ("major", _i32), ("ldo", _u32), ("sdo", _u32),
@@ -86,6 +100,8 @@ _SIGS = {
     "tcg_gemm_grouped_wgrad": ([_i32, _i64, _i64, _i64, _i32, _vp, _i64, _vp, _i64, _vp, _vp, _i32, _i64, _i64,
                                 _vp], _i32),
     "tcg_gemv_w4": ([_vp, _vp], _i32),
+    "tcg_moe_few": ([_vp, _vp], _i32),
+    "tcg_moe_few_work_bytes": ([_i64, _i32, _i64], _i64),
     "tcg_f8_quantize": ([_i32, _i32, _i32, _i64, _i64, _i32, _vp, _i64, _i32, _vp, _vp, _i64, _vp, _i64, _vp], _i32),
     "tcg_gemm_f8": ([_i32, _i64, _i64, _i64, _vp, _i32, _i64, _vp, _i64, _vp, _i32, _i64, _vp, _i64, _i32, _vp, _i32,
                      _i64, _vp], _i32),
@@ -316,6 +332,23 @@ def gemv_w4(fmt, in_type, R, N, K, A, lda, B, scale, D, d_type, ldd, group=0, ze
                       _ptr(D) or 0, d_type, ldd)
     rc = _lib.tcg_gemv_w4(a, _stream(stream))
     return _ok(rc, "gemv_w4") if check else rc
+
+
+def moe_few(x_type, w_type, T, H, I, topk, E, X, ldx, expert, weight, W1, W3, W2, work, Y, y_type, ldy, s1=None, s3=None,
+            s2=None, ld1=0, stride1=0, ld2=0, stride2=0, ld_s1=0, stride_s1=0, ld_s2=0, stride_s2=0, stream=None,
+            check=True):
+    """A mixture-of-experts layer for a few tokens (``tcg_moe_few``); returns the status (raises if ``check``)."""
+    a = _FEW_ARGS.pack(x_type, w_type, T, H, I, topk, E, _ptr(X) or 0, ldx, _ptr(expert) or 0, _ptr(weight) or 0,
+                       _ptr(W1) or 0, _ptr(W3) or 0, ld1, stride1, _ptr(W2) or 0, ld2, stride2, _ptr(s1) or 0,
+                       _ptr(s3) or 0, ld_s1, stride_s1, _ptr(s2) or 0, ld_s2, stride_s2, _ptr(work) or 0, _ptr(Y) or 0,
+                       y_type, ldy)
+    rc = _lib.tcg_moe_few(a, _stream(stream))
+    return _ok(rc, "moe_few") if check else rc
+
+
+def moe_few_work_bytes(T, topk, I) -> int:
+    """Bytes of moe_few's workspace (-1: sizes it does not take)."""
+    return _lib.tcg_moe_few_work_bytes(T, topk, I)
 
 
 def f8_quantize(q_type, blocks, R, C, x_type, X, ldx, Q, ldq, scale, ld_scale, pow2=False, groups=1, offsets=None,

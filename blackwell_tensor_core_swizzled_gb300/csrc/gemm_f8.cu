@@ -43,6 +43,7 @@
 #include "ptx.cuh"
 #include "ptx_moe.cuh"
 #include "tmem_ldst.cuh"
+#include "wait.cuh"
 
 namespace tcg {
 
@@ -105,28 +106,6 @@ __device__ __forceinline__ void mma_f8(uint32_t d, uint64_t a, uint64_t b, uint3
         "tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], %1, %2, %3, p;\n\t}" ::"r"(d),
         "l"(a), "l"(b), "r"(idesc), "r"(accum)
         : "memory");
-}
-
-// wait_uniform without a function call, across which the epilogue's sums would
-// be kept in local memory.
-__device__ __forceinline__ bool wait_inline(uint32_t bar, uint32_t parity, const WaitCtx& w, uint32_t site) {
-  bool ok = mbar_try_wait(bar, parity);
-  if (__all_sync(0xffffffffu, ok)) return true;
-#pragma unroll 1
-  for (int i = 0; i < 64 && !ok; ++i) ok = mbar_try_wait(bar, parity);
-  if (__all_sync(0xffffffffu, ok)) return true;
-  const uint64_t t0 = globaltimer();
-  while (!ok) {
-#pragma unroll 1
-    for (int i = 0; i < 32 && !ok; ++i) ok = mbar_try_wait(bar, parity);
-    if (ok || *w.abort_flag) break;
-    if (globaltimer() - t0 > w.timeout_ns) {
-      *w.abort_flag = 1u;
-      if (w.err) atomicCAS(w.err, 0ull, make_err(1u, site));
-      break;
-    }
-  }
-  return __all_sync(0xffffffffu, ok);
 }
 
 // A 4-byte copy global -> shared in flight (zero if !exists), and this lane's

@@ -1,0 +1,736 @@
+// A whole mixture-of-experts layer for a few tokens in two kernels.  Entry point,
+// host plan and kernels; the contract is in include/tcg.h.
+//
+//     y[t] = sum_e w[t, e] W2[e] (silu(W1[e] x[t]) * (W3[e] x[t]))
+//
+// Few tokens read each chosen expert's matrices once, so HBM bounds both
+// kernels, and what counts is that reads are always in flight.  The first makes
+// w h of every (expert, token) pair, the second multiplies by W2 and sums over a
+// token's experts.
+//
+// Every CTA finds the chosen experts by itself (a token mask for each), so no
+// kernel sorts.  A unit is 16 rows: of one expert's W1 and W3, or of y, whose
+// CTA then passes through all experts, so that sums over experts need neither
+// atomics nor memory.  A producer thread brings the rows in stages of 1 KB of
+// each (eight 128-byte slabs of 16 rows, one copy) into a ring, across units; each
+// of eight warps takes one slab, decodes it in registers and multiplies it with
+// mma.m16n8k16, tokens on the 8 columns: the tensor cores are idle most of the
+// time either way, and tcgen05 would want 8-bit weights against 8-bit
+// activations, or decoded ones in shared memory, at four times the bytes.
+//
+// The second kernel starts while the first runs (it needs half an SM): its lists
+// are made and its ring is full when the first ends.
+//
+// h is kept as two 16-bit values, h = hi + lo, both multiplied: one value of x's
+// type would add an error as large as that of rounding y (2.4e-3 instead of
+// 1.7e-3 of bf16 outputs' norm).
+#include <cuda.h>
+#include <cuda_bf16.h>
+#include <cuda_fp16.h>
+#include <cuda_runtime.h>
+
+#include <algorithm>
+#include <cstdint>
+#include <cstring>
+
+#include "common.h"
+#include "once.h"
+#include "ptx.cuh"
+#include "ptx_moe.cuh"
+#include "wait.cuh"
+
+namespace tcg {
+
+namespace {
+
+constexpr int BLOCK = 128;
+constexpr int MAX_TOKENS = 64;
+constexpr int MAX_TOPK = 64;
+constexpr int MAX_EXPERTS = 1024;
+constexpr int64_t MAX_EXTENT = int64_t{1} << 30;
+constexpr int WARPS = 8;                    // that multiply; one more brings the weights
+constexpr int FEW_THREADS = 32 * (WARPS + 1);
+constexpr int SLAB_BYTES = 16 * 128;
+constexpr int CHUNK = 128 * WARPS;          // bytes of a row in a stage
+constexpr int TILE_BYTES = SLAB_BYTES * WARPS;
+constexpr int RING_BYTES = 6 * TILE_BYTES;  // as stages of one matrix or two
+
+struct FewParams {
+  CUtensorMap slab[2];  // [E][128-byte slabs][rows][128]: W1 and W3, or W2
+  CUtensorMap edge[2];  // [E][rows][bytes] in single slabs, for a last stage whose rows end inside a slab
+  const int32_t* expert;
+  const float* weight;
+  int T, topk, E;
+  int K, N;        // length of the weights' rows, and their number
+  int row_bytes;
+  int matrices;
+  const uint16_t* X;  // [T][K]; second kernel: hi [pairs][K]
+  int64_t ldx;
+  uint16_t *hi, *lo;  // [pairs][ldh]
+  int64_t ldh;
+  const float* S[2];  // 8-bit weights' scales of 128 x 128
+  int64_t ld_s, stride_s;
+  void* Y;
+  int64_t ldy;
+  int y_type;
+  unsigned long long* err;
+  uint64_t timeout_ns;
+};
+
+// Shared memory behind the ring, from the sizes.
+struct Layout {
+  int sums, masks, list, base, token, weight, bars, bytes;
+  __host__ __device__ Layout(int T, int topk, int E, bool second) {
+    const int pairs = T * topk, most = pairs < E ? pairs : E;
+    int at = RING_BYTES;
+    auto take = [&](int n) {
+      const int here = at;
+      at += (n + 15) / 16 * 16;
+      return here;
+    };
+    sums = take(second ? WARPS * T * 16 * 4 : WARPS * 2 * 8 * 17 * 4);
+    masks = take(8 * E);
+    list = take(4 * most);
+    base = take(4 * (most + 1));
+    token = take(pairs);
+    weight = take(second ? 0 : 4 * pairs);
+    bars = take(2 * 6 * 8 + 8 * 4 + 16);
+    bytes = at + 1024;  // the ring starts on a swizzle period
+  }
+};
+
+// ---------------------------------------------------------------- arithmetic
+
+template <bool BF16>
+__device__ __forceinline__ void mma_16816(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
+  if constexpr (BF16)
+    asm volatile(
+        "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, {%0, %1, %2, %3};"
+        : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+        : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+  else
+    asm volatile(
+        "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, {%0, %1, %2, %3};"
+        : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+        : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+
+// Four E4M3 codes as two pairs of 16-bit values.  f16: values 0, 1 and 2, 3 by
+// conversion.  bf16, which has none: values 0, 2 and 1, 3; a code's seven lower
+// bits are a bf16's lower exponent bits and upper significand at a scale of
+// 2^-120 (subnormals included), which an exact multiplication takes out.
+template <bool BF16>
+__device__ __forceinline__ void decode4(uint32_t w, uint32_t& p, uint32_t& q) {
+  if constexpr (BF16) {
+    const uint32_t even = (w << 8 & 0x80008000u) | (w << 4 & 0x07f007f0u);
+    const uint32_t odd = (w & 0x80008000u) | (w >> 4 & 0x07f007f0u);
+    constexpr uint32_t SCALE = 0x7b807b80u;  // 2^120 twice
+    asm("mul.rn.bf16x2 %0, %1, %2;" : "=r"(p) : "r"(even), "r"(SCALE));
+    asm("mul.rn.bf16x2 %0, %1, %2;" : "=r"(q) : "r"(odd), "r"(SCALE));
+  } else {
+    asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(p) : "h"(static_cast<uint16_t>(w)));
+    asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(q) : "h"(static_cast<uint16_t>(w >> 16)));
+  }
+}
+
+// bit 7 of a byte: that code is a NaN (the bf16 decoding makes it 480)
+__device__ __forceinline__ uint32_t nan_codes(uint32_t w) { return (w & 0x7f7f7f7fu) + 0x01010101u; }
+
+__device__ __forceinline__ uint4 ld_shared_v4(uint32_t addr) {
+  uint4 v;
+  asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(addr));
+  return v;
+}
+
+template <bool BF16>
+__device__ __forceinline__ float to_f32(uint16_t v) {
+  if constexpr (BF16)
+    return __uint_as_float(static_cast<uint32_t>(v) << 16);
+  else
+    return __half2float(__ushort_as_half(v));
+}
+
+template <bool BF16>
+__device__ __forceinline__ uint16_t round16(float v) {
+  if constexpr (BF16)
+    return __bfloat16_as_ushort(__float2bfloat16_rn(v));
+  else
+    return __half_as_ushort(__float2half_rn(v));
+}
+
+__device__ __forceinline__ void workers_sync() { asm volatile("bar.sync 1, %0;" ::"n"(32 * WARPS) : "memory"); }
+
+// The same; true if all are.
+__device__ __forceinline__ bool workers_agree(bool ok) {
+  uint32_t all;
+  asm volatile(
+      "{\n\t.reg .pred p, q;\n\tsetp.ne.b32 p, %1, 0;\n\tbar.red.and.pred q, 1, %2, p;\n\tselp.b32 %0, 1, 0, q;\n\t}"
+      : "=r"(all)
+      : "r"(static_cast<uint32_t>(ok)), "n"(32 * WARPS)
+      : "memory");
+  return all != 0;
+}
+
+// -------------------------------------------------------------------- kernels
+
+// NT: 8-token columns.  W8: weights are E4M3 with scales, else of x's type.
+// SECOND: W2 and the sum over experts, else W1, W3 and the activation.
+template <bool BF16, bool W8, int NT, bool SECOND>
+__global__ void __launch_bounds__(FEW_THREADS, NT <= 2 ? 2 : 1) few_kernel(const __grid_constant__ FewParams p) {
+  extern __shared__ uint8_t smem_raw[];
+  const uint32_t raw = smem_u32(smem_raw);
+  const uint32_t sbase = (raw + 1023u) & ~1023u;
+  uint8_t* gbase = smem_raw + (sbase - raw);
+  const Layout at(p.T, p.topk, p.E, SECOND);
+  const int stage_bytes = TILE_BYTES * p.matrices, stages = RING_BYTES / stage_bytes;
+  unsigned long long* masks = reinterpret_cast<unsigned long long*>(gbase + at.masks);
+  int* list = reinterpret_cast<int*>(gbase + at.list);   // the chosen experts
+  int* base = reinterpret_cast<int*>(gbase + at.base);   // their first pair
+  uint8_t* token = gbase + at.token;                     // a pair's token
+  float* weight = reinterpret_cast<float*>(gbase + at.weight);
+  float* sums = reinterpret_cast<float*>(gbase + at.sums);
+  const uint32_t bar0 = sbase + at.bars;
+  auto full_bar = [&](uint32_t s) { return bar0 + 8u * s; };
+  auto empty_bar = [&](uint32_t s) { return bar0 + 8u * (6 + s); };
+  int* counts = reinterpret_cast<int*>(gbase + at.bars + 96);  // of eight ranges of experts
+  volatile uint32_t* abort_flag = reinterpret_cast<uint32_t*>(gbase + at.bars + 96 + 32);
+  const WaitCtx wctx{p.timeout_ns, p.err, abort_flag};
+
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int pairs = p.T * p.topk;
+  if (threadIdx.x == 0) {
+    for (int i = 0; i < p.matrices && p.row_bytes > 0; ++i) {
+      if (p.row_bytes >= 128) prefetch_tmap(&p.slab[i]);
+      prefetch_tmap(&p.edge[i]);
+    }
+    for (int s = 0; s < stages; ++s) {
+      mbar_init(full_bar(s), 1);
+      mbar_init(empty_bar(s), WARPS);
+    }
+    *abort_flag = 0u;
+    fence_mbarrier_init();
+  }
+  for (int e = threadIdx.x; e < p.E; e += FEW_THREADS) masks[e] = 0ull;
+  // The first kernel waits for what is before it.  The second starts after all
+  // CTAs of the first have, so that the choices and weights it reads ahead are
+  // complete; only h is not.
+  // (Rows of no length need no first kernel.)
+  if (!SECOND || p.row_bytes == 0) griddep_wait();
+  if constexpr (!SECOND) griddep_launch_dependents();
+  __syncthreads();
+  for (int i = threadIdx.x; i < pairs; i += FEW_THREADS) {
+    const unsigned e = static_cast<unsigned>(p.expert[i]);
+    if (e < static_cast<unsigned>(p.E)) atomicOr(&masks[e], 1ull << (i / p.topk));
+  }
+  __syncthreads();
+  // the chosen experts in rising order, each of eight warps 128 of them
+  unsigned votes[4];
+  if (warp < 8) {
+    int n = 0;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const int e = 128 * warp + 32 * i + lane;
+      votes[i] = __ballot_sync(0xffffffffu, e < p.E && masks[e] != 0ull);
+      n += __popc(votes[i]);
+    }
+    if (lane == 0) counts[warp] = n;
+  }
+  __syncthreads();
+  int chosen = 0;
+#pragma unroll
+  for (int w = 0; w < 8; ++w) {
+    if (w == warp) {
+      int n = chosen;
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        if (votes[i] >> lane & 1) list[n + __popc(votes[i] & ((1u << lane) - 1u))] = 128 * warp + 32 * i + lane;
+        n += __popc(votes[i]);
+      }
+    }
+    chosen += counts[w];
+  }
+  __syncthreads();
+
+  const int tiles = (p.N + 15) / 16;
+  const int units = SECOND ? tiles : chosen * tiles;
+  const int chunks = (p.row_bytes + CHUNK - 1) / CHUNK;
+  const int passes = SECOND ? chosen : 1;  // experts of a unit
+  // slabs of chunk c that exist
+  auto slabs_of = [&](int c) { return min(WARPS, (p.row_bytes - c * CHUNK + 127) / 128); };
+
+  if (warp == WARPS) {
+    // ------------------------------------------------------------- producer
+    uint32_t s = 0, ph = 0, sent = 0;
+    bool ok = true;
+    for (int u = blockIdx.x; u < units && ok; u += gridDim.x) {
+      const int n0 = (SECOND ? u : u % tiles) * 16;
+      for (int i = 0; i < passes && ok; ++i) {
+        const int e = list[SECOND ? i : u / tiles];
+        for (int c = 0; c < chunks; ++c) {
+          if (!wait_inline(empty_bar(s), ph ^ 1u, wctx, SITE_PROD_EMPTY)) {
+            ok = false;
+            break;
+          }
+          if (lane == 0) {
+            const uint32_t to = sbase + s * stage_bytes;
+            if (p.row_bytes % 128 == 0 || c + 1 < chunks) {
+              mbar_arrive_expect_tx(full_bar(s), static_cast<uint32_t>(stage_bytes));
+              for (int m = 0; m < p.matrices; ++m)
+                tma_load_4d(to + TILE_BYTES * m, &p.slab[m], 0, n0, c * WARPS, e, full_bar(s));
+            } else {
+              const int n = slabs_of(c);
+              mbar_arrive_expect_tx(full_bar(s), static_cast<uint32_t>(SLAB_BYTES * n * p.matrices));
+              for (int m = 0; m < p.matrices; ++m)
+                for (int w = 0; w < n; ++w)
+                  tma_load3<1>(to + TILE_BYTES * m + SLAB_BYTES * w, &p.edge[m], c * CHUNK + 128 * w, n0, e, full_bar(s));
+            }
+          }
+          __syncwarp();
+          ++sent;
+          if (++s == static_cast<uint32_t>(stages)) {
+            s = 0;
+            ph ^= 1u;
+          }
+        }
+      }
+    }
+    if (!ok && lane == 0) {
+      // let the copies in flight land before the CTA can exit
+      const uint32_t out = min(sent, static_cast<uint32_t>(stages));
+      for (uint32_t j = sent - out; j < sent; ++j) {
+        const uint64_t t0 = globaltimer();
+        while (!mbar_try_wait(full_bar(j % stages), (j / stages) & 1u) && globaltimer() - t0 < 20000000ull) {
+        }
+      }
+    }
+    return;
+  }
+
+  // ----------------------------------------------------------------- workers
+  // the pairs: experts in the list's order, their tokens rising
+  if (warp == 0) {
+    int run = 0;
+    for (int a0 = 0; a0 < chosen; a0 += 32) {
+      int n = a0 + lane < chosen ? __popcll(masks[list[a0 + lane]]) : 0, incl = n;
+#pragma unroll
+      for (int d = 1; d < 32; d <<= 1) {
+        const int o = __shfl_up_sync(0xffffffffu, incl, d);
+        if (lane >= d) incl += o;
+      }
+      if (a0 + lane < chosen) base[a0 + lane] = run + incl - n;
+      run += __shfl_sync(0xffffffffu, incl, 31);
+    }
+    if (lane == 0) base[chosen] = run;
+  }
+  workers_sync();
+  for (int a = warp; a < chosen; a += WARPS) {
+    const unsigned long long mask = masks[list[a]];
+    for (int t = lane; t < p.T; t += 32)
+      if (mask >> t & 1) {
+        const int pair = base[a] + __popcll(mask & ((1ull << t) - 1));
+        token[pair] = static_cast<uint8_t>(t);
+        if constexpr (!SECOND) {
+          float w = 0.0f;  // a token that names an expert twice gets it with both weights
+          for (int j = 0; j < p.topk; ++j)
+            if (p.expert[t * p.topk + j] == list[a]) w += p.weight ? p.weight[t * p.topk + j] : 1.0f;
+          weight[pair] = w;
+        }
+      }
+  }
+  workers_sync();
+  if constexpr (SECOND) {
+    griddep_wait();
+    griddep_launch_dependents();
+  }
+
+  const int g = lane >> 2, c4 = lane & 3;
+  constexpr int CODES = W8 ? 16 : 8;       // weights of 16 bytes
+  constexpr int WORDS = CODES / 2;         // of x against them
+  constexpr int M = SECOND ? 1 : 2;
+  uint32_t s = 0, ph = 0;
+  float acc[M][NT][4];
+  bool ok = true;
+  // This warp's share of expert list[a], rows n0..: adds to acc.
+  auto multiply = [&](int a, int n0) {
+    const int e = list[a], first = base[a], tokens = base[a + 1] - first;
+    const uint16_t* from[NT][SECOND ? 2 : 1];  // this lane's column's rows (null: no such token)
+#pragma unroll
+    for (int j = 0; j < NT; ++j) {
+      const int col = 8 * j + g;
+      const int64_t row = col >= tokens ? -1 : SECOND ? first + col : token[first + col];
+      from[j][0] = row < 0 ? nullptr : (SECOND ? p.hi : p.X) + row * p.ldx;
+      if constexpr (SECOND) from[j][1] = row < 0 ? nullptr : p.lo + row * p.ldx;
+    }
+    uint32_t bad[M][2] = {};  // NaN codes in rows g and g + 8
+    for (int c = 0; c < chunks; ++c) {
+      const int k0 = (c * CHUNK + 128 * warp) / (W8 ? 1 : 2);  // this warp's first k
+      const bool mine = warp < slabs_of(c);
+      float sc[M];
+      if constexpr (W8) {
+#pragma unroll
+        for (int m = 0; m < M; ++m)
+          sc[m] = mine && m < p.matrices
+                      ? __ldg(p.S[m] + e * p.stride_s + (n0 / BLOCK) * p.ld_s + (c * CHUNK + 128 * warp) / BLOCK)
+                      : 0.0f;
+      }
+      // the x of one column of tokens: chunks of 16 weight bytes c4 and c4 + 4
+      constexpr int PARTS = SECOND ? 2 : 1;
+      uint4 x[2][PARTS][WORDS / 4];
+      auto load_x = [&](int j, int h) {
+#pragma unroll
+        for (int q = 0; q < PARTS; ++q)
+#pragma unroll
+          for (int v = 0; v < WORDS / 4; ++v) {
+            const int k = k0 + CODES * (c4 + 4 * h);
+            x[j ? 0 : h][q][v] = mine && from[j][q] && k < p.K ? *reinterpret_cast<const uint4*>(from[j][q] + k + 8 * v)
+                                                              : make_uint4(0, 0, 0, 0);
+          }
+      };
+      load_x(0, 0);
+      load_x(0, 1);
+      if (!wait_inline(full_bar(s), ph, wctx, SITE_MMA_FULL)) {
+        ok = false;
+        return;
+      }
+      if (mine) {
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+          uint32_t A[M][CODES / 4][4];  // fragments of this lane's 16-byte chunk of rows g and g + 8
+#pragma unroll
+          for (int m = 0; m < M; ++m) {
+            if (m >= p.matrices) break;
+            const uint32_t slab = sbase + s * stage_bytes + TILE_BYTES * m + SLAB_BYTES * warp;
+#pragma unroll
+            for (int r = 0; r < 2; ++r) {
+              const uint4 v = ld_shared_v4(slab + 128u * (g + 8 * r) + 16u * ((c4 + 4 * h) ^ g));
+              const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+              if constexpr (W8) {
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                  decode4<BF16>(w[i], A[m][i][r], A[m][i][2 + r]);
+                  if constexpr (BF16) bad[m][r] |= nan_codes(w[i]);
+                }
+              } else {
+#pragma unroll
+                for (int i = 0; i < 2; ++i) A[m][i][r] = w[2 * i], A[m][i][2 + r] = w[2 * i + 1];
+              }
+            }
+          }
+#pragma unroll
+          for (int j = 0; j < NT; ++j) {
+            if (8 * j >= tokens) break;
+            if (j > 0) load_x(j, h);
+            float part[M][4] = {};
+#pragma unroll
+            for (int q = 0; q < PARTS; ++q) {
+              const uint32_t* w = reinterpret_cast<const uint32_t*>(&x[j ? 0 : h][q][0]);
+#pragma unroll
+              for (int i = 0; i < CODES / 4; ++i) {
+                // bf16 weights of 8 bits come as values 0, 2 and 1, 3; h lies so already
+                constexpr bool SWAP = BF16 && W8 && !SECOND;
+                const uint32_t b0 = SWAP ? __byte_perm(w[2 * i], w[2 * i + 1], 0x5410) : w[2 * i];
+                const uint32_t b1 = SWAP ? __byte_perm(w[2 * i], w[2 * i + 1], 0x7632) : w[2 * i + 1];
+#pragma unroll
+                for (int m = 0; m < M; ++m)
+                  if (m < p.matrices) mma_16816<BF16>(W8 ? part[m] : acc[m][j], A[m][i], b0, b1);
+              }
+            }
+            if constexpr (W8) {
+#pragma unroll
+              for (int m = 0; m < M; ++m)
+#pragma unroll
+                for (int i = 0; i < 4; ++i) acc[m][j][i] = fmaf(part[m][i], sc[m], acc[m][j][i]);
+            }
+          }
+        }
+      }
+      __syncwarp();
+      if (lane == 0) mbar_arrive(empty_bar(s));
+      if (++s == static_cast<uint32_t>(stages)) {
+        s = 0;
+        ph ^= 1u;
+      }
+    }
+    if constexpr (W8 && BF16) {
+      // a NaN code makes its whole row of products NaN
+#pragma unroll
+      for (int m = 0; m < M; ++m)
+#pragma unroll
+        for (int r = 0; r < 2; ++r) {
+          const bool nan = (bad[m][r] & 0x80808080u) != 0u;
+          const unsigned all = __ballot_sync(0xffffffffu, nan);
+          if (all >> (lane & 28) & 15u)
+#pragma unroll
+            for (int j = 0; j < NT; ++j) acc[m][j][2 * r] = acc[m][j][2 * r + 1] = __uint_as_float(0x7fffffffu);
+        }
+    }
+  };
+  auto clear = [&] {
+#pragma unroll
+    for (int m = 0; m < M; ++m)
+#pragma unroll
+      for (int j = 0; j < NT; ++j)
+#pragma unroll
+        for (int i = 0; i < 4; ++i) acc[m][j][i] = 0.0f;
+  };
+
+  if constexpr (!SECOND) {
+    for (int u = blockIdx.x; u < units; u += gridDim.x) {
+      const int a = u / tiles, n0 = (u % tiles) * 16;
+      const int first = base[a], tokens = base[a + 1] - first;
+      clear();
+      multiply(a, n0);
+      if (!workers_agree(ok)) return;
+#pragma unroll
+      for (int j = 0; j < NT; ++j) {
+        if (8 * j >= tokens) break;
+        // [warp][matrix][column][row]
+#pragma unroll
+        for (int m = 0; m < 2; ++m)
+#pragma unroll
+          for (int i = 0; i < 4; ++i)
+            sums[((warp * 2 + m) * 8 + 2 * c4 + (i & 1)) * 17 + g + 8 * (i >> 1)] = acc[m][j][i];
+        workers_sync();
+        const int row = threadIdx.x & 15, col = threadIdx.x >> 4;
+        if (col < 8 && 8 * j + col < tokens && n0 + row < p.N) {
+          float v[2] = {};
+#pragma unroll
+          for (int w = 0; w < WARPS; ++w)
+#pragma unroll
+            for (int m = 0; m < 2; ++m) v[m] += sums[((w * 2 + m) * 8 + col) * 17 + row];
+          const int pair = first + 8 * j + col;
+          const float silu = v[0] / (1.0f + expf(-v[0]));
+          const float h = (p.matrices > 1 ? silu * v[1] : silu) * weight[pair];
+          const uint16_t hi = round16<BF16>(h);
+          const float rest = h - to_f32<BF16>(hi);
+          int k = n0 + row;
+          if (W8 && BF16) k = (k & ~3) | (k & 1) << 1 | (k >> 1 & 1);  // values 0, 2, 1, 3, as decode4 has the weights
+          p.hi[pair * p.ldh + k] = hi;
+          p.lo[pair * p.ldh + k] = isfinite(rest) ? round16<BF16>(rest) : static_cast<uint16_t>(0);
+        }
+        workers_sync();
+      }
+    }
+  } else {
+    float* mine = sums + warp * p.T * 16;
+    for (int u = blockIdx.x; u < units; u += gridDim.x) {
+      const int n0 = u * 16;
+      for (int i = lane; i < p.T * 16; i += 32) mine[i] = 0.0f;
+      __syncwarp();
+      for (int a = 0; a < chosen && ok; ++a) {
+        const int first = base[a], tokens = base[a + 1] - first;
+        clear();
+        multiply(a, n0);
+#pragma unroll
+        for (int j = 0; j < NT; ++j) {
+          if (8 * j >= tokens) break;
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            const int col = 8 * j + 2 * c4 + (i & 1);
+            if (col < tokens) mine[token[first + col] * 16 + g + 8 * (i >> 1)] += acc[0][j][i];
+          }
+        }
+        __syncwarp();
+      }
+      if (!workers_agree(ok)) return;
+      for (int i = threadIdx.x; i < p.T * 16; i += 32 * WARPS) {
+        const int t = i >> 4, n = n0 + (i & 15);
+        float v = 0.0f;
+#pragma unroll
+        for (int w = 0; w < WARPS; ++w) v += sums[w * p.T * 16 + i];
+        if (n < p.N) {
+          const int64_t to = t * p.ldy + n;
+          if (p.y_type == OUT_F32)
+            static_cast<float*>(p.Y)[to] = v;
+          else
+            static_cast<uint16_t*>(p.Y)[to] = p.y_type == OUT_BF16 ? round16<true>(v) : round16<false>(v);
+        }
+      }
+      workers_sync();
+    }
+  }
+}
+
+// ----------------------------------------------------------------------- host
+
+using Kernel = void (*)(const FewParams);
+constexpr int MAX_SMEM = 232448;
+OncePerDevice<cudaError_t> g_setup;
+
+template <bool BF16, bool W8, bool SECOND>
+Kernel by_tokens(int T) {
+  return T <= 8    ? few_kernel<BF16, W8, 1, SECOND>
+         : T <= 16 ? few_kernel<BF16, W8, 2, SECOND>
+         : T <= 32 ? few_kernel<BF16, W8, 4, SECOND>
+                   : few_kernel<BF16, W8, 8, SECOND>;
+}
+
+template <bool SECOND>
+Kernel pick(bool bf16, bool w8, int T) {
+  if (bf16) return w8 ? by_tokens<true, true, SECOND>(T) : by_tokens<true, false, SECOND>(T);
+  return w8 ? by_tokens<false, true, SECOND>(T) : by_tokens<false, false, SECOND>(T);
+}
+
+cudaError_t setup(int dev) {
+  return g_setup(dev, [] {
+    for (int i = 0; i < 4; ++i)
+      for (int T : {8, 16, 32, 64})
+        for (Kernel k : {pick<false>(i & 1, i & 2, T), pick<true>(i & 1, i & 2, T)}) {
+          const cudaError_t e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, MAX_SMEM);
+          if (e != cudaSuccess) return e;
+        }
+    return cudaSuccess;
+  });
+}
+
+int64_t ceil_div(int64_t a, int64_t b) { return (a + b - 1) / b; }
+bool misaligned(const void* p, unsigned n) { return reinterpret_cast<uintptr_t>(p) % n != 0; }
+
+int launch(Kernel kernel, const FewParams& p, int64_t grid, int smem, cudaStream_t s) {
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(static_cast<unsigned>(grid), 1, 1);
+  cfg.blockDim = dim3(FEW_THREADS, 1, 1);
+  cfg.dynamicSmemBytes = static_cast<size_t>(smem);
+  cfg.stream = s;
+  cudaLaunchAttribute attr;
+  attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr.val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = &attr;
+  cfg.numAttrs = 1;
+  return record_cuda(cudaLaunchKernelEx(&cfg, kernel, p));
+}
+
+// Maps of one matrix of each expert: `rows` rows of `bytes`, `ld` bytes apart.
+int weight_maps(FewParams* p, int i, const void* W, int64_t bytes, int64_t rows, int64_t ld, int64_t stride) {
+  if (bytes >= 128)
+    if (int rc = make_slab_map(&p->slab[i], W, 128, rows, bytes / 128, p->E, ld, stride, 16, WARPS)) return rc;
+  return make_byte_map(&p->edge[i], W, bytes, rows, p->E, ld, stride, 128, 16);
+}
+
+// Weights [E][rows][length] of `size` bytes: whole 16-byte words
+int check_weights(const void* W, int64_t rows, int64_t length, int size, int64_t* ld, int64_t* stride) {
+  if (*ld == 0) *ld = length;
+  if (*stride == 0) *stride = rows * *ld;
+  if (!W || *ld < length || *stride < 0) return TCG_ERR_INVALID;
+  return misaligned(W, 16) || *ld * size % 16 || *stride * size % 16 || length * size % 16 ? TCG_ERR_ALIGNMENT : TCG_OK;
+}
+
+int check_scales(const float* S, int64_t rows, int64_t length, int64_t* ld, int64_t* stride) {
+  if (*ld == 0) *ld = ceil_div(length, BLOCK);
+  if (*stride == 0) *stride = ceil_div(rows, BLOCK) * *ld;
+  if (!S || *ld < ceil_div(length, BLOCK) || *stride < 0) return TCG_ERR_INVALID;
+  return misaligned(S, 4) ? TCG_ERR_ALIGNMENT : TCG_OK;
+}
+
+int64_t work_bytes(int64_t T, int topk, int64_t I) {
+  if (T < 0 || T > MAX_TOKENS || topk < 1 || topk > MAX_TOPK || I < 0 || I >= MAX_EXTENT) return -1;
+  return 4 * T * topk * I;
+}
+
+int run_few(const tcg_moe_few_args* args, cudaStream_t s) {
+  begin_product();
+  if (!args) return TCG_ERR_INVALID;
+  tcg_moe_few_args a = *args;
+  if (a.x_type != TCG_IN_F16 && a.x_type != TCG_IN_BF16) return TCG_ERR_INVALID;
+  if (a.w_type != a.x_type && a.w_type != TCG_IN_E4M3) return TCG_ERR_INVALID;
+  if (a.T < 0 || a.H < 0 || a.I < 0 || a.topk < 1 || a.E < 1 || a.y_type < TCG_F32 || a.y_type > TCG_BF16)
+    return TCG_ERR_INVALID;
+  if (a.T > MAX_TOKENS || a.topk > MAX_TOPK || a.E > MAX_EXPERTS || a.H >= MAX_EXTENT || a.I >= MAX_EXTENT)
+    return TCG_ERR_UNSUPPORTED;
+  if (a.T == 0 || a.H == 0) return TCG_OK;
+  const bool w8 = a.w_type == TCG_IN_E4M3;
+  const int size = w8 ? 1 : 2;
+  if (a.ldy == 0) a.ldy = a.H;
+  if (!a.Y || a.ldy < a.H || !a.expert) return TCG_ERR_INVALID;
+  if (misaligned(a.Y, a.y_type == TCG_F32 ? 4 : 2) || misaligned(a.expert, 4) || misaligned(a.weight, 4))
+    return TCG_ERR_ALIGNMENT;
+  if (a.I > 0) {
+    if (a.ldx == 0) a.ldx = a.H;
+    if (!a.X || a.ldx < a.H || !a.work) return TCG_ERR_INVALID;
+    if (misaligned(a.X, 16) || a.ldx % 8 || misaligned(a.work, 16)) return TCG_ERR_ALIGNMENT;
+    int64_t ld = a.ld1, stride = a.stride1;
+    if (int rc = check_weights(a.W1, a.I, a.H, size, &ld, &stride)) return rc;
+    if (a.W3 && misaligned(a.W3, 16)) return TCG_ERR_ALIGNMENT;
+    a.ld1 = ld, a.stride1 = stride;
+    if (int rc = check_weights(a.W2, a.H, a.I, size, &a.ld2, &a.stride2)) return rc;
+    if (w8) {
+      if (int rc = check_scales(a.S1, a.I, a.H, &a.ld_s1, &a.stride_s1)) return rc;
+      if (a.W3 && !a.S3) return TCG_ERR_INVALID;
+      if (misaligned(a.S3, 4)) return TCG_ERR_ALIGNMENT;
+      if (int rc = check_scales(a.S2, a.H, a.I, &a.ld_s2, &a.stride_s2)) return rc;
+    }
+  }
+  int dev;
+  if (int rc = current_device_checked(&dev)) return rc;
+  if (int rc = record_cuda(setup(dev))) return rc;
+  const bool bf16 = a.x_type == TCG_IN_BF16;
+  const int T = static_cast<int>(a.T), sms = device_sms(dev);
+  const int64_t pairs = a.T * a.topk;
+  FewParams p;
+  std::memset(&p, 0, sizeof p);
+  p.expert = a.expert;
+  p.weight = a.weight;
+  p.T = T;
+  p.topk = a.topk;
+  p.E = a.E;
+  p.hi = static_cast<uint16_t*>(a.work);
+  p.lo = p.hi + pairs * a.I;
+  p.ldh = a.I;
+  p.err = device_error_word(dev);
+  p.timeout_ns = wait_timeout_ns();
+  FewParams q = p;
+  int launches = 0;
+  if (a.I > 0) {
+    p.K = static_cast<int>(a.H);
+    p.N = static_cast<int>(a.I);
+    p.row_bytes = p.K * size;
+    p.matrices = a.W3 ? 2 : 1;
+    if (int rc = weight_maps(&p, 0, a.W1, p.row_bytes, a.I, a.ld1 * size, a.stride1 * size)) return rc;
+    if (a.W3)
+      if (int rc = weight_maps(&p, 1, a.W3, p.row_bytes, a.I, a.ld1 * size, a.stride1 * size)) return rc;
+    p.X = static_cast<const uint16_t*>(a.X);
+    p.ldx = a.ldx;
+    p.S[0] = a.S1;
+    p.S[1] = a.S3;
+    p.ld_s = a.ld_s1;
+    p.stride_s = a.stride_s1;
+    if (int rc = weight_maps(&q, 0, a.W2, a.I * size, a.H, a.ld2 * size, a.stride2 * size)) return rc;
+    const int64_t units = std::min<int64_t>(a.E, pairs) * ceil_div(a.I, 16);
+    if (units > INT32_MAX) return TCG_ERR_UNSUPPORTED;
+    if (int rc = launch(pick<false>(bf16, w8, T), p, std::min<int64_t>(units, sms), Layout(T, a.topk, a.E, false).bytes, s))
+      return rc;
+    ++launches;
+  }
+  q.K = static_cast<int>(a.I);
+  q.N = static_cast<int>(a.H);
+  q.row_bytes = q.K * size;
+  q.matrices = 1;
+  q.ldx = q.ldh;
+  q.S[0] = a.S2;
+  q.ld_s = a.ld_s2;
+  q.stride_s = a.stride_s2;
+  q.Y = a.Y;
+  q.ldy = a.ldy;
+  q.y_type = a.y_type;
+  if (int rc = launch(pick<true>(bf16, w8, T), q, std::min<int64_t>(ceil_div(a.H, 16), sms),
+                      Layout(T, a.topk, a.E, true).bytes, s))
+    return rc;
+  set_launch_count(launches + 1);
+  return TCG_OK;
+}
+
+}  // namespace
+
+}  // namespace tcg
+
+using namespace tcg;
+
+extern "C" {
+
+int64_t tcg_moe_few_work_bytes(int64_t T, int topk, int64_t I) { return work_bytes(T, topk, I); }
+
+int tcg_moe_few(const tcg_moe_few_args* args, void* stream) {
+  return guarded([&] { return run_few(args, static_cast<cudaStream_t>(stream)); });
+}
+
+}  // extern "C"

@@ -460,6 +460,38 @@ int tcg_gemm_f8_grouped_wgrad(tcg_input in_type, int64_t R, int64_t N, int64_t K
                               int64_t ld_sa, const int32_t* offsets, void* DW, tcg_dtype dw_type, int64_t lddw,
                               int64_t stride_dw, void* stream);
 
+/* A whole mixture-of-experts layer for T <= 64 tokens, in two kernels:
+ *     Y[t] = sum_j weight[t][j] * W2[e] (silu(W1[e] X[t]) * (W3[e] X[t])),  e = expert[t][j] in [0, E)
+ * (without W3: W2[e] silu(W1[e] X[t])).  Choices outside [0, E) are dropped; a
+ * token without kept choices gets zeros; a token that names an expert twice
+ * gets it with both weights.  Products are summed in fp32; the weighted
+ * activations are kept as two values of x_type (beyond f16's range infinite, as
+ * f16 activations are), Y is rounded once.  Every chosen expert's matrices are
+ * read once.  E4M3 weights keep all bits of X.  Results do not depend on
+ * timing. */
+typedef struct {
+  tcg_input x_type;      /* X: TCG_IN_F16 or TCG_IN_BF16 */
+  tcg_input w_type;      /* weights: x_type, or TCG_IN_E4M3 with fp32 scales for each 128 x 128 */
+  int64_t T, H, I;       /* H, I: whole 16-byte words of weights; T <= 64 */
+  int topk, E;           /* topk <= 64, E <= 1024 */
+  const void* X; int64_t ldx;              /* [T][H], 16-byte aligned base and rows */
+  const int32_t* expert;                   /* [T][topk] */
+  const float* weight;                     /* [T][topk], or NULL: 1 */
+  const void *W1, *W3;                     /* [E][I][H], 16-byte aligned base and rows; W3 or NULL */
+  int64_t ld1, stride1;                    /* of both, elements between rows / experts (0 = packed) */
+  const void* W2; int64_t ld2, stride2;    /* [E][H][I] */
+  const float *S1, *S3; int64_t ld_s1, stride_s1;  /* E4M3: [E][ceil(I/128)][ceil(H/128)] (0 = packed) */
+  const float* S2; int64_t ld_s2, stride_s2;       /* E4M3: [E][ceil(H/128)][ceil(I/128)] */
+  void* work;                              /* tcg_moe_few_work_bytes, 16-byte aligned; calls that may run
+                                              at the same time (graphs among them) need one each */
+  void* Y; tcg_dtype y_type; int64_t ldy;  /* [T][H], element aligned; must not overlap X */
+} tcg_moe_few_args;
+
+/* Bytes of args.work; -1 for sizes that tcg_moe_few does not take. */
+int64_t tcg_moe_few_work_bytes(int64_t T, int topk, int64_t I);
+
+int tcg_moe_few(const tcg_moe_few_args* args, void* stream);
+
 /* ---------------------------------------------------------------------------
  * Block-scale layout (the scale-factor rearrangement step).
  *

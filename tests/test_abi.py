@@ -452,3 +452,45 @@ def test_gemm_f8_validation_before_any_device_work(tcg):
     assert wgrad(N=60) == tcg.ERR_ALIGNMENT
     assert wgrad(DW=0x50002) == tcg.ERR_ALIGNMENT
     assert wgrad(N=0, DY=None, SDY=None, A=None, SA=None, off=None, DW=None) == tcg.OK
+
+
+def test_moe_few_validation_before_any_device_work(tcg):
+    def call(**kw):
+        a = dict(x_type=1, w_type=3, T=4, H=64, I=64, topk=2, E=8, X=0x10000, ldx=0, expert=0x20000, weight=0x30000,
+                 W1=0x40000, W3=0x50000, W2=0x60000, work=0x70000, Y=0x80000, y_type=2, ldy=0, s1=0x90000, s3=0xa0000,
+                 s2=0xb0000, stream=0, check=False)
+        a.update(kw)
+        return tcg.moe_few(**a)
+    assert tcg.raw_call("tcg_moe_few", None, None) == tcg.ERR_INVALID
+    assert call(x_type=3) == tcg.ERR_INVALID
+    assert call(w_type=0) == tcg.ERR_INVALID                 # 16-bit weights have x's type
+    assert call(w_type=4) == tcg.ERR_INVALID
+    assert call(y_type=3) == tcg.ERR_INVALID
+    for n in ("T", "H", "I"):
+        assert call(**{n: -1}) == tcg.ERR_INVALID
+    assert call(topk=0) == tcg.ERR_INVALID
+    assert call(E=0) == tcg.ERR_INVALID
+    assert call(T=65) == tcg.ERR_UNSUPPORTED
+    assert call(topk=65) == tcg.ERR_UNSUPPORTED
+    assert call(E=1025) == tcg.ERR_UNSUPPORTED
+    assert call(H=1 << 30) == tcg.ERR_UNSUPPORTED
+    for p in ("X", "expert", "W1", "W2", "work", "Y", "s1", "s3", "s2"):
+        assert call(**{p: None}) == tcg.ERR_INVALID, p
+    assert call(ldx=56) == tcg.ERR_INVALID
+    assert call(ldy=63) == tcg.ERR_INVALID
+    assert call(ld1=48) == tcg.ERR_INVALID
+    assert call(stride1=-16) == tcg.ERR_INVALID
+    assert call(H=256, ld_s1=1) == tcg.ERR_INVALID
+    assert call(ldx=68) == tcg.ERR_ALIGNMENT
+    assert call(H=72) == tcg.ERR_ALIGNMENT                    # 8-bit rows of whole 16-byte words
+    assert call(I=72) == tcg.ERR_ALIGNMENT
+    assert call(x_type=1, w_type=1, H=68) == tcg.ERR_ALIGNMENT
+    for p in ("X", "W1", "W3", "W2", "work"):
+        assert call(**{p: 0x10008}) == tcg.ERR_ALIGNMENT, p
+    for p in ("expert", "weight", "s1", "s3", "s2"):
+        assert call(**{p: 0x10002}) == tcg.ERR_ALIGNMENT, p
+    assert call(Y=0x80001) == tcg.ERR_ALIGNMENT
+    assert call(T=0, X=None, expert=None, W1=None, W2=None, work=None, Y=None) == tcg.OK
+    assert tcg.moe_few_work_bytes(4, 2, 64) == 4 * 4 * 2 * 64
+    assert tcg.moe_few_work_bytes(0, 2, 64) == 0
+    assert tcg.moe_few_work_bytes(65, 2, 64) == -1
