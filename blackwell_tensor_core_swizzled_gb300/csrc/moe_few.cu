@@ -68,6 +68,7 @@ struct FewParams {
   int64_t ldx;
   uint16_t *hi, *lo;  // [pairs][ldh]
   int64_t ldh;
+  int64_t lo_at;  // lo - hi
   const float* S[2];  // 8-bit weights' scales of 128 x 128
   int64_t ld_s, stride_s;
   void* Y;
@@ -115,26 +116,21 @@ __device__ __forceinline__ void mma_16816(float (&d)[4], const uint32_t (&a)[4],
         : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
 }
 
-// Four E4M3 codes as two pairs of 16-bit values.  f16: values 0, 1 and 2, 3 by
-// conversion.  bf16, which has none: values 0, 2 and 1, 3; a code's seven lower
-// bits are a bf16's lower exponent bits and upper significand at a scale of
-// 2^-120 (subnormals included), which an exact multiplication takes out.
+// Four E4M3 codes as two pairs of 16-bit values, by conversion to f16; bf16 has
+// none from E4M3, so values go on through fp32, whose upper halves they fit.
+// (Shifting the codes' bits into place took 12 instructions, with the test for
+// NaN that it needs, where this takes 8.)
 template <bool BF16>
 __device__ __forceinline__ void decode4(uint32_t w, uint32_t& p, uint32_t& q) {
+  asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(p) : "h"(static_cast<uint16_t>(w)));
+  asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(q) : "h"(static_cast<uint16_t>(w >> 16)));
   if constexpr (BF16) {
-    const uint32_t even = (w << 8 & 0x80008000u) | (w << 4 & 0x07f007f0u);
-    const uint32_t odd = (w & 0x80008000u) | (w >> 4 & 0x07f007f0u);
-    constexpr uint32_t SCALE = 0x7b807b80u;  // 2^120 twice
-    asm("mul.rn.bf16x2 %0, %1, %2;" : "=r"(p) : "r"(even), "r"(SCALE));
-    asm("mul.rn.bf16x2 %0, %1, %2;" : "=r"(q) : "r"(odd), "r"(SCALE));
-  } else {
-    asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(p) : "h"(static_cast<uint16_t>(w)));
-    asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(q) : "h"(static_cast<uint16_t>(w >> 16)));
+    const float2 a = __half22float2(*reinterpret_cast<const __half2*>(&p));
+    const float2 b = __half22float2(*reinterpret_cast<const __half2*>(&q));
+    p = __byte_perm(__float_as_uint(a.x), __float_as_uint(a.y), 0x7632);
+    q = __byte_perm(__float_as_uint(b.x), __float_as_uint(b.y), 0x7632);
   }
 }
-
-// bit 7 of a byte: that code is a NaN (the bf16 decoding makes it 480)
-__device__ __forceinline__ uint32_t nan_codes(uint32_t w) { return (w & 0x7f7f7f7fu) + 0x01010101u; }
 
 __device__ __forceinline__ uint4 ld_shared_v4(uint32_t addr) {
   uint4 v;
@@ -344,47 +340,64 @@ __global__ void __launch_bounds__(FEW_THREADS, NT <= 2 ? 2 : 1) few_kernel(const
   }
 
   const int g = lane >> 2, c4 = lane & 3;
-  constexpr int CODES = W8 ? 16 : 8;       // weights of 16 bytes
+  constexpr int SIZE = W8 ? 1 : 2;
+  constexpr int CODES = 16 / SIZE;         // weights of 16 bytes
   constexpr int WORDS = CODES / 2;         // of x against them
   constexpr int M = SECOND ? 1 : 2;
+  // few tokens: columns are tokens, whatever the expert, so that W2's sums stay in place
+  constexpr bool DIRECT = SECOND && NT == 1;
   uint32_t s = 0, ph = 0;
   float acc[M][NT][4];
   bool ok = true;
   // This warp's share of expert list[a], rows n0..: adds to acc.
   auto multiply = [&](int a, int n0) {
-    const int e = list[a], first = base[a], tokens = base[a + 1] - first;
-    const uint16_t* from[NT][SECOND ? 2 : 1];  // this lane's column's rows (null: no such token)
+    const int e = list[a], first = base[a], tokens = DIRECT ? 8 : base[a + 1] - first;
+    constexpr int PARTS = SECOND ? 2 : 1;
+    // this lane's column's rows, from its own k on (null: no such token)
+    const int k_lane = warp * (CHUNK / WARPS / SIZE) + CODES * c4;
+    const uint16_t* from[NT][PARTS];
 #pragma unroll
     for (int j = 0; j < NT; ++j) {
       const int col = 8 * j + g;
-      const int64_t row = col >= tokens ? -1 : SECOND ? first + col : token[first + col];
-      from[j][0] = row < 0 ? nullptr : (SECOND ? p.hi : p.X) + row * p.ldx;
-      if constexpr (SECOND) from[j][1] = row < 0 ? nullptr : p.lo + row * p.ldx;
+      bool exists = col < tokens;
+      int row = 0;
+      if constexpr (DIRECT) {
+        const uint32_t mask = static_cast<uint32_t>(masks[e]);
+        exists = mask >> g & 1;
+        row = first + __popc(mask & ((1u << g) - 1u));
+      } else if (exists) {
+        row = SECOND ? first + col : token[first + col];
+      }
+      const uint16_t* at = (SECOND ? p.hi : p.X) + row * p.ldx + k_lane;
+      from[j][0] = exists ? at : nullptr;
+      if constexpr (SECOND) from[j][1] = at + p.lo_at;
     }
-    uint32_t bad[M][2] = {};  // NaN codes in rows g and g + 8
-    for (int c = 0; c < chunks; ++c) {
-      const int k0 = (c * CHUNK + 128 * warp) / (W8 ? 1 : 2);  // this warp's first k
-      const bool mine = warp < slabs_of(c);
+    // DIRECT: which of this lane's sums (columns 2 c4, + 1) belong to the expert's
+    // tokens; in the others its weights, NaN perhaps, met zeros
+    const uint32_t columns = DIRECT ? 5u * (static_cast<uint32_t>(masks[e]) >> (2 * c4) & 3u) : 15u;
+    const float* scale[M];
+#pragma unroll
+    for (int m = 0; m < M; ++m)
+      if constexpr (W8) scale[m] = p.S[m] + e * p.stride_s + (n0 / BLOCK) * p.ld_s + warp;
+    int left = p.K - k_lane;                  // k from this lane's first on
+    int bytes = p.row_bytes - 128 * warp;     // of the rows, from this warp's slab on
+    for (int c = 0; c < chunks; ++c, left -= CHUNK / SIZE, bytes -= CHUNK) {
+      const bool mine = bytes > 0;
       float sc[M];
       if constexpr (W8) {
 #pragma unroll
-        for (int m = 0; m < M; ++m)
-          sc[m] = mine && m < p.matrices
-                      ? __ldg(p.S[m] + e * p.stride_s + (n0 / BLOCK) * p.ld_s + (c * CHUNK + 128 * warp) / BLOCK)
-                      : 0.0f;
+        for (int m = 0; m < M; ++m) sc[m] = mine && m < p.matrices ? __ldg(scale[m] + c * WARPS) : 0.0f;
       }
       // the x of one column of tokens: chunks of 16 weight bytes c4 and c4 + 4
-      constexpr int PARTS = SECOND ? 2 : 1;
       uint4 x[2][PARTS][WORDS / 4];
       auto load_x = [&](int j, int h) {
 #pragma unroll
         for (int q = 0; q < PARTS; ++q)
 #pragma unroll
-          for (int v = 0; v < WORDS / 4; ++v) {
-            const int k = k0 + CODES * (c4 + 4 * h);
-            x[j ? 0 : h][q][v] = mine && from[j][q] && k < p.K ? *reinterpret_cast<const uint4*>(from[j][q] + k + 8 * v)
-                                                              : make_uint4(0, 0, 0, 0);
-          }
+          for (int v = 0; v < WORDS / 4; ++v)
+            x[j ? 0 : h][q][v] = from[j][0] && 4 * CODES * h < left
+                                     ? *reinterpret_cast<const uint4*>(from[j][q] + c * (CHUNK / SIZE) + 4 * CODES * h + 8 * v)
+                                     : make_uint4(0, 0, 0, 0);
       };
       load_x(0, 0);
       load_x(0, 1);
@@ -408,7 +421,6 @@ __global__ void __launch_bounds__(FEW_THREADS, NT <= 2 ? 2 : 1) few_kernel(const
 #pragma unroll
                 for (int i = 0; i < 4; ++i) {
                   decode4<BF16>(w[i], A[m][i][r], A[m][i][2 + r]);
-                  if constexpr (BF16) bad[m][r] |= nan_codes(w[i]);
                 }
               } else {
 #pragma unroll
@@ -426,20 +438,17 @@ __global__ void __launch_bounds__(FEW_THREADS, NT <= 2 ? 2 : 1) few_kernel(const
               const uint32_t* w = reinterpret_cast<const uint32_t*>(&x[j ? 0 : h][q][0]);
 #pragma unroll
               for (int i = 0; i < CODES / 4; ++i) {
-                // bf16 weights of 8 bits come as values 0, 2 and 1, 3; h lies so already
-                constexpr bool SWAP = BF16 && W8 && !SECOND;
-                const uint32_t b0 = SWAP ? __byte_perm(w[2 * i], w[2 * i + 1], 0x5410) : w[2 * i];
-                const uint32_t b1 = SWAP ? __byte_perm(w[2 * i], w[2 * i + 1], 0x7632) : w[2 * i + 1];
 #pragma unroll
                 for (int m = 0; m < M; ++m)
-                  if (m < p.matrices) mma_16816<BF16>(W8 ? part[m] : acc[m][j], A[m][i], b0, b1);
+                  if (m < p.matrices) mma_16816<BF16>(W8 || DIRECT ? part[m] : acc[m][j], A[m][i], w[2 * i], w[2 * i + 1]);
               }
             }
-            if constexpr (W8) {
+            if constexpr (W8 || DIRECT) {
 #pragma unroll
               for (int m = 0; m < M; ++m)
 #pragma unroll
-                for (int i = 0; i < 4; ++i) acc[m][j][i] = fmaf(part[m][i], sc[m], acc[m][j][i]);
+                for (int i = 0; i < 4; ++i)
+                  if (!DIRECT || (columns >> i & 1)) acc[m][j][i] = W8 ? fmaf(part[m][i], sc[m], acc[m][j][i]) : acc[m][j][i] + part[m][i];
             }
           }
         }
@@ -450,19 +459,6 @@ __global__ void __launch_bounds__(FEW_THREADS, NT <= 2 ? 2 : 1) few_kernel(const
         s = 0;
         ph ^= 1u;
       }
-    }
-    if constexpr (W8 && BF16) {
-      // a NaN code makes its whole row of products NaN
-#pragma unroll
-      for (int m = 0; m < M; ++m)
-#pragma unroll
-        for (int r = 0; r < 2; ++r) {
-          const bool nan = (bad[m][r] & 0x80808080u) != 0u;
-          const unsigned all = __ballot_sync(0xffffffffu, nan);
-          if (all >> (lane & 28) & 15u)
-#pragma unroll
-            for (int j = 0; j < NT; ++j) acc[m][j][2 * r] = acc[m][j][2 * r + 1] = __uint_as_float(0x7fffffffu);
-        }
     }
   };
   auto clear = [&] {
@@ -503,10 +499,9 @@ __global__ void __launch_bounds__(FEW_THREADS, NT <= 2 ? 2 : 1) few_kernel(const
           const float h = (p.matrices > 1 ? silu * v[1] : silu) * weight[pair];
           const uint16_t hi = round16<BF16>(h);
           const float rest = h - to_f32<BF16>(hi);
-          int k = n0 + row;
-          if (W8 && BF16) k = (k & ~3) | (k & 1) << 1 | (k >> 1 & 1);  // values 0, 2, 1, 3, as decode4 has the weights
-          p.hi[pair * p.ldh + k] = hi;
-          p.lo[pair * p.ldh + k] = isfinite(rest) ? round16<BF16>(rest) : static_cast<uint16_t>(0);
+          const int64_t to = pair * p.ldh + n0 + row;
+          p.hi[to] = hi;
+          p.lo[to] = isfinite(rest) ? round16<BF16>(rest) : static_cast<uint16_t>(0);
         }
         workers_sync();
       }
@@ -515,9 +510,19 @@ __global__ void __launch_bounds__(FEW_THREADS, NT <= 2 ? 2 : 1) few_kernel(const
     float* mine = sums + warp * p.T * 16;
     for (int u = blockIdx.x; u < units; u += gridDim.x) {
       const int n0 = u * 16;
-      for (int i = lane; i < p.T * 16; i += 32) mine[i] = 0.0f;
-      __syncwarp();
-      for (int a = 0; a < chosen && ok; ++a) {
+      if constexpr (DIRECT) {
+        clear();
+        for (int a = 0; a < chosen && ok; ++a) multiply(a, n0);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const int t = 2 * c4 + (i & 1);
+          if (t < p.T) mine[t * 16 + g + 8 * (i >> 1)] = acc[0][0][i];
+        }
+      } else {
+        for (int i = lane; i < p.T * 16; i += 32) mine[i] = 0.0f;
+        __syncwarp();
+      }
+      for (int a = 0; a < chosen && ok && !DIRECT; ++a) {
         const int first = base[a], tokens = base[a + 1] - first;
         clear();
         multiply(a, n0);
@@ -676,6 +681,7 @@ int run_few(const tcg_moe_few_args* args, cudaStream_t s) {
   p.hi = static_cast<uint16_t*>(a.work);
   p.lo = p.hi + pairs * a.I;
   p.ldh = a.I;
+  p.lo_at = pairs * a.I;
   p.err = device_error_word(dev);
   p.timeout_ns = wait_timeout_ns();
   FewParams q = p;
