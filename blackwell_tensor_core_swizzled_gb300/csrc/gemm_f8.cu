@@ -108,15 +108,6 @@ __device__ __forceinline__ void mma_f8(uint32_t d, uint64_t a, uint64_t b, uint3
         : "memory");
 }
 
-// A 4-byte copy global -> shared in flight (zero if !exists), and this lane's
-// arrival on `bar` (one of 32) once its copies so far have landed.
-__device__ __forceinline__ void copy_f32(uint32_t to, const float* from, bool exists) {
-  asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"(to), "l"(from), "r"(exists ? 4 : 0) : "memory");
-}
-__device__ __forceinline__ void copies_arrive(uint32_t bar) {
-  asm volatile("cp.async.mbarrier.arrive.noinc.shared.b64 [%0];" ::"r"(bar) : "memory");
-}
-
 template <bool MORE, int N>
 __device__ __forceinline__ void set_registers() {
   if constexpr (MORE)

@@ -48,12 +48,13 @@ constexpr int MAX_TOKENS = 64;
 constexpr int MAX_TOPK = 64;
 constexpr int MAX_EXPERTS = 1024;
 constexpr int64_t MAX_EXTENT = int64_t{1} << 30;
-constexpr int WARPS = 8;                    // that multiply; one more brings the weights
-constexpr int FEW_THREADS = 32 * (WARPS + 1);
+constexpr int WARPS = 8;                    // that multiply; two more bring weights, and x and scales
+constexpr int FEW_THREADS = 32 * (WARPS + 2);
 constexpr int SLAB_BYTES = 16 * 128;
 constexpr int CHUNK = 128 * WARPS;          // bytes of a row in a stage
 constexpr int TILE_BYTES = SLAB_BYTES * WARPS;
-constexpr int RING_BYTES = 6 * TILE_BYTES;  // as stages of one matrix or two
+constexpr int MAX_STAGES = 6;
+constexpr int MAX_SMEM = 232448;
 
 struct FewParams {
   CUtensorMap slab[2];  // [E][128-byte slabs][rows][128]: W1 and W3, or W2
@@ -63,7 +64,7 @@ struct FewParams {
   int T, topk, E;
   int K, N;        // length of the weights' rows, and their number
   int row_bytes;
-  int matrices;
+  int matrices, stages;
   const uint16_t* X;  // [T][K]; second kernel: hi [pairs][K]
   int64_t ldx;
   uint16_t *hi, *lo;  // [pairs][ldh]
@@ -78,24 +79,32 @@ struct FewParams {
   uint64_t timeout_ns;
 };
 
-// Shared memory behind the ring, from the sizes.
+// Shared memory from the sizes: ring stages of weights, then of x and scales,
+// then lists.
 struct Layout {
-  int sums, masks, list, base, token, weight, bars, bytes;
-  __host__ __device__ Layout(int T, int topk, int E, bool second) {
+  int stage;               // bytes of a stage's weights
+  int x_row, x_part, x_stage;  // of x: a column, hi or lo of all columns, a stage with its scales
+  int x, sums, masks, list, base, token, weight, bars, bytes;
+  __host__ __device__ Layout(int T, int topk, int E, bool second, int size, int matrices, int stages) {
     const int pairs = T * topk, most = pairs < E ? pairs : E;
-    int at = RING_BYTES;
+    stage = TILE_BYTES * matrices;
+    x_row = CHUNK / size * 2 + (size == 1 ? 16 : 64);  // so that a quarter warp's words lie in different banks
+    x_part = x_row * (T < 8 ? T : 8);
+    x_stage = x_part * (second ? 2 : 1) + 2 * WARPS * 4;
+    int at = stages * stage;
     auto take = [&](int n) {
       const int here = at;
       at += (n + 15) / 16 * 16;
       return here;
     };
+    x = take(stages * x_stage);
     sums = take(second ? WARPS * T * 16 * 4 : WARPS * 2 * 8 * 17 * 4);
     masks = take(8 * E);
     list = take(4 * most);
     base = take(4 * (most + 1));
     token = take(pairs);
     weight = take(second ? 0 : 4 * pairs);
-    bars = take(2 * 6 * 8 + 8 * 4 + 16);
+    bars = take(2 * MAX_STAGES * 8 + 8 * 4 + 16);
     bytes = at + 1024;  // the ring starts on a swizzle period
   }
 };
@@ -154,6 +163,19 @@ __device__ __forceinline__ uint16_t round16(float v) {
     return __half_as_ushort(__float2half_rn(v));
 }
 
+__device__ __forceinline__ float ld_shared_f32(uint32_t addr) {
+  float v;
+  asm volatile("ld.shared.f32 %0, [%1];" : "=f"(v) : "r"(addr));
+  return v;
+}
+
+// Copies global -> shared in flight (zeros if !exists).
+__device__ __forceinline__ void copy_16(uint32_t to, const void* from, bool exists) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(to), "l"(from), "r"(exists ? 16 : 0) : "memory");
+}
+
+// all but the producer of weights
+__device__ __forceinline__ void consumers_sync() { asm volatile("bar.sync 2, %0;" ::"n"(32 * (WARPS + 1)) : "memory"); }
 __device__ __forceinline__ void workers_sync() { asm volatile("bar.sync 1, %0;" ::"n"(32 * WARPS) : "memory"); }
 
 // The same; true if all are.
@@ -172,13 +194,13 @@ __device__ __forceinline__ bool workers_agree(bool ok) {
 // NT: 8-token columns.  W8: weights are E4M3 with scales, else of x's type.
 // SECOND: W2 and the sum over experts, else W1, W3 and the activation.
 template <bool BF16, bool W8, int NT, bool SECOND>
-__global__ void __launch_bounds__(FEW_THREADS, NT <= 2 ? 2 : 1) few_kernel(const __grid_constant__ FewParams p) {
+__global__ void __launch_bounds__(FEW_THREADS, NT == 1 ? 2 : 1) few_kernel(const __grid_constant__ FewParams p) {
   extern __shared__ uint8_t smem_raw[];
   const uint32_t raw = smem_u32(smem_raw);
   const uint32_t sbase = (raw + 1023u) & ~1023u;
   uint8_t* gbase = smem_raw + (sbase - raw);
-  const Layout at(p.T, p.topk, p.E, SECOND);
-  const int stage_bytes = TILE_BYTES * p.matrices, stages = RING_BYTES / stage_bytes;
+  const Layout at(p.T, p.topk, p.E, SECOND, W8 ? 1 : 2, p.matrices, p.stages);
+  const int stage_bytes = at.stage, stages = p.stages;
   unsigned long long* masks = reinterpret_cast<unsigned long long*>(gbase + at.masks);
   int* list = reinterpret_cast<int*>(gbase + at.list);   // the chosen experts
   int* base = reinterpret_cast<int*>(gbase + at.base);   // their first pair
@@ -187,9 +209,9 @@ __global__ void __launch_bounds__(FEW_THREADS, NT <= 2 ? 2 : 1) few_kernel(const
   float* sums = reinterpret_cast<float*>(gbase + at.sums);
   const uint32_t bar0 = sbase + at.bars;
   auto full_bar = [&](uint32_t s) { return bar0 + 8u * s; };
-  auto empty_bar = [&](uint32_t s) { return bar0 + 8u * (6 + s); };
-  int* counts = reinterpret_cast<int*>(gbase + at.bars + 96);  // of eight ranges of experts
-  volatile uint32_t* abort_flag = reinterpret_cast<uint32_t*>(gbase + at.bars + 96 + 32);
+  auto empty_bar = [&](uint32_t s) { return bar0 + 8u * (MAX_STAGES + s); };
+  int* counts = reinterpret_cast<int*>(gbase + at.bars + 16 * MAX_STAGES);  // of eight ranges of experts
+  volatile uint32_t* abort_flag = reinterpret_cast<uint32_t*>(gbase + at.bars + 16 * MAX_STAGES + 32);
   const WaitCtx wctx{p.timeout_ns, p.err, abort_flag};
 
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -200,7 +222,7 @@ __global__ void __launch_bounds__(FEW_THREADS, NT <= 2 ? 2 : 1) few_kernel(const
       prefetch_tmap(&p.edge[i]);
     }
     for (int s = 0; s < stages; ++s) {
-      mbar_init(full_bar(s), 1);
+      mbar_init(full_bar(s), 1 + 32);  // the weights' bytes, the lanes' copies of x and scales
       mbar_init(empty_bar(s), WARPS);
     }
     *abort_flag = 0u;
@@ -255,7 +277,7 @@ __global__ void __launch_bounds__(FEW_THREADS, NT <= 2 ? 2 : 1) few_kernel(const
   auto slabs_of = [&](int c) { return min(WARPS, (p.row_bytes - c * CHUNK + 127) / 128); };
 
   if (warp == WARPS) {
-    // ------------------------------------------------------------- producer
+    // --------------------------------------------------- producer of weights
     uint32_t s = 0, ph = 0, sent = 0;
     bool ok = true;
     for (int u = blockIdx.x; u < units && ok; u += gridDim.x) {
@@ -302,7 +324,7 @@ __global__ void __launch_bounds__(FEW_THREADS, NT <= 2 ? 2 : 1) few_kernel(const
     return;
   }
 
-  // ----------------------------------------------------------------- workers
+
   // the pairs: experts in the list's order, their tokens rising
   if (warp == 0) {
     int run = 0;
@@ -318,8 +340,8 @@ __global__ void __launch_bounds__(FEW_THREADS, NT <= 2 ? 2 : 1) few_kernel(const
     }
     if (lane == 0) base[chosen] = run;
   }
-  workers_sync();
-  for (int a = warp; a < chosen; a += WARPS) {
+  consumers_sync();
+  for (int a = warp < WARPS ? warp : chosen; a < chosen; a += WARPS) {
     const unsigned long long mask = masks[list[a]];
     for (int t = lane; t < p.T; t += 32)
       if (mask >> t & 1) {
@@ -333,81 +355,117 @@ __global__ void __launch_bounds__(FEW_THREADS, NT <= 2 ? 2 : 1) few_kernel(const
         }
       }
   }
-  workers_sync();
-  if constexpr (SECOND) {
-    griddep_wait();
-    griddep_launch_dependents();
-  }
-
-  const int g = lane >> 2, c4 = lane & 3;
+  consumers_sync();
+  // few tokens: columns are tokens, whatever the expert, so that W2's sums stay in place
+  constexpr bool DIRECT = SECOND && NT == 1;
   constexpr int SIZE = W8 ? 1 : 2;
   constexpr int CODES = 16 / SIZE;         // weights of 16 bytes
   constexpr int WORDS = CODES / 2;         // of x against them
   constexpr int M = SECOND ? 1 : 2;
-  // few tokens: columns are tokens, whatever the expert, so that W2's sums stay in place
-  constexpr bool DIRECT = SECOND && NT == 1;
+  constexpr int PARTS = SECOND ? 2 : 1;    // hi and lo
+  if constexpr (SECOND) {
+    griddep_wait();
+    griddep_launch_dependents();
+  }
+  // the row of column `col` of expert list[a] (-1: no such token)
+  auto row_of = [&](int a, int col) {
+    const int first = base[a];
+    if constexpr (DIRECT) {
+      const uint32_t mask = static_cast<uint32_t>(masks[list[a]]);
+      return mask >> col & 1 ? first + __popc(mask & ((1u << col) - 1u)) : -1;
+    }
+    if (col >= base[a + 1] - first) return -1;
+    return SECOND ? first + col : static_cast<int>(token[first + col]);
+  };
+
+  if (warp == WARPS + 1) {
+    // ------------------------------------------- producer of x and of scales:
+    // a stage's x of the first eight tokens' columns and its scales come as far
+    // ahead as its weights (loaded by the workers, a stage ahead or at once,
+    // their latency under HBM's load was half of all time)
+    uint32_t s = 0, ph = 0;
+    for (int u = blockIdx.x; u < units; u += gridDim.x) {
+      const int n0 = (SECOND ? u : u % tiles) * 16;
+      for (int i = 0; i < passes; ++i) {
+        const int a = SECOND ? i : u / tiles;
+        const int64_t scale_at = list[a] * p.stride_s + (n0 / BLOCK) * p.ld_s;
+        // the lanes share out the expert's first 1, 2, 4 or 8 tokens (one warp takes
+        // 2000 cycles a stage if it passes over eight columns one by one)
+        const int first = base[a], tokens = base[a + 1] - first;
+        const int shift = tokens > 4 ? 2 : tokens > 2 ? 3 : tokens > 1 ? 4 : 5;  // log2 of a token's lanes
+        const int index = lane >> shift, piece = lane & ((1 << shift) - 1);
+        const bool exists = index < tokens;
+        const int t = exists ? token[first + index] : 0;
+        const uint16_t* x = (SECOND ? p.hi : p.X) + (SECOND ? first + index : t) * p.ldx;
+        const uint32_t col = DIRECT ? t : index;
+        for (int c = 0; c < chunks; ++c) {
+          if (!wait_inline(empty_bar(s), ph ^ 1u, wctx, SITE_PROD_EMPTY)) {
+            asm volatile("cp.async.wait_all;" ::: "memory");
+            return;
+          }
+          const uint32_t to = sbase + at.x + s * at.x_stage;
+          constexpr int PIECES = CHUNK / SIZE / 8;  // 16-byte words of a column
+          if (exists) {
+#pragma unroll
+            for (int q = 0; q < PARTS; ++q)
+#pragma unroll 4
+              for (int v = piece; v < PIECES; v += 1 << shift) {
+                const int k = c * (CHUNK / SIZE) + 8 * v;
+                copy_16(to + q * at.x_part + col * at.x_row + 16u * v, x + (q ? p.lo_at : 0) + k, k < p.K);
+              }
+          }
+          if constexpr (W8) {
+            const int m = lane >> 3, slab = c * WARPS + (lane & 7);
+            if (m < p.matrices)
+              copy_f32(to + PARTS * at.x_part + 4u * lane, p.S[m] + scale_at + slab, slab * 128 < p.row_bytes);
+          }
+          copies_arrive(full_bar(s));
+          if (++s == static_cast<uint32_t>(stages)) {
+            s = 0;
+            ph ^= 1u;
+          }
+        }
+      }
+    }
+    asm volatile("cp.async.wait_all;" ::: "memory");
+    return;
+  }
+
+  // ----------------------------------------------------------------- workers
+  const int g = lane >> 2, c4 = lane & 3;
   uint32_t s = 0, ph = 0;
   float acc[M][NT][4];
   bool ok = true;
-  // This warp's share of expert list[a], rows n0..: adds to acc.
-  auto multiply = [&](int a, int n0) {
-    const int e = list[a], first = base[a], tokens = DIRECT ? 8 : base[a + 1] - first;
-    constexpr int PARTS = SECOND ? 2 : 1;
-    // this lane's column's rows, from its own k on (null: no such token)
-    const int k_lane = warp * (CHUNK / WARPS / SIZE) + CODES * c4;
-    const uint16_t* from[NT][PARTS];
-#pragma unroll
-    for (int j = 0; j < NT; ++j) {
-      const int col = 8 * j + g;
-      bool exists = col < tokens;
-      int row = 0;
-      if constexpr (DIRECT) {
-        const uint32_t mask = static_cast<uint32_t>(masks[e]);
-        exists = mask >> g & 1;
-        row = first + __popc(mask & ((1u << g) - 1u));
-      } else if (exists) {
-        row = SECOND ? first + col : token[first + col];
-      }
-      const uint16_t* at = (SECOND ? p.hi : p.X) + row * p.ldx + k_lane;
-      from[j][0] = exists ? at : nullptr;
-      if constexpr (SECOND) from[j][1] = at + p.lo_at;
-    }
+  struct X {  // what this lane has of one column's x, against 16 weight bytes
+    uint4 v[PARTS][WORDS / 4];
+  };
+  // This warp's share of expert list[a]: adds to acc.
+  auto multiply = [&](int a) {
+    const int tokens = DIRECT ? 8 : base[a + 1] - base[a];
     // DIRECT: which of this lane's sums (columns 2 c4, + 1) belong to the expert's
-    // tokens; in the others its weights, NaN perhaps, met zeros
-    const uint32_t columns = DIRECT ? 5u * (static_cast<uint32_t>(masks[e]) >> (2 * c4) & 3u) : 15u;
-    const float* scale[M];
-#pragma unroll
-    for (int m = 0; m < M; ++m)
-      if constexpr (W8) scale[m] = p.S[m] + e * p.stride_s + (n0 / BLOCK) * p.ld_s + warp;
-    int left = p.K - k_lane;                  // k from this lane's first on
-    int bytes = p.row_bytes - 128 * warp;     // of the rows, from this warp's slab on
-    for (int c = 0; c < chunks; ++c, left -= CHUNK / SIZE, bytes -= CHUNK) {
-      const bool mine = bytes > 0;
-      float sc[M];
-      if constexpr (W8) {
-#pragma unroll
-        for (int m = 0; m < M; ++m) sc[m] = mine && m < p.matrices ? __ldg(scale[m] + c * WARPS) : 0.0f;
-      }
-      // the x of one column of tokens: chunks of 16 weight bytes c4 and c4 + 4
-      uint4 x[2][PARTS][WORDS / 4];
-      auto load_x = [&](int j, int h) {
-#pragma unroll
-        for (int q = 0; q < PARTS; ++q)
-#pragma unroll
-          for (int v = 0; v < WORDS / 4; ++v)
-            x[j ? 0 : h][q][v] = from[j][0] && 4 * CODES * h < left
-                                     ? *reinterpret_cast<const uint4*>(from[j][q] + c * (CHUNK / SIZE) + 4 * CODES * h + 8 * v)
-                                     : make_uint4(0, 0, 0, 0);
-      };
-      load_x(0, 0);
-      load_x(0, 1);
+    // tokens; the others' columns hold anything
+    const uint32_t columns = DIRECT ? 5u * (static_cast<uint32_t>(masks[list[a]]) >> (2 * c4) & 3u) : 15u;
+    for (int c = 0; c < chunks; ++c) {
       if (!wait_inline(full_bar(s), ph, wctx, SITE_MMA_FULL)) {
         ok = false;
         return;
       }
-      if (mine) {
+      if (c * CHUNK + 128 * warp < p.row_bytes) {
+        const uint32_t xs = sbase + at.x + s * at.x_stage;
+        float sc[M];
+        if constexpr (W8) {
+#pragma unroll
+          for (int m = 0; m < M; ++m) sc[m] = ld_shared_f32(xs + PARTS * at.x_part + 32u * m + 4u * warp);
+        }
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
+          const int k = warp * (128 / SIZE) + CODES * (c4 + 4 * h);  // of the stage
+          X now;
+#pragma unroll
+          for (int q = 0; q < PARTS; ++q)
+#pragma unroll
+            for (int v = 0; v < WORDS / 4; ++v)
+              now.v[q][v] = ld_shared_v4(xs + q * at.x_part + min(g, p.T - 1) * at.x_row + 2u * k + 16u * v);
           uint32_t A[M][CODES / 4][4];  // fragments of this lane's 16-byte chunk of rows g and g + 8
 #pragma unroll
           for (int m = 0; m < M; ++m) {
@@ -419,9 +477,7 @@ __global__ void __launch_bounds__(FEW_THREADS, NT <= 2 ? 2 : 1) few_kernel(const
               const uint32_t w[4] = {v.x, v.y, v.z, v.w};
               if constexpr (W8) {
 #pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                  decode4<BF16>(w[i], A[m][i][r], A[m][i][2 + r]);
-                }
+                for (int i = 0; i < 4; ++i) decode4<BF16>(w[i], A[m][i][r], A[m][i][2 + r]);
               } else {
 #pragma unroll
                 for (int i = 0; i < 2; ++i) A[m][i][r] = w[2 * i], A[m][i][2 + r] = w[2 * i + 1];
@@ -431,16 +487,28 @@ __global__ void __launch_bounds__(FEW_THREADS, NT <= 2 ? 2 : 1) few_kernel(const
 #pragma unroll
           for (int j = 0; j < NT; ++j) {
             if (8 * j >= tokens) break;
-            if (j > 0) load_x(j, h);
+            X then = now;
+            if (j + 1 < NT && 8 * (j + 1) < tokens) {
+              // further columns of tokens: from memory
+              const int row = row_of(a, 8 * (j + 1) + g), kk = c * (CHUNK / SIZE) + k;
+              const uint16_t* from = (SECOND ? p.hi : p.X) + row * p.ldx + kk;
+#pragma unroll
+              for (int q = 0; q < PARTS; ++q)
+#pragma unroll
+                for (int v = 0; v < WORDS / 4; ++v)
+                  then.v[q][v] = row >= 0 && kk < p.K ? reinterpret_cast<const uint4*>(from + (q ? p.lo_at : 0))[v]
+                                                      : make_uint4(0, 0, 0, 0);
+            }
             float part[M][4] = {};
 #pragma unroll
             for (int q = 0; q < PARTS; ++q) {
-              const uint32_t* w = reinterpret_cast<const uint32_t*>(&x[j ? 0 : h][q][0]);
+              const uint32_t* w = reinterpret_cast<const uint32_t*>(&now.v[q][0]);
 #pragma unroll
               for (int i = 0; i < CODES / 4; ++i) {
 #pragma unroll
                 for (int m = 0; m < M; ++m)
-                  if (m < p.matrices) mma_16816<BF16>(W8 || DIRECT ? part[m] : acc[m][j], A[m][i], w[2 * i], w[2 * i + 1]);
+                  if (m < p.matrices)
+                    mma_16816<BF16>(W8 || DIRECT ? part[m] : acc[m][j], A[m][i], w[2 * i], w[2 * i + 1]);
               }
             }
             if constexpr (W8 || DIRECT) {
@@ -448,8 +516,10 @@ __global__ void __launch_bounds__(FEW_THREADS, NT <= 2 ? 2 : 1) few_kernel(const
               for (int m = 0; m < M; ++m)
 #pragma unroll
                 for (int i = 0; i < 4; ++i)
-                  if (!DIRECT || (columns >> i & 1)) acc[m][j][i] = W8 ? fmaf(part[m][i], sc[m], acc[m][j][i]) : acc[m][j][i] + part[m][i];
+                  if (!DIRECT || (columns >> i & 1))
+                    acc[m][j][i] = W8 ? fmaf(part[m][i], sc[m], acc[m][j][i]) : acc[m][j][i] + part[m][i];
             }
+            now = then;
           }
         }
       }
@@ -475,7 +545,7 @@ __global__ void __launch_bounds__(FEW_THREADS, NT <= 2 ? 2 : 1) few_kernel(const
       const int a = u / tiles, n0 = (u % tiles) * 16;
       const int first = base[a], tokens = base[a + 1] - first;
       clear();
-      multiply(a, n0);
+      multiply(a);
       if (!workers_agree(ok)) return;
 #pragma unroll
       for (int j = 0; j < NT; ++j) {
@@ -512,7 +582,7 @@ __global__ void __launch_bounds__(FEW_THREADS, NT <= 2 ? 2 : 1) few_kernel(const
       const int n0 = u * 16;
       if constexpr (DIRECT) {
         clear();
-        for (int a = 0; a < chosen && ok; ++a) multiply(a, n0);
+        for (int a = 0; a < chosen && ok; ++a) multiply(a);
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
           const int t = 2 * c4 + (i & 1);
@@ -525,7 +595,7 @@ __global__ void __launch_bounds__(FEW_THREADS, NT <= 2 ? 2 : 1) few_kernel(const
       for (int a = 0; a < chosen && ok && !DIRECT; ++a) {
         const int first = base[a], tokens = base[a + 1] - first;
         clear();
-        multiply(a, n0);
+        multiply(a);
 #pragma unroll
         for (int j = 0; j < NT; ++j) {
           if (8 * j >= tokens) break;
@@ -559,7 +629,6 @@ __global__ void __launch_bounds__(FEW_THREADS, NT <= 2 ? 2 : 1) few_kernel(const
 // ----------------------------------------------------------------------- host
 
 using Kernel = void (*)(const FewParams);
-constexpr int MAX_SMEM = 232448;
 OncePerDevice<cudaError_t> g_setup;
 
 template <bool BF16, bool W8, bool SECOND>
@@ -625,6 +694,26 @@ int check_scales(const float* S, int64_t rows, int64_t length, int64_t* ld, int6
   if (*stride == 0) *stride = ceil_div(rows, BLOCK) * *ld;
   if (!S || *ld < ceil_div(length, BLOCK) || *stride < 0) return TCG_ERR_INVALID;
   return misaligned(S, 4) ? TCG_ERR_ALIGNMENT : TCG_OK;
+}
+
+// How a kernel runs: ring stages, shared memory and CTAs an SM.
+struct Shape {
+  int stages, smem, ctas;
+};
+
+// Two CTAs share an SM where half its memory holds 64 KB of weights and more
+// (up to eight tokens): twice the warps hide their latencies (1 token x 8 of 128
+// experts of 4096 x 1024, E4M3: 30 us, 43 with one).  Else one has what fits.
+Shape shape(int T, int topk, int E, bool second, int size, int matrices) {
+  for (int n = MAX_STAGES / matrices; T <= 8 && n * matrices >= 4; --n) {
+    const int bytes = Layout(T, topk, E, second, size, matrices, n).bytes;
+    if (bytes <= MAX_SMEM / 2 - 1024) return {n, bytes, 2};
+  }
+  for (int n = MAX_STAGES / matrices; n > 1; --n) {
+    const int bytes = Layout(T, topk, E, second, size, matrices, n).bytes;
+    if (bytes <= MAX_SMEM) return {n, bytes, 1};
+  }
+  return {1, Layout(T, topk, E, second, size, matrices, 1).bytes, 1};
 }
 
 int64_t work_bytes(int64_t T, int topk, int64_t I) {
@@ -703,14 +792,17 @@ int run_few(const tcg_moe_few_args* args, cudaStream_t s) {
     if (int rc = weight_maps(&q, 0, a.W2, a.I * size, a.H, a.ld2 * size, a.stride2 * size)) return rc;
     const int64_t units = std::min<int64_t>(a.E, pairs) * ceil_div(a.I, 16);
     if (units > INT32_MAX) return TCG_ERR_UNSUPPORTED;
-    if (int rc = launch(pick<false>(bf16, w8, T), p, std::min<int64_t>(units, sms), Layout(T, a.topk, a.E, false).bytes, s))
-      return rc;
+    const Shape h = shape(T, a.topk, a.E, false, size, p.matrices);
+    p.stages = h.stages;
+    if (int rc = launch(pick<false>(bf16, w8, T), p, std::min<int64_t>(units, h.ctas * sms), h.smem, s)) return rc;
     ++launches;
   }
   q.K = static_cast<int>(a.I);
   q.N = static_cast<int>(a.H);
   q.row_bytes = q.K * size;
   q.matrices = 1;
+  const Shape h = shape(T, a.topk, a.E, true, size, 1);
+  q.stages = h.stages;
   q.ldx = q.ldh;
   q.S[0] = a.S2;
   q.ld_s = a.ld_s2;
@@ -718,9 +810,7 @@ int run_few(const tcg_moe_few_args* args, cudaStream_t s) {
   q.Y = a.Y;
   q.ldy = a.ldy;
   q.y_type = a.y_type;
-  if (int rc = launch(pick<true>(bf16, w8, T), q, std::min<int64_t>(ceil_div(a.H, 16), sms),
-                      Layout(T, a.topk, a.E, true).bytes, s))
-    return rc;
+  if (int rc = launch(pick<true>(bf16, w8, T), q, std::min<int64_t>(ceil_div(a.H, 16), h.ctas * sms), h.smem, s)) return rc;
   set_launch_count(launches + 1);
   return TCG_OK;
 }
