@@ -75,6 +75,7 @@ struct F8Params {
   int C;         // weight: extent of c
   int K;         // contraction length unless weight
   int m_tiles;
+  int split;     // COLUMNS: CTAs of a cluster that share a unit's contraction (1, 2 or 4)
   // scales of single rows or columns: [block][row], b * fine_b + row
   const float* fine;
   int64_t fine_b;
@@ -145,6 +146,17 @@ __device__ __forceinline__ uint64_t mul2(uint64_t a, uint64_t b) {
   return d;
 }
 
+__device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
+  uint64_t d;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
+  return d;
+}
+__device__ __forceinline__ void st_cluster_2x64(uint32_t addr, uint64_t a, uint64_t b) {
+  asm volatile("st.shared::cluster.v2.b64 [%0], {%1, %2};" ::"r"(addr), "l"(a), "l"(b) : "memory");
+}
+__device__ __forceinline__ void ld_shared_2x64(uint32_t addr, uint64_t& a, uint64_t& b) {
+  asm volatile("ld.shared.v2.b64 {%0, %1}, [%2];" : "=l"(a), "=l"(b) : "r"(addr) : "memory");
+}
 __device__ __forceinline__ uint64_t ld_shared_b64(uint32_t addr) {
   uint64_t v;
   asm volatile("ld.shared.b64 %0, [%1];" : "=l"(v) : "r"(addr));
@@ -174,10 +186,12 @@ struct F8Cfg {
   static constexpr int SC_OFF = EPI_OFF + EPI_WARPS * STAGING * STAGING_BYTES;
   // a block's scales: Q's of the columns, then P's of the rows or of all; ROWS: P's of the rows, then Q's of 128 columns each
   static constexpr int SLOT_BYTES = 4 * (MODE == ROWS ? 128 + 4 : BN + (MODE == BOTH ? 128 : 4));
-  static constexpr int BAR_OFF = SC_OFF + SLOTS * SLOT_BYTES;
+  // split contractions: fragments of two column parts and four lane quadrants
+  static constexpr int RED_OFF = (SC_OFF + SLOTS * SLOT_BYTES + 127) / 128 * 128;
+  static constexpr int BAR_OFF = RED_OFF + (MODE == COLUMNS ? EPI_WARPS * 4096 : 0);
   // full[S], empty[S], rag[S], peer[S], acc_full[2], acc_empty[2], drain, tile_full[T], tile_empty[T],
-  // scale_full[L], scale_empty[L]
-  static constexpr int NUM_BARS = 4 * STAGES + 5 + 2 * TILES + 2 * SLOTS;
+  // scale_full[L], scale_empty[L], reduced
+  static constexpr int NUM_BARS = 4 * STAGES + 5 + 2 * TILES + 2 * SLOTS + 1;
   static constexpr int TILE_OFF = (BAR_OFF + NUM_BARS * 8 + 8 + 15) / 16 * 16;  // tmem slot + abort flag before it
   static constexpr int SEG_OFF = TILE_OFF + TILES * 48;
   static constexpr int SMEM_BYTES = 1024 + SEG_OFF + 2 * (MAX_GROUPS + 1) * 4;
@@ -197,6 +211,7 @@ struct alignas(16) FTile {
   int nkb;    // blocks of the contraction (0: the tile is zero)
   int last;   // depth of the last block
   int rows;   // ROWS: rows of the group from m0 on
+  int kb0;    // first block of this CTA
 };
 static_assert(sizeof(FTile) <= 48, "tile ring");
 
@@ -259,6 +274,12 @@ __device__ __forceinline__ FTile decode_unit(const F8Params& p, const int* seg, 
   t.mma_n = p.weight || p.q_mn ? BN : (t.ncols + 16 * CG - 1) / (16 * CG) * (16 * CG);
   t.nkb = (depth + BLOCK - 1) / BLOCK;
   t.last = depth - BLOCK * (t.nkb - 1);
+  t.kb0 = 0;
+  if constexpr (MODE == COLUMNS) {
+    const int per_cta = (t.nkb + p.split - 1) / p.split;
+    t.kb0 = min(t.nkb, per_cta * static_cast<int>(cluster_ctarank()));
+    t.nkb = min(per_cta, t.nkb - t.kb0);
+  }
   return t;
 }
 
@@ -281,6 +302,7 @@ __global__ void __launch_bounds__(F8Cfg<CG, BN, STAGES, MODE>::THREADS, 1) f8_ke
   auto tile_empty = [&](uint32_t i) { return bar0 + 8u * (4 * STAGES + 5 + TILES + i); };
   auto scf_bar = [&](uint32_t i) { return bar0 + 8u * (4 * STAGES + 5 + 2 * TILES + i); };
   auto sce_bar = [&](uint32_t i) { return bar0 + 8u * (4 * STAGES + 5 + 2 * TILES + SLOTS + i); };
+  const uint32_t red_bar = bar0 + 8u * (4 * STAGES + 5 + 2 * TILES + 2 * SLOTS);
   auto slot_at = [&](uint32_t i) { return sbase + C::SC_OFF + i * C::SLOT_BYTES; };
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(gbase + C::BAR_OFF + 8 * C::NUM_BARS);
   volatile uint32_t* abort_flag = tmem_slot + 1;
@@ -290,8 +312,9 @@ __global__ void __launch_bounds__(F8Cfg<CG, BN, STAGES, MODE>::THREADS, 1) f8_ke
   const int warp = threadIdx.x >> 5;
   const int lane = threadIdx.x & 31;
   const uint32_t rank = (CG == 2) ? cluster_ctarank() : 0u;
-  const int cluster_id = blockIdx.x / CG;
-  const int num_clusters = gridDim.x / CG;
+  const int across = MODE == COLUMNS ? p.split : CG;  // CTAs of a cluster
+  const int cluster_id = blockIdx.x / across;
+  const int num_clusters = gridDim.x / across;
   const WaitCtx wctx{p.timeout_ns, p.err, abort_flag};
 
   // the maps exist unless the contraction is empty
@@ -312,6 +335,7 @@ __global__ void __launch_bounds__(F8Cfg<CG, BN, STAGES, MODE>::THREADS, 1) f8_ke
       mbar_init(acce_bar(b), C::EPI_WARPS * CG);
     }
     mbar_init(drain_bar, 1);
+    mbar_init(red_bar, C::EPI_WARPS);
     for (uint32_t i = 0; i < TILES; ++i) {
       mbar_init(tile_full(i), 1);
       mbar_init(tile_empty(i), 3 + C::EPI_WARPS);
@@ -371,7 +395,7 @@ __global__ void __launch_bounds__(F8Cfg<CG, BN, STAGES, MODE>::THREADS, 1) f8_ke
   }
   tc_fence_before();
   __syncthreads();
-  if constexpr (CG == 2) cluster_sync();
+  if (across > 1) cluster_sync();
   tc_fence_after();
   const uint32_t tmem_base = *tmem_slot;
   griddep_launch_dependents();
@@ -420,14 +444,14 @@ __global__ void __launch_bounds__(F8Cfg<CG, BN, STAGES, MODE>::THREADS, 1) f8_ke
       t = next;
       // the tile after this one, ahead of this one's scales
       if (u + num_clusters < total_units && !publish(u + num_clusters, next)) break;
-      const int b0 = p.weight ? t.lo / BLOCK + t.g : 0;
+      const int b0 = p.weight ? t.lo / BLOCK + t.g : t.kb0;
       const int m0 = t.m0 + static_cast<int>(rank) * 128;
       // single scales of `n` columns or rows, and those of the other operand
       const int n = MODE == ROWS ? t.rows - static_cast<int>(rank) * 128 : t.ncols;
       const float* fine = p.fine + b0 * p.fine_b + (p.weight ? t.c0 : MODE == ROWS ? t.lo + m0 : t.lo + t.c0);
       const float* other = MODE == BOTH   ? p.other + b0 * p.other_b + m0
                            : MODE == ROWS ? p.other + t.g * p.other_group + (t.c0 / BLOCK + lane) * p.other_row
-                                          : p.other + t.g * p.other_group + (m0 / BLOCK) * p.other_row;
+                                          : p.other + t.g * p.other_group + (m0 / BLOCK) * p.other_row + b0 * p.other_b;
       constexpr int FINE = MODE == ROWS ? 128 : BN;
       for (int kb = 0; kb < t.nkb; ++kb, ++it) {
         const uint32_t i = it % SLOTS;
@@ -478,7 +502,7 @@ __global__ void __launch_bounds__(F8Cfg<CG, BN, STAGES, MODE>::THREADS, 1) f8_ke
         if (elect_one()) {
           const uint32_t sp = sbase + s * C::STAGE_BYTES;
           const uint32_t sq = sp + C::P_BYTES;
-          const int k0 = BLOCK * kb;
+          const int k0 = BLOCK * (t.kb0 + kb);
           const uint32_t fb = (CG == 2) ? mapa_shared(full_bar(s), 0) : full_bar(s);
           if (p.weight && kb == t.nkb - 1 && (t.last & 31)) {
             // the warp that zeroes the rows past the group's end waits for
@@ -815,6 +839,36 @@ __global__ void __launch_bounds__(F8Cfg<CG, BN, STAGES, MODE>::THREADS, 1) f8_ke
         }
       }
       if (!done) break;
+      if constexpr (MODE == COLUMNS) {
+        if (p.split > 1) {
+          // Every CTA of the cluster sends a lane quadrant's sums to the one CTA that
+          // adds them, in the order of the blocks, and stores them.  A cluster has
+          // one unit at most, so the buffer is written once.
+          const int quads = 4 / p.split, owner = q / quads, from = static_cast<int>(cluster_ctarank());
+          const uint32_t mine_at = sbase + C::RED_OFF + 4096u * ((q % quads * p.split + from) * 2 + part) + 16u * lane;
+          if (mine > 0) {
+            const uint32_t to = mapa_shared(mine_at, static_cast<uint32_t>(owner));
+#pragma unroll
+            for (int v = 0; v < 8; ++v) st_cluster_2x64(to + 512u * v, sum[0][v >> 2][2 * (v & 3)], sum[0][v >> 2][2 * (v & 3) + 1]);
+          }
+          __syncwarp();
+          if (lane == 0) mbar_arrive_cluster(mapa_shared(red_bar, static_cast<uint32_t>(owner)));
+          if (from != owner) continue;
+          if (!wait_inline(red_bar, 0u, wctx, SITE_EPI_ACC_FULL) || !mbar_try_wait_cluster(red_bar, 0u)) break;
+          if (mine <= 0) continue;
+          for (int r = 0; r < p.split; ++r) {
+            const uint32_t at = mine_at + 4096u * 2 * (r - from);
+#pragma unroll
+            for (int v = 0; v < 8; ++v) {
+              uint64_t a, b;
+              ld_shared_2x64(at + 512u * v, a, b);
+              uint64_t &x = sum[0][v >> 2][2 * (v & 3)], &y = sum[0][v >> 2][2 * (v & 3) + 1];
+              x = r ? add2(x, a) : a;
+              y = r ? add2(y, b) : b;
+            }
+          }
+        }
+      }
       const int m_warp = t.m0 + static_cast<int>(rank) * 128 + 32 * q;
       const int row0 = p.weight ? t.c0 : t.lo + t.c0, outer = p.weight ? t.g : 0;
       const int64_t pitch = p.ldd * p.d_size;
@@ -913,7 +967,7 @@ __global__ void __launch_bounds__(F8Cfg<CG, BN, STAGES, MODE>::THREADS, 1) f8_ke
   tc_fence_before();
   cta_barrier_unaligned();
   __syncwarp();
-  if constexpr (CG == 2) cluster_sync();
+  if (across > 1) cluster_sync();
   tc_fence_after();
   if (warp == 2) tmem_dealloc<CG>(tmem_base, 512);
 }
@@ -991,7 +1045,8 @@ int launch_f8(const KernelInfo& ki, F8Params& p, int dev, int64_t units, cudaStr
   if (units > INT32_MAX / 2) return TCG_ERR_UNSUPPORTED;
   int clusters = 0;
   if (int rc = max_resident_clusters(dev, ki, &clusters)) return rc;
-  const int cg = ki.cta_group;
+  const int cg = std::max(ki.cta_group, p.split);
+  if (p.split > 1) clusters = static_cast<int>(units);
   p.d_size = p.d_type == TCG_F32 ? 4 : 2;
   // TMA stores where the output's rows and matrices are 16-byte aligned and
   // end on such a boundary
@@ -1035,7 +1090,7 @@ struct Plan {
 
 Plan choose(int64_t R, int G, bool a_mn, bool square) {
   if (!square) return {variant<2, 256, 5, BOTH>(), BOTH};
-  if (!a_mn && R <= 64 * static_cast<int64_t>(G)) return {variant<1, 64, 7, COLUMNS>(), COLUMNS};
+  if (!a_mn && R <= 64 * static_cast<int64_t>(G)) return {variant<1, 64, 6, COLUMNS>(), COLUMNS};
   return {variant<2, 256, 5, ROWS>(), ROWS};
 }
 
@@ -1054,7 +1109,13 @@ int run_rows(const Plan& plan, F8Params& p, int dev, tcg_input type, const Opera
   p.other_b = plan.mode == BOTH || B.mn ? ld_sb : 1;
   // an upper bound of the units: a full tile per so many rows and one more per group
   const int64_t per = rows ? 128 * cg : plan.ki.bn;
-  return launch_f8(plan.ki, p, dev, (p.R / per + groups) * (rows ? 1 : 2) * p.m_tiles, s);
+  const int64_t units = (p.R / per + groups) * p.m_tiles;
+  // Where the tiles leave SMs idle, 2 or 4 CTAs share one's contraction (at least
+  // four blocks each).
+  p.split = 1;
+  if (plan.mode == COLUMNS)
+    while (p.split < 4 && units * p.split * 2 <= device_sms(dev) && p.K >= 8 * BLOCK * p.split) p.split *= 2;
+  return launch_f8(plan.ki, p, dev, units, s);
 }
 
 int run_dense(tcg_input type, int64_t M, int64_t N, int64_t K, const void* A, tcg_major a_major, int64_t lda,
@@ -1154,7 +1215,7 @@ int run_wgrad(tcg_input type, int64_t R, int64_t N, int64_t K, int G, const void
   p.offsets = offsets;
   p.G = G;
   p.R = static_cast<int>(R);
-  p.weight = 1;
+  p.weight = p.split = 1;
   p.M = static_cast<int>(K);
   p.C = static_cast<int>(N);
   p.m_tiles = static_cast<int>(ceil_div(K, 128 * ki.cta_group));
