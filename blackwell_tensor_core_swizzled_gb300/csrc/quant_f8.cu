@@ -13,13 +13,14 @@
 // Both kernels read X once, keep it in registers between the maximum and the
 // codes, and are bound by HBM.  Rows: a half warp (16-bit types) or a warp holds
 // a block's row, a warp takes 8 rows so that their 8 loads are in flight
-// together and the 8 scales, neighbours in memory, leave as one sector.  Columns
-// and squares: a CTA holds 128 x 128.
+// together and the 8 scales, neighbours in memory, leave as one sector.  Columns:
+// a warp holds 128 rows of 32 or 16 columns.  Squares: a CTA holds a block.
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 #include <cuda_fp8.h>
 #include <cuda_runtime.h>
 
+#include <algorithm>
 #include <cstdint>
 #include <type_traits>
 
@@ -35,11 +36,63 @@ constexpr int MAX_GROUPS = 1024;
 constexpr int64_t MAX_EXTENT = int64_t{1} << 30;
 constexpr int ROW_WARPS = 4;
 constexpr int ROWS = 8;  // rows of a warp
-constexpr int TILE_THREADS = 256;
+constexpr int COL_WARPS = 4;
+constexpr int SQUARE_THREADS = 256;
 
-__device__ __forceinline__ float to_f32(float v) { return v; }
-__device__ __forceinline__ float to_f32(__half v) { return __half2float(v); }
-__device__ __forceinline__ float to_f32(__nv_bfloat16 v) { return __bfloat162float(v); }
+// 16 bytes of X: V values of type T.  Maxima are taken of the words as they are
+// (pairs of 16-bit values at a time): converted first, the values took twice the
+// registers, and kept them until the codes.
+template <class T>
+struct Word {
+  static constexpr int V = 16 / static_cast<int>(sizeof(T));
+  uint32_t w[4];
+
+  __device__ __forceinline__ void load(const T* from, int n, bool aligned) {  // the first n values, then zeros
+    if (aligned) {
+      const uint4 v = n > 0 ? *reinterpret_cast<const uint4*>(from) : make_uint4(0, 0, 0, 0);
+      w[0] = v.x, w[1] = v.y, w[2] = v.z, w[3] = v.w;
+    } else if constexpr (sizeof(T) == 4) {
+#pragma unroll
+      for (int j = 0; j < 4; ++j) w[j] = j < n ? reinterpret_cast<const uint32_t*>(from)[j] : 0u;
+    } else {
+      const uint16_t* h = reinterpret_cast<const uint16_t*>(from);
+#pragma unroll
+      for (int j = 0; j < 4; ++j) w[j] = (2 * j < n ? h[2 * j] : 0u) | (2 * j + 1 < n ? h[2 * j + 1] : 0u) << 16;
+    }
+  }
+
+  __device__ __forceinline__ float value(int j) const {
+    if constexpr (std::is_same<T, float>::value)
+      return __uint_as_float(w[j]);
+    else if constexpr (std::is_same<T, __half>::value)
+      return __half2float(__ushort_as_half(static_cast<uint16_t>(w[j / 2] >> (16 * (j % 2)))));
+    else
+      return __uint_as_float(j % 2 ? w[j / 2] & 0xffff0000u : w[j / 2] << 16);
+  }
+};
+
+// The larger magnitudes of a word (already positive) and another; NaN are passed over.
+template <class T>
+__device__ __forceinline__ uint32_t most(uint32_t a, uint32_t x) {
+  if constexpr (std::is_same<T, float>::value) {
+    return __float_as_uint(fmaxf(__uint_as_float(a), fabsf(__uint_as_float(x))));
+  } else {
+    using T2 = typename std::conditional<std::is_same<T, __half>::value, __half2, __nv_bfloat162>::type;
+    const T2 m = __hmax2(*reinterpret_cast<const T2*>(&a), __habs2(*reinterpret_cast<const T2*>(&x)));
+    return *reinterpret_cast<const uint32_t*>(&m);
+  }
+}
+
+// The largest value of a word.
+template <class T>
+__device__ __forceinline__ float largest_in(uint32_t a) {
+  Word<T> x;
+  x.w[0] = a;
+  if constexpr (std::is_same<T, float>::value)
+    return x.value(0);
+  else
+    return fmaxf(x.value(0), x.value(1));
+}
 
 // How the values of a block become codes.
 struct Coder {
@@ -77,6 +130,10 @@ __device__ __forceinline__ Coder make_coder(float amax, bool pow2, float& scale)
   return {F * pre, a, 1.0f / a};
 }
 
+__device__ __forceinline__ Coder from_lane(const Coder& c, int lane) {
+  return {__shfl_sync(0xffffffffu, c.by, lane), __shfl_sync(0xffffffffu, c.a, lane), __shfl_sync(0xffffffffu, c.inv, lane)};
+}
+
 __device__ __forceinline__ float quotient(float x, const Coder& c) {
   const float n = x * c.by;
   const float y = n * c.inv;
@@ -92,111 +149,103 @@ __device__ __forceinline__ uint32_t encode4(float a, float b, float c, float d) 
   return lo | hi << 16;
 }
 
-// NaN are passed over
-__device__ __forceinline__ float most(float a, float x) { return fmaxf(a, fabsf(x)); }
+// V codes of a word.
+template <bool WIDE, class T, class F>
+__device__ __forceinline__ void store_codes(const Word<T>& x, uint8_t* q, int n, bool aligned, F&& coder) {
+  constexpr int V = Word<T>::V;
+  uint32_t code[V / 4];
+#pragma unroll
+  for (int j = 0; j < V; j += 4)
+    code[j / 4] = encode4<WIDE>(quotient(x.value(j), coder(j)), quotient(x.value(j + 1), coder(j + 1)),
+                                quotient(x.value(j + 2), coder(j + 2)), quotient(x.value(j + 3), coder(j + 3)));
+  if (!aligned) {
+#pragma unroll
+    for (int j = 0; j < V; ++j)
+      if (j < n) q[j] = static_cast<uint8_t>(code[j / 4] >> (8 * (j % 4)));
+  } else if (n > 0) {
+    if constexpr (V == 8)
+      *reinterpret_cast<uint2*>(q) = make_uint2(code[0], code[1]);
+    else
+      *reinterpret_cast<uint32_t*>(q) = code[0];
+  }
+}
 
 // ----------------------------------------------------------------------- rows
 //
-// V elements a lane, 128 / V lanes a block.  ALIGNED: X in 16-byte words, Q in
-// words of V bytes.
+// A word a lane, 16 or 32 lanes a block.  ALIGNED: X in 16-byte words, Q in words of
+// V bytes, and C whole words.
 template <class T, bool WIDE, bool ALIGNED>
 __global__ void __launch_bounds__(32 * ROW_WARPS) row_kernel(int64_t R, int64_t C, const T* __restrict__ X,
                                                              int64_t ldx, bool pow2, uint8_t* __restrict__ Q,
                                                              int64_t ldq, float* __restrict__ scale,
                                                              int64_t ld_scale, int64_t col_warps) {
-  constexpr int V = ALIGNED ? 16 / static_cast<int>(sizeof(T)) : 4;
-  constexpr int LANES = BLOCK / V;  // 16 or 32
+  constexpr int V = Word<T>::V;
+  constexpr int LANES = BLOCK / V;
   const int lane = threadIdx.x & 31;
   const int64_t w = static_cast<int64_t>(blockIdx.x) * ROW_WARPS + (threadIdx.x >> 5);
   const int64_t r0 = w / col_warps * ROWS;
   const int64_t c = (w % col_warps) * 32 * V + lane * V;
+  const int n = static_cast<int>(max(int64_t{0}, min(static_cast<int64_t>(V), C - c)));
   griddep_wait();
   if (r0 >= R) return;
   const int rows = static_cast<int>(min(static_cast<int64_t>(ROWS), R - r0));
-  float x[ROWS][V];
-  uint4 raw[ALIGNED ? ROWS : 1];
-  if constexpr (ALIGNED) {
+  Word<T> x[ROWS];
 #pragma unroll
-    for (int i = 0; i < ROWS; ++i)
-      raw[i] = i < rows && c < C ? *reinterpret_cast<const uint4*>(X + (r0 + i) * ldx + c) : make_uint4(0, 0, 0, 0);
-#pragma unroll
-    for (int i = 0; i < ROWS; ++i) {
-      const T* v = reinterpret_cast<const T*>(&raw[i]);
-#pragma unroll
-      for (int j = 0; j < V; ++j) x[i][j] = to_f32(v[j]);
-    }
-  } else {
-#pragma unroll
-    for (int i = 0; i < ROWS; ++i)
-#pragma unroll
-      for (int j = 0; j < V; ++j) x[i][j] = i < rows && c + j < C ? to_f32(X[(r0 + i) * ldx + c + j]) : 0.0f;
-  }
-  float mine = 0.0f;  // the scale of row lane % LANES
+  for (int i = 0; i < ROWS; ++i) x[i].load(X + (r0 + i) * ldx + c, i < rows ? n : 0, ALIGNED);
+  // a lane makes the coder of one row, for all lanes of its block (each of them all
+  // eight: as many instructions as the codes; 16384 x 8192 bf16 95 us, 71 so)
+  float mine = 0.0f;
 #pragma unroll
   for (int i = 0; i < ROWS; ++i) {
-    float a = 0.0f;
+    uint32_t m = 0;
 #pragma unroll
-    for (int j = 0; j < V; ++j) a = most(a, x[i][j]);
+    for (int j = 0; j < 4; ++j) m = most<T>(m, x[i].w[j]);
+    float a = largest_in<T>(m);
 #pragma unroll
     for (int d = LANES / 2; d; d >>= 1) a = fmaxf(a, __shfl_xor_sync(0xffffffffu, a, d));
-    float s;
-    const Coder k = make_coder<WIDE>(a, pow2, s);
-    if (lane % LANES == i) mine = s;
-    if (i < rows && c < C) {
-      uint8_t* q = Q + (r0 + i) * ldq + c;
-      uint32_t code[V / 4];
+    if (lane % ROWS == i) mine = a;
+  }
+  float s;
+  const Coder my = make_coder<WIDE>(mine, pow2, s);
 #pragma unroll
-      for (int j = 0; j < V; j += 4)
-        code[j / 4] = encode4<WIDE>(quotient(x[i][j], k), quotient(x[i][j + 1], k), quotient(x[i][j + 2], k),
-                                    quotient(x[i][j + 3], k));
-      if constexpr (ALIGNED && V == 8) {
-        *reinterpret_cast<uint2*>(q) = make_uint2(code[0], code[1]);
-      } else if constexpr (ALIGNED) {
-        *reinterpret_cast<uint32_t*>(q) = code[0];
-      } else {
-#pragma unroll
-        for (int j = 0; j < V; ++j)
-          if (c + j < C) q[j] = static_cast<uint8_t>(code[0] >> (8 * j));
-      }
-    }
+  for (int i = 0; i < ROWS; ++i) {
+    const Coder k = from_lane(my, lane / LANES * LANES + i);
+    if (i < rows) store_codes<WIDE>(x[i], Q + (r0 + i) * ldq + c, n, ALIGNED, [&](int) { return k; });
   }
   const int64_t block = (c - lane % LANES * V) / BLOCK;
-  if (lane % LANES < rows && block * BLOCK < C) scale[block * ld_scale + r0 + lane % LANES] = mine;
+  if (lane % LANES < rows && block * BLOCK < C) scale[block * ld_scale + r0 + lane % LANES] = s;
   griddep_launch_dependents();
 }
 
-// --------------------------------------------------------- columns and squares
+// -------------------------------------------------------------------- columns
 
-// A tile of up to 128 x 128: thread t holds rows t / 16 + 16 i and columns
-// 8 (t % 16) .. + 8.  SQUARE: one block; else a block a column.
-template <class T, bool WIDE, bool ALIGNED, bool SQUARE>
-__global__ void __launch_bounds__(TILE_THREADS) tile_kernel(int64_t R, int64_t C, const T* __restrict__ X, int64_t ldx,
-                                                            bool pow2, int G, const int32_t* __restrict__ offsets,
-                                                            uint8_t* __restrict__ Q, int64_t ldq,
-                                                            float* __restrict__ scale, int64_t ld_scale,
-                                                            int64_t col_tiles) {
-  __shared__ float top[TILE_THREADS / 32][BLOCK];
-  const int t = threadIdx.x;
-  const int64_t slot = blockIdx.x / col_tiles;  // the block's row of scales
-  const int64_t tile = blockIdx.x % col_tiles;
-  const int64_t c = tile * BLOCK + 8 * (t & 15);
+// A warp takes 128 rows by four times V columns at a time: lane 4 g + w holds rows
+// g + 8 i and columns V w .. + V.  Its maxima and coders go through shuffles alone,
+// so warps never wait for one another (as CTAs of 128 x 64 with barriers, 16385 x
+// 4096 bf16 took 55 to 67 us).  Four warps share a run of column tiles of one
+// block of rows, whose group each looks up once.
+template <class T, bool WIDE, bool ALIGNED>
+__global__ void __launch_bounds__(32 * COL_WARPS) column_kernel(int64_t R, int64_t C, const T* __restrict__ X,
+                                                                int64_t ldx, bool pow2, int G,
+                                                                const int32_t* __restrict__ offsets,
+                                                                uint8_t* __restrict__ Q, int64_t ldq,
+                                                                float* __restrict__ scale, int64_t ld_scale, int run) {
+  constexpr int V = Word<T>::V;
+  constexpr int COLS = 4 * V, PER = BLOCK / 8;
+  const int lane = threadIdx.x & 31, g8 = lane >> 2, w4 = lane & 3;
+  const int64_t tiles = (C + COLS - 1) / COLS, runs = (tiles + run - 1) / run;
+  const int64_t slot = blockIdx.x / runs;  // the block's row of scales
+  const int64_t first_tile = blockIdx.x % runs * run, end_tile = min(first_tile + run, tiles);
   griddep_wait();
   int64_t lo = slot * BLOCK, end = R;
   if (offsets) {
     // block j of group g has slot offsets[g] / 128 + g + j; the slots of groups rise
-    int below = 0;
-    for (int g = t; g < G; g += TILE_THREADS) {
-      const int64_t o = min(max(static_cast<int64_t>(offsets[g]), int64_t{0}), R);
-      below += o / BLOCK + g <= slot;
-    }
-#pragma unroll
-    for (int d = 16; d; d >>= 1) below += __shfl_xor_sync(0xffffffffu, below, d);
-    int* count = reinterpret_cast<int*>(&top[0][0]);
-    if ((t & 31) == 0) count[t >> 5] = below;
-    __syncthreads();
     int g = -1;
-    for (int i = 0; i < TILE_THREADS / 32; ++i) g += count[i];
-    __syncthreads();
+    for (int i = lane; i < G; i += 32) {
+      const int64_t o = min(max(static_cast<int64_t>(offsets[i]), int64_t{0}), R);
+      g += o / BLOCK + i <= slot;
+    }
+    g = __reduce_add_sync(0xffffffffu, g) + 31;
     if (g < 0) return;
     const int64_t first = min(max(static_cast<int64_t>(offsets[g]), int64_t{0}), R);
     end = min(max(static_cast<int64_t>(offsets[g + 1]), first), R);
@@ -204,90 +253,82 @@ __global__ void __launch_bounds__(TILE_THREADS) tile_kernel(int64_t R, int64_t C
   }
   if (lo >= end) return;  // a slot that no group uses keeps its value
   const int rows = static_cast<int>(min(static_cast<int64_t>(BLOCK), end - lo));
-  // kept in its own type: fp32 values took 64 registers, and a CTA more an SM
-  struct alignas(16) Row {
-    T v[8];
-  } x[8];
+  for (int64_t tile = first_tile + (threadIdx.x >> 5); tile < end_tile; tile += COL_WARPS) {
+    const int64_t c = tile * COLS + V * w4;
+    const int n = static_cast<int>(max(int64_t{0}, min(static_cast<int64_t>(V), C - c)));
+    Word<T> x[PER];
 #pragma unroll
-  for (int i = 0; i < 8; ++i) {
-    const int row = (t >> 4) + 16 * i;
-    const T* from = X + (lo + row) * ldx + c;
-    if constexpr (ALIGNED) {
-      constexpr int V = 16 / static_cast<int>(sizeof(T));
+    for (int i = 0; i < PER; ++i)
+      x[i].load(X + (lo + g8 + 8 * i) * ldx + c, g8 + 8 * i < rows ? n : 0, ALIGNED);
+    Word<T> top;  // of the columns
 #pragma unroll
-      for (int h = 0; h < 8; h += V)
-        *reinterpret_cast<uint4*>(&x[i].v[h]) =
-            row < rows && c + h < C ? *reinterpret_cast<const uint4*>(from + h) : make_uint4(0, 0, 0, 0);
-    } else {
+    for (int j = 0; j < 4; ++j) {
+      top.w[j] = 0;
 #pragma unroll
-      for (int j = 0; j < 8; ++j) x[i].v[j] = row < rows && c + j < C ? from[j] : T(0.0f);
+      for (int i = 0; i < PER; ++i) top.w[j] = most<T>(top.w[j], x[i].w[j]);
+#pragma unroll
+      for (int d = 16; d >= 4; d >>= 1) top.w[j] = most<T>(top.w[j], __shfl_xor_sync(0xffffffffu, top.w[j], d));
+    }
+    float mine = 0.0f;  // the largest of column V w4 + g8
+#pragma unroll
+    for (int j = 0; j < V; ++j)
+      if (g8 % V == j) mine = top.value(j);
+    float s;
+    const Coder my = make_coder<WIDE>(mine, pow2, s);
+    if (g8 < V && c + g8 < C) scale[slot * ld_scale + c + g8] = s;
+    Coder k[V];
+#pragma unroll
+    for (int j = 0; j < V; ++j) k[j] = from_lane(my, 4 * j + w4);
+#pragma unroll
+    for (int i = 0; i < PER; ++i) {
+      if (g8 + 8 * i >= rows) break;
+      store_codes<WIDE>(x[i], Q + (lo + g8 + 8 * i) * ldq + c, n, ALIGNED, [&](int j) { return k[j]; });
     }
   }
-  float a[8];
+  griddep_launch_dependents();
+}
+
+// -------------------------------------------------------------------- squares
+
+// A block a CTA: warp w holds rows 16 w .. + 16, in words of 16 bytes.
+template <class T, bool WIDE, bool ALIGNED>
+__global__ void __launch_bounds__(SQUARE_THREADS) square_kernel(int64_t R, int64_t C, const T* __restrict__ X,
+                                                                int64_t ldx, bool pow2, uint8_t* __restrict__ Q,
+                                                                int64_t ldq, float* __restrict__ scale,
+                                                                int64_t ld_scale, int64_t col_tiles) {
+  constexpr int V = Word<T>::V;
+  constexpr int ACROSS = BLOCK / V, DOWN = SQUARE_THREADS / ACROSS, PER = BLOCK / DOWN;
+  __shared__ float top[SQUARE_THREADS / 32];
+  const int t = threadIdx.x;
+  const int64_t lo = blockIdx.x / col_tiles * BLOCK, tile = blockIdx.x % col_tiles;
+  const int64_t c = tile * BLOCK + V * (t % ACROSS);
+  const int n = static_cast<int>(max(int64_t{0}, min(static_cast<int64_t>(V), C - c)));
+  const int rows = static_cast<int>(min(static_cast<int64_t>(BLOCK), R - lo));
+  griddep_wait();
+  Word<T> x[PER];
 #pragma unroll
-  for (int j = 0; j < 8; ++j) {
-    a[j] = 0.0f;
-#pragma unroll
-    for (int i = 0; i < 8; ++i) a[j] = most(a[j], to_f32(x[i].v[j]));
+  for (int i = 0; i < PER; ++i) {
+    const int row = t / ACROSS + DOWN * i;
+    x[i].load(X + (lo + row) * ldx + c, row < rows ? n : 0, ALIGNED);
   }
-  float s[8];
-  Coder k[SQUARE ? 1 : 8];
-  if constexpr (SQUARE) {
-    float m = a[0];
+  uint32_t w = 0;
 #pragma unroll
-    for (int j = 1; j < 8; ++j) m = fmaxf(m, a[j]);
+  for (int i = 0; i < PER; ++i)
 #pragma unroll
-    for (int d = 16; d; d >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, d));
-    if ((t & 31) == 0) top[0][t >> 5] = m;
-    __syncthreads();
+    for (int j = 0; j < 4; ++j) w = most<T>(w, x[i].w[j]);
+  float m = largest_in<T>(w), s;
 #pragma unroll
-    for (int i = 0; i < TILE_THREADS / 32; ++i) m = fmaxf(m, top[0][i]);
-    k[0] = make_coder<WIDE>(m, pow2, s[0]);
-    if (t == 0) scale[slot * ld_scale + tile] = s[0];
-  } else {
+  for (int d = 16; d; d >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, d));
+  if ((t & 31) == 0) top[t >> 5] = m;
+  __syncthreads();
 #pragma unroll
-    for (int j = 0; j < 8; ++j) a[j] = fmaxf(a[j], __shfl_xor_sync(0xffffffffu, a[j], 16));
-    if ((t & 31) < 16) {
-      *reinterpret_cast<float4*>(&top[t >> 5][8 * (t & 15)]) = make_float4(a[0], a[1], a[2], a[3]);
-      *reinterpret_cast<float4*>(&top[t >> 5][8 * (t & 15) + 4]) = make_float4(a[4], a[5], a[6], a[7]);
-    }
-    __syncthreads();
+  for (int i = 0; i < SQUARE_THREADS / 32; ++i) m = fmaxf(m, top[i]);
+  const Coder k = make_coder<WIDE>(m, pow2, s);
+  if (t == 0) scale[blockIdx.x / col_tiles * ld_scale + tile] = s;
 #pragma unroll
-    for (int i = 0; i < TILE_THREADS / 32; ++i)
-#pragma unroll
-      for (int j = 0; j < 8; ++j) a[j] = fmaxf(a[j], top[i][8 * (t & 15) + j]);
-#pragma unroll
-    for (int j = 0; j < 8; ++j) {
-      k[j] = make_coder<WIDE>(a[j], pow2, s[j]);
-      if (t < 16 && c + j < C) scale[slot * ld_scale + c + j] = s[j];
-    }
-  }
-#pragma unroll
-  for (int i = 0; i < 8; ++i) {
-    const int row = (t >> 4) + 16 * i;
-    if (row >= rows) break;
-    uint8_t* q = Q + (lo + row) * ldq + c;
-    uint32_t code[2];
-#pragma unroll
-    for (int h = 0; h < 2; ++h) {
-      float y[4];
-#pragma unroll
-      for (int j = 0; j < 4; ++j) y[j] = quotient(to_f32(x[i].v[4 * h + j]), k[SQUARE ? 0 : 4 * h + j]);
-      code[h] = encode4<WIDE>(y[0], y[1], y[2], y[3]);
-    }
-    if constexpr (ALIGNED) {
-      if (sizeof(T) == 2) {
-        if (c < C) *reinterpret_cast<uint2*>(q) = make_uint2(code[0], code[1]);
-      } else {
-#pragma unroll
-        for (int h = 0; h < 2; ++h)
-          if (c + 4 * h < C) *reinterpret_cast<uint32_t*>(q + 4 * h) = code[h];
-      }
-    } else {
-#pragma unroll
-      for (int j = 0; j < 8; ++j)
-        if (c + j < C) q[j] = static_cast<uint8_t>(code[j / 4] >> (8 * (j % 4)));
-    }
+  for (int i = 0; i < PER; ++i) {
+    const int row = t / ACROSS + DOWN * i;
+    if (row < rows) store_codes<WIDE>(x[i], Q + (lo + row) * ldq + c, n, ALIGNED, [&](int) { return k; });
   }
   griddep_launch_dependents();
 }
@@ -315,19 +356,23 @@ int64_t ceil_div(int64_t a, int64_t b) { return (a + b - 1) / b; }
 
 template <class T, bool WIDE, bool ALIGNED>
 int run_typed(tcg_f8_blocks blocks, bool pow2, int64_t R, int64_t C, const T* X, int64_t ldx, int G,
-              const int32_t* offsets, uint8_t* Q, int64_t ldq, float* scale, int64_t ld_scale, cudaStream_t s) {
+              const int32_t* offsets, uint8_t* Q, int64_t ldq, float* scale, int64_t ld_scale, int sms, cudaStream_t s) {
   if (blocks == TCG_F8_ROW) {
-    constexpr int64_t V = ALIGNED ? 16 / sizeof(T) : 4;
+    constexpr int64_t V = Word<T>::V;
     const int64_t col_warps = ceil_div(C, 32 * V);
     return launch(row_kernel<T, WIDE, ALIGNED>, ceil_div(ceil_div(R, ROWS) * col_warps, ROW_WARPS), 32 * ROW_WARPS, s,
                   R, C, X, ldx, pow2, Q, ldq, scale, ld_scale, col_warps);
   }
-  const int64_t tiles = ceil_div(C, BLOCK), slots = offsets ? R / BLOCK + G : ceil_div(R, BLOCK);
-  if (blocks == TCG_F8_SQUARE)
-    return launch(tile_kernel<T, WIDE, ALIGNED, true>, slots * tiles, TILE_THREADS, s, R, C, X, ldx, pow2, G, offsets,
-                  Q, ldq, scale, ld_scale, tiles);
-  return launch(tile_kernel<T, WIDE, ALIGNED, false>, slots * tiles, TILE_THREADS, s, R, C, X, ldx, pow2, G, offsets, Q,
-                ldq, scale, ld_scale, tiles);
+  if (blocks == TCG_F8_SQUARE) {
+    const int64_t tiles = ceil_div(C, BLOCK);
+    return launch(square_kernel<T, WIDE, ALIGNED>, ceil_div(R, BLOCK) * tiles, SQUARE_THREADS, s, R, C, X, ldx, pow2, Q,
+                  ldq, scale, ld_scale, tiles);
+  }
+  const int64_t tiles = ceil_div(C, 64 / static_cast<int64_t>(sizeof(T))), slots = offsets ? R / BLOCK + G : ceil_div(R, BLOCK);
+  // runs of up to 8 tiles a warp, as long as 16 CTAs an SM are left
+  const int run = COL_WARPS * static_cast<int>(std::max<int64_t>(1, std::min<int64_t>(8, slots * tiles / (16 * COL_WARPS * sms))));
+  return launch(column_kernel<T, WIDE, ALIGNED>, slots * ceil_div(tiles, run), 32 * COL_WARPS, s, R, C, X, ldx, pow2, G,
+                offsets, Q, ldq, scale, ld_scale, run);
 }
 
 int run_quantize(tcg_input q_type, tcg_f8_blocks blocks, int pow2, int64_t R, int64_t C, tcg_dtype x_type,
@@ -350,6 +395,7 @@ int run_quantize(tcg_input q_type, tcg_f8_blocks blocks, int pow2, int64_t R, in
   if (at(X) % size || at(scale) % 4 || at(offsets) % 4) return TCG_ERR_ALIGNMENT;
   int dev;
   if (int rc = current_device_checked(&dev)) return rc;
+  const int sms = device_sms(dev);
   const int64_t V = 16 / size;  // elements of a 16-byte word
   const bool aligned = at(X) % 16 == 0 && ldx % V == 0 && C % V == 0 && at(Q) % V == 0 && ldq % V == 0;
   const auto typed = [&](auto z) {
@@ -358,10 +404,10 @@ int run_quantize(tcg_input q_type, tcg_f8_blocks blocks, int pow2, int64_t R, in
     uint8_t* q = static_cast<uint8_t*>(Q);
     const bool p = pow2 != 0;
     if (q_type == TCG_IN_E5M2)
-      return aligned ? run_typed<T, true, true>(blocks, p, R, C, x, ldx, G, offsets, q, ldq, scale, ld_scale, s)
-                     : run_typed<T, true, false>(blocks, p, R, C, x, ldx, G, offsets, q, ldq, scale, ld_scale, s);
-    return aligned ? run_typed<T, false, true>(blocks, p, R, C, x, ldx, G, offsets, q, ldq, scale, ld_scale, s)
-                   : run_typed<T, false, false>(blocks, p, R, C, x, ldx, G, offsets, q, ldq, scale, ld_scale, s);
+      return aligned ? run_typed<T, true, true>(blocks, p, R, C, x, ldx, G, offsets, q, ldq, scale, ld_scale, sms, s)
+                     : run_typed<T, true, false>(blocks, p, R, C, x, ldx, G, offsets, q, ldq, scale, ld_scale, sms, s);
+    return aligned ? run_typed<T, false, true>(blocks, p, R, C, x, ldx, G, offsets, q, ldq, scale, ld_scale, sms, s)
+                   : run_typed<T, false, false>(blocks, p, R, C, x, ldx, G, offsets, q, ldq, scale, ld_scale, sms, s);
   };
   if (x_type == TCG_F32) return typed(float{});
   if (x_type == TCG_F16) return typed(__half{});
