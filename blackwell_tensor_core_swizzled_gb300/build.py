@@ -23,7 +23,7 @@ LIB = os.path.join(HERE, "libtcg.so")
 SOURCES = ["api.cu", "gemm_f16.cu", "gemm_tf32.cu", "gemm_mxf8.cu", "probes.cu", "gemm_mxf8_noalloc.cu",
            "splitk_reduce.cu", "gemm_chain.cu", "moe_host.cu", "moe.cu", "gemm_grouped.cu",
            "gemv_w4.cu", "gemv_w4_runs.cu", "quant_f8.cu", "gemm_f8.cu",
-           "moe_few.cu"]
+           "moe_few.cu", "gemv_f8.cu"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 
 

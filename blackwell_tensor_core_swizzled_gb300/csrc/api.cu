@@ -36,6 +36,7 @@ struct PlanRecord {
   bool grouped = false;
   int w4_rows = 0, w4_across = 0, w4_down = 0, w4_ctas = 0;  // 4-bit products; w4_rows 0: another
   bool w4_boxes = false;
+  int gemv_rows = 0, gemv_stages = 0, gemv_ctas = 0;  // few rows of 8-bit codes; gemv_rows 0: another
   bool k_zero = false;
   int cg = 0, bn = 0, clusters = 0, split = 0;
   int mc = 1;  // CTAs per cluster sharing B tiles by multicast
@@ -893,6 +894,13 @@ void record_w4_plan(int rows, int across, int down, int ctas, bool boxes) {
   t_plan.w4_boxes = boxes;
 }
 
+void record_gemv_f8_plan(int rows, int stages, int ctas) {
+  t_plan.valid = true;
+  t_plan.gemv_rows = rows;
+  t_plan.gemv_stages = stages;
+  t_plan.gemv_ctas = ctas;
+}
+
 void set_error_message(const char* msg) { t_last_error = msg ? msg : ""; }
 
 }  // namespace tcg
@@ -1216,6 +1224,11 @@ const char* tcg_last_plan_string(void) {
     char buf[200];
     std::snprintf(buf, sizeof buf, "4-bit, blocks of %d rows, warps %d across K and %d down, scales in %s, %d CTAs",
                   p.w4_rows, p.w4_across, p.w4_down, p.w4_boxes ? "boxes" : "runs", p.w4_ctas);
+    t_last_plan = buf;
+  } else if (p.gemv_rows) {
+    char buf[200];
+    std::snprintf(buf, sizeof buf, "8-bit, blocks of %d rows, ring of %d stages, %d CTAs", p.gemv_rows, p.gemv_stages,
+                  p.gemv_ctas);
     t_last_plan = buf;
   } else if (p.grouped) {
     char buf[200];

@@ -91,12 +91,18 @@ int make_store_map(CUtensorMap* map, const void* base, tcg_dtype type, uint64_t 
 // of inner x box_mid x box_slabs x 1.
 int make_slab_map(CUtensorMap* map, const void* base, uint64_t inner, uint64_t mid, uint64_t slabs, uint64_t outer,
                   uint64_t stride_mid, uint64_t stride_outer, uint32_t box_mid, uint32_t box_slabs);
+// Few rows of 8-bit codes against K-major matrices with square scales (gemv_f8.cu);
+// arguments checked, G groups or, offsets null, one of all rows.
+int run_gemv_f8(tcg_input type, int64_t R, int64_t N, int64_t K, int G, const void* A, int64_t lda, const float* SA,
+                int64_t ld_sa, const int32_t* offsets, const void* B, int64_t ldb, int64_t stride_b, const float* SB,
+                int64_t ld_sb, int64_t stride_sb, void* D, tcg_dtype d_type, int64_t ldd, int dev, cudaStream_t s);
 void set_launch_count(int n);
 // A product's call: no launches and no plan yet; then the plan of one that
 // queued work, for tcg_last_plan_string.
 void begin_product();
 void record_zero_plan();
 void record_grouped_plan(int cta_group, int tile_n, int clusters);
+void record_gemv_f8_plan(int rows, int stages, int ctas);
 void record_w4_plan(int rows, int across, int down, int ctas, bool boxes);
 
 }  // namespace tcg

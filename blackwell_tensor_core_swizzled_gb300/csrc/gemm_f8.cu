@@ -1088,6 +1088,10 @@ struct Plan {
   Scaling mode;
 };
 
+// Up to eight rows a group stream the matrices (gemv_f8.cu): 1 x 8192 x 8192 15 us,
+// here 19; 16 x 4096 x 4096 14 (in blocks of 16 rows, one CTA an SM) and 11.
+bool few_rows(int64_t R, int G) { return R <= 8 * static_cast<int64_t>(G); }
+
 Plan choose(int64_t R, int G, bool a_mn, bool square) {
   if (!square) return {variant<2, 256, 5, BOTH>(), BOTH};
   if (!a_mn && R <= 64 * static_cast<int64_t>(G)) return {variant<1, 64, 6, COLUMNS>(), COLUMNS};
@@ -1137,6 +1141,8 @@ int run_dense(tcg_input type, int64_t M, int64_t N, int64_t K, const void* A, tc
   }
   int dev;
   if (int rc = current_device_checked(&dev)) return rc;
+  if (sb_square && !a_mn && !b_mn && few_rows(M, 1))
+    return run_gemv_f8(type, M, N, K, 1, A, lda, SA, ld_sa, nullptr, B, ldb, N * ldb, SB, ld_sb, 0, D, d_type, ldd, dev, s);
   F8Params p;
   std::memset(&p, 0, sizeof p);
   p.G = 1;
@@ -1176,6 +1182,9 @@ int run_grouped(tcg_input type, int64_t R, int64_t N, int64_t K, int G, const vo
   }
   int dev;
   if (int rc = current_device_checked(&dev)) return rc;
+  if (!mn && few_rows(R, G))
+    return run_gemv_f8(type, R, N, K, G, A, lda, SA, ld_sa, offsets, B, ldb, stride_b, SB, ld_sb, stride_sb, D, d_type,
+                       ldd, dev, s);
   F8Params p;
   std::memset(&p, 0, sizeof p);
   p.offsets = offsets;

@@ -225,7 +225,7 @@ __global__ void __launch_bounds__(32 * ROW_WARPS) row_kernel(int64_t R, int64_t 
 // 4096 bf16 took 55 to 67 us).  Four warps share a run of column tiles of one
 // block of rows, whose group each looks up once.
 template <class T, bool WIDE, bool ALIGNED>
-__global__ void __launch_bounds__(32 * COL_WARPS) column_kernel(int64_t R, int64_t C, const T* __restrict__ X,
+__global__ void __launch_bounds__(32 * COL_WARPS, 3) column_kernel(int64_t R, int64_t C, const T* __restrict__ X,
                                                                 int64_t ldx, bool pow2, int G,
                                                                 const int32_t* __restrict__ offsets,
                                                                 uint8_t* __restrict__ Q, int64_t ldq,

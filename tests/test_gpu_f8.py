@@ -55,7 +55,7 @@ def dense(tcg, M, N, K, fmt, a_major, b_major, square, out, pad=0):
     close(to_host(D)[:, :N], am @ bm.T, np.abs(am) @ np.abs(bm).T, tau(K), out, (M, N, K, a_major, b_major, square))
 
 
-SIZES = [(1, 1, 1), (1, 128, 128), (3, 257, 129), (16, 136, 1000), (17, 384, 512), (64, 129, 260), (65, 264, 384),
+SIZES = [(1, 1, 1), (1, 128, 128), (3, 257, 129), (5, 40, 1023), (8, 1000, 3000), (16, 136, 1000), (17, 384, 512), (64, 129, 260), (65, 264, 384),
          (129, 130, 640), (256, 512, 2048), (300, 1000, 1100), (513, 200, 100)]
 
 
@@ -114,6 +114,8 @@ CASES = [
     ([257, 255, 513], 0, 0, 513, 1000, 0),
     ([3] * 40, 1, 1, 384, 192, 0),
     ([1, 2, 4, 8, 16, 31, 32, 48], 0, 0, 1030, 2056, 0),
+    ([20, 0, 1, 0, 0, 9, 0, 0, 2], 2, 3, 40, 1100, 1),
+    ([1] * 1024, 0, 0, 24, 130, 0),
 ]
 
 
@@ -165,3 +167,121 @@ def test_grouped_wgrad(tcg, sizes, before, after, N, K, pad):
             ref[g], S[g] = dy[sl].T @ a[sl], np.abs(dy[sl]).T @ np.abs(a[sl])
         close(to_host(DW)[:, :, :K], ref, S, tau(max(sizes)), out, out)
         assert bool((DW[:, :, K:] == 7.0).all())
+
+
+def test_plans(tcg):
+    """Which kernel a size takes, so that the cases above reach them all."""
+    for M, N, K, square, plan in ((8, 1000, 300, True, "8-bit, blocks of 8"), (9, 1000, 300, True, "tile 128x64"),
+                                  (16, 1000, 2000, True, "cta_group 2, tile 256x64"),
+                                  (16, 1000, 4000, True, "cta_group 4, tile 512x64"),
+                                  (65, 1000, 300, True, "tile 256x256"), (1, 300, 300, False, "tile 256x256")):
+        dense(tcg, M, N, K, "e4m3", "k", "k", square, "f32")
+        assert plan in tcg.last_plan_string(), (M, N, K, tcg.last_plan_string())
+
+
+@pytest.mark.parametrize("bad", [0x7f, 0xff])
+def test_other_groups_values_stay_out(tcg, bad):
+    """NaN codes in one group's rows or matrix reach no other group, nor do they
+    come back through loose rows."""
+    for sizes in ([5, 9, 70, 3], [2, 1, 3, 1]):
+        N, K = 136, 200
+        G, R = len(sizes), sum(sizes) + 4
+        off = group_offsets(sizes, 2)
+        t_off = torch.from_numpy(off).cuda()
+        A, _ = codes((R, K), "e4m3", 1)
+        B, _ = codes((G, N, K), "e4m3", 2)
+        DY, _ = codes((R, N), "e4m3", 3)
+        SA, _ = scales((blocks(K), R), "e4m3", 4)
+        SB, _ = scales((G, blocks(N), blocks(K)), "e4m3", 5)
+        SX, _ = scales((R // BLOCK + G, K), "e4m3", 6)
+        SY, _ = scales((R // BLOCK + G, N), "e4m3", 7)
+        outs = []
+        for poison in (False, True):
+            if poison:
+                A[off[2]:off[3]] = bad
+                A[:2] = A[R - 2:] = bad
+                DY[off[2]:off[3]] = bad
+                DY[:2] = DY[R - 2:] = bad
+                B[2] = bad
+            D = torch.zeros(R, N, device="cuda")
+            tcg.gemm_f8_grouped(tcg.IN_E4M3, R, N, K, G, A, A.shape[1], SA, R, t_off, B, tcg.K_MAJOR, B.shape[2], 0, SB, 0,
+                                0, D, tcg.F32, N)
+            W = torch.zeros(G, N, K, device="cuda")
+            tcg.gemm_f8_grouped_wgrad(tcg.IN_E4M3, R, N, K, G, DY, DY.shape[1], SY, N, A, A.shape[1], SX, K, t_off, W,
+                                      tcg.F32, K, 0)
+            ok(tcg)
+            outs.append((to_host(D), to_host(W)))
+        kept = np.r_[0:off[2], off[3]:R]
+        assert np.array_equal(outs[0][0][kept], outs[1][0][kept])
+        assert np.isnan(outs[1][0][off[2]:off[3]]).all()
+        groups = [0, 1, 3]
+        assert np.array_equal(outs[0][1][groups], outs[1][1][groups])
+        assert np.isnan(outs[1][1][2]).all()
+
+
+def test_gradients_against_differences(tcg):
+    """Codes that are small integers under scales of one: every sum is exact, so
+    the gradients equal differences of L = <DY, grouped(A, B)> exactly."""
+    sizes, N, K = [3, 0, 140, 6], 48, 144
+    G, R = len(sizes), sum(sizes)
+    off = torch.from_numpy(group_offsets(sizes)).cuda()
+    rng = np.random.default_rng(9)
+
+    def ints(*s):
+        return torch.from_numpy(rng.integers(-3, 4, size=s)).float().to(torch.float8_e4m3fn).view(torch.uint8).cuda()
+    A, B, DY = ints(R, K), ints(G, N, K), ints(R, N)
+    one = lambda *s: torch.ones(*s, device="cuda")  # noqa: E731
+    dy = DY.view(torch.float8_e4m3fn).double()
+
+    def loss(a, b):
+        D = torch.empty(R, N, device="cuda")
+        tcg.gemm_f8_grouped(tcg.IN_E4M3, R, N, K, G, a, K, one(blocks(K), R), R, off, b, tcg.K_MAJOR, K, 0,
+                            one(G, blocks(N), blocks(K)), 0, 0, D, tcg.F32, N)
+        return float((D.double() * dy).sum())
+    DA = torch.empty(R, K, device="cuda")
+    tcg.gemm_f8_grouped(tcg.IN_E4M3, R, K, N, G, DY, N, one(blocks(N), R), R, off, B, tcg.MN_MAJOR, K, N * K,
+                        one(G, blocks(N), blocks(K)), 0, 0, DA, tcg.F32, K)
+    DW = torch.empty(G, N, K, device="cuda")
+    tcg.gemm_f8_grouped_wgrad(tcg.IN_E4M3, R, N, K, G, DY, N, one(R // BLOCK + G, N), N, A, K, one(R // BLOCK + G, K), K,
+                              off, DW, tcg.F32, K, N * K)
+    ok(tcg)
+    base = loss(A, B)
+
+    def up(t, *i):
+        c = t.clone()
+        v = c.view(torch.float8_e4m3fn)[i].float() + 1
+        c[i] = v.to(torch.float8_e4m3fn).view(torch.uint8)
+        return c
+    for i in range(0, R, 7):
+        k = 7 * i % K
+        assert loss(up(A, i, k), B) - base == float(DA[i, k])
+    for g in range(G):
+        for n in (0, 17, N - 1):
+            k = (n + 5 * g) % K
+            assert loss(A, up(B, g, n, k)) - base == float(DW[g, n, k])
+
+
+def test_captured_on_two_streams(tcg):
+    """Two graphs on two streams, replayed together: nothing is shared."""
+    graphs = []
+    for M, N, K, seed in ((4, 2048, 2048, 1), (300, 512, 1024, 2), (16, 512, 4096, 3)):
+        A, a = codes((M, K), "e4m3", seed)
+        B, b = codes((N, K), "e4m3", seed + 10)
+        SA, sa = scales((blocks(K), M), "e4m3", seed + 20)
+        SB, sb = scales((blocks(N), blocks(K)), "e4m3", seed + 30, K ** -0.5)
+        D = torch.zeros(M, N, device="cuda")
+        side, graph = torch.cuda.Stream(), torch.cuda.CUDAGraph()
+        side.wait_stream(torch.cuda.current_stream())
+        with torch.cuda.graph(graph, stream=side):
+            tcg.gemm_f8(tcg.IN_E4M3, M, N, K, A, tcg.K_MAJOR, K, SA, M, B, tcg.K_MAJOR, K, SB, blocks(K), True, D, tcg.F32,
+                        N)
+        am, bm = a * along(sa, K).T, b * spread(sb, N, K)
+        graphs.append((graph, side, D, am @ bm.T, np.abs(am) @ np.abs(bm).T, K, (A, B, SA, SB)))
+    for _ in range(5):
+        for graph, side, *_ in graphs:
+            with torch.cuda.stream(side):
+                graph.replay()
+    torch.cuda.synchronize()
+    ok(tcg)
+    for _, _, D, ref, S, K, _ in graphs:
+        close(to_host(D), ref, S, tau(K), "f32")
