@@ -717,6 +717,24 @@ __global__ void __launch_bounds__(F8Cfg<CG, BN, STAGES, MODE>::THREADS, 1) f8_ke
           const int n0 = t.c0 + c_warp + 32 * i;
           const bool boxed = p.d_tma && rows == 32;  // columns clip at the map's end, a group's rows do not
           uint8_t* dst = static_cast<uint8_t*>(p.D) + (static_cast<int64_t>(row0) * p.ldd + n0 + lane) * p.d_size;
+          if (p.d_tma && !boxed) {
+            // a group's last rows: each lane its own, in 16-byte words
+            uint8_t* own = static_cast<uint8_t*>(p.D) + (static_cast<int64_t>(row0 + lane) * p.ldd + n0) * p.d_size;
+#pragma unroll
+            for (int j = 0; j < 8; ++j) {
+              uint32_t w[4];
+              unpair(sum[i][2 * j], w[0], w[1]);
+              unpair(sum[i][2 * j + 1], w[2], w[3]);
+              if (lane >= rows || n0 + 4 * j >= p.M) continue;
+              if (p.d_type == OUT_F32)
+                *reinterpret_cast<uint4*>(own + 16 * j) = make_uint4(w[0], w[1], w[2], w[3]);
+              else if (p.d_type == OUT_BF16)
+                *reinterpret_cast<uint2*>(own + 8 * j) = make_uint2(pack_bf16(w[0], w[1]), pack_bf16(w[2], w[3]));
+              else
+                *reinterpret_cast<uint2*>(own + 8 * j) = make_uint2(pack_f16(w[0], w[1]), pack_f16(w[2], w[3]));
+            }
+            continue;
+          }
           if (p.d_type == OUT_F32) {
             // two staging tiles of 16 rows
             if (lane == 0) bulk_wait_group_read<0>();
@@ -1088,9 +1106,13 @@ struct Plan {
   Scaling mode;
 };
 
-// Up to eight rows a group stream the matrices (gemv_f8.cu): 1 x 8192 x 8192 15 us,
-// here 19; 16 x 4096 x 4096 14 (in blocks of 16 rows, one CTA an SM) and 11.
-bool few_rows(int64_t R, int G) { return R <= 8 * static_cast<int64_t>(G); }
+// Up to two rows a group stream the matrices (gemv_f8.cu), and up to eight where
+// these have less than 64 MB: 1 x 8192 x 8192 15 us and, here, 19; 64 rows over 32
+// groups of 2048 x 2048 28.5 and 27.7; 8 x 4096 x 4096 8.2 and 11.1, 8 x 8192 x 8192
+// 22 and 19.7, 16 x 4096 x 4096 12.0 and 11.3; 128 rows over 32 groups 36 and 32.
+bool few_rows(int64_t R, int G, int64_t N, int64_t K) {
+  return R <= 2 * static_cast<int64_t>(G) || (R <= 8 * static_cast<int64_t>(G) && N * K < (int64_t{1} << 26) / G);
+}
 
 Plan choose(int64_t R, int G, bool a_mn, bool square) {
   if (!square) return {variant<2, 256, 5, BOTH>(), BOTH};
@@ -1141,7 +1163,7 @@ int run_dense(tcg_input type, int64_t M, int64_t N, int64_t K, const void* A, tc
   }
   int dev;
   if (int rc = current_device_checked(&dev)) return rc;
-  if (sb_square && !a_mn && !b_mn && few_rows(M, 1))
+  if (sb_square && !a_mn && !b_mn && few_rows(M, 1, N, K))
     return run_gemv_f8(type, M, N, K, 1, A, lda, SA, ld_sa, nullptr, B, ldb, N * ldb, SB, ld_sb, 0, D, d_type, ldd, dev, s);
   F8Params p;
   std::memset(&p, 0, sizeof p);
@@ -1182,7 +1204,7 @@ int run_grouped(tcg_input type, int64_t R, int64_t N, int64_t K, int G, const vo
   }
   int dev;
   if (int rc = current_device_checked(&dev)) return rc;
-  if (!mn && few_rows(R, G))
+  if (!mn && few_rows(R, G, N, K))
     return run_gemv_f8(type, R, N, K, G, A, lda, SA, ld_sa, offsets, B, ldb, stride_b, SB, ld_sb, stride_sb, D, d_type,
                        ldd, dev, s);
   F8Params p;
