@@ -11,7 +11,8 @@
 // Every CTA finds the chosen experts by itself (a token mask for each), so no
 // kernel sorts.  A unit is 16 rows: of one expert's W1 and W3, or of y, whose
 // CTA then passes through all experts, so that sums over experts need neither
-// atomics nor memory.  A producer thread brings the rows in stages of 1 KB of
+// atomics nor memory.  Eight tokens of an expert at a time: further ones pass over
+// its rows again, which then come from L2.  A producer thread brings the rows in stages of 1 KB of
 // each (eight 128-byte slabs of 16 rows, one copy) into a ring, across units; each
 // of eight warps takes one slab, decodes it in registers and multiplies it with
 // mma.m16n8k16, tokens on the 8 columns: the tensor cores are idle most of the
@@ -79,12 +80,17 @@ struct FewParams {
   uint64_t timeout_ns;
 };
 
+// What one pass over an expert's rows is for: up to eight of its tokens.
+struct Job {
+  int expert, first, tokens, block;  // first: its first pair; block: of the expert's tokens, by eights
+};
+
 // Shared memory from the sizes: ring stages of weights, then of x and scales,
 // then lists.
 struct Layout {
   int stage;               // bytes of a stage's weights
   int x_row, x_part, x_stage;  // of x: a column, hi or lo of all columns, a stage with its scales
-  int x, sums, masks, list, base, token, weight, bars, bytes;
+  int x, sums, masks, list, jobs, token, weight, bars, bytes;
   __host__ __device__ Layout(int T, int topk, int E, bool second, int size, int matrices, int stages) {
     const int pairs = T * topk, most = pairs < E ? pairs : E;
     stage = TILE_BYTES * matrices;
@@ -101,7 +107,7 @@ struct Layout {
     sums = take(second ? WARPS * T * 16 * 4 : WARPS * 2 * 8 * 17 * 4);
     masks = take(8 * E);
     list = take(4 * most);
-    base = take(4 * (most + 1));
+    jobs = take(16 * (most + pairs / 8));
     token = take(pairs);
     weight = take(second ? 0 : 4 * pairs);
     bars = take(2 * MAX_STAGES * 8 + 8 * 4 + 16);
@@ -191,10 +197,11 @@ __device__ __forceinline__ bool workers_agree(bool ok) {
 
 // -------------------------------------------------------------------- kernels
 
-// NT: 8-token columns.  W8: weights are E4M3 with scales, else of x's type.
-// SECOND: W2 and the sum over experts, else W1, W3 and the activation.
-template <bool BF16, bool W8, int NT, bool SECOND>
-__global__ void __launch_bounds__(FEW_THREADS, NT == 1 ? 2 : 1) few_kernel(const __grid_constant__ FewParams p) {
+// W8: weights are E4M3 with scales, else of x's type.  SECOND: W2 and the sum over
+// experts, else W1, W3 and the activation.  DIRECT (SECOND, up to eight tokens):
+// columns are tokens, whatever the expert, so that the sums stay in registers.
+template <bool BF16, bool W8, bool SECOND, bool DIRECT>
+__global__ void __launch_bounds__(FEW_THREADS, 2) few_kernel(const __grid_constant__ FewParams p) {
   extern __shared__ uint8_t smem_raw[];
   const uint32_t raw = smem_u32(smem_raw);
   const uint32_t sbase = (raw + 1023u) & ~1023u;
@@ -203,7 +210,7 @@ __global__ void __launch_bounds__(FEW_THREADS, NT == 1 ? 2 : 1) few_kernel(const
   const int stage_bytes = at.stage, stages = p.stages;
   unsigned long long* masks = reinterpret_cast<unsigned long long*>(gbase + at.masks);
   int* list = reinterpret_cast<int*>(gbase + at.list);   // the chosen experts
-  int* base = reinterpret_cast<int*>(gbase + at.base);   // their first pair
+  Job* job = reinterpret_cast<Job*>(gbase + at.jobs);
   uint8_t* token = gbase + at.token;                     // a pair's token
   float* weight = reinterpret_cast<float*>(gbase + at.weight);
   float* sums = reinterpret_cast<float*>(gbase + at.sums);
@@ -268,11 +275,34 @@ __global__ void __launch_bounds__(FEW_THREADS, NT == 1 ? 2 : 1) few_kernel(const
     chosen += counts[w];
   }
   __syncthreads();
+  // the pairs (experts rising, their tokens rising) and the jobs
+  int* job_count = counts + 7;
+  if (warp == 0) {
+    int pairs_run = 0, jobs_run = 0;
+    for (int a0 = 0; a0 < chosen; a0 += 32) {
+      const int e = a0 + lane < chosen ? list[a0 + lane] : -1;
+      const int n = e >= 0 ? __popcll(masks[e]) : 0, blocks = (n + 7) / 8;
+      int pairs_to = n, jobs_to = blocks;
+#pragma unroll
+      for (int d = 1; d < 32; d <<= 1) {
+        const int o = __shfl_up_sync(0xffffffffu, pairs_to, d), q = __shfl_up_sync(0xffffffffu, jobs_to, d);
+        if (lane >= d) pairs_to += o, jobs_to += q;
+      }
+      for (int i = 0; i < blocks; ++i)
+        job[jobs_run + jobs_to - blocks + i] = {e, pairs_run + pairs_to - n + 8 * i, min(8, n - 8 * i), i};
+      pairs_run += __shfl_sync(0xffffffffu, pairs_to, 31);
+      jobs_run += __shfl_sync(0xffffffffu, jobs_to, 31);
+    }
+    __syncwarp();
+    if (lane == 0) *job_count = jobs_run;
+  }
+  __syncthreads();
+  const int jobs = *job_count;
 
   const int tiles = (p.N + 15) / 16;
-  const int units = SECOND ? tiles : chosen * tiles;
+  const int units = SECOND ? tiles : jobs * tiles;
   const int chunks = (p.row_bytes + CHUNK - 1) / CHUNK;
-  const int passes = SECOND ? chosen : 1;  // experts of a unit
+  const int passes = SECOND ? jobs : 1;  // over rows, of a unit
   // slabs of chunk c that exist
   auto slabs_of = [&](int c) { return min(WARPS, (p.row_bytes - c * CHUNK + 127) / 128); };
 
@@ -283,7 +313,7 @@ __global__ void __launch_bounds__(FEW_THREADS, NT == 1 ? 2 : 1) few_kernel(const
     for (int u = blockIdx.x; u < units && ok; u += gridDim.x) {
       const int n0 = (SECOND ? u : u % tiles) * 16;
       for (int i = 0; i < passes && ok; ++i) {
-        const int e = list[SECOND ? i : u / tiles];
+        const int e = job[SECOND ? i : u / tiles].expert;
         for (int c = 0; c < chunks; ++c) {
           if (!wait_inline(empty_bar(s), ph ^ 1u, wctx, SITE_PROD_EMPTY)) {
             ok = false;
@@ -325,39 +355,24 @@ __global__ void __launch_bounds__(FEW_THREADS, NT == 1 ? 2 : 1) few_kernel(const
   }
 
 
-  // the pairs: experts in the list's order, their tokens rising
-  if (warp == 0) {
-    int run = 0;
-    for (int a0 = 0; a0 < chosen; a0 += 32) {
-      int n = a0 + lane < chosen ? __popcll(masks[list[a0 + lane]]) : 0, incl = n;
-#pragma unroll
-      for (int d = 1; d < 32; d <<= 1) {
-        const int o = __shfl_up_sync(0xffffffffu, incl, d);
-        if (lane >= d) incl += o;
-      }
-      if (a0 + lane < chosen) base[a0 + lane] = run + incl - n;
-      run += __shfl_sync(0xffffffffu, incl, 31);
-    }
-    if (lane == 0) base[chosen] = run;
-  }
-  consumers_sync();
-  for (int a = warp < WARPS ? warp : chosen; a < chosen; a += WARPS) {
-    const unsigned long long mask = masks[list[a]];
-    for (int t = lane; t < p.T; t += 32)
-      if (mask >> t & 1) {
-        const int pair = base[a] + __popcll(mask & ((1ull << t) - 1));
-        token[pair] = static_cast<uint8_t>(t);
+  // the pairs' tokens and weights
+  for (int j = warp < WARPS ? warp : jobs; j < jobs; j += WARPS) {
+    const Job a = job[j];
+    const unsigned long long mask = masks[a.expert];
+    for (int t = lane; t < p.T; t += 32) {
+      const int rank = __popcll(mask & ((1ull << t) - 1)) - 8 * a.block;
+      if ((mask >> t & 1) && rank >= 0 && rank < 8) {
+        token[a.first + rank] = static_cast<uint8_t>(t);
         if constexpr (!SECOND) {
           float w = 0.0f;  // a token that names an expert twice gets it with both weights
-          for (int j = 0; j < p.topk; ++j)
-            if (p.expert[t * p.topk + j] == list[a]) w += p.weight ? p.weight[t * p.topk + j] : 1.0f;
-          weight[pair] = w;
+          for (int i = 0; i < p.topk; ++i)
+            if (p.expert[t * p.topk + i] == a.expert) w += p.weight ? p.weight[t * p.topk + i] : 1.0f;
+          weight[a.first + rank] = w;
         }
       }
+    }
   }
   consumers_sync();
-  // few tokens: columns are tokens, whatever the expert, so that W2's sums stay in place
-  constexpr bool DIRECT = SECOND && NT == 1;
   constexpr int SIZE = W8 ? 1 : 2;
   constexpr int CODES = 16 / SIZE;         // weights of 16 bytes
   constexpr int WORDS = CODES / 2;         // of x against them
@@ -367,31 +382,20 @@ __global__ void __launch_bounds__(FEW_THREADS, NT == 1 ? 2 : 1) few_kernel(const
     griddep_wait();
     griddep_launch_dependents();
   }
-  // the row of column `col` of expert list[a] (-1: no such token)
-  auto row_of = [&](int a, int col) {
-    const int first = base[a];
-    if constexpr (DIRECT) {
-      const uint32_t mask = static_cast<uint32_t>(masks[list[a]]);
-      return mask >> col & 1 ? first + __popc(mask & ((1u << col) - 1u)) : -1;
-    }
-    if (col >= base[a + 1] - first) return -1;
-    return SECOND ? first + col : static_cast<int>(token[first + col]);
-  };
-
   if (warp == WARPS + 1) {
     // ------------------------------------------- producer of x and of scales:
-    // a stage's x of the first eight tokens' columns and its scales come as far
+    // a stage's x of the job's tokens and its scales come as far
     // ahead as its weights (loaded by the workers, a stage ahead or at once,
     // their latency under HBM's load was half of all time)
     uint32_t s = 0, ph = 0;
     for (int u = blockIdx.x; u < units; u += gridDim.x) {
       const int n0 = (SECOND ? u : u % tiles) * 16;
       for (int i = 0; i < passes; ++i) {
-        const int a = SECOND ? i : u / tiles;
-        const int64_t scale_at = list[a] * p.stride_s + (n0 / BLOCK) * p.ld_s;
-        // the lanes share out the expert's first 1, 2, 4 or 8 tokens (one warp takes
-        // 2000 cycles a stage if it passes over eight columns one by one)
-        const int first = base[a], tokens = base[a + 1] - first;
+        const Job a = job[SECOND ? i : u / tiles];
+        const int64_t scale_at = a.expert * p.stride_s + (n0 / BLOCK) * p.ld_s;
+        // the lanes share out 1, 2, 4 or 8 tokens (one warp takes 2000 cycles a stage
+        // if it passes over eight columns one by one)
+        const int first = a.first, tokens = a.tokens;
         const int shift = tokens > 4 ? 2 : tokens > 2 ? 3 : tokens > 1 ? 4 : 5;  // log2 of a token's lanes
         const int index = lane >> shift, piece = lane & ((1 << shift) - 1);
         const bool exists = index < tokens;
@@ -434,17 +438,13 @@ __global__ void __launch_bounds__(FEW_THREADS, NT == 1 ? 2 : 1) few_kernel(const
   // ----------------------------------------------------------------- workers
   const int g = lane >> 2, c4 = lane & 3;
   uint32_t s = 0, ph = 0;
-  float acc[M][NT][4];
+  float acc[M][4];
   bool ok = true;
-  struct X {  // what this lane has of one column's x, against 16 weight bytes
-    uint4 v[PARTS][WORDS / 4];
-  };
-  // This warp's share of expert list[a]: adds to acc.
-  auto multiply = [&](int a) {
-    const int tokens = DIRECT ? 8 : base[a + 1] - base[a];
+  // This warp's share of a job: adds to acc.
+  auto multiply = [&](const Job& a) {
     // DIRECT: which of this lane's sums (columns 2 c4, + 1) belong to the expert's
     // tokens; the others' columns hold anything
-    const uint32_t columns = DIRECT ? 5u * (static_cast<uint32_t>(masks[list[a]]) >> (2 * c4) & 3u) : 15u;
+    const uint32_t columns = DIRECT ? 5u * (static_cast<uint32_t>(masks[a.expert]) >> (2 * c4) & 3u) : 15u;
     for (int c = 0; c < chunks; ++c) {
       if (!wait_inline(full_bar(s), ph, wctx, SITE_MMA_FULL)) {
         ok = false;
@@ -460,12 +460,12 @@ __global__ void __launch_bounds__(FEW_THREADS, NT == 1 ? 2 : 1) few_kernel(const
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
           const int k = warp * (128 / SIZE) + CODES * (c4 + 4 * h);  // of the stage
-          X now;
+          uint4 x[PARTS][WORDS / 4];
 #pragma unroll
           for (int q = 0; q < PARTS; ++q)
 #pragma unroll
             for (int v = 0; v < WORDS / 4; ++v)
-              now.v[q][v] = ld_shared_v4(xs + q * at.x_part + min(g, p.T - 1) * at.x_row + 2u * k + 16u * v);
+              x[q][v] = ld_shared_v4(xs + q * at.x_part + min(g, p.T - 1) * at.x_row + 2u * k + 16u * v);
           uint32_t A[M][CODES / 4][4];  // fragments of this lane's 16-byte chunk of rows g and g + 8
 #pragma unroll
           for (int m = 0; m < M; ++m) {
@@ -484,42 +484,23 @@ __global__ void __launch_bounds__(FEW_THREADS, NT == 1 ? 2 : 1) few_kernel(const
               }
             }
           }
+          float part[M][4] = {};
 #pragma unroll
-          for (int j = 0; j < NT; ++j) {
-            if (8 * j >= tokens) break;
-            X then = now;
-            if (j + 1 < NT && 8 * (j + 1) < tokens) {
-              // further columns of tokens: from memory
-              const int row = row_of(a, 8 * (j + 1) + g), kk = c * (CHUNK / SIZE) + k;
-              const uint16_t* from = (SECOND ? p.hi : p.X) + row * p.ldx + kk;
+          for (int q = 0; q < PARTS; ++q) {
+            const uint32_t* w = reinterpret_cast<const uint32_t*>(&x[q][0]);
 #pragma unroll
-              for (int q = 0; q < PARTS; ++q)
-#pragma unroll
-                for (int v = 0; v < WORDS / 4; ++v)
-                  then.v[q][v] = row >= 0 && kk < p.K ? reinterpret_cast<const uint4*>(from + (q ? p.lo_at : 0))[v]
-                                                      : make_uint4(0, 0, 0, 0);
-            }
-            float part[M][4] = {};
-#pragma unroll
-            for (int q = 0; q < PARTS; ++q) {
-              const uint32_t* w = reinterpret_cast<const uint32_t*>(&now.v[q][0]);
-#pragma unroll
-              for (int i = 0; i < CODES / 4; ++i) {
-#pragma unroll
-                for (int m = 0; m < M; ++m)
-                  if (m < p.matrices)
-                    mma_16816<BF16>(W8 || DIRECT ? part[m] : acc[m][j], A[m][i], w[2 * i], w[2 * i + 1]);
-              }
-            }
-            if constexpr (W8 || DIRECT) {
+            for (int i = 0; i < CODES / 4; ++i) {
 #pragma unroll
               for (int m = 0; m < M; ++m)
-#pragma unroll
-                for (int i = 0; i < 4; ++i)
-                  if (!DIRECT || (columns >> i & 1))
-                    acc[m][j][i] = W8 ? fmaf(part[m][i], sc[m], acc[m][j][i]) : acc[m][j][i] + part[m][i];
+                if (m < p.matrices) mma_16816<BF16>(W8 || DIRECT ? part[m] : acc[m], A[m][i], w[2 * i], w[2 * i + 1]);
             }
-            now = then;
+          }
+          if constexpr (W8 || DIRECT) {
+#pragma unroll
+            for (int m = 0; m < M; ++m)
+#pragma unroll
+              for (int i = 0; i < 4; ++i)
+                if (!DIRECT || (columns >> i & 1)) acc[m][i] = W8 ? fmaf(part[m][i], sc[m], acc[m][i]) : acc[m][i] + part[m][i];
           }
         }
       }
@@ -535,77 +516,66 @@ __global__ void __launch_bounds__(FEW_THREADS, NT == 1 ? 2 : 1) few_kernel(const
 #pragma unroll
     for (int m = 0; m < M; ++m)
 #pragma unroll
-      for (int j = 0; j < NT; ++j)
-#pragma unroll
-        for (int i = 0; i < 4; ++i) acc[m][j][i] = 0.0f;
+      for (int i = 0; i < 4; ++i) acc[m][i] = 0.0f;
   };
 
   if constexpr (!SECOND) {
     for (int u = blockIdx.x; u < units; u += gridDim.x) {
-      const int a = u / tiles, n0 = (u % tiles) * 16;
-      const int first = base[a], tokens = base[a + 1] - first;
+      const Job a = job[u / tiles];
+      const int n0 = (u % tiles) * 16;
       clear();
       multiply(a);
       if (!workers_agree(ok)) return;
+      // [warp][matrix][column][row]
 #pragma unroll
-      for (int j = 0; j < NT; ++j) {
-        if (8 * j >= tokens) break;
-        // [warp][matrix][column][row]
+      for (int m = 0; m < 2; ++m)
 #pragma unroll
-        for (int m = 0; m < 2; ++m)
+        for (int i = 0; i < 4; ++i) sums[((warp * 2 + m) * 8 + 2 * c4 + (i & 1)) * 17 + g + 8 * (i >> 1)] = acc[m][i];
+      workers_sync();
+      const int row = threadIdx.x & 15, col = threadIdx.x >> 4;
+      if (col < a.tokens && n0 + row < p.N) {
+        float v[2] = {};
 #pragma unroll
-          for (int i = 0; i < 4; ++i)
-            sums[((warp * 2 + m) * 8 + 2 * c4 + (i & 1)) * 17 + g + 8 * (i >> 1)] = acc[m][j][i];
-        workers_sync();
-        const int row = threadIdx.x & 15, col = threadIdx.x >> 4;
-        if (col < 8 && 8 * j + col < tokens && n0 + row < p.N) {
-          float v[2] = {};
+        for (int w = 0; w < WARPS; ++w)
 #pragma unroll
-          for (int w = 0; w < WARPS; ++w)
-#pragma unroll
-            for (int m = 0; m < 2; ++m) v[m] += sums[((w * 2 + m) * 8 + col) * 17 + row];
-          const int pair = first + 8 * j + col;
-          const float silu = v[0] / (1.0f + expf(-v[0]));
-          const float h = (p.matrices > 1 ? silu * v[1] : silu) * weight[pair];
-          const uint16_t hi = round16<BF16>(h);
-          const float rest = h - to_f32<BF16>(hi);
-          const int64_t to = pair * p.ldh + n0 + row;
-          p.hi[to] = hi;
-          p.lo[to] = isfinite(rest) ? round16<BF16>(rest) : static_cast<uint16_t>(0);
-        }
-        workers_sync();
+          for (int m = 0; m < 2; ++m) v[m] += sums[((w * 2 + m) * 8 + col) * 17 + row];
+        const int pair = a.first + col;
+        const float silu = v[0] / (1.0f + expf(-v[0]));
+        const float h = (p.matrices > 1 ? silu * v[1] : silu) * weight[pair];
+        const uint16_t hi = round16<BF16>(h);
+        const float rest = h - to_f32<BF16>(hi);
+        const int64_t to = pair * p.ldh + n0 + row;
+        p.hi[to] = hi;
+        p.lo[to] = isfinite(rest) ? round16<BF16>(rest) : static_cast<uint16_t>(0);
       }
+      workers_sync();
     }
   } else {
     float* mine = sums + warp * p.T * 16;
     for (int u = blockIdx.x; u < units; u += gridDim.x) {
       const int n0 = u * 16;
+      clear();
       if constexpr (DIRECT) {
-        clear();
-        for (int a = 0; a < chosen && ok; ++a) multiply(a);
+        for (int j = 0; j < jobs && ok; ++j) multiply(job[j]);
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
           const int t = 2 * c4 + (i & 1);
-          if (t < p.T) mine[t * 16 + g + 8 * (i >> 1)] = acc[0][0][i];
+          if (t < p.T) mine[t * 16 + g + 8 * (i >> 1)] = acc[0][i];
         }
       } else {
         for (int i = lane; i < p.T * 16; i += 32) mine[i] = 0.0f;
         __syncwarp();
-      }
-      for (int a = 0; a < chosen && ok && !DIRECT; ++a) {
-        const int first = base[a], tokens = base[a + 1] - first;
-        clear();
-        multiply(a);
-#pragma unroll
-        for (int j = 0; j < NT; ++j) {
-          if (8 * j >= tokens) break;
+        for (int j = 0; j < jobs && ok; ++j) {
+          const Job a = job[j];
+          multiply(a);
 #pragma unroll
           for (int i = 0; i < 4; ++i) {
-            const int col = 8 * j + 2 * c4 + (i & 1);
-            if (col < tokens) mine[token[first + col] * 16 + g + 8 * (i >> 1)] += acc[0][j][i];
+            const int col = 2 * c4 + (i & 1);
+            if (col < a.tokens) mine[token[a.first + col] * 16 + g + 8 * (i >> 1)] += acc[0][i];
           }
+          clear();
+          __syncwarp();
         }
-        __syncwarp();
       }
       if (!workers_agree(ok)) return;
       for (int i = threadIdx.x; i < p.T * 16; i += 32 * WARPS) {
@@ -631,28 +601,25 @@ __global__ void __launch_bounds__(FEW_THREADS, NT == 1 ? 2 : 1) few_kernel(const
 using Kernel = void (*)(const FewParams);
 OncePerDevice<cudaError_t> g_setup;
 
-template <bool BF16, bool W8, bool SECOND>
-Kernel by_tokens(int T) {
-  return T <= 8    ? few_kernel<BF16, W8, 1, SECOND>
-         : T <= 16 ? few_kernel<BF16, W8, 2, SECOND>
-         : T <= 32 ? few_kernel<BF16, W8, 4, SECOND>
-                   : few_kernel<BF16, W8, 8, SECOND>;
+template <bool BF16, bool W8>
+Kernel pick(bool second, int T) {
+  return !second ? few_kernel<BF16, W8, false, false>
+         : T <= 8 ? few_kernel<BF16, W8, true, true>
+                  : few_kernel<BF16, W8, true, false>;
 }
 
-template <bool SECOND>
-Kernel pick(bool bf16, bool w8, int T) {
-  if (bf16) return w8 ? by_tokens<true, true, SECOND>(T) : by_tokens<true, false, SECOND>(T);
-  return w8 ? by_tokens<false, true, SECOND>(T) : by_tokens<false, false, SECOND>(T);
+Kernel pick(bool second, bool bf16, bool w8, int T) {
+  if (bf16) return w8 ? pick<true, true>(second, T) : pick<true, false>(second, T);
+  return w8 ? pick<false, true>(second, T) : pick<false, false>(second, T);
 }
 
 cudaError_t setup(int dev) {
   return g_setup(dev, [] {
     for (int i = 0; i < 4; ++i)
-      for (int T : {8, 16, 32, 64})
-        for (Kernel k : {pick<false>(i & 1, i & 2, T), pick<true>(i & 1, i & 2, T)}) {
-          const cudaError_t e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, MAX_SMEM);
-          if (e != cudaSuccess) return e;
-        }
+      for (Kernel k : {pick(false, i & 1, i & 2, 1), pick(true, i & 1, i & 2, 1), pick(true, i & 1, i & 2, MAX_TOKENS)}) {
+        const cudaError_t e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, MAX_SMEM);
+        if (e != cudaSuccess) return e;
+      }
     return cudaSuccess;
   });
 }
@@ -701,11 +668,12 @@ struct Shape {
   int stages, smem, ctas;
 };
 
-// Two CTAs share an SM where half its memory holds 64 KB of weights and more
-// (up to eight tokens): twice the warps hide their latencies (1 token x 8 of 128
-// experts of 4096 x 1024, E4M3: 30 us, 43 with one).  Else one has what fits.
+// Two CTAs share an SM where half its memory holds 32 KB of weights and more: twice
+// the warps hide their latencies (1 token x 8 of 128 experts of 4096 x 1024, E4M3:
+// 30 us, 43 with one; 32 tokens x 4 of 32 f16 experts of 4096 x 2048 263 and 321).
+// Else one has what fits.
 Shape shape(int T, int topk, int E, bool second, int size, int matrices) {
-  for (int n = MAX_STAGES / matrices; T <= 8 && n * matrices >= 4; --n) {
+  for (int n = MAX_STAGES / matrices; n * matrices >= 2; --n) {
     const int bytes = Layout(T, topk, E, second, size, matrices, n).bytes;
     if (bytes <= MAX_SMEM / 2 - 1024) return {n, bytes, 2};
   }
@@ -790,11 +758,11 @@ int run_few(const tcg_moe_few_args* args, cudaStream_t s) {
     p.ld_s = a.ld_s1;
     p.stride_s = a.stride_s1;
     if (int rc = weight_maps(&q, 0, a.W2, a.I * size, a.H, a.ld2 * size, a.stride2 * size)) return rc;
-    const int64_t units = std::min<int64_t>(a.E, pairs) * ceil_div(a.I, 16);
+    const int64_t units = std::min<int64_t>(a.E + pairs / 8, pairs) * ceil_div(a.I, 16);
     if (units > INT32_MAX) return TCG_ERR_UNSUPPORTED;
     const Shape h = shape(T, a.topk, a.E, false, size, p.matrices);
     p.stages = h.stages;
-    if (int rc = launch(pick<false>(bf16, w8, T), p, std::min<int64_t>(units, h.ctas * sms), h.smem, s)) return rc;
+    if (int rc = launch(pick(false, bf16, w8, T), p, std::min<int64_t>(units, h.ctas * sms), h.smem, s)) return rc;
     ++launches;
   }
   q.K = static_cast<int>(a.I);
@@ -810,7 +778,7 @@ int run_few(const tcg_moe_few_args* args, cudaStream_t s) {
   q.Y = a.Y;
   q.ldy = a.ldy;
   q.y_type = a.y_type;
-  if (int rc = launch(pick<true>(bf16, w8, T), q, std::min<int64_t>(ceil_div(a.H, 16), h.ctas * sms), h.smem, s)) return rc;
+  if (int rc = launch(pick(true, bf16, w8, T), q, std::min<int64_t>(ceil_div(a.H, 16), h.ctas * sms), h.smem, s)) return rc;
   set_launch_count(launches + 1);
   return TCG_OK;
 }
