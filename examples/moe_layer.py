@@ -1,5 +1,6 @@
-"""A mixture-of-experts layer: a training step forward and back, and decoding
-with 4-bit experts.
+"""A mixture-of-experts layer: a training step forward and back, in 16 bits and in
+8 bits with a scale for each block of 128, and decoding with 4-bit and with 8-bit
+experts.
 
     y[t] = sum_j p[t, j] W2[e] silu(W1[e] x[t]),   e = expert[t, j]
 
@@ -140,6 +141,82 @@ class MoeDecoder:
         return route.combine(self.product(route, torch.nn.functional.silu(h), self.w2), weight)
 
 
+class Codes:
+    """A matrix (or one for each expert) in 8 bits and its scales for each block of 128."""
+
+    def __init__(self, x: torch.Tensor, blocks: int, route: Route | None = None):
+        R, C = x.shape
+        groups = 1 if route is None else route.experts
+        shape = {tcg.F8_ROW: (-(-C // 128), R), tcg.F8_COLUMN: (R // 128 + groups if route else -(-R // 128), C),
+                 tcg.F8_SQUARE: (-(-R // 128), -(-C // 128))}[blocks]
+        self.q = torch.empty(R, C, dtype=torch.float8_e4m3fn, device=x.device)
+        self.scale = torch.empty(shape, device=x.device)
+        tcg.f8_quantize(tcg.IN_E4M3, blocks, R, C, OUT[x.dtype], x, x.stride(0), self.q, C, self.scale, shape[1],
+                        groups=groups, offsets=None if route is None else route.offsets)
+
+    @classmethod
+    def of_experts(cls, w: torch.Tensor) -> "Codes":
+        """w [E, N, K] with square blocks (N a multiple of 128: blocks end with the experts)."""
+        E, N, K = w.shape
+        c = cls(w.view(E * N, K), tcg.F8_SQUARE)
+        c.q, c.scale = c.q.view(E, N, K), c.scale.view(E, N // 128, -1)
+        return c
+
+
+class MoeLayer8:
+    """The layer with its products in 8 bits: of the experts, quantised once, and of
+    the rows and their gradients, as they come."""
+
+    def __init__(self, layer: MoeLayer):
+        self.layer, self.w1, self.w2 = layer, Codes.of_experts(layer.w1), Codes.of_experts(layer.w2)
+
+    def product(self, route: Route, rows: torch.Tensor, w: Codes, transposed: bool = False) -> torch.Tensor:
+        a = Codes(rows, tcg.F8_ROW)
+        E, n, k = w.q.shape
+        if transposed:
+            n, k = k, n
+        out = rows.new_empty(rows.shape[0], n)
+        tcg.gemm_f8_grouped(tcg.IN_E4M3, rows.shape[0], n, k, E, a.q, k, a.scale, rows.shape[0], route.offsets, w.q,
+                            tcg.MN_MAJOR if transposed else tcg.K_MAJOR, w.q.stride(1), w.q.stride(0), w.scale,
+                            w.scale.stride(1), w.scale.stride(0), out, OUT[out.dtype], n)
+        return out
+
+    def matrix_grad(self, route: Route, dout: torch.Tensor, rows: torch.Tensor) -> torch.Tensor:
+        d, a = Codes(dout, tcg.F8_COLUMN, route), Codes(rows, tcg.F8_COLUMN, route)
+        n, k = dout.shape[1], rows.shape[1]
+        dw = torch.empty(route.experts, n, k, dtype=torch.float32, device=rows.device)
+        tcg.gemm_f8_grouped_wgrad(tcg.IN_E4M3, rows.shape[0], n, k, route.experts, d.q, n, d.scale, n, a.q, k, a.scale, k,
+                                  route.offsets, dw, tcg.F32, k, n * k)
+        return dw
+
+    def forward(self, x: torch.Tensor, expert: torch.Tensor, weight: torch.Tensor):
+        route = Route(expert, self.layer.w1.shape[0])
+        xs = route.dispatch(x)
+        h = self.product(route, xs, self.w1)
+        a = torch.nn.functional.silu(h)
+        ys = self.product(route, a, self.w2)
+        return route.combine(ys, weight), (route, xs, h, a, ys, weight)
+
+    def backward(self, dy: torch.Tensor, kept):
+        route, xs, h, a, ys, weight = kept
+        dys, dweight = route.combine_grad(dy, ys, weight)
+        dw2 = self.matrix_grad(route, dys, a)
+        dh = torch.ops.aten.silu_backward(self.product(route, dys, self.w2, transposed=True), h)
+        dw1 = self.matrix_grad(route, dh, xs)
+        dx = route.combine(self.product(route, dh, self.w1, transposed=True), None)
+        return dx, dweight, dw1, dw2
+
+    def decode(self, x: torch.Tensor, expert: torch.Tensor, weight: torch.Tensor) -> torch.Tensor:
+        """y of up to 64 tokens in one call, with x as it is against the 8-bit experts."""
+        T, H = x.shape
+        E, inner, _ = self.w1.q.shape
+        y = torch.empty_like(x)
+        work = torch.empty(tcg.moe_few_work_bytes(T, expert.shape[1], inner), dtype=torch.uint8, device=x.device)
+        tcg.moe_few(IN[x.dtype], tcg.IN_E4M3, T, H, inner, expert.shape[1], E, x, x.stride(0), expert, weight, self.w1.q,
+                    None, self.w2.q, work, y, OUT[y.dtype], H, s1=self.w1.scale, s2=self.w2.scale)
+        return y
+
+
 def microseconds(f, n: int) -> float:
     for _ in range(3):
         f()
@@ -174,6 +251,17 @@ def main() -> None:
     off = ((y4 - y16).float().norm() / y16.float().norm()).item()
     print(f"decoding {o.batch} tokens with 4-bit experts: "
           f"{microseconds(lambda: decoder.forward(x[few], expert[few], weight[few]), o.repeat):.0f} us, "
+          f"{100 * off:.1f} % from the 16-bit layer")
+    layer8 = MoeLayer8(layer)
+    y8, kept = layer8.forward(x, expert, weight)
+    y = layer.forward(x, expert, weight)[0]
+    off = ((y8 - y).float().norm() / y.float().norm()).item()
+    print(f"in 8 bits: forward {microseconds(lambda: layer8.forward(x, expert, weight), o.repeat):.0f} us, backward "
+          f"{microseconds(lambda: layer8.backward(dy, kept), o.repeat):.0f} us, {100 * off:.1f} % from the 16-bit layer")
+    y8 = layer8.decode(x[few], expert[few], weight[few])
+    off = ((y8 - y16).float().norm() / y16.float().norm()).item()
+    print(f"decoding {o.batch} tokens with 8-bit experts: "
+          f"{microseconds(lambda: layer8.decode(x[few], expert[few], weight[few]), o.repeat):.0f} us, "
           f"{100 * off:.1f} % from the 16-bit layer")
     rc = tcg.check()
     if rc:
