@@ -2,32 +2,45 @@
 // the tensor cores: dense, by group, and the matrices' gradient by group.  Entry
 // points, host plan and kernel; the contract is in include/tcg.h.
 //
-// One kernel serves them all.  It computes C[m, c] = sum_b SP[b, m] SQ[b, c]
-// sum_{k in b} P[m, k] Q[c, k] over blocks b of 128 k, in tiles of 128 * CG rows
-// m by up to BN columns c, and stores it transposed, element (m, c) at
-// out[c * ldd + m]:
+// No MMA kind takes fp32 scales.  So the sum of a block of 128 k is one accumulator
+// in tensor memory (four MMAs of 32 k), and the epilogue's warps add it, scaled, to
+// sums in their registers while the MMAs fill the other accumulator: 128 x 256 sums
+// of a CTA are 128 registers of 256 threads.  All of it in fp32: one rounding of the
+// scales' product and one of each addition (BOTH: of each scaling too).
 //
-//             P (MMA rows)              Q (MMA columns)       contraction
-//   dense     B, rows n                 A, rows m             K
-//   grouped   B[g], rows n              the group's rows r    K
-//   weight    A, columns k, MN-major    DY, columns n         the group's rows
+// One kernel in three forms.  P has the MMA's rows, 128 for each CTA, and Q its
+// columns:
 //
-// No MMA kind takes fp32 scales.  So a block's sum is one accumulator (four
-// MMAs of 32 k), and the epilogue warps add it, scaled, to sums in their
-// registers, while the MMAs fill the other accumulator: 128 x 256 sums of a CTA
-// are 128 registers of 256 threads.  Each block costs the tensor pipe 512 cycles
-// (256 x 256 x 128 of a pair), the epilogue 256 cycles of tensor-memory reads
-// beside 256 of fp32 multiply-adds (512 where P's scales differ from row to row
-// as well: the factor is then formed for each element).
+//             tile        P                     Q                     scales
+//   ROWS      256 x 256   A, rows r             B or B[g], rows n     A's by row, B's square
+//   COLUMNS   128 x 64    B or B[g], rows n     A, rows r             A's by row, B's square
+//   BOTH      256 x 256   B, rows n             A, rows r             by row on either side
+//   (weight)  256 x 256   A, columns k, MN      DY, columns n, MN     by column of either
 //
-// A warp copies the blocks' scales ahead into a shared ring.
-//
-// The ragged extent of a product, the group's rows, is on the MMA's N side, any
-// multiple of 16 (32 for a pair) up to BN, so few rows cost few columns.  MN-major
-// Q (the gradients) takes whole boxes of 128 columns.  In the weight product the
-// contraction is ragged: rows of the next group within the last block are
+// ROWS: a lane holds one row, so that one factor, the product of the two scales,
+// serves all of its 128 columns.  (The first form, rows on the columns' side and a
+// factor for each read from shared memory by every lane, took 851 us for
+// 8192 x 8192 x 8192, where this takes 450.)
+// COLUMNS: few rows cost few columns, any multiple of 16; the result is stored
+// transposed.  Where its tiles leave SMs idle, two or four CTAs share a tile's
+// contraction and add their sums through the cluster's shared memory.
+// BOTH: a multiply and a multiply-add of each element.  The contraction of the
+// weight product is ragged: rows of the next group within the last block are
 // overwritten with zeros in shared memory up to the next multiple of 32, and the
 // MMAs beyond are not issued.
+//
+// What bounds them: a block of a pair's 256 x 256 takes the tensor pipe 512 cycles,
+// and the epilogue about 500 of waiting for commits and tensor-memory reads, one
+// after the other, beside 300 of multiply-adds (BOTH: 512).  With the two
+// accumulators that is 600 to 650 cycles a block for ROWS, 770 for BOTH.
+// 8192 x 8192 x 8192 in 421 us, 2.61 PFLOP/s; back to back for seconds the power
+// limit holds the clock at 1.91 GHz and it takes 450.  The weight gradient of
+// 4096 x 4096 over 8191 rows: 198 us, 1.39 PFLOP/s, of which 16 % is the last of 3.4
+// waves of tiles.  More warps for the epilogue (12, 16), reads of tensor memory a step
+// ahead, or one warp's arrival for all made each of them slower.
+//
+// A warp copies the blocks' scales ahead into a shared ring; one warp each brings P
+// and Q, another decodes the tile list.
 #include <cuda.h>
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
@@ -181,10 +194,11 @@ struct F8Cfg {
   static constexpr int Q_ROWS = BN / CG;
   static constexpr int Q_BYTES = Q_ROWS * 128;
   static constexpr int STAGE_BYTES = P_BYTES + Q_BYTES;
-  static constexpr int STAGING = PARTS >= 3 ? 1 : 2;  // staging tiles for each epilogue warp
+  static constexpr int STAGING = 2;  // staging tiles for each epilogue warp
   static constexpr int EPI_OFF = STAGES * STAGE_BYTES;
   static constexpr int SC_OFF = EPI_OFF + EPI_WARPS * STAGING * STAGING_BYTES;
-  // a block's scales: Q's of the columns, then P's of the rows or of all; ROWS: P's of the rows, then Q's of 128 columns each
+  // a block's scales: Q's of the columns, then P's of the rows or of all; ROWS: P's of
+  // the rows, then Q's of 128 columns each
   static constexpr int SLOT_BYTES = 4 * (MODE == ROWS ? 128 + 4 : BN + (MODE == BOTH ? 128 : 4));
   // split contractions: fragments of two column parts and four lane quadrants
   static constexpr int RED_OFF = (SC_OFF + SLOTS * SLOT_BYTES + 127) / 128 * 128;
@@ -419,229 +433,229 @@ __global__ void __launch_bounds__(F8Cfg<CG, BN, STAGES, MODE>::THREADS, 1) f8_ke
     return true;
   };
 
-  // registers at launch (384 threads x 168, 512 x 128): few for the four warps
-  // that feed, more for those that hold sums
+  // of the 384 x 168 registers at launch few for the four warps that feed, more for
+  // those that hold sums
   if (warp < 4) {
-  set_registers<false, C::PARTS == 4 ? 64 : C::PARTS == 3 ? 56 : 88>();
-  if (warp == 3) {
-    // ------------------------------------------- tile list and blocks' scales
-    uint32_t n = 0, it = 0;
-    auto publish = [&](int u, FTile& t) {
-      t = decode_unit<CG, BN, MODE>(p, seg, pre, u);
-      const uint32_t i = n % TILES;
-      if (!wait_inline(tile_empty(i), ((n / TILES) & 1u) ^ 1u, wctx, SITE_PROD_EMPTY)) return false;
-      if (lane == 0) {
-        tiles[i] = t;
-        mbar_arrive(tile_full(i));
-      }
-      __syncwarp();
-      ++n;
-      return true;
-    };
-    FTile t, next;
-    bool ok = cluster_id >= total_units || publish(cluster_id, next);
-    for (int u = cluster_id; u < total_units && ok; u += num_clusters) {
-      t = next;
-      // the tile after this one, ahead of this one's scales
-      if (u + num_clusters < total_units && !publish(u + num_clusters, next)) break;
-      const int b0 = p.weight ? t.lo / BLOCK + t.g : t.kb0;
-      const int m0 = t.m0 + static_cast<int>(rank) * 128;
-      // single scales of `n` columns or rows, and those of the other operand
-      const int n = MODE == ROWS ? t.rows - static_cast<int>(rank) * 128 : t.ncols;
-      const float* fine = p.fine + b0 * p.fine_b + (p.weight ? t.c0 : MODE == ROWS ? t.lo + m0 : t.lo + t.c0);
-      const float* other = MODE == BOTH   ? p.other + b0 * p.other_b + m0
-                           : MODE == ROWS ? p.other + t.g * p.other_group + (t.c0 / BLOCK + lane) * p.other_row
-                                          : p.other + t.g * p.other_group + (m0 / BLOCK) * p.other_row + b0 * p.other_b;
-      constexpr int FINE = MODE == ROWS ? 128 : BN;
-      for (int kb = 0; kb < t.nkb; ++kb, ++it) {
-        const uint32_t i = it % SLOTS;
-        if (!wait_inline(sce_bar(i), ((it / SLOTS) & 1u) ^ 1u, wctx, SITE_PROD_EMPTY)) {
-          ok = false;
-          break;
-        }
-        const uint32_t at = slot_at(i) + 4u * lane;
-#pragma unroll
-        for (int k = 0; k < FINE / 32; ++k)
-          if (lane + 32 * k < FINE) copy_f32(at + 128u * k, fine + lane + 32 * k, lane + 32 * k < n);
-        if constexpr (MODE == BOTH) {
-#pragma unroll
-          for (int k = 0; k < 4; ++k)
-            copy_f32(at + 4u * FINE + 128u * k, other + lane + 32 * k, m0 + lane + 32 * k < p.M);
-        } else if (lane < (MODE == ROWS ? BN / BLOCK : 1)) {
-          copy_f32(at + 4u * FINE, other, (MODE == ROWS ? t.c0 + BLOCK * lane : m0) < p.M);
-        }
-        copies_arrive(scf_bar(i));
-        fine += p.fine_b;
-        other += p.other_b;
-      }
-    }
-    // none in flight when the CTA ends
-    asm volatile("cp.async.wait_all;" ::: "memory");
-  } else if (warp != 1) {
-    // ---------------------------------------------- producers, of P and of Q
-    const bool brings_p = warp == 0;
-    uint32_t it = 0, s = 0, ph = 0, n = 0;
-    bool ok = true;
-    for (int u = cluster_id; u < total_units && ok; u += num_clusters) {
-      FTile t;
-      ok = fetch(n++, t);
-      if (!ok) break;
-      const int half = t.mma_n / CG;
-      const int m0 = t.m0 + static_cast<int>(rank) * 128;
-      const int c0 = t.c0 + static_cast<int>(rank) * half;
-      // the group is in the rows of the one operand and the matrix of the other
-      const int p_row = MODE == ROWS ? t.lo + m0 : m0, p_mat = MODE == ROWS || p.weight ? 0 : t.g;
-      const int q_row = MODE == ROWS || p.weight ? c0 : t.lo + c0, q_mat = MODE == ROWS ? t.g : 0;
-      const bool boxed = MODE == ROWS || p.weight || p.q_mn || half == C::Q_ROWS;  // Q in one box
-      const uint32_t tx = C::P_BYTES + static_cast<uint32_t>(boxed ? C::Q_BYTES : half * 128);
-      for (int kb = 0; kb < t.nkb; ++kb) {
-        if (!wait_inline(empty_bar(s), ph ^ 1u, wctx, SITE_PROD_EMPTY)) {
-          ok = false;
-          break;
-        }
-        if (elect_one()) {
-          const uint32_t sp = sbase + s * C::STAGE_BYTES;
-          const uint32_t sq = sp + C::P_BYTES;
-          const int k0 = BLOCK * (t.kb0 + kb);
-          const uint32_t fb = (CG == 2) ? mapa_shared(full_bar(s), 0) : full_bar(s);
-          if (p.weight && kb == t.nkb - 1 && (t.last & 31)) {
-            // the warp that zeroes the rows past the group's end waits for
-            // this CTA's bytes alone; full[s] just marks the stage
-            const int r0 = t.lo + k0;
-            if (brings_p) {
-              if (rank == 0) mbar_arrive(full_bar(s));
-              mbar_arrive_expect_tx(rag_bar(s), tx);
-              tma_load3<1>(sp, &p.tmap_p, m0, r0, 0, rag_bar(s));
-            } else {
-              tma_load3<1>(sq, &p.tmap_q, c0, r0, 0, rag_bar(s));
-            }
-          } else if (brings_p) {
-            if (rank == 0) mbar_arrive_expect_tx(full_bar(s), tx * CG);
-            if (!p.p_mn)
-              tma_load3<CG>(sp, &p.tmap_p, k0, p_row, p_mat, fb);
-            else
-              tma_load3<CG>(sp, &p.tmap_p, p_row, p.weight ? t.lo + k0 : k0, p_mat, fb);
-          } else if (p.q_mn) {
-            tma_load3<CG>(sq, &p.tmap_q, q_row, p.weight ? t.lo + k0 : k0, q_mat, fb);
-          } else if (boxed) {
-            tma_load3<CG>(sq, &p.tmap_q, k0, q_row, q_mat, fb);
-          } else {
-            for (int i = 0; i < half; i += 16) tma_load3<CG>(sq + 128 * i, &p.tmap_q16, k0, q_row + i, q_mat, fb);
-          }
+    set_registers<false, 88>();
+    if (warp == 3) {
+      // ------------------------------------------- tile list and blocks' scales
+      uint32_t n = 0, it = 0;
+      auto publish = [&](int u, FTile& t) {
+        t = decode_unit<CG, BN, MODE>(p, seg, pre, u);
+        const uint32_t i = n % TILES;
+        if (!wait_inline(tile_empty(i), ((n / TILES) & 1u) ^ 1u, wctx, SITE_PROD_EMPTY)) return false;
+        if (lane == 0) {
+          tiles[i] = t;
+          mbar_arrive(tile_full(i));
         }
         __syncwarp();
-        ++it;
-        if (++s == STAGES) {
-          s = 0;
-          ph ^= 1u;
-        }
-      }
-    }
-    if (!ok && elect_one()) {
-      // let the copies in flight land before the CTA can exit: full[s] counts
-      // the leader's and (for a pair) the peer's; ragged stages are waited
-      // for by time, as the peer's are
-      const uint32_t n_out = it < static_cast<uint32_t>(STAGES) ? it : static_cast<uint32_t>(STAGES);
-      if ((CG == 1 || rank == 0) && !p.weight && brings_p) {
-        for (uint32_t j = it - n_out; j < it; ++j) {
-          const uint64_t t0 = globaltimer();
-          while (!mbar_try_wait(full_bar(j % STAGES), (j / STAGES) & 1u) && globaltimer() - t0 < 20000000ull) {
-          }
-        }
-      } else {
-        const uint64_t t0 = globaltimer();
-        while (globaltimer() - t0 < 2000000ull) {
-        }
-      }
-    }
-    __syncwarp();
-  } else {
-    // --------------------------------- MMA issuer (leader), row zeroing (both)
-    const uint64_t p_desc0 = sdesc(sbase, p.p_hi);
-    const uint64_t q_desc0 = sdesc(sbase + C::P_BYTES, p.q_hi);
-    uint32_t s = 0, ph = 0, n = 0, tcount = 0, rag_ph = 0;  // rag_ph: one parity bit per stage
-    bool ok = true;
-    for (int u = cluster_id; u < total_units && ok; u += num_clusters) {
-      FTile t;
-      ok = fetch(n++, t);
-      if (!ok) break;
-      const bool issue = CG == 1 || rank == 0;
-      const uint32_t idesc = p.idesc | (static_cast<uint32_t>(t.mma_n >> 3) << 17);
-      for (int kb = 0; kb < t.nkb; ++kb) {
-        const bool last = kb == t.nkb - 1;
-        const bool ragged = p.weight && last && (t.last & 31);
-        const uint32_t b = tcount & 1u;
-        if (issue && !wait_inline(acce_bar(b), ((tcount >> 1) & 1u) ^ 1u, wctx, SITE_MMA_ACC_EMPTY)) {
-          ok = false;
-          break;
-        }
-        ++tcount;
-        const uint32_t d_tmem = tmem_base + b * BN;
-        if (issue && !wait_inline(full_bar(s), ph, wctx, SITE_MMA_FULL)) {
-          ok = false;
-          break;
-        }
-        if (ragged) {
-          const uint32_t par = (rag_ph >> s) & 1u;
-          rag_ph ^= 1u << s;
-          if (!wait_inline(rag_bar(s), par, wctx, SITE_MMA_FULL)) {
+        ++n;
+        return true;
+      };
+      FTile t, next;
+      bool ok = cluster_id >= total_units || publish(cluster_id, next);
+      for (int u = cluster_id; u < total_units && ok; u += num_clusters) {
+        t = next;
+        // the tile after this one, ahead of this one's scales
+        if (u + num_clusters < total_units && !publish(u + num_clusters, next)) break;
+        const int b0 = p.weight ? t.lo / BLOCK + t.g : t.kb0;
+        const int m0 = t.m0 + static_cast<int>(rank) * 128;
+        // single scales of `n` columns or rows, and those of the other operand
+        const int n = MODE == ROWS ? t.rows - static_cast<int>(rank) * 128 : t.ncols;
+        const float* fine = p.fine + b0 * p.fine_b + (p.weight ? t.c0 : MODE == ROWS ? t.lo + m0 : t.lo + t.c0);
+        const float* other = MODE == BOTH   ? p.other + b0 * p.other_b + m0
+                             : MODE == ROWS ? p.other + t.g * p.other_group + (t.c0 / BLOCK + lane) * p.other_row
+                                            : p.other + t.g * p.other_group + (m0 / BLOCK) * p.other_row + b0 * p.other_b;
+        constexpr int FINE = MODE == ROWS ? 128 : BN;
+        for (int kb = 0; kb < t.nkb; ++kb, ++it) {
+          const uint32_t i = it % SLOTS;
+          if (!wait_inline(sce_bar(i), ((it / SLOTS) & 1u) ^ 1u, wctx, SITE_PROD_EMPTY)) {
             ok = false;
             break;
           }
-          // rows [last, next multiple of 32) of P and Q; a row's 128 bytes are
-          // the same under the swizzle
-          const uint32_t sp = sbase + s * C::STAGE_BYTES;
-          const int rows = 32 - (t.last & 31);
-          for (int i = lane; i < 2 * rows * 8; i += 32) {
-            const int ch = i / (rows * 8), rr = i - ch * rows * 8;
-            st_shared_v4((ch ? sp + C::P_BYTES : sp) + 128u * (t.last + (rr >> 3)) + 16u * (rr & 7), 0u, 0u, 0u, 0u);
+          const uint32_t at = slot_at(i) + 4u * lane;
+  #pragma unroll
+          for (int k = 0; k < FINE / 32; ++k)
+            if (lane + 32 * k < FINE) copy_f32(at + 128u * k, fine + lane + 32 * k, lane + 32 * k < n);
+          if constexpr (MODE == BOTH) {
+  #pragma unroll
+            for (int k = 0; k < 4; ++k)
+              copy_f32(at + 4u * FINE + 128u * k, other + lane + 32 * k, m0 + lane + 32 * k < p.M);
+          } else if (lane < (MODE == ROWS ? BN / BLOCK : 1)) {
+            copy_f32(at + 4u * FINE, other, (MODE == ROWS ? t.c0 + BLOCK * lane : m0) < p.M);
           }
-          fence_proxy_async_shared();
+          copies_arrive(scf_bar(i));
+          fine += p.fine_b;
+          other += p.other_b;
+        }
+      }
+      // none in flight when the CTA ends
+      asm volatile("cp.async.wait_all;" ::: "memory");
+    } else if (warp != 1) {
+      // ---------------------------------------------- producers, of P and of Q
+      const bool brings_p = warp == 0;
+      uint32_t it = 0, s = 0, ph = 0, n = 0;
+      bool ok = true;
+      for (int u = cluster_id; u < total_units && ok; u += num_clusters) {
+        FTile t;
+        ok = fetch(n++, t);
+        if (!ok) break;
+        const int half = t.mma_n / CG;
+        const int m0 = t.m0 + static_cast<int>(rank) * 128;
+        const int c0 = t.c0 + static_cast<int>(rank) * half;
+        // the group is in the rows of the one operand and the matrix of the other
+        const int p_row = MODE == ROWS ? t.lo + m0 : m0, p_mat = MODE == ROWS || p.weight ? 0 : t.g;
+        const int q_row = MODE == ROWS || p.weight ? c0 : t.lo + c0, q_mat = MODE == ROWS ? t.g : 0;
+        const bool boxed = MODE == ROWS || p.weight || p.q_mn || half == C::Q_ROWS;  // Q in one box
+        const uint32_t tx = C::P_BYTES + static_cast<uint32_t>(boxed ? C::Q_BYTES : half * 128);
+        for (int kb = 0; kb < t.nkb; ++kb) {
+          if (!wait_inline(empty_bar(s), ph ^ 1u, wctx, SITE_PROD_EMPTY)) {
+            ok = false;
+            break;
+          }
+          if (elect_one()) {
+            const uint32_t sp = sbase + s * C::STAGE_BYTES;
+            const uint32_t sq = sp + C::P_BYTES;
+            const int k0 = BLOCK * (t.kb0 + kb);
+            const uint32_t fb = (CG == 2) ? mapa_shared(full_bar(s), 0) : full_bar(s);
+            if (p.weight && kb == t.nkb - 1 && (t.last & 31)) {
+              // the warp that zeroes the rows past the group's end waits for
+              // this CTA's bytes alone; full[s] just marks the stage
+              const int r0 = t.lo + k0;
+              if (brings_p) {
+                if (rank == 0) mbar_arrive(full_bar(s));
+                mbar_arrive_expect_tx(rag_bar(s), tx);
+                tma_load3<1>(sp, &p.tmap_p, m0, r0, 0, rag_bar(s));
+              } else {
+                tma_load3<1>(sq, &p.tmap_q, c0, r0, 0, rag_bar(s));
+              }
+            } else if (brings_p) {
+              if (rank == 0) mbar_arrive_expect_tx(full_bar(s), tx * CG);
+              if (!p.p_mn)
+                tma_load3<CG>(sp, &p.tmap_p, k0, p_row, p_mat, fb);
+              else
+                tma_load3<CG>(sp, &p.tmap_p, p_row, p.weight ? t.lo + k0 : k0, p_mat, fb);
+            } else if (p.q_mn) {
+              tma_load3<CG>(sq, &p.tmap_q, q_row, p.weight ? t.lo + k0 : k0, q_mat, fb);
+            } else if (boxed) {
+              tma_load3<CG>(sq, &p.tmap_q, k0, q_row, q_mat, fb);
+            } else {
+              for (int i = 0; i < half; i += 16) tma_load3<CG>(sq + 128 * i, &p.tmap_q16, k0, q_row + i, q_mat, fb);
+            }
+          }
           __syncwarp();
-          if constexpr (CG == 2) {
-            if (rank != 0) {
-              if (lane == 0) mbar_arrive_cluster(mapa_shared(peer_bar(s), 0));
-            } else if (!wait_inline(peer_bar(s), par, wctx, SITE_MMA_FULL) || !mbar_try_wait_cluster(peer_bar(s), par)) {
+          ++it;
+          if (++s == STAGES) {
+            s = 0;
+            ph ^= 1u;
+          }
+        }
+      }
+      if (!ok && elect_one()) {
+        // let the copies in flight land before the CTA can exit: full[s] counts
+        // the leader's and (for a pair) the peer's; ragged stages are waited
+        // for by time, as the peer's are
+        const uint32_t n_out = it < static_cast<uint32_t>(STAGES) ? it : static_cast<uint32_t>(STAGES);
+        if ((CG == 1 || rank == 0) && !p.weight && brings_p) {
+          for (uint32_t j = it - n_out; j < it; ++j) {
+            const uint64_t t0 = globaltimer();
+            while (!mbar_try_wait(full_bar(j % STAGES), (j / STAGES) & 1u) && globaltimer() - t0 < 20000000ull) {
+            }
+          }
+        } else {
+          const uint64_t t0 = globaltimer();
+          while (globaltimer() - t0 < 2000000ull) {
+          }
+        }
+      }
+      __syncwarp();
+    } else {
+      // --------------------------------- MMA issuer (leader), row zeroing (both)
+      const uint64_t p_desc0 = sdesc(sbase, p.p_hi);
+      const uint64_t q_desc0 = sdesc(sbase + C::P_BYTES, p.q_hi);
+      uint32_t s = 0, ph = 0, n = 0, tcount = 0, rag_ph = 0;  // rag_ph: one parity bit per stage
+      bool ok = true;
+      for (int u = cluster_id; u < total_units && ok; u += num_clusters) {
+        FTile t;
+        ok = fetch(n++, t);
+        if (!ok) break;
+        const bool issue = CG == 1 || rank == 0;
+        const uint32_t idesc = p.idesc | (static_cast<uint32_t>(t.mma_n >> 3) << 17);
+        for (int kb = 0; kb < t.nkb; ++kb) {
+          const bool last = kb == t.nkb - 1;
+          const bool ragged = p.weight && last && (t.last & 31);
+          const uint32_t b = tcount & 1u;
+          if (issue && !wait_inline(acce_bar(b), ((tcount >> 1) & 1u) ^ 1u, wctx, SITE_MMA_ACC_EMPTY)) {
+            ok = false;
+            break;
+          }
+          ++tcount;
+          const uint32_t d_tmem = tmem_base + b * BN;
+          if (issue && !wait_inline(full_bar(s), ph, wctx, SITE_MMA_FULL)) {
+            ok = false;
+            break;
+          }
+          if (ragged) {
+            const uint32_t par = (rag_ph >> s) & 1u;
+            rag_ph ^= 1u << s;
+            if (!wait_inline(rag_bar(s), par, wctx, SITE_MMA_FULL)) {
               ok = false;
               break;
             }
+            // rows [last, next multiple of 32) of P and Q; a row's 128 bytes are
+            // the same under the swizzle
+            const uint32_t sp = sbase + s * C::STAGE_BYTES;
+            const int rows = 32 - (t.last & 31);
+            for (int i = lane; i < 2 * rows * 8; i += 32) {
+              const int ch = i / (rows * 8), rr = i - ch * rows * 8;
+              st_shared_v4((ch ? sp + C::P_BYTES : sp) + 128u * (t.last + (rr >> 3)) + 16u * (rr & 7), 0u, 0u, 0u, 0u);
+            }
+            fence_proxy_async_shared();
+            __syncwarp();
+            if constexpr (CG == 2) {
+              if (rank != 0) {
+                if (lane == 0) mbar_arrive_cluster(mapa_shared(peer_bar(s), 0));
+              } else if (!wait_inline(peer_bar(s), par, wctx, SITE_MMA_FULL) || !mbar_try_wait_cluster(peer_bar(s), par)) {
+                ok = false;
+                break;
+              }
+            }
+          }
+          if (issue) {
+            tc_fence_after();
+            if (elect_one()) {
+              const uint64_t st = (s * static_cast<uint32_t>(C::STAGE_BYTES)) >> 4;
+              const int steps = p.weight && last ? (t.last + 31) >> 5 : 4;
+  #pragma unroll
+              for (int j = 0; j < 4; ++j)
+                if (j < steps)
+                  mma_f8<CG>(d_tmem, p_desc0 + st + j * p.p_kstep, q_desc0 + st + j * p.q_kstep, idesc, j ? 1u : 0u);
+              tc_commit<CG>(empty_bar(s));
+              tc_commit<CG>(accf_bar(b));
+            }
+            __syncwarp();
+          }
+          if (++s == STAGES) {
+            s = 0;
+            ph ^= 1u;
           }
         }
-        if (issue) {
-          tc_fence_after();
-          if (elect_one()) {
-            const uint64_t st = (s * static_cast<uint32_t>(C::STAGE_BYTES)) >> 4;
-            const int steps = p.weight && last ? (t.last + 31) >> 5 : 4;
-#pragma unroll
-            for (int j = 0; j < 4; ++j)
-              if (j < steps)
-                mma_f8<CG>(d_tmem, p_desc0 + st + j * p.p_kstep, q_desc0 + st + j * p.q_kstep, idesc, j ? 1u : 0u);
-            tc_commit<CG>(empty_bar(s));
-            tc_commit<CG>(accf_bar(b));
-          }
-          __syncwarp();
-        }
-        if (++s == STAGES) {
-          s = 0;
-          ph ^= 1u;
+      }
+      if (!ok && (CG == 1 || rank == 0) && elect_one()) {
+        tc_commit<CG>(drain_bar);
+        const uint64_t t0 = globaltimer();
+        while (!mbar_try_wait(drain_bar, 0) && globaltimer() - t0 < 20000000ull) {
         }
       }
+      __syncwarp();
     }
-    if (!ok && (CG == 1 || rank == 0) && elect_one()) {
-      tc_commit<CG>(drain_bar);
-      const uint64_t t0 = globaltimer();
-      while (!mbar_try_wait(drain_bar, 0) && globaltimer() - t0 < 20000000ull) {
-      }
-    }
-    __syncwarp();
-  }
   } else {
     // ------------------------------------------------------------ epilogue
-    set_registers<true, C::PARTS == 4 ? 104 : C::PARTS == 3 ? 152 : 208>();
+    set_registers<true, 208>();
     const int q = warp & 3;            // TMEM lane quadrant
     const int part = (warp - 4) >> 2;  // 32-column chunks part, part + PARTS, ...
     constexpr int ACROSS = 32 * C::PARTS;  // a warp's chunks of 32 columns lie so far apart
-    constexpr int MINE = MODE == ROWS ? 1 : (BN + ACROSS - 1) / ACROSS;
+    constexpr int MINE = (BN + ACROSS - 1) / ACROSS;
     uint32_t tcount = 0, n = 0, stores = 0;
     const uint32_t buf0 = sbase + C::EPI_OFF + static_cast<uint32_t>((warp - 4) * C::STAGING * STAGING_BYTES);
     // the staging tile to fill next: its last store has read it
@@ -785,178 +799,165 @@ __global__ void __launch_bounds__(F8Cfg<CG, BN, STAGES, MODE>::THREADS, 1) f8_ke
           }
           __syncwarp();
         }
-        continue;
-      }
-      uint64_t sum[MINE][2][8];  // chunk, 16 rows, pairs of columns as in the fragment
-#pragma unroll
-      for (int i = 0; i < MINE; ++i)
-#pragma unroll
-        for (int k = 0; k < 16; ++k) sum[i][k >> 3][k & 7] = 0ull;
-      const int mine = (t.ncols - 32 * part + ACROSS - 1) / ACROSS;  // this warp's chunks of 32 columns that exist
-      bool done = true;
-      for (int kb = 0; kb < t.nkb; ++kb, ++tcount) {
-        const uint32_t b = tcount & 1u, slot = tcount % SLOTS;
-        done = wait_inline(scf_bar(slot), (tcount / SLOTS) & 1u, wctx, SITE_EPI_ACC_FULL) &&
-               wait_inline(accf_bar(b), (tcount >> 1) & 1u, wctx, SITE_EPI_ACC_FULL);
-        if (!done) break;
-        tc_fence_after();
-        const uint32_t at = slot_at(slot);
-        uint64_t row[MODE == BOTH ? 4 : 1];  // P's factors of this lane's rows lane / 4 + 8 h (or of all), twice
-#pragma unroll
-        for (int h = 0; h < (MODE == BOTH ? 4 : 1); ++h) {
-          const uint32_t r = __float_as_uint(ld_shared_f32(at + 4u * (MODE == BOTH ? BN + 32 * q + 8 * h + (lane >> 2) : BN)));
-          row[h] = pair(r, r);
-        }
-        // fragments of 16 rows by 32 columns, the next step's reads in flight meanwhile
-        const uint32_t from = lanes + b * BN + 32 * part;
-        constexpr int STEP = 2, BUF = 1;  // fragments a step, steps in flight
-        uint32_t r[BUF][STEP][16];
-        auto read = [&](int h0) {
-#pragma unroll
-          for (int h = h0; h < h0 + STEP; ++h)
-            if (h < 2 * MINE && h / 2 < mine)
-              tmem_ld_16x256b_x4(from + ACROSS * (h / 2) + (static_cast<uint32_t>(h & 1) << 20), r[h / STEP % BUF][h % STEP]);
-        };
-        uint64_t f[4];  // factors of this lane's columns 8 j + 2 (lane % 4), + 1
-        if (BUF == 2) read(0);
-#pragma unroll
-        for (int h0 = 0; h0 < 2 * MINE; h0 += STEP) {
-          if (h0 / 2 >= mine) break;
-          if (BUF == 1) read(h0);
-#pragma unroll
-          for (int h = h0; h < h0 + STEP; ++h) {
-            if ((h & 1) == 0) {
-#pragma unroll
-              for (int j = 0; j < 4; ++j) {
-                f[j] = ld_shared_b64(at + 4u * (32 * part + ACROSS * (h / 2) + 8 * j + 2 * (lane & 3)));
-                if constexpr (MODE != BOTH) f[j] = mul2(f[j], row[0]);
+      } else {
+        uint64_t sum[MINE][2][8];  // chunk, 16 rows, pairs of columns as in the fragment
+  #pragma unroll
+        for (int i = 0; i < MINE; ++i)
+  #pragma unroll
+          for (int k = 0; k < 16; ++k) sum[i][k >> 3][k & 7] = 0ull;
+        const int mine = (t.ncols - 32 * part + ACROSS - 1) / ACROSS;  // this warp's chunks of 32 columns that exist
+        bool done = true;
+        for (int kb = 0; kb < t.nkb; ++kb, ++tcount) {
+          const uint32_t b = tcount & 1u, slot = tcount % SLOTS;
+          done = wait_inline(scf_bar(slot), (tcount / SLOTS) & 1u, wctx, SITE_EPI_ACC_FULL) &&
+                 wait_inline(accf_bar(b), (tcount >> 1) & 1u, wctx, SITE_EPI_ACC_FULL);
+          if (!done) break;
+          tc_fence_after();
+          const uint32_t at = slot_at(slot);
+          uint64_t row[MODE == BOTH ? 4 : 1];  // P's factors of this lane's rows lane / 4 + 8 h (or of all), twice
+  #pragma unroll
+          for (int h = 0; h < (MODE == BOTH ? 4 : 1); ++h) {
+            const uint32_t r = __float_as_uint(ld_shared_f32(at + 4u * (MODE == BOTH ? BN + 32 * q + 8 * h + (lane >> 2) : BN)));
+            row[h] = pair(r, r);
+          }
+          // a chunk's two fragments of 16 rows by 32 columns at a time
+          const uint32_t from = lanes + b * BN + 32 * part;
+  #pragma unroll
+          for (int i = 0; i < MINE; ++i) {
+            if (i >= mine) break;
+            uint32_t r[2][16];
+  #pragma unroll
+            for (int h = 0; h < 2; ++h)
+              tmem_ld_16x256b_x4(from + ACROSS * i + (static_cast<uint32_t>(h) << 20), r[h]);
+            uint64_t f[4];  // factors of this lane's columns 8 j + 2 (lane % 4), + 1
+  #pragma unroll
+            for (int j = 0; j < 4; ++j) {
+              f[j] = ld_shared_b64(at + 4u * (32 * part + ACROSS * i + 8 * j + 2 * (lane & 3)));
+              if constexpr (MODE != BOTH) f[j] = mul2(f[j], row[0]);
+            }
+            tc_wait_ld();
+  #pragma unroll
+            for (int h = 0; h < 2; ++h)
+  #pragma unroll
+              for (int k = 0; k < 8; ++k) {
+                if constexpr (MODE == BOTH)
+                  add_scaled(sum[i][h][k], r[h][2 * k], r[h][2 * k + 1], f[k / 2], row[2 * h + (k & 1)]);
+                else
+                  add_scaled(sum[i][h][k], r[h][2 * k], r[h][2 * k + 1], f[k / 2]);
               }
+          }
+          tc_fence_before();
+          __syncwarp();
+          if (lane == 0) {
+            mbar_arrive(sce_bar(slot));
+            if constexpr (CG == 2)
+              mbar_arrive_relaxed(mapa_shared(acce_bar(b), 0));  // no memory to order, only TMEM reads
+            else
+              mbar_arrive(acce_bar(b));
+          }
+        }
+        if (!done) break;
+        if constexpr (MODE == COLUMNS) {
+          if (p.split > 1) {
+            // Every CTA of the cluster sends a lane quadrant's sums to the one CTA that
+            // adds them, in the order of the blocks, and stores them.  A cluster has
+            // one unit at most, so the buffer is written once.
+            const int quads = 4 / p.split, owner = q / quads, from = static_cast<int>(cluster_ctarank());
+            const uint32_t mine_at = sbase + C::RED_OFF + 4096u * ((q % quads * p.split + from) * 2 + part) + 16u * lane;
+            if (mine > 0) {
+              const uint32_t to = mapa_shared(mine_at, static_cast<uint32_t>(owner));
+  #pragma unroll
+              for (int v = 0; v < 8; ++v) st_cluster_2x64(to + 512u * v, sum[0][v >> 2][2 * (v & 3)], sum[0][v >> 2][2 * (v & 3) + 1]);
             }
-            if (h == h0) {
-              tc_wait_ld();
-              if (BUF == 2) read(h0 + STEP);
-            }
-#pragma unroll
-            for (int k = 0; k < 8; ++k) {
-              uint32_t(&v)[16] = r[h / STEP % BUF][h % STEP];
-              if constexpr (MODE == BOTH)
-                add_scaled(sum[h / 2][h & 1][k], v[2 * k], v[2 * k + 1], f[k / 2], row[2 * (h & 1) + (k & 1)]);
-              else
-                add_scaled(sum[h / 2][h & 1][k], v[2 * k], v[2 * k + 1], f[k / 2]);
+            __syncwarp();
+            if (lane == 0) mbar_arrive_cluster(mapa_shared(red_bar, static_cast<uint32_t>(owner)));
+            if (from != owner) continue;
+            if (!wait_inline(red_bar, 0u, wctx, SITE_EPI_ACC_FULL) || !mbar_try_wait_cluster(red_bar, 0u)) break;
+            if (mine <= 0) continue;
+            for (int r = 0; r < p.split; ++r) {
+              const uint32_t at = mine_at + 4096u * 2 * (r - from);
+  #pragma unroll
+              for (int v = 0; v < 8; ++v) {
+                uint64_t a, b;
+                ld_shared_2x64(at + 512u * v, a, b);
+                uint64_t &x = sum[0][v >> 2][2 * (v & 3)], &y = sum[0][v >> 2][2 * (v & 3) + 1];
+                x = r ? add2(x, a) : a;
+                y = r ? add2(y, b) : b;
+              }
             }
           }
         }
-        tc_fence_before();
-        __syncwarp();
-        if (lane == 0) {
-          mbar_arrive(sce_bar(slot));
-          if constexpr (CG == 2)
-            mbar_arrive_relaxed(mapa_shared(acce_bar(b), 0));  // no memory to order, only TMEM reads
-          else
-            mbar_arrive(acce_bar(b));
-        }
-      }
-      if (!done) break;
-      if constexpr (MODE == COLUMNS) {
-        if (p.split > 1) {
-          // Every CTA of the cluster sends a lane quadrant's sums to the one CTA that
-          // adds them, in the order of the blocks, and stores them.  A cluster has
-          // one unit at most, so the buffer is written once.
-          const int quads = 4 / p.split, owner = q / quads, from = static_cast<int>(cluster_ctarank());
-          const uint32_t mine_at = sbase + C::RED_OFF + 4096u * ((q % quads * p.split + from) * 2 + part) + 16u * lane;
-          if (mine > 0) {
-            const uint32_t to = mapa_shared(mine_at, static_cast<uint32_t>(owner));
-#pragma unroll
-            for (int v = 0; v < 8; ++v) st_cluster_2x64(to + 512u * v, sum[0][v >> 2][2 * (v & 3)], sum[0][v >> 2][2 * (v & 3) + 1]);
+        const int m_warp = t.m0 + static_cast<int>(rank) * 128 + 32 * q;
+        const int row0 = p.weight ? t.c0 : t.lo + t.c0, outer = p.weight ? t.g : 0;
+        const int64_t pitch = p.ldd * p.d_size;
+        const bool m_ok = m_warp + lane < p.M;
+        uint8_t* dst = static_cast<uint8_t*>(p.D) + static_cast<int64_t>(row0) * pitch +
+                       (p.weight ? t.g * p.stride_d * p.d_size : 0) + static_cast<int64_t>(m_warp + lane) * p.d_size;
+  #pragma unroll
+        for (int i = 0; i < MINE; ++i) {
+          const int c = 32 * part + ACROSS * i;
+          if (i >= mine || m_warp >= p.M) break;
+          // rows of a matrix clip at the map's end, rows of a group do not
+          const bool boxed = p.d_tma && (p.weight || c + 32 <= t.ncols);
+          if (p.d_type == OUT_F32) {
+  #pragma unroll
+            for (int g = 0; g < 2; ++g) {  // a staging tile holds 16 rows of 32 m
+              const uint32_t buf = staging();
+  #pragma unroll
+              for (int h = 0; h < 4; ++h) {
+                const uint32_t m = 8u * h + (static_cast<uint32_t>(lane) >> 2);
+  #pragma unroll
+                for (int j = 0; j < 2; ++j) {
+                  uint32_t lo, hi;
+                  unpair(sum[i][h >> 1][2 * (2 * g + j) + (h & 1)], lo, hi);
+                  const uint32_t at = 8u * j + 2u * (lane & 3);
+                  st_shared_u32(buf + 128u * at + 16u * ((m >> 2) ^ (at & 7u)) + 4u * (m & 3u), lo);
+                  st_shared_u32(buf + 128u * (at + 1) + 16u * ((m >> 2) ^ ((at + 1) & 7u)) + 4u * (m & 3u), hi);
+                }
+              }
+              if (boxed) {
+                send(buf, m_warp, row0 + c + 16 * g, outer);
+                continue;
+              }
+              __syncwarp();
+              for (int k = 0; k < 16; ++k) {
+                const uint32_t m = static_cast<uint32_t>(lane);
+                if (m_ok && c + 16 * g + k < t.ncols)
+                  *reinterpret_cast<float*>(dst + (c + 16 * g + k) * pitch) =
+                      ld_shared_f32(buf + 128u * k + 16u * ((m >> 2) ^ (k & 7u)) + 4u * (m & 3u));
+              }
+              __syncwarp();
+            }
+            continue;
+          }
+          // stmatrix turns 8 m of 8 columns into 8 rows of 16 bytes: lane 8k + n
+          // addresses row 8j + n, m 8k..8k+7; a row's four 16-byte words are swizzled
+          const uint32_t buf = staging();
+          const bool bf = p.d_type == OUT_BF16;
+          const uint32_t k = static_cast<uint32_t>(lane) >> 3, n8 = static_cast<uint32_t>(lane) & 7u;
+  #pragma unroll
+          for (uint32_t j = 0; j < 4; ++j) {
+            const uint32_t to = 8u * j + n8;
+            uint32_t w[4];
+  #pragma unroll
+            for (int h = 0; h < 4; ++h) {
+              uint32_t lo, hi;
+              unpair(sum[i][h >> 1][2 * j + (h & 1)], lo, hi);
+              w[h] = bf ? pack_bf16(lo, hi) : pack_f16(lo, hi);
+            }
+            stmatrix_x4_trans(buf + 64u * to + 16u * (k ^ ((to >> 1) & 3u)), w[0], w[1], w[2], w[3]);
+          }
+          if (boxed) {
+            send(buf, m_warp, row0 + c, outer);
+            continue;
           }
           __syncwarp();
-          if (lane == 0) mbar_arrive_cluster(mapa_shared(red_bar, static_cast<uint32_t>(owner)));
-          if (from != owner) continue;
-          if (!wait_inline(red_bar, 0u, wctx, SITE_EPI_ACC_FULL) || !mbar_try_wait_cluster(red_bar, 0u)) break;
-          if (mine <= 0) continue;
-          for (int r = 0; r < p.split; ++r) {
-            const uint32_t at = mine_at + 4096u * 2 * (r - from);
-#pragma unroll
-            for (int v = 0; v < 8; ++v) {
-              uint64_t a, b;
-              ld_shared_2x64(at + 512u * v, a, b);
-              uint64_t &x = sum[0][v >> 2][2 * (v & 3)], &y = sum[0][v >> 2][2 * (v & 3) + 1];
-              x = r ? add2(x, a) : a;
-              y = r ? add2(y, b) : b;
-            }
-          }
+          for (int n = 0; n < 32; ++n)
+            if (m_ok && c + n < t.ncols)
+              *reinterpret_cast<uint16_t*>(dst + (c + n) * pitch) =
+                  ld_shared_u16(buf + 64u * n + 16u * (k ^ ((static_cast<uint32_t>(n) >> 1) & 3u)) + 2u * n8);
+          __syncwarp();
         }
-      }
-      const int m_warp = t.m0 + static_cast<int>(rank) * 128 + 32 * q;
-      const int row0 = p.weight ? t.c0 : t.lo + t.c0, outer = p.weight ? t.g : 0;
-      const int64_t pitch = p.ldd * p.d_size;
-      const bool m_ok = m_warp + lane < p.M;
-      uint8_t* dst = static_cast<uint8_t*>(p.D) + static_cast<int64_t>(row0) * pitch +
-                     (p.weight ? t.g * p.stride_d * p.d_size : 0) + static_cast<int64_t>(m_warp + lane) * p.d_size;
-#pragma unroll
-      for (int i = 0; i < MINE; ++i) {
-        const int c = 32 * part + ACROSS * i;
-        if (i >= mine || m_warp >= p.M) break;
-        // rows of a matrix clip at the map's end, rows of a group do not
-        const bool boxed = p.d_tma && (p.weight || c + 32 <= t.ncols);
-        if (p.d_type == OUT_F32) {
-#pragma unroll
-          for (int g = 0; g < 2; ++g) {  // a staging tile holds 16 rows of 32 m
-            const uint32_t buf = staging();
-#pragma unroll
-            for (int h = 0; h < 4; ++h) {
-              const uint32_t m = 8u * h + (static_cast<uint32_t>(lane) >> 2);
-#pragma unroll
-              for (int j = 0; j < 2; ++j) {
-                uint32_t lo, hi;
-                unpair(sum[i][h >> 1][2 * (2 * g + j) + (h & 1)], lo, hi);
-                const uint32_t at = 8u * j + 2u * (lane & 3);
-                st_shared_u32(buf + 128u * at + 16u * ((m >> 2) ^ (at & 7u)) + 4u * (m & 3u), lo);
-                st_shared_u32(buf + 128u * (at + 1) + 16u * ((m >> 2) ^ ((at + 1) & 7u)) + 4u * (m & 3u), hi);
-              }
-            }
-            if (boxed) {
-              send(buf, m_warp, row0 + c + 16 * g, outer);
-              continue;
-            }
-            __syncwarp();
-            for (int k = 0; k < 16; ++k) {
-              const uint32_t m = static_cast<uint32_t>(lane);
-              if (m_ok && c + 16 * g + k < t.ncols)
-                *reinterpret_cast<float*>(dst + (c + 16 * g + k) * pitch) =
-                    ld_shared_f32(buf + 128u * k + 16u * ((m >> 2) ^ (k & 7u)) + 4u * (m & 3u));
-            }
-            __syncwarp();
-          }
-          continue;
-        }
-        // stmatrix turns 8 m of 8 columns into 8 rows of 16 bytes: lane 8k + n
-        // addresses row 8j + n, m 8k..8k+7; a row's four 16-byte words are swizzled
-        const uint32_t buf = staging();
-        const bool bf = p.d_type == OUT_BF16;
-        const uint32_t k = static_cast<uint32_t>(lane) >> 3, n8 = static_cast<uint32_t>(lane) & 7u;
-#pragma unroll
-        for (uint32_t j = 0; j < 4; ++j) {
-          const uint32_t to = 8u * j + n8;
-          uint32_t w[4];
-#pragma unroll
-          for (int h = 0; h < 4; ++h) {
-            uint32_t lo, hi;
-            unpair(sum[i][h >> 1][2 * j + (h & 1)], lo, hi);
-            w[h] = bf ? pack_bf16(lo, hi) : pack_f16(lo, hi);
-          }
-          stmatrix_x4_trans(buf + 64u * to + 16u * (k ^ ((to >> 1) & 3u)), w[0], w[1], w[2], w[3]);
-        }
-        if (boxed) {
-          send(buf, m_warp, row0 + c, outer);
-          continue;
-        }
-        __syncwarp();
-        for (int n = 0; n < 32; ++n)
-          if (m_ok && c + n < t.ncols)
-            *reinterpret_cast<uint16_t*>(dst + (c + n) * pitch) =
-                ld_shared_u16(buf + 64u * n + 16u * (k ^ ((static_cast<uint32_t>(n) >> 1) & 3u)) + 2u * n8);
-        __syncwarp();
       }
     }
     if (lane == 0) bulk_wait_group_all();
@@ -1114,9 +1115,14 @@ bool few_rows(int64_t R, int G, int64_t N, int64_t K) {
   return R <= 2 * static_cast<int64_t>(G) || (R <= 8 * static_cast<int64_t>(G) && N * K < (int64_t{1} << 26) / G);
 }
 
-Plan choose(int64_t R, int G, bool a_mn, bool square) {
+// Tiles of 128 x 64 for up to 64 rows a group, and where there are no more of them
+// than SMs: 128 x 4096 x 4096 in 13.8 us (256 x 256: 21.0), 256 x 4096 x 4096 16.4
+// (21.3), 128 x 8192 x 8192 26.8 (35.5), 512 x 2048 x 8192 26.4 (34.8); beyond, 300 x
+// 4096 x 4096 takes 22.3 with 256 x 256.
+Plan choose(int64_t R, int64_t N, int G, int dev, bool a_mn, bool square) {
   if (!square) return {variant<2, 256, 5, BOTH>(), BOTH};
-  if (!a_mn && R <= 64 * static_cast<int64_t>(G)) return {variant<1, 64, 6, COLUMNS>(), COLUMNS};
+  const bool idle = (ceil_div(R, 64) + G - 1) * ceil_div(N, 128) <= device_sms(dev);
+  if (!a_mn && (R <= 64 * static_cast<int64_t>(G) || idle)) return {variant<1, 64, 6, COLUMNS>(), COLUMNS};
   return {variant<2, 256, 5, ROWS>(), ROWS};
 }
 
@@ -1133,9 +1139,9 @@ int run_rows(const Plan& plan, F8Params& p, int dev, tcg_input type, const Opera
   p.other_group = stride_sb;
   p.other_row = B.mn ? 1 : ld_sb;
   p.other_b = plan.mode == BOTH || B.mn ? ld_sb : 1;
-  // an upper bound of the units: a full tile per so many rows and one more per group
+  // an upper bound of the units: a full tile per so many rows, and a partial one more for each group
   const int64_t per = rows ? 128 * cg : plan.ki.bn;
-  const int64_t units = (p.R / per + groups) * p.m_tiles;
+  const int64_t units = (ceil_div(p.R, per) + groups - 1) * p.m_tiles;
   // Where the tiles leave SMs idle, 2 or 4 CTAs share one's contraction (at least
   // four blocks each).
   p.split = 1;
@@ -1174,7 +1180,7 @@ int run_dense(tcg_input type, int64_t M, int64_t N, int64_t K, const void* A, tc
   p.D = D;
   p.ldd = ldd;
   p.d_type = d_type;
-  return run_rows(choose(M, 1, a_mn, sb_square), p, dev, type, {A, a_mn, lda, (a_mn ? K : M) * lda, 1, M, K}, SA, ld_sa,
+  return run_rows(choose(M, N, 1, dev, a_mn, sb_square), p, dev, type, {A, a_mn, lda, (a_mn ? K : M) * lda, 1, M, K}, SA, ld_sa,
                   {B, b_mn, ldb, (b_mn ? K : N) * ldb, 1, N, K}, SB, ld_sb, 0, 1, s);
 }
 
@@ -1217,7 +1223,7 @@ int run_grouped(tcg_input type, int64_t R, int64_t N, int64_t K, int G, const vo
   p.D = D;
   p.ldd = ldd;
   p.d_type = d_type;
-  return run_rows(choose(R, G, false, true), p, dev, type, {A, false, lda, R * lda, 1, R, K}, SA, ld_sa,
+  return run_rows(choose(R, N, G, dev, false, true), p, dev, type, {A, false, lda, R * lda, 1, R, K}, SA, ld_sa,
                   {B, mn, ldb, stride_b, G, N, K}, SB, ld_sb, stride_sb, std::min<int64_t>(G, R), s);
 }
 
@@ -1240,7 +1246,7 @@ int run_wgrad(tcg_input type, int64_t R, int64_t N, int64_t K, int G, const void
   }
   int dev;
   if (int rc = current_device_checked(&dev)) return rc;
-  const KernelInfo ki = choose(R, G, true, false).ki;
+  const KernelInfo ki = variant<2, 256, 5, BOTH>();
   F8Params p;
   std::memset(&p, 0, sizeof p);
   p.offsets = offsets;

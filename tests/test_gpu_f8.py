@@ -86,6 +86,15 @@ def test_other_majors(tcg, M, N, K):
                 dense(tcg, M, N, K, "e4m3", a_major, b_major, square, "f32", 1)
 
 
+@pytest.mark.parametrize("M,N,K", [(1300, 1000, 300), (700, 2057, 72), (2049, 1032, 1), (577, 2600, 8200)])
+def test_large_tiles(tcg, M, N, K):
+    """More tiles of 128 x 64 than SMs: those of 256 x 256, ragged on every side."""
+    for out in ("f32", "bf16"):
+        dense(tcg, M, N, K, "e4m3", "k", "k", True, out)
+        assert "tile 256x256" in tcg.last_plan_string()
+    dense(tcg, M, N, K, "e5m2", "k", "mn", True, "f16", 1)
+
+
 def test_many_tiles(tcg):
     dense(tcg, 3000, 2600, 400, "e4m3", "k", "k", True, "bf16")
     dense(tcg, 40, 20000, 300, "e4m3", "k", "k", True, "f32")
@@ -116,6 +125,12 @@ CASES = [
     ([1, 2, 4, 8, 16, 31, 32, 48], 0, 0, 1030, 2056, 0),
     ([20, 0, 1, 0, 0, 9, 0, 0, 2], 2, 3, 40, 1100, 1),
     ([1] * 1024, 0, 0, 24, 130, 0),
+    # tiles of 256 rows
+    ([700, 0, 300], 3, 4, 2610, 520, 1),
+    ([130, 65, 33, 127, 129, 200], 0, 5, 1304, 136, 0),
+    ([257, 255, 513], 0, 0, 2104, 1000, 0),
+    ([128, 128, 256], 0, 0, 2560, 128, 0),
+    ([400, 1, 0, 31, 600], 1, 0, 1301, 264, 0),
 ]
 
 
@@ -174,7 +189,7 @@ def test_plans(tcg):
     for M, N, K, square, plan in ((8, 1000, 300, True, "8-bit, blocks of 8"), (9, 1000, 300, True, "tile 128x64"),
                                   (16, 1000, 2000, True, "cta_group 2, tile 256x64"),
                                   (16, 1000, 4000, True, "cta_group 4, tile 512x64"),
-                                  (65, 1000, 300, True, "tile 256x256"), (1, 300, 300, False, "tile 256x256")):
+                                  (256, 1000, 300, True, "tile 128x64"), (1300, 1000, 300, True, "tile 256x256"), (1, 300, 300, False, "tile 256x256")):
         dense(tcg, M, N, K, "e4m3", "k", "k", square, "f32")
         assert plan in tcg.last_plan_string(), (M, N, K, tcg.last_plan_string())
 
@@ -183,8 +198,8 @@ def test_plans(tcg):
 def test_other_groups_values_stay_out(tcg, bad):
     """NaN codes in one group's rows or matrix reach no other group, nor do they
     come back through loose rows."""
-    for sizes in ([5, 9, 70, 3], [2, 1, 3, 1]):
-        N, K = 136, 200
+    for sizes, N in (([5, 9, 70, 3], 136), ([2, 1, 3, 1], 136), ([300, 40, 200, 120], 2568)):
+        K = 200
         G, R = len(sizes), sum(sizes) + 4
         off = group_offsets(sizes, 2)
         t_off = torch.from_numpy(off).cuda()
@@ -264,7 +279,7 @@ def test_gradients_against_differences(tcg):
 def test_captured_on_two_streams(tcg):
     """Two graphs on two streams, replayed together: nothing is shared."""
     graphs = []
-    for M, N, K, seed in ((4, 2048, 2048, 1), (300, 512, 1024, 2), (16, 512, 4096, 3)):
+    for M, N, K, seed in ((4, 2048, 2048, 1), (300, 512, 1024, 2), (16, 512, 4096, 3), (1300, 1024, 256, 4)):
         A, a = codes((M, K), "e4m3", seed)
         B, b = codes((N, K), "e4m3", seed + 10)
         SA, sa = scales((blocks(K), M), "e4m3", seed + 20)
