@@ -117,10 +117,6 @@ __device__ __forceinline__ float2 ld_shared_2f32(uint32_t addr) {
   asm volatile("ld.shared.v2.f32 {%0, %1}, [%2];" : "=f"(v.x), "=f"(v.y) : "r"(addr));
   return v;
 }
-// The first n bytes of 16 global -> shared in flight, zeros behind them.
-__device__ __forceinline__ void copy_16(uint32_t to, const void* from, int n) {
-  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(to), "l"(from), "r"(n) : "memory");
-}
 __device__ __forceinline__ void workers_sync() { asm volatile("bar.sync 1, %0;" ::"n"(32 * WARPS) : "memory"); }
 __device__ __forceinline__ bool workers_agree(bool ok) {
   uint32_t all;

@@ -79,5 +79,9 @@ __device__ __forceinline__ void copy_f32(uint32_t to, const float* from, bool ex
 __device__ __forceinline__ void copies_arrive(uint32_t bar) {
   asm volatile("cp.async.mbarrier.arrive.noinc.shared.b64 [%0];" ::"r"(bar) : "memory");
 }
+// The first n bytes of 16 global -> shared in flight, zeros behind them.
+__device__ __forceinline__ void copy_16(uint32_t to, const void* from, int n) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(to), "l"(from), "r"(n) : "memory");
+}
 
 }  // namespace tcg

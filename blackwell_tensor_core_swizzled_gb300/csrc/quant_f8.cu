@@ -10,11 +10,13 @@
 // the rounded scale, 1 of 300 such ties went the other way), and other quotients
 // of 16-bit values lie at least 2^-13 off a tie.
 //
-// Both kernels read X once, keep it in registers between the maximum and the
-// codes, and are bound by HBM.  Rows: a half warp (16-bit types) or a warp holds
-// a block's row, a warp takes 8 rows so that their 8 loads are in flight
-// together and the 8 scales, neighbours in memory, leave as one sector.  Columns:
-// a warp holds 128 rows of 32 or 16 columns.  Squares: a CTA holds a block.
+// All three kernels read X once, keep it on the SM between the maximum and the
+// codes, and are bound by HBM.  Rows: a half warp (16-bit types) or a warp holds a
+// block's row, a warp takes 8 rows so that their 8 loads are in flight together and
+// the 8 scales, neighbours in memory, leave as one sector: 16384 x 8192 bf16 63 us,
+// 6.4 TB/s.  Columns: a warp holds 128 rows of 32 or 16 columns: 16384 x 4096 bf16
+// 35.6 us, 5.7 TB/s, 16384 x 16384 123.5 us, 6.6 TB/s (rows: 34.0 and 121.8).  Squares:
+// a CTA holds a block: 8192 x 8192 bf16 41.3 us, 4.9 TB/s.
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 #include <cuda_fp8.h>
@@ -26,6 +28,7 @@
 
 #include "common.h"
 #include "ptx.cuh"
+#include "ptx_moe.cuh"
 
 namespace tcg {
 
@@ -219,71 +222,90 @@ __global__ void __launch_bounds__(32 * ROW_WARPS) row_kernel(int64_t R, int64_t 
 
 // -------------------------------------------------------------------- columns
 
-// A warp takes 128 rows by four times V columns at a time: lane 4 g + w holds rows
-// g + 8 i and columns V w .. + V.  Its maxima and coders go through shuffles alone,
-// so warps never wait for one another (as CTAs of 128 x 64 with barriers, 16385 x
-// 4096 bf16 took 55 to 67 us).  Four warps share a run of column tiles of one
-// block of rows, whose group each looks up once.
+// A warp takes 128 rows by four times V columns: lane 4 g + w holds rows g + 8 i and
+// columns V w .. + V.  Its maxima and coders go through shuffles alone, so warps never
+// wait for one another (as CTAs of 128 x 64 with barriers, 16385 x 4096 bf16 took 55
+// to 67 us).  ALIGNED: between maxima and codes the words stay in shared memory, each
+// lane's its own, so that 24 warps of an SM have loads in flight (in registers there is
+// room for 12; 8192 x 8192 fp32 70 us, 57 so).  One tile a warp: with runs of tiles,
+// and each lane's next words copied while it codes, 16384 x 16384 bf16 took 143 us
+// instead of 124; with as many CTAs as fit and equal shares for all 20 to 30 % more.
 template <class T, bool WIDE, bool ALIGNED>
-__global__ void __launch_bounds__(32 * COL_WARPS, 3) column_kernel(int64_t R, int64_t C, const T* __restrict__ X,
-                                                                int64_t ldx, bool pow2, int G,
-                                                                const int32_t* __restrict__ offsets,
-                                                                uint8_t* __restrict__ Q, int64_t ldq,
-                                                                float* __restrict__ scale, int64_t ld_scale, int run) {
+__global__ void __launch_bounds__(32 * COL_WARPS, ALIGNED ? 6 : 3)
+    column_kernel(int64_t R, int64_t C, const T* __restrict__ X, int64_t ldx, bool pow2, int G,
+                  const int32_t* __restrict__ offsets, uint8_t* __restrict__ Q, int64_t ldq, float* __restrict__ scale,
+                  int64_t ld_scale, int64_t across) {
   constexpr int V = Word<T>::V;
   constexpr int COLS = 4 * V, PER = BLOCK / 8;
-  const int lane = threadIdx.x & 31, g8 = lane >> 2, w4 = lane & 3;
-  const int64_t tiles = (C + COLS - 1) / COLS, runs = (tiles + run - 1) / run;
-  const int64_t slot = blockIdx.x / runs;  // the block's row of scales
-  const int64_t first_tile = blockIdx.x % runs * run, end_tile = min(first_tile + run, tiles);
+  constexpr int UNROLL = ALIGNED ? 4 : PER;  // addresses of all sixteen words would spill
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, g8 = lane >> 2, w4 = lane & 3;
+  const int64_t slot = blockIdx.x / across;  // the block's row of scales
+  const int64_t c = ((blockIdx.x % across) * COL_WARPS + warp) * COLS + V * w4;
+  const int n = static_cast<int>(max(int64_t{0}, min(static_cast<int64_t>(V), C - c)));
   griddep_wait();
   int64_t lo = slot * BLOCK, end = R;
   if (offsets) {
     // block j of group g has slot offsets[g] / 128 + g + j; the slots of groups rise
-    int g = -1;
+    int g = -1, first = 0, next = 0;
     for (int i = lane; i < G; i += 32) {
-      const int64_t o = min(max(static_cast<int64_t>(offsets[i]), int64_t{0}), R);
-      g += o / BLOCK + i <= slot;
+      const int o = min(max(offsets[i], 0), static_cast<int>(R)), o1 = offsets[i + 1];
+      if (o / BLOCK + i <= slot) ++g, first = o, next = o1;
     }
     g = __reduce_add_sync(0xffffffffu, g) + 31;
     if (g < 0) return;
-    const int64_t first = min(max(static_cast<int64_t>(offsets[g]), int64_t{0}), R);
-    end = min(max(static_cast<int64_t>(offsets[g + 1]), first), R);
+    first = __shfl_sync(0xffffffffu, first, g);  // lane g % 32 met g last
+    end = min(max(__shfl_sync(0xffffffffu, next, g), first), static_cast<int>(R));
     lo = first + (slot - first / BLOCK - g) * BLOCK;
   }
-  if (lo >= end) return;  // a slot that no group uses keeps its value
+  if (lo >= end || c - V * w4 >= C) return;  // a slot that no group uses keeps its value
   const int rows = static_cast<int>(min(static_cast<int64_t>(BLOCK), end - lo));
-  for (int64_t tile = first_tile + (threadIdx.x >> 5); tile < end_tile; tile += COL_WARPS) {
-    const int64_t c = tile * COLS + V * w4;
-    const int n = static_cast<int>(max(int64_t{0}, min(static_cast<int64_t>(V), C - c)));
-    Word<T> x[PER];
-#pragma unroll
-    for (int i = 0; i < PER; ++i)
-      x[i].load(X + (lo + g8 + 8 * i) * ldx + c, g8 + 8 * i < rows ? n : 0, ALIGNED);
-    Word<T> top;  // of the columns
-#pragma unroll
-    for (int j = 0; j < 4; ++j) {
-      top.w[j] = 0;
-#pragma unroll
-      for (int i = 0; i < PER; ++i) top.w[j] = most<T>(top.w[j], x[i].w[j]);
-#pragma unroll
-      for (int d = 16; d >= 4; d >>= 1) top.w[j] = most<T>(top.w[j], __shfl_xor_sync(0xffffffffu, top.w[j], d));
+  __shared__ uint4 kept[ALIGNED ? COL_WARPS : 1][ALIGNED ? PER : 1][32];
+  Word<T> x[ALIGNED ? 1 : PER];
+  const auto word = [&](int i) -> const Word<T>& {
+    if constexpr (ALIGNED) {
+      const uint4 v = kept[warp][i][lane];
+      x[0].w[0] = v.x, x[0].w[1] = v.y, x[0].w[2] = v.z, x[0].w[3] = v.w;
+      return x[0];
+    } else {
+      return x[i];
     }
-    float mine = 0.0f;  // the largest of column V w4 + g8
+  };
+#pragma unroll UNROLL
+  for (int i = 0; i < PER; ++i) {
+    const bool exists = n > 0 && g8 + 8 * i < rows;
+    const T* from = X + (lo + g8 + 8 * i) * ldx + c;
+    if constexpr (ALIGNED)
+      copy_16(smem_u32(&kept[warp][i][lane]), exists ? from : X, exists ? 16 : 0);
+    else
+      x[i].load(from, exists ? n : 0, false);
+  }
+  if constexpr (ALIGNED) asm volatile("cp.async.wait_all;" ::: "memory");
+  Word<T> top = {};  // of the columns
 #pragma unroll
-    for (int j = 0; j < V; ++j)
-      if (g8 % V == j) mine = top.value(j);
-    float s;
-    const Coder my = make_coder<WIDE>(mine, pow2, s);
-    if (g8 < V && c + g8 < C) scale[slot * ld_scale + c + g8] = s;
-    Coder k[V];
+  for (int i = 0; i < PER; ++i) {
+    const Word<T>& v = word(i);
 #pragma unroll
-    for (int j = 0; j < V; ++j) k[j] = from_lane(my, 4 * j + w4);
+    for (int j = 0; j < 4; ++j) top.w[j] = most<T>(top.w[j], v.w[j]);
+  }
 #pragma unroll
-    for (int i = 0; i < PER; ++i) {
-      if (g8 + 8 * i >= rows) break;
-      store_codes<WIDE>(x[i], Q + (lo + g8 + 8 * i) * ldq + c, n, ALIGNED, [&](int j) { return k[j]; });
-    }
+  for (int j = 0; j < 4; ++j)
+#pragma unroll
+    for (int d = 16; d >= 4; d >>= 1) top.w[j] = most<T>(top.w[j], __shfl_xor_sync(0xffffffffu, top.w[j], d));
+  float mine = 0.0f;  // the largest of column V w4 + g8
+#pragma unroll
+  for (int j = 0; j < V; ++j)
+    if (g8 % V == j) mine = top.value(j);
+  float s;
+  const Coder my = make_coder<WIDE>(mine, pow2, s);
+  if (g8 < V && c + g8 < C) scale[slot * ld_scale + c + g8] = s;
+  Coder k[V];
+#pragma unroll
+  for (int j = 0; j < V; ++j) k[j] = from_lane(my, 4 * j + w4);
+#pragma unroll UNROLL
+  for (int i = 0; i < PER; ++i) {
+    const Word<T>& v = word(i);
+    if (g8 + 8 * i < rows)
+      store_codes<WIDE>(v, Q + (lo + g8 + 8 * i) * ldq + c, n, ALIGNED, [&](int j) { return k[j]; });
   }
   griddep_launch_dependents();
 }
@@ -356,7 +378,7 @@ int64_t ceil_div(int64_t a, int64_t b) { return (a + b - 1) / b; }
 
 template <class T, bool WIDE, bool ALIGNED>
 int run_typed(tcg_f8_blocks blocks, bool pow2, int64_t R, int64_t C, const T* X, int64_t ldx, int G,
-              const int32_t* offsets, uint8_t* Q, int64_t ldq, float* scale, int64_t ld_scale, int sms, cudaStream_t s) {
+              const int32_t* offsets, uint8_t* Q, int64_t ldq, float* scale, int64_t ld_scale, cudaStream_t s) {
   if (blocks == TCG_F8_ROW) {
     constexpr int64_t V = Word<T>::V;
     const int64_t col_warps = ceil_div(C, 32 * V);
@@ -368,11 +390,10 @@ int run_typed(tcg_f8_blocks blocks, bool pow2, int64_t R, int64_t C, const T* X,
     return launch(square_kernel<T, WIDE, ALIGNED>, ceil_div(R, BLOCK) * tiles, SQUARE_THREADS, s, R, C, X, ldx, pow2, Q,
                   ldq, scale, ld_scale, tiles);
   }
-  const int64_t tiles = ceil_div(C, 64 / static_cast<int64_t>(sizeof(T))), slots = offsets ? R / BLOCK + G : ceil_div(R, BLOCK);
-  // runs of up to 8 tiles a warp, as long as 16 CTAs an SM are left
-  const int run = COL_WARPS * static_cast<int>(std::max<int64_t>(1, std::min<int64_t>(8, slots * tiles / (16 * COL_WARPS * sms))));
-  return launch(column_kernel<T, WIDE, ALIGNED>, slots * ceil_div(tiles, run), 32 * COL_WARPS, s, R, C, X, ldx, pow2, G,
-                offsets, Q, ldq, scale, ld_scale, run);
+  const int64_t slots = offsets ? R / BLOCK + G : ceil_div(R, BLOCK);
+  const int64_t across = ceil_div(C, COL_WARPS * 64 / static_cast<int64_t>(sizeof(T)));
+  return launch(column_kernel<T, WIDE, ALIGNED>, slots * across, 32 * COL_WARPS, s, R, C, X, ldx, pow2, G, offsets, Q,
+                ldq, scale, ld_scale, across);
 }
 
 int run_quantize(tcg_input q_type, tcg_f8_blocks blocks, int pow2, int64_t R, int64_t C, tcg_dtype x_type,
@@ -395,7 +416,6 @@ int run_quantize(tcg_input q_type, tcg_f8_blocks blocks, int pow2, int64_t R, in
   if (at(X) % size || at(scale) % 4 || at(offsets) % 4) return TCG_ERR_ALIGNMENT;
   int dev;
   if (int rc = current_device_checked(&dev)) return rc;
-  const int sms = device_sms(dev);
   const int64_t V = 16 / size;  // elements of a 16-byte word
   const bool aligned = at(X) % 16 == 0 && ldx % V == 0 && C % V == 0 && at(Q) % V == 0 && ldq % V == 0;
   const auto typed = [&](auto z) {
@@ -404,10 +424,10 @@ int run_quantize(tcg_input q_type, tcg_f8_blocks blocks, int pow2, int64_t R, in
     uint8_t* q = static_cast<uint8_t*>(Q);
     const bool p = pow2 != 0;
     if (q_type == TCG_IN_E5M2)
-      return aligned ? run_typed<T, true, true>(blocks, p, R, C, x, ldx, G, offsets, q, ldq, scale, ld_scale, sms, s)
-                     : run_typed<T, true, false>(blocks, p, R, C, x, ldx, G, offsets, q, ldq, scale, ld_scale, sms, s);
-    return aligned ? run_typed<T, false, true>(blocks, p, R, C, x, ldx, G, offsets, q, ldq, scale, ld_scale, sms, s)
-                   : run_typed<T, false, false>(blocks, p, R, C, x, ldx, G, offsets, q, ldq, scale, ld_scale, sms, s);
+      return aligned ? run_typed<T, true, true>(blocks, p, R, C, x, ldx, G, offsets, q, ldq, scale, ld_scale, s)
+                     : run_typed<T, true, false>(blocks, p, R, C, x, ldx, G, offsets, q, ldq, scale, ld_scale, s);
+    return aligned ? run_typed<T, false, true>(blocks, p, R, C, x, ldx, G, offsets, q, ldq, scale, ld_scale, s)
+                   : run_typed<T, false, false>(blocks, p, R, C, x, ldx, G, offsets, q, ldq, scale, ld_scale, s);
   };
   if (x_type == TCG_F32) return typed(float{});
   if (x_type == TCG_F16) return typed(__half{});
