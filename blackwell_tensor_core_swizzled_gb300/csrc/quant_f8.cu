@@ -16,7 +16,7 @@
 // the 8 scales, neighbours in memory, leave as one sector: 16384 x 8192 bf16 63 us,
 // 6.4 TB/s.  Columns: a warp holds 128 rows of 32 or 16 columns: 16384 x 4096 bf16
 // 35.6 us, 5.7 TB/s, 16384 x 16384 123.5 us, 6.6 TB/s (rows: 34.0 and 121.8).  Squares:
-// a CTA holds a block: 8192 x 8192 bf16 41.3 us, 4.9 TB/s.
+// a CTA holds a block: 8192 x 8192 bf16 34.6 us, 5.8 TB/s.
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 #include <cuda_fp8.h>
@@ -312,12 +312,12 @@ __global__ void __launch_bounds__(32 * COL_WARPS, ALIGNED ? 6 : 3)
 
 // -------------------------------------------------------------------- squares
 
-// A block a CTA: warp w holds rows 16 w .. + 16, in words of 16 bytes.
+// A block a CTA, in words of 16 bytes.  Four CTAs an SM of 16-bit values (8192 x 8192:
+// 34.6 us; three 41, five 44), two of fp32 (60 us; one 92, three 68).
 template <class T, bool WIDE, bool ALIGNED>
-__global__ void __launch_bounds__(SQUARE_THREADS) square_kernel(int64_t R, int64_t C, const T* __restrict__ X,
-                                                                int64_t ldx, bool pow2, uint8_t* __restrict__ Q,
-                                                                int64_t ldq, float* __restrict__ scale,
-                                                                int64_t ld_scale, int64_t col_tiles) {
+__global__ void __launch_bounds__(SQUARE_THREADS, ALIGNED && sizeof(T) == 2 ? 4 : 2)
+    square_kernel(int64_t R, int64_t C, const T* __restrict__ X, int64_t ldx, bool pow2, uint8_t* __restrict__ Q,
+                  int64_t ldq, float* __restrict__ scale, int64_t ld_scale, int64_t col_tiles) {
   constexpr int V = Word<T>::V;
   constexpr int ACROSS = BLOCK / V, DOWN = SQUARE_THREADS / ACROSS, PER = BLOCK / DOWN;
   __shared__ float top[SQUARE_THREADS / 32];
