@@ -472,7 +472,7 @@ int tcg_gemm_f8_grouped_wgrad(tcg_input in_type, int64_t R, int64_t N, int64_t K
 typedef struct {
   tcg_input x_type;      /* X: TCG_IN_F16 or TCG_IN_BF16 */
   tcg_input w_type;      /* weights: x_type, or TCG_IN_E4M3 with fp32 scales for each 128 x 128 */
-  int64_t T, H, I;       /* H, I: whole 16-byte words of weights; T <= 64 */
+  int64_t T, H, I;       /* H, I: whole 16-byte words of weights, < 2^29; T <= 64 */
   int topk, E;           /* topk <= 64, E <= 1024 */
   const void* X; int64_t ldx;              /* [T][H], 16-byte aligned base and rows */
   const int32_t* expert;                   /* [T][topk] */
@@ -573,8 +573,8 @@ const char* tcg_last_error_string(void);
 int tcg_last_launch_count(void);
 
 /* How the most recent product on this thread was run (kernel tile, CTA group,
- * clusters, one pass / split-K / stream-K, operand swap; for the grouped and
- * 4-bit products their own), as text for logs and tests; empty if the call
+ * clusters, one pass / split-K / stream-K, operand swap; for the grouped,
+ * 8-bit and 4-bit products their own; tcg_moe_few has none), as text for logs and tests; empty if the call
  * queued nothing or failed.  The string is
  * formatted by this call, owned by the library and valid until this thread's
  * next tcg_last_plan_string call. */

@@ -473,7 +473,9 @@ def test_moe_few_validation_before_any_device_work(tcg):
     assert call(T=65) == tcg.ERR_UNSUPPORTED
     assert call(topk=65) == tcg.ERR_UNSUPPORTED
     assert call(E=1025) == tcg.ERR_UNSUPPORTED
-    assert call(H=1 << 30) == tcg.ERR_UNSUPPORTED
+    for n in ("H", "I"):  # a row of 16-bit weights would reach 2^30 bytes
+        assert call(w_type=1, **{n: 1 << 29}) == tcg.ERR_UNSUPPORTED
+    assert tcg.moe_few_work_bytes(1, 1, 1 << 29) == -1
     for p in ("X", "expert", "W1", "W2", "work", "Y", "s1", "s3", "s2"):
         assert call(**{p: None}) == tcg.ERR_INVALID, p
     assert call(ldx=56) == tcg.ERR_INVALID
