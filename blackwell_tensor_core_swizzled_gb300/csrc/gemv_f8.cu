@@ -14,7 +14,8 @@
 // warps' sums are added in shared memory, in order.  (tcgen05 wants tiles of 128
 // rows n: too few of them for all SMs, and 500 cycles a block between its waits and
 // commits where few columns take the pipe 50: 1 x 8192 x 8192 19 us there, 15 here;
-// 1 x 4096 x 4096 11 and 7.)
+// 1 x 4096 x 4096 11 and 7.)  1 x 8192 x 8192 runs at 4.5 TB/s, 5 us of its 15 being
+// the start: launch, cold code, the first bytes; 1 x 16384 x 4096 16.3 us.
 #include <cuda.h>
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>

@@ -111,6 +111,24 @@ def test_empty_contraction_and_empty_outputs(tcg):
     assert tcg.last_launch_count() == 0 and bool((D == 7.0).all())
 
 
+def test_grouped_without_rows_or_contraction(tcg):
+    off = torch.zeros(4, dtype=torch.int32, device="cuda")
+    W = torch.full((3, 40, 48), 7.0, device="cuda")
+    tcg.gemm_f8_grouped_wgrad(tcg.IN_E4M3, 0, 40, 48, 3, None, 0, None, 0, None, 0, None, 0, off, W, tcg.F32, 48, 0)
+    ok(tcg)
+    assert not to_host(W).any()
+    D = torch.full((5, 40), 7.0, device="cuda")
+    tcg.gemm_f8_grouped(tcg.IN_E4M3, 0, 40, 48, 3, None, 0, None, 0, off, None, tcg.K_MAJOR, 0, 0, None, 0, 0, D, tcg.F32,
+                        40)
+    assert tcg.last_launch_count() == 0 and bool((D == 7.0).all())
+    off.fill_(5)
+    off[0] = 0
+    tcg.gemm_f8_grouped(tcg.IN_E4M3, 5, 40, 0, 3, None, 0, None, 0, off, None, tcg.K_MAJOR, 0, 0, None, 0, 0, D, tcg.F32,
+                        40)
+    ok(tcg)
+    assert not to_host(D).any()
+
+
 CASES = [
     # sizes of the groups, loose rows before and after, N, K, rows padded by
     ([1], 0, 0, 16, 16, 0),
