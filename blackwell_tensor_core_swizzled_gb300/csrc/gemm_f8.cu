@@ -20,7 +20,7 @@
 // ROWS: a lane holds one row, so that one factor, the product of the two scales,
 // serves all of its 128 columns.  (The first form, rows on the columns' side and a
 // factor for each read from shared memory by every lane, took 851 us for
-// 8192 x 8192 x 8192, where this takes 450.)
+// 8192 x 8192 x 8192.)
 // COLUMNS: few rows cost few columns, any multiple of 16; the result is stored
 // transposed.  Where its tiles leave SMs idle, two or four CTAs share a tile's
 // contraction and add their sums through the cluster's shared memory.
@@ -30,14 +30,16 @@
 // MMAs beyond are not issued.
 //
 // What bounds them: a block of a pair's 256 x 256 takes the tensor pipe 512 cycles,
-// and the epilogue about 500 of waiting for commits and tensor-memory reads, one
-// after the other, beside 300 of multiply-adds (BOTH: 512).  With the two
-// accumulators that is 600 to 650 cycles a block for ROWS, 770 for BOTH.
-// 8192 x 8192 x 8192 in 421 us, 2.61 PFLOP/s; back to back for seconds the power
-// limit holds the clock at 1.91 GHz and it takes 450.  The weight gradient of
-// 4096 x 4096 over 8191 rows: 198 us, 1.39 PFLOP/s, of which 16 % is the last of 3.4
-// waves of tiles.  More warps for the epilogue (12, 16), reads of tensor memory a step
-// ahead, or one warp's arrival for all made each of them slower.
+// its 32 KB for each SM about 500 of what L2 delivers, and the epilogue's multiply-adds
+// 256 (BOTH: 512) beside as many of reads from tensor memory.  8192 x 8192 x 8192 takes
+// 411 us in bursts, 2.68 PFLOP/s (345 if the multiply-adds are left out, so much is the
+// operands' delivery); back to back for seconds the power limit holds the clock at 1.91
+// GHz and it takes about 445.  The weight gradient of 4096 x 4096 over 8191 rows takes
+// 184 us, 1.50 PFLOP/s (136 without the multiply-adds, 105 without the reads as well):
+// scaling both ways, and 16 % for the last of 3.4 waves of tiles.  More warps for the
+// epilogue (12, 16), an accumulator in two halves with barriers of their own (an MMA of
+// 128 columns takes most of the time of 256: 565 us), reads of tensor memory a step
+// ahead, or one warp's arrival for all made them slower.
 //
 // A warp copies the blocks' scales ahead into a shared ring; one warp each brings P
 // and Q, another decodes the tile list.
@@ -436,7 +438,7 @@ __global__ void __launch_bounds__(F8Cfg<CG, BN, STAGES, MODE>::THREADS, 1) f8_ke
   // of the 384 x 168 registers at launch few for the four warps that feed, more for
   // those that hold sums
   if (warp < 4) {
-    set_registers<false, 88>();
+    set_registers<false, 56>();
     if (warp == 3) {
       // ------------------------------------------- tile list and blocks' scales
       uint32_t n = 0, it = 0;
@@ -651,7 +653,7 @@ __global__ void __launch_bounds__(F8Cfg<CG, BN, STAGES, MODE>::THREADS, 1) f8_ke
     }
   } else {
     // ------------------------------------------------------------ epilogue
-    set_registers<true, 208>();
+    set_registers<true, 224>();
     const int q = warp & 3;            // TMEM lane quadrant
     const int part = (warp - 4) >> 2;  // 32-column chunks part, part + PARTS, ...
     constexpr int ACROSS = 32 * C::PARTS;  // a warp's chunks of 32 columns lie so far apart
@@ -820,31 +822,37 @@ __global__ void __launch_bounds__(F8Cfg<CG, BN, STAGES, MODE>::THREADS, 1) f8_ke
             const uint32_t r = __float_as_uint(ld_shared_f32(at + 4u * (MODE == BOTH ? BN + 32 * q + 8 * h + (lane >> 2) : BN)));
             row[h] = pair(r, r);
           }
-          // a chunk's two fragments of 16 rows by 32 columns at a time
+          // chunks' fragments of 16 rows by 32 columns, STEP chunks (or the one) at a time
           const uint32_t from = lanes + b * BN + 32 * part;
-  #pragma unroll
-          for (int i = 0; i < MINE; ++i) {
-            if (i >= mine) break;
-            uint32_t r[2][16];
-  #pragma unroll
-            for (int h = 0; h < 2; ++h)
-              tmem_ld_16x256b_x4(from + ACROSS * i + (static_cast<uint32_t>(h) << 20), r[h]);
-            uint64_t f[4];  // factors of this lane's columns 8 j + 2 (lane % 4), + 1
-  #pragma unroll
-            for (int j = 0; j < 4; ++j) {
-              f[j] = ld_shared_b64(at + 4u * (32 * part + ACROSS * i + 8 * j + 2 * (lane & 3)));
-              if constexpr (MODE != BOTH) f[j] = mul2(f[j], row[0]);
-            }
-            tc_wait_ld();
-  #pragma unroll
-            for (int h = 0; h < 2; ++h)
-  #pragma unroll
-              for (int k = 0; k < 8; ++k) {
-                if constexpr (MODE == BOTH)
-                  add_scaled(sum[i][h][k], r[h][2 * k], r[h][2 * k + 1], f[k / 2], row[2 * h + (k & 1)]);
-                else
-                  add_scaled(sum[i][h][k], r[h][2 * k], r[h][2 * k + 1], f[k / 2]);
+          constexpr int STEP = MINE < 2 ? MINE : 2;
+#pragma unroll
+          for (int i0 = 0; i0 < MINE; i0 += STEP) {
+            if (i0 >= mine) break;
+            uint32_t r[STEP][2][16];
+#pragma unroll
+            for (int i = 0; i < STEP; ++i)
+#pragma unroll
+              for (int h = 0; h < 2; ++h)
+                tmem_ld_16x256b_x4(from + ACROSS * (i0 + i) + (static_cast<uint32_t>(h) << 20), r[i][h]);
+#pragma unroll
+            for (int i = 0; i < STEP; ++i) {
+              uint64_t f[4];  // factors of this lane's columns 8 j + 2 (lane % 4), + 1
+#pragma unroll
+              for (int j = 0; j < 4; ++j) {
+                f[j] = ld_shared_b64(at + 4u * (32 * part + ACROSS * (i0 + i) + 8 * j + 2 * (lane & 3)));
+                if constexpr (MODE != BOTH) f[j] = mul2(f[j], row[0]);
               }
+              if (i == 0) tc_wait_ld();
+#pragma unroll
+              for (int h = 0; h < 2; ++h)
+#pragma unroll
+                for (int k = 0; k < 8; ++k) {
+                  if constexpr (MODE == BOTH)
+                    add_scaled(sum[i0 + i][h][k], r[i][h][2 * k], r[i][h][2 * k + 1], f[k / 2], row[2 * h + (k & 1)]);
+                  else
+                    add_scaled(sum[i0 + i][h][k], r[i][h][2 * k], r[i][h][2 * k + 1], f[k / 2]);
+                }
+            }
           }
           tc_fence_before();
           __syncwarp();
