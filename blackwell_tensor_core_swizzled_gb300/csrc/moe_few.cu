@@ -24,7 +24,7 @@
 // for each kernel, half of the second's hidden; 100 MB at 6.8 TB/s are 14.8); 32 tokens
 // x 4 of 32 f16 experts of 4096 x 2048, 252 us, 6.3 TB/s; 8 tokens x 8 of 64 experts of
 // 4096 x 1024 E4M3 104 us, 5.1 TB/s.  With more tokens an expert than eight the passes
-// from L2 count: 32 x 8 of 64 such experts 230 us.
+// from L2 count: 32 x 8 of 64 such experts 202 us.
 //
 // The second kernel starts while the first runs (it needs half an SM): its lists
 // are made and its ring is full when the first ends.
@@ -59,8 +59,6 @@ constexpr int64_t MAX_EXTENT = int64_t{1} << 29;  // rows' bytes are counted in 
 constexpr int WARPS = 8;                    // that multiply; two more bring weights, and x and scales
 constexpr int FEW_THREADS = 32 * (WARPS + 2);
 constexpr int SLAB_BYTES = 16 * 128;
-constexpr int CHUNK = 128 * WARPS;          // bytes of a row in a stage
-constexpr int TILE_BYTES = SLAB_BYTES * WARPS;
 constexpr int MAX_STAGES = 6;
 constexpr int MAX_SMEM = 232448;
 
@@ -92,6 +90,15 @@ struct Job {
   int expert, first, tokens, block;  // first: its first pair; block: of the expert's tokens, by eights
 };
 
+// Slabs of 128 bytes of each row in a stage: one a warp, or, where h comes in two
+// parts for more than eight tokens against 8-bit weights (33 KB to 16 KB of them), one
+// for two warps, so that two CTAs fit an SM: 32 tokens x 8 of 64 experts of 4096 x 1024
+// 202 us, 229 with whole stages (16 tokens, where two CTAs fit either way, 60 and 58;
+// one token, if its few columns came so too, 31.8 and 30.3).
+__host__ __device__ constexpr int slabs_a_stage(bool second, int size, bool direct) {
+  return second && size == 1 && !direct ? WARPS / 2 : WARPS;
+}
+
 // Shared memory from the sizes: ring stages of weights, then of x and scales,
 // then lists.
 struct Layout {
@@ -99,9 +106,9 @@ struct Layout {
   int x_row, x_part, x_stage;  // of x: a column, hi or lo of all columns, a stage with its scales
   int x, sums, masks, list, jobs, token, weight, bars, bytes;
   __host__ __device__ Layout(int T, int topk, int E, bool second, int size, int matrices, int stages) {
-    const int pairs = T * topk, most = pairs < E ? pairs : E;
-    stage = TILE_BYTES * matrices;
-    x_row = CHUNK / size * 2 + (size == 1 ? 16 : 64);  // so that a quarter warp's words lie in different banks
+    const int pairs = T * topk, most = pairs < E ? pairs : E, slabs = slabs_a_stage(second, size, T <= 8);
+    stage = SLAB_BYTES * slabs * matrices;
+    x_row = 128 * slabs / size * 2 + (size == 1 ? 16 : 64);  // so that a quarter warp's words lie in different banks
     x_part = x_row * (T < 8 ? T : 8);
     x_stage = x_part * (second ? 2 : 1) + 2 * WARPS * 4;
     int at = stages * stage;
@@ -208,6 +215,9 @@ __global__ void __launch_bounds__(FEW_THREADS, 2) few_kernel(const __grid_consta
   const uint32_t raw = smem_u32(smem_raw);
   const uint32_t sbase = (raw + 1023u) & ~1023u;
   uint8_t* gbase = smem_raw + (sbase - raw);
+  constexpr int SLABS = slabs_a_stage(SECOND, W8 ? 1 : 2, DIRECT);
+  constexpr int CHUNK = 128 * SLABS;  // bytes of a row in a stage
+  constexpr int TILE_BYTES = SLAB_BYTES * SLABS;
   const Layout at(p.T, p.topk, p.E, SECOND, W8 ? 1 : 2, p.matrices, p.stages);
   const int stage_bytes = at.stage, stages = p.stages;
   unsigned long long* masks = reinterpret_cast<unsigned long long*>(gbase + at.masks);
@@ -306,7 +316,7 @@ __global__ void __launch_bounds__(FEW_THREADS, 2) few_kernel(const __grid_consta
   const int chunks = (p.row_bytes + CHUNK - 1) / CHUNK;
   const int passes = SECOND ? jobs : 1;  // over rows, of a unit
   // slabs of chunk c that exist
-  auto slabs_of = [&](int c) { return min(WARPS, (p.row_bytes - c * CHUNK + 127) / 128); };
+  auto slabs_of = [&](int c) { return min(SLABS, (p.row_bytes - c * CHUNK + 127) / 128); };
 
   if (warp == WARPS) {
     // --------------------------------------------------- producer of weights
@@ -326,7 +336,7 @@ __global__ void __launch_bounds__(FEW_THREADS, 2) few_kernel(const __grid_consta
             if (p.row_bytes % 128 == 0 || c + 1 < chunks) {
               mbar_arrive_expect_tx(full_bar(s), static_cast<uint32_t>(stage_bytes));
               for (int m = 0; m < p.matrices; ++m)
-                tma_load_4d(to + TILE_BYTES * m, &p.slab[m], 0, n0, c * WARPS, e, full_bar(s));
+                tma_load_4d(to + TILE_BYTES * m, &p.slab[m], 0, n0, c * SLABS, e, full_bar(s));
             } else {
               const int n = slabs_of(c);
               mbar_arrive_expect_tx(full_bar(s), static_cast<uint32_t>(SLAB_BYTES * n * p.matrices));
@@ -420,8 +430,8 @@ __global__ void __launch_bounds__(FEW_THREADS, 2) few_kernel(const __grid_consta
               }
           }
           if constexpr (W8) {
-            const int m = lane >> 3, slab = c * WARPS + (lane & 7);
-            if (m < p.matrices)
+            const int m = lane >> 3, slab = c * SLABS + (lane & 7);
+            if (m < p.matrices && (lane & 7) < SLABS)
               copy_f32(to + PARTS * at.x_part + 4u * lane, p.S[m] + scale_at + slab, slab * 128 < p.row_bytes);
           }
           copies_arrive(full_bar(s));
@@ -438,6 +448,8 @@ __global__ void __launch_bounds__(FEW_THREADS, 2) few_kernel(const __grid_consta
 
   // ----------------------------------------------------------------- workers
   const int g = lane >> 2, c4 = lane & 3;
+  constexpr int SHARE = WARPS / SLABS;  // warps of a slab, each half of its rows' bytes
+  const int mine = warp / SHARE;        // this warp's slab
   uint32_t s = 0, ph = 0;
   float acc[M][4];
   bool ok = true;
@@ -451,16 +463,17 @@ __global__ void __launch_bounds__(FEW_THREADS, 2) few_kernel(const __grid_consta
         ok = false;
         return;
       }
-      if (c * CHUNK + 128 * warp < p.row_bytes) {
+      if (c * CHUNK + 128 * mine < p.row_bytes) {
         const uint32_t xs = sbase + at.x + s * at.x_stage;
         float sc[M];
         if constexpr (W8) {
 #pragma unroll
-          for (int m = 0; m < M; ++m) sc[m] = ld_shared_f32(xs + PARTS * at.x_part + 32u * m + 4u * warp);
+          for (int m = 0; m < M; ++m) sc[m] = ld_shared_f32(xs + PARTS * at.x_part + 32u * m + 4u * mine);
         }
 #pragma unroll
-        for (int h = 0; h < 2; ++h) {
-          const int k = warp * (128 / SIZE) + CODES * (c4 + 4 * h);  // of the stage
+        for (int i = 0; i < 2 / SHARE; ++i) {
+          const int h = SHARE == 1 ? i : warp & 1;
+          const int k = mine * (128 / SIZE) + CODES * (c4 + 4 * h);  // of the stage
           uint4 x[PARTS][WORDS / 4];
 #pragma unroll
           for (int q = 0; q < PARTS; ++q)
@@ -471,7 +484,7 @@ __global__ void __launch_bounds__(FEW_THREADS, 2) few_kernel(const __grid_consta
 #pragma unroll
           for (int m = 0; m < M; ++m) {
             if (m >= p.matrices) break;
-            const uint32_t slab = sbase + s * stage_bytes + TILE_BYTES * m + SLAB_BYTES * warp;
+            const uint32_t slab = sbase + s * stage_bytes + TILE_BYTES * m + SLAB_BYTES * mine;
 #pragma unroll
             for (int r = 0; r < 2; ++r) {
               const uint4 v = ld_shared_v4(slab + 128u * (g + 8 * r) + 16u * ((c4 + 4 * h) ^ g));
@@ -552,7 +565,7 @@ __global__ void __launch_bounds__(FEW_THREADS, 2) few_kernel(const __grid_consta
       workers_sync();
     }
   } else {
-    float* mine = sums + warp * p.T * 16;
+    float* own = sums + warp * p.T * 16;
     for (int u = blockIdx.x; u < units; u += gridDim.x) {
       const int n0 = u * 16;
       clear();
@@ -561,10 +574,10 @@ __global__ void __launch_bounds__(FEW_THREADS, 2) few_kernel(const __grid_consta
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
           const int t = 2 * c4 + (i & 1);
-          if (t < p.T) mine[t * 16 + g + 8 * (i >> 1)] = acc[0][i];
+          if (t < p.T) own[t * 16 + g + 8 * (i >> 1)] = acc[0][i];
         }
       } else {
-        for (int i = lane; i < p.T * 16; i += 32) mine[i] = 0.0f;
+        for (int i = lane; i < p.T * 16; i += 32) own[i] = 0.0f;
         __syncwarp();
         for (int j = 0; j < jobs && ok; ++j) {
           const Job a = job[j];
@@ -572,7 +585,7 @@ __global__ void __launch_bounds__(FEW_THREADS, 2) few_kernel(const __grid_consta
 #pragma unroll
           for (int i = 0; i < 4; ++i) {
             const int col = 2 * c4 + (i & 1);
-            if (col < a.tokens) mine[token[a.first + col] * 16 + g + 8 * (i >> 1)] += acc[0][i];
+            if (col < a.tokens) own[token[a.first + col] * 16 + g + 8 * (i >> 1)] += acc[0][i];
           }
           clear();
           __syncwarp();
@@ -643,9 +656,10 @@ int launch(Kernel kernel, const FewParams& p, int64_t grid, int smem, cudaStream
 }
 
 // Maps of one matrix of each expert: `rows` rows of `bytes`, `ld` bytes apart.
-int weight_maps(FewParams* p, int i, const void* W, int64_t bytes, int64_t rows, int64_t ld, int64_t stride) {
+int weight_maps(FewParams* p, int i, const void* W, int64_t bytes, int64_t rows, int64_t ld, int64_t stride,
+                int slabs) {
   if (bytes >= 128)
-    if (int rc = make_slab_map(&p->slab[i], W, 128, rows, bytes / 128, p->E, ld, stride, 16, WARPS)) return rc;
+    if (int rc = make_slab_map(&p->slab[i], W, 128, rows, bytes / 128, p->E, ld, stride, 16, slabs)) return rc;
   return make_byte_map(&p->edge[i], W, bytes, rows, p->E, ld, stride, 128, 16);
 }
 
@@ -669,19 +683,16 @@ struct Shape {
   int stages, smem, ctas;
 };
 
-// Two CTAs share an SM where half its memory holds 32 KB of weights and more: twice
+// Two CTAs share an SM where half its memory holds 24 KB of weights and more: twice
 // the warps hide their latencies (1 token x 8 of 128 experts of 4096 x 1024, E4M3:
 // 30 us, 43 with one; 32 tokens x 4 of 32 f16 experts of 4096 x 2048 263 and 321).
 // Else one has what fits.
 Shape shape(int T, int topk, int E, bool second, int size, int matrices) {
-  for (int n = MAX_STAGES / matrices; n * matrices >= 2; --n) {
-    const int bytes = Layout(T, topk, E, second, size, matrices, n).bytes;
-    if (bytes <= MAX_SMEM / 2 - 1024) return {n, bytes, 2};
-  }
-  for (int n = MAX_STAGES / matrices;; --n) {  // one stage fits whatever the lists (140 KB at most)
-    const int bytes = Layout(T, topk, E, second, size, matrices, n).bytes;
-    if (bytes <= MAX_SMEM) return {n, bytes, 1};
-  }
+  const auto at = [&](int n) { return Layout(T, topk, E, second, size, matrices, n); };
+  for (int n = MAX_STAGES / matrices; n * at(n).stage >= 24 << 10; --n)
+    if (at(n).bytes <= MAX_SMEM / 2 - 1024) return {n, at(n).bytes, 2};
+  for (int n = MAX_STAGES / matrices;; --n)  // one stage fits whatever the lists (140 KB at most)
+    if (at(n).bytes <= MAX_SMEM) return {n, at(n).bytes, 1};
 }
 
 int64_t work_bytes(int64_t T, int topk, int64_t I) {
@@ -748,16 +759,17 @@ int run_few(const tcg_moe_few_args* args, cudaStream_t s) {
     p.N = static_cast<int>(a.I);
     p.row_bytes = p.K * size;
     p.matrices = a.W3 ? 2 : 1;
-    if (int rc = weight_maps(&p, 0, a.W1, p.row_bytes, a.I, a.ld1 * size, a.stride1 * size)) return rc;
+    if (int rc = weight_maps(&p, 0, a.W1, p.row_bytes, a.I, a.ld1 * size, a.stride1 * size, WARPS)) return rc;
     if (a.W3)
-      if (int rc = weight_maps(&p, 1, a.W3, p.row_bytes, a.I, a.ld1 * size, a.stride1 * size)) return rc;
+      if (int rc = weight_maps(&p, 1, a.W3, p.row_bytes, a.I, a.ld1 * size, a.stride1 * size, WARPS)) return rc;
     p.X = static_cast<const uint16_t*>(a.X);
     p.ldx = a.ldx;
     p.S[0] = a.S1;
     p.S[1] = a.S3;
     p.ld_s = a.ld_s1;
     p.stride_s = a.stride_s1;
-    if (int rc = weight_maps(&q, 0, a.W2, a.I * size, a.H, a.ld2 * size, a.stride2 * size)) return rc;
+    if (int rc = weight_maps(&q, 0, a.W2, a.I * size, a.H, a.ld2 * size, a.stride2 * size, slabs_a_stage(true, size, T <= 8)))
+      return rc;
     const int64_t units = std::min<int64_t>(a.E + pairs / 8, pairs) * ceil_div(a.I, 16);
     if (units > INT32_MAX) return TCG_ERR_UNSUPPORTED;
     const Shape h = shape(T, a.topk, a.E, false, size, p.matrices);
