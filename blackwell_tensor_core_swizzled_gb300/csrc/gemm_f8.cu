@@ -51,6 +51,7 @@
 #include <algorithm>
 #include <cstdint>
 #include <cstring>
+#include <type_traits>
 
 #include "common.h"
 #include "desc.cuh"
@@ -476,11 +477,11 @@ __global__ void __launch_bounds__(F8Cfg<CG, BN, STAGES, MODE>::THREADS, 1) f8_ke
             break;
           }
           const uint32_t at = slot_at(i) + 4u * lane;
-  #pragma unroll
+#pragma unroll
           for (int k = 0; k < FINE / 32; ++k)
             if (lane + 32 * k < FINE) copy_f32(at + 128u * k, fine + lane + 32 * k, lane + 32 * k < n);
           if constexpr (MODE == BOTH) {
-  #pragma unroll
+#pragma unroll
             for (int k = 0; k < 4; ++k)
               copy_f32(at + 4u * FINE + 128u * k, other + lane + 32 * k, m0 + lane + 32 * k < p.M);
           } else if (lane < (MODE == ROWS ? BN / BLOCK : 1)) {
@@ -628,7 +629,7 @@ __global__ void __launch_bounds__(F8Cfg<CG, BN, STAGES, MODE>::THREADS, 1) f8_ke
             if (elect_one()) {
               const uint64_t st = (s * static_cast<uint32_t>(C::STAGE_BYTES)) >> 4;
               const int steps = p.weight && last ? (t.last + 31) >> 5 : 4;
-  #pragma unroll
+#pragma unroll
               for (int j = 0; j < 4; ++j)
                 if (j < steps)
                   mma_f8<CG>(d_tmem, p_desc0 + st + j * p.p_kstep, q_desc0 + st + j * p.q_kstep, idesc, j ? 1u : 0u);
@@ -727,30 +728,57 @@ __global__ void __launch_bounds__(F8Cfg<CG, BN, STAGES, MODE>::THREADS, 1) f8_ke
         const int m_warp = static_cast<int>(rank) * 128 + 32 * q;  // the warp's first row in the tile
         const int rows = min(32, t.rows - m_warp);
         const int row0 = t.lo + t.m0 + m_warp;
+        if (rows <= 0) continue;
+        if (p.d_tma && p.d_type != OUT_F32) {
+          // What most calls take, apart from the rest: instructions that are fetched once a
+          // tile have to be few and in a row (12289 rows, 64 groups, 4096 x 2048, f16, MN-major:
+          // 189 us in one loop with the other paths, 163 so).
+          const auto store = [&](auto bf) {
+#pragma unroll
+            for (int i = 0; i < CHUNKS; ++i) {
+              if (i >= mine) break;
+              const int n0 = t.c0 + c_warp + 32 * i;
+              const uint32_t buf = staging();
+#pragma unroll
+              for (uint32_t j = 0; j < 4; ++j) {
+                uint32_t w[4];
+#pragma unroll
+                for (int k = 0; k < 4; ++k) {
+                  uint32_t lo, hi;
+                  unpair(sum[i][4 * j + k], lo, hi);
+                  w[k] = decltype(bf)::value ? pack_bf16(lo, hi) : pack_f16(lo, hi);
+                }
+                st_shared_v4(buf + 64u * lane + 16u * (j ^ ((static_cast<uint32_t>(lane) >> 1) & 3u)), w[0], w[1], w[2],
+                             w[3]);
+              }
+              if (rows == 32) {  // columns clip at the map's end, a group's rows do not
+                send(buf, n0, row0, 0);
+                continue;
+              }
+              __syncwarp();
+              const int word = lane & 3;
+#pragma unroll
+              for (int k = 0; k < 32; k += 8) {
+                const int r = k + (lane >> 2);
+                const uint4 v = ld_shared_v4(buf + 64u * r + 16u * (word ^ ((r >> 1) & 3)));
+                if (r < rows && n0 + 8 * word < p.M)
+                  *reinterpret_cast<uint4*>(static_cast<uint16_t*>(p.D) + (row0 + r) * p.ldd + n0 + 8 * word) = v;
+              }
+              __syncwarp();
+            }
+          };
+          if (p.d_type == OUT_BF16)
+            store(std::true_type{});
+          else
+            store(std::false_type{});
+          continue;
+        }
 #pragma unroll
         for (int i = 0; i < CHUNKS; ++i) {
-          if (i >= mine || rows <= 0) break;
+          if (i >= mine) break;
           const int n0 = t.c0 + c_warp + 32 * i;
-          const bool boxed = p.d_tma && rows == 32;  // columns clip at the map's end, a group's rows do not
+          const bool boxed = p.d_tma && rows == 32;
           uint8_t* dst = static_cast<uint8_t*>(p.D) + (static_cast<int64_t>(row0) * p.ldd + n0 + lane) * p.d_size;
-          if (p.d_tma && !boxed) {
-            // a group's last rows: each lane its own, in 16-byte words
-            uint8_t* own = static_cast<uint8_t*>(p.D) + (static_cast<int64_t>(row0 + lane) * p.ldd + n0) * p.d_size;
-#pragma unroll
-            for (int j = 0; j < 8; ++j) {
-              uint32_t w[4];
-              unpair(sum[i][2 * j], w[0], w[1]);
-              unpair(sum[i][2 * j + 1], w[2], w[3]);
-              if (lane >= rows || n0 + 4 * j >= p.M) continue;
-              if (p.d_type == OUT_F32)
-                *reinterpret_cast<uint4*>(own + 16 * j) = make_uint4(w[0], w[1], w[2], w[3]);
-              else if (p.d_type == OUT_BF16)
-                *reinterpret_cast<uint2*>(own + 8 * j) = make_uint2(pack_bf16(w[0], w[1]), pack_bf16(w[2], w[3]));
-              else
-                *reinterpret_cast<uint2*>(own + 8 * j) = make_uint2(pack_f16(w[0], w[1]), pack_f16(w[2], w[3]));
-            }
-            continue;
-          }
           if (p.d_type == OUT_F32) {
             // two staging tiles of 16 rows
             if (lane == 0) bulk_wait_group_read<0>();
@@ -770,6 +798,17 @@ __global__ void __launch_bounds__(F8Cfg<CG, BN, STAGES, MODE>::THREADS, 1) f8_ke
               continue;
             }
             __syncwarp();
+            if (p.d_tma) {
+              const int word = lane & 7;
+              for (int k = 0; k < rows; k += 4) {
+                const int r = k + (lane >> 3);
+                const uint4 v = ld_shared_v4(buf0 + 128u * r + 16u * (word ^ (r & 7)));
+                if (r < rows && n0 + 4 * word < p.M)
+                  *reinterpret_cast<uint4*>(static_cast<float*>(p.D) + (row0 + r) * p.ldd + n0 + 4 * word) = v;
+              }
+              __syncwarp();
+              continue;
+            }
             for (int k = 0; k < rows; ++k) {
               const uint32_t from = buf0 + 128u * k + 16u * ((static_cast<uint32_t>(lane) >> 2) ^ (k & 7u)) + 4u * (lane & 3u);
               if (n0 + lane < p.M) *reinterpret_cast<float*>(dst + k * p.ldd * 4) = ld_shared_f32(from);
@@ -790,10 +829,6 @@ __global__ void __launch_bounds__(F8Cfg<CG, BN, STAGES, MODE>::THREADS, 1) f8_ke
             }
             st_shared_v4(buf + 64u * lane + 16u * (j ^ ((static_cast<uint32_t>(lane) >> 1) & 3u)), w[0], w[1], w[2], w[3]);
           }
-          if (boxed) {
-            send(buf, n0, row0, 0);
-            continue;
-          }
           __syncwarp();
           for (int k = 0; k < rows; ++k) {
             const uint32_t from = buf + 64u * k + 16u * ((static_cast<uint32_t>(lane) >> 3) ^ ((k >> 1) & 3u)) + 2u * (lane & 7u);
@@ -803,9 +838,9 @@ __global__ void __launch_bounds__(F8Cfg<CG, BN, STAGES, MODE>::THREADS, 1) f8_ke
         }
       } else {
         uint64_t sum[MINE][2][8];  // chunk, 16 rows, pairs of columns as in the fragment
-  #pragma unroll
+#pragma unroll
         for (int i = 0; i < MINE; ++i)
-  #pragma unroll
+#pragma unroll
           for (int k = 0; k < 16; ++k) sum[i][k >> 3][k & 7] = 0ull;
         const int mine = (t.ncols - 32 * part + ACROSS - 1) / ACROSS;  // this warp's chunks of 32 columns that exist
         bool done = true;
@@ -817,7 +852,7 @@ __global__ void __launch_bounds__(F8Cfg<CG, BN, STAGES, MODE>::THREADS, 1) f8_ke
           tc_fence_after();
           const uint32_t at = slot_at(slot);
           uint64_t row[MODE == BOTH ? 4 : 1];  // P's factors of this lane's rows lane / 4 + 8 h (or of all), twice
-  #pragma unroll
+#pragma unroll
           for (int h = 0; h < (MODE == BOTH ? 4 : 1); ++h) {
             const uint32_t r = __float_as_uint(ld_shared_f32(at + 4u * (MODE == BOTH ? BN + 32 * q + 8 * h + (lane >> 2) : BN)));
             row[h] = pair(r, r);
@@ -874,7 +909,7 @@ __global__ void __launch_bounds__(F8Cfg<CG, BN, STAGES, MODE>::THREADS, 1) f8_ke
             const uint32_t mine_at = sbase + C::RED_OFF + 4096u * ((q % quads * p.split + from) * 2 + part) + 16u * lane;
             if (mine > 0) {
               const uint32_t to = mapa_shared(mine_at, static_cast<uint32_t>(owner));
-  #pragma unroll
+#pragma unroll
               for (int v = 0; v < 8; ++v) st_cluster_2x64(to + 512u * v, sum[0][v >> 2][2 * (v & 3)], sum[0][v >> 2][2 * (v & 3) + 1]);
             }
             __syncwarp();
@@ -884,7 +919,7 @@ __global__ void __launch_bounds__(F8Cfg<CG, BN, STAGES, MODE>::THREADS, 1) f8_ke
             if (mine <= 0) continue;
             for (int r = 0; r < p.split; ++r) {
               const uint32_t at = mine_at + 4096u * 2 * (r - from);
-  #pragma unroll
+#pragma unroll
               for (int v = 0; v < 8; ++v) {
                 uint64_t a, b;
                 ld_shared_2x64(at + 512u * v, a, b);
@@ -901,20 +936,20 @@ __global__ void __launch_bounds__(F8Cfg<CG, BN, STAGES, MODE>::THREADS, 1) f8_ke
         const bool m_ok = m_warp + lane < p.M;
         uint8_t* dst = static_cast<uint8_t*>(p.D) + static_cast<int64_t>(row0) * pitch +
                        (p.weight ? t.g * p.stride_d * p.d_size : 0) + static_cast<int64_t>(m_warp + lane) * p.d_size;
-  #pragma unroll
+#pragma unroll
         for (int i = 0; i < MINE; ++i) {
           const int c = 32 * part + ACROSS * i;
           if (i >= mine || m_warp >= p.M) break;
           // rows of a matrix clip at the map's end, rows of a group do not
           const bool boxed = p.d_tma && (p.weight || c + 32 <= t.ncols);
           if (p.d_type == OUT_F32) {
-  #pragma unroll
+#pragma unroll
             for (int g = 0; g < 2; ++g) {  // a staging tile holds 16 rows of 32 m
               const uint32_t buf = staging();
-  #pragma unroll
+#pragma unroll
               for (int h = 0; h < 4; ++h) {
                 const uint32_t m = 8u * h + (static_cast<uint32_t>(lane) >> 2);
-  #pragma unroll
+#pragma unroll
                 for (int j = 0; j < 2; ++j) {
                   uint32_t lo, hi;
                   unpair(sum[i][h >> 1][2 * (2 * g + j) + (h & 1)], lo, hi);
@@ -943,11 +978,11 @@ __global__ void __launch_bounds__(F8Cfg<CG, BN, STAGES, MODE>::THREADS, 1) f8_ke
           const uint32_t buf = staging();
           const bool bf = p.d_type == OUT_BF16;
           const uint32_t k = static_cast<uint32_t>(lane) >> 3, n8 = static_cast<uint32_t>(lane) & 7u;
-  #pragma unroll
+#pragma unroll
           for (uint32_t j = 0; j < 4; ++j) {
             const uint32_t to = 8u * j + n8;
             uint32_t w[4];
-  #pragma unroll
+#pragma unroll
             for (int h = 0; h < 4; ++h) {
               uint32_t lo, hi;
               unpair(sum[i][h >> 1][2 * j + (h & 1)], lo, hi);

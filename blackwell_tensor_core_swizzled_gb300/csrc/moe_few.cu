@@ -161,11 +161,6 @@ __device__ __forceinline__ void decode4(uint32_t w, uint32_t& p, uint32_t& q) {
   }
 }
 
-__device__ __forceinline__ uint4 ld_shared_v4(uint32_t addr) {
-  uint4 v;
-  asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(addr));
-  return v;
-}
 
 template <bool BF16>
 __device__ __forceinline__ float to_f32(uint16_t v) {

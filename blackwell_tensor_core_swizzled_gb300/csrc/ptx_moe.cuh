@@ -71,6 +71,12 @@ __device__ __forceinline__ void st_shared_u32(uint32_t addr, uint32_t v) {
   asm volatile("st.shared.b32 [%0], %1;" ::"r"(addr), "r"(v) : "memory");
 }
 
+__device__ __forceinline__ uint4 ld_shared_v4(uint32_t addr) {
+  uint4 v;
+  asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(addr));
+  return v;
+}
+
 // A 4-byte copy global -> shared in flight (zero if !exists), and this lane's
 // arrival on `bar` (one of 32) once its copies so far have landed.
 __device__ __forceinline__ void copy_f32(uint32_t to, const float* from, bool exists) {
