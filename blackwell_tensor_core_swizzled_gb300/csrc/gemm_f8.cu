@@ -32,14 +32,15 @@
 // What bounds them: a block of a pair's 256 x 256 takes the tensor pipe 512 cycles,
 // its 32 KB for each SM about 500 of what L2 delivers, and the epilogue's multiply-adds
 // 256 (BOTH: 512) beside as many of reads from tensor memory.  8192 x 8192 x 8192 takes
-// 411 us in bursts, 2.68 PFLOP/s (345 if the multiply-adds are left out, so much is the
+// 409 us in bursts, 2.69 PFLOP/s (345 if the multiply-adds are left out, so much is the
 // operands' delivery); back to back for seconds the power limit holds the clock at 1.91
 // GHz and it takes about 445.  The weight gradient of 4096 x 4096 over 8191 rows takes
 // 184 us, 1.50 PFLOP/s (136 without the multiply-adds, 105 without the reads as well):
 // scaling both ways, and 16 % for the last of 3.4 waves of tiles.  More warps for the
 // epilogue (12, 16), an accumulator in two halves with barriers of their own (an MMA of
 // 128 columns takes most of the time of 256: 565 us), reads of tensor memory a step
-// ahead, or one warp's arrival for all made them slower.
+// ahead, or one warp's arrival for all made them slower; four staging tiles a warp
+// instead of two, at one ring stage less, 331 -> 341 us where stores count most.
 //
 // A warp copies the blocks' scales ahead into a shared ring; one warp each brings P
 // and Q, another decodes the tile list.
@@ -936,32 +937,77 @@ __global__ void __launch_bounds__(F8Cfg<CG, BN, STAGES, MODE>::THREADS, 1) f8_ke
         const bool m_ok = m_warp + lane < p.M;
         uint8_t* dst = static_cast<uint8_t*>(p.D) + static_cast<int64_t>(row0) * pitch +
                        (p.weight ? t.g * p.stride_d * p.d_size : 0) + static_cast<int64_t>(m_warp + lane) * p.d_size;
+        if (mine <= 0 || m_warp >= p.M) continue;
+        // half a chunk, 16 rows of 32 m
+        const auto fill_f32 = [&](uint32_t buf, int i, int g) {
+#pragma unroll
+          for (int h = 0; h < 4; ++h) {
+            const uint32_t m = 8u * h + (static_cast<uint32_t>(lane) >> 2);
+#pragma unroll
+            for (int j = 0; j < 2; ++j) {
+              uint32_t lo, hi;
+              unpair(sum[i][h >> 1][2 * (2 * g + j) + (h & 1)], lo, hi);
+              const uint32_t at = 8u * j + 2u * (lane & 3);
+              st_shared_u32(buf + 128u * at + 16u * ((m >> 2) ^ (at & 7u)) + 4u * (m & 3u), lo);
+              st_shared_u32(buf + 128u * (at + 1) + 16u * ((m >> 2) ^ ((at + 1) & 7u)) + 4u * (m & 3u), hi);
+            }
+          }
+        };
+        // stmatrix turns 8 m of 8 columns into 8 rows of 16 bytes: lane 8k + n
+        // addresses row 8j + n, m 8k..8k+7; a row's four 16-byte words are swizzled
+        const uint32_t k8 = static_cast<uint32_t>(lane) >> 3, n8 = static_cast<uint32_t>(lane) & 7u;
+        const auto fill_16 = [&](uint32_t buf, int i, bool bf) {
+#pragma unroll
+          for (uint32_t j = 0; j < 4; ++j) {
+            const uint32_t to = 8u * j + n8;
+            uint32_t w[4];
+#pragma unroll
+            for (int h = 0; h < 4; ++h) {
+              uint32_t lo, hi;
+              unpair(sum[i][h >> 1][2 * j + (h & 1)], lo, hi);
+              w[h] = bf ? pack_bf16(lo, hi) : pack_f16(lo, hi);
+            }
+            stmatrix_x4_trans(buf + 64u * to + 16u * (k8 ^ ((to >> 1) & 3u)), w[0], w[1], w[2], w[3]);
+          }
+        };
+        // rows of a matrix clip at the map's end, rows of a group do not
+        if (p.d_tma && (p.weight || 32 * part + ACROSS * (mine - 1) + 32 <= t.ncols)) {
+          // whole boxes, apart from the rest as above (the matrices' gradient of 32 experts of
+          // 2048 x 4096 354 us in one loop with the other paths, 331 so)
+          const int row = row0 + 32 * part;
+          const auto store = [&](auto type) {
+            constexpr int TYPE = decltype(type)::value;
+#pragma unroll
+            for (int i = 0; i < MINE; ++i) {
+              if (i >= mine) break;
+#pragma unroll
+              for (int g = 0; g < (TYPE == OUT_F32 ? 2 : 1); ++g) {
+                const uint32_t buf = staging();
+                if constexpr (TYPE == OUT_F32)
+                  fill_f32(buf, i, g);
+                else
+                  fill_16(buf, i, TYPE == OUT_BF16);
+                send(buf, m_warp, row + ACROSS * i + 16 * g, outer);
+              }
+            }
+          };
+          if (p.d_type == OUT_F32)
+            store(std::integral_constant<int, OUT_F32>{});
+          else if (p.d_type == OUT_BF16)
+            store(std::integral_constant<int, OUT_BF16>{});
+          else
+            store(std::integral_constant<int, OUT_F16>{});
+          continue;
+        }
 #pragma unroll
         for (int i = 0; i < MINE; ++i) {
           const int c = 32 * part + ACROSS * i;
-          if (i >= mine || m_warp >= p.M) break;
-          // rows of a matrix clip at the map's end, rows of a group do not
-          const bool boxed = p.d_tma && (p.weight || c + 32 <= t.ncols);
+          if (i >= mine) break;
           if (p.d_type == OUT_F32) {
 #pragma unroll
-            for (int g = 0; g < 2; ++g) {  // a staging tile holds 16 rows of 32 m
+            for (int g = 0; g < 2; ++g) {
               const uint32_t buf = staging();
-#pragma unroll
-              for (int h = 0; h < 4; ++h) {
-                const uint32_t m = 8u * h + (static_cast<uint32_t>(lane) >> 2);
-#pragma unroll
-                for (int j = 0; j < 2; ++j) {
-                  uint32_t lo, hi;
-                  unpair(sum[i][h >> 1][2 * (2 * g + j) + (h & 1)], lo, hi);
-                  const uint32_t at = 8u * j + 2u * (lane & 3);
-                  st_shared_u32(buf + 128u * at + 16u * ((m >> 2) ^ (at & 7u)) + 4u * (m & 3u), lo);
-                  st_shared_u32(buf + 128u * (at + 1) + 16u * ((m >> 2) ^ ((at + 1) & 7u)) + 4u * (m & 3u), hi);
-                }
-              }
-              if (boxed) {
-                send(buf, m_warp, row0 + c + 16 * g, outer);
-                continue;
-              }
+              fill_f32(buf, i, g);
               __syncwarp();
               for (int k = 0; k < 16; ++k) {
                 const uint32_t m = static_cast<uint32_t>(lane);
@@ -973,32 +1019,13 @@ __global__ void __launch_bounds__(F8Cfg<CG, BN, STAGES, MODE>::THREADS, 1) f8_ke
             }
             continue;
           }
-          // stmatrix turns 8 m of 8 columns into 8 rows of 16 bytes: lane 8k + n
-          // addresses row 8j + n, m 8k..8k+7; a row's four 16-byte words are swizzled
           const uint32_t buf = staging();
-          const bool bf = p.d_type == OUT_BF16;
-          const uint32_t k = static_cast<uint32_t>(lane) >> 3, n8 = static_cast<uint32_t>(lane) & 7u;
-#pragma unroll
-          for (uint32_t j = 0; j < 4; ++j) {
-            const uint32_t to = 8u * j + n8;
-            uint32_t w[4];
-#pragma unroll
-            for (int h = 0; h < 4; ++h) {
-              uint32_t lo, hi;
-              unpair(sum[i][h >> 1][2 * j + (h & 1)], lo, hi);
-              w[h] = bf ? pack_bf16(lo, hi) : pack_f16(lo, hi);
-            }
-            stmatrix_x4_trans(buf + 64u * to + 16u * (k ^ ((to >> 1) & 3u)), w[0], w[1], w[2], w[3]);
-          }
-          if (boxed) {
-            send(buf, m_warp, row0 + c, outer);
-            continue;
-          }
+          fill_16(buf, i, p.d_type == OUT_BF16);
           __syncwarp();
           for (int n = 0; n < 32; ++n)
             if (m_ok && c + n < t.ncols)
               *reinterpret_cast<uint16_t*>(dst + (c + n) * pitch) =
-                  ld_shared_u16(buf + 64u * n + 16u * (k ^ ((static_cast<uint32_t>(n) >> 1) & 3u)) + 2u * n8);
+                  ld_shared_u16(buf + 64u * n + 16u * (k8 ^ ((static_cast<uint32_t>(n) >> 1) & 3u)) + 2u * n8);
           __syncwarp();
         }
       }
