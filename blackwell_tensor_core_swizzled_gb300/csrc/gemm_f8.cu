@@ -4,7 +4,7 @@
 //
 // No MMA kind takes fp32 scales.  So the sum of a block of 128 k is one accumulator
 // in tensor memory (four MMAs of 32 k), and the epilogue's warps add it, scaled, to
-// sums in their registers while the MMAs fill the other accumulator: 128 x 256 sums
+// sums in their registers while the MMAs fill the next accumulator: 128 x 256 sums
 // of a CTA are 128 registers of 256 threads.  All of it in fp32: one rounding of the
 // scales' product and one of each addition (BOTH: of each scaling too).
 //
@@ -199,6 +199,9 @@ struct F8Cfg {
   static constexpr int Q_BYTES = Q_ROWS * 128;
   static constexpr int STAGE_BYTES = P_BYTES + Q_BYTES;
   static constexpr int STAGING = 2;  // staging tiles for each epilogue warp
+  // accumulators; of 64 columns four (256 rows over 64 groups of 4096 x 1024 56.5 us with two, 54.9
+  // with four or eight)
+  static constexpr int ACCS = 512 / BN < 4 ? 512 / BN : 4;
   static constexpr int EPI_OFF = STAGES * STAGE_BYTES;
   static constexpr int SC_OFF = EPI_OFF + EPI_WARPS * STAGING * STAGING_BYTES;
   // a block's scales: Q's of the columns, then P's of the rows or of all; ROWS: P's of
@@ -207,15 +210,15 @@ struct F8Cfg {
   // split contractions: fragments of two column parts and four lane quadrants
   static constexpr int RED_OFF = (SC_OFF + SLOTS * SLOT_BYTES + 127) / 128 * 128;
   static constexpr int BAR_OFF = RED_OFF + (MODE == COLUMNS ? EPI_WARPS * 4096 : 0);
-  // full[S], empty[S], rag[S], peer[S], acc_full[2], acc_empty[2], drain, tile_full[T], tile_empty[T],
+  // full[S], empty[S], rag[S], peer[S], acc_full[A], acc_empty[A], drain, tile_full[T], tile_empty[T],
   // scale_full[L], scale_empty[L], reduced
-  static constexpr int NUM_BARS = 4 * STAGES + 5 + 2 * TILES + 2 * SLOTS + 1;
+  static constexpr int NUM_BARS = 4 * STAGES + 1 + 2 * ACCS + 2 * TILES + 2 * SLOTS + 1;
   static constexpr int TILE_OFF = (BAR_OFF + NUM_BARS * 8 + 8 + 15) / 16 * 16;  // tmem slot + abort flag before it
   static constexpr int SEG_OFF = TILE_OFF + TILES * 48;
   static constexpr int SMEM_BYTES = 1024 + SEG_OFF + 2 * (MAX_GROUPS + 1) * 4;
   static_assert(Q_BYTES % 1024 == 0, "swizzle period");
   static_assert(SMEM_BYTES <= 232448, "dynamic shared memory");
-  static_assert(2 * BN <= 512, "two accumulators");
+  static_assert(ACCS >= 2, "the next accumulator is filled meanwhile");
 };
 
 // One unit: a tile of one group.
@@ -314,13 +317,14 @@ __global__ void __launch_bounds__(F8Cfg<CG, BN, STAGES, MODE>::THREADS, 1) f8_ke
   auto rag_bar = [&](uint32_t s) { return bar0 + 8u * (2 * STAGES + s); };
   auto peer_bar = [&](uint32_t s) { return bar0 + 8u * (3 * STAGES + s); };
   auto accf_bar = [&](uint32_t b) { return bar0 + 8u * (4 * STAGES + b); };
-  auto acce_bar = [&](uint32_t b) { return bar0 + 8u * (4 * STAGES + 2 + b); };
-  const uint32_t drain_bar = bar0 + 8u * (4 * STAGES + 4);
-  auto tile_full = [&](uint32_t i) { return bar0 + 8u * (4 * STAGES + 5 + i); };
-  auto tile_empty = [&](uint32_t i) { return bar0 + 8u * (4 * STAGES + 5 + TILES + i); };
-  auto scf_bar = [&](uint32_t i) { return bar0 + 8u * (4 * STAGES + 5 + 2 * TILES + i); };
-  auto sce_bar = [&](uint32_t i) { return bar0 + 8u * (4 * STAGES + 5 + 2 * TILES + SLOTS + i); };
-  const uint32_t red_bar = bar0 + 8u * (4 * STAGES + 5 + 2 * TILES + 2 * SLOTS);
+  auto acce_bar = [&](uint32_t b) { return bar0 + 8u * (4 * STAGES + C::ACCS + b); };
+  const uint32_t drain_bar = bar0 + 8u * (4 * STAGES + 2 * C::ACCS);
+  const uint32_t after = drain_bar + 8u;
+  auto tile_full = [&](uint32_t i) { return after + 8u * i; };
+  auto tile_empty = [&](uint32_t i) { return after + 8u * (TILES + i); };
+  auto scf_bar = [&](uint32_t i) { return after + 8u * (2 * TILES + i); };
+  auto sce_bar = [&](uint32_t i) { return after + 8u * (2 * TILES + SLOTS + i); };
+  const uint32_t red_bar = after + 8u * (2 * TILES + 2 * SLOTS);
   auto slot_at = [&](uint32_t i) { return sbase + C::SC_OFF + i * C::SLOT_BYTES; };
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(gbase + C::BAR_OFF + 8 * C::NUM_BARS);
   volatile uint32_t* abort_flag = tmem_slot + 1;
@@ -348,7 +352,7 @@ __global__ void __launch_bounds__(F8Cfg<CG, BN, STAGES, MODE>::THREADS, 1) f8_ke
       mbar_init(rag_bar(s), 1);
       mbar_init(peer_bar(s), 1);
     }
-    for (uint32_t b = 0; b < 2; ++b) {
+    for (uint32_t b = 0; b < C::ACCS; ++b) {
       mbar_init(accf_bar(b), 1);
       mbar_init(acce_bar(b), C::EPI_WARPS * CG);
     }
@@ -588,8 +592,8 @@ __global__ void __launch_bounds__(F8Cfg<CG, BN, STAGES, MODE>::THREADS, 1) f8_ke
         for (int kb = 0; kb < t.nkb; ++kb) {
           const bool last = kb == t.nkb - 1;
           const bool ragged = p.weight && last && (t.last & 31);
-          const uint32_t b = tcount & 1u;
-          if (issue && !wait_inline(acce_bar(b), ((tcount >> 1) & 1u) ^ 1u, wctx, SITE_MMA_ACC_EMPTY)) {
+          const uint32_t b = tcount % C::ACCS;
+          if (issue && !wait_inline(acce_bar(b), ((tcount / C::ACCS) & 1u) ^ 1u, wctx, SITE_MMA_ACC_EMPTY)) {
             ok = false;
             break;
           }
@@ -694,13 +698,13 @@ __global__ void __launch_bounds__(F8Cfg<CG, BN, STAGES, MODE>::THREADS, 1) f8_ke
           for (int k = 0; k < 16; ++k) sum[i][k] = 0ull;
         bool done = true;
         for (int kb = 0; kb < t.nkb; ++kb, ++tcount) {
-          const uint32_t b = tcount & 1u, slot = tcount % SLOTS;
+          const uint32_t b = tcount % C::ACCS, slot = tcount % SLOTS;
           done = wait_inline(scf_bar(slot), (tcount / SLOTS) & 1u, wctx, SITE_EPI_ACC_FULL);
           if (!done) break;
           const uint32_t at = slot_at(slot);
           const float f = ld_shared_f32(at + 4u * (32 * q + lane)) * ld_shared_f32(at + 4u * (128 + c_warp / BLOCK));
           const uint64_t ff = pair(__float_as_uint(f), __float_as_uint(f));
-          done = wait_inline(accf_bar(b), (tcount >> 1) & 1u, wctx, SITE_EPI_ACC_FULL);
+          done = wait_inline(accf_bar(b), (tcount / C::ACCS) & 1u, wctx, SITE_EPI_ACC_FULL);
           if (!done) break;
           tc_fence_after();
 #pragma unroll
@@ -846,9 +850,9 @@ __global__ void __launch_bounds__(F8Cfg<CG, BN, STAGES, MODE>::THREADS, 1) f8_ke
         const int mine = (t.ncols - 32 * part + ACROSS - 1) / ACROSS;  // this warp's chunks of 32 columns that exist
         bool done = true;
         for (int kb = 0; kb < t.nkb; ++kb, ++tcount) {
-          const uint32_t b = tcount & 1u, slot = tcount % SLOTS;
+          const uint32_t b = tcount % C::ACCS, slot = tcount % SLOTS;
           done = wait_inline(scf_bar(slot), (tcount / SLOTS) & 1u, wctx, SITE_EPI_ACC_FULL) &&
-                 wait_inline(accf_bar(b), (tcount >> 1) & 1u, wctx, SITE_EPI_ACC_FULL);
+                 wait_inline(accf_bar(b), (tcount / C::ACCS) & 1u, wctx, SITE_EPI_ACC_FULL);
           if (!done) break;
           tc_fence_after();
           const uint32_t at = slot_at(slot);
