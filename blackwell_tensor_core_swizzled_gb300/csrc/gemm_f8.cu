@@ -42,8 +42,8 @@
 // ahead, or one warp's arrival for all made them slower; four staging tiles a warp
 // instead of two, at one ring stage less, 331 -> 341 us where stores count most.
 //
-// A warp copies the blocks' scales ahead into a shared ring; one warp each brings P
-// and Q, another decodes the tile list.
+// One warp decodes the tile list and copies the blocks' scales ahead into a shared
+// ring, one each brings P and Q, one issues the MMAs.
 #include <cuda.h>
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>

@@ -165,16 +165,16 @@ def test_grouped(tcg, major, sizes, before, after, N, K, pad):
     SB, sb = scales((G, blocks(rows), blocks(cols)), fmt, 4, K ** -0.5, pad)
     a = a * along(sa, K).T
     b = b * spread(sb, rows, cols)
-    for out in ("f32", "bf16"):
-        D = torch.full((R, N + 3), 7.0, dtype=TORCH[out], device="cuda")
+    ref, S = np.zeros((R, N)), np.zeros((R, N))
+    for g in range(G):
+        sl, m = slice(off[g], off[g + 1]), b[g].T if major == "k" else b[g]
+        ref[sl], S[sl] = a[sl] @ m, np.abs(a[sl]) @ np.abs(m)
+    for out, more in (("f32", 3), ("bf16", 3), ("f32", 8), ("bf16", 8), ("f16", 8)):  # rows that end on 16 bytes or not
+        D = torch.full((R, N + more), 7.0, dtype=TORCH[out], device="cuda")
         tcg.gemm_f8_grouped(IN_TYPE[fmt], R, N, K, G, A, A.shape[1], SA, SA.shape[1], torch.from_numpy(off).cuda(), B,
                             tcg.K_MAJOR if major == "k" else tcg.MN_MAJOR, B.shape[2], 0, SB, SB.shape[2], 0, D,
-                            DTYPE[out], N + 3)
+                            DTYPE[out], N + more)
         ok(tcg)
-        ref, S = np.zeros((R, N)), np.zeros((R, N))
-        for g in range(G):
-            sl, m = slice(off[g], off[g + 1]), b[g].T if major == "k" else b[g]
-            ref[sl], S[sl] = a[sl] @ m, np.abs(a[sl]) @ np.abs(m)
         close(to_host(D)[:, :N], ref, S, tau(K), out, (major, out))
         assert bool((D[:, N:] == 7.0).all()), "wrote past the row"
 
@@ -189,10 +189,10 @@ def test_grouped_wgrad(tcg, sizes, before, after, N, K, pad):
     SA, sa = scales((R // BLOCK + G, K), "e4m3", 8, 1.0, pad)
     at = row_blocks(off, R)
     dy, a = dy * sdy[at], a * sa[at]
-    for out in ("f32", "bf16"):
-        DW = torch.full((G, N, K + 5), 7.0, dtype=TORCH[out], device="cuda")
+    for out, more in (("f32", 5), ("bf16", 5), ("f32", 8), ("bf16", 8), ("f16", 8)):
+        DW = torch.full((G, N, K + more), 7.0, dtype=TORCH[out], device="cuda")
         tcg.gemm_f8_grouped_wgrad(tcg.IN_E4M3, R, N, K, G, DY, DY.shape[1], SDY, SDY.shape[1], A, A.shape[1], SA,
-                                  SA.shape[1], torch.from_numpy(off).cuda(), DW, DTYPE[out], K + 5, 0)
+                                  SA.shape[1], torch.from_numpy(off).cuda(), DW, DTYPE[out], K + more, 0)
         ok(tcg)
         ref, S = np.zeros((G, N, K)), np.zeros((G, N, K))
         for g in range(G):
