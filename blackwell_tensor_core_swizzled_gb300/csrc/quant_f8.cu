@@ -8,7 +8,9 @@
 // one correction y + (F x - y a) / a, whose residual an fma gives exactly.  An
 // exact tie between two codes therefore stays one (with y alone, or x divided by
 // the rounded scale, 1 of 300 such ties went the other way), and other quotients
-// of 16-bit values lie at least 2^-13 off a tie.
+// of 16-bit values lie at least 2^-13 (bf16) or 2^-16 (f16) of themselves off a tie.
+// Those of fp32 values may lie as close as 2^-50, and F x has up to 27 bits: see
+// encode_f32.
 //
 // All three kernels read X once, keep it on the SM between the maximum and the
 // codes, and are bound by HBM.  Rows: a half warp (16-bit types) or a warp holds a
@@ -99,7 +101,7 @@ __device__ __forceinline__ float largest_in(uint32_t a) {
 
 // How the values of a block become codes.
 struct Coder {
-  float by;     // x * by is F x (a in normal range), exact but for fp32's last bit
+  float by;     // x * by is F x (a in normal range)
   float a, inv; // divided by a
 };
 
@@ -133,14 +135,58 @@ __device__ __forceinline__ Coder make_coder(float amax, bool pow2, float& scale)
   return {F * pre, a, 1.0f / a};
 }
 
+// Factors of fp32 x that give a little less and a little more than F x / a.  Each
+// product is within four roundings, 2^-22 of itself, of its own.
+struct Bounds {
+  float below, above;
+};
+__device__ __forceinline__ Bounds bounds(const Coder& c) {
+  const float k = c.by * c.inv;
+  return {k * (1.0f - 0x1p-21f), k * (1.0f + 0x1p-21f)};
+}
+__device__ __forceinline__ Bounds from_lane(const Bounds& b, int lane) {
+  return {__shfl_sync(0xffffffffu, b.below, lane), __shfl_sync(0xffffffffu, b.above, lane)};
+}
+
 __device__ __forceinline__ Coder from_lane(const Coder& c, int lane) {
   return {__shfl_sync(0xffffffffu, c.by, lane), __shfl_sync(0xffffffffu, c.a, lane), __shfl_sync(0xffffffffu, c.inv, lane)};
 }
 
+// Two fp32 operations in one instruction.
+__device__ __forceinline__ uint64_t pair(float lo, float hi) {
+  uint64_t v;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(v) : "f"(lo), "f"(hi));
+  return v;
+}
+__device__ __forceinline__ void unpair(uint64_t v, float& lo, float& hi) {
+  asm("mov.b64 {%0, %1}, %2;" : "=f"(lo), "=f"(hi) : "l"(v));
+}
+__device__ __forceinline__ uint64_t mul2(uint64_t a, uint64_t b) {
+  uint64_t d;
+  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
+  return d;
+}
+
+// F x / a of 16-bit x, so close that rounding it to a code rounds F x / a itself.
 __device__ __forceinline__ float quotient(float x, const Coder& c) {
   const float n = x * c.by;
   const float y = n * c.inv;
   return fmaf(fmaf(-y, c.a, n), c.inv, y);
+}
+
+// The same of fp32 x: F x = n + low exactly, z is one of the two fp32 values around
+// (n + low) / a, and `rest` has the sign of what is left, which two fmas give exactly
+// (multiples of z's and a's last bits, less than 2^25 of them).  Rounding to odd: of the
+// two values the one whose last bit is set, unless nothing is left.  Ties have few bits,
+// so that a quotient beside one stays on its side.
+__device__ __forceinline__ float odd_quotient(float x, const Coder& c) {
+  const float n = x * c.by, low = fmaf(x, c.by, -n);
+  const float y = n * c.inv;
+  const float z = fmaf(fmaf(-y, c.a, n) + low, c.inv, y);
+  const float rest = fmaf(-z, c.a, n) + low;
+  const uint32_t bits = __float_as_uint(z);
+  const int32_t step = static_cast<int32_t>(__float_as_uint(rest) ^ bits) >> 31 | 1;  // towards zero or away from it
+  return __uint_as_float(rest != 0.0f && !(bits & 1u) ? bits + step : bits);
 }
 
 // Four codes, the first in the low byte.
@@ -152,15 +198,29 @@ __device__ __forceinline__ uint32_t encode4(float a, float b, float c, float d) 
   return lo | hi << 16;
 }
 
-// V codes of a word.
-template <bool WIDE, class T, class F>
-__device__ __forceinline__ void store_codes(const Word<T>& x, uint8_t* q, int n, bool aligned, F&& coder) {
-  constexpr int V = Word<T>::V;
-  uint32_t code[V / 4];
+// Four codes of fp32 values, if `sure`: the same from a little less and from a little
+// more than F x / a.  Where they differ (1 of 2^16 values, and ties) odd_quotient
+// decides: in rows at once (8192 x 8192 49.8 us, behind the loop over a thread's words
+// 60.3), else behind that loop, where its code is small (columns 54.4, squares 59.0;
+// with odd_quotient for every value each took a quarter to a third more).
+template <bool WIDE, class F>
+__device__ __forceinline__ uint32_t encode_f32(const Word<float>& x, F&& bound, bool& sure) {
+  float lo[4], hi[4];
 #pragma unroll
-  for (int j = 0; j < V; j += 4)
-    code[j / 4] = encode4<WIDE>(quotient(x.value(j), coder(j)), quotient(x.value(j + 1), coder(j + 1)),
-                                quotient(x.value(j + 2), coder(j + 2)), quotient(x.value(j + 3), coder(j + 3)));
+  for (int j = 0; j < 4; j += 2) {
+    const Bounds a = bound(j), b = bound(j + 1);
+    const uint64_t v = pair(x.value(j), x.value(j + 1));
+    unpair(mul2(v, pair(a.below, b.below)), lo[j], lo[j + 1]);
+    unpair(mul2(v, pair(a.above, b.above)), hi[j], hi[j + 1]);
+  }
+  const uint32_t code = encode4<WIDE>(lo[0], lo[1], lo[2], lo[3]);
+  sure = code == encode4<WIDE>(hi[0], hi[1], hi[2], hi[3]);
+  return code;
+}
+
+// The first n of a word's V codes.
+template <int V>
+__device__ __forceinline__ void put_codes(const uint32_t (&code)[V / 4], uint8_t* q, int n, bool aligned) {
   if (!aligned) {
 #pragma unroll
     for (int j = 0; j < V; ++j)
@@ -171,6 +231,42 @@ __device__ __forceinline__ void store_codes(const Word<T>& x, uint8_t* q, int n,
     else
       *reinterpret_cast<uint32_t*>(q) = code[0];
   }
+}
+
+// What the codes of a type's values are made with.
+template <class T>
+using Maker = typename std::conditional<std::is_same<T, float>::value, Bounds, Coder>::type;
+template <class T>
+__device__ __forceinline__ Maker<T> maker(const Coder& c) {
+  if constexpr (std::is_same<T, float>::value)
+    return bounds(c);
+  else
+    return c;
+}
+
+// V codes of a word; true if store_exact_codes has to replace them.
+template <bool WIDE, class T, class F>
+__device__ __forceinline__ bool store_codes(const Word<T>& x, uint8_t* q, int n, bool aligned, F&& coder) {
+  constexpr int V = Word<T>::V;
+  uint32_t code[V / 4];
+  bool sure = true;
+  if constexpr (std::is_same<T, float>::value) {
+    code[0] = encode_f32<WIDE>(x, coder, sure);
+  } else {
+#pragma unroll
+    for (int j = 0; j < V; j += 4)
+      code[j / 4] = encode4<WIDE>(quotient(x.value(j), coder(j)), quotient(x.value(j + 1), coder(j + 1)),
+                                  quotient(x.value(j + 2), coder(j + 2)), quotient(x.value(j + 3), coder(j + 3)));
+  }
+  put_codes<V>(code, q, n, aligned);
+  return !sure;
+}
+
+template <bool WIDE, class F>
+__device__ __forceinline__ void store_exact_codes(const Word<float>& x, uint8_t* q, int n, bool aligned, F&& coder) {
+  const uint32_t code[1] = {encode4<WIDE>(odd_quotient(x.value(0), coder(0)), odd_quotient(x.value(1), coder(1)),
+                                          odd_quotient(x.value(2), coder(2)), odd_quotient(x.value(3), coder(3)))};
+  put_codes<4>(code, q, n, aligned);
 }
 
 // ----------------------------------------------------------------------- rows
@@ -210,10 +306,17 @@ __global__ void __launch_bounds__(32 * ROW_WARPS) row_kernel(int64_t R, int64_t 
   }
   float s;
   const Coder my = make_coder<WIDE>(mine, pow2, s);
+  const Maker<T> make = maker<T>(my);
 #pragma unroll
   for (int i = 0; i < ROWS; ++i) {
-    const Coder k = from_lane(my, lane / LANES * LANES + i);
-    if (i < rows) store_codes<WIDE>(x[i], Q + (r0 + i) * ldq + c, n, ALIGNED, [&](int) { return k; });
+    const Maker<T> k = from_lane(make, lane / LANES * LANES + i);
+    const bool d = i < rows && store_codes<WIDE>(x[i], Q + (r0 + i) * ldq + c, n, ALIGNED, [&](int) { return k; });
+    if constexpr (std::is_same<T, float>::value) {
+      if (__any_sync(0xffffffffu, d)) {
+        const Coder e = from_lane(my, lane / LANES * LANES + i);
+        if (d) store_exact_codes<WIDE>(x[i], Q + (r0 + i) * ldq + c, n, ALIGNED, [&](int) { return e; });
+      }
+    }
   }
   const int64_t block = (c - lane % LANES * V) / BLOCK;
   if (lane % LANES < rows && block * BLOCK < C) scale[block * ld_scale + r0 + lane % LANES] = s;
@@ -298,14 +401,31 @@ __global__ void __launch_bounds__(32 * COL_WARPS, ALIGNED ? 6 : 3)
   float s;
   const Coder my = make_coder<WIDE>(mine, pow2, s);
   if (g8 < V && c + g8 < C) scale[slot * ld_scale + c + g8] = s;
-  Coder k[V];
+  const Maker<T> make = maker<T>(my);
+  Maker<T> k[V];
 #pragma unroll
-  for (int j = 0; j < V; ++j) k[j] = from_lane(my, 4 * j + w4);
+  for (int j = 0; j < V; ++j) k[j] = from_lane(make, 4 * j + w4);
+  uint32_t doubt = 0;
 #pragma unroll UNROLL
   for (int i = 0; i < PER; ++i) {
     const Word<T>& v = word(i);
-    if (g8 + 8 * i < rows)
-      store_codes<WIDE>(v, Q + (lo + g8 + 8 * i) * ldq + c, n, ALIGNED, [&](int j) { return k[j]; });
+    if (g8 + 8 * i < rows &&
+        store_codes<WIDE>(v, Q + (lo + g8 + 8 * i) * ldq + c, n, ALIGNED, [&](int j) { return k[j]; }))
+      doubt |= 1u << i;
+  }
+  if constexpr (std::is_same<T, float>::value) {
+    if (__any_sync(0xffffffffu, doubt != 0)) {
+      Coder exact[V];
+#pragma unroll
+      for (int j = 0; j < V; ++j) exact[j] = from_lane(my, 4 * j + w4);
+#pragma unroll 1
+      for (; doubt; doubt &= doubt - 1) {
+        const int64_t row = lo + g8 + 8 * (__ffs(doubt) - 1);
+        Word<T> again;
+        again.load(X + row * ldx + c, n, ALIGNED);
+        store_exact_codes<WIDE>(again, Q + row * ldq + c, n, ALIGNED, [&](int j) { return exact[j]; });
+      }
+    }
   }
   griddep_launch_dependents();
 }
@@ -313,7 +433,7 @@ __global__ void __launch_bounds__(32 * COL_WARPS, ALIGNED ? 6 : 3)
 // -------------------------------------------------------------------- squares
 
 // A block a CTA, in words of 16 bytes.  Four CTAs an SM of 16-bit values (8192 x 8192:
-// 34.6 us; three 41, five 44), two of fp32 (60 us; one 92, three 68).
+// 34.6 us; three 41, five 44), two of fp32 (59 us; one 92, three 68).
 template <class T, bool WIDE, bool ALIGNED>
 __global__ void __launch_bounds__(SQUARE_THREADS, ALIGNED && sizeof(T) == 2 ? 4 : 2)
     square_kernel(int64_t R, int64_t C, const T* __restrict__ X, int64_t ldx, bool pow2, uint8_t* __restrict__ Q,
@@ -347,10 +467,22 @@ __global__ void __launch_bounds__(SQUARE_THREADS, ALIGNED && sizeof(T) == 2 ? 4 
   for (int i = 0; i < SQUARE_THREADS / 32; ++i) m = fmaxf(m, top[i]);
   const Coder k = make_coder<WIDE>(m, pow2, s);
   if (t == 0) scale[blockIdx.x / col_tiles * ld_scale + tile] = s;
+  const Maker<T> make = maker<T>(k);
+  uint32_t doubt = 0;
 #pragma unroll
   for (int i = 0; i < PER; ++i) {
     const int row = t / ACROSS + DOWN * i;
-    if (row < rows) store_codes<WIDE>(x[i], Q + (lo + row) * ldq + c, n, ALIGNED, [&](int) { return k; });
+    if (row < rows && store_codes<WIDE>(x[i], Q + (lo + row) * ldq + c, n, ALIGNED, [&](int) { return make; }))
+      doubt |= 1u << i;
+  }
+  if constexpr (std::is_same<T, float>::value) {
+#pragma unroll 1
+    for (; doubt; doubt &= doubt - 1) {
+      const int64_t row = lo + t / ACROSS + DOWN * (__ffs(doubt) - 1);
+      Word<T> again;
+      again.load(X + row * ldx + c, n, ALIGNED);
+      store_exact_codes<WIDE>(again, Q + row * ldq + c, n, ALIGNED, [&](int) { return k; });
+    }
   }
   griddep_launch_dependents();
 }

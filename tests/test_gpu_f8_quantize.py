@@ -2,6 +2,8 @@
 float64: every value must be the one nearest to F x / amax (16-bit inputs), so
 codes are compared exactly; fp32 inputs may differ where F x / amax lies within
 2^-22 of a tie.  Scales are one fp32 rounding (2^-24) off."""
+from fractions import Fraction
+
 import numpy as np
 import pytest
 import torch
@@ -164,3 +166,52 @@ def test_captured_on_a_side_stream(tcg):
     graph.replay()
     torch.cuda.synchronize()
     compare(Q.cpu().numpy(), S.double().cpu().numpy(), x[::-1], "row", "e4m3", False, "bf16")
+
+
+def next_to_ties(fmt, blocks_of, n, seed):
+    """fp32 [blocks][n]: a block's largest value, then values up to two steps of
+    fp32 beside those whose F x / amax lies half way between two codes."""
+    rng = np.random.default_rng(seed)
+    man, low, high = (3, -6, 8) if fmt == "e4m3" else (2, -14, 15)
+    top = np.float32(1 + rng.random((blocks_of, 1))) * np.float32(2) ** rng.integers(-100, 100, (blocks_of, 1)).astype(np.float32)
+    e = rng.integers(low - 1, high, (blocks_of, n))
+    step = 2.0 ** (np.maximum(e, low) - man)
+    first = np.where(e < low, 0, 1 << man)    # below the smallest normal code the steps are its own
+    tie = (first + rng.integers(0, 1 << man, e.shape) + 0.5) * step
+    x = (tie * top.astype(np.float64) / LARGEST[fmt]).astype(np.float32)
+    x = (x.view(np.int32) + rng.integers(-2, 3, e.shape, dtype=np.int32)).view(np.float32)
+    x *= rng.choice(np.float32([-1, 1]), e.shape)
+    x[:, :1] = top
+    assert np.all(np.abs(x) <= top)
+    return x
+
+
+def exact_code(x, top, fmt):
+    """The value of the code nearest to F x / top (ties to even), in whole numbers."""
+    man, low = (3, -6) if fmt == "e4m3" else (2, -14)
+    q = Fraction(float(abs(x))) * int(LARGEST[fmt]) / Fraction(float(top))
+    e = low
+    while q >= Fraction(2) ** (e + 1):
+        e += 1
+    step = Fraction(2) ** (e - man)
+    return float(round(q / step) * step) * np.sign(x)
+
+
+@pytest.mark.parametrize("fmt", ["e4m3", "e5m2"])
+@pytest.mark.parametrize("kind", ["row", "column", "square"])
+@pytest.mark.parametrize("n", [128, 101])  # in words, and value by value
+def test_fp32_is_rounded_once(tcg, fmt, kind, n):
+    """Codes of fp32 values next to ties are the nearest, not the nearest to a rounded F x / amax."""
+    if kind == "square":
+        x = next_to_ties(fmt, 1, n * n, n).reshape(n, n)
+    else:
+        x = next_to_ties(fmt, n, 128, n)
+        x = x.T.copy() if kind == "column" else x
+    R, C = x.shape
+    Q, S = run(tcg, torch.from_numpy(x).cuda(), R, C, "f32", kind, fmt, False)
+    got = table(fmt)[Q]
+    top = np.abs(x).max(axis={"row": 1, "column": 0, "square": (0, 1)}[kind], keepdims=True)
+    assert np.all(np.abs(S.reshape(-1) - (top / LARGEST[fmt]).reshape(-1)) <= 2.0 ** -23 * S.reshape(-1))
+    want = np.array([exact_code(v, t, fmt) for v, t in zip(x.ravel(), np.broadcast_to(top, x.shape).ravel())]).reshape(x.shape)
+    wrong = got != want
+    assert not wrong.any(), (int(wrong.sum()), x[wrong][:4], got[wrong][:4], want[wrong][:4])
