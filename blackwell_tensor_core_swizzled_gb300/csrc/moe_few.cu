@@ -31,7 +31,10 @@
 //
 // h is kept as two 16-bit values, h = hi + lo, both multiplied: one value of x's
 // type would add an error as large as that of rounding y (2.4e-3 instead of
-// 1.7e-3 of bf16 outputs' norm).
+// 1.7e-3 of bf16 outputs' norm).  In f16 lo is stored 2^11 times as large: as it is,
+// what hi leaves of an h of less than 2^-3 would lie below f16's normal range, and of
+// 2^-17 (a small weight of an ordinary activation) 2^-8 would be lost.  2^-22 of h is
+// lost now, or 2^-36.
 #include <cuda.h>
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
@@ -161,6 +164,11 @@ __device__ __forceinline__ void decode4(uint32_t w, uint32_t& p, uint32_t& q) {
   }
 }
 
+
+// What lo is multiplied by where it is stored.  hi leaves at most 2^-11 of itself, 2^4,
+// so that lo stays within f16's range; bf16 has fp32's.
+template <bool BF16>
+__device__ __forceinline__ constexpr float lo_factor() { return BF16 ? 1.0f : 2048.0f; }
 
 template <bool BF16>
 __device__ __forceinline__ float to_f32(uint16_t v) {
@@ -384,6 +392,9 @@ __global__ void __launch_bounds__(FEW_THREADS, 2) few_kernel(const __grid_consta
   constexpr int WORDS = CODES / 2;         // of x against them
   constexpr int M = SECOND ? 1 : 2;
   constexpr int PARTS = SECOND ? 2 : 1;    // hi and lo
+  constexpr bool LO_SCALED = SECOND && lo_factor<BF16>() != 1.0f;
+  constexpr int CHAINS = LO_SCALED ? 2 : 1;          // sums of hi, and of lo as it is stored
+  constexpr bool APART = W8 || DIRECT;               // a stage's sums are added to the others apart
   if constexpr (SECOND) {
     griddep_wait();
     griddep_launch_dependents();
@@ -446,7 +457,7 @@ __global__ void __launch_bounds__(FEW_THREADS, 2) few_kernel(const __grid_consta
   constexpr int SHARE = WARPS / SLABS;  // warps of a slab, each half of its rows' bytes
   const int mine = warp / SHARE;        // this warp's slab
   uint32_t s = 0, ph = 0;
-  float acc[M][4];
+  float acc[CHAINS][M][4];
   bool ok = true;
   // This warp's share of a job: adds to acc.
   auto multiply = [&](const Job& a) {
@@ -493,7 +504,7 @@ __global__ void __launch_bounds__(FEW_THREADS, 2) few_kernel(const __grid_consta
               }
             }
           }
-          float part[M][4] = {};
+          float part[CHAINS][M][4] = {};
 #pragma unroll
           for (int q = 0; q < PARTS; ++q) {
             const uint32_t* w = reinterpret_cast<const uint32_t*>(&x[q][0]);
@@ -501,15 +512,18 @@ __global__ void __launch_bounds__(FEW_THREADS, 2) few_kernel(const __grid_consta
             for (int i = 0; i < CODES / 4; ++i) {
 #pragma unroll
               for (int m = 0; m < M; ++m)
-                if (m < p.matrices) mma_16816<BF16>(W8 || DIRECT ? part[m] : acc[m], A[m][i], w[2 * i], w[2 * i + 1]);
+                if (m < p.matrices) mma_16816<BF16>(APART ? part[q % CHAINS][m] : acc[q % CHAINS][m], A[m][i], w[2 * i], w[2 * i + 1]);
             }
           }
-          if constexpr (W8 || DIRECT) {
+          if constexpr (APART) {
 #pragma unroll
             for (int m = 0; m < M; ++m)
 #pragma unroll
-              for (int i = 0; i < 4; ++i)
-                if (!DIRECT || (columns >> i & 1)) acc[m][i] = W8 ? fmaf(part[m][i], sc[m], acc[m][i]) : acc[m][i] + part[m][i];
+              for (int i = 0; i < 4; ++i) {
+                float& to = acc[0][m][i];
+                const float v = LO_SCALED ? fmaf(part[CHAINS - 1][m][i], 1.0f / lo_factor<BF16>(), part[0][m][i]) : part[0][m][i];
+                if (!DIRECT || (columns >> i & 1)) to = W8 ? fmaf(v, sc[m], to) : to + v;
+              }
           }
         }
       }
@@ -523,9 +537,15 @@ __global__ void __launch_bounds__(FEW_THREADS, 2) few_kernel(const __grid_consta
   };
   auto clear = [&] {
 #pragma unroll
-    for (int m = 0; m < M; ++m)
+    for (int j = 0; j < CHAINS; ++j)
 #pragma unroll
-      for (int i = 0; i < 4; ++i) acc[m][i] = 0.0f;
+      for (int m = 0; m < M; ++m)
+#pragma unroll
+        for (int i = 0; i < 4; ++i) acc[j][m][i] = 0.0f;
+  };
+  // W2's sum i of this lane
+  auto sum_of = [&](int i) {
+    return LO_SCALED && !APART ? fmaf(acc[CHAINS - 1][0][i], 1.0f / lo_factor<BF16>(), acc[0][0][i]) : acc[0][0][i];
   };
 
   if constexpr (!SECOND) {
@@ -539,7 +559,7 @@ __global__ void __launch_bounds__(FEW_THREADS, 2) few_kernel(const __grid_consta
 #pragma unroll
       for (int m = 0; m < 2; ++m)
 #pragma unroll
-        for (int i = 0; i < 4; ++i) sums[((warp * 2 + m) * 8 + 2 * c4 + (i & 1)) * 17 + g + 8 * (i >> 1)] = acc[m][i];
+        for (int i = 0; i < 4; ++i) sums[((warp * 2 + m) * 8 + 2 * c4 + (i & 1)) * 17 + g + 8 * (i >> 1)] = acc[0][m][i];
       workers_sync();
       const int row = threadIdx.x & 15, col = threadIdx.x >> 4;
       if (col < a.tokens && n0 + row < p.N) {
@@ -555,7 +575,7 @@ __global__ void __launch_bounds__(FEW_THREADS, 2) few_kernel(const __grid_consta
         const float rest = h - to_f32<BF16>(hi);
         const int64_t to = pair * p.ldh + n0 + row;
         p.hi[to] = hi;
-        p.lo[to] = isfinite(rest) ? round16<BF16>(rest) : static_cast<uint16_t>(0);
+        p.lo[to] = isfinite(rest) ? round16<BF16>(rest * lo_factor<BF16>()) : static_cast<uint16_t>(0);
       }
       workers_sync();
     }
@@ -569,7 +589,7 @@ __global__ void __launch_bounds__(FEW_THREADS, 2) few_kernel(const __grid_consta
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
           const int t = 2 * c4 + (i & 1);
-          if (t < p.T) own[t * 16 + g + 8 * (i >> 1)] = acc[0][i];
+          if (t < p.T) own[t * 16 + g + 8 * (i >> 1)] = sum_of(i);
         }
       } else {
         for (int i = lane; i < p.T * 16; i += 32) own[i] = 0.0f;
@@ -580,7 +600,7 @@ __global__ void __launch_bounds__(FEW_THREADS, 2) few_kernel(const __grid_consta
 #pragma unroll
           for (int i = 0; i < 4; ++i) {
             const int col = 2 * c4 + (i & 1);
-            if (col < a.tokens) own[token[a.first + col] * 16 + g + 8 * (i >> 1)] += acc[0][i];
+            if (col < a.tokens) own[token[a.first + col] * 16 + g + 8 * (i >> 1)] += sum_of(i);
           }
           clear();
           __syncwarp();

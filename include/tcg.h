@@ -465,8 +465,9 @@ int tcg_gemm_f8_grouped_wgrad(tcg_input in_type, int64_t R, int64_t N, int64_t K
  * (without W3: W2[e] silu(W1[e] X[t])).  Choices outside [0, E) are dropped; a
  * token without kept choices gets zeros; a token that names an expert twice
  * gets it with both weights.  Products are summed in fp32; the weighted
- * activations are kept as two values of x_type (beyond f16's range infinite, as
- * f16 activations are), Y is rounded once.  Every chosen expert's matrices are
+ * activations are kept as two values of x_type (of f16 ones 2^-22 of their size or
+ * 2^-36 is lost, of bf16 ones 2^-16; beyond f16's range they are infinite, as f16
+ * activations are), Y is rounded once.  Every chosen expert's matrices are
  * read once.  E4M3 weights keep all bits of X.  Results do not depend on
  * timing. */
 typedef struct {

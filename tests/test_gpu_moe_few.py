@@ -252,3 +252,23 @@ def test_captured_with_new_choices(tcg):
         assert tcg.check() == 0
         y, off = c.reference()
         close(to_host(Y), y, off, 1.0, "f32")
+
+
+@pytest.mark.parametrize("weights", ["e4m3", "f16"])
+@pytest.mark.parametrize("T,size", [(3, 2.0 ** -7), (3, 2.0 ** -11), (21, 2.0 ** -9)])
+def test_small_f16_activations_keep_their_bits(tcg, weights, T, size):
+    """Weights of the choices so small that w h lies below f16's normal range.  hi
+    leaves at most 2^-11 of it or 2^-25, lo = 2^11 times that 2^-11 of the rest or
+    2^-25: 2^-22 of w h or 2^-36."""
+    c = Case(T, 2, 4, 256, 192, "f16", weights, True, seed=T, scale=0.1)
+    c.weight *= np.float32(size)
+    if weights == "e4m3":
+        c.S["2"] *= 4096            # scales that bring y back
+        c.w["2"] = c.w["2"] * 4096
+    Y = c.run(tcg, "f32")
+    assert tcg.check() == 0, tcg.last_error_string()
+    y, off = c.reference()
+    for t in range(T):              # the bound above instead of the layer's 2^-25
+        for e in set(c.expert[t].tolist()):
+            off[t] -= (2.0 ** -25 - 2.0 ** -36) * np.abs(c.w["2"][e]).sum(axis=1)
+    close(to_host(Y), y, off, 1.0, "f32", (weights, T))
