@@ -34,6 +34,7 @@ thread_local int t_last_launches = 0;
 struct PlanRecord {
   bool valid = false;
   bool grouped = false;
+  int f8_shared = 0;  // products of 8-bit codes in tiles: the CTAs that share a tile's contraction; 0: another
   int w4_rows = 0, w4_across = 0, w4_down = 0, w4_ctas = 0;  // 4-bit products; w4_rows 0: another
   bool w4_boxes = false;
   int gemv_rows = 0, gemv_stages = 0, gemv_ctas = 0;  // few rows of 8-bit codes; gemv_rows 0: another
@@ -885,6 +886,12 @@ void record_grouped_plan(int cta_group, int tile_n, int clusters) {
   t_plan.clusters = clusters;
 }
 
+void record_f8_plan(bool grouped, int cta_group, int tile_n, int shared, int clusters) {
+  record_grouped_plan(cta_group, tile_n, clusters);
+  t_plan.grouped = grouped;
+  t_plan.f8_shared = shared;
+}
+
 void record_w4_plan(int rows, int across, int down, int ctas, bool boxes) {
   t_plan.valid = true;
   t_plan.w4_rows = rows;
@@ -1229,6 +1236,17 @@ const char* tcg_last_plan_string(void) {
     char buf[200];
     std::snprintf(buf, sizeof buf, "8-bit, blocks of %d rows, ring of %d stages, %d CTAs", p.gemv_rows, p.gemv_stages,
                   p.gemv_ctas);
+    t_last_plan = buf;
+  } else if (p.f8_shared) {
+    char shared[120] = "";
+    // In brackets, as logs had it before the tile and the CTAs that share it were told
+    // apart: the cluster's partial sums.
+    if (p.f8_shared > 1)
+      std::snprintf(shared, sizeof shared, ", contraction over %d CTAs (partial sums of a cluster: cta_group %d, tile %dx%d)",
+                    p.f8_shared, p.f8_shared, 128 * p.f8_shared, p.bn);
+    char buf[300];
+    std::snprintf(buf, sizeof buf, "8-bit%s, tile %dx%d by cta_group %d%s, %d clusters", p.grouped ? ", grouped" : "",
+                  128 * p.cg, p.bn, p.cg, shared, p.clusters);
     t_last_plan = buf;
   } else if (p.grouped) {
     char buf[200];

@@ -102,6 +102,7 @@ void set_launch_count(int n);
 void begin_product();
 void record_zero_plan();
 void record_grouped_plan(int cta_group, int tile_n, int clusters);
+void record_f8_plan(bool grouped, int cta_group, int tile_n, int shared, int clusters);
 void record_gemv_f8_plan(int rows, int stages, int ctas);
 void record_w4_plan(int rows, int across, int down, int ctas, bool boxes);
 

@@ -1171,7 +1171,7 @@ int launch_f8(const KernelInfo& ki, F8Params& p, int dev, int64_t units, cudaStr
   void* args[] = {&p};
   if (int rc = record_cuda(cudaLaunchKernelExC(&cfg, ki.func, args))) return rc;
   set_launch_count(1);
-  record_grouped_plan(cg, ki.bn, static_cast<int>(cfg.gridDim.x) / cg);
+  record_f8_plan(p.offsets != nullptr, ki.cta_group, ki.bn, p.split, static_cast<int>(cfg.gridDim.x) / cg);
   return TCG_OK;
 }
 

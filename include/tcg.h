@@ -575,10 +575,11 @@ int tcg_last_launch_count(void);
 
 /* How the most recent product on this thread was run (kernel tile, CTA group,
  * clusters, one pass / split-K / stream-K, operand swap; for the grouped,
- * 8-bit and 4-bit products their own; tcg_moe_few has none), as text for logs and tests; empty if the call
- * queued nothing or failed.  The string is
- * formatted by this call, owned by the library and valid until this thread's
- * next tcg_last_plan_string call. */
+ * 8-bit and 4-bit products their own, of 8-bit ones in tiles the CTAs that share
+ * a tile's contraction too; tcg_moe_few has none), as text for logs and tests;
+ * empty if the call queued nothing or failed.  The string is formatted by this
+ * call, owned by the library and valid until this thread's next
+ * tcg_last_plan_string call. */
 const char* tcg_last_plan_string(void);
 
 /* Phase trace of the next GEMM kernel launched by this thread (tcg_gemm and

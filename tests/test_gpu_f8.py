@@ -318,3 +318,28 @@ def test_captured_on_two_streams(tcg):
     ok(tcg)
     for _, _, D, ref, S, K, _ in graphs:
         close(to_host(D), ref, S, tau(K), "f32")
+
+
+def test_plan_names_the_tile_and_who_shares_it(tcg):
+    """The plan says the tile of the kernel that ran, the CTAs that share a
+    contraction, and whether there are groups."""
+    for M, N, K, square, tile, shared in (
+            (9, 1000, 300, True, "tile 128x64 by cta_group 1", 1), (16, 1000, 2000, True, "tile 128x64 by cta_group 1", 2),
+            (16, 1000, 4000, True, "tile 128x64 by cta_group 1", 4), (1300, 1000, 300, True, "tile 256x256 by cta_group 2", 1),
+            (1, 300, 300, False, "tile 256x256 by cta_group 2", 1)):
+        dense(tcg, M, N, K, "e4m3", "k", "k", square, "f32")
+        plan = tcg.last_plan_string()
+        assert plan.startswith("8-bit, " + tile) and "grouped" not in plan, plan
+        assert (f"contraction over {shared} CTAs" in plan) == (shared > 1), plan
+    off = torch.tensor([0, 20, 40], dtype=torch.int32, device="cuda")
+    for call in ("rows", "weight"):
+        A, SA, D = torch.zeros(40, 256, dtype=torch.uint8, device="cuda"), torch.ones(2, 256, device="cuda"), torch.empty(
+            2, 256, 256, device="cuda")
+        if call == "rows":
+            tcg.gemm_f8_grouped(tcg.IN_E4M3, 40, 256, 256, 2, A, 256, SA, 256, off, torch.zeros(
+                2, 256, 256, dtype=torch.uint8, device="cuda"), tcg.MN_MAJOR, 256, 0, torch.ones(2, 2, 2, device="cuda"), 0, 0,
+                D, tcg.F32, 256)
+        else:
+            tcg.gemm_f8_grouped_wgrad(tcg.IN_E4M3, 40, 256, 256, 2, A, 256, SA, 256, A, 256, SA, 256, off, D, tcg.F32, 256, 0)
+        ok(tcg)
+        assert tcg.last_plan_string().startswith("8-bit, grouped, tile "), tcg.last_plan_string()
