@@ -343,3 +343,68 @@ def test_plan_names_the_tile_and_who_shares_it(tcg):
             tcg.gemm_f8_grouped_wgrad(tcg.IN_E4M3, 40, 256, 256, 2, A, 256, SA, 256, A, 256, SA, 256, off, D, tcg.F32, 256, 0)
         ok(tcg)
         assert tcg.last_plan_string().startswith("8-bit, grouped, tile "), tcg.last_plan_string()
+
+
+def apart(t, more, fill):
+    """t [G][...] in a buffer whose matrices lie `more` elements further apart, and their stride."""
+    n = t[0].numel()
+    big = torch.full((t.shape[0], n + more), fill, dtype=t.dtype, device="cuda")
+    big[:, :n] = t.reshape(t.shape[0], n)
+    return big, n + more
+
+
+@pytest.mark.parametrize("major", ["k", "mn"])
+@pytest.mark.parametrize("sizes,N,K", [([1, 2, 0, 1], 136, 200), ([5, 0, 70, 30], 264, 300), ([300, 40, 0, 520], 2568, 200)])
+def test_matrices_and_scales_apart(tcg, major, sizes, N, K):
+    """Matrices, scales and gradients inside larger buffers, with NaN between them:
+    bit for bit the packed results, and nothing written between."""
+    G, R = len(sizes), sum(sizes)
+    off = torch.from_numpy(group_offsets(sizes)).cuda()
+    rows, cols = (N, K) if major == "k" else (K, N)
+    A, _ = codes((R, K), "e4m3", 1)
+    SA, _ = scales((blocks(K), R), "e4m3", 2)
+    B, _ = codes((G, rows, cols), "e4m3", 3)
+    SB, _ = scales((G, blocks(rows), blocks(cols)), "e4m3", 4)
+    DY, _ = codes((R, N), "e4m3", 5)
+    SY, _ = scales((R // BLOCK + G, N), "e4m3", 6)
+    SX, _ = scales((R // BLOCK + G, K), "e4m3", 7)
+    B2, stride_b = apart(B, 48, 0x7f)
+    SB2, stride_sb = apart(SB, 5, float("nan"))
+    outs, grads = [], []
+    for b, sb, s, ss in ((B, 0, SB, 0), (B2, stride_b, SB2, stride_sb)):
+        D = torch.zeros(R, N, device="cuda")
+        tcg.gemm_f8_grouped(tcg.IN_E4M3, R, N, K, G, A, A.shape[1], SA, R, off, b,
+                            tcg.K_MAJOR if major == "k" else tcg.MN_MAJOR, B.shape[2], sb, s, SB.shape[2], ss, D, tcg.F32, N)
+        ok(tcg)
+        outs.append(D)
+    assert torch.equal(*outs)
+    for more in (0, 12, 7):  # 16-byte strides, and none
+        W = torch.full((G, N * K + more), 7.0, device="cuda")
+        tcg.gemm_f8_grouped_wgrad(tcg.IN_E4M3, R, N, K, G, DY, DY.shape[1], SY, N, A, A.shape[1], SX, K, off, W, tcg.F32, K,
+                                  N * K + more if more else 0)
+        ok(tcg)
+        assert bool((W[:, N * K:] == 7.0).all()), "wrote between the matrices"
+        grads.append(W[:, :N * K])
+    assert torch.equal(grads[0], grads[1]) and torch.equal(grads[0], grads[2])
+
+
+@pytest.mark.parametrize("sizes,before,after,N,K,pad", [CASES[2], CASES[5], CASES[9], CASES[12]])
+def test_grouped_wgrad_of_e5m2(tcg, sizes, before, after, N, K, pad):
+    G, R = len(sizes), sum(sizes) + before + after
+    off = group_offsets(sizes, before)
+    DY, dy = codes((R, N), "e5m2", 5, pad)
+    A, a = codes((R, K), "e5m2", 6, pad)
+    SDY, sdy = scales((R // BLOCK + G, N), "e5m2", 7, 0.1, pad)
+    SA, sa = scales((R // BLOCK + G, K), "e5m2", 8, 1.0, pad)
+    at = row_blocks(off, R)
+    dy, a = dy * sdy[at], a * sa[at]
+    ref, S = np.zeros((G, N, K)), np.zeros((G, N, K))
+    for g in range(G):
+        sl = slice(off[g], off[g + 1])
+        ref[g], S[g] = dy[sl].T @ a[sl], np.abs(dy[sl]).T @ np.abs(a[sl])
+    for out in ("f32", "bf16"):
+        DW = torch.full((G, N, K), 7.0, dtype=TORCH[out], device="cuda")
+        tcg.gemm_f8_grouped_wgrad(tcg.IN_E5M2, R, N, K, G, DY, DY.shape[1], SDY, SDY.shape[1], A, A.shape[1], SA, SA.shape[1],
+                                  torch.from_numpy(off).cuda(), DW, DTYPE[out], K, 0)
+        ok(tcg)
+        close(to_host(DW), ref, S, tau(max(sizes)), out, out)

@@ -215,3 +215,15 @@ def test_fp32_is_rounded_once(tcg, fmt, kind, n):
     want = np.array([exact_code(v, t, fmt) for v, t in zip(x.ravel(), np.broadcast_to(top, x.shape).ravel())]).reshape(x.shape)
     wrong = got != want
     assert not wrong.any(), (int(wrong.sum()), x[wrong][:4], got[wrong][:4], want[wrong][:4])
+
+
+@pytest.mark.parametrize("sizes,before,after", [([0, 0, 3], 2, 1), ([130, 0, 1, 127, 128, 129, 300], 5, 9), ([1] * 1024, 3, 0)])
+@pytest.mark.parametrize("C", [72, 77])  # in words, and value by value
+def test_grouped_columns_by_powers_of_two(tcg, sizes, before, after, C):
+    R = sum(sizes) + before + after
+    off = group_offsets(sizes, before)
+    for dtype in ("bf16", "f16", "f32"):
+        for fmt in ("e4m3", "e5m2"):
+            X, x = data(R, C, dtype, 5)
+            Q, S = run(tcg, X, R, C, dtype, "column", fmt, True, offsets=off)
+            compare(Q, S, x, "column", fmt, True, dtype, offsets=off)

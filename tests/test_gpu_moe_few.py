@@ -272,3 +272,36 @@ def test_small_f16_activations_keep_their_bits(tcg, weights, T, size):
         for e in set(c.expert[t].tolist()):
             off[t] -= (2.0 ** -25 - 2.0 ** -36) * np.abs(c.w["2"][e]).sum(axis=1)
     close(to_host(Y), y, off, 1.0, "f32", (weights, T))
+
+
+@pytest.mark.parametrize("dtype,weights", [("bf16", "e4m3"), ("f16", "f16")])
+@pytest.mark.parametrize("T", [2, 24])
+def test_experts_and_their_scales_apart(tcg, dtype, weights, T):
+    """Experts inside larger buffers: strides between matrices and between scales
+    beyond the packed ones, NaN between them."""
+    c = Case(T, 2, 5, 272, 144, dtype, weights, True, seed=11)
+    want = to_host(c.run(tcg, "f32"))
+    stride = {}
+
+    def apart(t, more, fill):
+        if t is None:
+            return None, 0
+        E, n, k = t.shape
+        big = torch.full((E, n * k + more), fill, dtype=t.dtype, device="cuda")
+        big[:, :n * k] = t.reshape(E, n * k)
+        return big, n * k + more
+    for name, W in c.W.items():
+        ld = W.shape[2]
+        more = 16 * (3 if name == "2" else 5)
+        big, stride[name] = apart(W, more, 0x7f if weights == "e4m3" else float("nan"))
+        S, stride["s" + name] = apart(c.S[name], 7 if name == "2" else 3, float("nan"))
+        c.W[name], c.S[name] = (big, ld), (S, 0 if c.S[name] is None else c.S[name].shape[2])
+    expert, weight = torch.from_numpy(c.expert).cuda(), torch.from_numpy(c.weight).cuda()
+    work = torch.full((tcg.moe_few_work_bytes(T, 2, c.I),), 0xFF, dtype=torch.uint8, device="cuda")
+    Y = torch.full((T, c.H), 7.0, device="cuda")
+    tcg.moe_few(IN_TYPE[dtype], 3 if weights == "e4m3" else IN_TYPE[dtype], T, c.H, c.I, 2, 5, c.X, c.X.shape[1], expert,
+                weight, c.W["1"][0], c.W["3"][0], c.W["2"][0], work, Y, tcg.F32, c.H, s1=c.S["1"][0], s3=c.S["3"][0],
+                s2=c.S["2"][0], ld1=c.W["1"][1], stride1=stride["1"], ld2=c.W["2"][1], stride2=stride["2"],
+                ld_s1=c.S["1"][1], stride_s1=stride["s1"], ld_s2=c.S["2"][1], stride_s2=stride["s2"])
+    assert tcg.check() == 0, tcg.last_error_string()
+    assert np.array_equal(to_host(Y), want)
