@@ -74,3 +74,36 @@ def test_decoding(moe, T):  # noqa: F811
     y = layer8.decode(x, expert, weight)
     # x as it is, sums in fp32, one rounding
     near(host(y), plain(host(x), expert.cpu().numpy(), host(weight), decoded(layer8.w1), decoded(layer8.w2)), 2.0 ** -8)
+
+
+def test_captured_step_equals_the_eager_one(moe):  # noqa: F811
+    """Every operator of the 8-bit layer in one graph, forward, back and decoding,
+    each reading what the one before wrote: bit for bit the eager results, on new
+    inputs too."""
+    T, H, I, E, topk = 200, 256, 384, 6, 2
+    layer, x, expert, weight = inputs(moe, T, H, I, E, topk, torch.bfloat16)
+    layer8 = moe.MoeLayer8(layer)
+    dy = torch.randn(T, H, generator=torch.Generator().manual_seed(2)).to(x.dtype).cuda()
+
+    def step():
+        y, kept = layer8.forward(x, expert, weight)
+        return (y, *layer8.backward(dy, kept), layer8.decode(x[:16], expert[:16], weight[:16]))
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        step()
+    torch.cuda.current_stream().wait_stream(side)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        outs = step()
+    for seed in range(4):
+        g = torch.Generator().manual_seed(10 + seed)
+        x.copy_(torch.randn(T, H, generator=g))
+        dy.copy_(torch.randn(T, H, generator=g))
+        expert.copy_(torch.randint(-1, E + 1, (T, topk), generator=g))
+        weight.copy_(torch.rand(T, topk, generator=g))
+        want = [t.clone() for t in step()]
+        for _ in range(3):
+            graph.replay()
+        torch.cuda.synchronize()
+        assert all(torch.equal(a, b) for a, b in zip(outs, want))
