@@ -1181,18 +1181,31 @@ struct Plan {
   Scaling mode;
 };
 
-// Up to two rows a group stream the matrices (gemv_f8.cu), and up to eight where
-// these have less than 64 MB: 1 x 8192 x 8192 15 us and, here, 19; 64 rows over 32
-// groups of 2048 x 2048 28.5 and 27.7; 8 x 4096 x 4096 8.2 and 11.1, 8 x 8192 x 8192
-// 22 and 19.7, 16 x 4096 x 4096 12.0 and 11.3; 128 rows over 32 groups 36 and 32.
-bool few_rows(int64_t R, int G, int64_t N, int64_t K) {
-  return R <= 2 * static_cast<int64_t>(G) || (R <= 8 * static_cast<int64_t>(G) && N * K < (int64_t{1} << 26) / G);
+// A few rows a group stream the matrices (gemv_f8.cu) where the tiles of 128 x 64 are
+// few for the SMs; many keep every SM reading, and streaming passes over the matrix of
+// a popular group again for each eight of its rows.  Tiles and streamed, us:
+//     up to two rows a group, and a tile an SM for each 800 of K, but at least 2 and at most 7
+//       1 x 8192 x 8192 18.9 and 15.8; 32 rows over 16 groups of 4096 x 4096 52.9 and 46.4 (3.4 tiles
+//       an SM), 96 over 48 of 2048 x 4096 73.7 and 69.1 (5.1), 96 over 48 of 2048 x 8192 138.9 and 121.9;
+//       beyond, 128 over 64 of 4096 x 1024 53.8 and 80.4 (13.5; all rows in one group 8.9 and 27.2),
+//       256 over 128 of 4096 x 4096 319 and 360 (27; 17.5 and 132), 64 over 32 of 2048 x 2048 30.4 and 31.9 (3.4)
+//     up to eight, below 64 MB of matrices and up to 1.5 tiles an SM
+//       8 x 4096 x 4096 11.5 and 8.7, 64 rows over 8 groups of 2992 x 2048 17.7 and 15.8 (1.3);
+//       beyond, 8 x 8192 x 8192 18.9 and 21.5, 512 over 64 of 512 x 512 12.3 and 13.5 (1.7)
+// Only the average is known here: all of 32 rows in one of 16 groups of 4096 x 4096 take
+// 20.8 streamed and 14.7 in tiles.
+bool few_rows(int64_t R, int G, int64_t N, int64_t K, int sms) {
+  const int64_t tiles = G * ceil_div(N, 128);
+  if (R <= 2 * static_cast<int64_t>(G)) return tiles <= sms * std::min(std::max(K / 800.0, 2.0), 7.0);
+  return R <= 8 * static_cast<int64_t>(G) && N * K < (int64_t{1} << 26) / G && 2 * tiles <= 3 * sms;
 }
 
 // Tiles of 128 x 64 for up to 64 rows a group, and where there are no more of them
 // than SMs: 128 x 4096 x 4096 in 13.8 us (256 x 256: 21.0), 256 x 4096 x 4096 16.4
 // (21.3), 128 x 8192 x 8192 26.8 (35.5), 512 x 2048 x 8192 26.4 (34.8); beyond, 300 x
-// 4096 x 4096 takes 22.3 with 256 x 256.
+// 4096 x 4096 takes 19.8 with 256 x 256.  Here too the average decides: 2048 rows over 32
+// groups of 4096 x 2048 take 50 us if even (256 x 256: 65), 65 (72) with half of them in
+// one group and 43 (23) with all.
 Plan choose(int64_t R, int64_t N, int G, int dev, bool a_mn, bool square) {
   if (!square) return {variant<2, 256, 5, BOTH>(), BOTH};
   const bool idle = (ceil_div(R, 64) + G - 1) * ceil_div(N, 128) <= device_sms(dev);
@@ -1243,7 +1256,7 @@ int run_dense(tcg_input type, int64_t M, int64_t N, int64_t K, const void* A, tc
   }
   int dev;
   if (int rc = current_device_checked(&dev)) return rc;
-  if (sb_square && !a_mn && !b_mn && few_rows(M, 1, N, K))
+  if (sb_square && !a_mn && !b_mn && few_rows(M, 1, N, K, device_sms(dev)))
     return run_gemv_f8(type, M, N, K, 1, A, lda, SA, ld_sa, nullptr, B, ldb, N * ldb, SB, ld_sb, 0, D, d_type, ldd, dev, s);
   F8Params p;
   std::memset(&p, 0, sizeof p);
@@ -1284,7 +1297,7 @@ int run_grouped(tcg_input type, int64_t R, int64_t N, int64_t K, int G, const vo
   }
   int dev;
   if (int rc = current_device_checked(&dev)) return rc;
-  if (!mn && few_rows(R, G, N, K))
+  if (!mn && few_rows(R, G, N, K, device_sms(dev)))
     return run_gemv_f8(type, R, N, K, G, A, lda, SA, ld_sa, offsets, B, ldb, stride_b, SB, ld_sb, stride_sb, D, d_type,
                        ldd, dev, s);
   F8Params p;

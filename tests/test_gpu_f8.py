@@ -408,3 +408,34 @@ def test_grouped_wgrad_of_e5m2(tcg, sizes, before, after, N, K, pad):
                                   torch.from_numpy(off).cuda(), DW, DTYPE[out], K, 0)
         ok(tcg)
         close(to_host(DW), ref, S, tau(max(sizes)), out, out)
+
+
+@pytest.mark.parametrize("sizes,N,K,plan", [
+    ([2] * 16, 256, 272, "8-bit, blocks of 8"), ([1] * 48, 2048, 4096, "8-bit, blocks of 8"),
+    ([2] * 512, 128, 272, "tile 128x64"), ([0] * 300 + [600] + [0] * 299, 40, 272, "tile 128x64"),
+    ([8] * 8, 256, 272, "8-bit, blocks of 8"), ([0, 30, 2, 0, 0], 256, 272, "8-bit, blocks of 8"), ([8] * 300, 128, 272, "tile 128x64")])
+def test_many_matrices_are_not_streamed(tcg, sizes, N, K, plan):
+    """Few rows a group: streamed where the matrices' tiles are few, tiles where
+    they are many (one popular group among them), with the same results."""
+    G, R = len(sizes), sum(sizes)
+    off = group_offsets(sizes)
+    A, a = codes((R, K), "e4m3", 1)
+    SA, sa = scales((blocks(K), R), "e4m3", 2)
+    few = min(G, 40)            # as many matrices, the rest the first again
+    B, b = codes((few, N, K), "e4m3", 3)
+    SB, sb = scales((few, blocks(N), blocks(K)), "e4m3", 4, K ** -0.5)
+    pick = np.arange(G) % few
+    b = b * spread(sb, N, K)
+    ld = B.shape[2]
+    B, SB = B[torch.from_numpy(pick).cuda()].contiguous(), SB[torch.from_numpy(pick).cuda()].contiguous()
+    D = torch.full((R, N), 7.0, device="cuda")
+    tcg.gemm_f8_grouped(tcg.IN_E4M3, R, N, K, G, A, A.shape[1], SA, R, torch.from_numpy(off).cuda(), B, tcg.K_MAJOR, ld, 0,
+                        SB, 0, 0, D, tcg.F32, N)
+    ok(tcg)
+    assert plan in tcg.last_plan_string(), tcg.last_plan_string()
+    a = a * along(sa, K).T
+    ref, S = np.zeros((R, N)), np.zeros((R, N))
+    for g in range(G):
+        sl = slice(off[g], off[g + 1])
+        ref[sl], S[sl] = a[sl] @ b[pick[g]].T, np.abs(a[sl]) @ np.abs(b[pick[g]]).T
+    close(to_host(D), ref, S, tau(K), "f32", (sizes[:8], N, K))
