@@ -348,7 +348,9 @@ __global__ void __launch_bounds__(32 * COL_WARPS, ALIGNED ? 6 : 3)
   griddep_wait();
   int64_t lo = slot * BLOCK, end = R;
   if (offsets) {
-    // block j of group g has slot offsets[g] / 128 + g + j; the slots of groups rise
+    // block j of group g has slot offsets[g] / 128 + g + j; the slots of groups rise.  (For
+    // any offsets slot >= g, as some group of an index >= g was met, so that lo below is
+    // first % 128 + (slot - g) * 128 >= 0.)
     int g = -1, first = 0, next = 0;
     for (int i = lane; i < G; i += 32) {
       const int o = min(max(offsets[i], 0), static_cast<int>(R)), o1 = offsets[i + 1];

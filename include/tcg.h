@@ -420,8 +420,12 @@ typedef enum {
  * [offsets[g], offsets[g+1]) are group g, whose blocks begin at offsets[g];
  * its block j is scale row offsets[g] / 128 + g + j, in all R / 128 + G rows
  * (rounded down).  Codes of rows of no group and scale rows of no block are
- * left as they are.  X, scale element aligned; rows whose bases and strides are
- * 16-byte (Q: 4- or 8-byte) multiples move in words.  R, C < 2^30, G <= 1024. */
+ * left as they are.  (Offsets outside [0, R] are clamped to it; where they do not
+ * rise, codes and scales are unspecified, but nothing out of range is read or
+ * written.)  X, scale element aligned; rows
+ * move in words where C and X's base and stride are whole 16-byte words (8 16-bit
+ * or 4 fp32 values) and Q's base and stride multiples of as many bytes, else value
+ * by value, which takes two to five times as long.  R, C < 2^30, G <= 1024. */
 int tcg_f8_quantize(tcg_input q_type, tcg_f8_blocks blocks, int pow2, int64_t R, int64_t C, tcg_dtype x_type,
                     const void* X, int64_t ldx, int G, const int32_t* offsets, void* Q, int64_t ldq, float* scale,
                     int64_t ld_scale, void* stream);
@@ -435,9 +439,11 @@ int tcg_f8_quantize(tcg_input q_type, tcg_f8_blocks blocks, int pow2, int64_t R,
  * (sb_square 0, ld 0 = N), or one for each 128 x 128 of the stored matrix
  * (sb_square 1): [ceil(N/128)][ceil(K/128)] of a K-major B, [ceil(K/128)]
  * [ceil(N/128)] of an MN-major one.  A block's sum is the tensor cores'; blocks
- * are added in fp32, rounded once each; D is rounded once.  Forward
- * X W^T: both K-major.  Rows' gradient dY W: B = W, MN-major, square scales.
- * Matrix' gradient dY^T X: both MN-major.  K == 0: D = 0. */
+ * are added in fp32, rounded once each; D is rounded once.  With sb_square a
+ * block's factor SA * SB is formed in fp32 first: from 2^128 on it is infinite
+ * (a sum of zero then gives NaN), below 2^-126 it is off by up to 2^-150.
+ * Forward X W^T: both K-major.  Rows' gradient dY W: B = W, MN-major, square
+ * scales.  Matrix' gradient dY^T X: both MN-major.  K == 0: D = 0. */
 int tcg_gemm_f8(tcg_input in_type, int64_t M, int64_t N, int64_t K, const void* A, tcg_major a_major, int64_t lda,
                 const float* SA, int64_t ld_sa, const void* B, tcg_major b_major, int64_t ldb, const float* SB,
                 int64_t ld_sb, int sb_square, void* D, tcg_dtype d_type, int64_t ldd, void* stream);

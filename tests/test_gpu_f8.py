@@ -439,3 +439,21 @@ def test_many_matrices_are_not_streamed(tcg, sizes, N, K, plan):
         sl = slice(off[g], off[g + 1])
         ref[sl], S[sl] = a[sl] @ b[pick[g]].T, np.abs(a[sl]) @ np.abs(b[pick[g]]).T
     close(to_host(D), ref, S, tau(K), "f32", (sizes[:8], N, K))
+
+
+@pytest.mark.parametrize("M,square", [(3, True), (70, True), (1300, True), (70, False)])
+def test_factors_below_the_normal_range(tcg, M, square):
+    """Scales whose product is no normal fp32 number: it is off by 2^-150 at most,
+    so that many times a block's sum is added to the tolerance."""
+    N, K = 1000, 300
+    A, a = codes((M, K), "e4m3", 1)
+    B, b = codes((N, K), "e4m3", 2)
+    SA, sa = scales((blocks(K), M), "e4m3", 3, 2.0 ** -82)
+    SB, sb = scales((blocks(N), blocks(K)) if square else (blocks(K), N), "e4m3", 4, 2.0 ** -42)
+    D = torch.full((M, N), 7.0, device="cuda")
+    tcg.gemm_f8(tcg.IN_E4M3, M, N, K, A, tcg.K_MAJOR, A.shape[1], SA, M, B, tcg.K_MAJOR, B.shape[1], SB, SB.shape[1], square,
+                D, tcg.F32, N)
+    ok(tcg)
+    x, y = a * along(sa, K).T, b * (spread(sb, N, K) if square else along(sb, K).T)
+    S = tau(K) * (np.abs(x) @ np.abs(y).T) + 2.0 ** -150 * (1 + tau(K)) * (np.abs(a) @ np.abs(b).T)
+    close(to_host(D), x @ y.T, S, 1.0, "f32")
