@@ -22,7 +22,7 @@
 //
 // Measured: 1 token x 8 of 128 experts of 4096 x 1024 E4M3, bf16, 30 us (a start of 5
 // for each kernel, half of the second's hidden; 100 MB at 6.8 TB/s are 14.8); 32 tokens
-// x 4 of 32 f16 experts of 4096 x 2048, 252 us, 6.3 TB/s; 8 tokens x 8 of 64 experts of
+// x 4 of 32 f16 experts of 4096 x 2048, 254 us, 6.2 TB/s; 8 tokens x 8 of 64 experts of
 // 4096 x 1024 E4M3 104 us, 5.1 TB/s.  With more tokens an expert than eight the passes
 // from L2 count: 32 x 8 of 64 such experts 202 us.
 //
@@ -700,7 +700,8 @@ struct Shape {
 
 // Two CTAs share an SM where half its memory holds 24 KB of weights and more: twice
 // the warps hide their latencies (1 token x 8 of 128 experts of 4096 x 1024, E4M3:
-// 30 us, 43 with one; 32 tokens x 4 of 32 f16 experts of 4096 x 2048 263 and 321).
+// 30 us, 43 with one; 32 tokens x 4 of 32 f16 experts of 4096 x 2048 18 % less than
+// with one).
 // Else one has what fits.
 Shape shape(int T, int topk, int E, bool second, int size, int matrices) {
   const auto at = [&](int n) { return Layout(T, topk, E, second, size, matrices, n); };
