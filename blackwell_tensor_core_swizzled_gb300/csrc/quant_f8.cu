@@ -136,11 +136,13 @@ __device__ __forceinline__ Coder make_coder(float amax, bool pow2, float& scale)
 }
 
 // Factors of fp32 x that give a little less and a little more than F x / a.  Each
-// product is within four roundings, 2^-22 of itself, of its own.
+// product is within four roundings, 2^-22 of itself, of its own.  A power of two (by of
+// `pow2`, zeros and the smallest blocks; F has three significant bits) is exact.
 struct Bounds {
   float below, above;
 };
 __device__ __forceinline__ Bounds bounds(const Coder& c) {
+  if ((__float_as_uint(c.by) & 0x7fffffu) == 0) return {c.by, c.by};
   const float k = c.by * c.inv;
   return {k * (1.0f - 0x1p-21f), k * (1.0f + 0x1p-21f)};
 }
@@ -166,6 +168,11 @@ __device__ __forceinline__ uint64_t mul2(uint64_t a, uint64_t b) {
   asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
   return d;
 }
+__device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
+  uint64_t d;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(d) : "l"(a), "l"(b), "l"(c));
+  return d;
+}
 
 // F x / a of 16-bit x, so close that rounding it to a code rounds F x / a itself.
 __device__ __forceinline__ float quotient(float x, const Coder& c) {
@@ -174,16 +181,10 @@ __device__ __forceinline__ float quotient(float x, const Coder& c) {
   return fmaf(fmaf(-y, c.a, n), c.inv, y);
 }
 
-// The same of fp32 x: F x = n + low exactly, z is one of the two fp32 values around
-// (n + low) / a, and `rest` has the sign of what is left, which two fmas give exactly
-// (multiples of z's and a's last bits, less than 2^25 of them).  Rounding to odd: of the
-// two values the one whose last bit is set, unless nothing is left.  Ties have few bits,
-// so that a quotient beside one stays on its side.
-__device__ __forceinline__ float odd_quotient(float x, const Coder& c) {
-  const float n = x * c.by, low = fmaf(x, c.by, -n);
-  const float y = n * c.inv;
-  const float z = fmaf(fmaf(-y, c.a, n) + low, c.inv, y);
-  const float rest = fmaf(-z, c.a, n) + low;
+// Rounding to odd: of the two fp32 values around z + rest (rest the less of z's last
+// bit) the one whose last bit is set, unless rest is 0.  Ties have few bits, so that a
+// quotient beside one stays on its side.
+__device__ __forceinline__ float to_odd(float z, float rest) {
   const uint32_t bits = __float_as_uint(z);
   const int32_t step = static_cast<int32_t>(__float_as_uint(rest) ^ bits) >> 31 | 1;  // towards zero or away from it
   return __uint_as_float(rest != 0.0f && !(bits & 1u) ? bits + step : bits);
@@ -199,10 +200,10 @@ __device__ __forceinline__ uint32_t encode4(float a, float b, float c, float d) 
 }
 
 // Four codes of fp32 values, if `sure`: the same from a little less and from a little
-// more than F x / a.  Where they differ (1 of 2^16 values, and ties) odd_quotient
-// decides: in rows at once (8192 x 8192 49.8 us, behind the loop over a thread's words
-// 60.3), else behind that loop, where its code is small (columns 54.4, squares 59.0;
-// with odd_quotient for every value each took a quarter to a third more).
+// more than F x / a.  Where they differ (1 of 2^16 values, and ties) store_exact_codes
+// decides.  8192 x 8192 fp32, rows, columns and squares: 49.7, 54.1 and 57.8 us; where one
+// value of 300 is a tie (bf16 values) 54, 69 and 63, where every word has one (small
+// integers) 78, 92 and 85, about as much as with store_exact_codes throughout.
 template <bool WIDE, class F>
 __device__ __forceinline__ uint32_t encode_f32(const Word<float>& x, F&& bound, bool& sure) {
   float lo[4], hi[4];
@@ -262,10 +263,24 @@ __device__ __forceinline__ bool store_codes(const Word<T>& x, uint8_t* q, int n,
   return !sure;
 }
 
+// F x = m + low exactly; z is one of the two fp32 values around (m + low) / a, and the
+// sign of the rest is exact (multiples of z's and a's last bits, less than 2^25 of them).
 template <bool WIDE, class F>
 __device__ __forceinline__ void store_exact_codes(const Word<float>& x, uint8_t* q, int n, bool aligned, F&& coder) {
-  const uint32_t code[1] = {encode4<WIDE>(odd_quotient(x.value(0), coder(0)), odd_quotient(x.value(1), coder(1)),
-                                          odd_quotient(x.value(2), coder(2)), odd_quotient(x.value(3), coder(3)))};
+  float z[4], rest[4];
+  const uint64_t minus = pair(-1.0f, -1.0f);
+#pragma unroll
+  for (int j = 0; j < 4; j += 2) {
+    const Coder a = coder(j), b = coder(j + 1);
+    const uint64_t v = pair(x.value(j), x.value(j + 1)), inv = pair(a.inv, b.inv), less = pair(-a.a, -b.a);
+    const uint64_t m = mul2(v, pair(a.by, b.by));
+    const uint64_t less_low = fma2(v, pair(-a.by, -b.by), m);
+    const uint64_t y = mul2(m, inv);
+    const uint64_t zz = fma2(fma2(less_low, minus, fma2(y, less, m)), inv, y);
+    unpair(zz, z[j], z[j + 1]);
+    unpair(fma2(less_low, minus, fma2(zz, less, m)), rest[j], rest[j + 1]);
+  }
+  const uint32_t code[1] = {encode4<WIDE>(to_odd(z[0], rest[0]), to_odd(z[1], rest[1]), to_odd(z[2], rest[2]), to_odd(z[3], rest[3]))};
   put_codes<4>(code, q, n, aligned);
 }
 
@@ -407,25 +422,20 @@ __global__ void __launch_bounds__(32 * COL_WARPS, ALIGNED ? 6 : 3)
   Maker<T> k[V];
 #pragma unroll
   for (int j = 0; j < V; ++j) k[j] = from_lane(make, 4 * j + w4);
-  uint32_t doubt = 0;
 #pragma unroll UNROLL
   for (int i = 0; i < PER; ++i) {
     const Word<T>& v = word(i);
-    if (g8 + 8 * i < rows &&
-        store_codes<WIDE>(v, Q + (lo + g8 + 8 * i) * ldq + c, n, ALIGNED, [&](int j) { return k[j]; }))
-      doubt |= 1u << i;
-  }
-  if constexpr (std::is_same<T, float>::value) {
-    if (__any_sync(0xffffffffu, doubt != 0)) {
-      Coder exact[V];
+    if constexpr (!std::is_same<T, float>::value) {
+      if (g8 + 8 * i < rows)
+        store_codes<WIDE>(v, Q + (lo + g8 + 8 * i) * ldq + c, n, ALIGNED, [&](int j) { return k[j]; });
+    } else {
+      uint8_t* q = Q + (lo + g8 + 8 * i) * ldq + c;
+      const bool doubt = g8 + 8 * i < rows && store_codes<WIDE>(v, q, n, ALIGNED, [&](int j) { return k[j]; });
+      if (__any_sync(0xffffffffu, doubt)) {
+        Coder exact[V];
 #pragma unroll
-      for (int j = 0; j < V; ++j) exact[j] = from_lane(my, 4 * j + w4);
-#pragma unroll 1
-      for (; doubt; doubt &= doubt - 1) {
-        const int64_t row = lo + g8 + 8 * (__ffs(doubt) - 1);
-        Word<T> again;
-        again.load(X + row * ldx + c, n, ALIGNED);
-        store_exact_codes<WIDE>(again, Q + row * ldq + c, n, ALIGNED, [&](int j) { return exact[j]; });
+        for (int j = 0; j < V; ++j) exact[j] = from_lane(my, 4 * j + w4);
+        if (doubt) store_exact_codes<WIDE>(v, q, n, ALIGNED, [&](int j) { return exact[j]; });
       }
     }
   }
@@ -435,7 +445,7 @@ __global__ void __launch_bounds__(32 * COL_WARPS, ALIGNED ? 6 : 3)
 // -------------------------------------------------------------------- squares
 
 // A block a CTA, in words of 16 bytes.  Four CTAs an SM of 16-bit values (8192 x 8192:
-// 34.6 us; three 41, five 44), two of fp32 (59 us; one 92, three 68).
+// 34.6 us; three 41, five 44), two of fp32 (58 us; one 92, three 68).
 template <class T, bool WIDE, bool ALIGNED>
 __global__ void __launch_bounds__(SQUARE_THREADS, ALIGNED && sizeof(T) == 2 ? 4 : 2)
     square_kernel(int64_t R, int64_t C, const T* __restrict__ X, int64_t ldx, bool pow2, uint8_t* __restrict__ Q,
@@ -470,21 +480,13 @@ __global__ void __launch_bounds__(SQUARE_THREADS, ALIGNED && sizeof(T) == 2 ? 4 
   const Coder k = make_coder<WIDE>(m, pow2, s);
   if (t == 0) scale[blockIdx.x / col_tiles * ld_scale + tile] = s;
   const Maker<T> make = maker<T>(k);
-  uint32_t doubt = 0;
 #pragma unroll
   for (int i = 0; i < PER; ++i) {
     const int row = t / ACROSS + DOWN * i;
-    if (row < rows && store_codes<WIDE>(x[i], Q + (lo + row) * ldq + c, n, ALIGNED, [&](int) { return make; }))
-      doubt |= 1u << i;
-  }
-  if constexpr (std::is_same<T, float>::value) {
-#pragma unroll 1
-    for (; doubt; doubt &= doubt - 1) {
-      const int64_t row = lo + t / ACROSS + DOWN * (__ffs(doubt) - 1);
-      Word<T> again;
-      again.load(X + row * ldx + c, n, ALIGNED);
-      store_exact_codes<WIDE>(again, Q + row * ldq + c, n, ALIGNED, [&](int) { return k; });
-    }
+    uint8_t* q = Q + (lo + row) * ldq + c;
+    const bool doubt = row < rows && store_codes<WIDE>(x[i], q, n, ALIGNED, [&](int) { return make; });
+    if constexpr (std::is_same<T, float>::value)
+      if (doubt) store_exact_codes<WIDE>(x[i], q, n, ALIGNED, [&](int) { return k; });
   }
   griddep_launch_dependents();
 }

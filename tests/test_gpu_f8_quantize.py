@@ -227,3 +227,26 @@ def test_grouped_columns_by_powers_of_two(tcg, sizes, before, after, C):
             X, x = data(R, C, dtype, 5)
             Q, S = run(tcg, X, R, C, dtype, "column", fmt, True, offsets=off)
             compare(Q, S, x, "column", fmt, True, dtype, offsets=off)
+
+
+@pytest.mark.parametrize("kind", ["row", "column", "square"])
+@pytest.mark.parametrize("pow2", [False, True])
+@pytest.mark.parametrize("C", [256, 131])  # in words, and value by value
+def test_fp32_full_of_ties(tcg, kind, pow2, C):
+    """Small whole numbers, bf16 and f16 values in fp32: their ties go to even.  Their
+    quotients are so far off other ties that float64 shows the side."""
+    rng = np.random.default_rng(C)
+    R = 200
+    whole = rng.integers(-8, 9, (R, C)).astype(np.float32)
+    some = torch.from_numpy(rng.standard_normal((R, C)) * np.exp2(rng.integers(-9, 2, (R, C))))
+    for x in (whole, whole * np.float32(2.0 ** -120), some.bfloat16().float().numpy(), some.half().float().numpy()):
+        for fmt in ("e4m3", "e5m2"):
+            Q, S = run(tcg, torch.from_numpy(x).cuda(), R, C, "f32", kind, fmt, pow2)
+            s, unit, _ = reference(x.astype(np.float64), kind, fmt, pow2, S.shape)
+            i, j = index_of(kind, R, C)
+            s = np.maximum(s, 2.0 ** -126)
+            unit = np.where((s == 2.0 ** -126)[i, j], x.astype(np.float64) / s[i, j], unit)
+            assert np.all(np.abs(S - s) <= 2.0 ** -24 * np.abs(s))
+            got, want = table(fmt)[Q], nearest(unit, fmt)
+            wrong = got != want
+            assert not wrong.any(), (int(wrong.sum()), x[wrong][:4], got[wrong][:4], want[wrong][:4], unit[wrong][:4])
